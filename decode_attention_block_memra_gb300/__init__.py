@@ -17,6 +17,7 @@ from . import _build
 FORMATS = {"q8_0": 0, "q5_1": 1, "q4_0": 2, "fp8": 3, "nvfp4": 4}
 PAGE_SIZE = 16
 SPLIT_TOKENS = 1280
+MAX_TREE_NODES = 64
 
 DEVERR_BAD_PAGE = 1
 DEVERR_BAD_SLOT = 2
@@ -94,6 +95,11 @@ _SIGS = {
     "memra_decode_attn_noalloc": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_void_p,
                                                  ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 6 +
                                   [ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
+    "memra_kv_copy_pages": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_int32, ctypes.c_void_p]),
+    "memra_kv_compact": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                        ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
     "memra_testing_decode_attn_short_page": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p,
                                                             ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p] +
                                              [ctypes.c_int32] * 6 + [ctypes.c_float, ctypes.c_void_p,
@@ -297,6 +303,29 @@ def decode_attn_noalloc(cache: KVCache, q, page_table, seq_lens, max_seq_len: in
                                            _ptr(seq_lens), int(max_seq_len), B, Q, Hq, cache.n_kv_heads, D,
                                            float(sm_scale if sm_scale is not None else D ** -0.5), _ptr(out),
                                            _stream(stream)), "memra_decode_attn_noalloc")
+
+
+def kv_copy_pages(cache: KVCache, src_pages, dst_pages, n: int | None = None, stream=None) -> None:
+    """memra_kv_copy_pages: page src_pages[i] -> dst_pages[i] in both pools; int32 [n] on the device, negative skips."""
+    if n is None:
+        n = int(src_pages.shape[0])
+        if int(dst_pages.shape[0]) != n:
+            raise MemraError(1, "memra_kv_copy_pages")
+    _check(lib().memra_kv_copy_pages(cache.ref, _ptr(src_pages), _ptr(dst_pages), int(n), _stream(stream)),
+           "memra_kv_copy_pages")
+
+
+def kv_compact(cache: KVCache, page_table, seq_lens, max_seq_len: int, accepted, n_accepted, n_nodes: int,
+               stream=None) -> None:
+    """memra_kv_compact: the rows of nodes accepted[b, :n_accepted[b]] move to the front of sequence b's tree rows.
+
+    accepted int32 [B, max_accepted], n_accepted int32 [B]; seq_lens include
+    the n_nodes rows of the tree.
+    """
+    B, most = accepted.shape
+    _check(lib().memra_kv_compact(cache.ref, _ptr(page_table), int(page_table.shape[1]), _ptr(seq_lens),
+                                  int(max_seq_len), _ptr(accepted), int(most), _ptr(n_accepted), int(B), int(n_nodes),
+                                  _stream(stream)), "memra_kv_compact")
 
 
 def testing_decode_attn_short_page(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, out, workspace,

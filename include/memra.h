@@ -102,7 +102,8 @@ typedef enum {
 
 /* Bits the kernels OR into *memra_kv_cache.status. */
 #define MEMRA_DEVERR_BAD_PAGE    1   /* page id outside [0, num_pages): page skipped      */
-#define MEMRA_DEVERR_BAD_SLOT    2   /* append slot >= num_pages*16: row skipped          */
+#define MEMRA_DEVERR_BAD_SLOT    2   /* append slot >= num_pages*16, or an accepted node that
+                                        is not one of the tree's: row skipped             */
 #define MEMRA_DEVERR_BAD_SEQ_LEN 4   /* seq_len < q_len, > max_seq_len or > table: clamped */
 #define MEMRA_DEVERR_TIMEOUT     8   /* a pipeline wait gave up after ~1 s: result invalid */
 #define MEMRA_DEVERR_PREFIX     16   /* cascade: a page table differs from the first sequence's
@@ -302,6 +303,47 @@ int memra_decode_step_cascade(const memra_kv_cache *cache, const void *k_new, co
                               int32_t max_seq_len, int32_t prefix_len, int32_t batch, int32_t q_len, int32_t n_heads,
                               int32_t n_kv_heads, int32_t head_dim, float sm_scale, void *workspace,
                               size_t workspace_bytes, void *out, void *stream);
+
+/* Copies whole pages inside both pools: page src_pages[i] to page dst_pages[i]
+ * for i < n, every KV head's K and V segments, byte for byte.  It serves a fork
+ * (the new sequence shares the full pages of its parent and gets a copy of the
+ * partial last one), copy on write, and the compaction of a pool.
+ *   src_pages, dst_pages  device int32 [n].  A negative id on either side skips
+ *                         the copy (padding); an id >= num_pages skips it and
+ *                         sets MEMRA_DEVERR_BAD_PAGE.
+ * A page may be the source of several copies.  The destinations must be
+ * distinct, and none may be the source of another copy of the call: the copies
+ * run in no particular order.  n == 0 is a no-op. */
+int memra_kv_copy_pages(const memra_kv_cache *cache, const int32_t *src_pages, const int32_t *dst_pages, int32_t n,
+                        void *stream);
+
+/* Largest number of nodes of a draft tree (new tokens per sequence) that
+ * memra_tree_attn and memra_kv_compact take. */
+#define MEMRA_MAX_TREE_NODES 64
+
+/* Keeps the accepted nodes of a verified draft tree.  The rows of a sequence's
+ * n_nodes tree nodes lie at positions base .. base + n_nodes - 1, base =
+ * seq_lens[b] - n_nodes (the layout that memra_tree_attn reads).  For every i <
+ * n_accepted[b] the K and V rows of node accepted[b][i] move to position base +
+ * i, byte for byte, every KV head.  The caller's new length is then base +
+ * n_accepted[b]; the rows behind it keep their bytes.
+ *   page_table    device int32 [batch][max_pages_per_seq]
+ *   seq_lens      device int32 [batch]; lengths INCLUDING the n_nodes rows
+ *   max_seq_len   host upper bound of seq_lens
+ *   accepted      device int32 [batch][max_accepted], node indices of the kept
+ *                 path; any order, an index may repeat.  An index outside
+ *                 [0, n_nodes) skips its row and sets MEMRA_DEVERR_BAD_SLOT.
+ *   n_accepted    device int32 [batch], 0 .. max_accepted (outside: clamped,
+ *                 MEMRA_DEVERR_BAD_SEQ_LEN)
+ *   max_accepted  0 .. n_nodes;  n_nodes <= MEMRA_MAX_TREE_NODES, batch <= 65535
+ * Every row of a sequence is read before any is written.  The pages that
+ * receive rows must belong to one sequence of the batch.  A sequence shorter
+ * than n_nodes sets MEMRA_DEVERR_BAD_SEQ_LEN and moves only rows between
+ * positions >= 0; a page id outside the pool skips the row
+ * (MEMRA_DEVERR_BAD_PAGE).  batch == 0 or max_accepted == 0 is a no-op. */
+int memra_kv_compact(const memra_kv_cache *cache, const int32_t *page_table, int32_t max_pages_per_seq,
+                     const int32_t *seq_lens, int32_t max_seq_len, const int32_t *accepted, int32_t max_accepted,
+                     const int32_t *n_accepted, int32_t batch, int32_t n_nodes, void *stream);
 
 /* Fixed size of the device array that memra_decode_attn_noalloc uses for the
  * split-K partials (held on every device that calls it, until exit). */

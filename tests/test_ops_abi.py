@@ -1,0 +1,68 @@
+"""Host checks of the operators around the decode step: page copies, tree compaction (CPU only).
+
+Every refusal returns before any CUDA call, so the pointers are made-up numbers."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def memra():
+    from decode_attention_block_memra_gb300 import _build
+    try:
+        _build.build()
+    except RuntimeError as e:          # no nvcc on this machine
+        pytest.skip(str(e))
+    import decode_attention_block_memra_gb300 as m
+    m.lib()
+    return m
+
+
+def cache(memra, **kw):
+    c = memra.KVCacheStruct(0, 1, 16, 2, 128, 4, 4096, 8192, 1.0, 1.0, 0)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+
+
+def test_copy_pages_checks(memra):
+    def call(c=None, src=64, dst=128, n=3):
+        return memra.lib().memra_kv_copy_pages(ctypes.byref(c or cache(memra)), src, dst, n, None)
+
+    assert memra.lib().memra_kv_copy_pages(None, 64, 128, 1, None) == INVALID
+    assert call(n=-1) == INVALID
+    assert call(n=0, src=0, dst=0) == 0
+    assert call(src=0) == INVALID
+    assert call(dst=0) == INVALID
+    assert call(src=66) == INVALID
+    assert call(c=cache(memra, head_dim=64)) == UNSUPPORTED
+    assert call(c=cache(memra, k_fmt=1)) == UNSUPPORTED
+    assert call(c=cache(memra, num_pages=0)) == INVALID
+    assert call(c=cache(memra, n_kv_heads=2 ** 31 - 1)) == UNSUPPORTED
+
+
+def test_compact_checks(memra):
+    good = dict(pt=64, maxp=4, sl=64, maxlen=64, acc=64, most=4, n=64, B=2, nodes=8)
+
+    def call(c=None, **kw):
+        a = {**good, **kw}
+        return memra.lib().memra_kv_compact(ctypes.byref(c or cache(memra)), a["pt"], a["maxp"], a["sl"], a["maxlen"],
+                                            a["acc"], a["most"], a["n"], a["B"], a["nodes"], None)
+
+    assert call(c=cache(memra, page_size=32)) == UNSUPPORTED
+    for name in ("pt", "sl", "acc", "n"):
+        assert call(**{name: 0}) == INVALID
+        assert call(**{name: 66}) == INVALID
+    assert call(B=-1) == INVALID
+    assert call(B=65536) == UNSUPPORTED
+    assert call(nodes=0) == INVALID
+    assert call(nodes=memra.MAX_TREE_NODES + 1) == UNSUPPORTED
+    assert call(most=9) == INVALID                 # more kept rows than nodes
+    assert call(most=-1) == INVALID
+    assert call(maxp=0) == INVALID
+    assert call(maxlen=-1) == INVALID
+    assert call(B=0) == 0
+    assert call(most=0) == 0
