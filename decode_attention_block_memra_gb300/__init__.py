@@ -95,6 +95,9 @@ _SIGS = {
     "memra_decode_attn_noalloc": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_void_p,
                                                  ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 6 +
                                   [ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
+    "memra_prompt_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64] * 3 + [ctypes.c_void_p] +
+                          [ctypes.c_int32] * 5 + [ctypes.c_float, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                                  ctypes.c_void_p]),
     "memra_kv_copy_pages": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_int32, ctypes.c_void_p]),
     "memra_kv_compact": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int32,
@@ -303,6 +306,30 @@ def decode_attn_noalloc(cache: KVCache, q, page_table, seq_lens, max_seq_len: in
                                            _ptr(seq_lens), int(max_seq_len), B, Q, Hq, cache.n_kv_heads, D,
                                            float(sm_scale if sm_scale is not None else D ** -0.5), _ptr(out),
                                            _stream(stream)), "memra_decode_attn_noalloc")
+
+
+def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status=None, stream=None) -> None:
+    """memra_prompt_attn: causal attention of packed prompts.
+
+    q fp16 [tokens, Hq, D], k and v fp16 [tokens, Hkv, D]: any token stride, a
+    token's heads dense (views of one fused QKV buffer will do); cu_seqlens
+    int32 [B + 1]; out fp16 [tokens, Hq, D], dense.  status: a device int32
+    the kernel ORs DEVERR_* bits into (KVCache.status will do).
+    """
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (T, Hkv, D) or v.shape != k.shape or out.shape != q.shape or not out.is_contiguous():
+        raise MemraError(1, "memra_prompt_attn")
+    strides = []
+    for x in (q, k, v):
+        s = x.stride()
+        if s[2] != 1 or (x.shape[1] > 1 and s[1] != D):
+            raise MemraError(1, "memra_prompt_attn")
+        strides.append(s[0] if T > 1 else x.shape[1] * D)
+    _check(lib().memra_prompt_attn(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(cu_seqlens),
+                                   int(cu_seqlens.shape[0]) - 1, T, Hq, Hkv, D,
+                                   float(sm_scale if sm_scale is not None else D ** -0.5), int(window), _ptr(out),
+                                   _ptr(status), _stream(stream)), "memra_prompt_attn")
 
 
 def kv_copy_pages(cache: KVCache, src_pages, dst_pages, n: int | None = None, stream=None) -> None:

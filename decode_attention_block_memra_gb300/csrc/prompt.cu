@@ -1,0 +1,477 @@
+// Prompt attention: causal attention of whole prompts, packed one behind the
+// other, with grouped heads and an optional sliding window.
+//
+//   o[t, h] = sum_u p_u v[u, h / G] / sum_u p_u,  p_u = 2^(s_u - m),
+//   s_u = q[t, h] . k[u, h / G] * scale * log2(e),  u = max(first, t - W + 1) .. t
+//
+// One pass over the keys with a running reference maximum m and sum.  The two
+// products are dense contractions, so they run on the fifth-generation tensor
+// cores with their accumulators in tensor memory:
+//   * A tile is 128 query rows of one KV head: 128 / G consecutive tokens times
+//     the G heads of the group, so a short prompt of grouped heads still fills
+//     the M = 128 side and a tile's rows share one diagonal.
+//   * head_dim 128: a CTA holds two tiles (256 rows) and takes 128 keys at a
+//     time; while the softmax of one tile runs, the tensor cores work on the
+//     other's.  head_dim 256: one tile, 64 keys at a time, two score buffers,
+//     so the scores run one step ahead.
+//   * Q, K and V arrive by TMA tensor copies in the 128-byte-swizzled layout
+//     (K V ring of five 32 KB stages); V is read by the MMA as it lies, keys
+//     along rows (MN-major B), so nothing is transposed.
+//   * P goes to tensor memory in fp16 over the scores it came from and is the A
+//     operand of O += P V: no shared-memory round trip.
+// Warps: four softmax warps per tile (thread = row), one MMA warp, one load
+// warp.  The reference maximum moves only when a tile's maximum passes it by
+// more than kLazy (log2 units), so O in tensor memory is rescaled rarely; P
+// then stays <= 2^kLazy.  Scores, maxima, sums and O are float32; P is rounded
+// to fp16 (relative 2^-11 a weight), the operand type of the tensor cores.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "prompt.cuh"
+#include "tcgen05.cuh"
+
+namespace memra {
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr float kLazy = 8.f;
+
+template <int D>
+struct PromptCfg {
+  static constexpr int kTiles = D == 128 ? 2 : 1;       // query tiles of a CTA
+  static constexpr int kBufs = D == 128 ? 1 : 2;        // score buffers of a tile
+  static constexpr int kKeys = D == 128 ? 128 : 64;     // keys of a step
+  static constexpr int kStages = 5;
+  static constexpr int kBlocks = D / 64;                // 64-element column blocks of a row
+  static constexpr uint32_t kQBytes = kTileRows * D * 2;
+  static constexpr uint32_t kKvBytes = kKeys * D * 2;
+  static constexpr uint32_t kOffKv = kTiles * kQBytes;
+  static constexpr uint32_t kOffBar = kOffKv + kStages * kKvBytes;
+  static constexpr uint32_t kSmem = kOffBar + 256 + 1024;    // 1024: aligning the base
+  static constexpr int kThreads = 128 * kTiles + 64;
+  static constexpr uint32_t kOCol = 256;                // O behind the score buffers in tensor memory
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kTiles * kBufs * kKeys <= 256 && kTiles * D <= 256, "tensor memory");
+};
+
+// One TMA tensor copy: a box of a 3-D tensor map at (x, y, z) to shared memory.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// The sequence and the tile pair of this CTA, found from the packed lengths.
+struct Work {
+  int first, len;       // first row and rows of the sequence
+  int t0;               // first token of the CTA's first tile, within the sequence
+};
+
+// Steps [lo, hi) of kKeys keys that a tile of tokens t .. t + tpt - 1 takes; empty when the tile is.
+template <int D>
+__device__ __forceinline__ void tile_steps(const PromptParams &p, const Work &w, int t, int &lo, int &hi) {
+  constexpr int KT = PromptCfg<D>::kKeys;
+  lo = hi = 0;
+  if (t >= w.len) return;
+  const int last = min(w.len, t + p.tpt) - 1;
+  hi = last / KT + 1;
+  if (p.window > 0) lo = max(0, t - p.window + 1) / KT;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const PromptParams p) {
+  using C = PromptCfg<D>;
+  constexpr int NT = C::kTiles, NBUF = C::kBufs, KT = C::kKeys, ST = C::kStages;
+  constexpr int kMmaWarp = 4 * NT, kLoadWarp = 4 * NT + 1;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ Work s_work;
+  __shared__ uint32_t tmem_slot;
+  const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bars = sb + C::kOffBar;
+  auto kv_full = [&](int s) { return bars + 8 * s; };
+  auto kv_empty = [&](int s) { return bars + 8 * (ST + s); };
+  auto q_full = [&](int i) { return bars + 8 * (2 * ST + i); };
+  auto s_full = [&](int i, int b) { return bars + 8 * (2 * ST + 2 + 2 * i + b); };
+  auto p_full = [&](int i, int b) { return bars + 8 * (2 * ST + 6 + 2 * i + b); };
+  auto pv_done = [&](int i) { return bars + 8 * (2 * ST + 10 + i); };
+  const uint32_t v_zeroed = bars + 8 * (2 * ST + 12), drained = bars + 8 * (2 * ST + 13);
+
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  // Tiles are numbered sequence by sequence, a sequence's last (longest) first.
+  const int kvh = blockIdx.x % p.n_kv_heads, rank = blockIdx.x / p.n_kv_heads;
+  const int tpc = NT * p.tpt;                       // tokens of a CTA
+  if (warp == 0) {
+    int start = 0;
+    Work w{0, 0, -1};
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      int s = 0, e = 0;
+      if (b < p.batch) {
+        const int cs = p.cu_seqlens[b], ce = p.cu_seqlens[b + 1];
+        s = min(max(cs, 0), p.total);
+        e = min(max(ce, s), p.total);
+        if (blockIdx.x == 0 && (s != cs || e != ce)) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
+      }
+      const int tiles = (e - s + tpc - 1) / tpc;
+      int incl = tiles;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+      }
+      const int at = rank - start - (incl - tiles);
+      if (w.t0 < 0 && at >= 0 && at < tiles) w = Work{s, e - s, (tiles - 1 - at) * tpc};
+      const unsigned who = __ballot_sync(0xffffffffu, w.t0 >= 0);
+      start += __shfl_sync(0xffffffffu, incl, 31);
+      if (who && blockIdx.x != 0) {                 // CTA 0 checks every length
+        if (lane == __ffs(who) - 1) s_work = w;
+        break;
+      }
+      if (who && lane == __ffs(who) - 1) s_work = w;
+      if (!who && lane == 0) s_work = w;
+    }
+  }
+  if (tid == 32) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full(i), 1);
+      mbar_init(pv_done(i), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(s_full(i, b), 1);
+        mbar_init(p_full(i, b), 128);
+      }
+    }
+    mbar_init(v_zeroed, 1);
+    mbar_init(drained, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const Work w = s_work;
+  if (w.t0 < 0) return;                             // fewer tiles than the grid's bound
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(smem_addr(&tmem_slot), 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+
+  int lo[NT], hi[NT], jlo = 0, jhi = 0;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    tile_steps<D>(p, w, w.t0 + i * p.tpt, lo[i], hi[i]);
+    jhi = max(jhi, hi[i]);
+  }
+  jlo = lo[0];                                      // the first tile's keys start first, and it is never empty
+  const bool tail = jhi * KT > w.len;               // the last step's V holds rows behind the sequence
+  bool ok = true;
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------ loads --
+    const int slots = 2 * (jhi - jlo);
+    int issued = 0;
+    if (lane == 0) {
+      auto load_q = [&](int i) {
+        if (lo[i] == hi[i]) return;
+        mbar_arrive_expect_tx(q_full(i), static_cast<uint32_t>(p.group * p.tpt) * 128 * C::kBlocks);
+#pragma unroll
+        for (int c = 0; c < C::kBlocks; ++c)
+          tma_load_3d(sb + i * C::kQBytes + c * kTileRows * 128, &qmap, 64 * c, kvh * p.group,
+                      w.first + w.t0 + i * p.tpt, q_full(i));
+      };
+      load_q(0);
+      for (int n = 0; n < slots; ++n) {             // K and V of a step by turns
+        const int s = n % ST;
+        if (n >= ST) ok = mbar_wait_bounded(kv_empty(s), (n / ST - 1) & 1, p.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(kv_full(s), C::kKvBytes);
+#pragma unroll
+        for (int c = 0; c < C::kBlocks; ++c)
+          tma_load_3d(sb + C::kOffKv + s * C::kKvBytes + c * KT * 128, n & 1 ? &vmap : &kmap, 64 * c, kvh,
+                      w.first + (jlo + n / 2) * KT, kv_full(s));
+        issued = n + 1;
+        if (NT > 1 && n == 0) load_q(NT - 1);
+      }
+    }
+    __syncwarp();
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok && tail) {
+      // rows behind the sequence may hold anything, and 0 * inf is not 0: they become zeros
+      const int n = slots - 1, s = n % ST;
+      ok = mbar_wait_bounded(kv_full(s), (n / ST) & 1, p.status);
+      const int from = w.len - (jhi - 1) * KT;
+      const uint32_t v = sb + C::kOffKv + s * C::kKvBytes;
+      for (int i = lane; ok && i < (KT - from) * 8 * C::kBlocks; i += 32) {
+        const int u = i & 7, c = (i >> 3) % C::kBlocks, row = from + (i >> 3) / C::kBlocks;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + c * KT * 128 + row * 128 + 16 * u), "r"(0)
+                     : "memory");
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(v_zeroed);
+    }
+    // every copy has landed before the CTA can leave
+    if (lane == 0)
+      for (int n = max(0, issued - ST); n < issued; ++n) mbar_wait_bounded(kv_full(n % ST), (n / ST) & 1, p.status);
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------------------- MMA --
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
+      constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(kTileRows, D);
+      auto slot_full = [&](int n) { return mbar_wait_bounded(kv_full(n % ST), (n / ST) & 1, p.status); };
+      // S_i(j) = Q_i K(j)^T into score buffer b
+      auto mma_s = [&](int i, int b, int j) {
+        const int n = 2 * (j - jlo);
+        ok = ok && slot_full(n);
+        if (ok && j == lo[i]) ok = mbar_wait_bounded(q_full(i), 0, p.status);
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint32_t q = sb + i * C::kQBytes, k = sb + C::kOffKv + (n % ST) * C::kKvBytes;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc::mma_f16(tmem + (i * NBUF + b) * KT,
+                      tc::smem_desc_sw128(q + (ks / 4) * kTileRows * 128 + (ks % 4) * 32, 16, 1024),
+                      tc::smem_desc_sw128(k + (ks / 4) * KT * 128 + (ks % 4) * 32, 16, 1024), idesc_s, ks > 0);
+        tc::commit(s_full(i, b));
+      };
+      // O_i += P_i(j) V(j), P in the columns of its scores
+      auto mma_o = [&](int i, int b, int j) {
+        const int n = 2 * (j - jlo) + 1, u = j - lo[i];
+        ok = ok && mbar_wait_bounded(p_full(i, b), (u / NBUF) & 1, p.status);
+        ok = ok && slot_full(n);
+        if (ok && tail && j == jhi - 1) ok = mbar_wait_bounded(v_zeroed, 0, p.status);
+        if (!ok) return;
+        tc::fence_after_sync();
+        const uint32_t v = sb + C::kOffKv + (n % ST) * C::kKvBytes;
+#pragma unroll
+        for (int ks = 0; ks < KT / 16; ++ks)
+          tc::mma_f16_ta(tmem + C::kOCol + i * D, tmem + (i * NBUF + b) * KT + 8 * ks,
+                         tc::smem_desc_sw128(v + ks * 2048, KT * 128, 1024), idesc_o, u > 0 || ks > 0);
+        if (NBUF > 1 || j == hi[i] - 1) tc::commit(pv_done(i));
+      };
+      auto release = [&](int n) {
+        if (ok) tc::commit(kv_empty(n % ST));
+      };
+      if constexpr (NT == 2) {
+        for (int j = jlo; j < jhi && ok; ++j) {
+          for (int i = 0; i < NT; ++i)
+            if (j == lo[i] && lo[i] < hi[i]) mma_s(i, 0, j);
+          release(2 * (j - jlo));                   // every tile's scores of step j are issued
+          for (int i = 0; i < NT; ++i) {
+            if (j >= lo[i] && j < hi[i]) mma_o(i, 0, j);
+            if (ok && j >= lo[i] && j + 1 < hi[i]) mma_s(i, 0, j + 1);
+          }
+          release(2 * (j - jlo) + 1);
+        }
+      } else {
+        auto scores = [&](int j) {
+          if (!ok || j >= jhi) return;
+          mma_s(0, (j - jlo) & 1, j);
+          release(2 * (j - jlo));
+        };
+        scores(jlo);
+        scores(jlo + 1);
+        for (int j = jlo; j < jhi && ok; ++j) {
+          mma_o(0, (j - jlo) & 1, j);
+          release(2 * (j - jlo) + 1);
+          scores(j + 2);                            // behind the product that reads its buffer's P
+        }
+      }
+      // what was issued has completed before the CTA can leave
+      tc::commit(drained);
+      mbar_wait_bounded(drained, 0, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax --
+    const int i = NT == 1 ? 0 : warp >> 2;
+    const int rl = tid & 127;
+    const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int tl = rl / p.group, t = w.t0 + i * p.tpt + tl;       // the row's token within the sequence
+    const bool live = tl < p.tpt && t < w.len;
+    const int tile_first = w.t0 + i * p.tpt, tile_last = min(w.len, tile_first + p.tpt) - 1;
+    const int n_steps = hi[i] - lo[i];
+    float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+    const uint32_t o_col = tmem + tlane + C::kOCol + i * D;
+#pragma unroll 1
+    for (int u = 0; u < n_steps; ++u) {
+      const int j = lo[i] + u, b = NBUF > 1 ? u & 1 : 0;
+      const uint32_t s_col = tmem + tlane + (i * NBUF + b) * KT;
+      ok = mbar_wait_bounded(s_full(i, b), (u / NBUF) & 1, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::fence_after_sync();
+      uint32_t s[KT];
+#pragma unroll
+      for (int c = 0; c < KT; c += 32) tc::ld_32x32b_x32(s_col + c, s + c);
+      tc::wait_ld_all();
+      tc::hold<KT>(s);
+      // keys behind the row's token, or before its window
+      if (j * KT + KT - 1 > tile_first || (p.window > 0 && j * KT < tile_last - p.window + 1)) {
+        const int last = t - j * KT, first = p.window > 0 ? last - p.window + 1 : 0;
+#pragma unroll
+        for (int c = 0; c < KT; ++c)
+          if (c > last || c < first) s[c] = 0xff800000u;          // -inf
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < KT; c += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[c + e]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      float alpha = 1.f;
+      if (live && top > m + kLazy) {                // also the first step with a key (m = -inf)
+        if (m != -INFINITY) alpha = fast_exp2(m - top);
+        m = top;
+      }
+      if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O's rows of this warp times alpha, once the product before has completed
+        // (one score buffer: these scores were issued behind it)
+        if (NBUF > 1) {
+          ok = mbar_wait_bounded(pv_done(i), (u - 1) & 1, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc::ld_32x32b_x32(o_col + c, o);
+          tc::wait_ld_all();
+          tc::hold<32>(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tc::st_32x32b_x32(o_col + c, o);
+        }
+        l0 *= alpha;
+        l1 *= alpha;
+      }
+      const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int c = 0; c < KT; c += 64) {
+        uint32_t w2[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float p0 = fast_exp2(fmaf(__uint_as_float(s[c + 2 * e]), p.scale_log2, -mu));
+          const float p1 = fast_exp2(fmaf(__uint_as_float(s[c + 2 * e + 1]), p.scale_log2, -mu));
+          l0 += p0;
+          l1 += p1;
+          w2[e] = pack_half2(p0, p1);
+        }
+        tc::st_32x32b_x32(s_col + c / 2, w2);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(p_full(i, b));
+    }
+    // The last product.  Two score buffers: the product before it may still be
+    // running, so its phase comes first (a parity names only the next phase).
+    if (NBUF > 1 && n_steps > 1 && ok) ok = mbar_wait_bounded(pv_done(i), (n_steps - 2) & 1, p.status);
+    if (n_steps > 0 && ok) ok = mbar_wait_bounded(pv_done(i), NBUF > 1 ? (n_steps - 1) & 1 : 0, p.status);
+    if (__all_sync(0xffffffffu, n_steps > 0 && ok)) {
+      tc::fence_after_sync();
+      const float l = l0 + l1, inv = l > 0.f ? 1.f / l : 0.f;
+      const int head = kvh * p.group + rl % p.group;
+      __half *dst = p.out + (static_cast<size_t>(w.first + t) * p.n_heads + head) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tc::ld_32x32b_x32(o_col + c, o);
+        tc::wait_ld_all();
+        tc::hold<32>(o);
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 x;
+            x.x = pack_half2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+            x.y = pack_half2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            x.z = pack_half2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+            x.w = pack_half2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+            *reinterpret_cast<uint4 *>(dst + c + e) = x;
+          }
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// The driver's tensor-map encoder, looked up once (the library links the runtime only).
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// [tokens][heads][D] fp16 as a 3-D map with boxes of 64 elements x heads x tokens, 128-byte swizzle.
+bool encode_rows(CUtensorMap *map, const void *base, int D, int heads, int tokens, int64_t stride, int box_heads,
+                 int box_tokens) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_one(const PromptParams &p, cudaStream_t st) {
+  using C = PromptCfg<D>;
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  CUtensorMap qm, km, vm;
+  if (!encode_rows(&qm, p.q, D, p.n_heads, p.total, p.q_stride, p.group, p.tpt) ||
+      !encode_rows(&km, p.k, D, p.n_kv_heads, p.total, p.k_stride, 1, C::kKeys) ||
+      !encode_rows(&vm, p.v, D, p.n_kv_heads, p.total, p.v_stride, 1, C::kKeys))
+    return cudaErrorInvalidValue;
+  // at most this many CTAs' worth of tokens, whatever the lengths: one partial each sequence
+  const int64_t tiles = static_cast<int64_t>(p.total) / (C::kTiles * p.tpt) + p.batch;
+  const int64_t grid = tiles * p.n_kv_heads;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(prompt_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, st, qm, km, vm,
+                    p);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(int D, const PromptParams &p, cudaStream_t st) {
+  return D == 128 ? launch_one<128>(p, st) : launch_one<256>(p, st);
+}
+
+}  // namespace memra

@@ -304,6 +304,35 @@ int memra_decode_step_cascade(const memra_kv_cache *cache, const void *k_new, co
                               int32_t n_kv_heads, int32_t head_dim, float sm_scale, void *workspace,
                               size_t workspace_bytes, void *out, void *stream);
 
+/* Causal attention of whole prompts, packed one behind the other: what runs
+ * before memra_kv_append stores a prompt's rows and decoding begins.
+ *   q           device fp16, token t's heads at q + t * q_stride, [n_heads][head_dim]
+ *   k, v        device fp16, token t's heads at k + t * k_stride (v: v_stride),
+ *               [n_kv_heads][head_dim]
+ *   *_stride    elements from one token to the next, multiples of 8, at least
+ *               the token's heads (wider when q, k and v share one buffer)
+ *   cu_seqlens  device int32 [batch + 1]: sequence b is the rows cu_seqlens[b]
+ *               .. cu_seqlens[b+1] - 1, non-decreasing, between 0 and
+ *               total_tokens; a sequence may be empty.  Lengths that are not so
+ *               are clamped and set MEMRA_DEVERR_BAD_SEQ_LEN in *status.
+ *   total_tokens  rows of q, k and v (host); rows of no sequence may hold
+ *               anything, and their rows of out are left as they are
+ *   sm_scale    softmax scale, finite and > 0
+ *   window      0: the row of token p (within its sequence) sees keys 0 .. p;
+ *               > 0: keys max(0, p - window + 1) .. p
+ *   out         device fp16 [total_tokens][n_heads][head_dim]
+ *   status      device int32 the kernel ORs MEMRA_DEVERR_* bits into, or NULL
+ * n_heads % n_kv_heads == 0, n_heads / n_kv_heads <= MEMRA_MAX_GROUP, head_dim
+ * 128 or 256, batch and n_kv_heads <= 65535.  Scores, softmax and output are
+ * accumulated in float32; the weights enter the product with V in fp16.  A
+ * sequence's result bytes are the same alone or packed with others, and no two
+ * sequences see each other's rows.  No workspace.  batch == 0 or total_tokens
+ * == 0 is a no-op. */
+int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, const int32_t *cu_seqlens, int32_t batch, int32_t total_tokens,
+                      int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale, int32_t window, void *out,
+                      int32_t *status, void *stream);
+
 /* Copies whole pages inside both pools: page src_pages[i] to page dst_pages[i]
  * for i < n, every KV head's K and V segments, byte for byte.  It serves a fork
  * (the new sequence shares the full pages of its parent and gets a copy of the

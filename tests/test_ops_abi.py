@@ -66,3 +66,37 @@ def test_compact_checks(memra):
     assert call(maxlen=-1) == INVALID
     assert call(B=0) == 0
     assert call(most=0) == 0
+
+
+def test_prompt_checks(memra):
+    good = dict(q=64, qs=1024, k=64, ks=256, v=64, vs=256, cu=64, B=2, T=10, Hq=8, Hkv=2, D=128, scale=0.1, window=0,
+                out=64, status=0)
+
+    def call(**kw):
+        a = {**good, **kw}
+        return memra.lib().memra_prompt_attn(a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["cu"], a["B"], a["T"],
+                                             a["Hq"], a["Hkv"], a["D"], a["scale"], a["window"], a["out"], a["status"],
+                                             None)
+
+    assert call(B=0) == 0
+    assert call(T=0) == 0
+    for name in ("q", "k", "v", "out"):
+        assert call(**{name: 0}) == INVALID
+        assert call(**{name: 72}) == INVALID
+    assert call(cu=0) == INVALID
+    assert call(cu=66) == INVALID
+    assert call(status=66) == INVALID
+    assert call(qs=1016) == INVALID                # less than a token's heads
+    assert call(ks=248) == INVALID
+    assert call(vs=260) == INVALID                 # not a multiple of 8
+    assert call(qs=1 << 38) == UNSUPPORTED
+    assert call(Hq=7) == INVALID
+    assert call(Hkv=0) == INVALID
+    assert call(D=64) == UNSUPPORTED
+    assert call(Hq=129 * 2, qs=129 * 256) == UNSUPPORTED
+    assert call(window=-1) == INVALID
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(scale=scale) == INVALID
+    assert call(B=65536) == UNSUPPORTED
+    assert call(B=-1) == INVALID
+    assert call(T=-1) == INVALID
