@@ -98,6 +98,11 @@ _SIGS = {
     "memra_prompt_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64] * 3 + [ctypes.c_void_p] +
                           [ctypes.c_int32] * 5 + [ctypes.c_float, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
                                                   ctypes.c_void_p]),
+    "memra_tree_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 5),
+    "memra_tree_attn": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p] +
+                        [ctypes.c_int32] * 5 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                                ctypes.c_void_p]),
     "memra_kv_copy_pages": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_void_p,
                                            ctypes.c_int32, ctypes.c_void_p]),
     "memra_kv_compact": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int32,
@@ -330,6 +335,24 @@ def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status
                                    int(cu_seqlens.shape[0]) - 1, T, Hq, Hkv, D,
                                    float(sm_scale if sm_scale is not None else D ** -0.5), int(window), _ptr(out),
                                    _ptr(status), _stream(stream)), "memra_prompt_attn")
+
+
+def tree_attn_workspace_bytes(batch: int, n_nodes: int, n_heads: int, head_dim: int, max_seq_len: int) -> int:
+    return int(lib().memra_tree_attn_workspace_bytes(batch, n_nodes, n_heads, head_dim, max_seq_len))
+
+
+def tree_attn(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, tree_mask, out, workspace, sm_scale=None,
+              stream=None) -> None:
+    """memra_tree_attn: q fp16 [B, N, Hq, D], a tree of N drafted nodes per sequence -> out fp16 [B, N, Hq, D].
+
+    The tree's rows are the last N of each sequence (seq_lens include them).
+    tree_mask int64 [B, N]: bit j of word [b, i] shows node j to node i; every
+    node sees all keys before the tree.
+    """
+    a = _decode_args(cache, q, page_table, seq_lens, max_seq_len, out, workspace, sm_scale)
+    if tuple(tree_mask.shape) != tuple(q.shape[:2]):
+        raise MemraError(1, "memra_tree_attn")
+    _check(lib().memra_tree_attn(*a[:6], _ptr(tree_mask), *a[6:], _stream(stream)), "memra_tree_attn")
 
 
 def kv_copy_pages(cache: KVCache, src_pages, dst_pages, n: int | None = None, stream=None) -> None:

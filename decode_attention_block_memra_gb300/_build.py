@@ -24,9 +24,11 @@ LIB = os.path.join(HERE, "libmemra.so")
 STAMP = LIB + ".sha256"
 
 SOURCES = ["api.cu", "kv_append.cu", "combine.cu", "decode_d128.cu", "decode_d256.cu", "noalloc.cu", "cascade.cu",
-           "api_pages.cu", "pages.cu", "api_prompt.cu", "prompt.cu"]
+           "api_pages.cu", "pages.cu", "api_prompt.cu", "prompt.cu",
+           "api_tree.cu", "tree.cu"]
 HEADERS = ["memra_device.cuh", "decode_kernel.cuh", "kv_quant.cuh", "cascade.cuh", "tcgen05.cuh",
-           "host_checks.cuh", "pages.cuh", "prompt.cuh"]
+           "host_checks.cuh", "pages.cuh", "prompt.cuh", "kv_stage.cuh",
+           "tree.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]

@@ -25,19 +25,6 @@ struct Plan {
   size_t smem;
 };
 
-// Streaming multiprocessors of the current device (queried once per device).
-int device_sms() {
-  static int cached[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  if (!cached[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 1;
-    cached[dev] = n;
-  }
-  return cached[dev];
-}
-
 // Splits one long sequence gets per KV head: one wave of the GPU.
 int split_target(const Plan &pl, int n_kv_heads) {
   const int t = device_sms() * pl.ctas_per_sm / (n_kv_heads > 0 ? n_kv_heads : 1);

@@ -333,6 +333,42 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
                       int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale, int32_t window, void *out,
                       int32_t *status, void *stream);
 
+/* Largest number of nodes of a draft tree (new tokens per sequence) that
+ * memra_tree_attn and memra_kv_compact take. */
+#define MEMRA_MAX_TREE_NODES 64
+
+/* Attention of a tree of drafted tokens over the paged cache: the verify step
+ * of tree speculation, where memra_decode_attn verifies one chain.
+ *   q             device fp16 [batch][n_nodes][n_heads][head_dim]
+ *   page_table    device int32 [batch][max_pages_per_seq]
+ *   seq_lens      device int32 [batch]; lengths INCLUDING the n_nodes rows of
+ *                 the tree, which are the sequence's last (append them first
+ *                 with memra_kv_append): node j sits at seq_lens[b]-n_nodes+j
+ *   max_seq_len   host upper bound of seq_lens
+ *   tree_mask     device uint64 [batch][n_nodes], 8-byte aligned: node i of
+ *                 sequence b sees node j (itself included) iff bit j of word
+ *                 [b][i] is set; bits >= n_nodes are ignored.  Every node sees
+ *                 all keys before the tree.
+ *   n_nodes       1 .. MEMRA_MAX_TREE_NODES.  A sequence with fewer nodes pads
+ *                 its tree with rows that no word names.
+ *   workspace     device, >= memra_tree_attn_workspace_bytes(...) bytes
+ *   out           device fp16 [batch][n_nodes][n_heads][head_dim]
+ * All K and V formats, head_dim 128 or 256, n_heads / n_kv_heads <=
+ * MEMRA_MAX_GROUP, n_kv_heads <= 65535, batch * ceil(n_nodes * n_heads /
+ * n_kv_heads / 128) <= 65535; sm_scale finite.  K^ and V^ enter the products
+ * exactly (or as fp16 pairs), the softmax weights in fp16; everything is
+ * accumulated in float32.  A sequence's result bytes are the same alone or in
+ * any batch.  A row that sees no key yields zeros.  A sequence shorter than n_nodes
+ * sets MEMRA_DEVERR_BAD_SEQ_LEN; its nodes at positions below 0 are seen by
+ * no row and yield zeros.  Keys of a page id outside the pool are left out
+ * (MEMRA_DEVERR_BAD_PAGE).  batch == 0 is a no-op. */
+size_t memra_tree_attn_workspace_bytes(int32_t batch, int32_t n_nodes, int32_t n_heads, int32_t head_dim,
+                                       int32_t max_seq_len);
+int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *page_table, int32_t max_pages_per_seq,
+                    const int32_t *seq_lens, int32_t max_seq_len, const uint64_t *tree_mask, int32_t batch,
+                    int32_t n_nodes, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale,
+                    void *workspace, size_t workspace_bytes, void *out, void *stream);
+
 /* Copies whole pages inside both pools: page src_pages[i] to page dst_pages[i]
  * for i < n, every KV head's K and V segments, byte for byte.  It serves a fork
  * (the new sequence shares the full pages of its parent and gets a copy of the
@@ -345,10 +381,6 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
  * run in no particular order.  n == 0 is a no-op. */
 int memra_kv_copy_pages(const memra_kv_cache *cache, const int32_t *src_pages, const int32_t *dst_pages, int32_t n,
                         void *stream);
-
-/* Largest number of nodes of a draft tree (new tokens per sequence) that
- * memra_tree_attn and memra_kv_compact take. */
-#define MEMRA_MAX_TREE_NODES 64
 
 /* Keeps the accepted nodes of a verified draft tree.  The rows of a sequence's
  * n_nodes tree nodes lie at positions base .. base + n_nodes - 1, base =

@@ -1,0 +1,284 @@
+"""Tree attention on the GPU against its definition in float64 over the oracle's dequantized cache.
+
+Tolerance, per output element, from the arithmetic (u = 2^-11, half a step of
+fp16, relative): the output's rounding u |o|; each weight's rounding to fp16,
+u sum p |v| / sum p, or 2^-25 absolute for a weight below fp16's normal range
+(the largest weight of a split is at least 1); the float32 scores, each K = 16
+step of a product (hi and lo parts: twice head_dim / 16 of them) off by at most
+2^-22 of the absolute products so far, and 2^-19 for exponentials, sums and the
+merge: a relative error of twice that on every weight; and 2^-21 of the largest
+value for a dequantized pair hi + lo, with its share on the scores.
+"""
+import numpy as np
+import pytest
+
+import workloads as W
+from oracle import attention, quant
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -11
+PAIRS = [(k, v) for k in W.K_FORMATS for v in W.V_FORMATS]
+
+
+@pytest.fixture(scope="module")
+def memra():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_attention_block_memra_gb300 import _build
+    _build.build()
+    import decode_attention_block_memra_gb300 as m
+    m.lib()
+    return m
+
+
+def random_tree(rng, nodes):
+    """Words of a random tree: bit j of word i, node j is on node i's path from a root (i included)."""
+    words = np.zeros(nodes, np.uint64)
+    for i in range(nodes):
+        parent = rng.integers(-1, i) if i else -1
+        words[i] = np.uint64(1 << i) | (words[parent] if parent >= 0 else np.uint64(0))
+    return words
+
+
+def chain(nodes):
+    return np.array([(1 << (i + 1)) - 1 for i in range(nodes)], np.uint64)
+
+
+def reference(w, words, lens=None, missing_pages=()):
+    """(o, tolerance) float64 [B, N, Hq, D] of the workload's rows under the mask words."""
+    cache = attention.quantize_cache(w)
+    B, N, Hq, D = w.q.shape
+    G = w.group
+    o, tol = np.zeros(w.q.shape), np.zeros(w.q.shape)
+    for b in range(B):
+        T = int(w.seq_lens[b])
+        rows = attention.sequence_rows(w, b)
+        key = np.arange(T) - (T - N)
+        sees = np.ones((N, T), bool)
+        for i in range(N):
+            for j in range(N):
+                sees[i, T - N + j] = bool(int(words[b, i]) >> j & 1)
+        for col in missing_pages:
+            sees[:, 16 * col:16 * col + 16] = False
+        assert key[-1] == N - 1
+        for h in range(w.n_kv_heads):
+            k = quant.dequantize_rows(quant.select_rows(cache["k"][h], rows)).astype(np.float64)
+            v = quant.dequantize_rows(quant.select_rows(cache["v"][h], rows)).astype(np.float64)
+            q = w.q[b, :, h * G:(h + 1) * G].astype(np.float64)
+            s = np.einsum("igd,td->igt", q, k) * w.sm_scale
+            mass = np.einsum("igd,td->igt", np.abs(q), np.abs(k)) * w.sm_scale
+            s = np.where(sees[:, None], s, -np.inf)
+            top = s.max(-1, keepdims=True)
+            p = np.exp(s - np.where(np.isfinite(top), top, 0))
+            l = p.sum(-1, keepdims=True)
+            p = np.divide(p, l, out=np.zeros_like(p), where=l > 0)
+            mass = np.where(sees[:, None], mass, 0).max(-1, keepdims=True)
+            step = 2 * ((D // 8 + 2) * 2.0 ** -22 * mass + 2.0 ** -21 * mass + 2.0 ** -19)
+            heads = slice(h * G, (h + 1) * G)
+            o[b, :, heads] = p @ v
+            tol[b, :, heads] = (U * np.abs(p @ v) + (U + step) * (p @ np.abs(v)) +
+                                (T * 2.0 ** -25 + 2.0 ** -21) * np.abs(v).max())
+    return o, tol
+
+
+def run(memra, w, words, mask_extra=None, max_seq_len=None, sm_scale=None, seed=3, sentinel=True):
+    from decode_attention_block_memra_gb300.runner import upload
+    dw = upload(w, fill_seed=seed)
+    memra.kv_append(dw.cache, dw.step_k, dw.step_v, dw.step_slots)
+    B, N, Hq, D = w.q.shape
+    M = max_seq_len or w.max_seq_len
+    n = memra.tree_attn_workspace_bytes(B, N, Hq, D, M)
+    ws = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda")      # NaN everywhere
+    mask = torch.from_numpy(words.view(np.int64).copy()).cuda()
+    dw.out.fill_(float("nan"))
+    args = (dw.cache, dw.q, dw.page_table, dw.seq_lens, M, mask, dw.out, ws, sm_scale or w.sm_scale)
+    memra.tree_attn(*args)
+    return dw, args
+
+
+def check(memra, w, words, **kw):
+    dw, args = run(memra, w, words, **kw)
+    assert memra.read_status(dw.cache) == 0
+    want, tol = reference(w, words)
+    got = dw.out.cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    worst = float((np.abs(got - want) / tol).max())
+    assert worst <= 1, worst
+    return dw, args, got
+
+
+def words_for(w, seed=0, make=random_tree):
+    rng = np.random.default_rng(seed)
+    return np.stack([make(rng, w.q_len) for _ in range(w.batch)])
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("kf,vf", PAIRS)
+def test_formats(memra, kf, vf, D):
+    w = W.random_case(50 + D, batch=3, q_len=9, n_heads=16, n_kv_heads=2, head_dim=D, k_fmt=kf, v_fmt=vf,
+                      ctx=(9, 1700))
+    check(memra, w, words_for(w, 1))
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("nodes,n_heads,n_kv_heads", [
+    (1, 8, 2), (2, 4, 4), (16, 32, 4), (17, 32, 4),      # 128 rows, then two tiles
+    (33, 16, 2), (64, 8, 2), (64, 16, 2),                # 264, 256 and 512 rows of a KV head
+    (5, 6, 2), (13, 10, 2), (64, 3, 3), (3, 128, 1), (64, 12, 1)])
+def test_shapes(memra, nodes, n_heads, n_kv_heads, D):
+    w = W.random_case(nodes * 7 + n_heads, batch=2, q_len=nodes, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=D,
+                      ctx=(nodes, 700))
+    check(memra, w, words_for(w, nodes))
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("T", [4, 5, 15, 16, 17, 31, 32, 33, 63, 64, 65, 68, 127, 128, 132, 511, 512, 513, 516, 1024,
+                               1027])
+def test_length_edges(memra, T, D):
+    # T = 4: the tree alone, no key before it
+    w = W.make_workload(f"t{T}", batch=1, q_len=4, n_heads=8, n_kv_heads=1, head_dim=D, k_fmt="q8_0", v_fmt="q5_1",
+                        seed=T, seq_lens=[T], permute_pages=True, extra_pages=2)
+    check(memra, w, words_for(w, T))
+
+
+def test_rows_that_see_nothing(memra):
+    w = W.make_workload("empty", batch=2, q_len=6, n_heads=8, n_kv_heads=2, head_dim=128, k_fmt="q8_0", v_fmt="q5_1",
+                        seed=1, seq_lens=[6, 40], permute_pages=True, extra_pages=2)
+    words = np.zeros((2, 6), np.uint64)
+    words[0, 3] = 1 << 5                     # one row of the first sequence sees one node, a later one
+    dw, _, got = check(memra, w, words)
+    assert (got[0, [0, 1, 2, 4, 5]] == 0).all() and (got[1] != 0).any()
+
+
+def test_bits_past_the_tree_are_ignored(memra):
+    w = W.random_case(5, batch=2, q_len=7, n_heads=8, n_kv_heads=2, ctx=(7, 90))
+    words = words_for(w, 2)
+    _, _, want = check(memra, w, words)
+    dw, _ = run(memra, w, words | np.uint64(0xFFFFFFFFFFFFFF80))
+    assert np.array_equal(dw.out.cpu().numpy().astype(np.float64), want)
+
+
+def test_a_chain_is_the_causal_verify(memra):
+    w = W.random_case(6, batch=3, q_len=5, n_heads=16, n_kv_heads=4, ctx=(100, 2600))
+    words = np.stack([chain(5)] * 3)
+    dw, _, got = check(memra, w, words)
+    out = torch.empty_like(dw.out)
+    memra.decode_attn(dw.cache, dw.q, dw.page_table, dw.seq_lens, w.max_seq_len, out, dw.workspace, w.sm_scale)
+    assert np.abs(out.cpu().numpy().astype(np.float64) - got).max() <= 4e-3     # 2e-3 from the definition each
+
+
+@pytest.mark.parametrize("D,lens", [(128, [40000]), (256, [21000, 530]), (128, [9000, 70, 2049])])
+def test_many_splits(memra, D, lens):
+    w = W.make_workload("long", batch=len(lens), q_len=4, n_heads=8, n_kv_heads=2, head_dim=D, k_fmt="q8_0",
+                        v_fmt="q5_1", seed=7, seq_lens=lens, permute_pages=True)
+    check(memra, w, words_for(w, 3))
+
+
+def test_splits_at_their_largest(memra):
+    # 16 KV heads x 8 row CTAs leave the plan about one split: more than 8,192 keys make more than the target
+    w = W.make_workload("wide", batch=1, q_len=64, n_heads=16 * 32, n_kv_heads=16, head_dim=128, k_fmt="fp8",
+                        v_fmt="fp8", seed=8, seq_lens=[8192 + 8192 + 70])
+    words = words_for(w, 4)
+    dw, args = run(memra, w, words)
+    assert memra.read_status(dw.cache) == 0
+    got = dw.out.cpu().numpy().astype(np.float64)
+    # two KV heads of the sixteen, against the definition
+    for h in (0, 15):
+        one = W.Workload(**{**w.__dict__})
+        one.n_heads, one.n_kv_heads = 32, 1
+        one.q = w.q[:, :, 32 * h:32 * h + 32]
+        one.k_rows, one.v_rows = w.k_rows[:, h:h + 1], w.v_rows[:, h:h + 1]
+        want, tol = reference(one, words)
+        assert (np.abs(got[:, :, 32 * h:32 * h + 32] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_same_bytes_alone_or_batched(memra, D):
+    w = W.random_case(9, batch=3, q_len=6, n_heads=16, n_kv_heads=2, head_dim=D, ctx=(300, 3000))
+    words = words_for(w, 5)
+    dw, args, got = check(memra, w, words)
+    for b in range(3):
+        out = torch.empty_like(dw.out[b:b + 1])
+        memra.tree_attn(dw.cache, dw.q[b:b + 1], dw.page_table[b:b + 1].contiguous(), dw.seq_lens[b:b + 1].clone(),
+                        int(w.seq_lens[b]), args[5][b:b + 1].contiguous(), out, args[7], w.sm_scale)
+        assert torch.equal(out[0], dw.out[b])
+
+
+def test_peaked_scores_and_a_negative_scale(memra):
+    w = W.random_case(10, batch=2, q_len=8, n_heads=16, n_kv_heads=2, ctx=(500, 1500))
+    w.q = (w.q.astype(np.float32) * 40).astype(np.float16)
+    check(memra, w, words_for(w, 6))
+    w2 = W.random_case(11, batch=2, q_len=8, n_heads=16, n_kv_heads=2, ctx=(500, 1500))
+    words = words_for(w2, 7)
+    dw, _ = run(memra, w2, words, sm_scale=-w2.sm_scale)
+    w2.q = -w2.q
+    want, tol = reference(w2, words)
+    assert (np.abs(dw.out.cpu().numpy().astype(np.float64) - want) <= tol).all()
+
+
+def test_bad_pages_are_left_out(memra):
+    w = W.random_case(12, batch=1, q_len=4, n_heads=8, n_kv_heads=2, ctx=(300, 300))
+    words = words_for(w, 8)
+    dw, args = run(memra, w, words)
+    memra.read_status(dw.cache)
+    table = dw.page_table.clone()
+    table[0, 3], table[0, 5] = w.num_pages, -1
+    memra.tree_attn(dw.cache, dw.q, table, *args[3:])
+    assert memra.read_status(dw.cache) == memra.DEVERR_BAD_PAGE
+    want, tol = reference(w, words, missing_pages=(3, 5))
+    assert (np.abs(dw.out.cpu().numpy().astype(np.float64) - want) <= tol).all()
+
+
+def test_lengths_out_of_range(memra):
+    w = W.random_case(13, batch=2, q_len=6, n_heads=8, n_kv_heads=2, ctx=(100, 100))
+    words = words_for(w, 9)
+    dw, args = run(memra, w, words)
+    for lens, M in (([100, 4], 100), ([100, 10 ** 9], 10 ** 9), ([-7, 0], 100)):
+        dw.out.fill_(float("nan"))
+        n = memra.tree_attn_workspace_bytes(2, 6, 8, 128, min(M, 112))
+        M = min(M, 112)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+        memra.tree_attn(dw.cache, dw.q, dw.page_table, torch.tensor(lens, dtype=torch.int32, device="cuda"), M,
+                        args[5], dw.out, ws, w.sm_scale)
+        assert memra.read_status(dw.cache) == memra.DEVERR_BAD_SEQ_LEN
+        assert bool(torch.isfinite(dw.out).all())
+        for b, T in enumerate(lens):
+            if T < 6:                        # nodes at positions below 0
+                assert bool((dw.out[b, :6 - max(T, 0)] == 0).all())
+
+
+def test_captured_call_reads_new_lengths_and_words(memra):
+    w = W.random_case(14, batch=2, q_len=4, n_heads=8, n_kv_heads=2, ctx=(900, 1300))
+    words = words_for(w, 10)
+    dw, args, got = check(memra, w, words)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        memra.tree_attn(*args)
+    dw.out.zero_()
+    g.replay()
+    assert np.array_equal(dw.out.cpu().numpy().astype(np.float64), got)
+    other = words_for(w, 11)
+    args[5].copy_(torch.from_numpy(other.view(np.int64).copy()))
+    g.replay()
+    want, tol = reference(w, other)
+    assert (np.abs(dw.out.cpu().numpy().astype(np.float64) - want) <= tol).all()
+
+
+def test_two_streams_with_their_own_workspaces(memra):
+    w = W.random_case(15, batch=2, q_len=8, n_heads=32, n_kv_heads=4, ctx=(3000, 5000))
+    words = words_for(w, 12)
+    dw, args, got = check(memra, w, words)
+    outs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        out, ws = torch.empty_like(dw.out), torch.empty_like(args[7])
+        outs.append((out, ws))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, (out, ws) in zip(streams, outs):
+            memra.tree_attn(*args[:6], out, ws, args[8], stream=s)
+    torch.cuda.synchronize()
+    for out, _ in outs:
+        assert torch.equal(out, dw.out)

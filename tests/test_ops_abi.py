@@ -100,3 +100,43 @@ def test_prompt_checks(memra):
     assert call(B=65536) == UNSUPPORTED
     assert call(B=-1) == INVALID
     assert call(T=-1) == INVALID
+
+
+def test_tree_checks(memra):
+    good = dict(q=64, pt=64, maxp=4, sl=64, maxlen=64, mask=64, B=2, N=8, Hq=8, Hkv=2, D=128, scale=0.1, ws=64,
+                wsb=1 << 20, out=64)
+
+    def call(c=None, **kw):
+        a = {**good, **kw}
+        return memra.lib().memra_tree_attn(ctypes.byref(c or cache(memra)), a["q"], a["pt"], a["maxp"], a["sl"],
+                                           a["maxlen"], a["mask"], a["B"], a["N"], a["Hq"], a["Hkv"], a["D"],
+                                           a["scale"], a["ws"], a["wsb"], a["out"], None)
+
+    assert call(B=0) == 0
+    for name in ("q", "pt", "sl", "mask", "out"):
+        assert call(**{name: 0}) == INVALID
+    for name, at in (("q", 72), ("out", 72), ("pt", 66), ("sl", 66), ("mask", 68)):
+        assert call(**{name: at}) == INVALID
+    assert call(c=cache(memra, k_pool=72)) == INVALID
+    assert call(c=cache(memra, v_fmt=0)) == UNSUPPORTED
+    assert call(N=0) == INVALID
+    assert call(N=memra.MAX_TREE_NODES + 1) == UNSUPPORTED
+    assert call(Hq=7) == INVALID
+    assert call(Hkv=4) == INVALID                  # not the cache's
+    assert call(D=256) == INVALID
+    assert call(Hq=2 * 129) == UNSUPPORTED
+    assert call(B=-1) == INVALID
+    assert call(B=65536) == UNSUPPORTED
+    assert call(maxp=0) == INVALID
+    assert call(maxlen=-1) == INVALID
+    assert call(scale=float("nan")) == INVALID
+    need = memra.tree_attn_workspace_bytes(2, 8, 8, 128, 5000)
+    assert need == 2 * 8 * 8 * 10 * 129 * 4        # ten splits of 512 tokens at most
+    assert call(maxlen=5000, wsb=need - 1) == WORKSPACE
+    assert call(maxlen=5000, wsb=need, ws=72) == INVALID
+    assert call(maxlen=5000, wsb=need, ws=0) == INVALID
+    assert memra.tree_attn_workspace_bytes(2, 8, 8, 128, 512) == 0
+    assert memra.tree_attn_workspace_bytes(2, 65, 8, 128, 5000) == 0
+    assert memra.tree_attn_workspace_bytes(2, 8, 8, 64, 5000) == 0
+    # 262,144 tokens: 160 partials a row, whatever the device
+    assert memra.tree_attn_workspace_bytes(1, 64, 32, 128, 262144) == 64 * 32 * 160 * 129 * 4
