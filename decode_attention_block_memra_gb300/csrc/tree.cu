@@ -10,9 +10,9 @@
 // sequence and row tiles):
 //   * a producer thread copies raw pages into a ring of three chunks;
 //   * eight staging warps dequantize a chunk's K and V into double-buffered
-//     fp16 operand tiles (core-matrix order): exact hi + lo pairs for q8_0,
-//     q5_1 and q4_0, single values for fp8 and NVFP4 (kv_stage.cuh), so only P
-//     is rounded (fp16, relative 2^-11 a weight);
+//     fp16 operand tiles: exact hi + lo pairs for q8_0, q5_1 and q4_0, single
+//     values for fp8 and NVFP4, so only P is rounded (fp16, relative 2^-11 a
+//     weight); q5_1's minima are a narrow tile of their own;
 //   * one MMA thread: S = Q K^T with Q in tensor memory, O += P V with P in
 //     tensor memory over its scores; neither A operand touches shared memory,
 //     whose bandwidth the staged tiles need;
@@ -51,13 +51,19 @@ struct TreeCfg {
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
   static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
   static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
+  // q5_1's minima as a tile of 16 block rows (NB of them real) with 16 columns of tensor
+  // memory; two row tiles leave no columns for it
+  static constexpr bool kMTile = VF == MEMRA_KV_Q5_1 && MT == 1;
+  static constexpr bool kVRows = VF != MEMRA_KV_NVFP4;          // V staged as token rows (MN-major)
   static constexpr uint32_t kTile = kKeys * D * 2;              // one operand tile: 16 KB
+  static constexpr uint32_t kMBytes = kMTile ? 16 * kKeys * 2 : 0;
   static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kTile * (kVLo ? 2 : 1);
   static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
   // barriers and page ids, then two K^ buffers, two V^T buffers and the raw chunks; the output rows
   // reuse everything behind the page ids
-  static constexpr uint32_t kOffBar = 0, kOffPid = 256, kOffK = kOffPid + 4 * kSplitPagesMax;
-  static constexpr uint32_t kOffV = kOffK + 2 * kKBuf, kOffRaw = kOffV + 2 * kVBuf;
+  static constexpr uint32_t kOffBar = 0, kOffPid = 256;
+  static constexpr uint32_t kOffK = (kOffPid + 4 * kTreeSplitPages + 1023) & ~1023u;
+  static constexpr uint32_t kOffV = kOffK + 2 * kKBuf, kOffM = kOffV + 2 * kVBuf, kOffRaw = kOffM + 2 * kMBytes;
   static constexpr uint32_t kEnd = kOffRaw + kRaw * kRawBytes;
   static constexpr uint32_t kRowBytes = D * 4 + 16;             // padded output row
   static constexpr uint32_t kEndRows = kOffK + MT * kTileRows * kRowBytes;
@@ -66,31 +72,74 @@ struct TreeCfg {
   static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows;
   static constexpr uint32_t kSmem = kNeed < 116 * 1024 ? 116 * 1024 : kNeed;
   static constexpr uint32_t kQCol = 0, kOCol = MT * D / 2, kSCol = kOCol + MT * D;   // tensor-memory columns
+  static constexpr uint32_t kMCol = kSCol + MT * kBufs * kKeys;
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(kSCol + MT * kBufs * kKeys <= 512, "tensor memory");
-  static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 256 == 0, "alignment");
+  static_assert(kMCol + (kMTile ? 16 : 0) <= 512, "tensor memory");
+  static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
 };
 
-// K^ and V^T operand tiles of one chunk, written by the staging warps.
-// `valid`: tokens of the chunk that exist; `pmask`: its pages that do.
+// ---- staging: a chunk's raw pages in shared memory to operand tiles -------------
+// Every raw code byte is read by 16-byte loads in lane order (the order of the
+// page layout: conflict-free), and each value goes to the tile from the thread
+// that read it.  A warp task is one 512-byte run of codes.
+
+// K^ (token rows, dims along K, core matrices of 8 tokens x 8 dims): token n,
+// dims 8 u .. 8 u + 7 are the 16 bytes at ((n / 8) * (D / 8) + u) * 128 + (n % 8) * 16.
+// Tokens that do not exist stage whatever the pages hold: their scores are masked.
 template <int D, int KF, int KEYS>
-__device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, uint32_t lo_off, uint32_t pmask, int st) {
-  constexpr int KSEG = k_seg_bytes(KF, D), IT = KEYS * (D / 8) / kStageThreads;
-  static_assert(IT * kStageThreads == KEYS * (D / 8), "whole items");
-  KRaw kr[IT];
+__device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, int lane) {
+  constexpr int NB = D / 32, SEG = k_seg_bytes(KF, D), B2 = D / 64;
+  constexpr uint32_t LO = KEYS * D * 2;
+  const int tg = lane >> 2, kc = lane & 3;
+  if constexpr (KF == MEMRA_KV_NVFP4) {
+    // run (page, 64-dim block): words (b % 2, e / 4), bytes tp + 2 (e % 4 / 2), nibbles e % 2
+    constexpr int TASKS = KEYS / kPage * B2;
+    static_assert(TASKS % kStageWarps == 0, "whole tasks");
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {      // item i = (token group, 8-dim group, token in group), byte 16 i
-    const int i = st + it * kStageThreads, n = ((i >> 3) / (D / 8)) * 8 + (i & 7);
-    kr[it] = load_k8<D, KF>(raw + (n / kPage) * KSEG, n % kPage, (i >> 3) % (D / 8));
-  }
+    for (int it = 0; it < TASKS / kStageWarps; ++it) {
+      const int task = warp + it * kStageWarps, pg = task / B2, b2 = task % B2;
+      const uint32_t seg = raw + pg * SEG;
+      const uint4 x = lds128(seg + (b2 * 32 + lane) * 16);
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int i = st + it * kStageThreads, n = ((i >> 3) / (D / 8)) * 8 + (i & 7);
-    uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-    if ((pmask >> (n / kPage)) & 1u) convert_k8<KF>(kr[it], n % kPage, hi, lo);
-    sts128(buf + 16 * i, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-    if constexpr (KF == MEMRA_KV_Q8_0) sts128(buf + lo_off + 16 * i, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      for (int tp = 0; tp < 2; ++tp)
+#pragma unroll
+        for (int bp = 0; bp < 2; ++bp) {
+          const uint32_t w0 = (bp ? x.z : x.x) >> (8 * tp), w1 = (bp ? x.w : x.y) >> (8 * tp);
+          const int t = 8 * tp + tg, u = (2 * b2 + bp) * 4 + kc;
+          const __half2 s2 = e4m3_scale_h2(lds8(seg + 8 * D + t * (D / 16) + (u >> 1)));
+          uint4 h;
+          h.x = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2(w0 & 0xFFu)), s2));
+          h.y = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2((w0 >> 16) & 0xFFu)), s2));
+          h.z = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2(w1 & 0xFFu)), s2));
+          h.w = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2((w1 >> 16) & 0xFFu)), s2));
+          sts128(buf + ((2 * pg + tp) * (D / 8) + u) * 128 + tg * 16, h);
+        }
+    }
+  } else {
+    // run (page, token half, 64-dim block): 8 bytes for each of the two 32-dim blocks
+    constexpr int TASKS = KEYS / 8 * B2;
+    static_assert(TASKS % kStageWarps == 0, "whole tasks");
+#pragma unroll
+    for (int it = 0; it < TASKS / kStageWarps; ++it) {
+      const int task = warp + it * kStageWarps, g = task / B2, b2 = task % B2;     // token group, block pair
+      const uint32_t seg = raw + (g >> 1) * SEG;
+      const uint4 x = lds128(seg + (((g & 1) * B2 + b2) * 32 + lane) * 16);
+      uint32_t d = 0;
+      if constexpr (KF == MEMRA_KV_Q8_0) d = lds32(seg + 16 * D + ((8 * (g & 1) + tg) * NB + 2 * b2) * 2);
+#pragma unroll
+      for (int bp = 0; bp < 2; ++bp) {
+        uint32_t hi[4], lo[4];
+        convert_k8<KF>(KRaw{bp ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y), bp ? d >> 16 : d & 0xFFFFu}, 0, hi, lo);
+        const uint32_t at = buf + (g * (D / 8) + (2 * b2 + bp) * 4 + kc) * 128 + tg * 16;
+        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        if constexpr (KF == MEMRA_KV_Q8_0) sts128(at + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+    }
   }
+}
+
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
 
 // Eight tokens (pairs in words) of which the first n exist; the others become zeros.
@@ -101,75 +150,155 @@ __device__ __forceinline__ uint4 keep_tokens(const uint32_t (&x)[4], int n) {
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-template <int D, int VF, int KEYS>
-__device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t lo_off, uint32_t pmask, int valid,
-                                        int st) {
-  constexpr int NB = D / 32, VSEG = v_seg_bytes(VF, D), PAGES = KEYS / kPage;
-  constexpr bool kLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
-  constexpr int TASKS = VF == MEMRA_KV_NVFP4 ? PAGES * 2 * (D / 16) * 8 : PAGES * 2 * NB * 8 * 2;
-  constexpr int IT = TASKS / kStageThreads;
-  static_assert(IT * kStageThreads == TASKS, "whole tasks");
-  // dim dd, token group g (8 tokens): one 16-byte row of a core matrix
-  auto store = [&](int dd, int g, uint4 h, uint4 l) {
-    const uint32_t off = ((dd >> 3) * (KEYS / 8) + g) * 128 + (dd & 7) * 16;
-    sts128(buf + off, h);
-    if constexpr (kLo) sts128(buf + lo_off + off, l);
+// Tokens of page pg of the chunk that exist: `valid` of the chunk's, none of a page left out.
+__device__ __forceinline__ int page_tokens(uint32_t pmask, int pg, int valid) {
+  return (pmask >> pg) & 1u ? valid - kPage * pg : 0;
+}
+
+// V^ of q5_1, q4_0 and fp8: token rows of 128 bytes (64 dims), 128-byte-swizzled
+// (the 16-byte unit of a row is XORed with the row's index in its group of 8),
+// one block of KEYS rows per 64 dims: the MN-major B operand of O += P V.  A
+// lane holds 4 consecutive dims of 4 tokens, so nothing is transposed, and a
+// warp's 8-byte stores fill all banks.  Tokens that do not exist become zeros:
+// 0 * (what their bytes stand for) need not be 0.  q5_1 stages d q alone where
+// the minima go through their own tile (M_TILE), else d q + m by a TwoSum.
+template <int D, int VF, int KEYS, bool M_TILE>
+__device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int warp, int lane) {
+  constexpr int NB = D / 32, SEG = v_seg_bytes(VF, D), B2 = D / 64;
+  constexpr uint32_t LO = KEYS * D * 2;
+  const int vg = lane >> 2, c = lane & 3;
+  // token 8 p + 2 c + f of page pg, block b, dims 4 vg .. + 3
+  auto at = [&](int pg, int p, int f, int b) {
+    const int r8 = 2 * c + f, row = kPage * pg + 8 * p + r8;
+    return buf + (b >> 1) * KEYS * 128 + row * 128 + ((((b & 1) * 64 + vg * 8)) ^ (r8 << 4));
   };
-  const uint4 z = make_uint4(0, 0, 0, 0);
-  if constexpr (VF == MEMRA_KV_NVFP4) {
-    // task (page, half page, 16-dim block b16, rr): dims 16 b16 + rr and + 8
-    uint32_t cw[IT][4], sw[IT][4];
+  if constexpr (VF == MEMRA_KV_FP8_E4M3) {
+    // run (page, 32-dim block): words 2 h + p, bytes 2 s + f
+    constexpr int TASKS = KEYS / kPage * NB;
+    static_assert(TASKS % kStageWarps == 0, "whole tasks");
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int task = st + it * kStageThreads, rr = task & 7, b16 = (task >> 3) % (D / 16);
-      const uint32_t seg = raw + task / (16 * (D / 16)) * VSEG;
+    for (int it = 0; it < TASKS / kStageWarps; ++it) {
+      const int task = warp + it * kStageWarps, pg = task / NB, b = task % NB, n = page_tokens(pmask, pg, valid);
+      const uint4 x = lds128(raw + pg * SEG + (b * 32 + lane) * 16);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        cw[it][c] = lds32(seg + ((b16 >> 2) * 32 + 4 * rr + c) * 16 + (b16 & 3) * 4);
-        sw[it][c] = lds32(seg + 8 * D + (c * (D / 16) + b16) * 4);
-      }
-    }
-#pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int task = st + it * kStageThreads, rr = task & 7, b16 = (task >> 3) % (D / 16),
-                ph = (task / (8 * (D / 16))) & 1, ps = task / (16 * (D / 16)), g = 2 * ps + ph;
-      uint32_t h0[4], h1[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        __half2 v[2];
+      for (int p = 0; p < 2; ++p) {
+        // bytes (s0 f0, s0 f1, s1 f0, s1 f1) to (s0 f0, s1 f0, s0 f1, s1 f1): one pair per token
+        uint32_t h0[2], h1[2];
+        e4m3x4_to_half2x2(__byte_perm(p ? x.y : x.x, 0, 0x3120), h0[0], h0[1]);
+        e4m3x4_to_half2x2(__byte_perm(p ? x.w : x.z, 0, 0x3120), h1[0], h1[1]);
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const int sh = 8 * (f + 2 * ph);
-          v[f] = __hmul2(bits_h2(e2m1x2_to_half2((cw[it][c] >> sh) & 0xFFu)), e4m3_scale_h2(sw[it][c] >> sh));
+          const bool live = 8 * p + 2 * c + f < n;
+          sts64(at(pg, p, f, b), live ? h0[f] : 0u, live ? h1[f] : 0u);
         }
-        h0[c] = h2_bits(__lows2half2(v[0], v[1]));
-        h1[c] = h2_bits(__highs2half2(v[0], v[1]));
       }
-      const int n = (pmask >> ps) & 1u ? valid - 8 * g : 0;
-      store(16 * b16 + rr, g, keep_tokens(h0, n), z);
-      store(16 * b16 + rr + 8, g, keep_tokens(h1, n), z);
     }
   } else {
-    // task (page, half page, block b, vg, pair h): dims 32 b + 4 vg + 2 h + s, tokens 8 half + 2 c + f
-    VRaw vr[IT];
+    // run (page, 64-dim block): words 2 (b % 2) + h, bytes 2 f + p, nibbles s
+    constexpr int TASKS = KEYS / kPage * B2;
+    static_assert(TASKS % kStageWarps == 0, "whole tasks");
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int task = st + it * kStageThreads;
-      vr[it] = load_v_task<D, VF>(raw + task / (32 * NB) * VSEG, (task / (16 * NB)) & 1, (task >> 4) % NB,
-                                  (task >> 1) & 7, task & 1);
-    }
+    for (int it = 0; it < TASKS / kStageWarps; ++it) {
+      const int task = warp + it * kStageWarps, pg = task / B2, b2 = task % B2, n = page_tokens(pmask, pg, valid);
+      const uint32_t seg = raw + pg * SEG;
+      const uint4 x4 = lds128(seg + (b2 * 32 + lane) * 16);
+      const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
+      const uint32_t hw = VF == MEMRA_KV_Q5_1 ? lds32(seg + 8 * D + (lane * (NB / 2) + b2) * 4) : 0u;
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      const int task = st + it * kStageThreads, h = task & 1, vg = (task >> 1) & 7, b = (task >> 4) % NB,
-                ph = (task / (16 * NB)) & 1, ps = task / (32 * NB), g = 2 * ps + ph;
-      uint32_t hi[2][4], lo[2][4];
-      convert_v_task<VF>(vr[it], ph, b, h, hi, lo);
-      const int n = (pmask >> ps) & 1u ? valid - 8 * g : 0;
+      for (int bp = 0; bp < 2; ++bp) {
+        const int b = 2 * b2 + bp;
+        // scales (and minima) of the lane's tokens: halves 2 p + f
+        const uint2 dw = lds64(seg + (VF == MEMRA_KV_Q5_1 ? 10 : 8) * D + (c * NB + b) * 8);
+        uint2 mw = make_uint2(0, 0);
+        if constexpr (VF == MEMRA_KV_Q5_1 && !M_TILE) mw = lds64(seg + 11 * D + (c * NB + b) * 8);
+        uint32_t hi[4][2], lo[4][2];     // [byte 2 f + p][h]
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        store(32 * b + 4 * vg + 2 * h + e, g, keep_tokens(hi[e], n), kLo ? keep_tokens(lo[e], n) : z);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t l4 = xw[2 * bp + h] & 0x0F0F0F0Fu, h4 = (xw[2 * bp + h] >> 4) & 0x0F0F0F0Fu;
+          if constexpr (VF == MEMRA_KV_Q5_1) {
+            l4 |= ((hw << 4) >> (2 * bp + h)) & 0x10101010u;
+            h4 |= (hw >> (2 * bp + h)) & 0x10101010u;
+          }
+          const uint32_t p01 = __byte_perm(l4, h4, 0x5140), p23 = __byte_perm(l4, h4, 0x7362);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // 1024 + q as fp16 for dims s = 0, 1; then q / 2 (q5_1) or (q - 8) / 2 (q4_0), exactly
+            const __half2 q2 = __hfma2(bits_h2(__byte_perm(k < 2 ? p01 : p23, 0x64646464u, k & 1 ? 0x4342 : 0x4140)),
+                                       __float2half2_rn(0.5f), __float2half2_rn(VF == MEMRA_KV_Q5_1 ? -512.f : -516.f));
+            const int f = k >> 1, p = k & 1;
+            const uint32_t sel = f ? 0x3232 : 0x1010;
+            const __half2 d2 = bits_h2(__byte_perm(p ? dw.y : dw.x, 0, sel));
+            const __half2 p_hi = __hmul2_rn(q2, d2);
+            const __half2 p_lo = __hfma2(q2, d2, __hneg2(p_hi));
+            if constexpr (VF == MEMRA_KV_Q5_1 && !M_TILE) {
+              const __half2 m2 = __hmul2_rn(bits_h2(__byte_perm(p ? mw.y : mw.x, 0, sel)), __float2half2_rn(0.5f));
+              const __half2 s2 = __hadd2_rn(p_hi, m2);
+              const __half2 bb = __hsub2_rn(s2, p_hi);
+              const __half2 e2 = __hadd2_rn(__hsub2_rn(p_hi, __hsub2_rn(s2, bb)), __hsub2_rn(m2, bb));
+              hi[k][h] = h2_bits(s2);
+              lo[k][h] = h2_bits(__hadd2_rn(e2, p_lo));
+            } else {
+              hi[k][h] = h2_bits(p_hi);
+              lo[k][h] = h2_bits(p_lo);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int f = k >> 1, p = k & 1;
+          const bool live = 8 * p + 2 * c + f < n;
+          const uint32_t to = at(pg, p, f, b);
+          sts64(to, live ? hi[k][0] : 0u, live ? hi[k][1] : 0u);
+          sts64(to + LO, live ? lo[k][0] : 0u, live ? lo[k][1] : 0u);
+        }
+      }
     }
   }
+}
+
+// V^T of NVFP4 (dim rows, tokens along K, core matrices): its lanes hold single
+// dims, so a task gathers the 8 tokens of two dims and stores 16-byte rows.
+template <int D, int KEYS>
+__device__ __forceinline__ void stage_v_nvfp4(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int st) {
+  constexpr int SEG = v_seg_bytes(MEMRA_KV_NVFP4, D), TASKS = KEYS / kPage * 2 * (D / 16) * 8, IT = TASKS / kStageThreads;
+  static_assert(IT * kStageThreads == TASKS, "whole tasks");
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {      // task (page, half page, 16-dim block b16, rr): dims 16 b16 + rr and + 8
+    const int task = st + it * kStageThreads, rr = task & 7, b16 = (task >> 3) % (D / 16),
+              ph = (task / (8 * (D / 16))) & 1, pg = task / (16 * (D / 16)), g = 2 * pg + ph;
+    const uint32_t seg = raw + pg * SEG;
+    uint32_t h0[4], h1[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t cw = lds32(seg + ((b16 >> 2) * 32 + 4 * rr + c) * 16 + (b16 & 3) * 4);
+      const uint32_t sw = lds32(seg + 8 * D + (c * (D / 16) + b16) * 4);
+      __half2 v[2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int sh = 8 * (f + 2 * ph);
+        v[f] = __hmul2(bits_h2(e2m1x2_to_half2((cw >> sh) & 0xFFu)), e4m3_scale_h2(sw >> sh));
+      }
+      h0[c] = h2_bits(__lows2half2(v[0], v[1]));
+      h1[c] = h2_bits(__highs2half2(v[0], v[1]));
+    }
+    const int n = page_tokens(pmask, pg, valid) - 8 * ph, d0 = 16 * b16 + rr;
+    const uint32_t at = buf + ((d0 >> 3) * (KEYS / 8) + g) * 128 + (d0 & 7) * 16;
+    sts128(at, keep_tokens(h0, n));
+    sts128(at + (KEYS / 8) * 128, keep_tokens(h1, n));
+  }
+}
+
+// The minima of q5_1 as a tile of their own: row b (32-dim block), tokens along
+// K, so that sum_t P[., t] m[t, b] is one more narrow MMA and joins O at the end.
+template <int D, int KEYS>
+__device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int lane) {
+  constexpr int NB = D / 32, SEG = v_seg_bytes(MEMRA_KV_Q5_1, D);
+  static_assert(KEYS / 8 * NB == 32, "one lane per block and token group");
+  const int b = lane % NB, g = lane / NB;
+  uint32_t x[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) x[c] = lds32(raw + (g >> 1) * SEG + 11 * D + ((c * NB + b) * 4 + 2 * (g & 1)) * 2);
+  sts128(buf + g * 128 + b * 16, keep_tokens(x, page_tokens(pmask, g >> 1, valid) - 8 * (g & 1)));
 }
 
 template <int D, int KF, int VF, int MT>
@@ -291,7 +420,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     // -------------------------------------------------------------------- MMA --
     if (lane == 0) {
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
-      constexpr uint32_t idesc_o = tc::idesc_f16_f32(kTileRows, D);
+      constexpr uint32_t idesc_o = C::kVRows ? tc::idesc_f16_f32_bmn(kTileRows, D) : tc::idesc_f16_f32(kTileRows, D);
+      auto v_desc = [](uint32_t v, int ks) {
+        return C::kVRows ? tc::smem_desc_sw128(v + 2048 * ks, KT * 128, 1024) : tc::smem_desc(v + 256 * ks, 128, (KT / 8) * 128);
+      };
       auto wait = [&](int kind, int k, int phase) {
         ok = ok && mbar_wait_bounded(bar(kind, k), phase & 1, p.status);
       };
@@ -323,10 +455,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         const uint32_t d = tmem + C::kOCol + i * D;
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks) {
-          tc::mma_f16_ta(d, a0 + 8 * ks, tc::smem_desc(v + 256 * ks, 128, (KT / 8) * 128), idesc_o,
-                         ci > 0 || ks > 0);
-          if constexpr (C::kVLo)
-            tc::mma_f16_ta(d, a0 + 8 * ks, tc::smem_desc(v + C::kTile + 256 * ks, 128, (KT / 8) * 128), idesc_o, 1);
+          tc::mma_f16_ta(d, a0 + 8 * ks, v_desc(v, ks), idesc_o, ci > 0 || ks > 0);
+          if constexpr (C::kVLo) tc::mma_f16_ta(d, a0 + 8 * ks, v_desc(v + C::kTile, ks), idesc_o, 1);
+          if constexpr (C::kMTile)
+            tc::mma_f16_ta(tmem + C::kMCol, a0 + 8 * ks,
+                           tc::smem_desc(sb + C::kOffM + vb * C::kMBytes + 256 * ks, 128, (KT / 8) * 128),
+                           tc::idesc_f16_f32(kTileRows, 16), ci > 0 || ks > 0);
         }
         if (i == MT - 1) tc::commit(bar(kVEmpty, vb));
         if (NBUF > 1 || ci == n_chunks - 1) tc::commit(bar(kPvDone, i));
@@ -353,7 +487,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- staging --
-    const int st = tid - 128;
+    const int sw = warp - 4;
+    if constexpr (C::kMTile) {               // the block rows that are none, and the gaps, once
+      for (uint32_t i = tid - 128; i < 2 * C::kMBytes / 16; i += kStageThreads)
+        sts128(sb + C::kOffM + 16 * i, make_uint4(0, 0, 0, 0));
+      named_barrier_sync(1, kStageThreads);
+    }
     for (int ci = 0; ci < n_chunks; ++ci) {
       const int s = ci % kRaw, k = ci & 1;
       const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, pmask = chunk_mask(ci);
@@ -361,14 +500,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       if (ok && ci >= 2) ok = mbar_wait_bounded(bar(kKEmpty, k), ((ci >> 1) - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      stage_k<D, KF, KT>(rawk, sb + C::kOffK + k * C::kKBuf, C::kTile, pmask, st);
+      stage_k<D, KF, KT>(rawk, sb + C::kOffK + k * C::kKBuf, sw, lane);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kKFull, k));
       if (ci >= 2) ok = mbar_wait_bounded(bar(kVEmpty, k), ((ci >> 1) - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      stage_v<D, VF, KT>(rawk + NP * C::kKSeg, sb + C::kOffV + k * C::kVBuf, C::kTile, pmask, count - ci * KT, st);
+      const uint32_t rawv = rawk + NP * C::kKSeg, vbuf = sb + C::kOffV + k * C::kVBuf;
+      if constexpr (C::kVRows)
+        stage_v<D, VF, KT, C::kMTile>(rawv, vbuf, pmask, count - ci * KT, sw, lane);
+      else
+        stage_v_nvfp4<D, KT>(rawv, vbuf, pmask, count - ci * KT, tid - 128);
+      if constexpr (C::kMTile)
+        if (sw == (ci & (kStageWarps - 1)))
+          stage_m<D, KT>(rawv, sb + C::kOffM + k * C::kMBytes, pmask, count - ci * KT, lane);
       fence_proxy_async();                   // V^T for the tensor cores, the raw chunk for the next copies
       __syncwarp();
       if (lane == 0) {
@@ -462,6 +608,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
             tc::st_32x32b_x32(tmem + tlane + C::kOCol + i * D + c, o);
           }
+          if constexpr (C::kMTile) {
+            uint32_t o[16];
+            tc::ld_32x32b_x16(tmem + tlane + C::kMCol, o);
+            tc::wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::st_32x32b_x16(tmem + tlane + C::kMCol, o);
+          }
           l[i] *= alpha;
         }
         const float mu = m[i] == -INFINITY ? 0.f : m[i];
@@ -499,16 +653,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     for (int i = 0; i < MT; ++i) {
       const int r = r0 + i * kTileRows + tid;
       const float inv = l[i] > 0.f ? p.v_post / l[i] : 0.f;
+      uint32_t ms[16];                       // the minima's sums, per 32-dim block; a half as the staged values are
+      if constexpr (C::kMTile) {
+        tc::ld_32x32b_x16(tmem + tlane + C::kMCol, ms);
+        tc::wait_ld(ms);
+      }
       const uint32_t row = sb + C::kOffK + (i * kTileRows + tid) * C::kRowBytes;
-#pragma unroll 1
-      for (int c = 0; ok && c < D; c += 32) {
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        if (!ok) break;
         uint32_t o[32];
         tc::ld_32x32b_x32(tmem + tlane + C::kOCol + i * D + c, o);
         tc::wait_ld_all();
         tc::hold<32>(o);
+        const float half_m = C::kMTile ? 0.5f * __uint_as_float(ms[c / 32]) : 0.f;
         float x[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = l[i] > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
+        for (int e = 0; e < 32; ++e) x[e] = l[i] > 0.f ? (__uint_as_float(o[e]) + half_m) * inv : 0.f;
         if (ns == 1) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)

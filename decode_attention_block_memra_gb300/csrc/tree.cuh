@@ -20,24 +20,27 @@ __host__ __device__ constexpr int tree_tiles(int D, int rows) { return D == 128 
 // Smallest split: it keeps a CTA's fixed costs (the query tile, the first
 // pages' latency, the output rows) to a fraction of its time.
 constexpr int kTreeSplitTokens = 512;
+// Largest split (its page ids lie in shared memory).
+constexpr int kTreeSplitMax = 16384;
+constexpr int kTreeSplitPages = kTreeSplitMax / kPage;
 // Most splits that a sequence is cut into to fill the GPU.
 constexpr int kTreeMaxSplits = 160;
 
 // Split size of a sequence of T tokens: about `target` splits, never fewer
-// than kTreeSplitTokens or more than kSplitTokensMax tokens, a multiple of 64.
+// than kTreeSplitTokens or more than kTreeSplitMax tokens, a multiple of 64.
 // It depends on T and `target` (the device, the KV heads and the rows of one
 // sequence) only: a sequence's bytes are the same alone or in any batch.
 __host__ __device__ __forceinline__ int tree_split_tokens(int T, int target) {
   const int c = ((T > 0 ? (T - 1) / target + 1 : 0) + 63) / 64 * 64;
-  return c < kTreeSplitTokens ? kTreeSplitTokens : (c > kSplitTokensMax ? kSplitTokensMax : c);
+  return c < kTreeSplitTokens ? kTreeSplitTokens : (c > kTreeSplitMax ? kTreeSplitMax : c);
 }
 
 __host__ __device__ __forceinline__ int tree_ceil(int T, int c) { return T > 0 ? (T - 1) / c + 1 : 0; }
 
 // Most splits of any sequence of up to T tokens: those of the smallest size,
-// capped by the target, or past target * kSplitTokensMax tokens by the largest size.
+// capped by the target, or past target * kTreeSplitMax tokens by the largest size.
 __host__ __device__ __forceinline__ int tree_most_splits(int T, int target) {
-  const int cap = tree_ceil(T, kSplitTokensMax) > target ? tree_ceil(T, kSplitTokensMax) : target;
+  const int cap = tree_ceil(T, kTreeSplitMax) > target ? tree_ceil(T, kTreeSplitMax) : target;
   return tree_ceil(T, kTreeSplitTokens) < cap ? tree_ceil(T, kTreeSplitTokens) : cap;
 }
 
