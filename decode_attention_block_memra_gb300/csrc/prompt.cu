@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       for (int n = max(0, issued - ST); n < issued; ++n) mbar_wait_bounded(kv_full(n % ST), (n / ST) & 1, p.status);
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------------- MMA --
-    if (lane == 0) {
+    if (tc::elect_one()) {
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
       constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(kTileRows, D);
       auto slot_full = [&](int n) { return mbar_wait_bounded(kv_full(n % ST), (n / ST) & 1, p.status); };

@@ -67,6 +67,16 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// Whole warp: true on one lane.  MMA loops run under this and not under a lane
+// comparison: the compiler then knows that one thread is active and keeps the
+// descriptors in uniform registers (10 clocks to issue an MMA instead of 45,
+// and 70 beside busy warps; a 128 x 64 x 16 MMA itself takes 32).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // One thread: D[tmem] (+)= A[smem] * B[smem]^T, M x N x 16, fp16 in, fp32
 // accumulate; accumulate = 0 overwrites D.
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,

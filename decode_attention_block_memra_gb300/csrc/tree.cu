@@ -8,11 +8,11 @@
 // the M side of tcgen05 MMAs, so a page is read and dequantized once for all of
 // them (twice or more only past 256 rows).  CTA = (split of the keys, KV head,
 // sequence and row tiles):
-//   * a producer thread copies raw pages into a ring of three chunks;
+//   * a producer thread copies raw pages into a ring of chunks (64 keys);
 //   * eight staging warps dequantize a chunk's K and V into double-buffered
 //     fp16 operand tiles: exact hi + lo pairs for q8_0, q5_1 and q4_0, single
 //     values for fp8 and NVFP4, so only P is rounded (fp16, relative 2^-11 a
-//     weight); q5_1's minima are a narrow tile of their own;
+//     weight);
 //   * one MMA thread: S = Q K^T with Q in tensor memory, O += P V with P in
 //     tensor memory over its scores; neither A operand touches shared memory,
 //     whose bandwidth the staged tiles need;
@@ -41,29 +41,32 @@ constexpr int kStageWarps = 8;
 constexpr int kStageThreads = 32 * kStageWarps;
 constexpr int kMmaWarp = 4 + kStageWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kTreeThreads = 32 * (kCopyWarp + 1);
-constexpr int kRaw = 3;                    // chunks of raw pages
 
 template <int D, int KF, int VF, int MT>
 struct TreeCfg {
-  static constexpr int kKeys = tree_chunk_tokens(D);
-  static constexpr int kPages = kKeys / kPage;
+  static constexpr int kPages = kTreeKeys / kPage;
   static constexpr int kBufs = MT == 1 ? 2 : 1;                 // score buffers of a tile
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
   static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
   static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
-  // q5_1's minima as a tile of 16 block rows (NB of them real) with 16 columns of tensor
-  // memory; two row tiles leave no columns for it
-  static constexpr bool kMTile = VF == MEMRA_KV_Q5_1 && MT == 1;
+  // q5_1's minima as 16 more columns of V^ (one per 32-dim block; the others zero), joined to O at the
+  // end: an exact d q + m in two fp16 parts costs ten operations a pair, d q alone three.  Two row tiles
+  // (or head_dim 256) leave no tensor memory or no MMA width for them.
+  static constexpr bool kMCols = VF == MEMRA_KV_Q5_1 && MT == 1 && D == 128;
+  static constexpr int kOCols = D + (kMCols ? 16 : 0);
   static constexpr bool kVRows = VF != MEMRA_KV_NVFP4;          // V staged as token rows (MN-major)
-  static constexpr uint32_t kTile = kKeys * D * 2;              // one operand tile: 16 KB
-  static constexpr uint32_t kMBytes = kMTile ? 16 * kKeys * 2 : 0;
-  static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kTile * (kVLo ? 2 : 1);
+  // operand tiles and how many chunks of them: head_dim 256 has room for one where a tile is a pair
+  static constexpr uint32_t kTile = kTreeKeys * D * 2;
+  static constexpr uint32_t kLoOff = kTile + (kMCols ? kTreeKeys * 128 : 0);      // V: hi, minima, lo
+  static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kVLo ? kLoOff + kTile : kTile;
+  static constexpr int kKBufs = D == 256 && kKLo ? 1 : 2, kVBufs = D == 256 && kVLo ? 1 : 2;
+  static constexpr int kRaw = D == 256 ? 2 : 3;                 // chunks of raw pages
   static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
-  // barriers and page ids, then two K^ buffers, two V^T buffers and the raw chunks; the output rows
-  // reuse everything behind the page ids
+  // barriers and page ids, then K^ and V^ tiles and the raw chunks; the output rows reuse everything
+  // behind the page ids
   static constexpr uint32_t kOffBar = 0, kOffPid = 256;
   static constexpr uint32_t kOffK = (kOffPid + 4 * kTreeSplitPages + 1023) & ~1023u;
-  static constexpr uint32_t kOffV = kOffK + 2 * kKBuf, kOffM = kOffV + 2 * kVBuf, kOffRaw = kOffM + 2 * kMBytes;
+  static constexpr uint32_t kOffV = kOffK + kKBufs * kKBuf, kOffRaw = kOffV + kVBufs * kVBuf;
   static constexpr uint32_t kEnd = kOffRaw + kRaw * kRawBytes;
   static constexpr uint32_t kRowBytes = D * 4 + 16;             // padded output row
   static constexpr uint32_t kEndRows = kOffK + MT * kTileRows * kRowBytes;
@@ -71,10 +74,9 @@ struct TreeCfg {
   // columns, and one that shares an SM with another holder of them would wait.
   static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows;
   static constexpr uint32_t kSmem = kNeed < 116 * 1024 ? 116 * 1024 : kNeed;
-  static constexpr uint32_t kQCol = 0, kOCol = MT * D / 2, kSCol = kOCol + MT * D;   // tensor-memory columns
-  static constexpr uint32_t kMCol = kSCol + MT * kBufs * kKeys;
+  static constexpr uint32_t kQCol = 0, kOCol = MT * D / 2, kSCol = kOCol + MT * kOCols;   // tensor-memory columns
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(kMCol + (kMTile ? 16 : 0) <= 512, "tensor memory");
+  static_assert(kSCol + MT * kBufs * kTreeKeys <= 512, "tensor memory");
   static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
 };
 
@@ -83,8 +85,11 @@ struct TreeCfg {
 // page layout: conflict-free), and each value goes to the tile from the thread
 // that read it.  A warp task is one 512-byte run of codes.
 
-// K^ (token rows, dims along K, core matrices of 8 tokens x 8 dims): token n,
-// dims 8 u .. 8 u + 7 are the 16 bytes at ((n / 8) * (D / 8) + u) * 128 + (n % 8) * 16.
+// K^: token rows of 128 bytes (64 dims, the K axis of the score MMA), 128-byte-
+// swizzled (the 16-byte unit of a row is XORed with the row's index in its group
+// of 8), one block of KEYS rows per 64 dims.  A lane holds the same 8 dims of
+// two 32-dim blocks; lanes of odd tokens store the second block first, so that
+// eight lanes' 16-byte stores always fall on different banks.
 // Tokens that do not exist stage whatever the pages hold: their scores are masked.
 template <int D, int KF, int KEYS>
 __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, int lane) {
@@ -103,16 +108,17 @@ __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, in
 #pragma unroll
       for (int tp = 0; tp < 2; ++tp)
 #pragma unroll
-        for (int bp = 0; bp < 2; ++bp) {
+        for (int e = 0; e < 2; ++e) {
+          const bool bp = e ^ (tg & 1);
           const uint32_t w0 = (bp ? x.z : x.x) >> (8 * tp), w1 = (bp ? x.w : x.y) >> (8 * tp);
-          const int t = 8 * tp + tg, u = (2 * b2 + bp) * 4 + kc;
-          const __half2 s2 = e4m3_scale_h2(lds8(seg + 8 * D + t * (D / 16) + (u >> 1)));
+          const int t = 8 * tp + tg, u = 4 * bp + kc;
+          const __half2 s2 = e4m3_scale_h2(lds8(seg + 8 * D + t * (D / 16) + 4 * b2 + (u >> 1)));
           uint4 h;
           h.x = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2(w0 & 0xFFu)), s2));
           h.y = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2((w0 >> 16) & 0xFFu)), s2));
           h.z = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2(w1 & 0xFFu)), s2));
           h.w = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2((w1 >> 16) & 0xFFu)), s2));
-          sts128(buf + ((2 * pg + tp) * (D / 8) + u) * 128 + tg * 16, h);
+          sts128(buf + b2 * KEYS * 128 + (kPage * pg + t) * 128 + ((u ^ tg) << 4), h);
         }
     }
   } else {
@@ -127,10 +133,11 @@ __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, in
       uint32_t d = 0;
       if constexpr (KF == MEMRA_KV_Q8_0) d = lds32(seg + 16 * D + ((8 * (g & 1) + tg) * NB + 2 * b2) * 2);
 #pragma unroll
-      for (int bp = 0; bp < 2; ++bp) {
+      for (int e = 0; e < 2; ++e) {
+        const bool bp = e ^ (tg & 1);
         uint32_t hi[4], lo[4];
-        convert_k8<KF>(KRaw{bp ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y), bp ? d >> 16 : d & 0xFFFFu}, 0, hi, lo);
-        const uint32_t at = buf + (g * (D / 8) + (2 * b2 + bp) * 4 + kc) * 128 + tg * 16;
+        convert_k8<KF>(KRaw{make_uint2(bp ? x.z : x.x, bp ? x.w : x.y), bp ? d >> 16 : d & 0xFFFFu}, 0, hi, lo);
+        const uint32_t at = buf + b2 * KEYS * 128 + (8 * g + tg) * 128 + (((4 * bp + kc) ^ tg) << 4);
         sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
         if constexpr (KF == MEMRA_KV_Q8_0) sts128(at + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       }
@@ -161,11 +168,10 @@ __device__ __forceinline__ int page_tokens(uint32_t pmask, int pg, int valid) {
 // lane holds 4 consecutive dims of 4 tokens, so nothing is transposed, and a
 // warp's 8-byte stores fill all banks.  Tokens that do not exist become zeros:
 // 0 * (what their bytes stand for) need not be 0.  q5_1 stages d q alone where
-// the minima go through their own tile (M_TILE), else d q + m by a TwoSum.
-template <int D, int VF, int KEYS, bool M_TILE>
+// the minima have columns of their own (M_COLS), else d q + m by a TwoSum.
+template <int D, int VF, int KEYS, bool M_COLS, uint32_t LO>
 __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int warp, int lane) {
   constexpr int NB = D / 32, SEG = v_seg_bytes(VF, D), B2 = D / 64;
-  constexpr uint32_t LO = KEYS * D * 2;
   const int vg = lane >> 2, c = lane & 3;
   // token 8 p + 2 c + f of page pg, block b, dims 4 vg .. + 3
   auto at = [&](int pg, int p, int f, int b) {
@@ -210,7 +216,7 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
         // scales (and minima) of the lane's tokens: halves 2 p + f
         const uint2 dw = lds64(seg + (VF == MEMRA_KV_Q5_1 ? 10 : 8) * D + (c * NB + b) * 8);
         uint2 mw = make_uint2(0, 0);
-        if constexpr (VF == MEMRA_KV_Q5_1 && !M_TILE) mw = lds64(seg + 11 * D + (c * NB + b) * 8);
+        if constexpr (VF == MEMRA_KV_Q5_1 && !M_COLS) mw = lds64(seg + 11 * D + (c * NB + b) * 8);
         uint32_t hi[4][2], lo[4][2];     // [byte 2 f + p][h]
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -230,7 +236,7 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
             const __half2 d2 = bits_h2(__byte_perm(p ? dw.y : dw.x, 0, sel));
             const __half2 p_hi = __hmul2_rn(q2, d2);
             const __half2 p_lo = __hfma2(q2, d2, __hneg2(p_hi));
-            if constexpr (VF == MEMRA_KV_Q5_1 && !M_TILE) {
+            if constexpr (VF == MEMRA_KV_Q5_1 && !M_COLS) {
               const __half2 m2 = __hmul2_rn(bits_h2(__byte_perm(p ? mw.y : mw.x, 0, sel)), __float2half2_rn(0.5f));
               const __half2 s2 = __hadd2_rn(p_hi, m2);
               const __half2 bb = __hsub2_rn(s2, p_hi);
@@ -288,33 +294,35 @@ __device__ __forceinline__ void stage_v_nvfp4(uint32_t raw, uint32_t buf, uint32
   }
 }
 
-// The minima of q5_1 as a tile of their own: row b (32-dim block), tokens along
-// K, so that sum_t P[., t] m[t, b] is one more narrow MMA and joins O at the end.
+// The minima of q5_1 as columns of V^: a further 64-column block of which the
+// MMA takes 16, token n's minima of the D / 32 blocks in its first 16-byte unit.
 template <int D, int KEYS>
-__device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int lane) {
+__device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int n) {
   constexpr int NB = D / 32, SEG = v_seg_bytes(MEMRA_KV_Q5_1, D);
-  static_assert(KEYS / 8 * NB == 32, "one lane per block and token group");
-  const int b = lane % NB, g = lane / NB;
-  uint32_t x[4];
+  static_assert(NB == 4, "8 bytes of minima");
+  const int pg = n / kPage, t = n % kPage;
+  const uint32_t at = raw + pg * SEG + 11 * D + (((t & 7) >> 1) * NB * 4 + 2 * (t >> 3) + (t & 1)) * 2;
+  uint32_t m[NB];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) x[c] = lds32(raw + (g >> 1) * SEG + 11 * D + ((c * NB + b) * 4 + 2 * (g & 1)) * 2);
-  sts128(buf + g * 128 + b * 16, keep_tokens(x, page_tokens(pmask, g >> 1, valid) - 8 * (g & 1)));
+  for (int b = 0; b < NB; ++b) m[b] = lds16(at + 8 * b);
+  const bool live = t < page_tokens(pmask, pg, valid);
+  sts64(buf + n * 128 + ((n & 7) << 4), live ? m[0] | (m[1] << 16) : 0u, live ? m[2] | (m[3] << 16) : 0u);
 }
 
 template <int D, int KF, int VF, int MT>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams p) {
   using C = TreeCfg<D, KF, VF, MT>;
-  constexpr int KT = C::kKeys, NP = C::kPages, NBUF = C::kBufs;
+  constexpr int KT = kTreeKeys, NP = C::kPages, NBUF = C::kBufs, RAW = C::kRaw;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bars = sb + C::kOffBar;
   auto raw_full = [&](int s) { return bars + 8 * s; };
-  auto raw_empty = [&](int s) { return bars + 8 * (kRaw + s); };
+  auto raw_empty = [&](int s) { return bars + 8 * (RAW + s); };
   enum { kKFull = 0, kKEmpty, kVFull, kVEmpty, kSFull, kPFull, kPvDone };
-  auto bar = [&](int kind, int b) { return bars + 8 * (2 * kRaw + 2 * kind + b); };
-  const uint32_t drained = bars + 8 * (2 * kRaw + 14), q_ready = drained + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * (2 * kRaw + 16));
+  auto bar = [&](int kind, int b) { return bars + 8 * (2 * RAW + 2 * kind + b); };
+  const uint32_t drained = bars + 8 * (2 * RAW + 14), q_ready = drained + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * (2 * RAW + 16));
   int *pid_s = reinterpret_cast<int *>(smem + C::kOffPid);
 
   grid_dependency_wait();
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     tc::tmem_relinquish();
   }
   if (tid == 32 * kCopyWarp) {
-    for (int s = 0; s < kRaw; ++s) {
+    for (int s = 0; s < RAW; ++s) {
       mbar_init(raw_full(s), 1);
       mbar_init(raw_empty(s), kStageWarps);
     }
@@ -392,8 +400,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const size_t vstride = static_cast<size_t>(p.n_kv_heads) * C::kVSeg;
       int issued = 0;
       for (int ci = 0; ci < n_chunks; ++ci) {
-        const int s = ci % kRaw;
-        if (ci >= kRaw) ok = mbar_wait_bounded(raw_empty(s), (ci / kRaw - 1) & 1, p.status);
+        const int s = ci % RAW;
+        if (ci >= RAW) ok = mbar_wait_bounded(raw_empty(s), (ci / RAW - 1) & 1, p.status);
         if (!ok) break;
         const uint32_t m = chunk_mask(ci), buf = sb + C::kOffRaw + s * C::kRawBytes;
         if (m) {
@@ -412,15 +420,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         issued = ci + 1;
       }
       // every copy has landed before the CTA can leave
-      for (int ci = max(0, issued - kRaw); ci < issued; ++ci)
-        mbar_wait_bounded(raw_full(ci % kRaw), (ci / kRaw) & 1, p.status);
+      for (int ci = max(0, issued - RAW); ci < issued; ++ci)
+        mbar_wait_bounded(raw_full(ci % RAW), (ci / RAW) & 1, p.status);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------------- MMA --
-    if (lane == 0) {
+    if (tc::elect_one()) {
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
       constexpr uint32_t idesc_o = C::kVRows ? tc::idesc_f16_f32_bmn(kTileRows, D) : tc::idesc_f16_f32(kTileRows, D);
+      constexpr uint32_t idesc_oc = C::kMCols ? tc::idesc_f16_f32_bmn(kTileRows, C::kOCols) : idesc_o;
       auto v_desc = [](uint32_t v, int ks) {
         return C::kVRows ? tc::smem_desc_sw128(v + 2048 * ks, KT * 128, 1024) : tc::smem_desc(v + 256 * ks, 128, (KT / 8) * 128);
       };
@@ -429,38 +438,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       };
       // S_i(ci) = Q_i K^T into score buffer sbuf of tile i
       auto mma_s = [&](int i, int ci) {
-        const int kb = ci & 1, sbuf = NBUF > 1 ? ci & 1 : 0;
-        wait(kKFull, kb, ci >> 1);
+        const int kb = ci % C::kKBufs, sbuf = NBUF > 1 ? ci & 1 : 0;
+        wait(kKFull, kb, ci / C::kKBufs);
         if (!ok) return;
         tc::fence_after_sync();
         const uint32_t k = sb + C::kOffK + kb * C::kKBuf, d = tmem + C::kSCol + (i * NBUF + sbuf) * KT;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t a = tmem + C::kQCol + i * (D / 2) + 8 * ks;
-          tc::mma_f16_ta(d, a, tc::smem_desc(k + 256 * ks, 128, (D / 8) * 128), idesc_s, ks > 0);
-          if constexpr (C::kKLo)
-            tc::mma_f16_ta(d, a, tc::smem_desc(k + C::kTile + 256 * ks, 128, (D / 8) * 128), idesc_s, 1);
+          const uint32_t at = k + (ks / 4) * KT * 128 + (ks % 4) * 32;
+          tc::mma_f16_ta(d, a, tc::smem_desc_sw128(at, 16, 1024), idesc_s, ks > 0);
+          if constexpr (C::kKLo) tc::mma_f16_ta(d, a, tc::smem_desc_sw128(at + C::kTile, 16, 1024), idesc_s, 1);
         }
         if (i == MT - 1) tc::commit(bar(kKEmpty, kb));
         tc::commit(bar(kSFull, MT == 1 ? sbuf : i));
       };
       // O_i += P_i(ci) V
       auto mma_o = [&](int i, int ci) {
-        const int vb = ci & 1, sbuf = NBUF > 1 ? ci & 1 : 0;
+        const int vb = ci % C::kVBufs, sbuf = NBUF > 1 ? ci & 1 : 0;
         wait(kPFull, MT == 1 ? sbuf : i, MT == 1 ? ci >> 1 : ci);
-        wait(kVFull, vb, ci >> 1);
+        wait(kVFull, vb, ci / C::kVBufs);
         if (!ok) return;
         tc::fence_after_sync();
         const uint32_t v = sb + C::kOffV + vb * C::kVBuf, a0 = tmem + C::kSCol + (i * NBUF + sbuf) * KT;
-        const uint32_t d = tmem + C::kOCol + i * D;
+        const uint32_t d = tmem + C::kOCol + i * C::kOCols;
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks) {
-          tc::mma_f16_ta(d, a0 + 8 * ks, v_desc(v, ks), idesc_o, ci > 0 || ks > 0);
-          if constexpr (C::kVLo) tc::mma_f16_ta(d, a0 + 8 * ks, v_desc(v + C::kTile, ks), idesc_o, 1);
-          if constexpr (C::kMTile)
-            tc::mma_f16_ta(tmem + C::kMCol, a0 + 8 * ks,
-                           tc::smem_desc(sb + C::kOffM + vb * C::kMBytes + 256 * ks, 128, (KT / 8) * 128),
-                           tc::idesc_f16_f32(kTileRows, 16), ci > 0 || ks > 0);
+          tc::mma_f16_ta(d, a0 + 8 * ks, v_desc(v, ks), idesc_oc, ci > 0 || ks > 0);
+          if constexpr (C::kVLo) tc::mma_f16_ta(d, a0 + 8 * ks, v_desc(v + C::kLoOff, ks), idesc_o, 1);
         }
         if (i == MT - 1) tc::commit(bar(kVEmpty, vb));
         if (NBUF > 1 || ci == n_chunks - 1) tc::commit(bar(kPvDone, i));
@@ -488,37 +493,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- staging --
     const int sw = warp - 4;
-    if constexpr (C::kMTile) {               // the block rows that are none, and the gaps, once
-      for (uint32_t i = tid - 128; i < 2 * C::kMBytes / 16; i += kStageThreads)
-        sts128(sb + C::kOffM + 16 * i, make_uint4(0, 0, 0, 0));
+    if constexpr (C::kMCols) {               // the unused columns of the minima's blocks, once
+      for (uint32_t i = tid - 128; i < C::kVBufs * KT * 8u; i += kStageThreads)
+        sts128(sb + C::kOffV + (i / (KT * 8)) * C::kVBuf + C::kTile + 16 * (i % (KT * 8)), make_uint4(0, 0, 0, 0));
       named_barrier_sync(1, kStageThreads);
     }
     for (int ci = 0; ci < n_chunks; ++ci) {
-      const int s = ci % kRaw, k = ci & 1;
-      const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, pmask = chunk_mask(ci);
-      ok = mbar_wait_bounded(raw_full(s), (ci / kRaw) & 1, p.status);
-      if (ok && ci >= 2) ok = mbar_wait_bounded(bar(kKEmpty, k), ((ci >> 1) - 1) & 1, p.status);
+      const int s = ci % RAW, kb = ci % C::kKBufs, vb = ci % C::kVBufs, valid = count - ci * KT;
+      const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, rawv = rawk + NP * C::kKSeg, pmask = chunk_mask(ci);
+      ok = mbar_wait_bounded(raw_full(s), (ci / RAW) & 1, p.status);
+      if (ok && ci >= C::kKBufs) ok = mbar_wait_bounded(bar(kKEmpty, kb), (ci / C::kKBufs - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      stage_k<D, KF, KT>(rawk, sb + C::kOffK + k * C::kKBuf, sw, lane);
+      stage_k<D, KF, KT>(rawk, sb + C::kOffK + kb * C::kKBuf, sw, lane);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kKFull, k));
-      if (ci >= 2) ok = mbar_wait_bounded(bar(kVEmpty, k), ((ci >> 1) - 1) & 1, p.status);
+      if (lane == 0) mbar_arrive(bar(kKFull, kb));
+      if (ci >= C::kVBufs) ok = mbar_wait_bounded(bar(kVEmpty, vb), (ci / C::kVBufs - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t rawv = rawk + NP * C::kKSeg, vbuf = sb + C::kOffV + k * C::kVBuf;
+      const uint32_t vbuf = sb + C::kOffV + vb * C::kVBuf;
       if constexpr (C::kVRows)
-        stage_v<D, VF, KT, C::kMTile>(rawv, vbuf, pmask, count - ci * KT, sw, lane);
+        stage_v<D, VF, KT, C::kMCols, C::kLoOff>(rawv, vbuf, pmask, valid, sw, lane);
       else
-        stage_v_nvfp4<D, KT>(rawv, vbuf, pmask, count - ci * KT, tid - 128);
-      if constexpr (C::kMTile)
-        if (sw == (ci & (kStageWarps - 1)))
-          stage_m<D, KT>(rawv, sb + C::kOffM + k * C::kMBytes, pmask, count - ci * KT, lane);
-      fence_proxy_async();                   // V^T for the tensor cores, the raw chunk for the next copies
+        stage_v_nvfp4<D, KT>(rawv, vbuf, pmask, valid, tid - 128);
+      if constexpr (C::kMCols) {             // 32 tokens by each of two warps, other ones each time
+        const int part = (sw - 2 * ci) & (kStageWarps - 1);
+        if (part < KT / 32) stage_m<D, KT>(rawv, vbuf + C::kTile, pmask, valid, 32 * part + lane);
+      }
+      fence_proxy_async();                   // V^ for the tensor cores, the raw chunk for the next copies
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(kVFull, k));
+        mbar_arrive(bar(kVFull, vb));
         mbar_arrive(raw_empty(s));
       }
     }
@@ -601,20 +607,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
-            tc::ld_32x32b_x32(tmem + tlane + C::kOCol + i * D + c, o);
+            tc::ld_32x32b_x32(tmem + tlane + C::kOCol + i * C::kOCols + c, o);
             tc::wait_ld_all();
             tc::hold<32>(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::st_32x32b_x32(tmem + tlane + C::kOCol + i * D + c, o);
+            tc::st_32x32b_x32(tmem + tlane + C::kOCol + i * C::kOCols + c, o);
           }
-          if constexpr (C::kMTile) {
+          if constexpr (C::kMCols) {
             uint32_t o[16];
-            tc::ld_32x32b_x16(tmem + tlane + C::kMCol, o);
+            tc::ld_32x32b_x16(tmem + tlane + C::kOCol + D, o);
             tc::wait_ld(o);
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::st_32x32b_x16(tmem + tlane + C::kMCol, o);
+            tc::st_32x32b_x16(tmem + tlane + C::kOCol + D, o);
           }
           l[i] *= alpha;
         }
@@ -654,8 +660,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const int r = r0 + i * kTileRows + tid;
       const float inv = l[i] > 0.f ? p.v_post / l[i] : 0.f;
       uint32_t ms[16];                       // the minima's sums, per 32-dim block; a half as the staged values are
-      if constexpr (C::kMTile) {
-        tc::ld_32x32b_x16(tmem + tlane + C::kMCol, ms);
+      if constexpr (C::kMCols) {
+        tc::ld_32x32b_x16(tmem + tlane + C::kOCol + D, ms);
         tc::wait_ld(ms);
       }
       const uint32_t row = sb + C::kOffK + (i * kTileRows + tid) * C::kRowBytes;
@@ -663,10 +669,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       for (int c = 0; c < D; c += 32) {
         if (!ok) break;
         uint32_t o[32];
-        tc::ld_32x32b_x32(tmem + tlane + C::kOCol + i * D + c, o);
+        tc::ld_32x32b_x32(tmem + tlane + C::kOCol + i * C::kOCols + c, o);
         tc::wait_ld_all();
         tc::hold<32>(o);
-        const float half_m = C::kMTile ? 0.5f * __uint_as_float(ms[c / 32]) : 0.f;
+        const float half_m = C::kMCols ? 0.5f * __uint_as_float(ms[c / 32]) : 0.f;
         float x[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = l[i] > 0.f ? (__uint_as_float(o[e]) + half_m) * inv : 0.f;

@@ -11,7 +11,7 @@
 namespace memra {
 
 // Keys of one step of the split pass (the N of the score MMA).
-__host__ __device__ constexpr int tree_chunk_tokens(int D) { return D == 128 ? 64 : 32; }
+constexpr int kTreeKeys = 64;
 
 // Row tiles (128 rows: nodes x the group's heads) that one CTA holds: two at
 // head_dim 128 where the rows need them, so that a page is dequantized once for 256 rows.
