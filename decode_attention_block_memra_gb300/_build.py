@@ -28,7 +28,7 @@ SOURCES = ["api.cu", "kv_append.cu", "combine.cu", "decode_d128.cu", "decode_d25
            "api_tree.cu", "tree.cu"]
 HEADERS = ["memra_device.cuh", "decode_kernel.cuh", "kv_quant.cuh", "cascade.cuh", "tcgen05.cuh",
            "host_checks.cuh", "pages.cuh", "prompt.cuh", "kv_stage.cuh",
-           "tree.cuh"]
+           "tree.cuh", "softmax_tile.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]

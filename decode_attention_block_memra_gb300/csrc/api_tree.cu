@@ -42,7 +42,7 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
     return MEMRA_ERR_UNSUPPORTED;
   if (!std::isfinite(sm_scale)) return MEMRA_ERR_INVALID_ARG;
   const int group = n_heads / n_kv_heads, rows = n_nodes * group;
-  const int row_ctas = static_cast<int>(ceil_div(rows, 128 * tree_tiles(head_dim, rows)));
+  const int row_ctas = static_cast<int>(ceil_div(rows, 128));
   const int64_t all_rows = static_cast<int64_t>(batch) * n_nodes * n_heads;
   if (static_cast<int64_t>(batch) * row_ctas > 65535 || all_rows > INT32_MAX) return MEMRA_ERR_UNSUPPORTED;
   if (batch == 0) return MEMRA_OK;
@@ -74,11 +74,14 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   p.num_pages = cache->num_pages;
   p.max_pages = max_pages_per_seq;
   p.max_seq_len = max_seq_len;
-  p.target = std::min(kTreeMaxSplits, std::max(1, device_sms() / (n_kv_heads * row_ctas)));
+  p.target = std::min(kTreeMaxSplits, std::max(1, device_sms() * tree_ctas_per_sm(head_dim) / (n_kv_heads * row_ctas)));
   p.max_splits = tree_most_splits(max_seq_len, kTreeMaxSplits);
   p.row_ctas = row_ctas;
   // staged values: q8_0 / q5_1 / q4_0 at half size, fp8 / NVFP4 without their tensor scale
-  p.scale_log2 = sm_scale * (cache->k_fmt == MEMRA_KV_Q8_0 ? 2.f : cache->k_scale) * 1.4426950408889634f;
+  p.scale_log2 = std::fabs(sm_scale) * (cache->k_fmt == MEMRA_KV_Q8_0 ? 2.f : cache->k_scale) * 1.4426950408889634f;
+  p.q_and = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
+  p.q_xor = sm_scale < 0.f ? 0x80008000u : 0u;
+  if (p.scale_log2 == 0.f) p.scale_log2 = 1.f;
   p.v_post = scaled_format(cache->v_fmt) ? cache->v_scale : 2.f;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = cuda_status(launch_tree(head_dim, cache->k_fmt, cache->v_fmt, p, s));

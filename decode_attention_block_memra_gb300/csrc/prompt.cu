@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include "prompt.cuh"
+#include "softmax_tile.cuh"
 #include "tcgen05.cuh"
 
 namespace memra {
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     // ------------------------------------------------------------------ loads --
     const int slots = 2 * (jhi - jlo);
     int issued = 0;
-    if (lane == 0) {
+    const bool leader = tc::elect_one();
+    if (leader) {
       auto load_q = [&](int i) {
         if (lo[i] == hi[i]) return;
         mbar_arrive_expect_tx(q_full(i), static_cast<uint32_t>(p.group * p.tpt) * 128 * C::kBlocks);
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       load_q(0);
       for (int n = 0; n < slots; ++n) {             // K and V of a step by turns
         const int s = n % ST;
-        if (n >= ST) ok = mbar_wait_bounded(kv_empty(s), (n / ST - 1) & 1, p.status);
+        if (n >= ST) ok = mbar_wait_suspended(kv_empty(s), (n / ST - 1) & 1, p.status);
         if (!ok) break;
         mbar_arrive_expect_tx(kv_full(s), C::kKvBytes);
 #pragma unroll
@@ -206,11 +208,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
     }
     __syncwarp();
-    ok = __shfl_sync(0xffffffffu, ok, 0);
+    ok = __all_sync(0xffffffffu, ok);
     if (ok && tail) {
       // rows behind the sequence may hold anything, and 0 * inf is not 0: they become zeros
       const int n = slots - 1, s = n % ST;
-      ok = mbar_wait_bounded(kv_full(s), (n / ST) & 1, p.status);
+      ok = mbar_wait_suspended(kv_full(s), (n / ST) & 1, p.status);
       const int from = w.len - (jhi - 1) * KT;
       const uint32_t v = sb + C::kOffKv + s * C::kKvBytes;
       for (int i = lane; ok && i < (KT - from) * 8 * C::kBlocks; i += 32) {
@@ -220,22 +222,22 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(v_zeroed);
+      if (leader && ok) mbar_arrive(v_zeroed);
     }
     // every copy has landed before the CTA can leave
-    if (lane == 0)
-      for (int n = max(0, issued - ST); n < issued; ++n) mbar_wait_bounded(kv_full(n % ST), (n / ST) & 1, p.status);
+    if (leader)
+      for (int n = max(0, issued - ST); n < issued; ++n) mbar_wait_suspended(kv_full(n % ST), (n / ST) & 1, p.status);
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------------- MMA --
     if (tc::elect_one()) {
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
       constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(kTileRows, D);
-      auto slot_full = [&](int n) { return mbar_wait_bounded(kv_full(n % ST), (n / ST) & 1, p.status); };
+      auto slot_full = [&](int n) { return mbar_wait_suspended(kv_full(n % ST), (n / ST) & 1, p.status); };
       // S_i(j) = Q_i K(j)^T into score buffer b
       auto mma_s = [&](int i, int b, int j) {
         const int n = 2 * (j - jlo);
         ok = ok && slot_full(n);
-        if (ok && j == lo[i]) ok = mbar_wait_bounded(q_full(i), 0, p.status);
+        if (ok && j == lo[i]) ok = mbar_wait_suspended(q_full(i), 0, p.status);
         if (!ok) return;
         tc::fence_after_sync();
         const uint32_t q = sb + i * C::kQBytes, k = sb + C::kOffKv + (n % ST) * C::kKvBytes;
@@ -249,9 +251,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       // O_i += P_i(j) V(j), P in the columns of its scores
       auto mma_o = [&](int i, int b, int j) {
         const int n = 2 * (j - jlo) + 1, u = j - lo[i];
-        ok = ok && mbar_wait_bounded(p_full(i, b), (u / NBUF) & 1, p.status);
+        ok = ok && mbar_wait_suspended(p_full(i, b), (u / NBUF) & 1, p.status);
         ok = ok && slot_full(n);
-        if (ok && tail && j == jhi - 1) ok = mbar_wait_bounded(v_zeroed, 0, p.status);
+        if (ok && tail && j == jhi - 1) ok = mbar_wait_suspended(v_zeroed, 0, p.status);
         if (!ok) return;
         tc::fence_after_sync();
         const uint32_t v = sb + C::kOffKv + (n % ST) * C::kKvBytes;
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
       // what was issued has completed before the CTA can leave
       tc::commit(drained);
-      mbar_wait_bounded(drained, 0, p.status);
+      mbar_wait_suspended(drained, 0, p.status);
     }
     __syncwarp();
   } else {
@@ -303,13 +305,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     const bool live = tl < p.tpt && t < w.len;
     const int tile_first = w.t0 + i * p.tpt, tile_last = min(w.len, tile_first + p.tpt) - 1;
     const int n_steps = hi[i] - lo[i];
-    float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float m = -INFINITY;
+    uint64_t l = 0;                                 // two sums, of the even and the odd keys
     const uint32_t o_col = tmem + tlane + C::kOCol + i * D;
 #pragma unroll 1
     for (int u = 0; u < n_steps; ++u) {
       const int j = lo[i] + u, b = NBUF > 1 ? u & 1 : 0;
       const uint32_t s_col = tmem + tlane + (i * NBUF + b) * KT;
-      ok = mbar_wait_bounded(s_full(i, b), (u / NBUF) & 1, p.status);
+      ok = mbar_wait_suspended(s_full(i, b), (u / NBUF) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
@@ -325,12 +328,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         for (int c = 0; c < KT; ++c)
           if (c > last || c < first) s[c] = 0xff800000u;          // -inf
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < KT; c += 4)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[c + e]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      const float top = row_max(s) * p.scale_log2;
       float alpha = 1.f;
       if (live && top > m + kLazy) {                // also the first step with a key (m = -inf)
         if (m != -INFINITY) alpha = fast_exp2(m - top);
@@ -340,7 +338,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         // O's rows of this warp times alpha, once the product before has completed
         // (one score buffer: these scores were issued behind it)
         if (NBUF > 1) {
-          ok = mbar_wait_bounded(pv_done(i), (u - 1) & 1, p.status);
+          ok = mbar_wait_suspended(pv_done(i), (u - 1) & 1, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc::fence_after_sync();
@@ -355,21 +353,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
           tc::st_32x32b_x32(o_col + c, o);
         }
-        l0 *= alpha;
-        l1 *= alpha;
+        l = fma_f2(l, pack_f2(alpha, alpha), 0);
       }
       const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
       for (int c = 0; c < KT; c += 64) {
         uint32_t w2[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float p0 = fast_exp2(fmaf(__uint_as_float(s[c + 2 * e]), p.scale_log2, -mu));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(s[c + 2 * e + 1]), p.scale_log2, -mu));
-          l0 += p0;
-          l1 += p1;
-          w2[e] = pack_half2(p0, p1);
-        }
+        row_weights<32>(s + c, p.scale_log2, mu, w2, l);
         tc::st_32x32b_x32(s_col + c / 2, w2);
       }
       tc::wait_st();
@@ -378,11 +368,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     }
     // The last product.  Two score buffers: the product before it may still be
     // running, so its phase comes first (a parity names only the next phase).
-    if (NBUF > 1 && n_steps > 1 && ok) ok = mbar_wait_bounded(pv_done(i), (n_steps - 2) & 1, p.status);
-    if (n_steps > 0 && ok) ok = mbar_wait_bounded(pv_done(i), NBUF > 1 ? (n_steps - 1) & 1 : 0, p.status);
+    if (NBUF > 1 && n_steps > 1 && ok) ok = mbar_wait_suspended(pv_done(i), (n_steps - 2) & 1, p.status);
+    if (n_steps > 0 && ok) ok = mbar_wait_suspended(pv_done(i), NBUF > 1 ? (n_steps - 1) & 1 : 0, p.status);
     if (__all_sync(0xffffffffu, n_steps > 0 && ok)) {
       tc::fence_after_sync();
-      const float l = l0 + l1, inv = l > 0.f ? 1.f / l : 0.f;
+      float l0, l1;
+      unpack_f2(l, l0, l1);
+      const float inv = l0 + l1 > 0.f ? 1.f / (l0 + l1) : 0.f;
       const int head = kvh * p.group + rl % p.group;
       __half *dst = p.out + (static_cast<size_t>(w.first + t) * p.n_heads + head) * D;
 #pragma unroll 1

@@ -5,21 +5,21 @@
 //   o_i = sum_u p_iu V^_u / sum_u p_iu,  p_iu = 2^(q_i . K^_u * scale * log2(e) - m_i)
 //
 // The rows of one KV head, nodes x the group's query heads, 128 to a tile, are
-// the M side of tcgen05 MMAs, so a page is read and dequantized once for all of
-// them (twice or more only past 256 rows).  CTA = (split of the keys, KV head,
-// sequence and row tiles):
-//   * a producer thread copies raw pages into a ring of chunks (64 keys);
-//   * eight staging warps dequantize a chunk's K and V into double-buffered
-//     fp16 operand tiles: exact hi + lo pairs for q8_0, q5_1 and q4_0, single
-//     values for fp8 and NVFP4, so only P is rounded (fp16, relative 2^-11 a
-//     weight);
+// the M side of tcgen05 MMAs, so a page is read and dequantized once for 128 of
+// them.  CTA = (split of the keys, KV head, sequence and row tile):
+//   * a copy warp brings raw pages into a ring of two chunks (64 keys);
+//   * staging warps dequantize a chunk into fp16 operand tiles: exact hi + lo
+//     pairs for q8_0, q5_1 and q4_0, single values for fp8 and NVFP4, so only P
+//     is rounded (fp16, relative 2^-11 a weight);
 //   * one MMA thread: S = Q K^T with Q in tensor memory, O += P V with P in
-//     tensor memory over its scores; neither A operand touches shared memory,
+//     tensor memory over its scores; the A operands stay out of shared memory,
 //     whose bandwidth the staged tiles need;
-//   * four softmax warps, thread = row (of each tile in turn).
-// One tile: two score buffers, the scores run a chunk ahead.  Two tiles
-// (head_dim 128): one buffer each, the tensor cores work on one tile while the
-// softmax takes the other.
+//   * four softmax warps, thread = row.
+// head_dim 128: two CTAs share an SM (256 tensor-memory columns each, one score
+// buffer), so one's chain of copy, staging, MMA and softmax fills the other's
+// gaps, its first and last steps included.  head_dim 256: one CTA with two score
+// buffers, the scores a chunk ahead.
+// What bounds it is the staging: the MMAs take half its time.
 // A sequence of one split writes its rows directly; the others leave (o, lse)
 // partials that tree_merge_kernel joins.
 #include <cuda_fp16.h>
@@ -29,6 +29,7 @@
 #include <type_traits>
 
 #include "kv_stage.cuh"
+#include "softmax_tile.cuh"
 #include "tcgen05.cuh"
 #include "tree.cuh"
 
@@ -37,46 +38,51 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr float kLazy = 8.f;               // log2 units: P stays <= 256 between rescales
-constexpr int kStageWarps = 8;
-constexpr int kStageThreads = 32 * kStageWarps;
-constexpr int kMmaWarp = 4 + kStageWarps, kCopyWarp = kMmaWarp + 1;
-constexpr int kTreeThreads = 32 * (kCopyWarp + 1);
 
-template <int D, int KF, int VF, int MT>
+template <int D, int KF, int VF>
 struct TreeCfg {
+  static constexpr int kCtas = tree_ctas_per_sm(D);
+  static constexpr int kStageWarps = D == 128 ? 4 : 8;
+  static constexpr int kMmaWarp = 4 + kStageWarps, kCopyWarp = kMmaWarp + 1, kThreads = 32 * (kCopyWarp + 1);
   static constexpr int kPages = kTreeKeys / kPage;
-  static constexpr int kBufs = MT == 1 ? 2 : 1;                 // score buffers of a tile
+  static constexpr int kBufs = D == 128 ? 1 : 2;                // score buffers
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
   static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
   static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
   // q5_1's minima as 16 more columns of V^ (one per 32-dim block; the others zero), joined to O at the
-  // end: an exact d q + m in two fp16 parts costs ten operations a pair, d q alone three.  Two row tiles
-  // (or head_dim 256) leave no tensor memory or no MMA width for them.
-  static constexpr bool kMCols = VF == MEMRA_KV_Q5_1 && MT == 1 && D == 128;
-  static constexpr int kOCols = D + (kMCols ? 16 : 0);
+  // end: an exact d q + m in two fp16 parts costs ten operations a pair, d q alone three.  The MMA is at
+  // most 256 wide, so at head_dim 256 the pair it is.
+  static constexpr bool kMCols = VF == MEMRA_KV_Q5_1 && D == 128;
+  static constexpr int kOCols = D + (D == 128 ? 16 : 0);
   static constexpr bool kVRows = VF != MEMRA_KV_NVFP4;          // V staged as token rows (MN-major)
-  // operand tiles and how many chunks of them: head_dim 256 has room for one where a tile is a pair
+  // operand tiles: one chunk of them where a tile is a hi + lo pair, else two
   static constexpr uint32_t kTile = kTreeKeys * D * 2;
   static constexpr uint32_t kLoOff = kTile + (kMCols ? kTreeKeys * 128 : 0);      // V: hi, minima, lo
   static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kVLo ? kLoOff + kTile : kTile;
-  static constexpr int kKBufs = D == 256 && kKLo ? 1 : 2, kVBufs = D == 256 && kVLo ? 1 : 2;
-  static constexpr int kRaw = D == 256 ? 2 : 3;                 // chunks of raw pages
+  static constexpr int kKBufs = kKLo ? 1 : 2, kVBufs = kVLo ? 1 : 2;
+  static constexpr int kRaw = 2;                                // chunks of raw pages
   static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
-  // barriers and page ids, then K^ and V^ tiles and the raw chunks; the output rows reuse everything
-  // behind the page ids
-  static constexpr uint32_t kOffBar = 0, kOffPid = 256;
-  static constexpr uint32_t kOffK = (kOffPid + 4 * kTreeSplitPages + 1023) & ~1023u;
-  static constexpr uint32_t kOffV = kOffK + kKBufs * kKBuf, kOffRaw = kOffV + kVBufs * kVBuf;
+  // Q in tensor memory, but for the last 32 dims at head_dim 128 (two CTAs share its 512 columns:
+  // 48 of Q, 144 of O, 64 of scores each), which lie in shared memory
+  static constexpr int kQTmem = D == 128 ? 96 : D, kQSmem = D - kQTmem;
+  // barriers and page ids, then K^ and V^ tiles, Q's last dims and the raw chunks; the output rows reuse
+  // everything behind the page ids
+  static constexpr uint32_t kOffBar = 0, kOffPid = 256, kOffK = 4096;
+  static constexpr uint32_t kOffV = kOffK + kKBufs * kKBuf, kOffQ = kOffV + kVBufs * kVBuf;
+  static constexpr uint32_t kOffRaw = kOffQ + kTileRows * kQSmem * 2;
   static constexpr uint32_t kEnd = kOffRaw + kRaw * kRawBytes;
   static constexpr uint32_t kRowBytes = D * 4 + 16;             // padded output row
-  static constexpr uint32_t kEndRows = kOffK + MT * kTileRows * kRowBytes;
-  // One CTA per SM, whatever runs beside it: a CTA takes all 512 tensor-memory
-  // columns, and one that shares an SM with another holder of them would wait.
-  static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows;
-  static constexpr uint32_t kSmem = kNeed < 116 * 1024 ? 116 * 1024 : kNeed;
-  static constexpr uint32_t kQCol = 0, kOCol = MT * D / 2, kSCol = kOCol + MT * kOCols;   // tensor-memory columns
-  static_assert(kSmem <= 232448, "shared memory");
-  static_assert(kSCol + MT * kBufs * kTreeKeys <= 512, "tensor memory");
+  static constexpr uint32_t kEndRows = kOffK + kTileRows * kRowBytes;
+  // Tensor memory: a CTA that found its columns taken would wait in its
+  // allocation, so shared memory is sized that no more CTAs of this or the
+  // library's other tensor-memory kernels fit an SM than its 512 columns hold.
+  static constexpr uint32_t kTCols = D == 128 ? 256 : 512;
+  static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows, kFloor = (D == 128 ? 78 : 150) * 1024;
+  static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
+  static constexpr uint32_t kQCol = 0, kOCol = kQTmem / 2, kSCol = kOCol + kOCols;   // tensor-memory columns
+  static_assert(kOffPid + 4 * kTreeSplitPages <= kOffK, "page ids");
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 232448, "shared memory");
+  static_assert(kSCol + kBufs * kTreeKeys <= static_cast<int>(kTCols) && kCtas * kTCols <= 512, "tensor memory");
   static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
 };
 
@@ -85,13 +91,32 @@ struct TreeCfg {
 // page layout: conflict-free), and each value goes to the tile from the thread
 // that read it.  A warp task is one 512-byte run of codes.
 
+// Eight q8_0 or fp8 codes of K as fp16: q8_0 q d / 2 in hi + lo parts (d2 the
+// scale in both halves), fp8 the value in hi.
+template <int KF>
+__device__ __forceinline__ void convert_k16(uint2 w, uint32_t d2, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  if constexpr (KF == MEMRA_KV_Q8_0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // stored q + 128, spliced under 1024: 1152 + q, then q / 2 exactly
+      const uint32_t code = __byte_perm(k < 2 ? w.x : w.y, 0x64646464u, k & 1 ? 0x4342 : 0x4140);
+      const uint32_t qh = hfma2_u32(code, 0x38003800u, 0xE080E080u);          // 0.5, -576
+      hi[k] = hmul2_u32(qh, d2);
+      lo[k] = hfms2_u32(qh, d2, hi[k]);
+    }
+  } else {
+    e4m3x4_to_half2x2(w.x, hi[0], hi[1]);
+    e4m3x4_to_half2x2(w.y, hi[2], hi[3]);
+  }
+}
+
 // K^: token rows of 128 bytes (64 dims, the K axis of the score MMA), 128-byte-
 // swizzled (the 16-byte unit of a row is XORed with the row's index in its group
 // of 8), one block of KEYS rows per 64 dims.  A lane holds the same 8 dims of
 // two 32-dim blocks; lanes of odd tokens store the second block first, so that
 // eight lanes' 16-byte stores always fall on different banks.
 // Tokens that do not exist stage whatever the pages hold: their scores are masked.
-template <int D, int KF, int KEYS>
+template <int D, int KF, int KEYS, int WARPS>
 __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, int lane) {
   constexpr int NB = D / 32, SEG = k_seg_bytes(KF, D), B2 = D / 64;
   constexpr uint32_t LO = KEYS * D * 2;
@@ -99,10 +124,10 @@ __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, in
   if constexpr (KF == MEMRA_KV_NVFP4) {
     // run (page, 64-dim block): words (b % 2, e / 4), bytes tp + 2 (e % 4 / 2), nibbles e % 2
     constexpr int TASKS = KEYS / kPage * B2;
-    static_assert(TASKS % kStageWarps == 0, "whole tasks");
+    static_assert(TASKS % WARPS == 0, "whole tasks");
 #pragma unroll
-    for (int it = 0; it < TASKS / kStageWarps; ++it) {
-      const int task = warp + it * kStageWarps, pg = task / B2, b2 = task % B2;
+    for (int it = 0; it < TASKS / WARPS; ++it) {
+      const int task = warp + it * WARPS, pg = task / B2, b2 = task % B2;
       const uint32_t seg = raw + pg * SEG;
       const uint4 x = lds128(seg + (b2 * 32 + lane) * 16);
 #pragma unroll
@@ -123,24 +148,39 @@ __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, in
     }
   } else {
     // run (page, token half, 64-dim block): 8 bytes for each of the two 32-dim blocks
-    constexpr int TASKS = KEYS / 8 * B2;
-    static_assert(TASKS % kStageWarps == 0, "whole tasks");
+    constexpr unsigned TASKS = KEYS / 8 * B2, STEP = WARPS / B2;     // a warp's token groups are STEP apart
+    static_assert(TASKS % WARPS == 0 && WARPS % B2 == 0 && (STEP % 2 == 0 || STEP == 1), "whole tasks");
+    const unsigned g0 = static_cast<unsigned>(warp) / B2, b2 = static_cast<unsigned>(warp) % B2;
+    const bool odd = tg & 1;
+    const uint32_t sel0 = odd ? 0x3232u : 0x1010u, sel1 = odd ? 0x1010u : 0x3232u;
+    const uint32_t row = buf + b2 * (KEYS * 128) + (8 * g0 + tg) * 128;
+    const uint32_t to0 = row + (((odd ? 4 : 0) + kc) ^ tg) * 16, to1 = row + (((odd ? 0 : 4) + kc) ^ tg) * 16;
+    const uint32_t codes = raw + (g0 >> 1) * SEG + (((g0 & 1) * B2 + b2) * 32 + lane) * 16;
+    const uint32_t scales = raw + (g0 >> 1) * SEG + 16 * D + ((8 * (g0 & 1) + tg) * NB + 2 * b2) * 2;
+    // (STEP = 1: every warp starts at group 0, so the halves of a page alternate)
+    auto code_off = [](unsigned it) { return it * STEP / 2 * SEG + (it * STEP) % 2 * (B2 * 512); };
+    auto scale_off = [](unsigned it) { return it * STEP / 2 * SEG + (it * STEP) % 2 * (8 * NB * 2); };
+    constexpr unsigned PER = TASKS / WARPS, BATCH = PER < 4 ? PER : 4;
+    uint4 x[BATCH];
+    uint32_t d[BATCH];
 #pragma unroll
-    for (int it = 0; it < TASKS / kStageWarps; ++it) {
-      const int task = warp + it * kStageWarps, g = task / B2, b2 = task % B2;     // token group, block pair
-      const uint32_t seg = raw + (g >> 1) * SEG;
-      const uint4 x = lds128(seg + (((g & 1) * B2 + b2) * 32 + lane) * 16);
-      uint32_t d = 0;
-      if constexpr (KF == MEMRA_KV_Q8_0) d = lds32(seg + 16 * D + ((8 * (g & 1) + tg) * NB + 2 * b2) * 2);
+    for (unsigned it = 0; it < PER; ++it) {
+      if (it % BATCH == 0) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool bp = e ^ (tg & 1);
-        uint32_t hi[4], lo[4];
-        convert_k8<KF>(KRaw{make_uint2(bp ? x.z : x.x, bp ? x.w : x.y), bp ? d >> 16 : d & 0xFFFFu}, 0, hi, lo);
-        const uint32_t at = buf + b2 * KEYS * 128 + (8 * g + tg) * 128 + (((4 * bp + kc) ^ tg) << 4);
-        sts128(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        if constexpr (KF == MEMRA_KV_Q8_0) sts128(at + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        for (unsigned e = 0; e < BATCH; ++e) {
+          x[e] = lds128(codes + code_off(it + e));
+          d[e] = KF == MEMRA_KV_Q8_0 ? lds32(scales + scale_off(it + e)) : 0u;
+        }
       }
+      const uint4 y = x[it % BATCH];
+      const uint2 w0 = make_uint2(odd ? y.z : y.x, odd ? y.w : y.y), w1 = make_uint2(odd ? y.x : y.z, odd ? y.y : y.w);
+      uint32_t hi[4], lo[4];
+      convert_k16<KF>(w0, __byte_perm(d[it % BATCH], 0, sel0), hi, lo);
+      sts128(to0 + it * STEP * 1024, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      if constexpr (KF == MEMRA_KV_Q8_0) sts128(to0 + it * STEP * 1024 + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      convert_k16<KF>(w1, __byte_perm(d[it % BATCH], 0, sel1), hi, lo);
+      sts128(to1 + it * STEP * 1024, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      if constexpr (KF == MEMRA_KV_Q8_0) sts128(to1 + it * STEP * 1024 + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
   }
 }
@@ -169,7 +209,7 @@ __device__ __forceinline__ int page_tokens(uint32_t pmask, int pg, int valid) {
 // warp's 8-byte stores fill all banks.  Tokens that do not exist become zeros:
 // 0 * (what their bytes stand for) need not be 0.  q5_1 stages d q alone where
 // the minima have columns of their own (M_COLS), else d q + m by a TwoSum.
-template <int D, int VF, int KEYS, bool M_COLS, uint32_t LO>
+template <int D, int VF, int KEYS, int WARPS, bool M_COLS, uint32_t LO>
 __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int warp, int lane) {
   constexpr int NB = D / 32, SEG = v_seg_bytes(VF, D), B2 = D / 64;
   const int vg = lane >> 2, c = lane & 3;
@@ -181,10 +221,10 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
   if constexpr (VF == MEMRA_KV_FP8_E4M3) {
     // run (page, 32-dim block): words 2 h + p, bytes 2 s + f
     constexpr int TASKS = KEYS / kPage * NB;
-    static_assert(TASKS % kStageWarps == 0, "whole tasks");
+    static_assert(TASKS % WARPS == 0, "whole tasks");
 #pragma unroll
-    for (int it = 0; it < TASKS / kStageWarps; ++it) {
-      const int task = warp + it * kStageWarps, pg = task / NB, b = task % NB, n = page_tokens(pmask, pg, valid);
+    for (int it = 0; it < TASKS / WARPS; ++it) {
+      const int task = warp + it * WARPS, pg = task / NB, b = task % NB, n = page_tokens(pmask, pg, valid);
       const uint4 x = lds128(raw + pg * SEG + (b * 32 + lane) * 16);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -201,61 +241,72 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
     }
   } else {
     // run (page, 64-dim block): words 2 (b % 2) + h, bytes 2 f + p, nibbles s
-    constexpr int TASKS = KEYS / kPage * B2;
-    static_assert(TASKS % kStageWarps == 0, "whole tasks");
+    constexpr unsigned TASKS = KEYS / kPage * B2, STEP = WARPS / B2;       // a warp's pages are STEP apart
+    static_assert(TASKS % WARPS == 0 && WARPS % B2 == 0, "whole tasks");
+    const unsigned pg0 = static_cast<unsigned>(warp) / B2, b2 = static_cast<unsigned>(warp) % B2;
+    uint32_t to[2][2];                   // [b % 2][f], the row of p = 0
 #pragma unroll
-    for (int it = 0; it < TASKS / kStageWarps; ++it) {
-      const int task = warp + it * kStageWarps, pg = task / B2, b2 = task % B2, n = page_tokens(pmask, pg, valid);
-      const uint32_t seg = raw + pg * SEG;
-      const uint4 x4 = lds128(seg + (b2 * 32 + lane) * 16);
-      const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
-      const uint32_t hw = VF == MEMRA_KV_Q5_1 ? lds32(seg + 8 * D + (lane * (NB / 2) + b2) * 4) : 0u;
+    for (int e = 0; e < 4; ++e)
+      to[e >> 1][e & 1] = buf + b2 * (KEYS * 128) + (kPage * pg0 + 2 * c + (e & 1)) * 128 +
+                          (((e >> 1) * 64 + vg * 8) ^ ((2 * c + (e & 1)) << 4));
+    const uint32_t seg0 = raw + pg0 * SEG;
+    const uint32_t codes = seg0 + (b2 * 32 + lane) * 16, fifths = seg0 + 8 * D + (lane * (NB / 2) + b2) * 4;
+    const uint32_t scales = seg0 + (VF == MEMRA_KV_Q5_1 ? 10 : 8) * D + (c * NB + 2 * b2) * 8;
+#pragma unroll
+    for (unsigned it = 0; it < TASKS / WARPS; ++it) {
+      const uint32_t off = it * STEP * SEG, row = it * STEP * (kPage * 128);
+      const uint4 x4 = lds128(codes + off);
+      const uint32_t hw = VF == MEMRA_KV_Q5_1 ? lds32(fifths + off) : 0u;
+      const uint4 d4 = lds128(scales + off);           // scales of the lane's tokens (halves 2 p + f), two blocks
+      uint4 m4 = make_uint4(0, 0, 0, 0);
+      if constexpr (VF == MEMRA_KV_Q5_1 && !M_COLS) m4 = lds128(scales + D + off);
+      const int n = page_tokens(pmask, pg0 + it * STEP, valid);
 #pragma unroll
       for (int bp = 0; bp < 2; ++bp) {
-        const int b = 2 * b2 + bp;
-        // scales (and minima) of the lane's tokens: halves 2 p + f
-        const uint2 dw = lds64(seg + (VF == MEMRA_KV_Q5_1 ? 10 : 8) * D + (c * NB + b) * 8);
-        uint2 mw = make_uint2(0, 0);
-        if constexpr (VF == MEMRA_KV_Q5_1 && !M_COLS) mw = lds64(seg + 11 * D + (c * NB + b) * 8);
         uint32_t hi[4][2], lo[4][2];     // [byte 2 f + p][h]
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t l4 = xw[2 * bp + h] & 0x0F0F0F0Fu, h4 = (xw[2 * bp + h] >> 4) & 0x0F0F0F0Fu;
+          const uint32_t x = bp ? (h ? x4.w : x4.z) : (h ? x4.y : x4.x);
+          uint32_t l4 = x & 0x0F0F0F0Fu, h4 = (x >> 4) & 0x0F0F0F0Fu;
           if constexpr (VF == MEMRA_KV_Q5_1) {
-            l4 |= ((hw << 4) >> (2 * bp + h)) & 0x10101010u;
+            l4 |= (hw << (4 - 2 * bp - h)) & 0x10101010u;
             h4 |= (hw >> (2 * bp + h)) & 0x10101010u;
           }
           const uint32_t p01 = __byte_perm(l4, h4, 0x5140), p23 = __byte_perm(l4, h4, 0x7362);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             // 1024 + q as fp16 for dims s = 0, 1; then q / 2 (q5_1) or (q - 8) / 2 (q4_0), exactly
-            const __half2 q2 = __hfma2(bits_h2(__byte_perm(k < 2 ? p01 : p23, 0x64646464u, k & 1 ? 0x4342 : 0x4140)),
-                                       __float2half2_rn(0.5f), __float2half2_rn(VF == MEMRA_KV_Q5_1 ? -512.f : -516.f));
+            const uint32_t q2 = hfma2_u32(__byte_perm(k < 2 ? p01 : p23, 0x64646464u, k & 1 ? 0x4342 : 0x4140), 0x38003800u,
+                                          VF == MEMRA_KV_Q5_1 ? 0xE000E000u : 0xE008E008u);   // 0.5, -512 or -516
             const int f = k >> 1, p = k & 1;
             const uint32_t sel = f ? 0x3232 : 0x1010;
-            const __half2 d2 = bits_h2(__byte_perm(p ? dw.y : dw.x, 0, sel));
-            const __half2 p_hi = __hmul2_rn(q2, d2);
-            const __half2 p_lo = __hfma2(q2, d2, __hneg2(p_hi));
+            const uint32_t d2 = __byte_perm(bp ? (p ? d4.w : d4.z) : (p ? d4.y : d4.x), 0, sel);
+            const uint32_t p_hi = h2_bits(__hmul2_rn(bits_h2(q2), bits_h2(d2)));
+            const uint32_t p_lo = hfms2_u32(q2, d2, p_hi);
             if constexpr (VF == MEMRA_KV_Q5_1 && !M_COLS) {
-              const __half2 m2 = __hmul2_rn(bits_h2(__byte_perm(p ? mw.y : mw.x, 0, sel)), __float2half2_rn(0.5f));
-              const __half2 s2 = __hadd2_rn(p_hi, m2);
-              const __half2 bb = __hsub2_rn(s2, p_hi);
-              const __half2 e2 = __hadd2_rn(__hsub2_rn(p_hi, __hsub2_rn(s2, bb)), __hsub2_rn(m2, bb));
+              const __half2 m2 = __hmul2_rn(bits_h2(__byte_perm(bp ? (p ? m4.w : m4.z) : (p ? m4.y : m4.x), 0, sel)),
+                                            __float2half2_rn(0.5f));
+              const __half2 s2 = __hadd2_rn(bits_h2(p_hi), m2);
+              const __half2 bb = __hsub2_rn(s2, bits_h2(p_hi));
+              const __half2 e2 = __hadd2_rn(__hsub2_rn(bits_h2(p_hi), __hsub2_rn(s2, bb)), __hsub2_rn(m2, bb));
               hi[k][h] = h2_bits(s2);
-              lo[k][h] = h2_bits(__hadd2_rn(e2, p_lo));
+              lo[k][h] = h2_bits(__hadd2_rn(e2, bits_h2(p_lo)));
             } else {
-              hi[k][h] = h2_bits(p_hi);
-              lo[k][h] = h2_bits(p_lo);
+              hi[k][h] = p_hi;
+              lo[k][h] = p_lo;
             }
           }
         }
+        if (n < kPage) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (8 * (k & 1) + 2 * c + (k >> 1) >= n) hi[k][0] = hi[k][1] = lo[k][0] = lo[k][1] = 0u;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int f = k >> 1, p = k & 1;
-          const bool live = 8 * p + 2 * c + f < n;
-          const uint32_t to = at(pg, p, f, b);
-          sts64(to, live ? hi[k][0] : 0u, live ? hi[k][1] : 0u);
-          sts64(to + LO, live ? lo[k][0] : 0u, live ? lo[k][1] : 0u);
+          const uint32_t at = to[bp][k >> 1] + row + (k & 1) * 1024;
+          sts64(at, hi[k][0], hi[k][1]);
+          sts64(at + LO, lo[k][0], lo[k][1]);
         }
       }
     }
@@ -264,13 +315,13 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
 
 // V^T of NVFP4 (dim rows, tokens along K, core matrices): its lanes hold single
 // dims, so a task gathers the 8 tokens of two dims and stores 16-byte rows.
-template <int D, int KEYS>
+template <int D, int KEYS, int WARPS>
 __device__ __forceinline__ void stage_v_nvfp4(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int st) {
-  constexpr int SEG = v_seg_bytes(MEMRA_KV_NVFP4, D), TASKS = KEYS / kPage * 2 * (D / 16) * 8, IT = TASKS / kStageThreads;
-  static_assert(IT * kStageThreads == TASKS, "whole tasks");
+  constexpr int SEG = v_seg_bytes(MEMRA_KV_NVFP4, D), TASKS = KEYS / kPage * 2 * (D / 16) * 8, IT = TASKS / (32 * WARPS);
+  static_assert(IT * (32 * WARPS) == TASKS, "whole tasks");
 #pragma unroll
   for (int it = 0; it < IT; ++it) {      // task (page, half page, 16-dim block b16, rr): dims 16 b16 + rr and + 8
-    const int task = st + it * kStageThreads, rr = task & 7, b16 = (task >> 3) % (D / 16),
+    const int task = st + it * (32 * WARPS), rr = task & 7, b16 = (task >> 3) % (D / 16),
               ph = (task / (8 * (D / 16))) & 1, pg = task / (16 * (D / 16)), g = 2 * pg + ph;
     const uint32_t seg = raw + pg * SEG;
     uint32_t h0[4], h1[4];
@@ -309,30 +360,31 @@ __device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint32_t pma
   sts64(buf + n * 128 + ((n & 7) << 4), live ? m[0] | (m[1] << 16) : 0u, live ? m[2] | (m[3] << 16) : 0u);
 }
 
-template <int D, int KF, int VF, int MT>
-__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams p) {
-  using C = TreeCfg<D, KF, VF, MT>;
-  constexpr int KT = kTreeKeys, NP = C::kPages, NBUF = C::kBufs, RAW = C::kRaw;
+template <int D, int KF, int VF>
+__global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, VF>::kCtas)
+    tree_kernel(const TreeParams p) {
+  using C = TreeCfg<D, KF, VF>;
+  constexpr int KT = kTreeKeys, NP = C::kPages, NBUF = C::kBufs, RAW = C::kRaw, SW = C::kStageWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bars = sb + C::kOffBar;
   auto raw_full = [&](int s) { return bars + 8 * s; };
   auto raw_empty = [&](int s) { return bars + 8 * (RAW + s); };
-  enum { kKFull = 0, kKEmpty, kVFull, kVEmpty, kSFull, kPFull, kPvDone };
+  enum { kKFull = 0, kKEmpty, kVFull, kVEmpty, kSFull, kPFull };
   auto bar = [&](int kind, int b) { return bars + 8 * (2 * RAW + 2 * kind + b); };
-  const uint32_t drained = bars + 8 * (2 * RAW + 14), q_ready = drained + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * (2 * RAW + 16));
+  const uint32_t pv_done = bars + 8 * (2 * RAW + 12), drained = pv_done + 8, q_ready = drained + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * (2 * RAW + 15));
   int *pid_s = reinterpret_cast<int *>(smem + C::kOffPid);
 
   grid_dependency_wait();
   allow_dependent_launch();
-  const int kvh = blockIdx.y, b = blockIdx.z / p.row_ctas, rc = blockIdx.z % p.row_ctas;
-  const int rows = p.n_nodes * p.group, r0 = rc * MT * kTileRows;
+  const int kvh = blockIdx.y, b = blockIdx.z / p.row_ctas, r0 = blockIdx.z % p.row_ctas * kTileRows;
+  const int rows = p.n_nodes * p.group;
   const int T0 = p.seq_lens[b];
   const int T = max(0, min(min(T0, p.max_seq_len),
                            static_cast<int>(min(static_cast<long long>(p.max_pages) * kPage, 2147483647ll))));
-  if (blockIdx.x == 0 && kvh == 0 && rc == 0 && tid == 0 && (T != T0 || T0 < p.n_nodes))
+  if (blockIdx.x == 0 && kvh == 0 && r0 == 0 && tid == 0 && (T != T0 || T0 < p.n_nodes))
     flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
   const int split_len = tree_split_tokens(T, p.target);
   const int ns = tree_ceil(T, split_len);
@@ -342,183 +394,187 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   };
   if (static_cast<int>(blockIdx.x) >= ns) {
     if (T <= 0 && blockIdx.x == 0)           // no key at all: zeros
-      for (int i = tid; i < min(MT * kTileRows, rows - r0) * (D / 8); i += kTreeThreads)
+      for (int i = tid; i < min(kTileRows, rows - r0) * (D / 8); i += C::kThreads)
         *reinterpret_cast<uint4 *>(p.out + row_id(r0 + i / (D / 8)) * D + 8 * (i % (D / 8))) = make_uint4(0, 0, 0, 0);
     return;
   }
   const int first = blockIdx.x * split_len, count = min(T - first, split_len);
   const int n_chunks = (count + KT - 1) / KT, n_pages = (count + kPage - 1) / kPage;
-  for (int i = tid; i < n_chunks * NP; i += kTreeThreads) {
+  int bad = 0;
+  for (int i = tid; i < n_chunks * NP; i += C::kThreads) {
     int pid = -1;
     if (i < n_pages) {
       pid = p.page_table[static_cast<size_t>(b) * p.max_pages + first / kPage + i];
       if (pid < 0 || pid >= p.num_pages) {
         flag_error(p.status, MEMRA_DEVERR_BAD_PAGE);
         pid = -1;
+        bad = 1;
       }
     }
     pid_s[i] = pid;
   }
-  if (warp == kMmaWarp) {
-    tc::tmem_alloc(smem_addr(tmem_slot), 512);
+  if (warp == C::kMmaWarp) {
+    tc::tmem_alloc(smem_addr(tmem_slot), C::kTCols);
     tc::tmem_relinquish();
   }
-  if (tid == 32 * kCopyWarp) {
+  if (tid == 32 * C::kCopyWarp) {
     for (int s = 0; s < RAW; ++s) {
       mbar_init(raw_full(s), 1);
-      mbar_init(raw_empty(s), kStageWarps);
+      mbar_init(raw_empty(s), SW);
     }
     for (int k = 0; k < 2; ++k) {
-      mbar_init(bar(kKFull, k), kStageWarps);
+      mbar_init(bar(kKFull, k), SW);
       mbar_init(bar(kKEmpty, k), 1);
-      mbar_init(bar(kVFull, k), kStageWarps);
+      mbar_init(bar(kVFull, k), SW);
       mbar_init(bar(kVEmpty, k), 1);
       mbar_init(bar(kSFull, k), 1);
       mbar_init(bar(kPFull, k), 128);
-      mbar_init(bar(kPvDone, k), 1);
     }
+    mbar_init(pv_done, 1);
     mbar_init(drained, 1);
     mbar_init(q_ready, 128);
     fence_barrier_init();
   }
   tc::fence_before_sync();
-  __syncthreads();
+  bad = __syncthreads_or(bad);
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  // The chunk's pages, one bit each, without those left out (rows past the end are masked by position).
   auto chunk_mask = [&](int ci) {
-    uint32_t m = 0;
+    uint32_t m = (1u << NP) - 1u;
+    if (bad) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) m |= (pid_s[ci * NP + i] >= 0 ? 1u : 0u) << i;
+      for (int i = 0; i < NP; ++i)
+        if (ci * NP + i < n_pages && pid_s[ci * NP + i] < 0) m &= ~(1u << i);
+    }
     return m;
   };
   bool ok = true;
 
-  if (warp == kCopyWarp) {
+  if (warp == C::kCopyWarp) {
     // ----------------------------------------------------------------- copies --
-    if (lane == 0) {
-      const size_t kstride = static_cast<size_t>(p.n_kv_heads) * C::kKSeg;
-      const size_t vstride = static_cast<size_t>(p.n_kv_heads) * C::kVSeg;
-      int issued = 0;
-      for (int ci = 0; ci < n_chunks; ++ci) {
-        const int s = ci % RAW;
-        if (ci >= RAW) ok = mbar_wait_bounded(raw_empty(s), (ci / RAW - 1) & 1, p.status);
-        if (!ok) break;
-        const uint32_t m = chunk_mask(ci), buf = sb + C::kOffRaw + s * C::kRawBytes;
-        if (m) {
-          mbar_arrive_expect_tx(raw_full(s), __popc(m) * (C::kKSeg + C::kVSeg));
-          for (int i = 0; i < NP; ++i) {
-            const int pg = pid_s[ci * NP + i];
-            if (pg < 0) continue;
-            bulk_copy_g2s_nohint(buf + i * C::kKSeg, p.k_pool + pg * kstride + static_cast<size_t>(kvh) * C::kKSeg,
-                                 C::kKSeg, raw_full(s));
-            bulk_copy_g2s_nohint(buf + NP * C::kKSeg + i * C::kVSeg,
-                                 p.v_pool + pg * vstride + static_cast<size_t>(kvh) * C::kVSeg, C::kVSeg, raw_full(s));
-          }
-        } else {
+    // Lane = (page of the chunk, K or V): one copy each, issued together (from
+    // one thread the eight copies of a chunk took 1,600 clocks to issue).
+    const int pg = lane >> 1;
+    const bool is_v = lane & 1, copies = pg < NP;
+    const uint32_t bytes = is_v ? C::kVSeg : C::kKSeg;
+    const uint32_t to = sb + C::kOffRaw + (is_v ? NP * C::kKSeg : 0) + pg * bytes;
+    const uint8_t *from = (is_v ? p.v_pool : p.k_pool) + static_cast<size_t>(kvh) * bytes;
+    const size_t stride = static_cast<size_t>(p.n_kv_heads) * bytes;
+    int issued = 0;
+    for (int ci = 0; ci < n_chunks; ++ci) {
+      const int s = ci % RAW;
+      if (ci >= RAW) ok = mbar_wait_suspended(raw_empty(s), (ci / RAW - 1) & 1, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int pid = copies ? pid_s[ci * NP + pg] : -1;
+      const int n = __popc(__ballot_sync(0xffffffffu, pid >= 0)) / 2;
+      if (lane == 0) {
+        if (n)
+          mbar_arrive_expect_tx(raw_full(s), n * (C::kKSeg + C::kVSeg));
+        else
           mbar_arrive(raw_full(s));
-        }
-        issued = ci + 1;
       }
-      // every copy has landed before the CTA can leave
-      for (int ci = max(0, issued - RAW); ci < issued; ++ci)
-        mbar_wait_bounded(raw_full(ci % RAW), (ci / RAW) & 1, p.status);
+      __syncwarp();
+      if (pid >= 0) bulk_copy_g2s_nohint(to + s * C::kRawBytes, from + pid * stride, bytes, raw_full(s));
+      issued = ci + 1;
     }
+    // every copy has landed before the CTA can leave
+    for (int ci = max(0, issued - RAW); ci < issued; ++ci)
+      mbar_wait_suspended(raw_full(ci % RAW), (ci / RAW) & 1, p.status);
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == C::kMmaWarp) {
     // -------------------------------------------------------------------- MMA --
     if (tc::elect_one()) {
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
       constexpr uint32_t idesc_o = C::kVRows ? tc::idesc_f16_f32_bmn(kTileRows, D) : tc::idesc_f16_f32(kTileRows, D);
       constexpr uint32_t idesc_oc = C::kMCols ? tc::idesc_f16_f32_bmn(kTileRows, C::kOCols) : idesc_o;
       auto v_desc = [](uint32_t v, int ks) {
-        return C::kVRows ? tc::smem_desc_sw128(v + 2048 * ks, KT * 128, 1024) : tc::smem_desc(v + 256 * ks, 128, (KT / 8) * 128);
+        return C::kVRows ? tc::smem_desc_sw128(v + 2048 * ks, KT * 128, 1024)
+                         : tc::smem_desc(v + 256 * ks, 128, (KT / 8) * 128);
       };
       auto wait = [&](int kind, int k, int phase) {
-        ok = ok && mbar_wait_bounded(bar(kind, k), phase & 1, p.status);
+        ok = ok && mbar_wait_suspended(bar(kind, k), phase & 1, p.status);
       };
-      // S_i(ci) = Q_i K^T into score buffer sbuf of tile i
-      auto mma_s = [&](int i, int ci) {
-        const int kb = ci % C::kKBufs, sbuf = NBUF > 1 ? ci & 1 : 0;
+      // S(ci) = Q K^T
+      auto mma_s = [&](int ci) {
+        if (!ok || ci >= n_chunks) return;
+        const int kb = ci % C::kKBufs, sbuf = ci % NBUF;
         wait(kKFull, kb, ci / C::kKBufs);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t k = sb + C::kOffK + kb * C::kKBuf, d = tmem + C::kSCol + (i * NBUF + sbuf) * KT;
+        const uint32_t k = sb + C::kOffK + kb * C::kKBuf, d = tmem + C::kSCol + sbuf * KT;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t a = tmem + C::kQCol + i * (D / 2) + 8 * ks;
           const uint32_t at = k + (ks / 4) * KT * 128 + (ks % 4) * 32;
-          tc::mma_f16_ta(d, a, tc::smem_desc_sw128(at, 16, 1024), idesc_s, ks > 0);
-          if constexpr (C::kKLo) tc::mma_f16_ta(d, a, tc::smem_desc_sw128(at + C::kTile, 16, 1024), idesc_s, 1);
+#pragma unroll
+          for (int lo = 0; lo < (C::kKLo ? 2 : 1); ++lo) {
+            const uint64_t bd = tc::smem_desc_sw128(at + lo * C::kTile, 16, 1024);
+            if (16 * ks < C::kQTmem)
+              tc::mma_f16_ta(d, tmem + C::kQCol + 8 * ks, bd, idesc_s, ks + lo > 0);
+            else
+              tc::mma_f16(d, tc::smem_desc(sb + C::kOffQ + 256 * (ks - C::kQTmem / 16), 128, C::kQSmem / 8 * 128), bd,
+                          idesc_s, 1);
+          }
         }
-        if (i == MT - 1) tc::commit(bar(kKEmpty, kb));
-        tc::commit(bar(kSFull, MT == 1 ? sbuf : i));
+        tc::commit(bar(kKEmpty, kb));
+        tc::commit(bar(kSFull, sbuf));
       };
-      // O_i += P_i(ci) V
-      auto mma_o = [&](int i, int ci) {
-        const int vb = ci % C::kVBufs, sbuf = NBUF > 1 ? ci & 1 : 0;
-        wait(kPFull, MT == 1 ? sbuf : i, MT == 1 ? ci >> 1 : ci);
+      // O += P(ci) V, P in the columns of its scores
+      auto mma_o = [&](int ci) {
+        const int vb = ci % C::kVBufs, sbuf = ci % NBUF;
+        wait(kPFull, sbuf, ci / NBUF);
         wait(kVFull, vb, ci / C::kVBufs);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t v = sb + C::kOffV + vb * C::kVBuf, a0 = tmem + C::kSCol + (i * NBUF + sbuf) * KT;
-        const uint32_t d = tmem + C::kOCol + i * C::kOCols;
+        const uint32_t v = sb + C::kOffV + vb * C::kVBuf, a = tmem + C::kSCol + sbuf * KT, d = tmem + C::kOCol;
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks) {
-          tc::mma_f16_ta(d, a0 + 8 * ks, v_desc(v, ks), idesc_oc, ci > 0 || ks > 0);
-          if constexpr (C::kVLo) tc::mma_f16_ta(d, a0 + 8 * ks, v_desc(v + C::kLoOff, ks), idesc_o, 1);
+          tc::mma_f16_ta(d, a + 8 * ks, v_desc(v, ks), idesc_oc, ci > 0 || ks > 0);
+          if constexpr (C::kVLo) tc::mma_f16_ta(d, a + 8 * ks, v_desc(v + C::kLoOff, ks), idesc_o, 1);
         }
-        if (i == MT - 1) tc::commit(bar(kVEmpty, vb));
-        if (NBUF > 1 || ci == n_chunks - 1) tc::commit(bar(kPvDone, i));
+        tc::commit(bar(kVEmpty, vb));
+        if (NBUF > 1 || ci == n_chunks - 1) tc::commit(pv_done);
       };
-      ok = mbar_wait_bounded(q_ready, 0, p.status);
-      if constexpr (MT == 1) {
-        if (ok) mma_s(0, 0);
-        if (ok && n_chunks > 1) mma_s(0, 1);
-        for (int ci = 0; ci < n_chunks && ok; ++ci) {
-          mma_o(0, ci);
-          if (ok && ci + 2 < n_chunks) mma_s(0, ci + 2);   // behind the product that reads its buffer's P
-        }
-      } else {
-        for (int i = 0; i < MT && ok; ++i) mma_s(i, 0);
-        for (int ci = 0; ci < n_chunks && ok; ++ci)
-          for (int i = 0; i < MT && ok; ++i) {
-            mma_o(i, ci);
-            if (ok && ci + 1 < n_chunks) mma_s(i, ci + 1);
-          }
+      ok = mbar_wait_suspended(q_ready, 0, p.status);
+      for (int ci = 0; ci < NBUF; ++ci) mma_s(ci);
+      for (int ci = 0; ci < n_chunks && ok; ++ci) {
+        mma_o(ci);
+        mma_s(ci + NBUF);                    // behind the product that reads its buffer's P
       }
       tc::commit(drained);                   // what was issued completes before the CTA can leave
-      mbar_wait_bounded(drained, 0, p.status);
+      mbar_wait_suspended(drained, 0, p.status);
     }
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- staging --
     const int sw = warp - 4;
-    if constexpr (C::kMCols) {               // the unused columns of the minima's blocks, once
-      for (uint32_t i = tid - 128; i < C::kVBufs * KT * 8u; i += kStageThreads)
+    if constexpr (C::kMCols) {               // the unused columns of the minima's block, once
+      for (uint32_t i = tid - 128; i < C::kVBufs * KT * 8u; i += 32 * SW)
         sts128(sb + C::kOffV + (i / (KT * 8)) * C::kVBuf + C::kTile + 16 * (i % (KT * 8)), make_uint4(0, 0, 0, 0));
-      named_barrier_sync(1, kStageThreads);
+      named_barrier_sync(1, 32 * SW);
     }
     for (int ci = 0; ci < n_chunks; ++ci) {
       const int s = ci % RAW, kb = ci % C::kKBufs, vb = ci % C::kVBufs, valid = count - ci * KT;
-      const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, rawv = rawk + NP * C::kKSeg, pmask = chunk_mask(ci);
-      ok = mbar_wait_bounded(raw_full(s), (ci / RAW) & 1, p.status);
-      if (ok && ci >= C::kKBufs) ok = mbar_wait_bounded(bar(kKEmpty, kb), (ci / C::kKBufs - 1) & 1, p.status);
+      const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, rawv = rawk + NP * C::kKSeg;
+      ok = mbar_wait_suspended(raw_full(s), (ci / RAW) & 1, p.status);
+      if (ok && ci >= C::kKBufs) ok = mbar_wait_suspended(bar(kKEmpty, kb), (ci / C::kKBufs - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      stage_k<D, KF, KT>(rawk, sb + C::kOffK + kb * C::kKBuf, sw, lane);
+      stage_k<D, KF, KT, SW>(rawk, sb + C::kOffK + kb * C::kKBuf, sw, lane);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kKFull, kb));
-      if (ci >= C::kVBufs) ok = mbar_wait_bounded(bar(kVEmpty, vb), (ci / C::kVBufs - 1) & 1, p.status);
+      if (ci >= C::kVBufs) ok = mbar_wait_suspended(bar(kVEmpty, vb), (ci / C::kVBufs - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t vbuf = sb + C::kOffV + vb * C::kVBuf;
+      const uint32_t vbuf = sb + C::kOffV + vb * C::kVBuf, pmask = chunk_mask(ci);
       if constexpr (C::kVRows)
-        stage_v<D, VF, KT, C::kMCols, C::kLoOff>(rawv, vbuf, pmask, valid, sw, lane);
+        stage_v<D, VF, KT, SW, C::kMCols, C::kLoOff>(rawv, vbuf, pmask, valid, sw, lane);
       else
-        stage_v_nvfp4<D, KT>(rawv, vbuf, pmask, valid, tid - 128);
+        stage_v_nvfp4<D, KT, SW>(rawv, vbuf, pmask, valid, tid - 128);
       if constexpr (C::kMCols) {             // 32 tokens by each of two warps, other ones each time
-        const int part = (sw - 2 * ci) & (kStageWarps - 1);
+        const int part = (sw - 2 * ci) & (SW - 1);
         if (part < KT / 32) stage_m<D, KT>(rawv, vbuf + C::kTile, pmask, valid, 32 * part + lane);
       }
       fence_proxy_async();                   // V^ for the tensor cores, the raw chunk for the next copies
@@ -531,182 +587,157 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   } else {
     // ---------------------------------------------------------------- softmax --
     const uint32_t tlane = static_cast<uint32_t>(warp * 32) << 16;
-    uint64_t word[MT];
-    float m[MT], l[MT];
+    const int r = r0 + tid;
+    const bool live = r < rows;
+    uint64_t word = 0;
+    if (live && T - p.n_nodes + r / p.group >= 0) word = p.mask[static_cast<size_t>(b) * p.n_nodes + r / p.group];
+    {
+      // the row of Q (negated for a negative scale, zeros for scale 0: the softmax takes the largest
+      // score for the largest weight): fp16 pairs into tensor memory, the last dims into core matrices
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (live ? row_id(r) : 0) * D);
+      auto load = [&](int u) {
+        const uint4 y = live ? src[u] : make_uint4(0, 0, 0, 0);
+        return make_uint4((y.x & p.q_and) ^ p.q_xor, (y.y & p.q_and) ^ p.q_xor, (y.z & p.q_and) ^ p.q_xor,
+                          (y.w & p.q_and) ^ p.q_xor);
+      };
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int r = r0 + i * kTileRows + tid;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      word[i] = 0;
-      if (r < rows && T - p.n_nodes + r / p.group >= 0) word[i] = p.mask[static_cast<size_t>(b) * p.n_nodes + r / p.group];
-      // the row of Q, fp16 pairs as they lie, into tensor memory
-      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (r < rows ? row_id(r) : 0) * D);
+      for (int c = 0; c < C::kQTmem / 2; c += 16) {
+        uint32_t x[16];
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t x[32];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 y = r < rows ? src[c / 4 + e] : make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < 4; ++e) {
+          const uint4 y = load(c / 4 + e);
           x[4 * e] = y.x, x[4 * e + 1] = y.y, x[4 * e + 2] = y.z, x[4 * e + 3] = y.w;
         }
-        tc::st_32x32b_x32(tmem + tlane + C::kQCol + i * (D / 2) + c, x);
+        tc::st_32x32b_x16(tmem + tlane + C::kQCol + c, x);
       }
+#pragma unroll
+      for (int u = 0; u < C::kQSmem / 8; ++u)
+        sts128(sb + C::kOffQ + ((tid >> 3) * (C::kQSmem / 8) + u) * 128 + (tid & 7) * 16, load(C::kQTmem / 8 + u));
     }
     tc::wait_st();
+    fence_proxy_async();
     tc::fence_before_sync();
     mbar_arrive(q_ready);
     const int base = T - p.n_nodes;          // position of the tree's first row
+    const uint32_t o_col = tmem + tlane + C::kOCol;
+    float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-    for (int ci = 0; ci < n_chunks && ok; ++ci) {
+    for (int ci = 0; ci < n_chunks; ++ci) {
       const uint32_t pmask = chunk_mask(ci);
-      const int tok0 = first + ci * KT, sbuf = NBUF > 1 ? ci & 1 : 0;
+      const int tok0 = first + ci * KT, sbuf = ci % NBUF;
+      const uint32_t s_col = tmem + tlane + C::kSCol + sbuf * KT;
+      ok = mbar_wait_suspended(bar(kSFull, sbuf), (ci / NBUF) & 1, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::fence_after_sync();
+      uint32_t s[KT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int sk = MT == 1 ? sbuf : i;
-        const uint32_t s_col = tmem + tlane + C::kSCol + (i * NBUF + sbuf) * KT;
-        ok = mbar_wait_bounded(bar(kSFull, sk), (MT == 1 ? ci >> 1 : ci) & 1, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc::fence_after_sync();
-        uint32_t s[KT];
+      for (int c = 0; c < KT; c += 32) tc::ld_32x32b_x32(s_col + c, s + c);
+      tc::wait_ld_all();
+      tc::hold<KT>(s);
+      if (pmask != (1u << NP) - 1u || tok0 + KT > base) {
 #pragma unroll
-        for (int c = 0; c < KT; c += 32) tc::ld_32x32b_x32(s_col + c, s + c);
-        tc::wait_ld_all();
-        tc::hold<KT>(s);
-#pragma unroll
-        for (int c = 0; c < KT; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) * p.scale_log2);
-        if (pmask != (1u << NP) - 1u || tok0 + KT > base) {
-#pragma unroll
-          for (int c = 0; c < KT; ++c) {
-            const int j = tok0 + c - base;   // the tree's row, if >= 0
-            const bool sees = ((pmask >> (c / kPage)) & 1u) && (j < 0 || (j < p.n_nodes && ((word[i] >> j) & 1u)));
-            if (!sees) s[c] = 0xff800000u;   // -inf
-          }
+        for (int c = 0; c < KT; ++c) {
+          const int j = tok0 + c - base;     // the tree's row, if >= 0
+          const bool sees = ((pmask >> (c / kPage)) & 1u) && (j < 0 || (j < p.n_nodes && ((word >> j) & 1u)));
+          if (!sees) s[c] = 0xff800000u;     // -inf
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < KT; c += 4)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[c + e]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        float alpha = 1.f;
-        if (top > m[i] + kLazy) {            // also the first chunk with a key (m = -inf)
-          if (m[i] != -INFINITY) alpha = fast_exp2(m[i] - top);
-          m[i] = top;
-        }
-        if (ci > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O's rows of this warp times alpha, once the product before has
-          // completed (one score buffer: these scores were issued behind it)
-          if (NBUF > 1) {
-            ok = mbar_wait_bounded(bar(kPvDone, i), (ci - 1) & 1, p.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc::fence_after_sync();
-          }
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tc::ld_32x32b_x32(tmem + tlane + C::kOCol + i * C::kOCols + c, o);
-            tc::wait_ld_all();
-            tc::hold<32>(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::st_32x32b_x32(tmem + tlane + C::kOCol + i * C::kOCols + c, o);
-          }
-          if constexpr (C::kMCols) {
-            uint32_t o[16];
-            tc::ld_32x32b_x16(tmem + tlane + C::kOCol + D, o);
-            tc::wait_ld(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::st_32x32b_x16(tmem + tlane + C::kOCol + D, o);
-          }
-          l[i] *= alpha;
-        }
-        const float mu = m[i] == -INFINITY ? 0.f : m[i];
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < KT; c += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p0 = fast_exp2(__uint_as_float(s[c + 2 * e]) - mu);
-            const float p1 = fast_exp2(__uint_as_float(s[c + 2 * e + 1]) - mu);
-            l0 += p0;
-            l1 += p1;
-            w[e] = pack_half2(p0, p1);
-          }
-          tc::st_32x32b_x16(s_col + c / 2, w);
-        }
-        l[i] += l0 + l1;
-        tc::wait_st();
-        tc::fence_before_sync();
-        mbar_arrive(bar(kPFull, sk));
       }
-    }
-    // The last product of each tile.  Two score buffers: the product before it may still be
-    // running, so its phase comes first (a parity names only the next phase).
+      const float top = row_max(s) * p.scale_log2;
+      float alpha = 1.f;
+      if (top > m + kLazy) {                 // also the first chunk with a key (m = -inf)
+        if (m != -INFINITY) alpha = fast_exp2(m - top);
+        m = top;
+      }
+      if (ci > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O's rows of this warp times alpha, once the product before has
+        // completed (one score buffer: these scores were issued behind it)
+        if (NBUF > 1) {
+          ok = mbar_wait_suspended(pv_done, (ci - 1) & 1, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+        }
+#pragma unroll 1
+        for (int c = 0; c < C::kOCols; c += 16) {
+          uint32_t o[16];
+          tc::ld_32x32b_x16(o_col + c, o);
+          tc::wait_ld(o);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (NBUF > 1 && n_chunks > 1 && ok) ok = mbar_wait_bounded(bar(kPvDone, i), (n_chunks - 2) & 1, p.status);
-      if (ok) ok = mbar_wait_bounded(bar(kPvDone, i), NBUF > 1 ? (n_chunks - 1) & 1 : 0, p.status);
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tc::st_32x32b_x16(o_col + c, o);
+        }
+        l *= alpha;
+      }
+      const float mu = m == -INFINITY ? 0.f : m;
+      uint64_t sum = 0;
+#pragma unroll
+      for (int c = 0; c < KT; c += 32) {
+        uint32_t w[16];
+        row_weights<16>(s + c, p.scale_log2, mu, w, sum);
+        tc::st_32x32b_x16(s_col + c / 2, w);
+      }
+      float l0, l1;
+      unpack_f2(sum, l0, l1);
+      l += l0 + l1;
+      tc::wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(bar(kPFull, sbuf));
     }
-    // (every tile's last product is done: the operand tiles and raw pages are free for the output rows)
+    // The last product.  Two score buffers: the product before it may still be
+    // running, so its phase comes first (a parity names only the next phase).
+    if (NBUF > 1 && n_chunks > 1 && ok) ok = mbar_wait_suspended(pv_done, (n_chunks - 2) & 1, p.status);
+    if (ok) ok = mbar_wait_suspended(pv_done, NBUF > 1 ? (n_chunks - 1) & 1 : 0, p.status);
+    // (every MMA is done: the operand tiles and raw pages are free for the output rows)
     ok = __all_sync(0xffffffffu, ok);
     tc::fence_after_sync();
+    const float inv = l > 0.f ? p.v_post / l : 0.f;
+    uint32_t ms[16];                         // the minima's sums, per 32-dim block; a half as the staged values are
+    if constexpr (C::kMCols) {
+      tc::ld_32x32b_x16(o_col + D, ms);
+      tc::wait_ld(ms);
+    }
+    const uint32_t row = sb + C::kOffK + tid * C::kRowBytes;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int r = r0 + i * kTileRows + tid;
-      const float inv = l[i] > 0.f ? p.v_post / l[i] : 0.f;
-      uint32_t ms[16];                       // the minima's sums, per 32-dim block; a half as the staged values are
-      if constexpr (C::kMCols) {
-        tc::ld_32x32b_x16(tmem + tlane + C::kOCol + D, ms);
-        tc::wait_ld(ms);
+    for (int c = 0; c < D; c += 16) {
+      if (!ok) break;
+      uint32_t o[16];
+      tc::ld_32x32b_x16(o_col + c, o);
+      tc::wait_ld(o);
+      const float half_m = C::kMCols ? 0.5f * __uint_as_float(ms[c / 32]) : 0.f;
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = l > 0.f ? (__uint_as_float(o[e]) + half_m) * inv : 0.f;
+      if (ns == 1) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+          sts128(row + (c + e) * 2, make_uint4(pack_half2(x[e], x[e + 1]), pack_half2(x[e + 2], x[e + 3]),
+                                               pack_half2(x[e + 4], x[e + 5]), pack_half2(x[e + 6], x[e + 7])));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          sts128(row + (c + e) * 4, make_uint4(__float_as_uint(x[e]), __float_as_uint(x[e + 1]),
+                                               __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])));
       }
-      const uint32_t row = sb + C::kOffK + (i * kTileRows + tid) * C::kRowBytes;
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        if (!ok) break;
-        uint32_t o[32];
-        tc::ld_32x32b_x32(tmem + tlane + C::kOCol + i * C::kOCols + c, o);
-        tc::wait_ld_all();
-        tc::hold<32>(o);
-        const float half_m = C::kMCols ? 0.5f * __uint_as_float(ms[c / 32]) : 0.f;
-        float x[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = l[i] > 0.f ? (__uint_as_float(o[e]) + half_m) * inv : 0.f;
-        if (ns == 1) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            sts128(row + (c + e) * 2, make_uint4(pack_half2(x[e], x[e + 1]), pack_half2(x[e + 2], x[e + 3]),
-                                                 pack_half2(x[e + 4], x[e + 5]), pack_half2(x[e + 6], x[e + 7])));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            sts128(row + (c + e) * 4, make_uint4(__float_as_uint(x[e]), __float_as_uint(x[e + 1]),
-                                                 __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])));
-        }
+    }
+    // the row by one bulk copy; a partial's lse by a plain store (-inf, never weighed, without a
+    // visible key or after a wait that gave up)
+    if (live) {
+      const size_t id = row_id(r), slot = id * p.max_splits + blockIdx.x;
+      if (ok) {
+        fence_proxy_async();
+        if (ns == 1)
+          bulk_store_s2g(p.out + id * D, row, D * 2);
+        else
+          bulk_store_s2g(p.o_part + slot * D, row, D * 4);
       }
-      // the row by one bulk copy; a partial's lse by a plain store (-inf, never weighed, without a
-      // visible key or after a wait that gave up)
-      if (r < rows) {
-        const size_t id = row_id(r), slot = id * p.max_splits + blockIdx.x;
-        if (ok) {
-          fence_proxy_async();
-          if (ns == 1)
-            bulk_store_s2g(p.out + id * D, row, D * 2);
-          else
-            bulk_store_s2g(p.o_part + slot * D, row, D * 4);
-        }
-        if (ns > 1) p.lse_part[slot] = ok && l[i] > 0.f ? m[i] + __log2f(l[i]) : -INFINITY;
-      }
+      if (ns > 1) p.lse_part[slot] = ok && l > 0.f ? m + __log2f(l) : -INFINITY;
     }
     bulk_store_wait();
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+  if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, C::kTCols);
 }
 
 // Merge of a row's partials: warp = row, each lane D / 32 consecutive outputs.
@@ -773,10 +804,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
     *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-template <int D, int KF, int VF, int MT>
+template <int D, int KF, int VF>
 cudaError_t launch_one(const TreeParams &p, cudaStream_t st) {
-  using C = TreeCfg<D, KF, VF, MT>;
-  auto kernel = tree_kernel<D, KF, VF, MT>;
+  using C = TreeCfg<D, KF, VF>;
+  auto kernel = tree_kernel<D, KF, VF>;
   static bool ready[64] = {};                // the shared-memory limit, set once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -785,19 +816,14 @@ cudaError_t launch_one(const TreeParams &p, cudaStream_t st) {
   if (!ready[dev]) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
   const int most = std::max(1, tree_most_splits(p.max_seq_len, p.target));
   const dim3 grid(static_cast<unsigned>(most), static_cast<unsigned>(p.n_kv_heads),
                   static_cast<unsigned>(p.batch * p.row_ctas));
-  return launch_pdl(kernel, grid, dim3(kTreeThreads), C::kSmem, st, p);
-}
-
-template <int D, int KF, int VF>
-cudaError_t launch_tiles(const TreeParams &p, cudaStream_t st) {
-  if constexpr (D == 128)
-    if (tree_tiles(D, p.n_nodes * p.group) == 2) return launch_one<D, KF, VF, 2>(p, st);
-  return launch_one<D, KF, VF, 1>(p, st);
+  return launch_pdl(kernel, grid, dim3(C::kThreads), C::kSmem, st, p);
 }
 
 template <int D>
@@ -805,10 +831,10 @@ cudaError_t launch_formats(int kf, int vf, const TreeParams &p, cudaStream_t st)
   auto by_v = [&](auto kc) -> cudaError_t {
     constexpr int K = decltype(kc)::value;
     switch (vf) {
-      case MEMRA_KV_Q5_1: return launch_tiles<D, K, MEMRA_KV_Q5_1>(p, st);
-      case MEMRA_KV_Q4_0: return launch_tiles<D, K, MEMRA_KV_Q4_0>(p, st);
-      case MEMRA_KV_FP8_E4M3: return launch_tiles<D, K, MEMRA_KV_FP8_E4M3>(p, st);
-      case MEMRA_KV_NVFP4: return launch_tiles<D, K, MEMRA_KV_NVFP4>(p, st);
+      case MEMRA_KV_Q5_1: return launch_one<D, K, MEMRA_KV_Q5_1>(p, st);
+      case MEMRA_KV_Q4_0: return launch_one<D, K, MEMRA_KV_Q4_0>(p, st);
+      case MEMRA_KV_FP8_E4M3: return launch_one<D, K, MEMRA_KV_FP8_E4M3>(p, st);
+      case MEMRA_KV_NVFP4: return launch_one<D, K, MEMRA_KV_NVFP4>(p, st);
       default: return cudaErrorInvalidValue;
     }
   };

@@ -13,15 +13,14 @@ namespace memra {
 // Keys of one step of the split pass (the N of the score MMA).
 constexpr int kTreeKeys = 64;
 
-// Row tiles (128 rows: nodes x the group's heads) that one CTA holds: two at
-// head_dim 128 where the rows need them, so that a page is dequantized once for 256 rows.
-__host__ __device__ constexpr int tree_tiles(int D, int rows) { return D == 128 && rows > 128 ? 2 : 1; }
+// CTAs of the split pass that share an SM.
+__host__ __device__ constexpr int tree_ctas_per_sm(int D) { return D == 128 ? 2 : 1; }
 
 // Smallest split: it keeps a CTA's fixed costs (the query tile, the first
 // pages' latency, the output rows) to a fraction of its time.
 constexpr int kTreeSplitTokens = 512;
 // Largest split (its page ids lie in shared memory).
-constexpr int kTreeSplitMax = 16384;
+constexpr int kTreeSplitMax = 15360;
 constexpr int kTreeSplitPages = kTreeSplitMax / kPage;
 // Most splits that a sequence is cut into to fill the GPU.
 constexpr int kTreeMaxSplits = 160;
@@ -58,8 +57,9 @@ struct TreeParams {
   int batch, n_nodes, n_heads, group, n_kv_heads, num_pages, max_pages, max_seq_len;
   int target;                   // splits that fill the GPU
   int max_splits;               // partials per row in the workspace
-  int row_ctas;                 // CTAs over the rows of one KV head
-  float scale_log2;             // sm_scale * (post-scale of the staged K values) * log2(e)
+  int row_ctas;                 // 128-row tiles of one KV head
+  float scale_log2;             // |sm_scale| * (post-scale of the staged K values) * log2(e); 1 for sm_scale 0
+  uint32_t q_and, q_xor;        // applied to the query's fp16 pairs: the scale's sign, or zeros for sm_scale 0
   float v_post;                 // post-scale of the staged V values
 };
 

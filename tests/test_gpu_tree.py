@@ -177,7 +177,7 @@ def test_many_splits(memra, D, lens):
 
 
 def test_splits_at_their_largest(memra):
-    # 16 KV heads x 8 row CTAs leave the plan about one split: more than 16,384 keys make more than the target
+    # 16 KV heads x 8 row CTAs leave the plan about one split: more than 15,360 keys make more than the target
     w = W.make_workload("wide", batch=1, q_len=64, n_heads=16 * 32, n_kv_heads=16, head_dim=128, k_fmt="fp8",
                         v_fmt="fp8", seed=8, seq_lens=[8192 + 8192 + 70])
     words = words_for(w, 4)
