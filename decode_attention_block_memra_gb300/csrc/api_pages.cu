@@ -41,7 +41,7 @@ int memra_kv_compact(const memra_kv_cache *cache, const int32_t *page_table, int
   if (st) return st;
   if (batch < 0 || n_nodes < 1 || max_accepted < 0 || max_pages_per_seq < 1 || max_seq_len < 0)
     return MEMRA_ERR_INVALID_ARG;
-  if (n_nodes > MEMRA_MAX_TREE_NODES || batch > 65535) return MEMRA_ERR_UNSUPPORTED;
+  if (n_nodes > MEMRA_MAX_TREE_NODES || batch > 65535 || cache->n_kv_heads > 65535) return MEMRA_ERR_UNSUPPORTED;
   if (max_accepted > n_nodes) return MEMRA_ERR_INVALID_ARG;
   if (batch == 0 || max_accepted == 0) return MEMRA_OK;
   if (!page_table || !seq_lens || !accepted || !n_accepted || !aligned4(page_table) || !aligned4(seq_lens) ||
@@ -65,6 +65,7 @@ int memra_kv_compact(const memra_kv_cache *cache, const int32_t *page_table, int
   p.v_fmt = cache->v_fmt;
   p.k_seg = k_seg_bytes(cache->k_fmt, cache->head_dim);
   p.v_seg = v_seg_bytes(cache->v_fmt, cache->head_dim);
+  p.parts = 0;
   return cuda_status(launch_compact(cache->head_dim, p, batch, static_cast<cudaStream_t>(stream)));
 }
 

@@ -29,9 +29,10 @@ struct CompactParams {
   int32_t *status;
   int n_kv_heads, num_pages, max_pages, max_seq_len, n_nodes, max_accepted;
   int k_fmt, v_fmt, k_seg, v_seg;
+  int parts;                      // CTAs over the bytes of a row, set by the launcher
 };
 
 cudaError_t launch_copy_pages(CopyPagesParams p, cudaStream_t st);
-cudaError_t launch_compact(int D, const CompactParams &p, int batch, cudaStream_t st);
+cudaError_t launch_compact(int D, CompactParams p, int batch, cudaStream_t st);
 
 }  // namespace memra

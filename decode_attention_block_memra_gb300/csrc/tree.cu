@@ -400,40 +400,73 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
   }
   const int first = blockIdx.x * split_len, count = min(T - first, split_len);
   const int n_chunks = (count + KT - 1) / KT, n_pages = (count + kPage - 1) / kPage;
+  // Page id of a page of the split, -1 for one left out or past the end.
+  const int32_t *table = p.page_table + static_cast<size_t>(b) * p.max_pages + first / kPage;
+  auto page_id = [&](int i) {
+    if (i >= n_pages) return -1;
+    const int pid = table[i];
+    return pid >= 0 && pid < p.num_pages ? pid : -1;
+  };
+  // The copy warp sets the barriers up and sends for the first chunks while the others prepare.
+  // Lane = (page of a chunk, K or V): one copy each, issued together (from one
+  // thread the eight copies of a chunk took 1,600 clocks to issue).
+  const int cp_page = lane >> 1;
+  const bool cp_v = lane & 1;
+  const uint32_t cp_bytes = cp_v ? C::kVSeg : C::kKSeg;
+  auto copy_chunk = [&](int ci, int pid) {
+    const int s = ci % RAW, n = __popc(__ballot_sync(0xffffffffu, pid >= 0)) / 2;
+    if (lane == 0) {
+      if (n)
+        mbar_arrive_expect_tx(raw_full(s), n * (C::kKSeg + C::kVSeg));
+      else
+        mbar_arrive(raw_full(s));
+    }
+    __syncwarp();
+    if (pid >= 0)
+      bulk_copy_g2s_nohint(sb + C::kOffRaw + s * C::kRawBytes + (cp_v ? NP * C::kKSeg : 0) + cp_page * cp_bytes,
+                           (cp_v ? p.v_pool : p.k_pool) + (static_cast<size_t>(pid) * p.n_kv_heads + kvh) * cp_bytes,
+                           cp_bytes, raw_full(s));
+  };
   int bad = 0;
-  for (int i = tid; i < n_chunks * NP; i += C::kThreads) {
-    int pid = -1;
-    if (i < n_pages) {
-      pid = p.page_table[static_cast<size_t>(b) * p.max_pages + first / kPage + i];
-      if (pid < 0 || pid >= p.num_pages) {
+  if (warp == C::kCopyWarp) {
+    int pid[RAW];
+#pragma unroll
+    for (int ci = 0; ci < RAW; ++ci) pid[ci] = cp_page < NP ? page_id(ci * NP + cp_page) : -1;
+    if (lane == 0) {
+      for (int s = 0; s < RAW; ++s) {
+        mbar_init(raw_full(s), 1);
+        mbar_init(raw_empty(s), SW);
+      }
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(bar(kKFull, k), SW);
+        mbar_init(bar(kKEmpty, k), 1);
+        mbar_init(bar(kVFull, k), SW);
+        mbar_init(bar(kVEmpty, k), 1);
+        mbar_init(bar(kSFull, k), 1);
+        mbar_init(bar(kPFull, k), 128);
+      }
+      mbar_init(pv_done, 1);
+      mbar_init(drained, 1);
+      mbar_init(q_ready, 128);
+      fence_barrier_init();
+    }
+    __syncwarp();
+#pragma unroll
+    for (int ci = 0; ci < RAW; ++ci)
+      if (ci < n_chunks) copy_chunk(ci, pid[ci]);
+  } else {
+    for (int i = tid; i < n_chunks * NP; i += 32 * C::kCopyWarp) {
+      const int pid = page_id(i);
+      pid_s[i] = pid;
+      if (pid < 0 && i < n_pages) {
         flag_error(p.status, MEMRA_DEVERR_BAD_PAGE);
-        pid = -1;
         bad = 1;
       }
     }
-    pid_s[i] = pid;
-  }
-  if (warp == C::kMmaWarp) {
-    tc::tmem_alloc(smem_addr(tmem_slot), C::kTCols);
-    tc::tmem_relinquish();
-  }
-  if (tid == 32 * C::kCopyWarp) {
-    for (int s = 0; s < RAW; ++s) {
-      mbar_init(raw_full(s), 1);
-      mbar_init(raw_empty(s), SW);
+    if (warp == C::kMmaWarp) {
+      tc::tmem_alloc(smem_addr(tmem_slot), C::kTCols);
+      tc::tmem_relinquish();
     }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(bar(kKFull, k), SW);
-      mbar_init(bar(kKEmpty, k), 1);
-      mbar_init(bar(kVFull, k), SW);
-      mbar_init(bar(kVEmpty, k), 1);
-      mbar_init(bar(kSFull, k), 1);
-      mbar_init(bar(kPFull, k), 128);
-    }
-    mbar_init(pv_done, 1);
-    mbar_init(drained, 1);
-    mbar_init(q_ready, 128);
-    fence_barrier_init();
   }
   tc::fence_before_sync();
   bad = __syncthreads_or(bad);
@@ -453,30 +486,13 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
 
   if (warp == C::kCopyWarp) {
     // ----------------------------------------------------------------- copies --
-    // Lane = (page of the chunk, K or V): one copy each, issued together (from
-    // one thread the eight copies of a chunk took 1,600 clocks to issue).
-    const int pg = lane >> 1;
-    const bool is_v = lane & 1, copies = pg < NP;
-    const uint32_t bytes = is_v ? C::kVSeg : C::kKSeg;
-    const uint32_t to = sb + C::kOffRaw + (is_v ? NP * C::kKSeg : 0) + pg * bytes;
-    const uint8_t *from = (is_v ? p.v_pool : p.k_pool) + static_cast<size_t>(kvh) * bytes;
-    const size_t stride = static_cast<size_t>(p.n_kv_heads) * bytes;
-    int issued = 0;
-    for (int ci = 0; ci < n_chunks; ++ci) {
-      const int s = ci % RAW;
-      if (ci >= RAW) ok = mbar_wait_suspended(raw_empty(s), (ci / RAW - 1) & 1, p.status);
+    int issued = min(n_chunks, RAW);
+    for (int ci = RAW; ci < n_chunks; ++ci) {
+      const int pid = cp_page < NP ? pid_s[ci * NP + cp_page] : -1;
+      ok = mbar_wait_suspended(raw_empty(ci % RAW), (ci / RAW - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int pid = copies ? pid_s[ci * NP + pg] : -1;
-      const int n = __popc(__ballot_sync(0xffffffffu, pid >= 0)) / 2;
-      if (lane == 0) {
-        if (n)
-          mbar_arrive_expect_tx(raw_full(s), n * (C::kKSeg + C::kVSeg));
-        else
-          mbar_arrive(raw_full(s));
-      }
-      __syncwarp();
-      if (pid >= 0) bulk_copy_g2s_nohint(to + s * C::kRawBytes, from + pid * stride, bytes, raw_full(s));
+      copy_chunk(ci, pid);
       issued = ci + 1;
     }
     // every copy has landed before the CTA can leave
@@ -591,6 +607,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
     const bool live = r < rows;
     uint64_t word = 0;
     if (live && T - p.n_nodes + r / p.group >= 0) word = p.mask[static_cast<size_t>(b) * p.n_nodes + r / p.group];
+    if (p.n_nodes < 64) word &= (1ull << p.n_nodes) - 1ull;
     {
       // the row of Q (negated for a negative scale, zeros for scale 0: the softmax takes the largest
       // score for the largest weight): fp16 pairs into tensor memory, the last dims into core matrices
@@ -636,12 +653,17 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       tc::wait_ld_all();
       tc::hold<KT>(s);
       if (pmask != (1u << NP) - 1u || tok0 + KT > base) {
+        // bit c: the row sees key tok0 + c.  Keys before the tree, then the tree's by the word (whose
+        // bits past the tree are cleared, so rows past the end are hidden too).
+        const int off = tok0 - base;         // -63 .. 63 where the chunk holds rows of the tree
+        uint64_t sees = off <= -KT ? ~0ull : off < 0 ? word << -off | ((1ull << -off) - 1ull) : word >> off;
 #pragma unroll
-        for (int c = 0; c < KT; ++c) {
-          const int j = tok0 + c - base;     // the tree's row, if >= 0
-          const bool sees = ((pmask >> (c / kPage)) & 1u) && (j < 0 || (j < p.n_nodes && ((word >> j) & 1u)));
-          if (!sees) s[c] = 0xff800000u;     // -inf
-        }
+        for (int i = 0; i < NP; ++i)
+          if (!((pmask >> i) & 1u)) sees &= ~(0xFFFFull << (kPage * i));
+        const uint32_t half[2] = {static_cast<uint32_t>(sees), static_cast<uint32_t>(sees >> 32)};
+#pragma unroll
+        for (int c = 0; c < KT; ++c)
+          if (!(half[c / 32] & (1u << (c % 32)))) s[c] = 0xff800000u;      // -inf
       }
       const float top = row_max(s) * p.scale_log2;
       float alpha = 1.f;
@@ -720,20 +742,39 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
                                                __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])));
       }
     }
-    // the row by one bulk copy; a partial's lse by a plain store (-inf, never weighed, without a
-    // visible key or after a wait that gave up)
-    if (live) {
-      const size_t id = row_id(r), slot = id * p.max_splits + blockIdx.x;
-      if (ok) {
-        fence_proxy_async();
-        if (ns == 1)
-          bulk_store_s2g(p.out + id * D, row, D * 2);
-        else
-          bulk_store_s2g(p.o_part + slot * D, row, D * 4);
+    // The warp's 32 rows to memory, each by the whole warp (a bulk copy per row
+    // took 100 clocks to issue, 32 of them one after another).
+    const int64_t id = live ? static_cast<int64_t>(row_id(r)) : -1;
+    if (live && ns > 1)                      // -inf, never weighed, without a visible key or after a wait that gave up
+      p.lse_part[id * p.max_splits + blockIdx.x] = ok && l > 0.f ? m + __log2f(l) : -INFINITY;
+    __syncwarp();
+    const uint32_t row0 = sb + C::kOffK + warp * 32 * C::kRowBytes;
+    constexpr int BATCH = 8;                 // rows in flight
+    auto write_rows = [&](auto units, auto to_row) {     // 16-byte units of a row; a row's address
+      constexpr int U = decltype(units)::value;
+#pragma unroll 1
+      for (int e0 = 0; e0 < 32; e0 += BATCH) {
+        uint4 x[BATCH][(U + 31) / 32];
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e)
+#pragma unroll
+          for (int c = 0; c < U; c += 32)
+            if (U >= 32 || lane < U) x[e][c / 32] = lds128(row0 + (e0 + e) * C::kRowBytes + (c + lane) * 16);
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+          const int64_t to = __shfl_sync(0xffffffffu, id, e0 + e);
+#pragma unroll
+          for (int c = 0; c < U; c += 32)
+            if (to >= 0 && (U >= 32 || lane < U)) to_row(to)[c + lane] = x[e][c / 32];
+        }
       }
-      if (ns > 1) p.lse_part[slot] = ok && l > 0.f ? m + __log2f(l) : -INFINITY;
-    }
-    bulk_store_wait();
+    };
+    if (ok && ns == 1)
+      write_rows(std::integral_constant<int, D / 8>{}, [&](int64_t to) { return reinterpret_cast<uint4 *>(p.out + to * D); });
+    if (ok && ns > 1)
+      write_rows(std::integral_constant<int, D / 4>{}, [&](int64_t to) {
+        return reinterpret_cast<uint4 *>(p.o_part + (to * p.max_splits + blockIdx.x) * D);
+      });
   }
   tc::fence_before_sync();
   __syncthreads();

@@ -18,7 +18,7 @@ __host__ __device__ constexpr int tree_ctas_per_sm(int D) { return D == 128 ? 2 
 
 // Smallest split: it keeps a CTA's fixed costs (the query tile, the first
 // pages' latency, the output rows) to a fraction of its time.
-constexpr int kTreeSplitTokens = 512;
+constexpr int kTreeSplitTokens = 768;
 // Largest split (its page ids lie in shared memory).
 constexpr int kTreeSplitMax = 15360;
 constexpr int kTreeSplitPages = kTreeSplitMax / kPage;

@@ -396,7 +396,8 @@ int memra_kv_copy_pages(const memra_kv_cache *cache, const int32_t *src_pages, c
  *                 [0, n_nodes) skips its row and sets MEMRA_DEVERR_BAD_SLOT.
  *   n_accepted    device int32 [batch], 0 .. max_accepted (outside: clamped,
  *                 MEMRA_DEVERR_BAD_SEQ_LEN)
- *   max_accepted  0 .. n_nodes;  n_nodes <= MEMRA_MAX_TREE_NODES, batch <= 65535
+ *   max_accepted  0 .. n_nodes;  n_nodes <= MEMRA_MAX_TREE_NODES, batch and
+ *                 n_kv_heads <= 65535
  * Every row of a sequence is read before any is written.  The pages that
  * receive rows must belong to one sequence of the batch.  A sequence shorter
  * than n_nodes sets MEMRA_DEVERR_BAD_SEQ_LEN and moves only rows between

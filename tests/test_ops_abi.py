@@ -131,11 +131,11 @@ def test_tree_checks(memra):
     assert call(maxlen=-1) == INVALID
     assert call(scale=float("nan")) == INVALID
     need = memra.tree_attn_workspace_bytes(2, 8, 8, 128, 5000)
-    assert need == 2 * 8 * 8 * 10 * 129 * 4        # ten splits of 512 tokens at most
+    assert need == 2 * 8 * 8 * 7 * 129 * 4         # seven splits of 768 tokens at most
     assert call(maxlen=5000, wsb=need - 1) == WORKSPACE
     assert call(maxlen=5000, wsb=need, ws=72) == INVALID
     assert call(maxlen=5000, wsb=need, ws=0) == INVALID
-    assert memra.tree_attn_workspace_bytes(2, 8, 8, 128, 512) == 0
+    assert memra.tree_attn_workspace_bytes(2, 8, 8, 128, 768) == 0
     assert memra.tree_attn_workspace_bytes(2, 65, 8, 128, 5000) == 0
     assert memra.tree_attn_workspace_bytes(2, 8, 8, 64, 5000) == 0
     # 262,144 tokens: 160 partials a row, whatever the device
