@@ -1,4 +1,4 @@
-// Entry points of tree attention in include/memra.h: argument validation, the split target, the launches.
+// Entry points of tree attention in include/memra.h: argument validation, the plan, the launches.
 #include <algorithm>
 
 #include "host_checks.cuh"
@@ -8,12 +8,17 @@ using namespace memra;
 
 namespace {
 
+// The plan word (16 bytes), the partial rows, their log-sum-exp.
 size_t tree_workspace(int64_t rows, int32_t head_dim, int32_t max_seq_len, size_t *lse_offset) {
-  const size_t parts = static_cast<size_t>(rows) * tree_most_splits(max_seq_len, kTreeMaxSplits);
-  const size_t o_bytes = (parts * head_dim * sizeof(float) + 255) & ~static_cast<size_t>(255);
-  if (lse_offset) *lse_offset = o_bytes;
-  return o_bytes + parts * sizeof(float);
+  const int splits = tree_max_splits(max_seq_len);
+  const size_t parts = splits > 1 ? static_cast<size_t>(rows) * splits : 0;
+  const size_t o_bytes = parts * head_dim * sizeof(float);
+  if (lse_offset) *lse_offset = 16 + o_bytes;
+  return 16 + o_bytes + parts * sizeof(float);
 }
+
+// Every sequence fits one split, whatever the plan: no partials, no merge.
+bool one_split(int32_t max_seq_len) { return tree_max_splits(max_seq_len) <= 1; }
 
 }  // namespace
 
@@ -24,7 +29,6 @@ size_t memra_tree_attn_workspace_bytes(int32_t batch, int32_t n_nodes, int32_t n
   if (batch < 0 || n_nodes < 1 || n_nodes > MEMRA_MAX_TREE_NODES || n_heads < 1 ||
       (head_dim != 128 && head_dim != 256) || max_seq_len < 0)
     return 0;
-  if (max_seq_len <= kTreeSplitTokens) return 0;     // one split: no partials
   return tree_workspace(static_cast<int64_t>(batch) * n_nodes * n_heads, head_dim, max_seq_len, nullptr);
 }
 
@@ -42,9 +46,10 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
     return MEMRA_ERR_UNSUPPORTED;
   if (!std::isfinite(sm_scale)) return MEMRA_ERR_INVALID_ARG;
   const int group = n_heads / n_kv_heads, rows = n_nodes * group;
-  const int row_ctas = static_cast<int>(ceil_div(rows, 128));
+  const int row_tiles = static_cast<int>(ceil_div(rows, 128));
   const int64_t all_rows = static_cast<int64_t>(batch) * n_nodes * n_heads;
-  if (static_cast<int64_t>(batch) * row_ctas > 65535 || all_rows > INT32_MAX) return MEMRA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n_kv_heads) * row_tiles > 65535 || batch > 65535 || all_rows > INT32_MAX)
+    return MEMRA_ERR_UNSUPPORTED;
   if (batch == 0) return MEMRA_OK;
   if (!q || !page_table || !seq_lens || !tree_mask || !out || !aligned16(q) || !aligned16(out) ||
       (reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
@@ -52,7 +57,7 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
     return MEMRA_ERR_INVALID_ARG;
   const size_t need = memra_tree_attn_workspace_bytes(batch, n_nodes, n_heads, head_dim, max_seq_len);
   if (workspace_bytes < need) return MEMRA_ERR_WORKSPACE;
-  if (need && (!workspace || !aligned16(workspace))) return MEMRA_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace)) return MEMRA_ERR_INVALID_ARG;
   size_t lse = 0;
   tree_workspace(all_rows, head_dim, max_seq_len, &lse);
   TreeParams p;
@@ -63,7 +68,8 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   p.seq_lens = seq_lens;
   p.mask = tree_mask;
   p.out = static_cast<__half *>(out);
-  p.o_part = static_cast<float *>(workspace);
+  p.plan = static_cast<int32_t *>(workspace);
+  p.o_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 16);
   p.lse_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + lse);
   p.status = cache->status;
   p.batch = batch;
@@ -74,9 +80,13 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   p.num_pages = cache->num_pages;
   p.max_pages = max_pages_per_seq;
   p.max_seq_len = max_seq_len;
-  p.target = std::min(kTreeMaxSplits, std::max(1, device_sms() * tree_ctas_per_sm(head_dim) / (n_kv_heads * row_ctas)));
-  p.max_splits = tree_most_splits(max_seq_len, kTreeMaxSplits);
-  p.row_ctas = row_ctas;
+  p.len_limit = static_cast<int32_t>(std::min<int64_t>(max_seq_len, static_cast<int64_t>(max_pages_per_seq) * kPage));
+  // Where the sequences alone fill the GPU four times over, none is cut for its sake (and no CTA adds
+  // up the lengths of so many).
+  p.slots = std::max(1, device_sms() * tree_ctas_per_sm(head_dim) / (n_kv_heads * row_tiles));
+  if (batch >= 4 * p.slots) p.slots = 0;
+  p.max_splits = tree_max_splits(max_seq_len);
+  p.row_tiles = row_tiles;
   // staged values: q8_0 / q5_1 / q4_0 at half size, fp8 / NVFP4 without their tensor scale
   p.scale_log2 = std::fabs(sm_scale) * (cache->k_fmt == MEMRA_KV_Q8_0 ? 2.f : cache->k_scale) * 1.4426950408889634f;
   p.q_and = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;
@@ -85,7 +95,7 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   p.v_post = scaled_format(cache->v_fmt) ? cache->v_scale : 2.f;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = cuda_status(launch_tree(head_dim, cache->k_fmt, cache->v_fmt, p, s));
-  if (st || max_seq_len <= kTreeSplitTokens) return st;      // every sequence fits one split: nothing to merge
+  if (st || one_split(max_seq_len)) return st;
   return cuda_status(launch_tree_merge(head_dim, p, s));
 }
 

@@ -55,21 +55,23 @@ struct TreeCfg {
   static constexpr bool kMCols = VF == MEMRA_KV_Q5_1 && D == 128;
   static constexpr int kOCols = D + (D == 128 ? 16 : 0);
   static constexpr bool kVRows = VF != MEMRA_KV_NVFP4;          // V staged as token rows (MN-major)
-  // operand tiles: one chunk of them where a tile is a hi + lo pair, else two
   static constexpr uint32_t kTile = kTreeKeys * D * 2;
   static constexpr uint32_t kLoOff = kTile + (kMCols ? kTreeKeys * 128 : 0);      // V: hi, minima, lo
   static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kVLo ? kLoOff + kTile : kTile;
-  static constexpr int kKBufs = kKLo ? 1 : 2, kVBufs = kVLo ? 1 : 2;
-  static constexpr int kRaw = 2;                                // chunks of raw pages
   static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
   // Q in tensor memory, but for the last 32 dims at head_dim 128 (two CTAs share its 512 columns:
   // 48 of Q, 144 of O, 64 of scores each), which lie in shared memory
   static constexpr int kQTmem = D == 128 ? 96 : D, kQSmem = D - kQTmem;
+  // V^ tiles: two in turn where a tile is no pair, so that staging runs ahead of the product
+  static constexpr int kVBufs = kVLo ? 1 : 2;
   // barriers and page ids, then K^ and V^ tiles, Q's last dims and the raw chunks; the output rows reuse
   // everything behind the page ids
   static constexpr uint32_t kOffBar = 0, kOffPid = 256, kOffK = 4096;
-  static constexpr uint32_t kOffV = kOffK + kKBufs * kKBuf, kOffQ = kOffV + kVBufs * kVBuf;
+  static constexpr uint32_t kOffV = kOffK + kKBuf, kOffQ = kOffV + kVBufs * kVBuf;
   static constexpr uint32_t kOffRaw = kOffQ + kTileRows * kQSmem * 2;
+  // chunks of raw pages in flight: as many as fit, four at most
+  static constexpr uint32_t kRoom = (kCtas == 2 ? 113 : 227) * 1024;
+  static constexpr int kRaw = (kRoom - kOffRaw) / kRawBytes < 4 ? (kRoom - kOffRaw) / kRawBytes : 4;
   static constexpr uint32_t kEnd = kOffRaw + kRaw * kRawBytes;
   static constexpr uint32_t kRowBytes = D * 4 + 16;             // padded output row
   static constexpr uint32_t kEndRows = kOffK + kTileRows * kRowBytes;
@@ -80,7 +82,7 @@ struct TreeCfg {
   static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows, kFloor = (D == 128 ? 78 : 150) * 1024;
   static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
   static constexpr uint32_t kQCol = 0, kOCol = kQTmem / 2, kSCol = kOCol + kOCols;   // tensor-memory columns
-  static_assert(kOffPid + 4 * kTreeSplitPages <= kOffK, "page ids");
+  static_assert(kOffPid + 4 * kTreeSplitPages <= kOffK && kRaw >= 2, "page ids; a chunk ahead");
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 232448, "shared memory");
   static_assert(kSCol + kBufs * kTreeKeys <= static_cast<int>(kTCols) && kCtas * kTCols <= 512, "tensor memory");
   static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
@@ -360,6 +362,53 @@ __device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint32_t pma
   sts64(buf + n * 128 + ((n & 7) << 4), live ? m[0] | (m[1] << 16) : 0u, live ? m[2] | (m[3] << 16) : 0u);
 }
 
+// Sequence length as the kernels use it.
+__device__ __forceinline__ int tree_len(const TreeParams &p, int T) { return max(0, min(T, p.len_limit)); }
+
+// Work item of the split pass.
+struct TreeItem {
+  int b, T, split, ns;    // b < 0: no such item
+  int C;                  // chunks of a split wanted in this call
+  bool bad;               // the sequence's length was out of range
+};
+
+// Item `index` of the call, by a whole warp from the sequences' lengths.
+__device__ __forceinline__ TreeItem find_item(const TreeParams &p, int index, int lane) {
+  TreeItem it{-1, 0, 0, 0, kTreeMaxChunks, false};
+  const int first = lane < p.batch ? p.seq_lens[lane] : 0;       // a short batch is read once
+  if (p.slots > 0) {
+    int total = tree_ceil(tree_len(p, first), kTreeKeys);
+    for (int b = 32 + lane; b < p.batch; b += 32) total += tree_ceil(tree_len(p, p.seq_lens[b]), kTreeKeys);
+    total = __reduce_add_sync(0xffffffffu, total);
+    it.C = min(max(tree_ceil(total, p.slots), kTreeMinChunks), kTreeMaxChunks);
+  }
+  int start = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane, T0 = b0 == 0 ? first : b < p.batch ? p.seq_lens[b] : 0, T = tree_len(p, T0);
+    const int chunks = tree_ceil(T, kTreeKeys);
+    const int ns = b < p.batch ? max(1, tree_ceil(chunks, tree_split_chunks(chunks, it.C))) : 0;
+    int incl = ns;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
+    }
+    const int at = index - start - (incl - ns);
+    const unsigned who = __ballot_sync(0xffffffffu, at >= 0 && at < ns);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      it.b = b0 + src;
+      it.T = __shfl_sync(0xffffffffu, T, src);
+      it.ns = __shfl_sync(0xffffffffu, ns, src);
+      it.split = __shfl_sync(0xffffffffu, at, src);
+      it.bad = __shfl_sync(0xffffffffu, T != T0 || T0 < p.n_nodes, src);
+      break;
+    }
+    start += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return it;
+}
+
 template <int D, int KF, int VF>
 __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, VF>::kCtas)
     tree_kernel(const TreeParams p) {
@@ -379,26 +428,29 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
 
   grid_dependency_wait();
   allow_dependent_launch();
-  const int kvh = blockIdx.y, b = blockIdx.z / p.row_ctas, r0 = blockIdx.z % p.row_ctas * kTileRows;
+  // Items outermost: the CTAs past the last item come last, so that the others
+  // fill the SMs evenly, and those of one split's pages run side by side.
+  const int side = p.n_kv_heads * p.row_tiles, index = blockIdx.x / side;
+  const int kvh = blockIdx.x % side / p.row_tiles, r0 = blockIdx.x % p.row_tiles * kTileRows;
   const int rows = p.n_nodes * p.group;
-  const int T0 = p.seq_lens[b];
-  const int T = max(0, min(min(T0, p.max_seq_len),
-                           static_cast<int>(min(static_cast<long long>(p.max_pages) * kPage, 2147483647ll))));
-  if (blockIdx.x == 0 && kvh == 0 && r0 == 0 && tid == 0 && (T != T0 || T0 < p.n_nodes))
-    flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
-  const int split_len = tree_split_tokens(T, p.target);
-  const int ns = tree_ceil(T, split_len);
+  // This CTA's sequence and split: items are numbered sequence by sequence
+  // (one at least each).  Every warp finds it for itself.
+  const TreeItem item = find_item(p, index, lane);
+  const int b = item.b, T = item.T, ns = item.ns;
+  if (blockIdx.x == 0 && tid == 0) *p.plan = item.C;
+  if (b < 0) return;                         // fewer items than the grid's bound
+  if (item.split == 0 && kvh == 0 && r0 == 0 && tid == 0 && item.bad) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
   // Global row of row r of this KV head: node r / group, head r % group of the group.
   auto row_id = [&](int r) {
     return (static_cast<size_t>(b) * p.n_nodes + r / p.group) * p.n_heads + kvh * p.group + r % p.group;
   };
-  if (static_cast<int>(blockIdx.x) >= ns) {
-    if (T <= 0 && blockIdx.x == 0)           // no key at all: zeros
-      for (int i = tid; i < min(kTileRows, rows - r0) * (D / 8); i += C::kThreads)
-        *reinterpret_cast<uint4 *>(p.out + row_id(r0 + i / (D / 8)) * D + 8 * (i % (D / 8))) = make_uint4(0, 0, 0, 0);
+  if (T <= 0) {                              // no key at all: zeros
+    for (int i = tid; i < min(kTileRows, rows - r0) * (D / 8); i += C::kThreads)
+      *reinterpret_cast<uint4 *>(p.out + row_id(r0 + i / (D / 8)) * D + 8 * (i % (D / 8))) = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int first = blockIdx.x * split_len, count = min(T - first, split_len);
+  const int split_len = tree_split_chunks(tree_ceil(T, KT), item.C) * KT;
+  const int first = item.split * split_len, count = min(T - first, split_len);
   const int n_chunks = (count + KT - 1) / KT, n_pages = (count + kPage - 1) / kPage;
   // Page id of a page of the split, -1 for one left out or past the end.
   const int32_t *table = p.page_table + static_cast<size_t>(b) * p.max_pages + first / kPage;
@@ -515,11 +567,11 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       // S(ci) = Q K^T
       auto mma_s = [&](int ci) {
         if (!ok || ci >= n_chunks) return;
-        const int kb = ci % C::kKBufs, sbuf = ci % NBUF;
-        wait(kKFull, kb, ci / C::kKBufs);
+        const int sbuf = ci % NBUF;
+        wait(kKFull, 0, ci);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t k = sb + C::kOffK + kb * C::kKBuf, d = tmem + C::kSCol + sbuf * KT;
+        const uint32_t k = sb + C::kOffK, d = tmem + C::kSCol + sbuf * KT;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t at = k + (ks / 4) * KT * 128 + (ks % 4) * 32;
@@ -533,23 +585,23 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
                           idesc_s, 1);
           }
         }
-        tc::commit(bar(kKEmpty, kb));
+        tc::commit(bar(kKEmpty, 0));
         tc::commit(bar(kSFull, sbuf));
       };
       // O += P(ci) V, P in the columns of its scores
       auto mma_o = [&](int ci) {
-        const int vb = ci % C::kVBufs, sbuf = ci % NBUF;
+        const int sbuf = ci % NBUF;
         wait(kPFull, sbuf, ci / NBUF);
-        wait(kVFull, vb, ci / C::kVBufs);
+        wait(kVFull, ci % C::kVBufs, ci / C::kVBufs);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t v = sb + C::kOffV + vb * C::kVBuf, a = tmem + C::kSCol + sbuf * KT, d = tmem + C::kOCol;
+        const uint32_t v = sb + C::kOffV + ci % C::kVBufs * C::kVBuf, a = tmem + C::kSCol + sbuf * KT, d = tmem + C::kOCol;
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks) {
           tc::mma_f16_ta(d, a + 8 * ks, v_desc(v, ks), idesc_oc, ci > 0 || ks > 0);
           if constexpr (C::kVLo) tc::mma_f16_ta(d, a + 8 * ks, v_desc(v + C::kLoOff, ks), idesc_o, 1);
         }
-        tc::commit(bar(kVEmpty, vb));
+        tc::commit(bar(kVEmpty, ci % C::kVBufs));
         if (NBUF > 1 || ci == n_chunks - 1) tc::commit(pv_done);
       };
       ok = mbar_wait_suspended(q_ready, 0, p.status);
@@ -566,21 +618,21 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
     // ---------------------------------------------------------------- staging --
     const int sw = warp - 4;
     if constexpr (C::kMCols) {               // the unused columns of the minima's block, once
-      for (uint32_t i = tid - 128; i < C::kVBufs * KT * 8u; i += 32 * SW)
-        sts128(sb + C::kOffV + (i / (KT * 8)) * C::kVBuf + C::kTile + 16 * (i % (KT * 8)), make_uint4(0, 0, 0, 0));
+      for (uint32_t i = tid - 128; i < KT * 8u; i += 32 * SW)
+        sts128(sb + C::kOffV + C::kTile + 16 * i, make_uint4(0, 0, 0, 0));
       named_barrier_sync(1, 32 * SW);
     }
     for (int ci = 0; ci < n_chunks; ++ci) {
-      const int s = ci % RAW, kb = ci % C::kKBufs, vb = ci % C::kVBufs, valid = count - ci * KT;
+      const int s = ci % RAW, vb = ci % C::kVBufs, valid = count - ci * KT;
       const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, rawv = rawk + NP * C::kKSeg;
       ok = mbar_wait_suspended(raw_full(s), (ci / RAW) & 1, p.status);
-      if (ok && ci >= C::kKBufs) ok = mbar_wait_suspended(bar(kKEmpty, kb), (ci / C::kKBufs - 1) & 1, p.status);
+      if (ok && ci >= 1) ok = mbar_wait_suspended(bar(kKEmpty, 0), (ci - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      stage_k<D, KF, KT, SW>(rawk, sb + C::kOffK + kb * C::kKBuf, sw, lane);
+      stage_k<D, KF, KT, SW>(rawk, sb + C::kOffK, sw, lane);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kKFull, kb));
+      if (lane == 0) mbar_arrive(bar(kKFull, 0));
       if (ci >= C::kVBufs) ok = mbar_wait_suspended(bar(kVEmpty, vb), (ci / C::kVBufs - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -746,7 +798,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
     // took 100 clocks to issue, 32 of them one after another).
     const int64_t id = live ? static_cast<int64_t>(row_id(r)) : -1;
     if (live && ns > 1)                      // -inf, never weighed, without a visible key or after a wait that gave up
-      p.lse_part[id * p.max_splits + blockIdx.x] = ok && l > 0.f ? m + __log2f(l) : -INFINITY;
+      p.lse_part[id * p.max_splits + item.split] = ok && l > 0.f ? m + __log2f(l) : -INFINITY;
     __syncwarp();
     const uint32_t row0 = sb + C::kOffK + warp * 32 * C::kRowBytes;
     constexpr int BATCH = 8;                 // rows in flight
@@ -773,7 +825,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       write_rows(std::integral_constant<int, D / 8>{}, [&](int64_t to) { return reinterpret_cast<uint4 *>(p.out + to * D); });
     if (ok && ns > 1)
       write_rows(std::integral_constant<int, D / 4>{}, [&](int64_t to) {
-        return reinterpret_cast<uint4 *>(p.o_part + (to * p.max_splits + blockIdx.x) * D);
+        return reinterpret_cast<uint4 *>(p.o_part + (to * p.max_splits + item.split) * D);
       });
   }
   tc::fence_before_sync();
@@ -790,19 +842,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
   const int64_t per_seq = static_cast<int64_t>(p.n_nodes) * p.n_heads;
+  allow_dependent_launch();
   if (row >= p.batch * per_seq) return;
-  const int T0 = p.seq_lens[row / per_seq];
-  const int T = max(0, min(min(T0, p.max_seq_len),
-                           static_cast<int>(min(static_cast<long long>(p.max_pages) * kPage, 2147483647ll))));
-  const int split_len = tree_split_tokens(T, p.target), ns = tree_ceil(T, split_len);
-  grid_dependency_wait();                    // the partials are complete
-  if (ns <= 1) return;                       // the split pass wrote this row
+  const int chunks = tree_ceil(tree_len(p, p.seq_lens[row / per_seq]), kTreeKeys);
   const float *lse = p.lse_part + row * p.max_splits;
   const float *src = p.o_part + row * p.max_splits * D + lane * PER;
   float mw = -INFINITY, L = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int k0 = 0; k0 < ns; k0 += BATCH) {   // BATCH partials in flight
+  grid_dependency_wait();                    // the partials and the plan are complete
+  // BATCH partials in flight.  The first ones are read before the plan says how
+  // many there are: what is behind them is never weighed.
+  int ns = p.max_splits;
+  for (int k0 = 0; k0 < ns; k0 += BATCH) {
     float ls[BATCH];
     float4 x[BATCH][PER / 4];
 #pragma unroll
@@ -813,9 +865,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
 #pragma unroll
       for (int e = 0; e < PER / 4; ++e) x[u][e] = in ? at[e] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    if (k0 == 0) {
+      ns = tree_ceil(chunks, tree_split_chunks(chunks, *p.plan));
+      if (ns <= 1) return;                   // the split pass wrote this row
+    }
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      if (ls[u] == -INFINITY) continue;      // its row may hold anything
+      if (k0 + u >= ns || ls[u] == -INFINITY) continue;      // its row may hold anything
       if (ls[u] > mw) {
         const float sc = fast_exp2(mw - ls[u]);
         L *= sc;
@@ -861,9 +917,16 @@ cudaError_t launch_one(const TreeParams &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  const int most = std::max(1, tree_most_splits(p.max_seq_len, p.target));
-  const dim3 grid(static_cast<unsigned>(most), static_cast<unsigned>(p.n_kv_heads),
-                  static_cast<unsigned>(p.batch * p.row_ctas));
+  // Items of the call at most: one wave's worth and one more per sequence, or
+  // where kTreeMaxChunks cuts shorter, that many; and no sequence has more than
+  // the longest can have.
+  const int64_t chunks = tree_ceil(p.max_seq_len, kTreeKeys);
+  const int64_t items = std::min<int64_t>(
+      p.batch + std::max<int64_t>(p.slots, (p.batch * chunks + kTreeMaxChunks - 1) / kTreeMaxChunks),
+      static_cast<int64_t>(p.batch) * std::max(1, p.max_splits));
+  const int64_t ctas = items * p.n_kv_heads * p.row_tiles;
+  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(ctas));
   return launch_pdl(kernel, grid, dim3(C::kThreads), C::kSmem, st, p);
 }
 

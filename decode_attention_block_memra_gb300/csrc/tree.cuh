@@ -16,31 +16,35 @@ constexpr int kTreeKeys = 64;
 // CTAs of the split pass that share an SM.
 __host__ __device__ constexpr int tree_ctas_per_sm(int D) { return D == 128 ? 2 : 1; }
 
-// Smallest split: it keeps a CTA's fixed costs (the query tile, the first
-// pages' latency, the output rows) to a fraction of its time.
-constexpr int kTreeSplitTokens = 768;
-// Largest split (its page ids lie in shared memory).
-constexpr int kTreeSplitMax = 15360;
-constexpr int kTreeSplitPages = kTreeSplitMax / kPage;
-// Most splits that a sequence is cut into to fill the GPU.
+// The split plan.  A call's keys, in chunks of kTreeKeys, are cut so that one
+// wave of the GPU holds all CTAs: C = ceil(chunks of all sequences x KV heads x
+// row tiles / slots) chunks each, at least kTreeMinChunks (below it a CTA's fixed
+// costs, about three chunks' time, weigh more than the split gains) and at most
+// kTreeMaxChunks (page ids in shared memory); a sequence's splits are made equal.
+// It depends on the lengths of all sequences of the call: a row's partial sums
+// are grouped differently in another batch, and its last bits may differ.
+constexpr int kTreeMinChunks = 4;
+constexpr int kTreeMaxChunks = 240;
+constexpr int kTreeSplitPages = kTreeMaxChunks * kTreeKeys / kPage;
+// Most splits of a sequence, unless kTreeMaxChunks makes more.
 constexpr int kTreeMaxSplits = 160;
 
-// Split size of a sequence of T tokens: about `target` splits, never fewer
-// than kTreeSplitTokens or more than kTreeSplitMax tokens, a multiple of 64.
-// It depends on T and `target` (the device, the KV heads and the rows of one
-// sequence) only: a sequence's bytes are the same alone or in any batch.
-__host__ __device__ __forceinline__ int tree_split_tokens(int T, int target) {
-  const int c = ((T > 0 ? (T - 1) / target + 1 : 0) + 63) / 64 * 64;
-  return c < kTreeSplitTokens ? kTreeSplitTokens : (c > kTreeSplitMax ? kTreeSplitMax : c);
+__host__ __device__ __forceinline__ int tree_ceil(int n, int c) { return n > 0 ? (n - 1) / c + 1 : 0; }
+
+// Chunks of a split of a sequence of `chunks` chunks, C chunks wanted.
+__host__ __device__ __forceinline__ int tree_split_chunks(int chunks, int C) {
+  int c = C < tree_ceil(chunks, kTreeMaxSplits) ? tree_ceil(chunks, kTreeMaxSplits) : C;
+  if (c > kTreeMaxChunks) c = kTreeMaxChunks;
+  const int ns = tree_ceil(chunks, c);
+  return ns > 1 ? tree_ceil(chunks, ns) : c;
 }
 
-__host__ __device__ __forceinline__ int tree_ceil(int T, int c) { return T > 0 ? (T - 1) / c + 1 : 0; }
-
-// Most splits of any sequence of up to T tokens: those of the smallest size,
-// capped by the target, or past target * kTreeSplitMax tokens by the largest size.
-__host__ __device__ __forceinline__ int tree_most_splits(int T, int target) {
-  const int cap = tree_ceil(T, kTreeSplitMax) > target ? tree_ceil(T, kTreeSplitMax) : target;
-  return tree_ceil(T, kTreeSplitTokens) < cap ? tree_ceil(T, kTreeSplitTokens) : cap;
+// Most splits of any sequence of up to max_seq_len tokens, whatever the device and the call.
+__host__ __device__ __forceinline__ int tree_max_splits(int max_seq_len) {
+  const int chunks = tree_ceil(max_seq_len, kTreeKeys);
+  const int by_min = tree_ceil(chunks, kTreeMinChunks), by_max = tree_ceil(chunks, kTreeMaxChunks);
+  const int cap = by_max > kTreeMaxSplits ? by_max : kTreeMaxSplits;
+  return by_min < cap ? by_min : cap;
 }
 
 struct TreeParams {
@@ -53,11 +57,13 @@ struct TreeParams {
   __half *out;
   float *o_part;                // [batch * n_nodes * n_heads][max_splits][D]
   float *lse_part;              // [batch * n_nodes * n_heads][max_splits]
+  int32_t *plan;                // C, from the split pass to the merge
   int32_t *status;
   int batch, n_nodes, n_heads, group, n_kv_heads, num_pages, max_pages, max_seq_len;
-  int target;                   // splits that fill the GPU
+  int len_limit;                // min(max_seq_len, tokens of a page table's row): lengths are clamped to it
+  int slots;                    // CTAs of a wave per (KV head, row tile), 0: sequences are cut at kTreeMaxChunks only
   int max_splits;               // partials per row in the workspace
-  int row_ctas;                 // 128-row tiles of one KV head
+  int row_tiles;                // 128-row tiles of one KV head
   float scale_log2;             // |sm_scale| * (post-scale of the staged K values) * log2(e); 1 for sm_scale 0
   uint32_t q_and, q_xor;        // applied to the query's fp16 pairs: the scale's sign, or zeros for sm_scale 0
   float v_post;                 // post-scale of the staged V values

@@ -354,11 +354,12 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
  *   workspace     device, >= memra_tree_attn_workspace_bytes(...) bytes
  *   out           device fp16 [batch][n_nodes][n_heads][head_dim]
  * All K and V formats, head_dim 128 or 256, n_heads / n_kv_heads <=
- * MEMRA_MAX_GROUP, n_kv_heads <= 65535, batch * ceil(n_nodes * n_heads /
+ * MEMRA_MAX_GROUP, batch <= 65535, n_kv_heads * ceil(n_nodes * n_heads /
  * n_kv_heads / 128) <= 65535; sm_scale finite.  K^ and V^ enter the products
  * exactly (or as fp16 pairs), the softmax weights in fp16; everything is
- * accumulated in float32.  A sequence's result bytes are the same alone or in
- * any batch.  A row that sees no key yields zeros.  A sequence shorter than n_nodes
+ * accumulated in float32.  The keys are cut by the lengths of the whole call,
+ * so that it fills the GPU: the same call gives the same bytes, another batch
+ * groups a row's sums differently and may differ in the last bits.  A row that sees no key yields zeros.  A sequence shorter than n_nodes
  * sets MEMRA_DEVERR_BAD_SEQ_LEN; its nodes at positions below 0 are seen by
  * no row and yield zeros.  Keys of a page id outside the pool are left out
  * (MEMRA_DEVERR_BAD_PAGE).  batch == 0 is a no-op. */

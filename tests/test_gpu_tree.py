@@ -177,7 +177,7 @@ def test_many_splits(memra, D, lens):
 
 
 def test_splits_at_their_largest(memra):
-    # 16 KV heads x 8 row CTAs leave the plan about one split: more than 15,360 keys make more than the target
+    # 16 KV heads x 16 row tiles leave a wave one split: more than 15,360 keys make two
     w = W.make_workload("wide", batch=1, q_len=64, n_heads=16 * 32, n_kv_heads=16, head_dim=128, k_fmt="fp8",
                         v_fmt="fp8", seed=8, seq_lens=[8192 + 8192 + 70])
     words = words_for(w, 4)
@@ -195,15 +195,31 @@ def test_splits_at_their_largest(memra):
 
 
 @pytest.mark.parametrize("D", [128, 256])
-def test_same_bytes_alone_or_batched(memra, D):
+def test_alone_and_batched(memra, D):
+    """A sequence alone (cut into other splits) within the tolerance; the same call twice, the same bytes."""
     w = W.random_case(9, batch=3, q_len=6, n_heads=16, n_kv_heads=2, head_dim=D, ctx=(300, 3000))
     words = words_for(w, 5)
     dw, args, got = check(memra, w, words)
+    want, tol = reference(w, words)
+    again = torch.empty_like(dw.out)
+    memra.tree_attn(*args[:6], again, *args[7:])
+    assert torch.equal(again, dw.out)
     for b in range(3):
         out = torch.empty_like(dw.out[b:b + 1])
         memra.tree_attn(dw.cache, dw.q[b:b + 1], dw.page_table[b:b + 1].contiguous(), dw.seq_lens[b:b + 1].clone(),
                         int(w.seq_lens[b]), args[5][b:b + 1].contiguous(), out, args[7], w.sm_scale)
-        assert torch.equal(out[0], dw.out[b])
+        assert (np.abs(out[0].cpu().numpy().astype(np.float64) - want[b]) <= tol[b]).all()
+
+
+@pytest.mark.parametrize("batch,n_heads,n_kv_heads", [(33, 8, 2), (70, 4, 4), (400, 8, 4)])
+def test_many_sequences(memra, batch, n_heads, n_kv_heads):
+    # more than a warp's worth of lengths, empty ones among them; the last fills the GPU without any cut
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(3, 200, batch)
+    lens[::7] = 3
+    w = W.make_workload("many", batch=batch, q_len=3, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=128,
+                        k_fmt="q8_0", v_fmt="q5_1", seed=batch, seq_lens=lens, permute_pages=True)
+    check(memra, w, words_for(w, batch), max_seq_len=3000 if batch > 100 else None)
 
 
 def test_peaked_scores_and_a_negative_scale(memra):

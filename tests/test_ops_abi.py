@@ -131,12 +131,12 @@ def test_tree_checks(memra):
     assert call(maxlen=-1) == INVALID
     assert call(scale=float("nan")) == INVALID
     need = memra.tree_attn_workspace_bytes(2, 8, 8, 128, 5000)
-    assert need == 2 * 8 * 8 * 7 * 129 * 4         # seven splits of 768 tokens at most
+    assert need == 16 + 2 * 8 * 8 * 20 * 129 * 4   # 79 chunks of 64 keys: 20 splits of 4 chunks at most
     assert call(maxlen=5000, wsb=need - 1) == WORKSPACE
     assert call(maxlen=5000, wsb=need, ws=72) == INVALID
     assert call(maxlen=5000, wsb=need, ws=0) == INVALID
-    assert memra.tree_attn_workspace_bytes(2, 8, 8, 128, 768) == 0
+    assert memra.tree_attn_workspace_bytes(2, 8, 8, 128, 256) == 16      # one split: the plan word alone
     assert memra.tree_attn_workspace_bytes(2, 65, 8, 128, 5000) == 0
     assert memra.tree_attn_workspace_bytes(2, 8, 8, 64, 5000) == 0
     # 262,144 tokens: 160 partials a row, whatever the device
-    assert memra.tree_attn_workspace_bytes(1, 64, 32, 128, 262144) == 64 * 32 * 160 * 129 * 4
+    assert memra.tree_attn_workspace_bytes(1, 64, 32, 128, 262144) == 16 + 64 * 32 * 160 * 129 * 4
