@@ -6,19 +6,24 @@
 //
 // One pass over the keys with a running reference maximum m and sum.  The two
 // products are dense contractions, so they run on the fifth-generation tensor
-// cores with their accumulators in tensor memory:
+// cores with their accumulators in tensor memory, and the kernel is built so
+// that they never wait for the softmax:
 //   * A tile is 128 query rows of one KV head: 128 / G consecutive tokens times
 //     the G heads of the group, so a short prompt of grouped heads still fills
 //     the M = 128 side and a tile's rows share one diagonal.
-//   * head_dim 128: a CTA holds two tiles (256 rows) and takes 128 keys at a
-//     time; while the softmax of one tile runs, the tensor cores work on the
-//     other's.  head_dim 256: one tile, 64 keys at a time, two score buffers,
-//     so the scores run one step ahead.
+//   * head_dim 128: a CTA holds two tiles (256 rows) and takes 128 keys a step.
+//     The tiles share one score buffer, free again as soon as the softmax warps
+//     hold the scores in registers, and P has columns of its own; the MMAs go
+//     S0(j) PV0(j-1) S1(j) PV1(j-1), so each softmax has a whole step's MMAs
+//     (2,048 clocks) to finish in.
+//   * head_dim 256: one tile, 64 keys a step, Q in tensor memory (an A operand
+//     in shared memory would need more than its bandwidth at N = 64), two score
+//     buffers that P overwrites; the scores run two steps ahead.
 //   * Q, K and V arrive by TMA tensor copies in the 128-byte-swizzled layout
-//     (K V ring of five 32 KB stages); V is read by the MMA as it lies, keys
-//     along rows (MN-major B), so nothing is transposed.
-//   * P goes to tensor memory in fp16 over the scores it came from and is the A
-//     operand of O += P V: no shared-memory round trip.
+//     (K V ring of 32 KB stages); V is read by the MMA as it lies, keys along
+//     rows (MN-major B), so nothing is transposed.
+//   * P goes to tensor memory in fp16 and is the A operand of O += P V: no
+//     shared-memory round trip.
 // Warps: four softmax warps per tile (thread = row), one MMA warp, one load
 // warp.  The reference maximum moves only when a tile's maximum passes it by
 // more than kLazy (log2 units), so O in tensor memory is rescaled rarely; P
@@ -29,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include "prompt.cuh"
+#include "kv_stage.cuh"
 #include "softmax_tile.cuh"
 #include "tcgen05.cuh"
 
@@ -41,19 +47,19 @@ constexpr float kLazy = 8.f;
 template <int D>
 struct PromptCfg {
   static constexpr int kTiles = D == 128 ? 2 : 1;       // query tiles of a CTA
-  static constexpr int kBufs = D == 128 ? 1 : 2;        // score buffers of a tile
   static constexpr int kKeys = D == 128 ? 128 : 64;     // keys of a step
-  static constexpr int kStages = 5;
+  static constexpr bool kQSmem = D == 128;              // where Q lies
+  static constexpr int kStages = D == 128 ? 5 : 7;
   static constexpr int kBlocks = D / 64;                // 64-element column blocks of a row
   static constexpr uint32_t kQBytes = kTileRows * D * 2;
   static constexpr uint32_t kKvBytes = kKeys * D * 2;
-  static constexpr uint32_t kOffKv = kTiles * kQBytes;
+  static constexpr uint32_t kOffKv = kQSmem ? kTiles * kQBytes : 0;
   static constexpr uint32_t kOffBar = kOffKv + kStages * kKvBytes;
   static constexpr uint32_t kSmem = kOffBar + 256 + 1024;    // 1024: aligning the base
   static constexpr int kThreads = 128 * kTiles + 64;
-  static constexpr uint32_t kOCol = 256;                // O behind the score buffers in tensor memory
+  // tensor-memory columns: D 128 scores 0, P 128 + 64 i, O 256 + 128 i; D 256 scores 64 b, Q 128, O 256
+  static constexpr uint32_t kQCol = 128, kOCol = 256;
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(kTiles * kBufs * kKeys <= 256 && kTiles * D <= 256, "tensor memory");
 };
 
 // One TMA tensor copy: a box of a 3-D tensor map at (x, y, z) to shared memory.
@@ -87,7 +93,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const PromptParams p) {
   using C = PromptCfg<D>;
-  constexpr int NT = C::kTiles, NBUF = C::kBufs, KT = C::kKeys, ST = C::kStages;
+  constexpr int NT = C::kTiles, KT = C::kKeys, ST = C::kStages;
+  constexpr int NBUF = NT == 2 ? 1 : 2;             // uses of a tile's barriers that alternate: the score buffers
   constexpr int kMmaWarp = 4 * NT, kLoadWarp = 4 * NT + 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Work s_work;
@@ -101,7 +108,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   auto s_full = [&](int i, int b) { return bars + 8 * (2 * ST + 2 + 2 * i + b); };
   auto p_full = [&](int i, int b) { return bars + 8 * (2 * ST + 6 + 2 * i + b); };
   auto pv_done = [&](int i) { return bars + 8 * (2 * ST + 10 + i); };
-  const uint32_t v_zeroed = bars + 8 * (2 * ST + 12), drained = bars + 8 * (2 * ST + 13);
+  const uint32_t v_zeroed = bars + 8 * (2 * ST + 12), drained = v_zeroed + 8, s_read = drained + 8;
+  // columns of tile i's scores and P (score buffer b)
+  auto s_col_of = [&](int b) { return static_cast<uint32_t>(NT == 2 ? 0 : b * KT); };
+  auto p_col_of = [&](int i, int b) { return static_cast<uint32_t>(NT == 2 ? 128 + 64 * i : b * KT); };
 
   grid_dependency_wait();
   allow_dependent_launch();
@@ -146,15 +156,16 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       mbar_init(kv_empty(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full(i), 1);
+      mbar_init(q_full(i), C::kQSmem ? 1 : 4);
       mbar_init(pv_done(i), 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(s_full(i, b), 1);
-        mbar_init(p_full(i, b), 128);
+        mbar_init(p_full(i, b), 4);
       }
     }
     mbar_init(v_zeroed, 1);
     mbar_init(drained, 1);
+    mbar_init(s_read, 4);
     fence_barrier_init();
   }
   __syncthreads();
@@ -186,7 +197,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     const bool leader = tc::elect_one();
     if (leader) {
       auto load_q = [&](int i) {
-        if (lo[i] == hi[i]) return;
+        if (!C::kQSmem || lo[i] == hi[i]) return;
         mbar_arrive_expect_tx(q_full(i), static_cast<uint32_t>(p.group * p.tpt) * 128 * C::kBlocks);
 #pragma unroll
         for (int c = 0; c < C::kBlocks; ++c)
@@ -233,24 +244,32 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
       constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(kTileRows, D);
       auto slot_full = [&](int n) { return mbar_wait_suspended(kv_full(n % ST), (n / ST) & 1, p.status); };
-      // S_i(j) = Q_i K(j)^T into score buffer b
-      auto mma_s = [&](int i, int b, int j) {
-        const int n = 2 * (j - jlo);
+      int n_scores = 0;                             // score MMAs issued
+      // S_i(j) = Q_i K(j)^T
+      auto mma_s = [&](int i, int j) {
+        const int n = 2 * (j - jlo), b = NBUF > 1 ? (j - lo[i]) & 1 : 0;
         ok = ok && slot_full(n);
         if (ok && j == lo[i]) ok = mbar_wait_suspended(q_full(i), 0, p.status);
+        // the shared score buffer: the scores before these are in registers
+        if (NT == 2 && ok && n_scores > 0) ok = mbar_wait_suspended(s_read, (n_scores - 1) & 1, p.status);
         if (!ok) return;
+        ++n_scores;
         tc::fence_after_sync();
-        const uint32_t q = sb + i * C::kQBytes, k = sb + C::kOffKv + (n % ST) * C::kKvBytes;
+        const uint32_t q = sb + i * C::kQBytes, k = sb + C::kOffKv + (n % ST) * C::kKvBytes, d = tmem + s_col_of(b);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_f16(tmem + (i * NBUF + b) * KT,
-                      tc::smem_desc_sw128(q + (ks / 4) * kTileRows * 128 + (ks % 4) * 32, 16, 1024),
-                      tc::smem_desc_sw128(k + (ks / 4) * KT * 128 + (ks % 4) * 32, 16, 1024), idesc_s, ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t bd = tc::smem_desc_sw128(k + (ks / 4) * KT * 128 + (ks % 4) * 32, 16, 1024);
+          if constexpr (C::kQSmem)
+            tc::mma_f16(d, tc::smem_desc_sw128(q + (ks / 4) * kTileRows * 128 + (ks % 4) * 32, 16, 1024), bd, idesc_s,
+                        ks > 0);
+          else
+            tc::mma_f16_ta(d, tmem + C::kQCol + 8 * ks, bd, idesc_s, ks > 0);
+        }
         tc::commit(s_full(i, b));
       };
-      // O_i += P_i(j) V(j), P in the columns of its scores
-      auto mma_o = [&](int i, int b, int j) {
-        const int n = 2 * (j - jlo) + 1, u = j - lo[i];
+      // O_i += P_i(j) V(j)
+      auto mma_o = [&](int i, int j) {
+        const int n = 2 * (j - jlo) + 1, u = j - lo[i], b = NBUF > 1 ? u & 1 : 0;
         ok = ok && mbar_wait_suspended(p_full(i, b), (u / NBUF) & 1, p.status);
         ok = ok && slot_full(n);
         if (ok && tail && j == jhi - 1) ok = mbar_wait_suspended(v_zeroed, 0, p.status);
@@ -259,34 +278,33 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         const uint32_t v = sb + C::kOffKv + (n % ST) * C::kKvBytes;
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks)
-          tc::mma_f16_ta(tmem + C::kOCol + i * D, tmem + (i * NBUF + b) * KT + 8 * ks,
+          tc::mma_f16_ta(tmem + C::kOCol + i * D, tmem + p_col_of(i, b) + 8 * ks,
                          tc::smem_desc_sw128(v + ks * 2048, KT * 128, 1024), idesc_o, u > 0 || ks > 0);
-        if (NBUF > 1 || j == hi[i] - 1) tc::commit(pv_done(i));
+        tc::commit(pv_done(i));
       };
       auto release = [&](int n) {
         if (ok) tc::commit(kv_empty(n % ST));
       };
+      auto takes = [&](int i, int j) { return j >= lo[i] && j < hi[i]; };
       if constexpr (NT == 2) {
-        for (int j = jlo; j < jhi && ok; ++j) {
-          for (int i = 0; i < NT; ++i)
-            if (j == lo[i] && lo[i] < hi[i]) mma_s(i, 0, j);
-          release(2 * (j - jlo));                   // every tile's scores of step j are issued
+        for (int j = jlo; j <= jhi && ok; ++j) {
           for (int i = 0; i < NT; ++i) {
-            if (j >= lo[i] && j < hi[i]) mma_o(i, 0, j);
-            if (ok && j >= lo[i] && j + 1 < hi[i]) mma_s(i, 0, j + 1);
+            if (ok && takes(i, j)) mma_s(i, j);
+            if (ok && takes(i, j - 1)) mma_o(i, j - 1);
           }
-          release(2 * (j - jlo) + 1);
+          if (j < jhi) release(2 * (j - jlo));      // K(j)
+          if (j > jlo) release(2 * (j - jlo) - 1);  // V(j - 1)
         }
       } else {
         auto scores = [&](int j) {
           if (!ok || j >= jhi) return;
-          mma_s(0, (j - jlo) & 1, j);
+          mma_s(0, j);
           release(2 * (j - jlo));
         };
         scores(jlo);
         scores(jlo + 1);
         for (int j = jlo; j < jhi && ok; ++j) {
-          mma_o(0, (j - jlo) & 1, j);
+          mma_o(0, j);
           release(2 * (j - jlo) + 1);
           scores(j + 2);                            // behind the product that reads its buffer's P
         }
@@ -308,10 +326,30 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     float m = -INFINITY;
     uint64_t l = 0;                                 // two sums, of the even and the odd keys
     const uint32_t o_col = tmem + tlane + C::kOCol + i * D;
+    if constexpr (!C::kQSmem) {
+      // the row of Q, fp16 pairs as they lie
+      const int head = kvh * p.group + rl % p.group;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          p.q + (live ? static_cast<int64_t>(w.first + t) * p.q_stride + static_cast<int64_t>(head) * D : 0));
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t x[32];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint4 y = live ? src[c / 4 + e] : make_uint4(0, 0, 0, 0);
+          x[4 * e] = y.x, x[4 * e + 1] = y.y, x[4 * e + 2] = y.z, x[4 * e + 3] = y.w;
+        }
+        tc::st_32x32b_x32(tmem + tlane + C::kQCol + c, x);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(i));
+    }
 #pragma unroll 1
     for (int u = 0; u < n_steps; ++u) {
       const int j = lo[i] + u, b = NBUF > 1 ? u & 1 : 0;
-      const uint32_t s_col = tmem + tlane + (i * NBUF + b) * KT;
+      const uint32_t s_col = tmem + tlane + s_col_of(b), p_col = tmem + tlane + p_col_of(i, b);
       ok = mbar_wait_suspended(s_full(i, b), (u / NBUF) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -321,12 +359,21 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       for (int c = 0; c < KT; c += 32) tc::ld_32x32b_x32(s_col + c, s + c);
       tc::wait_ld_all();
       tc::hold<KT>(s);
-      // keys behind the row's token, or before its window
-      if (j * KT + KT - 1 > tile_first || (p.window > 0 && j * KT < tile_last - p.window + 1)) {
-        const int last = t - j * KT, first = p.window > 0 ? last - p.window + 1 : 0;
+      if (NT == 2) {                                // the score buffer is the other tile's turn
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_read);
+      }
+      const int last = t - j * KT;                  // the row's own key, in this step's columns
+      if (j * KT + KT - 1 > tile_first) {           // keys behind the row's token
 #pragma unroll
         for (int c = 0; c < KT; ++c)
-          if (c > last || c < first) s[c] = 0xff800000u;          // -inf
+          if (c > last) s[c] = 0xff800000u;         // -inf
+      }
+      if (p.window > 0 && j * KT < tile_last - p.window + 1) {    // keys before its window
+#pragma unroll
+        for (int c = 0; c < KT; ++c)
+          if (c < last - p.window + 1) s[c] = 0xff800000u;
       }
       const float top = row_max(s) * p.scale_log2;
       float alpha = 1.f;
@@ -334,15 +381,15 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         if (m != -INFINITY) alpha = fast_exp2(m - top);
         m = top;
       }
-      if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // O's rows of this warp times alpha, once the product before has completed
-        // (one score buffer: these scores were issued behind it)
-        if (NBUF > 1) {
-          ok = mbar_wait_suspended(pv_done(i), (u - 1) & 1, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc::fence_after_sync();
-        }
+      const bool moved = u > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+      if (u > 0 && (NT == 2 || moved)) {
+        // the product before has completed: it has read P's columns (their own, head_dim 128), and O is still
+        ok = mbar_wait_suspended(pv_done(i), (u - 1) & 1, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      if (moved) {                                  // O's rows of this warp times alpha
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -357,43 +404,55 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
       const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int c = 0; c < KT; c += 64) {
-        uint32_t w2[32];
-        row_weights<32>(s + c, p.scale_log2, mu, w2, l);
-        tc::st_32x32b_x32(s_col + c / 2, w2);
+      for (int c = 0; c < KT; c += 32) {
+        uint32_t w2[16];
+        row_weights<16>(s + c, p.scale_log2, mu, w2, l);
+        tc::st_32x32b_x16(p_col + c / 2, w2);
       }
       tc::wait_st();
       tc::fence_before_sync();
-      mbar_arrive(p_full(i, b));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(i, b));
     }
     // The last product.  Two score buffers: the product before it may still be
     // running, so its phase comes first (a parity names only the next phase).
     if (NBUF > 1 && n_steps > 1 && ok) ok = mbar_wait_suspended(pv_done(i), (n_steps - 2) & 1, p.status);
-    if (n_steps > 0 && ok) ok = mbar_wait_suspended(pv_done(i), NBUF > 1 ? (n_steps - 1) & 1 : 0, p.status);
+    if (n_steps > 0 && ok) ok = mbar_wait_suspended(pv_done(i), (n_steps - 1) & 1, p.status);
     if (__all_sync(0xffffffffu, n_steps > 0 && ok)) {
       tc::fence_after_sync();
       float l0, l1;
       unpack_f2(l, l0, l1);
       const float inv = l0 + l1 > 0.f ? 1.f / (l0 + l1) : 0.f;
-      const int head = kvh * p.group + rl % p.group;
-      __half *dst = p.out + (static_cast<size_t>(w.first + t) * p.n_heads + head) * D;
-#pragma unroll 1
+      // The row into shared memory (the tile's Q, or at head_dim 256 the ring: both read for the last
+      // time), 16-byte units XORed with the row so that eight rows' stores fall on different banks ...
+      constexpr uint32_t kRow = D * 2;
+      const uint32_t rows = sb + (C::kQSmem ? i * C::kQBytes : C::kOffKv) + (warp & 3) * 32 * kRow;
+#pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         tc::ld_32x32b_x32(o_col + c, o);
         tc::wait_ld_all();
         tc::hold<32>(o);
-        if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 x;
-            x.x = pack_half2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-            x.y = pack_half2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            x.z = pack_half2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-            x.w = pack_half2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-            *reinterpret_cast<uint4 *>(dst + c + e) = x;
-          }
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t x[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            x[h] = pack_half2(__uint_as_float(o[e + 2 * h]) * inv, __uint_as_float(o[e + 2 * h + 1]) * inv);
+          sts128(rows + lane * kRow + ((((c + e) / 8) ^ (lane & 7)) * 16), make_uint4(x[0], x[1], x[2], x[3]));
         }
+      }
+      // ... and from there to memory, the heads of a token side by side.
+      const int64_t to =
+          live ? (static_cast<int64_t>(w.first + t) * p.n_heads + kvh * p.group + rl % p.group) * D : -1;
+      __syncwarp();
+      constexpr int U = D / 8, PER = 32 / U;        // 16-byte units of a row, rows at a time
+#pragma unroll 8
+      for (int e = 0; e < 32; e += PER) {
+        const int row = e + lane / U, u = lane % U;
+        const uint4 x = lds128(rows + row * kRow + (u ^ (row & 7)) * 16);
+        const int64_t at = __shfl_sync(0xffffffffu, to, row);
+        if (at >= 0) *reinterpret_cast<uint4 *>(p.out + at + 8 * u) = x;
       }
     }
   }

@@ -495,11 +495,11 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
         mbar_init(bar(kVFull, k), SW);
         mbar_init(bar(kVEmpty, k), 1);
         mbar_init(bar(kSFull, k), 1);
-        mbar_init(bar(kPFull, k), 128);
+        mbar_init(bar(kPFull, k), 4);
       }
       mbar_init(pv_done, 1);
       mbar_init(drained, 1);
-      mbar_init(q_ready, 128);
+      mbar_init(q_ready, 4);
       fence_barrier_init();
     }
     __syncwarp();
@@ -686,7 +686,8 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
     tc::wait_st();
     fence_proxy_async();
     tc::fence_before_sync();
-    mbar_arrive(q_ready);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_ready);
     const int base = T - p.n_nodes;          // position of the tree's first row
     const uint32_t o_col = tmem + tlane + C::kOCol;
     float m = -INFINITY, l = 0.f;
@@ -756,7 +757,8 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       l += l0 + l1;
       tc::wait_st();
       tc::fence_before_sync();
-      mbar_arrive(bar(kPFull, sbuf));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kPFull, sbuf));
     }
     // The last product.  Two score buffers: the product before it may still be
     // running, so its phase comes first (a parity names only the next phase).
