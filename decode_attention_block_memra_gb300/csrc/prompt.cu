@@ -255,13 +255,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         if (!ok) return;
         ++n_scores;
         tc::fence_after_sync();
-        const uint32_t q = sb + i * C::kQBytes, k = sb + C::kOffKv + (n % ST) * C::kKvBytes, d = tmem + s_col_of(b);
+        const uint32_t d = tmem + s_col_of(b);
+        const uint64_t qd = tc::smem_desc_sw128(sb + i * C::kQBytes, 16, 1024);
+        const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffKv + (n % ST) * C::kKvBytes, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t bd = tc::smem_desc_sw128(k + (ks / 4) * KT * 128 + (ks % 4) * 32, 16, 1024);
+          const uint64_t bd = tc::desc_at(kd, (ks / 4) * KT * 128 + (ks % 4) * 32);
           if constexpr (C::kQSmem)
-            tc::mma_f16(d, tc::smem_desc_sw128(q + (ks / 4) * kTileRows * 128 + (ks % 4) * 32, 16, 1024), bd, idesc_s,
-                        ks > 0);
+            tc::mma_f16(d, tc::desc_at(qd, (ks / 4) * kTileRows * 128 + (ks % 4) * 32), bd, idesc_s, ks > 0);
           else
             tc::mma_f16_ta(d, tmem + C::kQCol + 8 * ks, bd, idesc_s, ks > 0);
         }
@@ -275,11 +276,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         if (ok && tail && j == jhi - 1) ok = mbar_wait_suspended(v_zeroed, 0, p.status);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t v = sb + C::kOffKv + (n % ST) * C::kKvBytes;
+        const uint64_t vd = tc::smem_desc_sw128(sb + C::kOffKv + (n % ST) * C::kKvBytes, KT * 128, 1024);
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks)
-          tc::mma_f16_ta(tmem + C::kOCol + i * D, tmem + p_col_of(i, b) + 8 * ks,
-                         tc::smem_desc_sw128(v + ks * 2048, KT * 128, 1024), idesc_o, u > 0 || ks > 0);
+          tc::mma_f16_ta(tmem + C::kOCol + i * D, tmem + p_col_of(i, b) + 8 * ks, tc::desc_at(vd, ks * 2048), idesc_o,
+                         u > 0 || ks > 0);
         tc::commit(pv_done(i));
       };
       auto release = [&](int n) {
@@ -288,6 +289,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       auto takes = [&](int i, int j) { return j >= lo[i] && j < hi[i]; };
       if constexpr (NT == 2) {
         for (int j = jlo; j <= jhi && ok; ++j) {
+#pragma unroll
           for (int i = 0; i < NT; ++i) {
             if (ok && takes(i, j)) mma_s(i, j);
             if (ok && takes(i, j - 1)) mma_o(i, j - 1);
@@ -382,8 +384,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         m = top;
       }
       const bool moved = u > 0 && __any_sync(0xffffffffu, alpha != 1.f);
-      if (u > 0 && (NT == 2 || moved)) {
-        // the product before has completed: it has read P's columns (their own, head_dim 128), and O is still
+      if (u > 0 && (NT == 2 || moved || u == n_steps - 1)) {
+        // The product before has completed: it has read P's columns (their own, head_dim 128), and O is
+        // still.  At the last step in any case: the wait behind the loop names the last product by its
+        // parity, which the product two before has too.
         ok = mbar_wait_suspended(pv_done(i), (u - 1) & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -414,9 +418,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full(i, b));
     }
-    // The last product.  Two score buffers: the product before it may still be
-    // running, so its phase comes first (a parity names only the next phase).
-    if (NBUF > 1 && n_steps > 1 && ok) ok = mbar_wait_suspended(pv_done(i), (n_steps - 2) & 1, p.status);
     if (n_steps > 0 && ok) ok = mbar_wait_suspended(pv_done(i), (n_steps - 1) & 1, p.status);
     if (__all_sync(0xffffffffu, n_steps > 0 && ok)) {
       tc::fence_after_sync();

@@ -36,6 +36,9 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo,
   return smem_desc(addr, lbo, sbo) | (2ull << 61);
 }
 
+// The same operand `bytes` (a multiple of 16) further on: shared memory ends far below the field's.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
 // Instruction descriptor of an MMA of kind::f16: fp32 accumulator (bits 4-5 =
 // 1), A and B fp16 (bits 7-9, 10-12 = 0), neither negated, both K-major (bits
 // 15, 16 = 0), N / 8 at bits 17-22, M / 16 at bits 24-28.

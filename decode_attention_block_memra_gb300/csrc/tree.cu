@@ -557,10 +557,6 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
       constexpr uint32_t idesc_o = C::kVRows ? tc::idesc_f16_f32_bmn(kTileRows, D) : tc::idesc_f16_f32(kTileRows, D);
       constexpr uint32_t idesc_oc = C::kMCols ? tc::idesc_f16_f32_bmn(kTileRows, C::kOCols) : idesc_o;
-      auto v_desc = [](uint32_t v, int ks) {
-        return C::kVRows ? tc::smem_desc_sw128(v + 2048 * ks, KT * 128, 1024)
-                         : tc::smem_desc(v + 256 * ks, 128, (KT / 8) * 128);
-      };
       auto wait = [&](int kind, int k, int phase) {
         ok = ok && mbar_wait_suspended(bar(kind, k), phase & 1, p.status);
       };
@@ -571,18 +567,18 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
         wait(kKFull, 0, ci);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t k = sb + C::kOffK, d = tmem + C::kSCol + sbuf * KT;
+        const uint32_t d = tmem + C::kSCol + sbuf * KT;
+        const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
+        const uint64_t qd = tc::smem_desc(sb + C::kOffQ, 128, C::kQSmem / 8 * 128);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t at = k + (ks / 4) * KT * 128 + (ks % 4) * 32;
 #pragma unroll
           for (int lo = 0; lo < (C::kKLo ? 2 : 1); ++lo) {
-            const uint64_t bd = tc::smem_desc_sw128(at + lo * C::kTile, 16, 1024);
+            const uint64_t bd = tc::desc_at(kd, (ks / 4) * KT * 128 + (ks % 4) * 32 + lo * C::kTile);
             if (16 * ks < C::kQTmem)
               tc::mma_f16_ta(d, tmem + C::kQCol + 8 * ks, bd, idesc_s, ks + lo > 0);
             else
-              tc::mma_f16(d, tc::smem_desc(sb + C::kOffQ + 256 * (ks - C::kQTmem / 16), 128, C::kQSmem / 8 * 128), bd,
-                          idesc_s, 1);
+              tc::mma_f16(d, tc::desc_at(qd, 256 * (ks - C::kQTmem / 16)), bd, idesc_s, 1);
           }
         }
         tc::commit(bar(kKEmpty, 0));
@@ -596,10 +592,12 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
         if (!ok) return;
         tc::fence_after_sync();
         const uint32_t v = sb + C::kOffV + ci % C::kVBufs * C::kVBuf, a = tmem + C::kSCol + sbuf * KT, d = tmem + C::kOCol;
+        const uint64_t vd = C::kVRows ? tc::smem_desc_sw128(v, KT * 128, 1024) : tc::smem_desc(v, 128, (KT / 8) * 128);
+        constexpr uint32_t kStep = C::kVRows ? 2048 : 256;       // a K = 16 step further on
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks) {
-          tc::mma_f16_ta(d, a + 8 * ks, v_desc(v, ks), idesc_oc, ci > 0 || ks > 0);
-          if constexpr (C::kVLo) tc::mma_f16_ta(d, a + 8 * ks, v_desc(v + C::kLoOff, ks), idesc_o, 1);
+          tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks), idesc_oc, ci > 0 || ks > 0);
+          if constexpr (C::kVLo) tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks + C::kLoOff), idesc_o, 1);
         }
         tc::commit(bar(kVEmpty, ci % C::kVBufs));
         if (NBUF > 1 || ci == n_chunks - 1) tc::commit(pv_done);
@@ -724,15 +722,17 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
         if (m != -INFINITY) alpha = fast_exp2(m - top);
         m = top;
       }
-      if (ci > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // O's rows of this warp times alpha, once the product before has
-        // completed (one score buffer: these scores were issued behind it)
-        if (NBUF > 1) {
-          ok = mbar_wait_suspended(pv_done, (ci - 1) & 1, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc::fence_after_sync();
-        }
+      const bool moved = ci > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+      if (NBUF > 1 && ci > 0 && (moved || ci == n_chunks - 1)) {
+        // The product before has completed, O is still (one score buffer: these scores were issued behind
+        // it).  At the last chunk in any case: the wait behind the loop names the last product by its
+        // parity, which the product two before has too.
+        ok = mbar_wait_suspended(pv_done, (ci - 1) & 1, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::fence_after_sync();
+      }
+      if (moved) {                           // O's rows of this warp times alpha
 #pragma unroll 1
         for (int c = 0; c < C::kOCols; c += 16) {
           uint32_t o[16];
@@ -760,9 +760,6 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kPFull, sbuf));
     }
-    // The last product.  Two score buffers: the product before it may still be
-    // running, so its phase comes first (a parity names only the next phase).
-    if (NBUF > 1 && n_chunks > 1 && ok) ok = mbar_wait_suspended(pv_done, (n_chunks - 2) & 1, p.status);
     if (ok) ok = mbar_wait_suspended(pv_done, NBUF > 1 ? (n_chunks - 1) & 1 : 0, p.status);
     // (every MMA is done: the operand tiles and raw pages are free for the output rows)
     ok = __all_sync(0xffffffffu, ok);

@@ -193,6 +193,20 @@ def test_captured_call_reads_new_lengths(memra):
         assert bool(((out[a:b].double() - want).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_many_calls_in_a_row(memra, D):
+    """No wait runs out and no byte changes over thousands of calls (a wait that names the wrong phase would)."""
+    q, k, v, cu, out = check(memra, [700, 300, 64], 8, 2, D, window=150, seed=12)
+    want = out.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for _ in range(3000):
+        out.zero_()
+        memra.prompt_attn(q, k, v, cu, out, window=150, status=status)
+        same &= (out == want).all()
+    assert int(status) == 0 and bool(same)
+
+
 def test_binding_refuses_other_layouts(memra):
     q = torch.zeros(4, 8, 128, device="cuda").half()
     k = torch.zeros(4, 2, 128, device="cuda").half()

@@ -282,6 +282,21 @@ def test_captured_call_reads_new_lengths_and_words(memra):
     assert (np.abs(dw.out.cpu().numpy().astype(np.float64) - want) <= tol).all()
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_many_calls_in_a_row(memra, D):
+    """No wait runs out and no byte changes over thousands of calls (a wait that names the wrong phase would)."""
+    w = W.random_case(16, batch=4, q_len=5, n_heads=16, n_kv_heads=2, head_dim=D, k_fmt="fp8", v_fmt="fp8",
+                      ctx=(300, 2500))
+    dw, args, got = check(memra, w, words_for(w, 13))
+    want = dw.out.clone()
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for _ in range(3000):
+        dw.out.zero_()
+        memra.tree_attn(*args)
+        same &= (dw.out == want).all()
+    assert memra.read_status(dw.cache) == 0 and bool(same)
+
+
 def test_two_streams_with_their_own_workspaces(memra):
     w = W.random_case(15, batch=2, q_len=8, n_heads=32, n_kv_heads=4, ctx=(3000, 5000))
     words = words_for(w, 12)
