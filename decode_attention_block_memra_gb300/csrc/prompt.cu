@@ -13,9 +13,8 @@
 //     the M = 128 side and a tile's rows share one diagonal.
 //   * head_dim 128: a CTA holds two tiles (256 rows) and takes 128 keys a step.
 //     The tiles share one score buffer, free again as soon as the softmax warps
-//     hold the scores in registers, and P has columns of its own; the MMAs go
-//     S0(j) PV0(j-1) S1(j) PV1(j-1), so each softmax has a whole step's MMAs
-//     (2,048 clocks) to finish in.
+//     hold the scores in registers, and P has columns of its own, so each softmax
+//     has a whole step's MMAs (2,048 clocks) to finish in.
 //   * head_dim 256: one tile, 64 keys a step, Q in tensor memory (an A operand
 //     in shared memory would need more than its bandwidth at N = 64), two score
 //     buffers that P overwrites; the scores run two steps ahead.
@@ -24,8 +23,8 @@
 //     rows (MN-major B), so nothing is transposed.
 //   * P goes to tensor memory in fp16 and is the A operand of O += P V: no
 //     shared-memory round trip.
-// Warps: four softmax warps per tile (thread = row), one MMA warp, one load
-// warp.  The reference maximum moves only when a tile's maximum passes it by
+// Warps: four softmax warps per tile (thread = row), one that issues the score
+// MMAs, one that issues the products, one that loads.  The reference maximum moves only when a tile's maximum passes it by
 // more than kLazy (log2 units), so O in tensor memory is rescaled rarely; P
 // then stays <= 2^kLazy.  Scores, maxima, sums and O are float32; P is rounded
 // to fp16 (relative 2^-11 a weight), the operand type of the tensor cores.
@@ -54,9 +53,12 @@ struct PromptCfg {
   static constexpr uint32_t kQBytes = kTileRows * D * 2;
   static constexpr uint32_t kKvBytes = kKeys * D * 2;
   static constexpr uint32_t kOffKv = kQSmem ? kTiles * kQBytes : 0;
+  // head_dim 256: Q passes through the ring's last stages on its way to tensor memory
+  static constexpr int kQStage = kStages - static_cast<int>(kQBytes / kKvBytes);
+  static constexpr uint32_t kOffQ = kQSmem ? 0 : kOffKv + kQStage * kKvBytes;
   static constexpr uint32_t kOffBar = kOffKv + kStages * kKvBytes;
   static constexpr uint32_t kSmem = kOffBar + 256 + 1024;    // 1024: aligning the base
-  static constexpr int kThreads = 128 * kTiles + 64;
+  static constexpr int kThreads = 128 * kTiles + 96;
   // tensor-memory columns: D 128 scores 0, P 128 + 64 i, O 256 + 128 i; D 256 scores 64 b, Q 128, O 256
   static constexpr uint32_t kQCol = 128, kOCol = 256;
   static_assert(kSmem <= 232448, "shared memory");
@@ -77,6 +79,51 @@ struct Work {
   int t0;               // first token of the CTA's first tile, within the sequence
 };
 
+// A sequence's rows as the kernel uses them: within 0 .. total, not before they start.
+__device__ __forceinline__ Work clamp_rows(const PromptParams &p, int b, bool report) {
+  Work w{0, 0, -1};
+  if (b < p.batch) {
+    const int cs = p.cu_seqlens[b], ce = p.cu_seqlens[b + 1];
+    w.first = min(max(cs, 0), p.total);
+    w.len = min(max(ce, w.first), p.total) - w.first;
+    if (report && (w.first != cs || w.first + w.len != ce)) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
+  }
+  return w;
+}
+
+__device__ __forceinline__ Work broadcast(const Work &w, int src) {
+  return Work{__shfl_sync(0xffffffffu, w.first, src), __shfl_sync(0xffffffffu, w.len, src),
+              __shfl_sync(0xffffffffu, w.t0, src)};
+}
+
+// The `rank`-th piece of `tpc` tokens of the call, by a whole warp; t0 < 0: there
+// is none.  Pieces are numbered sequence by sequence, a sequence's last (its
+// longest) first.  (Ordering the pieces of all sequences by length instead gained
+// nothing: 516 against 512 us on 8 ragged prompts of up to 4,860 tokens, 32/4
+// heads, D 128.)  CTA 0 checks every length.
+__device__ __forceinline__ Work find_work(const PromptParams &p, int rank, int tpc, int lane) {
+  const bool report = blockIdx.x == 0;
+  Work found{0, 0, -1};
+  int start = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    Work w = clamp_rows(p, b0 + lane, report);
+    const int pieces = (w.len + tpc - 1) / tpc;
+    int incl = pieces;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
+    }
+    const int nth = rank - start - (incl - pieces);
+    if (nth >= 0 && nth < pieces) w.t0 = (pieces - 1 - nth) * tpc;
+    const unsigned who = __ballot_sync(0xffffffffu, w.t0 >= 0);
+    if (who) found = broadcast(w, __ffs(who) - 1);
+    if (who && !report) break;
+    start += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return found;
+}
+
 // Steps [lo, hi) of kKeys keys that a tile of tokens t .. t + tpt - 1 takes; empty when the tile is.
 template <int D>
 __device__ __forceinline__ void tile_steps(const PromptParams &p, const Work &w, int t, int &lo, int &hi) {
@@ -95,7 +142,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   using C = PromptCfg<D>;
   constexpr int NT = C::kTiles, KT = C::kKeys, ST = C::kStages;
   constexpr int NBUF = NT == 2 ? 1 : 2;             // uses of a tile's barriers that alternate: the score buffers
-  constexpr int kMmaWarp = 4 * NT, kLoadWarp = 4 * NT + 1;
+  constexpr int kScoreWarp = 4 * NT, kOutWarp = kScoreWarp + 1, kLoadWarp = kScoreWarp + 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Work s_work;
   __shared__ uint32_t tmem_slot;
@@ -108,7 +155,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   auto s_full = [&](int i, int b) { return bars + 8 * (2 * ST + 2 + 2 * i + b); };
   auto p_full = [&](int i, int b) { return bars + 8 * (2 * ST + 6 + 2 * i + b); };
   auto pv_done = [&](int i) { return bars + 8 * (2 * ST + 10 + i); };
-  const uint32_t v_zeroed = bars + 8 * (2 * ST + 12), drained = v_zeroed + 8, s_read = drained + 8;
+  const uint32_t v_zeroed = bars + 8 * (2 * ST + 12), s_read = v_zeroed + 8;
+  auto drained = [&](int which) { return s_read + 8 + 8 * which; };
+  auto s_free = [&](int b) { return s_read + 24 + 8 * b; };
+  // Q in shared memory; where it goes on to tensor memory, q_full follows when it is there
+  auto q_landed = [&](int i) { return C::kQSmem ? q_full(i) : s_read + 40; };
   // columns of tile i's scores and P (score buffer b)
   auto s_col_of = [&](int b) { return static_cast<uint32_t>(NT == 2 ? 0 : b * KT); };
   auto p_col_of = [&](int i, int b) { return static_cast<uint32_t>(NT == 2 ? 128 + 64 * i : b * KT); };
@@ -116,39 +167,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   grid_dependency_wait();
   allow_dependent_launch();
 
-  // Tiles are numbered sequence by sequence, a sequence's last (longest) first.
   const int kvh = blockIdx.x % p.n_kv_heads, rank = blockIdx.x / p.n_kv_heads;
-  const int tpc = NT * p.tpt;                       // tokens of a CTA
   if (warp == 0) {
-    int start = 0;
-    Work w{0, 0, -1};
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const int b = b0 + lane;
-      int s = 0, e = 0;
-      if (b < p.batch) {
-        const int cs = p.cu_seqlens[b], ce = p.cu_seqlens[b + 1];
-        s = min(max(cs, 0), p.total);
-        e = min(max(ce, s), p.total);
-        if (blockIdx.x == 0 && (s != cs || e != ce)) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
-      }
-      const int tiles = (e - s + tpc - 1) / tpc;
-      int incl = tiles;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += up;
-      }
-      const int at = rank - start - (incl - tiles);
-      if (w.t0 < 0 && at >= 0 && at < tiles) w = Work{s, e - s, (tiles - 1 - at) * tpc};
-      const unsigned who = __ballot_sync(0xffffffffu, w.t0 >= 0);
-      start += __shfl_sync(0xffffffffu, incl, 31);
-      if (who && blockIdx.x != 0) {                 // CTA 0 checks every length
-        if (lane == __ffs(who) - 1) s_work = w;
-        break;
-      }
-      if (who && lane == __ffs(who) - 1) s_work = w;
-      if (!who && lane == 0) s_work = w;
-    }
+    const Work w = find_work(p, rank, NT * p.tpt, lane);
+    if (lane == 0) s_work = w;
   }
   if (tid == 32) {
     for (int s = 0; s < ST; ++s) {
@@ -164,14 +186,18 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       }
     }
     mbar_init(v_zeroed, 1);
-    mbar_init(drained, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(drained(b), 1);
+      mbar_init(s_free(b), 1);
+      if (!C::kQSmem && b == 0) mbar_init(q_landed(0), 1);
+    }
     mbar_init(s_read, 4);
     fence_barrier_init();
   }
   __syncthreads();
   const Work w = s_work;
   if (w.t0 < 0) return;                             // fewer tiles than the grid's bound
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc::tmem_alloc(smem_addr(&tmem_slot), 512);
     tc::tmem_relinquish();
   }
@@ -197,17 +223,18 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     const bool leader = tc::elect_one();
     if (leader) {
       auto load_q = [&](int i) {
-        if (!C::kQSmem || lo[i] == hi[i]) return;
-        mbar_arrive_expect_tx(q_full(i), static_cast<uint32_t>(p.group * p.tpt) * 128 * C::kBlocks);
+        if (lo[i] == hi[i]) return;
+        mbar_arrive_expect_tx(q_landed(i), static_cast<uint32_t>(p.group * p.tpt) * 128 * C::kBlocks);
 #pragma unroll
         for (int c = 0; c < C::kBlocks; ++c)
-          tma_load_3d(sb + i * C::kQBytes + c * kTileRows * 128, &qmap, 64 * c, kvh * p.group,
-                      w.first + w.t0 + i * p.tpt, q_full(i));
+          tma_load_3d(sb + C::kOffQ + i * C::kQBytes + c * kTileRows * 128, &qmap, 64 * c, kvh * p.group,
+                      w.first + w.t0 + i * p.tpt, q_landed(i));
       };
       load_q(0);
       for (int n = 0; n < slots; ++n) {             // K and V of a step by turns
         const int s = n % ST;
-        if (n >= ST) ok = mbar_wait_suspended(kv_empty(s), (n / ST - 1) & 1, p.status);
+        if (!C::kQSmem && n == C::kQStage) ok = mbar_wait_suspended(q_full(0), 0, p.status);   // Q has left the ring
+        if (ok && n >= ST) ok = mbar_wait_suspended(kv_empty(s), (n / ST - 1) & 1, p.status);
         if (!ok) break;
         mbar_arrive_expect_tx(kv_full(s), C::kKvBytes);
 #pragma unroll
@@ -238,82 +265,75 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     // every copy has landed before the CTA can leave
     if (leader)
       for (int n = max(0, issued - ST); n < issued; ++n) mbar_wait_suspended(kv_full(n % ST), (n / ST) & 1, p.status);
-  } else if (warp == kMmaWarp) {
-    // -------------------------------------------------------------------- MMA --
+  } else if (warp == kScoreWarp) {
+    // ----------------------------------------------------------------- scores --
+    // S_i(j) = Q_i K(j)^T, step by step, the tiles in turn
     if (tc::elect_one()) {
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kTileRows, KT);
-      constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(kTileRows, D);
-      auto slot_full = [&](int n) { return mbar_wait_suspended(kv_full(n % ST), (n / ST) & 1, p.status); };
-      int n_scores = 0;                             // score MMAs issued
-      // S_i(j) = Q_i K(j)^T
-      auto mma_s = [&](int i, int j) {
-        const int n = 2 * (j - jlo), b = NBUF > 1 ? (j - lo[i]) & 1 : 0;
-        ok = ok && slot_full(n);
-        if (ok && j == lo[i]) ok = mbar_wait_suspended(q_full(i), 0, p.status);
-        // the shared score buffer: the scores before these are in registers
-        if (NT == 2 && ok && n_scores > 0) ok = mbar_wait_suspended(s_read, (n_scores - 1) & 1, p.status);
-        if (!ok) return;
-        ++n_scores;
-        tc::fence_after_sync();
-        const uint32_t d = tmem + s_col_of(b);
-        const uint64_t qd = tc::smem_desc_sw128(sb + i * C::kQBytes, 16, 1024);
-        const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffKv + (n % ST) * C::kKvBytes, 16, 1024);
+      int issued = 0;
+      for (int j = jlo; j < jhi && ok; ++j) {
+        const int n = 2 * (j - jlo), stage = n % ST;
+        ok = mbar_wait_suspended(kv_full(stage), (n / ST) & 1, p.status);
+        const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffKv + stage * C::kKvBytes, 16, 1024);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t bd = tc::desc_at(kd, (ks / 4) * KT * 128 + (ks % 4) * 32);
-          if constexpr (C::kQSmem)
-            tc::mma_f16(d, tc::desc_at(qd, (ks / 4) * kTileRows * 128 + (ks % 4) * 32), bd, idesc_s, ks > 0);
-          else
-            tc::mma_f16_ta(d, tmem + C::kQCol + 8 * ks, bd, idesc_s, ks > 0);
-        }
-        tc::commit(s_full(i, b));
-      };
-      // O_i += P_i(j) V(j)
-      auto mma_o = [&](int i, int j) {
-        const int n = 2 * (j - jlo) + 1, u = j - lo[i], b = NBUF > 1 ? u & 1 : 0;
-        ok = ok && mbar_wait_suspended(p_full(i, b), (u / NBUF) & 1, p.status);
-        ok = ok && slot_full(n);
-        if (ok && tail && j == jhi - 1) ok = mbar_wait_suspended(v_zeroed, 0, p.status);
-        if (!ok) return;
-        tc::fence_after_sync();
-        const uint64_t vd = tc::smem_desc_sw128(sb + C::kOffKv + (n % ST) * C::kKvBytes, KT * 128, 1024);
-#pragma unroll
-        for (int ks = 0; ks < KT / 16; ++ks)
-          tc::mma_f16_ta(tmem + C::kOCol + i * D, tmem + p_col_of(i, b) + 8 * ks, tc::desc_at(vd, ks * 2048), idesc_o,
-                         u > 0 || ks > 0);
-        tc::commit(pv_done(i));
-      };
-      auto release = [&](int n) {
-        if (ok) tc::commit(kv_empty(n % ST));
-      };
-      auto takes = [&](int i, int j) { return j >= lo[i] && j < hi[i]; };
-      if constexpr (NT == 2) {
-        for (int j = jlo; j <= jhi && ok; ++j) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            if (ok && takes(i, j)) mma_s(i, j);
-            if (ok && takes(i, j - 1)) mma_o(i, j - 1);
+        for (int i = 0; i < NT; ++i) {
+          if (!ok || j < lo[i] || j >= hi[i]) continue;
+          const int u = j - lo[i], b = NBUF > 1 ? u & 1 : 0;
+          if (u == 0) ok = mbar_wait_suspended(q_full(i), 0, p.status);
+          if (NT == 2) {                            // one buffer: the scores before these are in registers
+            if (ok && issued > 0) ok = mbar_wait_suspended(s_read, (issued - 1) & 1, p.status);
+          } else {                                  // two: the product that read this one's P is done
+            if (ok && u >= 2) ok = mbar_wait_suspended(s_free(b), ((u >> 1) - 1) & 1, p.status);
           }
-          if (j < jhi) release(2 * (j - jlo));      // K(j)
-          if (j > jlo) release(2 * (j - jlo) - 1);  // V(j - 1)
+          if (!ok) continue;
+          ++issued;
+          tc::fence_after_sync();
+          const uint32_t d = tmem + s_col_of(b);
+          const uint64_t qd = tc::smem_desc_sw128(sb + i * C::kQBytes, 16, 1024);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t bd = tc::desc_at(kd, (ks / 4) * KT * 128 + (ks % 4) * 32);
+            if constexpr (C::kQSmem)
+              tc::mma_f16(d, tc::desc_at(qd, (ks / 4) * kTileRows * 128 + (ks % 4) * 32), bd, idesc_s, ks > 0);
+            else
+              tc::mma_f16_ta(d, tmem + C::kQCol + 8 * ks, bd, idesc_s, ks > 0);
+          }
+          tc::commit(s_full(i, b));
         }
-      } else {
-        auto scores = [&](int j) {
-          if (!ok || j >= jhi) return;
-          mma_s(0, j);
-          release(2 * (j - jlo));
-        };
-        scores(jlo);
-        scores(jlo + 1);
-        for (int j = jlo; j < jhi && ok; ++j) {
-          mma_o(0, j);
-          release(2 * (j - jlo) + 1);
-          scores(j + 2);                            // behind the product that reads its buffer's P
-        }
+        if (ok) tc::commit(kv_empty(stage));
       }
-      // what was issued has completed before the CTA can leave
-      tc::commit(drained);
-      mbar_wait_suspended(drained, 0, p.status);
+      tc::commit(drained(0));                       // what was issued has completed before the CTA can leave
+      mbar_wait_suspended(drained(0), 0, p.status);
+    }
+    __syncwarp();
+  } else if (warp == kOutWarp) {
+    // --------------------------------------------------------------- products --
+    // O_i += P_i(j) V(j), from a thread of its own: neither kind of MMA waits for the other's operands
+    if (tc::elect_one()) {
+      constexpr uint32_t idesc_o = tc::idesc_f16_f32_bmn(kTileRows, D);
+      for (int j = jlo; j < jhi && ok; ++j) {
+        const int n = 2 * (j - jlo) + 1, stage = n % ST;
+        ok = mbar_wait_suspended(kv_full(stage), (n / ST) & 1, p.status);
+        if (ok && tail && j == jhi - 1) ok = mbar_wait_suspended(v_zeroed, 0, p.status);
+        const uint64_t vd = tc::smem_desc_sw128(sb + C::kOffKv + stage * C::kKvBytes, KT * 128, 1024);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          if (!ok || j < lo[i] || j >= hi[i]) continue;
+          const int u = j - lo[i], b = NBUF > 1 ? u & 1 : 0;
+          ok = mbar_wait_suspended(p_full(i, b), (u / NBUF) & 1, p.status);
+          if (!ok) continue;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int ks = 0; ks < KT / 16; ++ks)
+            tc::mma_f16_ta(tmem + C::kOCol + i * D, tmem + p_col_of(i, b) + 8 * ks, tc::desc_at(vd, ks * 2048), idesc_o,
+                           u > 0 || ks > 0);
+          if (NT == 1) tc::commit(s_free(b));
+          tc::commit(pv_done(i));
+        }
+        if (ok) tc::commit(kv_empty(stage));
+      }
+      tc::commit(drained(1));
+      mbar_wait_suspended(drained(1), 0, p.status);
     }
     __syncwarp();
   } else {
@@ -329,27 +349,27 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     uint64_t l = 0;                                 // two sums, of the even and the odd keys
     const uint32_t o_col = tmem + tlane + C::kOCol + i * D;
     if constexpr (!C::kQSmem) {
-      // the row of Q, fp16 pairs as they lie
-      const int head = kvh * p.group + rl % p.group;
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          p.q + (live ? static_cast<int64_t>(w.first + t) * p.q_stride + static_cast<int64_t>(head) * D : 0));
+      // the row of Q, fp16 pairs as they lie (row by row from memory this took 7,000 clocks)
+      ok = mbar_wait_suspended(q_landed(0), 0, p.status);
+      ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
       for (int c = 0; c < D / 2; c += 32) {
         uint32_t x[32];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint4 y = live ? src[c / 4 + e] : make_uint4(0, 0, 0, 0);
+          const uint4 y = lds128(sb + C::kOffQ + c / 32 * kTileRows * 128 + rl * 128 + ((e ^ (rl & 7)) * 16));
           x[4 * e] = y.x, x[4 * e + 1] = y.y, x[4 * e + 2] = y.z, x[4 * e + 3] = y.w;
         }
         tc::st_32x32b_x32(tmem + tlane + C::kQCol + c, x);
       }
       tc::wait_st();
       tc::fence_before_sync();
+      fence_proxy_async();                          // the ring's stages are the copies' again
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(i));
+      if (ok && lane == 0) mbar_arrive(q_full(i));
     }
 #pragma unroll 1
-    for (int u = 0; u < n_steps; ++u) {
+    for (int u = 0; u < n_steps && ok; ++u) {
       const int j = lo[i] + u, b = NBUF > 1 ? u & 1 : 0;
       const uint32_t s_col = tmem + tlane + s_col_of(b), p_col = tmem + tlane + p_col_of(i, b);
       ok = mbar_wait_suspended(s_full(i, b), (u / NBUF) & 1, p.status);
@@ -459,7 +479,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+  if (warp == kScoreWarp) tc::tmem_dealloc(tmem, 512);
 }
 
 // The driver's tensor-map encoder, looked up once (the library links the runtime only).
