@@ -314,6 +314,15 @@ def decode_attn_noalloc(cache: KVCache, q, page_table, seq_lens, max_seq_len: in
                                            _stream(stream)), "memra_decode_attn_noalloc")
 
 
+def _need_dense(where: str, *wanted) -> None:
+    """Refuse tensors that are not dense, not of the (dtype, shape) wanted, or not on the current device."""
+    import torch
+    device = torch._C._cuda_getDevice()
+    for t, dtype, shape in wanted:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+            raise MemraError(1, where)
+
+
 def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status=None, stream=None) -> None:
     """memra_prompt_attn: causal attention of packed prompts.
 
@@ -322,14 +331,15 @@ def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status
     int32 [B + 1]; out fp16 [tokens, Hq, D], dense.  status: a device int32
     the kernel ORs DEVERR_* bits into (KVCache.status will do).
     """
+    import torch
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    if k.shape != (T, Hkv, D) or v.shape != k.shape or out.shape != q.shape or not out.is_contiguous():
-        raise MemraError(1, "memra_prompt_attn")
+    _need_dense("memra_prompt_attn", (out, torch.float16, q.shape), (cu_seqlens, torch.int32, cu_seqlens.shape))
     strides = []
     for x in (q, k, v):
         s = x.stride()
-        if s[2] != 1 or (x.shape[1] > 1 and s[1] != D):
+        if (x.shape != (T, Hq if x is q else Hkv, D) or s[2] != 1 or (x.shape[1] > 1 and s[1] != D) or
+                x.dtype is not torch.float16 or x.get_device() != out.get_device()):
             raise MemraError(1, "memra_prompt_attn")
         strides.append(s[0] if T > 1 else x.shape[1] * D)
     _check(lib().memra_prompt_attn(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(cu_seqlens),
@@ -350,18 +360,24 @@ def tree_attn(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, tree_ma
     tree_mask int64 [B, N]: bit j of word [b, i] shows node j to node i; every
     node sees all keys before the tree.
     """
+    import torch
+    B = q.shape[0]
+    _need_dense("memra_tree_attn", (q, torch.float16, q.shape), (out, torch.float16, q.shape),
+                (page_table, torch.int32, (B, page_table.shape[1])), (seq_lens, torch.int32, (B,)),
+                (tree_mask, torch.int64, q.shape[:2]))
     a = _decode_args(cache, q, page_table, seq_lens, max_seq_len, out, workspace, sm_scale)
-    if tuple(tree_mask.shape) != tuple(q.shape[:2]):
-        raise MemraError(1, "memra_tree_attn")
     _check(lib().memra_tree_attn(*a[:6], _ptr(tree_mask), *a[6:], _stream(stream)), "memra_tree_attn")
 
 
 def kv_copy_pages(cache: KVCache, src_pages, dst_pages, n: int | None = None, stream=None) -> None:
     """memra_kv_copy_pages: page src_pages[i] -> dst_pages[i] in both pools; int32 [n] on the device, negative skips."""
+    import torch
+    most = src_pages.shape[0]
+    _need_dense("memra_kv_copy_pages", (src_pages, torch.int32, (most,)), (dst_pages, torch.int32, (most,)))
     if n is None:
-        n = int(src_pages.shape[0])
-        if int(dst_pages.shape[0]) != n:
-            raise MemraError(1, "memra_kv_copy_pages")
+        n = most
+    elif n > most:
+        raise MemraError(1, "memra_kv_copy_pages")
     _check(lib().memra_kv_copy_pages(cache.ref, _ptr(src_pages), _ptr(dst_pages), int(n), _stream(stream)),
            "memra_kv_copy_pages")
 
@@ -373,7 +389,10 @@ def kv_compact(cache: KVCache, page_table, seq_lens, max_seq_len: int, accepted,
     accepted int32 [B, max_accepted], n_accepted int32 [B]; seq_lens include
     the n_nodes rows of the tree.
     """
+    import torch
     B, most = accepted.shape
+    _need_dense("memra_kv_compact", (accepted, torch.int32, (B, most)), (n_accepted, torch.int32, (B,)),
+                (page_table, torch.int32, (B, page_table.shape[1])), (seq_lens, torch.int32, (B,)))
     _check(lib().memra_kv_compact(cache.ref, _ptr(page_table), int(page_table.shape[1]), _ptr(seq_lens),
                                   int(max_seq_len), _ptr(accepted), int(most), _ptr(n_accepted), int(B), int(n_nodes),
                                   _stream(stream)), "memra_kv_compact")

@@ -49,14 +49,16 @@ struct TreeCfg {
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
   static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
   static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
-  // q5_1's minima as 16 more columns of V^ (one per 32-dim block; the others zero), joined to O at the
-  // end: an exact d q + m in two fp16 parts costs ten operations a pair, d q alone three.  The MMA is at
-  // most 256 wide, so at head_dim 256 the pair it is.
+  // q5_1's d q + m as d (q - 16) and, in 16 more columns of V^, the blocks' centres m + 16 d (hi and lo
+  // parts; the others zero), joined to O at the end: an exact d q + m in two fp16 parts costs ten
+  // operations a pair, d (q - 16) three.  (Centres and not minima: the sums of d q and of m over a long
+  // context are large and nearly cancel, and the float32 accumulators lose what is left.)  The MMA is
+  // at most 256 wide, so at head_dim 256 the pair it is.
   static constexpr bool kMCols = VF == MEMRA_KV_Q5_1 && D == 128;
   static constexpr int kOCols = D + (D == 128 ? 16 : 0);
   static constexpr bool kVRows = VF != MEMRA_KV_NVFP4;          // V staged as token rows (MN-major)
   static constexpr uint32_t kTile = kTreeKeys * D * 2;
-  static constexpr uint32_t kLoOff = kTile + (kMCols ? kTreeKeys * 128 : 0);      // V: hi, minima, lo
+  static constexpr uint32_t kLoOff = kTile + (kMCols ? kTreeKeys * 128 : 0);      // V: hi, centres, lo
   static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kVLo ? kLoOff + kTile : kTile;
   static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
   // Q in tensor memory, but for the last 32 dims at head_dim 128 (two CTAs share its 512 columns:
@@ -209,8 +211,8 @@ __device__ __forceinline__ int page_tokens(uint32_t pmask, int pg, int valid) {
 // one block of KEYS rows per 64 dims: the MN-major B operand of O += P V.  A
 // lane holds 4 consecutive dims of 4 tokens, so nothing is transposed, and a
 // warp's 8-byte stores fill all banks.  Tokens that do not exist become zeros:
-// 0 * (what their bytes stand for) need not be 0.  q5_1 stages d q alone where
-// the minima have columns of their own (M_COLS), else d q + m by a TwoSum.
+// 0 * (what their bytes stand for) need not be 0.  q5_1 stages d (q - 16) where
+// the blocks' centres have columns of their own (M_COLS), else d q + m by a TwoSum.
 template <int D, int VF, int KEYS, int WARPS, bool M_COLS, uint32_t LO>
 __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int warp, int lane) {
   constexpr int NB = D / 32, SEG = v_seg_bytes(VF, D), B2 = D / 64;
@@ -277,9 +279,9 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
           const uint32_t p01 = __byte_perm(l4, h4, 0x5140), p23 = __byte_perm(l4, h4, 0x7362);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            // 1024 + q as fp16 for dims s = 0, 1; then q / 2 (q5_1) or (q - 8) / 2 (q4_0), exactly
+            // 1024 + q as fp16 for dims s = 0, 1; then q / 2 (q5_1), (q - 16) / 2 or (q - 8) / 2 (q4_0), exactly
             const uint32_t q2 = hfma2_u32(__byte_perm(k < 2 ? p01 : p23, 0x64646464u, k & 1 ? 0x4342 : 0x4140), 0x38003800u,
-                                          VF == MEMRA_KV_Q5_1 ? 0xE000E000u : 0xE008E008u);   // 0.5, -512 or -516
+                                          VF == MEMRA_KV_Q4_0 ? 0xE008E008u : M_COLS ? 0xE010E010u : 0xE000E000u);   // 0.5; -516, -520, -512
             const int f = k >> 1, p = k & 1;
             const uint32_t sel = f ? 0x3232 : 0x1010;
             const uint32_t d2 = __byte_perm(bp ? (p ? d4.w : d4.z) : (p ? d4.y : d4.x), 0, sel);
@@ -347,19 +349,29 @@ __device__ __forceinline__ void stage_v_nvfp4(uint32_t raw, uint32_t buf, uint32
   }
 }
 
-// The minima of q5_1 as columns of V^: a further 64-column block of which the
-// MMA takes 16, token n's minima of the D / 32 blocks in its first 16-byte unit.
+// The centres of q5_1's blocks, m / 2 + 8 d in hi + lo parts (a TwoSum; half the
+// value, as everything is staged), as columns of V^: a further 64-column block of
+// which the MMA takes 16, token n's hi and then lo parts of the four blocks in
+// its first 16-byte unit.
 template <int D, int KEYS>
 __device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int n) {
   constexpr int NB = D / 32, SEG = v_seg_bytes(MEMRA_KV_Q5_1, D);
-  static_assert(NB == 4, "8 bytes of minima");
+  static_assert(NB == 4, "8 bytes of each part");
   const int pg = n / kPage, t = n % kPage;
-  const uint32_t at = raw + pg * SEG + 11 * D + (((t & 7) >> 1) * NB * 4 + 2 * (t >> 3) + (t & 1)) * 2;
-  uint32_t m[NB];
+  const uint32_t at = raw + pg * SEG + 10 * D + (((t & 7) >> 1) * NB * 4 + 2 * (t >> 3) + (t & 1)) * 2;
+  uint32_t hi[2], lo[2];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) m[b] = lds16(at + 8 * b);
+  for (int e = 0; e < 2; ++e) {            // two blocks at a time
+    const __half2 d = bits_h2(lds16(at + 16 * e) | (lds16(at + 16 * e + 8) << 16));
+    const __half2 m = bits_h2(lds16(at + D + 16 * e) | (lds16(at + D + 16 * e + 8) << 16));
+    const __half2 a = __hmul2_rn(m, __float2half2_rn(0.5f)), b = __hmul2_rn(d, __float2half2_rn(8.f));
+    const __half2 s = __hadd2_rn(a, b), bb = __hsub2_rn(s, a);
+    hi[e] = h2_bits(s);
+    lo[e] = h2_bits(__hadd2_rn(__hsub2_rn(a, __hsub2_rn(s, bb)), __hsub2_rn(b, bb)));
+  }
   const bool live = t < page_tokens(pmask, pg, valid);
-  sts64(buf + n * 128 + ((n & 7) << 4), live ? m[0] | (m[1] << 16) : 0u, live ? m[2] | (m[3] << 16) : 0u);
+  const uint4 x = live ? make_uint4(hi[0], hi[1], lo[0], lo[1]) : make_uint4(0, 0, 0, 0);
+  sts128(buf + n * 128 + ((n & 7) << 4), x);
 }
 
 // Sequence length as the kernels use it.
@@ -380,7 +392,8 @@ __device__ __forceinline__ TreeItem find_item(const TreeParams &p, int index, in
     int total = tree_ceil(tree_len(p, first), kTreeKeys);
     for (int b = 32 + lane; b < p.batch; b += 32) total += tree_ceil(tree_len(p, p.seq_lens[b]), kTreeKeys);
     total = __reduce_add_sync(0xffffffffu, total);
-    it.C = min(max(tree_ceil(total, p.slots), kTreeMinChunks), kTreeMaxChunks);
+    const int waves = tree_ceil(tree_ceil(total, p.slots), kTreeMaxChunks);
+    it.C = min(max(tree_ceil(total, p.slots * max(waves, 1)), kTreeMinChunks), kTreeMaxChunks);
   }
   int start = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -615,7 +628,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- staging --
     const int sw = warp - 4;
-    if constexpr (C::kMCols) {               // the unused columns of the minima's block, once
+    if constexpr (C::kMCols) {               // the unused columns of the centres' block, once
       for (uint32_t i = tid - 128; i < KT * 8u; i += 32 * SW)
         sts128(sb + C::kOffV + C::kTile + 16 * i, make_uint4(0, 0, 0, 0));
       named_barrier_sync(1, 32 * SW);
@@ -765,7 +778,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
     ok = __all_sync(0xffffffffu, ok);
     tc::fence_after_sync();
     const float inv = l > 0.f ? p.v_post / l : 0.f;
-    uint32_t ms[16];                         // the minima's sums, per 32-dim block; a half as the staged values are
+    uint32_t ms[16];                         // the centres' sums, per 32-dim block: hi parts, lo parts
     if constexpr (C::kMCols) {
       tc::ld_32x32b_x16(o_col + D, ms);
       tc::wait_ld(ms);
@@ -777,10 +790,10 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       uint32_t o[16];
       tc::ld_32x32b_x16(o_col + c, o);
       tc::wait_ld(o);
-      const float half_m = C::kMCols ? 0.5f * __uint_as_float(ms[c / 32]) : 0.f;
+      const float centre = C::kMCols ? __uint_as_float(ms[c / 32]) + __uint_as_float(ms[4 + c / 32]) : 0.f;
       float x[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = l > 0.f ? (__uint_as_float(o[e]) + half_m) * inv : 0.f;
+      for (int e = 0; e < 16; ++e) x[e] = l > 0.f ? (__uint_as_float(o[e]) + centre) * inv : 0.f;
       if (ns == 1) {
 #pragma unroll
         for (int e = 0; e < 16; e += 8)
@@ -916,12 +929,12 @@ cudaError_t launch_one(const TreeParams &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready[dev] = true;
   }
-  // Items of the call at most: one wave's worth and one more per sequence, or
-  // where kTreeMaxChunks cuts shorter, that many; and no sequence has more than
-  // the longest can have.
-  const int64_t chunks = tree_ceil(p.max_seq_len, kTreeKeys);
+  // Items of the call at most: the waves' worth and one more per sequence; and
+  // no sequence has more than the longest can have.
+  const int64_t chunks = p.batch * static_cast<int64_t>(tree_ceil(p.max_seq_len, kTreeKeys));
+  const int64_t per_wave = static_cast<int64_t>(std::max(p.slots, 1)) * kTreeMaxChunks;
   const int64_t items = std::min<int64_t>(
-      p.batch + std::max<int64_t>(p.slots, (p.batch * chunks + kTreeMaxChunks - 1) / kTreeMaxChunks),
+      p.batch + std::max(p.slots, 1) * std::max<int64_t>((chunks + per_wave - 1) / per_wave, 1),
       static_cast<int64_t>(p.batch) * std::max(1, p.max_splits));
   const int64_t ctas = items * p.n_kv_heads * p.row_tiles;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;

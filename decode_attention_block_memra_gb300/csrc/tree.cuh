@@ -17,14 +17,17 @@ constexpr int kTreeKeys = 64;
 __host__ __device__ constexpr int tree_ctas_per_sm(int D) { return D == 128 ? 2 : 1; }
 
 // The split plan.  A call's keys, in chunks of kTreeKeys, are cut so that one
-// wave of the GPU holds all CTAs: C = ceil(chunks of all sequences x KV heads x
-// row tiles / slots) chunks each, at least kTreeMinChunks (below it a CTA's fixed
-// costs, about three chunks' time, weigh more than the split gains) and at most
-// kTreeMaxChunks (page ids in shared memory); a sequence's splits are made equal.
+// wave of the GPU (or as few whole waves as kTreeMaxChunks allows) holds all
+// CTAs: C = ceil(chunks of all sequences x KV heads x row tiles / slots) chunks
+// each, at least kTreeMinChunks (below it a CTA's fixed costs, about three
+// chunks' time, weigh more than the split gains) and at most kTreeMaxChunks: the
+// tensor cores cut the float32 sums at every step, and over 13,824 keys in one
+// split what was lost came to a quarter of the output's own rounding; a
+// sequence's splits are made equal.
 // It depends on the lengths of all sequences of the call: a row's partial sums
 // are grouped differently in another batch, and its last bits may differ.
 constexpr int kTreeMinChunks = 4;
-constexpr int kTreeMaxChunks = 240;
+constexpr int kTreeMaxChunks = 120;
 constexpr int kTreeSplitPages = kTreeMaxChunks * kTreeKeys / kPage;
 // Most splits of a sequence, unless kTreeMaxChunks makes more.
 constexpr int kTreeMaxSplits = 160;

@@ -351,7 +351,8 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
  *                 all keys before the tree.
  *   n_nodes       1 .. MEMRA_MAX_TREE_NODES.  A sequence with fewer nodes pads
  *                 its tree with rows that no word names.
- *   workspace     device, >= memra_tree_attn_workspace_bytes(...) bytes
+ *   workspace     device, >= memra_tree_attn_workspace_bytes(...) bytes; calls
+ *                 that may overlap on the GPU need one each
  *   out           device fp16 [batch][n_nodes][n_heads][head_dim]
  * All K and V formats, head_dim 128 or 256, n_heads / n_kv_heads <=
  * MEMRA_MAX_GROUP, batch <= 65535, n_kv_heads * ceil(n_nodes * n_heads /

@@ -160,3 +160,35 @@ def build_pools(w, cache=None, fill=None, rows=None):
         layout.write_rows(kp, "k", quant.select_rows(cache["k"][h], idx), w.slots[idx], h, D)
         layout.write_rows(vp, "v", quant.select_rows(cache["v"][h], idx), w.slots[idx], h, D)
     return kp, vp
+
+
+def masked_rows(q: np.ndarray, k: np.ndarray, v: np.ndarray, sees: np.ndarray, sm_scale: float) -> np.ndarray:
+    """q [R, Hq, D], k / v [T, Hkv, D], sees bool [R, T] -> out [R, Hq, D] float64; rows that see nothing are zeros.
+
+    The definition with an arbitrary mask, for prompts (causal, perhaps a band) and draft trees.
+    """
+    q, k, v = (np.asarray(x, dtype=np.float64) for x in (q, k, v))
+    R, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    out = np.zeros((R, Hq, D))
+    for h in range(Hq):
+        s = np.where(sees, q[:, h] @ k[:, h // G].T * sm_scale, -np.inf)
+        top = s.max(axis=1, keepdims=True)
+        p = np.exp(s - np.where(np.isfinite(top), top, 0.0))
+        mass = p.sum(axis=1, keepdims=True)
+        out[:, h] = np.divide(p, mass, out=np.zeros_like(p), where=mass > 0) @ v[:, h // G]
+    return out
+
+
+def prompt_sees(n: int, window: int = 0) -> np.ndarray:
+    """bool [n, n]: token t sees tokens max(0, t - window + 1) .. t (window 0: 0 .. t)."""
+    at = np.arange(n)
+    sees = at[None, :] <= at[:, None]
+    return sees & (at[None, :] > at[:, None] - window) if window else sees
+
+
+def tree_sees(words, context: int) -> np.ndarray:
+    """bool [N, context + N]: every node sees the context, node i sees node j iff bit j of words[i] is set."""
+    n = len(words)
+    bits = np.array([[int(w) >> j & 1 for j in range(n)] for w in words], dtype=bool).reshape(n, n)
+    return np.concatenate([np.ones((n, context), bool), bits], axis=1)

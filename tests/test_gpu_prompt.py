@@ -177,6 +177,22 @@ def test_bad_lengths_are_clamped_and_flagged(memra):
         status.zero_()
 
 
+def test_rows_past_32_bit_offsets(memra):
+    # 70,000 tokens x 128 heads x 256: the last sequences' rows start past 2^31 elements
+    n, Hq, D, lens = 70_000, 128, 256, [70] * 1000
+    g = torch.Generator(device="cuda").manual_seed(13)
+    q = torch.empty(n, Hq, D, dtype=torch.float16, device="cuda")
+    q.normal_(generator=g)
+    k, v = (torch.randn(n, 1, D, device="cuda", generator=g).half() for _ in range(2))
+    out = torch.empty_like(q)
+    cu = torch.arange(0, n + 1, 70, dtype=torch.int32, device="cuda")
+    memra.prompt_attn(q, k, v, cu, out)
+    for b in (0, 500, 999):
+        sl = slice(70 * b, 70 * b + 70)
+        want, tol = reference(q[sl], k[sl], v[sl])
+        assert bool(((out[sl].double() - want).abs() <= tol).all())
+
+
 def test_captured_call_reads_new_lengths(memra):
     q, k, v, cu, out = check(memra, [90, 38], 8, 2, 128, seed=11)
     first = out.clone()
@@ -212,6 +228,8 @@ def test_binding_refuses_other_layouts(memra):
     k = torch.zeros(4, 2, 128, device="cuda").half()
     cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
     bad = torch.zeros(4, 128, 8, device="cuda").half().transpose(1, 2)
-    for args in ((bad, k, k, cu, q), (q, k[:3], k, cu, q), (q, k, k[:, :1], cu, q), (q, k, k, cu, bad)):
+    for args in ((bad, k, k, cu, q), (q, k[:3], k, cu, q), (q, k, k[:, :1], cu, q), (q, k, k, cu, bad),
+                 (q.float(), k, k, cu, q), (q, k.cpu(), k, cu, q), (q, k, k, cu.long(), q), (q, k, k, cu.cpu(), q),
+                 (q, k, k, cu, q.bfloat16())):
         with pytest.raises(memra.MemraError):
             memra.prompt_attn(*args)

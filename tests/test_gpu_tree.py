@@ -126,7 +126,7 @@ def test_formats(memra, kf, vf, D):
 @pytest.mark.parametrize("nodes,n_heads,n_kv_heads", [
     (1, 8, 2), (2, 4, 4), (16, 32, 4), (17, 32, 4),      # 128 rows, then two tiles
     (33, 16, 2), (64, 8, 2), (64, 16, 2),                # 264, 256 and 512 rows of a KV head
-    (5, 6, 2), (13, 10, 2), (64, 3, 3), (3, 128, 1), (64, 12, 1)])
+    (5, 6, 2), (13, 10, 2), (64, 3, 3), (3, 128, 1), (64, 12, 1), (64, 128, 1)])
 def test_shapes(memra, nodes, n_heads, n_kv_heads, D):
     w = W.random_case(nodes * 7 + n_heads, batch=2, q_len=nodes, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=D,
                       ctx=(nodes, 700))
@@ -177,7 +177,7 @@ def test_many_splits(memra, D, lens):
 
 
 def test_splits_at_their_largest(memra):
-    # 16 KV heads x 16 row tiles leave a wave one split: more than 15,360 keys make two
+    # 16 KV heads x 16 row tiles leave a wave one split: more than 2 x 7,680 keys make three
     w = W.make_workload("wide", batch=1, q_len=64, n_heads=16 * 32, n_kv_heads=16, head_dim=128, k_fmt="fp8",
                         v_fmt="fp8", seed=8, seq_lens=[8192 + 8192 + 70])
     words = words_for(w, 4)
@@ -192,6 +192,26 @@ def test_splits_at_their_largest(memra):
         one.k_rows, one.v_rows = w.k_rows[:, h:h + 1], w.v_rows[:, h:h + 1]
         want, tol = reference(one, words)
         assert (np.abs(got[:, :, 32 * h:32 * h + 32] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("kf,vf", [("q8_0", "q5_1"), ("fp8", "q4_0"), ("nvfp4", "nvfp4")])
+def test_long_sums_keep_their_precision(memra, kf, vf):
+    """Means over 15,000 keys in one split are a hundredth of the values: what nearly cancels in the sums
+    must not cost precision.  Relative in the 2-norm the output's rounding and the weights' (independent of
+    the values' signs) are at most u each."""
+    w = W.make_workload("long_sums", batch=1, q_len=64, n_heads=16 * 32, n_kv_heads=16, head_dim=128, k_fmt=kf,
+                        v_fmt=vf, seed=19, seq_lens=[15_000])
+    w.q = (w.q.astype(np.float32) * 0.5).astype(np.float16)
+    words = words_for(w, 19)
+    dw, _ = run(memra, w, words)
+    assert memra.read_status(dw.cache) == 0
+    got = dw.out.cpu().numpy().astype(np.float64)
+    one = W.Workload(**{**w.__dict__})
+    one.n_heads, one.n_kv_heads = 32, 1
+    one.q, one.k_rows, one.v_rows = w.q[:, :, 64:96], w.k_rows[:, 2:3], w.v_rows[:, 2:3]
+    want, _ = reference(one, words)
+    err = np.linalg.norm(got[:, :, 64:96] - want) / np.linalg.norm(want)
+    assert err <= 2 * U, err
 
 
 @pytest.mark.parametrize("D", [128, 256])
@@ -245,6 +265,49 @@ def test_bad_pages_are_left_out(memra):
     assert memra.read_status(dw.cache) == memra.DEVERR_BAD_PAGE
     want, tol = reference(w, words, missing_pages=(3, 5))
     assert (np.abs(dw.out.cpu().numpy().astype(np.float64) - want) <= tol).all()
+
+
+def test_pages_past_32_bit_offsets(memra):
+    # 8 KV heads: page 250,000 of q8_0 K starts past 4 GiB
+    w = W.random_case(17, batch=2, q_len=4, n_heads=16, n_kv_heads=8, ctx=(100, 300))
+    high = 250_000 - w.num_pages
+    w.page_table = (w.page_table + high).astype(np.int32)
+    w.slots = (w.slots + 16 * high).astype(np.int32)
+    w.num_pages = 250_000
+    from decode_attention_block_memra_gb300.runner import upload
+    dw = upload(w)
+    memra.kv_append(dw.cache, dw.step_k, dw.step_v, dw.step_slots)
+    words = words_for(w, 17)
+    mask = torch.from_numpy(words.view(np.int64).copy()).cuda()
+    ws = torch.empty(memra.tree_attn_workspace_bytes(2, 4, 16, 128, w.max_seq_len), dtype=torch.uint8, device="cuda")
+    memra.tree_attn(dw.cache, dw.q, dw.page_table, dw.seq_lens, w.max_seq_len, mask, dw.out, ws, w.sm_scale)
+    assert memra.read_status(dw.cache) == 0
+    want, tol = reference(w, words)
+    assert (np.abs(dw.out.cpu().numpy().astype(np.float64) - want) <= tol).all()
+    kept = torch.tensor([[1, 3]] * 2, dtype=torch.int32, device="cuda")
+    pool = dw.cache.k_pool.view(w.num_pages, 8, -1)
+    before = pool[high:].clone()
+    memra.kv_compact(dw.cache, dw.page_table, dw.seq_lens, w.max_seq_len, kept,
+                     torch.full((2,), 2, dtype=torch.int32, device="cuda"), 4)
+    assert memra.read_status(dw.cache) == 0
+    assert not torch.equal(pool[high:], before) and not bool(pool[:high].any())
+
+
+def test_binding_refuses_other_tensors(memra):
+    w = W.random_case(18, batch=2, q_len=4, n_heads=8, n_kv_heads=2, ctx=(40, 60))
+    dw, args = run(memra, w, words_for(w, 18))
+    cache, q, table, lens, M, mask, out, ws, scale = args
+    for bad in ((cache, q.float(), table, lens, M, mask, out, ws), (cache, q, table[:1], lens, M, mask, out, ws),
+                (cache, q, table, lens.long(), M, mask, out, ws), (cache, q, table, lens, M, mask.int(), out, ws),
+                (cache, q, table, lens, M, mask[:, :3], out, ws), (cache, q, table.cpu(), lens, M, mask, out, ws),
+                (cache, q, table, lens, M, mask, out[:1], ws), (cache, q.transpose(1, 2), table, lens, M, mask, out, ws)):
+        with pytest.raises(memra.MemraError):
+            memra.tree_attn(*bad)
+    kept, count = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for bad in ((table[:1], lens, M, kept, count), (table, lens[:1], M, kept, count), (table, lens, M, kept.long(), count),
+                (table, lens, M, kept, count[:1]), (table, lens, M, kept.cpu(), count)):
+        with pytest.raises(memra.MemraError):
+            memra.kv_compact(cache, *bad, 4)
 
 
 def test_lengths_out_of_range(memra):
