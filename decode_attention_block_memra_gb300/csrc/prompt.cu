@@ -28,6 +28,11 @@
 // more than kLazy (log2 units), so O in tensor memory is rescaled rarely; P
 // then stays <= 2^kLazy.  Scores, maxima, sums and O are float32; P is rounded
 // to fp16 (relative 2^-11 a weight), the operand type of the tensor cores.
+// What bounds it: the tensor cores.  16,384 tokens, 32/4 heads, D 128: 1.47 ms a
+// call in a loop (1,500 TFLOP/s, the power cap on), 1.28 ms for a single one, the
+// tensor pipe active 77% of the time; 8 ragged prompts of up to 4,860 tokens 510 us
+// (1,283 TFLOP/s); 9,713 tokens, 16/2 heads, D 256, window 1,024: 148 us (940
+// TFLOP/s, 17 steps a CTA); 256 tokens, 8/2 heads: 8.5 us, all latency.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
