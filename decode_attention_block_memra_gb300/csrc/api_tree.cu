@@ -46,9 +46,10 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
     return MEMRA_ERR_UNSUPPORTED;
   if (!std::isfinite(sm_scale)) return MEMRA_ERR_INVALID_ARG;
   const int group = n_heads / n_kv_heads, rows = n_nodes * group;
-  const int row_tiles = static_cast<int>(ceil_div(rows, 128));
+  const int tiles = tree_tiles(head_dim, rows);
+  const int row_ctas = static_cast<int>(ceil_div(rows, 128 * tiles));
   const int64_t all_rows = static_cast<int64_t>(batch) * n_nodes * n_heads;
-  if (static_cast<int64_t>(n_kv_heads) * row_tiles > 65535 || batch > 65535 || all_rows > INT32_MAX)
+  if (static_cast<int64_t>(n_kv_heads) * row_ctas > 65535 || batch > 65535 || all_rows > INT32_MAX)
     return MEMRA_ERR_UNSUPPORTED;
   if (batch == 0) return MEMRA_OK;
   if (!q || !page_table || !seq_lens || !tree_mask || !out || !aligned16(q) || !aligned16(out) ||
@@ -83,10 +84,10 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   p.len_limit = static_cast<int32_t>(std::min<int64_t>(max_seq_len, static_cast<int64_t>(max_pages_per_seq) * kPage));
   // Where the sequences alone fill the GPU four times over, none is cut for its sake (and no CTA adds
   // up the lengths of so many).
-  p.slots = std::max(1, device_sms() * tree_ctas_per_sm(head_dim) / (n_kv_heads * row_tiles));
+  p.slots = std::max(1, device_sms() * tree_ctas_per_sm(head_dim, tiles) / (n_kv_heads * row_ctas));
   if (batch >= 4 * p.slots) p.slots = 0;
   p.max_splits = tree_max_splits(max_seq_len);
-  p.row_tiles = row_tiles;
+  p.row_ctas = row_ctas;
   // staged values: q8_0 / q5_1 / q4_0 at half size, fp8 / NVFP4 without their tensor scale
   p.scale_log2 = std::fabs(sm_scale) * (cache->k_fmt == MEMRA_KV_Q8_0 ? 2.f : cache->k_scale) * 1.4426950408889634f;
   p.q_and = p.scale_log2 == 0.f ? 0u : 0xFFFFFFFFu;

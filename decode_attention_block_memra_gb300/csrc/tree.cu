@@ -6,7 +6,7 @@
 //
 // The rows of one KV head, nodes x the group's query heads, 128 to a tile, are
 // the M side of tcgen05 MMAs, so a page is read and dequantized once for 128 of
-// them.  CTA = (split of the keys, KV head, sequence and row tile):
+// them (256 at head_dim 128).  CTA = (split of the keys, KV head, sequence, its rows):
 //   * a copy warp brings raw pages into a ring of two to four chunks (64 keys);
 //   * staging warps dequantize a chunk into fp16 operand tiles: exact hi + lo
 //     pairs for q8_0, q5_1 and q4_0, single values for fp8 and NVFP4, so only P
@@ -14,16 +14,17 @@
 //   * one MMA thread: S = Q K^T with Q in tensor memory, O += P V with P in
 //     tensor memory over its scores; the A operands stay out of shared memory,
 //     whose bandwidth the staged tiles need;
-//   * four softmax warps, thread = row.
-// head_dim 128: two CTAs share an SM (256 tensor-memory columns each, one score
-// buffer), so one's chain of copy, staging, MMA and softmax fills the other's
-// gaps, its first and last steps included.  head_dim 256: one CTA with two score
+//   * four softmax warps a row tile, thread = row.
+// head_dim 128, up to 128 rows: two CTAs share an SM (256 tensor-memory columns
+// each, one score buffer), so one's chain of copy, staging, MMA and softmax fills
+// the other's gaps, its first and last steps included; more rows: one CTA with two
+// row tiles, which fill each other's gaps.  head_dim 256: one CTA with two score
 // buffers, the scores a chunk ahead.
 // What bounds it is the staging: a chunk of q8_0/q5_1 costs 4,900 warp
 // instructions, 70% of the issue slots of the 1,750 clocks it takes an SM, against
 // 1,060 clocks of MMAs.  8 sequences x 16 nodes over 6,316 keys (32/4 heads, D 128,
 // q8_0/q5_1): 38.8 us a call, 7 of them the merge, for 47 MB of pages; 64 nodes over
-// 262,144 keys: 446 us; 31 nodes on 12 ragged sequences, D 256, fp8: 97.5 us.
+// 262,144 keys: 363 us; 31 nodes on 12 ragged sequences, D 256, fp8: 97.5 us.
 // A sequence of one split writes its rows directly; the others leave (o, lse)
 // partials that tree_merge_kernel joins.
 #include <cuda_fp16.h>
@@ -43,13 +44,13 @@ namespace {
 constexpr int kTileRows = 128;
 constexpr float kLazy = 8.f;               // log2 units: P stays <= 256 between rescales
 
-template <int D, int KF, int VF>
+template <int D, int KF, int VF, int MT>
 struct TreeCfg {
-  static constexpr int kCtas = tree_ctas_per_sm(D);
-  static constexpr int kStageWarps = D == 128 ? 4 : 8;
-  static constexpr int kMmaWarp = 4 + kStageWarps, kCopyWarp = kMmaWarp + 1, kThreads = 32 * (kCopyWarp + 1);
+  static constexpr int kCtas = tree_ctas_per_sm(D, MT);
+  static constexpr int kStageWarps = kCtas == 2 ? 4 : 8, kStageWarp0 = 4 * MT;
+  static constexpr int kMmaWarp = kStageWarp0 + kStageWarps, kCopyWarp = kMmaWarp + 1, kThreads = 32 * (kCopyWarp + 1);
   static constexpr int kPages = kTreeKeys / kPage;
-  static constexpr int kBufs = D == 128 ? 1 : 2;                // score buffers
+  static constexpr int kBufs = D == 128 ? 1 : 2;                // score buffers of a row tile
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
   static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
   static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
@@ -65,32 +66,34 @@ struct TreeCfg {
   static constexpr uint32_t kLoOff = kTile + (kMCols ? kTreeKeys * 128 : 0);      // V: hi, centres, lo
   static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kVLo ? kLoOff + kTile : kTile;
   static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
-  // Q in tensor memory, but for the last 32 dims at head_dim 128 (two CTAs share its 512 columns:
+  // Q in tensor memory, but for the last 32 dims at head_dim 128 (two row tiles share its 512 columns,
   // 48 of Q, 144 of O, 64 of scores each), which lie in shared memory
   static constexpr int kQTmem = D == 128 ? 96 : D, kQSmem = D - kQTmem;
-  // V^ tiles: two in turn where a tile is no pair, so that staging runs ahead of the product
-  static constexpr int kVBufs = kVLo ? 1 : 2;
+  // Operand tiles in turn, so that staging runs ahead of the MMAs: two V^ tiles where they are no pairs,
+  // two of each in a CTA of two row tiles (two CTAs on an SM run ahead of each other).
+  static constexpr int kKBufs = MT == 2 ? 2 : 1, kVBufs = MT == 2 || !kVLo ? 2 : 1;
   // barriers and page ids, then K^ and V^ tiles, Q's last dims and the raw chunks; the output rows reuse
   // everything behind the page ids
   static constexpr uint32_t kOffBar = 0, kOffPid = 256, kOffK = 4096;
-  static constexpr uint32_t kOffV = kOffK + kKBuf, kOffQ = kOffV + kVBufs * kVBuf;
-  static constexpr uint32_t kOffRaw = kOffQ + kTileRows * kQSmem * 2;
+  static constexpr uint32_t kOffV = kOffK + kKBufs * kKBuf, kOffQ = kOffV + kVBufs * kVBuf;
+  static constexpr uint32_t kOffRaw = kOffQ + MT * kTileRows * kQSmem * 2;
   // chunks of raw pages in flight: as many as fit, four at most
   static constexpr uint32_t kRoom = (kCtas == 2 ? 113 : 227) * 1024;
   static constexpr int kRaw = (kRoom - kOffRaw) / kRawBytes < 4 ? (kRoom - kOffRaw) / kRawBytes : 4;
   static constexpr uint32_t kEnd = kOffRaw + kRaw * kRawBytes;
   static constexpr uint32_t kRowBytes = D * 4 + 16;             // padded output row
-  static constexpr uint32_t kEndRows = kOffK + kTileRows * kRowBytes;
+  static constexpr uint32_t kEndRows = kOffK + MT * kTileRows * kRowBytes;
   // Tensor memory: a CTA that found its columns taken would wait in its
   // allocation, so shared memory is sized that no more CTAs of this or the
   // library's other tensor-memory kernels fit an SM than its 512 columns hold.
-  static constexpr uint32_t kTCols = D == 128 ? 256 : 512;
-  static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows, kFloor = (D == 128 ? 78 : 150) * 1024;
+  static constexpr uint32_t kTCols = 512 / kCtas;
+  static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows, kFloor = (kCtas == 2 ? 78 : 150) * 1024;
   static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
-  static constexpr uint32_t kQCol = 0, kOCol = kQTmem / 2, kSCol = kOCol + kOCols;   // tensor-memory columns
+  // tensor-memory columns: Q, O, scores, those of the second row tile behind those of the first
+  static constexpr uint32_t kQCol = 0, kOCol = MT * kQTmem / 2, kSCol = kOCol + MT * kOCols;
   static_assert(kOffPid + 4 * kTreeSplitPages <= kOffK && kRaw >= 2, "page ids; a chunk ahead");
   static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 232448, "shared memory");
-  static_assert(kSCol + kBufs * kTreeKeys <= static_cast<int>(kTCols) && kCtas * kTCols <= 512, "tensor memory");
+  static_assert(kSCol + MT * kBufs * kTreeKeys <= static_cast<int>(kTCols) && kCtas * kTCols <= 512, "tensor memory");
   static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
 };
 
@@ -426,10 +429,10 @@ __device__ __forceinline__ TreeItem find_item(const TreeParams &p, int index, in
   return it;
 }
 
-template <int D, int KF, int VF>
-__global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, VF>::kCtas)
+template <int D, int KF, int VF, int MT>
+__global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, KF, VF, MT>::kCtas)
     tree_kernel(const TreeParams p) {
-  using C = TreeCfg<D, KF, VF>;
+  using C = TreeCfg<D, KF, VF, MT>;
   constexpr int KT = kTreeKeys, NP = C::kPages, NBUF = C::kBufs, RAW = C::kRaw, SW = C::kStageWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_addr(smem);
@@ -439,16 +442,18 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
   auto raw_empty = [&](int s) { return bars + 8 * (RAW + s); };
   enum { kKFull = 0, kKEmpty, kVFull, kVEmpty, kSFull, kPFull };
   auto bar = [&](int kind, int b) { return bars + 8 * (2 * RAW + 2 * kind + b); };
-  const uint32_t pv_done = bars + 8 * (2 * RAW + 12), drained = pv_done + 8, q_ready = drained + 8;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * (2 * RAW + 15));
+  auto pv_done = [&](int i) { return bars + 8 * (2 * RAW + 12 + i); };
+  auto q_ready = [&](int i) { return bars + 8 * (2 * RAW + 14 + i); };
+  const uint32_t drained = bars + 8 * (2 * RAW + 16);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * (2 * RAW + 17));
   int *pid_s = reinterpret_cast<int *>(smem + C::kOffPid);
 
   grid_dependency_wait();
   allow_dependent_launch();
   // Items outermost: the CTAs past the last item come last, so that the others
   // fill the SMs evenly, and those of one split's pages run side by side.
-  const int side = p.n_kv_heads * p.row_tiles, index = blockIdx.x / side;
-  const int kvh = blockIdx.x % side / p.row_tiles, r0 = blockIdx.x % p.row_tiles * kTileRows;
+  const int side = p.n_kv_heads * p.row_ctas, index = blockIdx.x / side;
+  const int kvh = blockIdx.x % side / p.row_ctas, r0 = blockIdx.x % p.row_ctas * (MT * kTileRows);
   const int rows = p.n_nodes * p.group;
   // This CTA's sequence and split: items are numbered sequence by sequence
   // (one at least each).  Every warp finds it for itself.
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
     return (static_cast<size_t>(b) * p.n_nodes + r / p.group) * p.n_heads + kvh * p.group + r % p.group;
   };
   if (T <= 0) {                              // no key at all: zeros
-    for (int i = tid; i < min(kTileRows, rows - r0) * (D / 8); i += C::kThreads)
+    for (int i = tid; i < min(MT * kTileRows, rows - r0) * (D / 8); i += C::kThreads)
       *reinterpret_cast<uint4 *>(p.out + row_id(r0 + i / (D / 8)) * D + 8 * (i % (D / 8))) = make_uint4(0, 0, 0, 0);
     return;
   }
@@ -514,9 +519,11 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
         mbar_init(bar(kSFull, k), 1);
         mbar_init(bar(kPFull, k), 4);
       }
-      mbar_init(pv_done, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(pv_done(i), 1);
+        mbar_init(q_ready(i), 4);
+      }
       mbar_init(drained, 1);
-      mbar_init(q_ready, 4);
       fence_barrier_init();
     }
     __syncwarp();
@@ -577,38 +584,42 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       auto wait = [&](int kind, int k, int phase) {
         ok = ok && mbar_wait_suspended(bar(kind, k), phase & 1, p.status);
       };
-      // S(ci) = Q K^T
-      auto mma_s = [&](int ci) {
+      // Score buffer and barrier of tile i at chunk ci, and which use of it that is.
+      auto buf = [](int i, int ci) { return MT == 2 ? i : ci % NBUF; };
+      // S_i(ci) = Q_i K^T
+      auto mma_s = [&](int i, int ci) {
         if (!ok || ci >= n_chunks) return;
-        const int sbuf = ci % NBUF;
-        wait(kKFull, 0, ci);
+        const int kb = ci % C::kKBufs, sk = buf(i, ci);
+        wait(kKFull, kb, ci / C::kKBufs);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t d = tmem + C::kSCol + sbuf * KT;
-        const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffK, 16, 1024);
-        const uint64_t qd = tc::smem_desc(sb + C::kOffQ, 128, C::kQSmem / 8 * 128);
+        const uint32_t d = tmem + C::kSCol + sk * KT;
+        const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffK + kb * C::kKBuf, 16, 1024);
+        const uint64_t qd = tc::smem_desc(sb + C::kOffQ + i * kTileRows * C::kQSmem * 2, 128, C::kQSmem / 8 * 128);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
           for (int lo = 0; lo < (C::kKLo ? 2 : 1); ++lo) {
             const uint64_t bd = tc::desc_at(kd, (ks / 4) * KT * 128 + (ks % 4) * 32 + lo * C::kTile);
             if (16 * ks < C::kQTmem)
-              tc::mma_f16_ta(d, tmem + C::kQCol + 8 * ks, bd, idesc_s, ks + lo > 0);
+              tc::mma_f16_ta(d, tmem + C::kQCol + i * (C::kQTmem / 2) + 8 * ks, bd, idesc_s, ks + lo > 0);
             else
               tc::mma_f16(d, tc::desc_at(qd, 256 * (ks - C::kQTmem / 16)), bd, idesc_s, 1);
           }
         }
-        tc::commit(bar(kKEmpty, 0));
-        tc::commit(bar(kSFull, sbuf));
+        if (i == MT - 1) tc::commit(bar(kKEmpty, kb));
+        tc::commit(bar(kSFull, sk));
       };
-      // O += P(ci) V, P in the columns of its scores
-      auto mma_o = [&](int ci) {
-        const int sbuf = ci % NBUF;
-        wait(kPFull, sbuf, ci / NBUF);
-        wait(kVFull, ci % C::kVBufs, ci / C::kVBufs);
+      // O_i += P_i(ci) V, P in the columns of its scores
+      auto mma_o = [&](int i, int ci) {
+        if (!ok) return;
+        const int vb = ci % C::kVBufs, sk = buf(i, ci);
+        wait(kPFull, sk, ci / NBUF);
+        wait(kVFull, vb, ci / C::kVBufs);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t v = sb + C::kOffV + ci % C::kVBufs * C::kVBuf, a = tmem + C::kSCol + sbuf * KT, d = tmem + C::kOCol;
+        const uint32_t v = sb + C::kOffV + vb * C::kVBuf, a = tmem + C::kSCol + sk * KT;
+        const uint32_t d = tmem + C::kOCol + i * C::kOCols;
         const uint64_t vd = C::kVRows ? tc::smem_desc_sw128(v, KT * 128, 1024) : tc::smem_desc(v, 128, (KT / 8) * 128);
         constexpr uint32_t kStep = C::kVRows ? 2048 : 256;       // a K = 16 step further on
 #pragma unroll
@@ -616,38 +627,43 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
           tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks), idesc_oc, ci > 0 || ks > 0);
           if constexpr (C::kVLo) tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks + C::kLoOff), idesc_o, 1);
         }
-        tc::commit(bar(kVEmpty, ci % C::kVBufs));
-        if (NBUF > 1 || ci == n_chunks - 1) tc::commit(pv_done);
+        if (i == MT - 1) tc::commit(bar(kVEmpty, vb));
+        if (NBUF > 1 || ci == n_chunks - 1) tc::commit(pv_done(i));
       };
-      ok = mbar_wait_suspended(q_ready, 0, p.status);
-      for (int ci = 0; ci < NBUF; ++ci) mma_s(ci);
-      for (int ci = 0; ci < n_chunks && ok; ++ci) {
-        mma_o(ci);
-        mma_s(ci + NBUF);                    // behind the product that reads its buffer's P
-      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) ok = ok && mbar_wait_suspended(q_ready(i), 0, p.status);
+      for (int ci = 0; ci < NBUF; ++ci)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) mma_s(i, ci);
+      for (int ci = 0; ci < n_chunks && ok; ++ci)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          mma_o(i, ci);
+          mma_s(i, ci + NBUF);               // behind the product that reads its buffer's P
+        }
       tc::commit(drained);                   // what was issued completes before the CTA can leave
       mbar_wait_suspended(drained, 0, p.status);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= C::kStageWarp0) {
     // ---------------------------------------------------------------- staging --
-    const int sw = warp - 4;
+    const int sw = warp - C::kStageWarp0, st = tid - 32 * C::kStageWarp0;
     if constexpr (C::kMCols) {               // the unused columns of the centres' block, once
-      for (uint32_t i = tid - 128; i < KT * 8u; i += 32 * SW)
-        sts128(sb + C::kOffV + C::kTile + 16 * i, make_uint4(0, 0, 0, 0));
+      for (uint32_t i = st; i < C::kVBufs * KT * 8u; i += 32 * SW)
+        sts128(sb + C::kOffV + (i / (KT * 8)) * C::kVBuf + C::kTile + 16 * (i % (KT * 8)), make_uint4(0, 0, 0, 0));
       named_barrier_sync(1, 32 * SW);
     }
     for (int ci = 0; ci < n_chunks; ++ci) {
-      const int s = ci % RAW, vb = ci % C::kVBufs, valid = count - ci * KT;
+      const int s = ci % RAW, kb = ci % C::kKBufs, vb = ci % C::kVBufs, valid = count - ci * KT;
       const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, rawv = rawk + NP * C::kKSeg;
       ok = mbar_wait_suspended(raw_full(s), (ci / RAW) & 1, p.status);
-      if (ok && ci >= 1) ok = mbar_wait_suspended(bar(kKEmpty, 0), (ci - 1) & 1, p.status);
+      if (ok && ci >= C::kKBufs) ok = mbar_wait_suspended(bar(kKEmpty, kb), (ci / C::kKBufs - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      stage_k<D, KF, KT, SW>(rawk, sb + C::kOffK, sw, lane);
+      stage_k<D, KF, KT, SW>(rawk, sb + C::kOffK + kb * C::kKBuf, sw, lane);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kKFull, 0));
+      if (lane == 0) mbar_arrive(bar(kKFull, kb));
       if (ci >= C::kVBufs) ok = mbar_wait_suspended(bar(kVEmpty, vb), (ci / C::kVBufs - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -655,7 +671,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       if constexpr (C::kVRows)
         stage_v<D, VF, KT, SW, C::kMCols, C::kLoOff>(rawv, vbuf, pmask, valid, sw, lane);
       else
-        stage_v_nvfp4<D, KT, SW>(rawv, vbuf, pmask, valid, tid - 128);
+        stage_v_nvfp4<D, KT, SW>(rawv, vbuf, pmask, valid, st);
       if constexpr (C::kMCols) {             // 32 tokens by each of two warps, other ones each time
         const int part = (sw - 2 * ci) & (SW - 1);
         if (part < KT / 32) stage_m<D, KT>(rawv, vbuf + C::kTile, pmask, valid, 32 * part + lane);
@@ -669,8 +685,9 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
     }
   } else {
     // ---------------------------------------------------------------- softmax --
-    const uint32_t tlane = static_cast<uint32_t>(warp * 32) << 16;
-    const int r = r0 + tid;
+    const int i = MT == 1 ? 0 : warp >> 2, rl = tid & 127;         // row tile, row in it
+    const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int r = r0 + i * kTileRows + rl;
     const bool live = r < rows;
     uint64_t word = 0;
     if (live && T - p.n_nodes + r / p.group >= 0) word = p.mask[static_cast<size_t>(b) * p.n_nodes + r / p.group];
@@ -692,26 +709,27 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
           const uint4 y = load(c / 4 + e);
           x[4 * e] = y.x, x[4 * e + 1] = y.y, x[4 * e + 2] = y.z, x[4 * e + 3] = y.w;
         }
-        tc::st_32x32b_x16(tmem + tlane + C::kQCol + c, x);
+        tc::st_32x32b_x16(tmem + tlane + C::kQCol + i * (C::kQTmem / 2) + c, x);
       }
 #pragma unroll
       for (int u = 0; u < C::kQSmem / 8; ++u)
-        sts128(sb + C::kOffQ + ((tid >> 3) * (C::kQSmem / 8) + u) * 128 + (tid & 7) * 16, load(C::kQTmem / 8 + u));
+        sts128(sb + C::kOffQ + i * kTileRows * C::kQSmem * 2 + ((rl >> 3) * (C::kQSmem / 8) + u) * 128 + (rl & 7) * 16,
+               load(C::kQTmem / 8 + u));
     }
     tc::wait_st();
     fence_proxy_async();
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(q_ready);
+    if (lane == 0) mbar_arrive(q_ready(i));
     const int base = T - p.n_nodes;          // position of the tree's first row
-    const uint32_t o_col = tmem + tlane + C::kOCol;
+    const uint32_t o_col = tmem + tlane + C::kOCol + i * C::kOCols;
     float m = -INFINITY, l = 0.f;
 #pragma unroll 1
     for (int ci = 0; ci < n_chunks; ++ci) {
       const uint32_t pmask = chunk_mask(ci);
-      const int tok0 = first + ci * KT, sbuf = ci % NBUF;
-      const uint32_t s_col = tmem + tlane + C::kSCol + sbuf * KT;
-      ok = mbar_wait_suspended(bar(kSFull, sbuf), (ci / NBUF) & 1, p.status);
+      const int tok0 = first + ci * KT, sk = MT == 2 ? i : ci % NBUF;
+      const uint32_t s_col = tmem + tlane + C::kSCol + sk * KT;
+      ok = mbar_wait_suspended(bar(kSFull, sk), (ci / NBUF) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
@@ -744,7 +762,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
         // The product before has completed, O is still (one score buffer: these scores were issued behind
         // it).  At the last chunk in any case: the wait behind the loop names the last product by its
         // parity, which the product two before has too.
-        ok = mbar_wait_suspended(pv_done, (ci - 1) & 1, p.status);
+        ok = mbar_wait_suspended(pv_done(i), (ci - 1) & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::fence_after_sync();
@@ -775,9 +793,11 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kPFull, sbuf));
+      if (lane == 0) mbar_arrive(bar(kPFull, sk));
     }
-    if (ok) ok = mbar_wait_suspended(pv_done, NBUF > 1 ? (n_chunks - 1) & 1 : 0, p.status);
+    if (ok) ok = mbar_wait_suspended(pv_done(i), NBUF > 1 ? (n_chunks - 1) & 1 : 0, p.status);
+    // (two row tiles: the other's last product reads the operand tiles too)
+    if (MT == 2 && ok) ok = mbar_wait_suspended(pv_done(i ^ 1), 0, p.status);
     // (every MMA is done: the operand tiles and raw pages are free for the output rows)
     ok = __all_sync(0xffffffffu, ok);
     tc::fence_after_sync();
@@ -787,7 +807,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF>::kThreads, TreeCfg<D, KF, V
       tc::ld_32x32b_x16(o_col + D, ms);
       tc::wait_ld(ms);
     }
-    const uint32_t row = sb + C::kOffK + tid * C::kRowBytes;
+    const uint32_t row = sb + C::kOffK + (i * kTileRows + rl) * C::kRowBytes;
 #pragma unroll
     for (int c = 0; c < D; c += 16) {
       if (!ok) break;
@@ -917,10 +937,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
     *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-template <int D, int KF, int VF>
+template <int D, int KF, int VF, int MT>
 cudaError_t launch_one(const TreeParams &p, cudaStream_t st) {
-  using C = TreeCfg<D, KF, VF>;
-  auto kernel = tree_kernel<D, KF, VF>;
+  using C = TreeCfg<D, KF, VF, MT>;
+  auto kernel = tree_kernel<D, KF, VF, MT>;
   static bool ready[64] = {};                // the shared-memory limit, set once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -940,10 +960,17 @@ cudaError_t launch_one(const TreeParams &p, cudaStream_t st) {
   const int64_t items = std::min<int64_t>(
       p.batch + std::max(p.slots, 1) * std::max<int64_t>((chunks + per_wave - 1) / per_wave, 1),
       static_cast<int64_t>(p.batch) * std::max(1, p.max_splits));
-  const int64_t ctas = items * p.n_kv_heads * p.row_tiles;
+  const int64_t ctas = items * p.n_kv_heads * p.row_ctas;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(ctas));
   return launch_pdl(kernel, grid, dim3(C::kThreads), C::kSmem, st, p);
+}
+
+template <int D, int KF, int VF>
+cudaError_t launch_tiles(const TreeParams &p, cudaStream_t st) {
+  if constexpr (D == 128)
+    if (tree_tiles(D, p.n_nodes * p.group) == 2) return launch_one<D, KF, VF, 2>(p, st);
+  return launch_one<D, KF, VF, 1>(p, st);
 }
 
 template <int D>
@@ -951,10 +978,10 @@ cudaError_t launch_formats(int kf, int vf, const TreeParams &p, cudaStream_t st)
   auto by_v = [&](auto kc) -> cudaError_t {
     constexpr int K = decltype(kc)::value;
     switch (vf) {
-      case MEMRA_KV_Q5_1: return launch_one<D, K, MEMRA_KV_Q5_1>(p, st);
-      case MEMRA_KV_Q4_0: return launch_one<D, K, MEMRA_KV_Q4_0>(p, st);
-      case MEMRA_KV_FP8_E4M3: return launch_one<D, K, MEMRA_KV_FP8_E4M3>(p, st);
-      case MEMRA_KV_NVFP4: return launch_one<D, K, MEMRA_KV_NVFP4>(p, st);
+      case MEMRA_KV_Q5_1: return launch_tiles<D, K, MEMRA_KV_Q5_1>(p, st);
+      case MEMRA_KV_Q4_0: return launch_tiles<D, K, MEMRA_KV_Q4_0>(p, st);
+      case MEMRA_KV_FP8_E4M3: return launch_tiles<D, K, MEMRA_KV_FP8_E4M3>(p, st);
+      case MEMRA_KV_NVFP4: return launch_tiles<D, K, MEMRA_KV_NVFP4>(p, st);
       default: return cudaErrorInvalidValue;
     }
   };

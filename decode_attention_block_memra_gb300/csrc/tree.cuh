@@ -13,12 +13,16 @@ namespace memra {
 // Keys of one step of the split pass (the N of the score MMA).
 constexpr int kTreeKeys = 64;
 
-// CTAs of the split pass that share an SM.
-__host__ __device__ constexpr int tree_ctas_per_sm(int D) { return D == 128 ? 2 : 1; }
+// Row tiles (128 rows: nodes x the group's heads) that a CTA holds, and CTAs that
+// share an SM.  At head_dim 128 an SM holds two row tiles either way: past 128
+// rows as one CTA, so that a page is dequantized once for both (64 nodes x 8 heads
+// over 262,144 keys: 363 us, 438 with two CTAs of one tile).
+__host__ __device__ constexpr int tree_tiles(int D, int rows) { return D == 128 && rows > 128 ? 2 : 1; }
+__host__ __device__ constexpr int tree_ctas_per_sm(int D, int tiles) { return D == 128 && tiles == 1 ? 2 : 1; }
 
 // The split plan.  A call's keys, in chunks of kTreeKeys, are cut so that one
 // wave of the GPU (or as few whole waves as kTreeMaxChunks allows) holds all
-// CTAs: C = ceil(chunks of all sequences x KV heads x row tiles / slots) chunks
+// CTAs: C = ceil(chunks of all sequences x KV heads x row CTAs / slots) chunks
 // each, at least kTreeMinChunks (below it a CTA's fixed costs, about three
 // chunks' time, weigh more than the split gains) and at most kTreeMaxChunks: the
 // tensor cores cut the float32 sums at every step, and over 13,824 keys in one
@@ -64,9 +68,9 @@ struct TreeParams {
   int32_t *status;
   int batch, n_nodes, n_heads, group, n_kv_heads, num_pages, max_pages, max_seq_len;
   int len_limit;                // min(max_seq_len, tokens of a page table's row): lengths are clamped to it
-  int slots;                    // CTAs of a wave per (KV head, row tile), 0: sequences are cut at kTreeMaxChunks only
+  int slots;                    // CTAs of a wave per (KV head, rows of a CTA), 0: sequences are cut at kTreeMaxChunks only
   int max_splits;               // partials per row in the workspace
-  int row_tiles;                // 128-row tiles of one KV head
+  int row_ctas;                 // CTAs over the rows of one KV head
   float scale_log2;             // |sm_scale| * (post-scale of the staged K values) * log2(e); 1 for sm_scale 0
   uint32_t q_and, q_xor;        // applied to the query's fp16 pairs: the scale's sign, or zeros for sm_scale 0
   float v_post;                 // post-scale of the staged V values

@@ -122,6 +122,21 @@ def test_formats(memra, kf, vf, D):
     check(memra, w, words_for(w, 1))
 
 
+@pytest.mark.parametrize("kf,vf", PAIRS)
+def test_formats_at_two_row_tiles(memra, kf, vf):
+    w = W.random_case(51, batch=2, q_len=19, n_heads=16, n_kv_heads=2, head_dim=128, k_fmt=kf, v_fmt=vf,
+                      ctx=(19, 2900))
+    check(memra, w, words_for(w, 3))
+
+
+@pytest.mark.parametrize("T", [20, 63, 64, 65, 128, 129, 191, 193, 256, 300, 1029])
+def test_length_edges_at_two_row_tiles(memra, T):
+    # 160 rows; T = 20: the tree alone
+    w = W.make_workload(f"e{T}", batch=1, q_len=20, n_heads=8, n_kv_heads=1, head_dim=128, k_fmt="q8_0", v_fmt="q5_1",
+                        seed=T, seq_lens=[T], permute_pages=True, extra_pages=2)
+    check(memra, w, words_for(w, T))
+
+
 @pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("nodes,n_heads,n_kv_heads", [
     (1, 8, 2), (2, 4, 4), (16, 32, 4), (17, 32, 4),      # 128 rows, then two tiles
@@ -345,10 +360,10 @@ def test_captured_call_reads_new_lengths_and_words(memra):
     assert (np.abs(dw.out.cpu().numpy().astype(np.float64) - want) <= tol).all()
 
 
-@pytest.mark.parametrize("D", [128, 256])
-def test_many_calls_in_a_row(memra, D):
+@pytest.mark.parametrize("D,nodes", [(128, 5), (256, 5), (128, 30)])
+def test_many_calls_in_a_row(memra, D, nodes):
     """No wait runs out and no byte changes over thousands of calls (a wait that names the wrong phase would)."""
-    w = W.random_case(16, batch=4, q_len=5, n_heads=16, n_kv_heads=2, head_dim=D, k_fmt="fp8", v_fmt="fp8",
+    w = W.random_case(16, batch=4, q_len=nodes, n_heads=16, n_kv_heads=2, head_dim=D, k_fmt="fp8", v_fmt="fp8",
                       ctx=(300, 2500))
     dw, args, got = check(memra, w, words_for(w, 13))
     want = dw.out.clone()
