@@ -85,7 +85,8 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   // Where the sequences alone fill the GPU four times over, none is cut for its sake (and no CTA adds
   // up the lengths of so many).
   p.slots = std::max(1, device_sms() * tree_ctas_per_sm(head_dim, tiles) / (n_kv_heads * row_ctas));
-  if (batch >= 4 * p.slots) p.slots = 0;
+  p.alone = std::max(1, device_sms() / (n_kv_heads * row_ctas));
+  if (batch >= 4 * p.slots || one_split(max_seq_len)) p.slots = 0;
   p.max_splits = tree_max_splits(max_seq_len);
   p.row_ctas = row_ctas;
   // staged values: q8_0 / q5_1 / q4_0 at half size, fp8 / NVFP4 without their tensor scale

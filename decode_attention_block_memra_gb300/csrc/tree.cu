@@ -24,7 +24,7 @@
 // instructions, 70% of the issue slots of the 1,750 clocks it takes an SM, against
 // 1,060 clocks of MMAs.  8 sequences x 16 nodes over 6,316 keys (32/4 heads, D 128,
 // q8_0/q5_1): 38.8 us a call, 7 of them the merge, for 47 MB of pages; 64 nodes over
-// 262,144 keys: 363 us; 31 nodes on 12 ragged sequences, D 256, fp8: 97.5 us.
+// 262,144 keys: 363 us; 31 nodes on 12 ragged sequences, D 256, fp8: 75.9 us.
 // A sequence of one split writes its rows directly; the others leave (o, lse)
 // partials that tree_merge_kernel joins.
 #include <cuda_fp16.h>
@@ -388,25 +388,57 @@ __device__ __forceinline__ int tree_len(const TreeParams &p, int T) { return max
 struct TreeItem {
   int b, T, split, ns;    // b < 0: no such item
   int C;                  // chunks of a split wanted in this call
+  int per;                // chunks of a split of this sequence
   bool bad;               // the sequence's length was out of range
 };
 
 // Item `index` of the call, by a whole warp from the sequences' lengths.
 __device__ __forceinline__ TreeItem find_item(const TreeParams &p, int index, int lane) {
-  TreeItem it{-1, 0, 0, 0, kTreeMaxChunks, false};
+  TreeItem it{-1, 0, 0, 0, kTreeMaxChunks, 0, false};
   const int first = lane < p.batch ? p.seq_lens[lane] : 0;       // a short batch is read once
+  const int first_chunks = tree_ceil(tree_len(p, first), kTreeKeys);
+  // splits of a sequence, and the chunks of one
+  auto splits = [&](int chunks, int &per) {
+    per = tree_split_chunks(chunks, it.C);
+    return max(1, tree_ceil(chunks, per));
+  };
+  int first_per = 0, first_ns = 0, C = kTreeMaxChunks;
   if (p.slots > 0) {
-    int total = tree_ceil(tree_len(p, first), kTreeKeys);
-    for (int b = 32 + lane; b < p.batch; b += 32) total += tree_ceil(tree_len(p, p.seq_lens[b]), kTreeKeys);
+    auto chunks_of = [&](int b) { return tree_ceil(tree_len(p, p.seq_lens[b]), kTreeKeys); };
+    int total = first_chunks;
+    for (int b = 32 + lane; b < p.batch; b += 32) total += chunks_of(b);
     total = __reduce_add_sync(0xffffffffu, total);
-    const int waves = tree_ceil(tree_ceil(total, p.slots), kTreeMaxChunks);
-    it.C = min(max(tree_ceil(total, p.slots * max(waves, 1)), kTreeMinChunks), kTreeMaxChunks);
+    int places = p.alone;
+    C = tree_ceil(total, places);
+    if (C > kTreeAloneChunks) {
+      places = p.slots;
+      C = tree_ceil(total, places);
+      if (C > kTreeMaxChunks) {
+        places *= tree_ceil(C, kTreeMaxChunks);
+        C = tree_ceil(total, places);
+      }
+    }
+    C = min(max(C, kTreeMinChunks), kTreeMaxChunks);
+    // Each sequence's last split takes a place however short it is: C grows until all fit.
+    for (int trial = 0;; ++trial) {
+      it.C = C;
+      first_ns = splits(first_chunks, first_per);
+      if (trial == kTreeTrials || C == kTreeMaxChunks) break;
+      int items = lane < p.batch ? first_ns : 0, per;
+      for (int b = 32 + lane; b < p.batch; b += 32) items += splits(chunks_of(b), per);
+      const int over = __reduce_add_sync(0xffffffffu, items) - places;
+      if (over <= 0 || over >= places) break;
+      C = min(max(tree_ceil(total, places - over), C + 1), kTreeMaxChunks);
+    }
+  } else {
+    first_ns = splits(first_chunks, first_per);
   }
   int start = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int b = b0 + lane, T0 = b0 == 0 ? first : b < p.batch ? p.seq_lens[b] : 0, T = tree_len(p, T0);
-    const int chunks = tree_ceil(T, kTreeKeys);
-    const int ns = b < p.batch ? max(1, tree_ceil(chunks, tree_split_chunks(chunks, it.C))) : 0;
+    int per = first_per, ns = first_ns;
+    if (b0 > 0) ns = splits(tree_ceil(T, kTreeKeys), per);
+    if (b >= p.batch) ns = 0;
     int incl = ns;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -420,6 +452,7 @@ __device__ __forceinline__ TreeItem find_item(const TreeParams &p, int index, in
       it.b = b0 + src;
       it.T = __shfl_sync(0xffffffffu, T, src);
       it.ns = __shfl_sync(0xffffffffu, ns, src);
+      it.per = __shfl_sync(0xffffffffu, per, src);
       it.split = __shfl_sync(0xffffffffu, at, src);
       it.bad = __shfl_sync(0xffffffffu, T != T0 || T0 < p.n_nodes, src);
       break;
@@ -471,8 +504,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
       *reinterpret_cast<uint4 *>(p.out + row_id(r0 + i / (D / 8)) * D + 8 * (i % (D / 8))) = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int split_len = tree_split_chunks(tree_ceil(T, KT), item.C) * KT;
-  const int first = item.split * split_len, count = min(T - first, split_len);
+  const int split_len = item.per * KT, first = item.split * split_len, count = min(T - first, split_len);
   const int n_chunks = (count + KT - 1) / KT, n_pages = (count + kPage - 1) / kPage;
   // Page id of a page of the split, -1 for one left out or past the end.
   const int32_t *table = p.page_table + static_cast<size_t>(b) * p.max_pages + first / kPage;

@@ -22,16 +22,23 @@ __host__ __device__ constexpr int tree_ctas_per_sm(int D, int tiles) { return D 
 
 // The split plan.  A call's keys, in chunks of kTreeKeys, are cut so that one
 // wave of the GPU (or as few whole waves as kTreeMaxChunks allows) holds all
-// CTAs: C = ceil(chunks of all sequences x KV heads x row CTAs / slots) chunks
-// each, at least kTreeMinChunks (below it a CTA's fixed costs, about three
-// chunks' time, weigh more than the split gains) and at most kTreeMaxChunks: the
-// tensor cores cut the float32 sums at every step, and over 13,824 keys in one
-// split what was lost came to a quarter of the output's own rounding; a
-// sequence's splits are made equal.
+// CTAs: C = ceil(chunks of all sequences / places) chunks each, and more
+// (kTreeTrials times at most) while the sequences' rounded-up splits are more than
+// the places (8 sequences of 4,104 keys at head_dim 256: 50 us with 160 splits on
+// 152 SMs, 39 us with 128).  Where CTAs share an SM, the places are the SMs as long
+// as C is at most kTreeAloneChunks: sharing is worth a quarter, but prologues and
+// the merge cost less with fewer splits (8 sequences x 4 KV heads of 1,032 keys:
+// 17.9 us alone, 20.2 shared; of 2,056 keys 24.3 and 23.3).
+// C is at least kTreeMinChunks (the workspace's size goes by it) and at most
+// kTreeMaxChunks: the tensor cores cut the float32 sums at every step, and over
+// 13,824 keys in one split what was lost came to a quarter of the output's own
+// rounding.  A sequence's splits are made equal.
 // It depends on the lengths of all sequences of the call: a row's partial sums
 // are grouped differently in another batch, and its last bits may differ.
 constexpr int kTreeMinChunks = 4;
 constexpr int kTreeMaxChunks = 120;
+constexpr int kTreeAloneChunks = 6;
+constexpr int kTreeTrials = 4;
 constexpr int kTreeSplitPages = kTreeMaxChunks * kTreeKeys / kPage;
 // Most splits of a sequence, unless kTreeMaxChunks makes more.
 constexpr int kTreeMaxSplits = 160;
@@ -68,7 +75,8 @@ struct TreeParams {
   int32_t *status;
   int batch, n_nodes, n_heads, group, n_kv_heads, num_pages, max_pages, max_seq_len;
   int len_limit;                // min(max_seq_len, tokens of a page table's row): lengths are clamped to it
-  int slots;                    // CTAs of a wave per (KV head, rows of a CTA), 0: sequences are cut at kTreeMaxChunks only
+  int slots;                    // CTAs of a wave per (KV head, rows of a CTA), 0: sequences are cut at kTreeMaxChunks only (or not at all)
+  int alone;                    // of those, CTAs that have an SM each
   int max_splits;               // partials per row in the workspace
   int row_ctas;                 // CTAs over the rows of one KV head
   float scale_log2;             // |sm_scale| * (post-scale of the staged K values) * log2(e); 1 for sm_scale 0
