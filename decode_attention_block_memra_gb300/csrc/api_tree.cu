@@ -84,8 +84,7 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   p.len_limit = static_cast<int32_t>(std::min<int64_t>(max_seq_len, static_cast<int64_t>(max_pages_per_seq) * kPage));
   // Where the sequences alone fill the GPU four times over, none is cut for its sake (and no CTA adds
   // up the lengths of so many).
-  p.slots = std::max(1, device_sms() * tree_ctas_per_sm(head_dim, tiles) / (n_kv_heads * row_ctas));
-  p.alone = std::max(1, device_sms() / (n_kv_heads * row_ctas));
+  p.slots = std::max(1, device_sms() / (n_kv_heads * row_ctas));
   if (batch >= 4 * p.slots || one_split(max_seq_len)) p.slots = 0;
   p.max_splits = tree_max_splits(max_seq_len);
   p.row_ctas = row_ctas;

@@ -14,17 +14,21 @@
 //   * one MMA thread: S = Q K^T with Q in tensor memory, O += P V with P in
 //     tensor memory over its scores; the A operands stay out of shared memory,
 //     whose bandwidth the staged tiles need;
-//   * four softmax warps a row tile, thread = row.
-// head_dim 128, up to 128 rows: two CTAs share an SM (256 tensor-memory columns
-// each, one score buffer), so one's chain of copy, staging, MMA and softmax fills
-// the other's gaps, its first and last steps included; more rows: one CTA with two
-// row tiles, which fill each other's gaps.  head_dim 256: one CTA with two score
-// buffers, the scores a chunk ahead.
-// What bounds it is the staging: a chunk of q8_0/q5_1 costs 4,900 warp
-// instructions, 70% of the issue slots of the 1,750 clocks it takes an SM, against
-// 1,060 clocks of MMAs.  8 sequences x 16 nodes over 6,316 keys (32/4 heads, D 128,
-// q8_0/q5_1): 38.8 us a call, 7 of them the merge, for 47 MB of pages; 64 nodes over
-// 262,144 keys: 363 us; 31 nodes on 12 ragged sequences, D 256, fp8: 75.9 us.
+//   * groups of four softmax warps, thread = row.
+// One CTA to an SM.  At head_dim 128 it has two softmax groups, each with an O of
+// its own, and one's softmax fills the gaps of the other's MMAs: two row tiles
+// past 128 rows; else one row tile whose chunks they take by turns, their O joined
+// at the end (8 sequences x 16 nodes over 4,104 keys: 28.3 us, 31.2 as two CTAs on
+// an SM, which also leave twice the partial rows to the merge).  Four of the eight
+// staging warps take every other chunk (all eight on each: 44.8 for 39.8 us below).
+// head_dim 256: one group, two score buffers, the scores a chunk ahead.
+// What bounds it is the staging and the tensor cores' operand reads: both share a
+// shared memory of 128 bytes a clock, and a chunk of q8_0/q5_1 is 28 KB in, 64 KB
+// of tiles out, and 66 KB read by the MMAs of each row tile, for 1,060 clocks of
+// MMAs and 4,900 warp instructions.  8 sequences x 16 nodes over 6,316 keys (32/4
+// heads, D 128, q8_0/q5_1): 39.8 us a call, 5 of them the merge, for 47 MB of pages (4
+// splits a sequence on 128 of 152 SMs: 5 would not fit); 64 nodes over 262,144 keys:
+// 367 us; 31 nodes on 12 ragged sequences, D 256, fp8: 74.7 us.
 // A sequence of one split writes its rows directly; the others leave (o, lse)
 // partials that tree_merge_kernel joins.
 #include <cuda_fp16.h>
@@ -46,11 +50,17 @@ constexpr float kLazy = 8.f;               // log2 units: P stays <= 256 between
 
 template <int D, int KF, int VF, int MT>
 struct TreeCfg {
-  static constexpr int kCtas = tree_ctas_per_sm(D, MT);
-  static constexpr int kStageWarps = kCtas == 2 ? 4 : 8, kStageWarp0 = 4 * MT;
-  static constexpr int kMmaWarp = kStageWarp0 + kStageWarps, kCopyWarp = kMmaWarp + 1, kThreads = 32 * (kCopyWarp + 1);
+  // Softmax groups of four warps, each with an O of its own: one per row tile; at head_dim 128 a single
+  // row tile has two, which take the chunks by turns (kTurns) and are joined at the end.
+  static constexpr int kGroups = D == 128 ? 2 : 1;
+  static constexpr bool kTurns = kGroups > MT;
+  static constexpr int kStep = kTurns ? 2 : 1;                  // chunks from one of a group's to its next
+  static constexpr int kAhead = MT == 2 ? 1 : 2;                // chunks whose scores run ahead of the products
+  // Staging warps in as many groups, each with K^ and V^ tiles of its own.
+  static constexpr int kStageGroups = kGroups, kStageWarps = 8 / kStageGroups;
+  static constexpr int kStageWarp0 = 4 * kGroups, kMmaWarp = kStageWarp0 + 8, kCopyWarp = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kCopyWarp + 1);
   static constexpr int kPages = kTreeKeys / kPage;
-  static constexpr int kBufs = D == 128 ? 1 : 2;                // score buffers of a row tile
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
   static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
   static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
@@ -66,34 +76,34 @@ struct TreeCfg {
   static constexpr uint32_t kLoOff = kTile + (kMCols ? kTreeKeys * 128 : 0);      // V: hi, centres, lo
   static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kVLo ? kLoOff + kTile : kTile;
   static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
-  // Q in tensor memory, but for the last 32 dims at head_dim 128 (two row tiles share its 512 columns,
+  // Q in tensor memory, but for the last 32 dims at head_dim 128 (two row tiles fill its 512 columns with
   // 48 of Q, 144 of O, 64 of scores each), which lie in shared memory
   static constexpr int kQTmem = D == 128 ? 96 : D, kQSmem = D - kQTmem;
-  // Operand tiles in turn, so that staging runs ahead of the MMAs: two V^ tiles where they are no pairs,
-  // two of each in a CTA of two row tiles (two CTAs on an SM run ahead of each other).
-  static constexpr int kKBufs = MT == 2 ? 2 : 1, kVBufs = MT == 2 || !kVLo ? 2 : 1;
+  // Operand tiles in turn, so that staging runs ahead of the MMAs, where they fit.
+  static constexpr int kKBufs = kGroups, kVBufs = kGroups == 2 || !kVLo ? 2 : 1;
   // barriers and page ids, then K^ and V^ tiles, Q's last dims and the raw chunks; the output rows reuse
   // everything behind the page ids
   static constexpr uint32_t kOffBar = 0, kOffPid = 256, kOffK = 4096;
   static constexpr uint32_t kOffV = kOffK + kKBufs * kKBuf, kOffQ = kOffV + kVBufs * kVBuf;
   static constexpr uint32_t kOffRaw = kOffQ + MT * kTileRows * kQSmem * 2;
   // chunks of raw pages in flight: as many as fit, four at most
-  static constexpr uint32_t kRoom = (kCtas == 2 ? 113 : 227) * 1024;
+  static constexpr uint32_t kRoom = 227 * 1024;
   static constexpr int kRaw = (kRoom - kOffRaw) / kRawBytes < 4 ? (kRoom - kOffRaw) / kRawBytes : 4;
   static constexpr uint32_t kEnd = kOffRaw + kRaw * kRawBytes;
   static constexpr uint32_t kRowBytes = D * 4 + 16;             // padded output row
-  static constexpr uint32_t kEndRows = kOffK + MT * kTileRows * kRowBytes;
+  static constexpr uint32_t kOffMl = kOffK + MT * kTileRows * kRowBytes;          // (m, l) of two groups, at the end
+  static constexpr uint32_t kEndRows = kOffMl + (kTurns ? 2 * kTileRows * 8 : 0);
   // Tensor memory: a CTA that found its columns taken would wait in its
   // allocation, so shared memory is sized that no more CTAs of this or the
   // library's other tensor-memory kernels fit an SM than its 512 columns hold.
-  static constexpr uint32_t kTCols = 512 / kCtas;
-  static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows, kFloor = (kCtas == 2 ? 78 : 150) * 1024;
+  static constexpr uint32_t kTCols = 512;
+  static constexpr uint32_t kNeed = kEnd > kEndRows ? kEnd : kEndRows, kFloor = 150 * 1024;
   static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
-  // tensor-memory columns: Q, O, scores, those of the second row tile behind those of the first
-  static constexpr uint32_t kQCol = 0, kOCol = MT * kQTmem / 2, kSCol = kOCol + MT * kOCols;
+  // tensor-memory columns: Q of each row tile, O of each group, two score buffers
+  static constexpr uint32_t kQCol = 0, kOCol = MT * kQTmem / 2, kSCol = kOCol + kGroups * kOCols;
   static_assert(kOffPid + 4 * kTreeSplitPages <= kOffK && kRaw >= 2, "page ids; a chunk ahead");
-  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 232448, "shared memory");
-  static_assert(kSCol + MT * kBufs * kTreeKeys <= static_cast<int>(kTCols) && kCtas * kTCols <= 512, "tensor memory");
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kSCol + 2 * kTreeKeys <= kTCols, "tensor memory");
   static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
 };
 
@@ -408,15 +418,11 @@ __device__ __forceinline__ TreeItem find_item(const TreeParams &p, int index, in
     int total = first_chunks;
     for (int b = 32 + lane; b < p.batch; b += 32) total += chunks_of(b);
     total = __reduce_add_sync(0xffffffffu, total);
-    int places = p.alone;
+    int places = p.slots;
     C = tree_ceil(total, places);
-    if (C > kTreeAloneChunks) {
-      places = p.slots;
+    if (C > kTreeMaxChunks) {
+      places *= tree_ceil(C, kTreeMaxChunks);
       C = tree_ceil(total, places);
-      if (C > kTreeMaxChunks) {
-        places *= tree_ceil(C, kTreeMaxChunks);
-        C = tree_ceil(total, places);
-      }
     }
     C = min(max(C, kTreeMinChunks), kTreeMaxChunks);
     // Each sequence's last split takes a place however short it is: C grows until all fit.
@@ -463,10 +469,10 @@ __device__ __forceinline__ TreeItem find_item(const TreeParams &p, int index, in
 }
 
 template <int D, int KF, int VF, int MT>
-__global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, KF, VF, MT>::kCtas)
+__global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
     tree_kernel(const TreeParams p) {
   using C = TreeCfg<D, KF, VF, MT>;
-  constexpr int KT = kTreeKeys, NP = C::kPages, NBUF = C::kBufs, RAW = C::kRaw, SW = C::kStageWarps;
+  constexpr int KT = kTreeKeys, NP = C::kPages, RAW = C::kRaw, SW = C::kStageWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -616,8 +622,9 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
       auto wait = [&](int kind, int k, int phase) {
         ok = ok && mbar_wait_suspended(bar(kind, k), phase & 1, p.status);
       };
-      // Score buffer and barrier of tile i at chunk ci, and which use of it that is.
-      auto buf = [](int i, int ci) { return MT == 2 ? i : ci % NBUF; };
+      // Score buffer and barrier of row tile i at chunk ci; its O.
+      auto buf = [](int i, int ci) { return MT == 2 ? i : ci & 1; };
+      auto group = [](int i, int ci) { return C::kTurns ? ci & 1 : i; };
       // S_i(ci) = Q_i K^T
       auto mma_s = [&](int i, int ci) {
         if (!ok || ci >= n_chunks) return;
@@ -646,32 +653,32 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
       auto mma_o = [&](int i, int ci) {
         if (!ok) return;
         const int vb = ci % C::kVBufs, sk = buf(i, ci);
-        wait(kPFull, sk, ci / NBUF);
+        wait(kPFull, sk, ci / C::kAhead);
         wait(kVFull, vb, ci / C::kVBufs);
         if (!ok) return;
         tc::fence_after_sync();
         const uint32_t v = sb + C::kOffV + vb * C::kVBuf, a = tmem + C::kSCol + sk * KT;
-        const uint32_t d = tmem + C::kOCol + i * C::kOCols;
+        const uint32_t d = tmem + C::kOCol + group(i, ci) * C::kOCols;
         const uint64_t vd = C::kVRows ? tc::smem_desc_sw128(v, KT * 128, 1024) : tc::smem_desc(v, 128, (KT / 8) * 128);
         constexpr uint32_t kStep = C::kVRows ? 2048 : 256;       // a K = 16 step further on
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks) {
-          tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks), idesc_oc, ci > 0 || ks > 0);
+          tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks), idesc_oc, ci >= C::kStep || ks > 0);
           if constexpr (C::kVLo) tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks + C::kLoOff), idesc_o, 1);
         }
         if (i == MT - 1) tc::commit(bar(kVEmpty, vb));
-        if (NBUF > 1 || ci == n_chunks - 1) tc::commit(pv_done(i));
+        if (C::kGroups == 1 || ci + C::kStep >= n_chunks) tc::commit(pv_done(group(i, ci)));
       };
 #pragma unroll
-      for (int i = 0; i < MT; ++i) ok = ok && mbar_wait_suspended(q_ready(i), 0, p.status);
-      for (int ci = 0; ci < NBUF; ++ci)
+      for (int i = 0; i < C::kGroups; ++i) ok = ok && mbar_wait_suspended(q_ready(i), 0, p.status);
+      for (int ci = 0; ci < C::kAhead; ++ci)
 #pragma unroll
         for (int i = 0; i < MT; ++i) mma_s(i, ci);
       for (int ci = 0; ci < n_chunks && ok; ++ci)
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           mma_o(i, ci);
-          mma_s(i, ci + NBUF);               // behind the product that reads its buffer's P
+          mma_s(i, ci + C::kAhead);          // behind the product that reads its buffer's P
         }
       tc::commit(drained);                   // what was issued completes before the CTA can leave
       mbar_wait_suspended(drained, 0, p.status);
@@ -679,17 +686,20 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
     __syncwarp();
   } else if (warp >= C::kStageWarp0) {
     // ---------------------------------------------------------------- staging --
-    const int sw = warp - C::kStageWarp0, st = tid - 32 * C::kStageWarp0;
+    const int sg = (warp - C::kStageWarp0) / SW, sw = (warp - C::kStageWarp0) % SW, st = 32 * sw + lane;
     if constexpr (C::kMCols) {               // the unused columns of the centres' block, once
-      for (uint32_t i = st; i < C::kVBufs * KT * 8u; i += 32 * SW)
-        sts128(sb + C::kOffV + (i / (KT * 8)) * C::kVBuf + C::kTile + 16 * (i % (KT * 8)), make_uint4(0, 0, 0, 0));
-      named_barrier_sync(1, 32 * SW);
+      for (int vb = sg; vb < C::kVBufs; vb += C::kStageGroups)
+        for (uint32_t i = st; i < KT * 8u; i += 32 * SW)
+          sts128(sb + C::kOffV + vb * C::kVBuf + C::kTile + 16 * i, make_uint4(0, 0, 0, 0));
+      named_barrier_sync(1 + sg, 32 * SW);
     }
-    for (int ci = 0; ci < n_chunks; ++ci) {
+    for (int ci = sg; ci < n_chunks; ci += C::kStageGroups) {
       const int s = ci % RAW, kb = ci % C::kKBufs, vb = ci % C::kVBufs, valid = count - ci * KT;
       const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, rawv = rawk + NP * C::kKSeg;
-      ok = mbar_wait_suspended(raw_full(s), (ci / RAW) & 1, p.status);
-      if (ok && ci >= C::kKBufs) ok = mbar_wait_suspended(bar(kKEmpty, kb), (ci / C::kKBufs - 1) & 1, p.status);
+      // (K^'s tile first: that its last scores are done says that the chunk RAW before this one has landed,
+      // so that the raw chunk's parity names this use of its place and not the one two before)
+      if (ci >= C::kKBufs) ok = mbar_wait_suspended(bar(kKEmpty, kb), (ci / C::kKBufs - 1) & 1, p.status);
+      if (ok) ok = mbar_wait_suspended(raw_full(s), (ci / RAW) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       stage_k<D, KF, KT, SW>(rawk, sb + C::kOffK + kb * C::kKBuf, sw, lane);
@@ -717,7 +727,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
     }
   } else {
     // ---------------------------------------------------------------- softmax --
-    const int i = MT == 1 ? 0 : warp >> 2, rl = tid & 127;         // row tile, row in it
+    const int g = warp >> 2, i = MT == 2 ? g : 0, rl = tid & 127;  // group, row tile, row in it
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int r = r0 + i * kTileRows + rl;
     const bool live = r < rows;
@@ -735,6 +745,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
       };
 #pragma unroll
       for (int c = 0; c < C::kQTmem / 2; c += 16) {
+        if (C::kTurns && g != (c >= 32)) continue;               // the groups halve the row's 64 words
         uint32_t x[16];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -743,25 +754,27 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
         }
         tc::st_32x32b_x16(tmem + tlane + C::kQCol + i * (C::kQTmem / 2) + c, x);
       }
+      if (!C::kTurns || g == 1) {
 #pragma unroll
-      for (int u = 0; u < C::kQSmem / 8; ++u)
-        sts128(sb + C::kOffQ + i * kTileRows * C::kQSmem * 2 + ((rl >> 3) * (C::kQSmem / 8) + u) * 128 + (rl & 7) * 16,
-               load(C::kQTmem / 8 + u));
+        for (int u = 0; u < C::kQSmem / 8; ++u)
+          sts128(sb + C::kOffQ + i * kTileRows * C::kQSmem * 2 + ((rl >> 3) * (C::kQSmem / 8) + u) * 128 + (rl & 7) * 16,
+                 load(C::kQTmem / 8 + u));
+      }
     }
     tc::wait_st();
     fence_proxy_async();
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(q_ready(i));
+    if (lane == 0) mbar_arrive(q_ready(g));
     const int base = T - p.n_nodes;          // position of the tree's first row
-    const uint32_t o_col = tmem + tlane + C::kOCol + i * C::kOCols;
+    const uint32_t o_col = tmem + tlane + C::kOCol + g * C::kOCols;
     float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-    for (int ci = 0; ci < n_chunks; ++ci) {
+    for (int ci = C::kTurns ? g : 0; ci < n_chunks; ci += C::kStep) {
       const uint32_t pmask = chunk_mask(ci);
-      const int tok0 = first + ci * KT, sk = MT == 2 ? i : ci % NBUF;
+      const int tok0 = first + ci * KT, sk = MT == 2 ? i : ci & 1;
       const uint32_t s_col = tmem + tlane + C::kSCol + sk * KT;
-      ok = mbar_wait_suspended(bar(kSFull, sk), (ci / NBUF) & 1, p.status);
+      ok = mbar_wait_suspended(bar(kSFull, sk), (ci / C::kAhead) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
@@ -789,10 +802,10 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
         if (m != -INFINITY) alpha = fast_exp2(m - top);
         m = top;
       }
-      const bool moved = ci > 0 && __any_sync(0xffffffffu, alpha != 1.f);
-      if (NBUF > 1 && ci > 0 && (moved || ci == n_chunks - 1)) {
-        // The product before has completed, O is still (one score buffer: these scores were issued behind
-        // it).  At the last chunk in any case: the wait behind the loop names the last product by its
+      const bool moved = ci >= C::kStep && __any_sync(0xffffffffu, alpha != 1.f);
+      if (C::kGroups == 1 && ci > 0 && (moved || ci == n_chunks - 1)) {
+        // The product before has completed, O is still (a group of two: these scores were issued behind it).
+        // At the last chunk in any case: the wait behind the loop names the last product by its
         // parity, which the product two before has too.
         ok = mbar_wait_suspended(pv_done(i), (ci - 1) & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
@@ -827,29 +840,71 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kPFull, sk));
     }
-    if (ok) ok = mbar_wait_suspended(pv_done(i), NBUF > 1 ? (n_chunks - 1) & 1 : 0, p.status);
-    // (two row tiles: the other's last product reads the operand tiles too)
-    if (MT == 2 && ok) ok = mbar_wait_suspended(pv_done(i ^ 1), 0, p.status);
+    if constexpr (C::kGroups == 1) {
+      if (ok) ok = mbar_wait_suspended(pv_done(0), (n_chunks - 1) & 1, p.status);
+    } else {
+      // the other group's last product too: it reads the operand tiles, and its O is joined to this one
+      for (int e = 0; e < 2; ++e)
+        if (ok && (!C::kTurns || e < n_chunks)) ok = mbar_wait_suspended(pv_done(e), 0, p.status);
+    }
     // (every MMA is done: the operand tiles and raw pages are free for the output rows)
     ok = __all_sync(0xffffffffu, ok);
     tc::fence_after_sync();
+    // O = sum of w[e] O_e over the row's groups
+    float w[C::kStep];
+    if constexpr (C::kTurns) {
+      // this group's (m, l) for the other, l < 0 after a wait that gave up
+      const uint32_t ml = sb + C::kOffMl + rl * 8;
+      sts64(ml + g * kTileRows * 8, __float_as_uint(m), __float_as_uint(ok ? l : -1.f));
+      named_barrier_sync(3, 32 * 8);
+      const float m1 = __uint_as_float(lds32(ml + (g ^ 1) * kTileRows * 8));
+      const float l1 = __uint_as_float(lds32(ml + (g ^ 1) * kTileRows * 8 + 4));
+      ok = __all_sync(0xffffffffu, ok && !(l1 < 0.f));
+      const float top = fmaxf(m, m1), mine = l > 0.f ? fast_exp2(m - top) : 0.f, other = l1 > 0.f ? fast_exp2(m1 - top) : 0.f;
+      w[0] = g ? other : mine, w[C::kStep - 1] = g ? mine : other;
+      l = l * mine + l1 * other;
+      m = top;
+    } else {
+      w[0] = l > 0.f ? 1.f : 0.f;
+    }
     const float inv = l > 0.f ? p.v_post / l : 0.f;
-    uint32_t ms[16];                         // the centres' sums, per 32-dim block: hi parts, lo parts
+#pragma unroll
+    for (int e = 0; e < C::kStep; ++e) w[e] *= inv;
+    const uint32_t o_cols = C::kTurns ? tmem + tlane + C::kOCol : o_col;         // of the row's first group
+    uint32_t ms[C::kStep][16];               // the centres' sums, per 32-dim block: hi parts, lo parts
     if constexpr (C::kMCols) {
-      tc::ld_32x32b_x16(o_col + D, ms);
-      tc::wait_ld(ms);
+#pragma unroll
+      for (int e = 0; e < C::kStep; ++e) {
+        tc::ld_32x32b_x16(o_cols + e * C::kOCols + D, ms[e]);
+        tc::wait_ld(ms[e]);
+      }
     }
     const uint32_t row = sb + C::kOffK + (i * kTileRows + rl) * C::kRowBytes;
 #pragma unroll
-    for (int c = 0; c < D; c += 16) {
+    for (int c0 = 0; c0 < D / C::kStep; c0 += 16) {              // (by turns: half of the columns each)
       if (!ok) break;
-      uint32_t o[16];
-      tc::ld_32x32b_x16(o_col + c, o);
-      tc::wait_ld(o);
-      const float centre = C::kMCols ? __uint_as_float(ms[c / 32]) + __uint_as_float(ms[4 + c / 32]) : 0.f;
+      const int c = C::kTurns ? g * (D / 2) + c0 : c0;
       float x[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = l > 0.f ? (__uint_as_float(o[e]) + centre) * inv : 0.f;
+      for (int e = 0; e < 16; ++e) x[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < C::kStep; ++k) {
+        uint32_t o[16];
+        tc::ld_32x32b_x16(o_cols + k * C::kOCols + c, o);
+        tc::wait_ld(o);
+        float centre = 0.f;
+        if constexpr (C::kMCols) {
+          const float lower = __uint_as_float(ms[k][c0 / 32]) + __uint_as_float(ms[k][4 + c0 / 32]);
+          centre = lower;
+          if constexpr (C::kTurns) {
+            const float upper = __uint_as_float(ms[k][2 + c0 / 32]) + __uint_as_float(ms[k][6 + c0 / 32]);
+            centre = g ? upper : lower;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)         // (a group without a visible key: its O may hold anything)
+          x[e] = w[k] != 0.f ? fmaf(__uint_as_float(o[e]) + centre, w[k], x[e]) : x[e];
+      }
       if (ns == 1) {
 #pragma unroll
         for (int e = 0; e < 16; e += 8)
@@ -862,18 +917,23 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, TreeCfg<D, K
                                                __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])));
       }
     }
-    // The warp's 32 rows to memory, each by the whole warp (a bulk copy per row
-    // took 100 clocks to issue, 32 of them one after another).
-    const int64_t id = live ? static_cast<int64_t>(row_id(r)) : -1;
-    if (live && ns > 1)                      // -inf, never weighed, without a visible key or after a wait that gave up
-      p.lse_part[id * p.max_splits + item.split] = ok && l > 0.f ? m + __log2f(l) : -INFINITY;
-    __syncwarp();
-    const uint32_t row0 = sb + C::kOffK + warp * 32 * C::kRowBytes;
+    if (live && ns > 1 && (!C::kTurns || g == 0))                // -inf, never weighed, without a visible key or after a wait that gave up
+      p.lse_part[static_cast<int64_t>(row_id(r)) * p.max_splits + item.split] = ok && l > 0.f ? m + __log2f(l) : -INFINITY;
+    // The rows to memory, each by a whole warp (a bulk copy per row took 100 clocks
+    // to issue, 32 of them one after another).
+    constexpr int WR = 32 / C::kStep;        // rows of a warp
+    const int wr = r0 + WR * warp + lane;
+    const int64_t id = lane < WR && wr < rows ? static_cast<int64_t>(row_id(wr)) : -1;
+    if constexpr (C::kTurns)
+      named_barrier_sync(3, 32 * 8);         // both halves of the rows are there
+    else
+      __syncwarp();
+    const uint32_t row0 = sb + C::kOffK + warp * WR * C::kRowBytes;
     constexpr int BATCH = 8;                 // rows in flight
     auto write_rows = [&](auto units, auto to_row) {     // 16-byte units of a row; a row's address
       constexpr int U = decltype(units)::value;
 #pragma unroll 1
-      for (int e0 = 0; e0 < 32; e0 += BATCH) {
+      for (int e0 = 0; e0 < WR; e0 += BATCH) {
         uint4 x[BATCH][(U + 31) / 32];
 #pragma unroll
         for (int e = 0; e < BATCH; ++e)

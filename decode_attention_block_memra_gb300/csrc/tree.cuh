@@ -13,22 +13,17 @@ namespace memra {
 // Keys of one step of the split pass (the N of the score MMA).
 constexpr int kTreeKeys = 64;
 
-// Row tiles (128 rows: nodes x the group's heads) that a CTA holds, and CTAs that
-// share an SM.  At head_dim 128 an SM holds two row tiles either way: past 128
-// rows as one CTA, so that a page is dequantized once for both (64 nodes x 8 heads
-// over 262,144 keys: 363 us, 438 with two CTAs of one tile).
+// Row tiles (128 rows: nodes x the group's heads) of a CTA, one CTA to an SM: two
+// past 128 rows at head_dim 128, so that a page is dequantized once for both (64
+// nodes x 8 heads over 262,144 keys: 363 us, 438 with two CTAs of one tile).
 __host__ __device__ constexpr int tree_tiles(int D, int rows) { return D == 128 && rows > 128 ? 2 : 1; }
-__host__ __device__ constexpr int tree_ctas_per_sm(int D, int tiles) { return D == 128 && tiles == 1 ? 2 : 1; }
 
 // The split plan.  A call's keys, in chunks of kTreeKeys, are cut so that one
 // wave of the GPU (or as few whole waves as kTreeMaxChunks allows) holds all
 // CTAs: C = ceil(chunks of all sequences / places) chunks each, and more
 // (kTreeTrials times at most) while the sequences' rounded-up splits are more than
 // the places (8 sequences of 4,104 keys at head_dim 256: 50 us with 160 splits on
-// 152 SMs, 39 us with 128).  Where CTAs share an SM, the places are the SMs as long
-// as C is at most kTreeAloneChunks: sharing is worth a quarter, but prologues and
-// the merge cost less with fewer splits (8 sequences x 4 KV heads of 1,032 keys:
-// 17.9 us alone, 20.2 shared; of 2,056 keys 24.3 and 23.3).
+// 152 SMs, 40 us with 144).
 // C is at least kTreeMinChunks (the workspace's size goes by it) and at most
 // kTreeMaxChunks: the tensor cores cut the float32 sums at every step, and over
 // 13,824 keys in one split what was lost came to a quarter of the output's own
@@ -37,7 +32,6 @@ __host__ __device__ constexpr int tree_ctas_per_sm(int D, int tiles) { return D 
 // are grouped differently in another batch, and its last bits may differ.
 constexpr int kTreeMinChunks = 4;
 constexpr int kTreeMaxChunks = 120;
-constexpr int kTreeAloneChunks = 6;
 constexpr int kTreeTrials = 4;
 constexpr int kTreeSplitPages = kTreeMaxChunks * kTreeKeys / kPage;
 // Most splits of a sequence, unless kTreeMaxChunks makes more.
@@ -76,7 +70,6 @@ struct TreeParams {
   int batch, n_nodes, n_heads, group, n_kv_heads, num_pages, max_pages, max_seq_len;
   int len_limit;                // min(max_seq_len, tokens of a page table's row): lengths are clamped to it
   int slots;                    // CTAs of a wave per (KV head, rows of a CTA), 0: sequences are cut at kTreeMaxChunks only (or not at all)
-  int alone;                    // of those, CTAs that have an SM each
   int max_splits;               // partials per row in the workspace
   int row_ctas;                 // CTAs over the rows of one KV head
   float scale_log2;             // |sm_scale| * (post-scale of the staged K values) * log2(e); 1 for sm_scale 0
