@@ -56,13 +56,16 @@ struct TreeCfg {
   static constexpr bool kTurns = kGroups > MT;
   static constexpr int kStep = kTurns ? 2 : 1;                  // chunks from one of a group's to its next
   static constexpr int kAhead = MT == 2 ? 1 : 2;                // chunks whose scores run ahead of the products
-  // Staging warps in as many groups, each with K^ and V^ tiles of its own.
-  static constexpr int kStageGroups = kGroups, kStageWarps = 8 / kStageGroups;
+  static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
+  static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
+  // Staging warps in two groups that take the chunks by turns, each with K^ and V^ tiles of its own;
+  // at head_dim 256, where shared memory holds no two pairs, with NVFP4 and fp8 only (12 sequences x 31
+  // nodes over 3,000 keys: 45.1 for 48.0 us), but not with fp8 alone, whose staging is short (39.1 for 38.4).
+  static constexpr bool kNv = KF == MEMRA_KV_NVFP4 || VF == MEMRA_KV_NVFP4;
+  static constexpr int kStageGroups = D == 128 || (kNv && !kKLo && !kVLo) ? 2 : 1, kStageWarps = 8 / kStageGroups;
   static constexpr int kStageWarp0 = 4 * kGroups, kMmaWarp = kStageWarp0 + 8, kCopyWarp = kMmaWarp + 1;
   static constexpr int kThreads = 32 * (kCopyWarp + 1);
   static constexpr int kPages = kTreeKeys / kPage;
-  static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
-  static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
   static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
   // q5_1's d q + m as d (q - 16) and, in 16 more columns of V^, the blocks' centres m + 16 d (hi and lo
   // parts; the others zero), joined to O at the end: an exact d q + m in two fp16 parts costs ten
@@ -80,7 +83,7 @@ struct TreeCfg {
   // 48 of Q, 144 of O, 64 of scores each), which lie in shared memory
   static constexpr int kQTmem = D == 128 ? 96 : D, kQSmem = D - kQTmem;
   // Operand tiles in turn, so that staging runs ahead of the MMAs, where they fit.
-  static constexpr int kKBufs = kGroups, kVBufs = kGroups == 2 || !kVLo ? 2 : 1;
+  static constexpr int kKBufs = kStageGroups, kVBufs = kStageGroups == 2 || !kVLo ? 2 : 1;
   // barriers and page ids, then K^ and V^ tiles, Q's last dims and the raw chunks; the output rows reuse
   // everything behind the page ids
   static constexpr uint32_t kOffBar = 0, kOffPid = 256, kOffK = 4096;
