@@ -213,28 +213,29 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
 
-// Eight tokens (pairs in words) of which the first n exist; the others become zeros.
-__device__ __forceinline__ uint4 keep_tokens(const uint32_t (&x)[4], int n) {
+// Eight tokens (pairs in words), those whose bit is set; the others become zeros.
+__device__ __forceinline__ uint4 keep_tokens(const uint32_t (&x)[4], uint32_t bits) {
   uint32_t y[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) y[c] = x[c] & (n >= 2 * c + 2 ? 0xFFFFFFFFu : n == 2 * c + 1 ? 0xFFFFu : 0u);
+  for (int c = 0; c < 4; ++c)
+    y[c] = x[c] & (((bits >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((bits >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u));
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-// Tokens of page pg of the chunk that exist: `valid` of the chunk's, none of a page left out.
-__device__ __forceinline__ int page_tokens(uint32_t pmask, int pg, int valid) {
-  return (pmask >> pg) & 1u ? valid - kPage * pg : 0;
+// The 16 bits of page pg in the chunk's.
+__device__ __forceinline__ uint32_t page_bits(uint64_t keep, int pg) {
+  return static_cast<uint32_t>(keep >> (kPage * pg)) & 0xFFFFu;
 }
 
 // V^ of q5_1, q4_0 and fp8: token rows of 128 bytes (64 dims), 128-byte-swizzled
 // (the 16-byte unit of a row is XORed with the row's index in its group of 8),
 // one block of KEYS rows per 64 dims: the MN-major B operand of O += P V.  A
 // lane holds 4 consecutive dims of 4 tokens, so nothing is transposed, and a
-// warp's 8-byte stores fill all banks.  Tokens that do not exist become zeros:
+// warp's 8-byte stores fill all banks.  Tokens without a bit in `keep` become zeros:
 // 0 * (what their bytes stand for) need not be 0.  q5_1 stages d (q - 16) where
 // the blocks' centres have columns of their own (M_COLS), else d q + m by a TwoSum.
 template <int D, int VF, int KEYS, int WARPS, bool M_COLS, uint32_t LO>
-__device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int warp, int lane) {
+__device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint64_t keep, int warp, int lane) {
   constexpr int NB = D / 32, SEG = v_seg_bytes(VF, D), B2 = D / 64;
   const int vg = lane >> 2, c = lane & 3;
   // token 8 p + 2 c + f of page pg, block b, dims 4 vg .. + 3
@@ -248,7 +249,8 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
     static_assert(TASKS % WARPS == 0, "whole tasks");
 #pragma unroll
     for (int it = 0; it < TASKS / WARPS; ++it) {
-      const int task = warp + it * WARPS, pg = task / NB, b = task % NB, n = page_tokens(pmask, pg, valid);
+      const int task = warp + it * WARPS, pg = task / NB, b = task % NB;
+      const uint32_t bits = page_bits(keep, pg);
       const uint4 x = lds128(raw + pg * SEG + (b * 32 + lane) * 16);
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
@@ -258,7 +260,7 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
         e4m3x4_to_half2x2(__byte_perm(p ? x.w : x.z, 0, 0x3120), h1[0], h1[1]);
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          const bool live = 8 * p + 2 * c + f < n;
+          const bool live = (bits >> (8 * p + 2 * c + f)) & 1u;
           sts64(at(pg, p, f, b), live ? h0[f] : 0u, live ? h1[f] : 0u);
         }
       }
@@ -284,7 +286,7 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
       const uint4 d4 = lds128(scales + off);           // scales of the lane's tokens (halves 2 p + f), two blocks
       uint4 m4 = make_uint4(0, 0, 0, 0);
       if constexpr (VF == MEMRA_KV_Q5_1 && !M_COLS) m4 = lds128(scales + D + off);
-      const int n = page_tokens(pmask, pg0 + it * STEP, valid);
+      const uint32_t bits = page_bits(keep, pg0 + it * STEP);
 #pragma unroll
       for (int bp = 0; bp < 2; ++bp) {
         uint32_t hi[4][2], lo[4][2];     // [byte 2 f + p][h]
@@ -321,10 +323,10 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
             }
           }
         }
-        if (n < kPage) {
+        if (bits != 0xFFFFu) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (8 * (k & 1) + 2 * c + (k >> 1) >= n) hi[k][0] = hi[k][1] = lo[k][0] = lo[k][1] = 0u;
+            if (!((bits >> (8 * (k & 1) + 2 * c + (k >> 1))) & 1u)) hi[k][0] = hi[k][1] = lo[k][0] = lo[k][1] = 0u;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -340,7 +342,7 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint32_t pma
 // V^T of NVFP4 (dim rows, tokens along K, core matrices): its lanes hold single
 // dims, so a task gathers the 8 tokens of two dims and stores 16-byte rows.
 template <int D, int KEYS, int WARPS>
-__device__ __forceinline__ void stage_v_nvfp4(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int st) {
+__device__ __forceinline__ void stage_v_nvfp4(uint32_t raw, uint32_t buf, uint64_t keep, int st) {
   constexpr int SEG = v_seg_bytes(MEMRA_KV_NVFP4, D), TASKS = KEYS / kPage * 2 * (D / 16) * 8, IT = TASKS / (32 * WARPS);
   static_assert(IT * (32 * WARPS) == TASKS, "whole tasks");
 #pragma unroll
@@ -362,10 +364,11 @@ __device__ __forceinline__ void stage_v_nvfp4(uint32_t raw, uint32_t buf, uint32
       h0[c] = h2_bits(__lows2half2(v[0], v[1]));
       h1[c] = h2_bits(__highs2half2(v[0], v[1]));
     }
-    const int n = page_tokens(pmask, pg, valid) - 8 * ph, d0 = 16 * b16 + rr;
+    const uint32_t bits = page_bits(keep, pg) >> (8 * ph);
+    const int d0 = 16 * b16 + rr;
     const uint32_t at = buf + ((d0 >> 3) * (KEYS / 8) + g) * 128 + (d0 & 7) * 16;
-    sts128(at, keep_tokens(h0, n));
-    sts128(at + (KEYS / 8) * 128, keep_tokens(h1, n));
+    sts128(at, keep_tokens(h0, bits));
+    sts128(at + (KEYS / 8) * 128, keep_tokens(h1, bits));
   }
 }
 
@@ -374,7 +377,7 @@ __device__ __forceinline__ void stage_v_nvfp4(uint32_t raw, uint32_t buf, uint32
 // which the MMA takes 16, token n's hi and then lo parts of the four blocks in
 // its first 16-byte unit.
 template <int D, int KEYS>
-__device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint32_t pmask, int valid, int n) {
+__device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint64_t keep, int n) {
   constexpr int NB = D / 32, SEG = v_seg_bytes(MEMRA_KV_Q5_1, D);
   static_assert(NB == 4, "8 bytes of each part");
   const int pg = n / kPage, t = n % kPage;
@@ -389,9 +392,22 @@ __device__ __forceinline__ void stage_m(uint32_t raw, uint32_t buf, uint32_t pma
     hi[e] = h2_bits(s);
     lo[e] = h2_bits(__hadd2_rn(__hsub2_rn(a, __hsub2_rn(s, bb)), __hsub2_rn(b, bb)));
   }
-  const bool live = t < page_tokens(pmask, pg, valid);
+  const bool live = (keep >> n) & 1u;
   const uint4 x = live ? make_uint4(hi[0], hi[1], lo[0], lo[1]) : make_uint4(0, 0, 0, 0);
   sts128(buf + n * 128 + ((n & 7) << 4), x);
+}
+
+// Bit c: the row whose word is `word` sees key tok0 + c; `off` = tok0 - (position of the tree's first row).
+__device__ __forceinline__ uint64_t seen_keys(uint64_t word, int off) {
+  return off <= -kTreeKeys ? ~0ull : off < 0 ? word << -off | ((1ull << -off) - 1ull) : word >> off;
+}
+
+// The keys of the chunk's pages whose bit is set.
+__device__ __forceinline__ uint64_t page_keys(uint32_t pmask) {
+  uint64_t keys = 0;
+#pragma unroll
+  for (int i = 0; i < kTreeKeys / kPage; ++i) keys |= (pmask >> i) & 1u ? 0xFFFFull << (kPage * i) : 0ull;
+  return keys;
 }
 
 // Sequence length as the kernels use it.
@@ -696,6 +712,16 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
           sts128(sb + C::kOffV + vb * C::kVBuf + C::kTile + 16 * i, make_uint4(0, 0, 0, 0));
       named_barrier_sync(1 + sg, 32 * SW);
     }
+    // the words of all nodes together, for a split that holds rows of the tree
+    const int base = T - p.n_nodes;
+    uint64_t named = 0;
+    if (first + n_chunks * KT > base) {
+      for (int j = lane; j < p.n_nodes; j += 32)
+        if (base + j >= 0) named |= p.mask[static_cast<size_t>(b) * p.n_nodes + j];
+      const uint32_t lower = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(named));
+      const uint32_t upper = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(named >> 32));
+      named = static_cast<uint64_t>(upper) << 32 | lower;
+    }
     for (int ci = sg; ci < n_chunks; ci += C::kStageGroups) {
       const int s = ci % RAW, kb = ci % C::kKBufs, vb = ci % C::kVBufs, valid = count - ci * KT;
       const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, rawv = rawk + NP * C::kKSeg;
@@ -712,14 +738,19 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
       if (ci >= C::kVBufs) ok = mbar_wait_suspended(bar(kVEmpty, vb), (ci / C::kVBufs - 1) & 1, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t vbuf = sb + C::kOffV + vb * C::kVBuf, pmask = chunk_mask(ci);
+      const uint32_t vbuf = sb + C::kOffV + vb * C::kVBuf;
+      // Tokens that any row may see; not those of a page left out, nor rows of the tree that no word names:
+      // they need not have been written.
+      uint64_t keep = valid < KT ? (1ull << valid) - 1ull : ~0ull;
+      if (first + (ci + 1) * KT > base) keep &= seen_keys(named, first + ci * KT - base);
+      if (bad) keep &= page_keys(chunk_mask(ci));
       if constexpr (C::kVRows)
-        stage_v<D, VF, KT, SW, C::kMCols, C::kLoOff>(rawv, vbuf, pmask, valid, sw, lane);
+        stage_v<D, VF, KT, SW, C::kMCols, C::kLoOff>(rawv, vbuf, keep, sw, lane);
       else
-        stage_v_nvfp4<D, KT, SW>(rawv, vbuf, pmask, valid, st);
+        stage_v_nvfp4<D, KT, SW>(rawv, vbuf, keep, st);
       if constexpr (C::kMCols) {             // 32 tokens by each of two warps, other ones each time
         const int part = (sw - 2 * ci) & (SW - 1);
-        if (part < KT / 32) stage_m<D, KT>(rawv, vbuf + C::kTile, pmask, valid, 32 * part + lane);
+        if (part < KT / 32) stage_m<D, KT>(rawv, vbuf + C::kTile, keep, 32 * part + lane);
       }
       fence_proxy_async();                   // V^ for the tensor cores, the raw chunk for the next copies
       __syncwarp();
@@ -789,11 +820,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
       if (pmask != (1u << NP) - 1u || tok0 + KT > base) {
         // bit c: the row sees key tok0 + c.  Keys before the tree, then the tree's by the word (whose
         // bits past the tree are cleared, so rows past the end are hidden too).
-        const int off = tok0 - base;         // -63 .. 63 where the chunk holds rows of the tree
-        uint64_t sees = off <= -KT ? ~0ull : off < 0 ? word << -off | ((1ull << -off) - 1ull) : word >> off;
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-          if (!((pmask >> i) & 1u)) sees &= ~(0xFFFFull << (kPage * i));
+        const uint64_t sees = seen_keys(word, tok0 - base) & page_keys(pmask);
         const uint32_t half[2] = {static_cast<uint32_t>(sees), static_cast<uint32_t>(sees >> 32)};
 #pragma unroll
         for (int c = 0; c < KT; ++c)

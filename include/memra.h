@@ -350,7 +350,8 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
  *                 [b][i] is set; bits >= n_nodes are ignored.  Every node sees
  *                 all keys before the tree.
  *   n_nodes       1 .. MEMRA_MAX_TREE_NODES.  A sequence with fewer nodes pads
- *                 its tree with rows that no word names.
+ *                 its tree with rows that no word names; they need not have
+ *                 been written.
  *   workspace     device, >= memra_tree_attn_workspace_bytes(...) bytes; calls
  *                 that may overlap on the GPU need one each
  *   out           device fp16 [batch][n_nodes][n_heads][head_dim]
@@ -360,7 +361,8 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
  * exactly (or as fp16 pairs), the softmax weights in fp16; everything is
  * accumulated in float32.  The keys are cut by the lengths of the whole call,
  * so that it fills the GPU: the same call gives the same bytes, another batch
- * groups a row's sums differently and may differ in the last bits.  A row that sees no key yields zeros.  A sequence shorter than n_nodes
+ * groups a row's sums differently and may differ in the last bits.  A row that
+ * sees no key yields zeros.  A sequence shorter than n_nodes
  * sets MEMRA_DEVERR_BAD_SEQ_LEN; its nodes at positions below 0 are seen by
  * no row and yield zeros.  Keys of a page id outside the pool are left out
  * (MEMRA_DEVERR_BAD_PAGE).  batch == 0 is a no-op. */

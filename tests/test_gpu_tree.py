@@ -167,6 +167,39 @@ def test_rows_that_see_nothing(memra):
     assert (got[0, [0, 1, 2, 4, 5]] == 0).all() and (got[1] != 0).any()
 
 
+@pytest.mark.parametrize("D,nodes", [(128, 9), (256, 9), (128, 40)])
+@pytest.mark.parametrize("kf,vf", PAIRS)
+def test_unnamed_rows_may_hold_anything(memra, kf, vf, D, nodes):
+    """Rows of a padded tree that no word names, whose bytes stand for NaN."""
+    w = W.random_case(60 + D, batch=2, q_len=nodes, n_heads=8, n_kv_heads=2, head_dim=D, k_fmt=kf, v_fmt=vf,
+                      ctx=(nodes + 60, nodes + 90))
+    words = words_for(w, 17)
+    used = np.array([nodes - 4, 3])
+    for b, n in enumerate(used):
+        words[b, n:] = 0
+        words[b, :n] &= np.uint64((1 << int(n)) - 1)
+    want, tol = reference(w, words)
+    dw, args = run(memra, w, words)
+    unnamed = set()
+    for b, n in enumerate(used):
+        for t in range(int(w.seq_lens[b]) - nodes + int(n), int(w.seq_lens[b])):
+            unnamed.add(int(w.page_table[b, t // 16]) * 16 + t % 16)
+    keep = [i for i, s in enumerate(dw.step_slots.tolist()) if s not in unnamed]
+    assert len(keep) == used.sum()
+    for pool in (dw.cache.k_pool, dw.cache.v_pool):
+        pool.fill_(0xFF)
+    before = w.prefill_rows
+    memra.kv_append(dw.cache, *(torch.from_numpy(np.ascontiguousarray(x[before])).cuda()
+                                for x in (w.k_rows, w.v_rows, w.slots)))
+    memra.kv_append(dw.cache, dw.step_k[keep].contiguous(), dw.step_v[keep].contiguous(),
+                    dw.step_slots[keep].contiguous())
+    dw.out.fill_(float("nan"))
+    memra.tree_attn(*args)
+    assert memra.read_status(dw.cache) == 0
+    worst = float((np.abs(dw.out.cpu().numpy().astype(np.float64) - want) / tol).max())
+    assert worst <= 1, worst
+
+
 def test_bits_past_the_tree_are_ignored(memra):
     w = W.random_case(5, batch=2, q_len=7, n_heads=8, n_kv_heads=2, ctx=(7, 90))
     words = words_for(w, 2)
