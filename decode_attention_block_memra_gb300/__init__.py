@@ -323,6 +323,15 @@ def _need_dense(where: str, *wanted) -> None:
             raise MemraError(1, where)
 
 
+def _need_here(where: str, *tensors) -> None:
+    """Refuse tensors that are not on the current device."""
+    import torch
+    device = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise MemraError(1, where)
+
+
 def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status=None, stream=None) -> None:
     """memra_prompt_attn: causal attention of packed prompts.
 
@@ -335,6 +344,7 @@ def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     _need_dense("memra_prompt_attn", (out, torch.float16, q.shape), (cu_seqlens, torch.int32, cu_seqlens.shape))
+    _need_here("memra_prompt_attn", status)
     strides = []
     for x in (q, k, v):
         s = x.stride()
@@ -365,6 +375,7 @@ def tree_attn(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, tree_ma
     _need_dense("memra_tree_attn", (q, torch.float16, q.shape), (out, torch.float16, q.shape),
                 (page_table, torch.int32, (B, page_table.shape[1])), (seq_lens, torch.int32, (B,)),
                 (tree_mask, torch.int64, q.shape[:2]))
+    _need_here("memra_tree_attn", cache.k_pool, cache.v_pool, workspace)
     a = _decode_args(cache, q, page_table, seq_lens, max_seq_len, out, workspace, sm_scale)
     _check(lib().memra_tree_attn(*a[:6], _ptr(tree_mask), *a[6:], _stream(stream)), "memra_tree_attn")
 
@@ -374,6 +385,7 @@ def kv_copy_pages(cache: KVCache, src_pages, dst_pages, n: int | None = None, st
     import torch
     most = src_pages.shape[0]
     _need_dense("memra_kv_copy_pages", (src_pages, torch.int32, (most,)), (dst_pages, torch.int32, (most,)))
+    _need_here("memra_kv_copy_pages", cache.k_pool, cache.v_pool)
     if n is None:
         n = most
     elif n > most:
@@ -393,6 +405,7 @@ def kv_compact(cache: KVCache, page_table, seq_lens, max_seq_len: int, accepted,
     B, most = accepted.shape
     _need_dense("memra_kv_compact", (accepted, torch.int32, (B, most)), (n_accepted, torch.int32, (B,)),
                 (page_table, torch.int32, (B, page_table.shape[1])), (seq_lens, torch.int32, (B,)))
+    _need_here("memra_kv_compact", cache.k_pool, cache.v_pool)
     _check(lib().memra_kv_compact(cache.ref, _ptr(page_table), int(page_table.shape[1]), _ptr(seq_lens),
                                   int(max_seq_len), _ptr(accepted), int(most), _ptr(n_accepted), int(B), int(n_nodes),
                                   _stream(stream)), "memra_kv_compact")

@@ -233,3 +233,5 @@ def test_binding_refuses_other_layouts(memra):
                  (q, k, k, cu, q.bfloat16())):
         with pytest.raises(memra.MemraError):
             memra.prompt_attn(*args)
+    with pytest.raises(memra.MemraError):
+        memra.prompt_attn(q, k, k, cu, q, status=torch.zeros(1, dtype=torch.int32))

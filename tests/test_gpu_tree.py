@@ -345,10 +345,12 @@ def test_binding_refuses_other_tensors(memra):
     w = W.random_case(18, batch=2, q_len=4, n_heads=8, n_kv_heads=2, ctx=(40, 60))
     dw, args = run(memra, w, words_for(w, 18))
     cache, q, table, lens, M, mask, out, ws, scale = args
+    on_host = memra.KVCache("q8_0", "q5_1", cache.num_pages, cache.n_kv_heads, cache.head_dim, device="cpu")
     for bad in ((cache, q.float(), table, lens, M, mask, out, ws), (cache, q, table[:1], lens, M, mask, out, ws),
                 (cache, q, table, lens.long(), M, mask, out, ws), (cache, q, table, lens, M, mask.int(), out, ws),
                 (cache, q, table, lens, M, mask[:, :3], out, ws), (cache, q, table.cpu(), lens, M, mask, out, ws),
-                (cache, q, table, lens, M, mask, out[:1], ws), (cache, q.transpose(1, 2), table, lens, M, mask, out, ws)):
+                (cache, q, table, lens, M, mask, out[:1], ws), (cache, q.transpose(1, 2), table, lens, M, mask, out, ws),
+                (cache, q, table, lens, M, mask, out, ws.cpu()), (on_host, q, table, lens, M, mask, out, ws)):
         with pytest.raises(memra.MemraError):
             memra.tree_attn(*bad)
     kept, count = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
@@ -356,6 +358,11 @@ def test_binding_refuses_other_tensors(memra):
                 (table, lens, M, kept, count[:1]), (table, lens, M, kept.cpu(), count)):
         with pytest.raises(memra.MemraError):
             memra.kv_compact(cache, *bad, 4)
+    with pytest.raises(memra.MemraError):
+        memra.kv_compact(on_host, table, lens, M, kept, count, 4)
+    pages = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(memra.MemraError):
+        memra.kv_copy_pages(on_host, pages, pages + 1)
 
 
 def test_lengths_out_of_range(memra):
