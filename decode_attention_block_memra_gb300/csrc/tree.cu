@@ -18,7 +18,7 @@
 // One CTA to an SM.  At head_dim 128 it has two softmax groups, each with an O of
 // its own, and one's softmax fills the gaps of the other's MMAs: two row tiles
 // past 128 rows; else one row tile whose chunks they take by turns, their O joined
-// at the end (8 sequences x 16 nodes over 4,104 keys: 28.3 us, 31.2 as two CTAs on
+// at the end (8 sequences x 8 nodes over 4,104 keys: 28.3 us, 31.2 as two CTAs on
 // an SM, which also leave twice the partial rows to the merge).  Four of the eight
 // staging warps take every other chunk (all eight on each: 44.8 for 39.8 us below).
 // head_dim 256: one group, two score buffers, the scores a chunk ahead.
@@ -26,9 +26,9 @@
 // shared memory of 128 bytes a clock, and a chunk of q8_0/q5_1 is 28 KB in, 64 KB
 // of tiles out, and 66 KB read by the MMAs of each row tile, for 1,060 clocks of
 // MMAs and 4,900 warp instructions.  8 sequences x 16 nodes over 6,316 keys (32/4
-// heads, D 128, q8_0/q5_1): 39.8 us a call, 5 of them the merge, for 47 MB of pages (4
+// heads, D 128, q8_0/q5_1): 40.5 us a call, 5 of them the merge, for 47 MB of pages (4
 // splits a sequence on 128 of 152 SMs: 5 would not fit); 64 nodes over 262,144 keys:
-// 367 us; 31 nodes on 12 ragged sequences, D 256, fp8: 74.7 us.
+// 366 us; 31 nodes on 12 ragged sequences, D 256, fp8: 75.5 us.
 // A sequence of one split writes its rows directly; the others leave (o, lse)
 // partials that tree_merge_kernel joins.
 #include <cuda_fp16.h>
