@@ -79,9 +79,9 @@ struct TreeCfg {
   static constexpr uint32_t kLoOff = kTile + (kMCols ? kTreeKeys * 128 : 0);      // V: hi, centres, lo
   static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kVLo ? kLoOff + kTile : kTile;
   static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
-  // Q in tensor memory, but for the last 32 dims at head_dim 128 (two row tiles fill its 512 columns with
-  // 48 of Q, 144 of O, 64 of scores each), which lie in shared memory
-  static constexpr int kQTmem = D == 128 ? 96 : D, kQSmem = D - kQTmem;
+  // Q in tensor memory.  Two row tiles fill its 512 columns with 48 of Q, 144 of O and 64 of scores each:
+  // Q's last 32 dims lie in shared memory.
+  static constexpr int kQTmem = MT == 2 ? 96 : D, kQSmem = D - kQTmem;
   // Operand tiles in turn, so that staging runs ahead of the MMAs, where they fit.
   static constexpr int kKBufs = kStageGroups, kVBufs = kStageGroups == 2 || !kVLo ? 2 : 1;
   // barriers and page ids, then K^ and V^ tiles, Q's last dims and the raw chunks; the output rows reuse
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
       };
 #pragma unroll
       for (int c = 0; c < C::kQTmem / 2; c += 16) {
-        if (C::kTurns && g != (c >= 32)) continue;               // the groups halve the row's 64 words
+        if (C::kTurns && g != (c >= 32)) continue;               // half of the row by each group
         uint32_t x[16];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -788,12 +788,10 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
         }
         tc::st_32x32b_x16(tmem + tlane + C::kQCol + i * (C::kQTmem / 2) + c, x);
       }
-      if (!C::kTurns || g == 1) {
 #pragma unroll
-        for (int u = 0; u < C::kQSmem / 8; ++u)
-          sts128(sb + C::kOffQ + i * kTileRows * C::kQSmem * 2 + ((rl >> 3) * (C::kQSmem / 8) + u) * 128 + (rl & 7) * 16,
-                 load(C::kQTmem / 8 + u));
-      }
+      for (int u = 0; u < C::kQSmem / 8; ++u)
+        sts128(sb + C::kOffQ + i * kTileRows * C::kQSmem * 2 + ((rl >> 3) * (C::kQSmem / 8) + u) * 128 + (rl & 7) * 16,
+               load(C::kQTmem / 8 + u));
     }
     tc::wait_st();
     fence_proxy_async();
