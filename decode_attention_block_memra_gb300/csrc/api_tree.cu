@@ -81,11 +81,15 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   p.num_pages = cache->num_pages;
   p.max_pages = max_pages_per_seq;
   p.max_seq_len = max_seq_len;
-  p.len_limit = static_cast<int32_t>(std::min<int64_t>(max_seq_len, static_cast<int64_t>(max_pages_per_seq) * kPage));
+  // (positions up to a chunk past the end stay below 2^31)
+  p.len_limit = static_cast<int32_t>(std::min<int64_t>(
+      std::min<int64_t>(max_seq_len, INT32_MAX - kTreeKeys), static_cast<int64_t>(max_pages_per_seq) * kPage));
   // Where the sequences alone fill the GPU four times over, none is cut for its sake (and no CTA adds
-  // up the lengths of so many).
+  // up the lengths of so many, nor of more chunks than 32 bits count).
   p.slots = std::max(1, device_sms() / (n_kv_heads * row_ctas));
-  if (batch >= 4 * p.slots || one_split(max_seq_len)) p.slots = 0;
+  if (batch >= 4 * p.slots || one_split(max_seq_len) ||
+      static_cast<int64_t>(batch) * tree_ceil(max_seq_len, kTreeKeys) > INT32_MAX)
+    p.slots = 0;
   p.max_splits = tree_max_splits(max_seq_len);
   p.row_ctas = row_ctas;
   // staged values: q8_0 / q5_1 / q4_0 at half size, fp8 / NVFP4 without their tensor scale
