@@ -159,11 +159,16 @@ def _ptr(x) -> int:
     return x.data_ptr()
 
 
+def _device() -> int:
+    import torch
+    return torch._C._cuda_getDevice()
+
+
 def _stream(stream) -> int:
     if stream is None:
         # the current stream's handle without building a Stream object (3 us of a call's 8)
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -205,6 +210,8 @@ class KVCache:
         self.v_pool = v_pool if v_pool is not None else torch.zeros(vb, dtype=torch.uint8, device=device)
         assert self.k_pool.numel() == kb and self.v_pool.numel() == vb
         self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        on = {t.get_device() for t in (self.k_pool, self.v_pool, self.status)}
+        self.device_index = on.pop() if len(on) == 1 else None
         self.struct = KVCacheStruct(fmt_id(k_fmt), fmt_id(v_fmt), PAGE_SIZE, n_kv_heads, head_dim, num_pages,
                                     self.k_pool.data_ptr(), self.v_pool.data_ptr(), float(k_scale), float(v_scale),
                                     self.status.data_ptr())
@@ -314,22 +321,13 @@ def decode_attn_noalloc(cache: KVCache, q, page_table, seq_lens, max_seq_len: in
                                            _stream(stream)), "memra_decode_attn_noalloc")
 
 
-def _need_dense(where: str, *wanted) -> None:
-    """Refuse tensors that are not dense, not of the (dtype, shape) wanted, or not on the current device."""
-    import torch
-    device = torch._C._cuda_getDevice()
+def _need_dense(where: str, *wanted) -> int:
+    """Refuse tensors that are not dense, not of the (dtype, shape) wanted, or not on the current device: its index."""
+    device = _device()
     for t, dtype, shape in wanted:
         if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
             raise MemraError(1, where)
-
-
-def _need_here(where: str, *tensors) -> None:
-    """Refuse tensors that are not on the current device."""
-    import torch
-    device = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise MemraError(1, where)
+    return device
 
 
 def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status=None, stream=None) -> None:
@@ -344,7 +342,8 @@ def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     _need_dense("memra_prompt_attn", (out, torch.float16, q.shape), (cu_seqlens, torch.int32, cu_seqlens.shape))
-    _need_here("memra_prompt_attn", status)
+    if status is not None and status.get_device() != out.get_device():
+        raise MemraError(1, "memra_prompt_attn")
     strides = []
     for x in (q, k, v):
         s = x.stride()
@@ -372,10 +371,11 @@ def tree_attn(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, tree_ma
     """
     import torch
     B = q.shape[0]
-    _need_dense("memra_tree_attn", (q, torch.float16, q.shape), (out, torch.float16, q.shape),
-                (page_table, torch.int32, (B, page_table.shape[1])), (seq_lens, torch.int32, (B,)),
-                (tree_mask, torch.int64, q.shape[:2]))
-    _need_here("memra_tree_attn", cache.k_pool, cache.v_pool, workspace)
+    device = _need_dense("memra_tree_attn", (q, torch.float16, q.shape), (out, torch.float16, q.shape),
+                         (page_table, torch.int32, (B, page_table.shape[1])), (seq_lens, torch.int32, (B,)),
+                         (tree_mask, torch.int64, q.shape[:2]))
+    if cache.device_index != device or (workspace is not None and workspace.get_device() != device):
+        raise MemraError(1, "memra_tree_attn")
     a = _decode_args(cache, q, page_table, seq_lens, max_seq_len, out, workspace, sm_scale)
     _check(lib().memra_tree_attn(*a[:6], _ptr(tree_mask), *a[6:], _stream(stream)), "memra_tree_attn")
 
@@ -384,14 +384,13 @@ def kv_copy_pages(cache: KVCache, src_pages, dst_pages, n: int | None = None, st
     """memra_kv_copy_pages: page src_pages[i] -> dst_pages[i] in both pools; int32 [n] on the device, negative skips."""
     import torch
     most = src_pages.shape[0]
-    _need_dense("memra_kv_copy_pages", (src_pages, torch.int32, (most,)), (dst_pages, torch.int32, (most,)))
-    _need_here("memra_kv_copy_pages", cache.k_pool, cache.v_pool)
+    device = _need_dense("memra_kv_copy_pages", (src_pages, torch.int32, (most,)), (dst_pages, torch.int32, (most,)))
     if n is None:
         n = most
-    elif n > most:
+    if n > most or cache.device_index != device:
         raise MemraError(1, "memra_kv_copy_pages")
-    _check(lib().memra_kv_copy_pages(cache.ref, _ptr(src_pages), _ptr(dst_pages), int(n), _stream(stream)),
-           "memra_kv_copy_pages")
+    rc = lib().memra_kv_copy_pages(cache.ref, src_pages.data_ptr(), dst_pages.data_ptr(), int(n), _stream(stream))
+    _check(rc, "memra_kv_copy_pages")
 
 
 def kv_compact(cache: KVCache, page_table, seq_lens, max_seq_len: int, accepted, n_accepted, n_nodes: int,
@@ -403,12 +402,15 @@ def kv_compact(cache: KVCache, page_table, seq_lens, max_seq_len: int, accepted,
     """
     import torch
     B, most = accepted.shape
-    _need_dense("memra_kv_compact", (accepted, torch.int32, (B, most)), (n_accepted, torch.int32, (B,)),
-                (page_table, torch.int32, (B, page_table.shape[1])), (seq_lens, torch.int32, (B,)))
-    _need_here("memra_kv_compact", cache.k_pool, cache.v_pool)
-    _check(lib().memra_kv_compact(cache.ref, _ptr(page_table), int(page_table.shape[1]), _ptr(seq_lens),
-                                  int(max_seq_len), _ptr(accepted), int(most), _ptr(n_accepted), int(B), int(n_nodes),
-                                  _stream(stream)), "memra_kv_compact")
+    pages = page_table.shape[-1]
+    i32 = torch.int32
+    device = _need_dense("memra_kv_compact", (accepted, i32, (B, most)), (n_accepted, i32, (B,)),
+                         (page_table, i32, (B, pages)), (seq_lens, i32, (B,)))
+    if cache.device_index != device:
+        raise MemraError(1, "memra_kv_compact")
+    rc = lib().memra_kv_compact(cache.ref, page_table.data_ptr(), pages, seq_lens.data_ptr(), int(max_seq_len),
+                                accepted.data_ptr(), most, n_accepted.data_ptr(), B, int(n_nodes), _stream(stream))
+    _check(rc, "memra_kv_compact")
 
 
 def testing_decode_attn_short_page(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, out, workspace,
