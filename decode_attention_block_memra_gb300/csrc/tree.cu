@@ -26,7 +26,7 @@
 // shared memory of 128 bytes a clock, and a chunk of q8_0/q5_1 is 28 KB in, 64 KB
 // of tiles out, and 66 KB read by the MMAs of each row tile, for 1,060 clocks of
 // MMAs and 4,900 warp instructions.  8 sequences x 16 nodes over 6,316 keys (32/4
-// heads, D 128, q8_0/q5_1): 40.5 us a call, 5 of them the merge, for 47 MB of pages (4
+// heads, D 128, q8_0/q5_1): 40.1 us a call, 5 of them the merge, for 47 MB of pages (4
 // splits a sequence on 128 of 152 SMs: 5 would not fit); 64 nodes over 262,144 keys:
 // 366 us; 31 nodes on 12 ragged sequences, D 256, fp8: 75.5 us.
 // A sequence of one split writes its rows directly; the others leave (o, lse)
