@@ -24,10 +24,19 @@
 //   * P goes to tensor memory in fp16 and is the A operand of O += P V: no
 //     shared-memory round trip.
 // Warps: four softmax warps per tile (thread = row), one that issues the score
-// MMAs, one that issues the products, one that loads.  The reference maximum moves only when a tile's maximum passes it by
-// more than kLazy (log2 units), so O in tensor memory is rescaled rarely; P
-// then stays <= 2^kLazy.  Scores, maxima, sums and O are float32; P is rounded
-// to fp16 (relative 2^-11 a weight), the operand type of the tensor cores.
+// MMAs, one that issues the products, one that loads.  The reference maximum
+// moves only when a tile's maximum passes it by more than kLazy (log2 units), so
+// O in tensor memory is rescaled rarely; P then stays <= 2^kLazy.  Scores, maxima,
+// sums and O are float32; P is rounded to fp16 (relative 2^-11 a weight), the
+// operand type of the tensor cores.
+// The tensor cores cut an accumulator's last bits at every step (half of 2^-21 of
+// it on average, always towards zero: a mean over 524,288 keys in one sum was off
+// by 2.8e-3), so no more than kSumKeys keys go into one sum.  Then each element's
+// fp16 part moves to the row's place in `out`, over a power of two that keeps it
+// in range, and what is left of it, exact in float32, stays in O as the start of
+// the next sum: no bit is lost and no scratch is needed.  On 16,384 tokens this takes
+// 1% of the time (1,459 to 1,474 us; as a branch inside the step loop, where its
+// registers spill the loop's, 1,640).
 // What bounds it: the tensor cores.  16,384 tokens, 32/4 heads, D 128: 1.47 ms a
 // call in a loop (1,500 TFLOP/s, the power cap on), 1.28 ms for a single one, the
 // tensor pipe active 77% of the time; 8 ragged prompts of up to 4,860 tokens 510 us
@@ -47,6 +56,7 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr float kLazy = 8.f;
+constexpr int kSumKeys = 8192;             // most keys of one float32 sum in the tensor cores
 
 template <int D>
 struct PromptCfg {
@@ -352,7 +362,53 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     const int n_steps = hi[i] - lo[i];
     float m = -INFINITY;
     uint64_t l = 0;                                 // two sums, of the even and the odd keys
+    // What earlier sums left in the row of `out`: fp16 parts, times `far`; and their weights' sum
+    constexpr int kSumSteps = kSumKeys / KT;
+    float far = 0.f, l_far = 0.f;
     const uint32_t o_col = tmem + tlane + C::kOCol + i * D;
+    auto row_at = [&] { return (static_cast<int64_t>(w.first + t) * p.n_heads + kvh * p.group + rl % p.group) * D; };
+    // O plus what the row of `out` holds (`held`): the whole to O, or its fp16 part, over `up`, to the row and
+    // the rest to O.  (An infinity stays in O: what goes to the row is cut to fp16's range.)
+    auto join = [&](bool held, bool split, float up) {
+      const uint64_t far2 = pack_f2(far, far), down2 = pack_f2(1.f / up, 1.f / up), minus_up2 = pack_f2(-up, -up);
+      uint4 *const row = reinterpret_cast<uint4 *>(p.out + (live ? row_at() : 0));
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 128) {
+        uint4 x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = held && live ? row[c0 / 8 + e] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t o[32];
+          tc::ld_32x32b_x32(o_col + c0 + c, o);
+          tc::wait_ld_all();
+          tc::hold<32>(o);
+          uint32_t *y = &x[c / 8].x;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 old = __half22float2(bits_h2(y[e]));
+            uint64_t s = fma_f2(pack_f2(old.x, old.y), far2,
+                                pack_f2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])));
+            if (split) {
+              float s0, s1;
+              unpack_f2(mul_f2(s, down2), s0, s1);
+              y[e] = pack_half2_sat(s0, s1);
+              const float2 hi = __half22float2(bits_h2(y[e]));
+              s = fma_f2(pack_f2(hi.x, hi.y), minus_up2, s);
+            }
+            float s0, s1;
+            unpack_f2(s, s0, s1);
+            o[2 * e] = __float_as_uint(s0), o[2 * e + 1] = __float_as_uint(s1);
+          }
+          tc::st_32x32b_x32(o_col + c0 + c, o);
+        }
+        if (split && live)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) row[c0 / 8 + e] = x[e];
+        __syncwarp();
+      }
+      tc::wait_st();
+    };
     if constexpr (!C::kQSmem) {
       // the row of Q, fp16 pairs as they lie (row by row from memory this took 7,000 clocks)
       ok = mbar_wait_suspended(q_landed(0), 0, p.status);
@@ -373,82 +429,104 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(q_full(i));
     }
+    int end = 0;                                    // the first step of the next sum
 #pragma unroll 1
-    for (int u = 0; u < n_steps && ok; ++u) {
-      const int j = lo[i] + u, b = NBUF > 1 ? u & 1 : 0;
-      const uint32_t s_col = tmem + tlane + s_col_of(b), p_col = tmem + tlane + p_col_of(i, b);
-      ok = mbar_wait_suspended(s_full(i, b), (u / NBUF) & 1, p.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc::fence_after_sync();
-      uint32_t s[KT];
-#pragma unroll
-      for (int c = 0; c < KT; c += 32) tc::ld_32x32b_x32(s_col + c, s + c);
-      tc::wait_ld_all();
-      tc::hold<KT>(s);
-      if (NT == 2) {                                // the score buffer is the other tile's turn
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_read);
-      }
-      const int last = t - j * KT;                  // the row's own key, in this step's columns
-      if (j * KT + KT - 1 > tile_first) {           // keys behind the row's token
-#pragma unroll
-        for (int c = 0; c < KT; ++c)
-          if (c > last) s[c] = 0xff800000u;         // -inf
-      }
-      if (p.window > 0 && j * KT < tile_last - p.window + 1) {    // keys before its window
-#pragma unroll
-        for (int c = 0; c < KT; ++c)
-          if (c < last - p.window + 1) s[c] = 0xff800000u;
-      }
-      const float top = row_max(s) * p.scale_log2;
-      float alpha = 1.f;
-      if (live && top > m + kLazy) {                // also the first step with a key (m = -inf)
-        if (m != -INFINITY) alpha = fast_exp2(m - top);
-        m = top;
-      }
-      const bool moved = u > 0 && __any_sync(0xffffffffu, alpha != 1.f);
-      if (u > 0 && (NT == 2 || moved || u == n_steps - 1)) {
-        // The product before has completed: it has read P's columns (their own, head_dim 128), and O is
-        // still.  At the last step in any case: the wait behind the loop names the last product by its
-        // parity, which the product two before has too.
-        ok = mbar_wait_suspended(pv_done(i), (u - 1) & 1, p.status);
+    for (int first = 0; first < n_steps && ok; first = end) {
+      end = min(n_steps, first + kSumSteps);
+#pragma unroll 1
+      for (int u = first; u < end && ok; ++u) {
+        const int j = lo[i] + u, b = NBUF > 1 ? u & 1 : 0;
+        const uint32_t s_col = tmem + tlane + s_col_of(b), p_col = tmem + tlane + p_col_of(i, b);
+        ok = mbar_wait_suspended(s_full(i, b), (u / NBUF) & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc::fence_after_sync();
-      }
-      if (moved) {                                  // O's rows of this warp times alpha
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tc::ld_32x32b_x32(o_col + c, o);
-          tc::wait_ld_all();
-          tc::hold<32>(o);
+        uint32_t s[KT];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tc::st_32x32b_x32(o_col + c, o);
+        for (int c = 0; c < KT; c += 32) tc::ld_32x32b_x32(s_col + c, s + c);
+        tc::wait_ld_all();
+        tc::hold<KT>(s);
+        if (NT == 2) {                                // the score buffer is the other tile's turn
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_read);
         }
-        l = fma_f2(l, pack_f2(alpha, alpha), 0);
-      }
-      const float mu = m == -INFINITY ? 0.f : m;
+        const int last = t - j * KT;                  // the row's own key, in this step's columns
+        if (j * KT + KT - 1 > tile_first) {           // keys behind the row's token
 #pragma unroll
-      for (int c = 0; c < KT; c += 32) {
-        uint32_t w2[16];
-        row_weights<16>(s + c, p.scale_log2, mu, w2, l);
-        tc::st_32x32b_x16(p_col + c / 2, w2);
+          for (int c = 0; c < KT; ++c)
+            if (c > last) s[c] = 0xff800000u;         // -inf
+        }
+        if (p.window > 0 && j * KT < tile_last - p.window + 1) {    // keys before its window
+#pragma unroll
+          for (int c = 0; c < KT; ++c)
+            if (c < last - p.window + 1) s[c] = 0xff800000u;
+        }
+        const float top = row_max(s) * p.scale_log2;
+        float alpha = 1.f;
+        if (live && top > m + kLazy) {                // also the first step with a key (m = -inf)
+          if (m != -INFINITY) alpha = fast_exp2(m - top);
+          m = top;
+        }
+        const bool moved = u > 0 && __any_sync(0xffffffffu, alpha != 1.f);
+        if (u > 0 && (NT == 2 || moved || u == end - 1)) {
+          // The product before has completed: it has read P's columns (their own, head_dim 128), and O is
+          // still.  At the last step in any case: the wait behind the loop names the last product by its
+          // parity, which the product two before has too.
+          ok = mbar_wait_suspended(pv_done(i), (u - 1) & 1, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::fence_after_sync();
+        }
+        if (moved) {                                  // O's rows of this warp times alpha
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tc::ld_32x32b_x32(o_col + c, o);
+            tc::wait_ld_all();
+            tc::hold<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::st_32x32b_x32(o_col + c, o);
+          }
+          l = fma_f2(l, pack_f2(alpha, alpha), 0);
+          far *= alpha, l_far *= alpha;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        uint64_t sum = 0;                             // (a step's own, so that no long sum takes single weights)
+#pragma unroll
+        for (int c = 0; c < KT; c += 32) {
+          uint32_t w2[16];
+          row_weights<16>(s + c, p.scale_log2, mu, w2, sum);
+          tc::st_32x32b_x16(p_col + c / 2, w2);
+        }
+        l = add_f2(l, sum);
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(i, b));
       }
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(i, b));
+      if (ok) ok = mbar_wait_suspended(pv_done(i), (end - 1) & 1, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok && end < n_steps) {
+        tc::fence_after_sync();
+        float l0, l1;
+        unpack_f2(l, l0, l1);
+        l_far += l0 + l1;
+        l = 0;
+        // |O| <= the largest |V| times the weights' sum: a power of two above that brings O into fp16's range
+        const float up = l_far < 1e30f ? __uint_as_float(((__float_as_uint(l_far) >> 23) + 2u) << 23) : 1.f;
+        join(first > 0, true, up);
+        far = up;
+      }
     }
-    if (n_steps > 0 && ok) ok = mbar_wait_suspended(pv_done(i), (n_steps - 1) & 1, p.status);
     if (__all_sync(0xffffffffu, n_steps > 0 && ok)) {
       tc::fence_after_sync();
       float l0, l1;
       unpack_f2(l, l0, l1);
-      const float inv = l0 + l1 > 0.f ? 1.f / (l0 + l1) : 0.f;
+      l0 += l1 + l_far;
+      const float inv = l0 > 0.f ? 1.f / l0 : 0.f;
+      if (n_steps > kSumSteps) join(true, false, 1.f);
       // The row into shared memory (the tile's Q, or at head_dim 256 the ring: both read for the last
       // time), 16-byte units XORed with the row so that eight rows' stores fall on different banks ...
       constexpr uint32_t kRow = D * 2;
@@ -469,8 +547,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         }
       }
       // ... and from there to memory, the heads of a token side by side.
-      const int64_t to =
-          live ? (static_cast<int64_t>(w.first + t) * p.n_heads + kvh * p.group + rl % p.group) * D : -1;
+      const int64_t to = live ? row_at() : -1;
       __syncwarp();
       constexpr int U = D / 8, PER = 32 / U;        // 16-byte units of a row, rows at a time
 #pragma unroll 8

@@ -324,10 +324,13 @@ int memra_decode_step_cascade(const memra_kv_cache *cache, const void *k_new, co
  *   status      device int32 the kernel ORs MEMRA_DEVERR_* bits into, or NULL
  * n_heads % n_kv_heads == 0, n_heads / n_kv_heads <= MEMRA_MAX_GROUP, head_dim
  * 128 or 256, batch and n_kv_heads <= 65535.  Scores, softmax and output are
- * accumulated in float32; the weights enter the product with V in fp16.  A
- * sequence's result bytes are the same alone or packed with others, and no two
- * sequences see each other's rows.  No workspace.  batch == 0 or total_tokens
- * == 0 is a no-op. */
+ * accumulated in float32, 8,192 keys to a sum of the tensor cores (which cut a
+ * sum's last bits at every step) and the sums joined; the weights enter the
+ * product with V in fp16.  While the call runs, rows of out may hold parts of
+ * those sums.  A sequence's result bytes are the same alone or packed with
+ * others, and no two sequences see each other's rows.  A v that is not finite
+ * may also reach rows of its sequence within 256 tokens of those that see it.
+ * No workspace.  batch == 0 or total_tokens == 0 is a no-op. */
 int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                       int64_t v_stride, const int32_t *cu_seqlens, int32_t batch, int32_t total_tokens,
                       int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale, int32_t window, void *out,

@@ -156,6 +156,107 @@ def test_alone_or_packed_same_bytes(memra, D):
         begin += n
 
 
+@pytest.mark.parametrize("D", [128, 256])
+def test_long_means_keep_their_precision(memra, D):
+    """Equal scores over up to 524,288 keys: every weight is 1 exactly, every row the mean of the values before it.
+
+    What is left are the output's rounding (half a step, 2^-11 for values in
+    [1, 2)) and the float32 sums: at most 512 steps of 16 keys in one sum, each
+    off by at most 2^-21 of the sum so far, half of its end on average, so 2^-13
+    relative and 2^-12 for values below 2.  A single sum over all the keys would
+    be off by thousands of steps' cuts, all towards zero.
+    """
+    n = 524_288
+    g = torch.Generator(device="cuda").manual_seed(14)
+    v = (1.9 + 0.09 * torch.rand(n, 1, D, device="cuda", generator=g)).half()
+    q, k = torch.zeros_like(v), torch.randn(n, 1, D, device="cuda", generator=g).half()
+    out = torch.empty_like(v)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    memra.prompt_attn(q, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"), out, status=status)
+    assert int(status) == 0
+    rows = torch.arange(1, n + 1, device="cuda", dtype=torch.float64)[:, None, None]
+    err = (out.double() - v.double().cumsum(0) / rows).abs()      # (the values are multiples of 2^-10: sums are exact)
+    assert float(err.max()) <= 2.0 ** -11 + 2.0 ** -12, [float(x.max()) for x in err.split(n // 8)]
+
+
+def far_rows(memra, n, D, window=0, mult=1.0, drift=0.0, seed=0):
+    """(got, want, tolerance) of some rows of one prompt of n tokens: its ends and around each 8,192 keys, two heads."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    Hq, Hkv = 8, 2
+    q, k, v = (torch.randn(n, h, D, device="cuda", generator=g) for h in (Hq, Hkv, Hkv))
+    q *= mult
+    if drift:                                        # scores that rise along the keys
+        q[..., 0], k[..., 0] = 1.0, drift * torch.arange(n, device="cuda")[:, None] * D ** 0.5
+    q, k, v = q.half(), k.half(), v.half()
+    out = torch.empty_like(q)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    memra.prompt_attn(q, k, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"), out, window=window,
+                      status=status)
+    assert int(status) == 0
+    rows = torch.unique(torch.cat([torch.arange(a, a + 40) for a in (0, *range(8192 - 20, n - 40, 8192), n - 40)]))
+    rows = rows.cuda()
+    at = torch.arange(n, device="cuda")
+    seen = at[None] <= rows[:, None]
+    if window:
+        seen &= at[None] > rows[:, None] - window
+    parts = []
+    for h in (0, Hq - 1):
+        qd, kd, vd = q[rows, h].double(), k[:, h // 4].double(), v[:, h // 4].double()
+        p = torch.softmax((qd @ kd.T * D ** -0.5).masked_fill(~seen, -np.inf), 1)
+        mass = (qd.abs() @ kd.abs().T * D ** -0.5).masked_fill(~seen, 0).amax(1, keepdim=True)
+        weight = 2 * ((D // 16 + 2) * 2.0 ** -22 * mass + 2.0 ** -20)
+        want = p @ vd
+        # as in reference(), and 2^-13 for 512 steps of the sums of products
+        tol = U * want.abs() + (U + weight + 2.0 ** -13) * (p @ vd.abs()) + n * 2.0 ** -25 * vd.abs().max()
+        parts.append((out[rows, h].double(), want, tol))
+    return [torch.stack(x) for x in zip(*parts)]
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("n,window", [(8192, 0), (8193, 0), (16_640, 0), (40_001, 0), (40_001, 1000), (40_001, 12_345),
+                                      (40_001, 30_000)])
+def test_long_prompts(memra, n, window, D):
+    """Against float64, element by element, and in the 2-norm: there the output's rounding and the weights' are
+    at most u each, and the float32 parts of tol add 2^-12."""
+    got, want, tol = far_rows(memra, n, D, window, mult=0.5, seed=n + window)
+    assert bool(((got - want).abs() <= tol).all())
+    assert float((got - want).norm() / want.norm()) <= 2 * U + 2.0 ** -12
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("drift", [-0.002, 0.0005, 0.002, 0.02])
+def test_long_prompts_with_drifting_scores(memra, drift, D):
+    # scores that rise or fall by 20 to 800 over the keys: what was summed before is scaled down again and again, or rules
+    got, want, tol = far_rows(memra, 40_001, D, mult=1.0, drift=drift, seed=15)
+    assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_infinite_values_reach_the_rows_that_see_them(memra, D):
+    n = 20_000
+    g = torch.Generator(device="cuda").manual_seed(16)
+    q, k, v = (torch.randn(n, h, D, device="cuda", generator=g).half() for h in (4, 1, 1))
+    cu, out, want = torch.tensor([0, n], dtype=torch.int32, device="cuda"), torch.empty_like(q), torch.empty_like(q)
+    memra.prompt_attn(q * 0.1, k, v, cu, want)
+    v[40, 0, 3], v[40, 0, 7] = float("inf"), float("-inf")
+    memra.prompt_attn(q * 0.1, k, v, cu, out)
+    assert bool((out[40:, :, 3] == float("inf")).all()) and bool((out[40:, :, 7] == float("-inf")).all())
+    keep = [c for c in range(D) if c not in (3, 7)]
+    assert torch.equal(out[..., keep], want[..., keep])
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("value", [65504.0, -65504.0, 2.0 ** -14, 3 * 2.0 ** -24])
+def test_long_means_at_the_ends_of_the_range(memra, value, D):
+    # equal weights and values, over five sums: half a step of fp16 and 2^-13 for the sums
+    n = 40_000
+    v = torch.full((n, 1, D), value, device="cuda").half()
+    q, out = torch.zeros_like(v), torch.empty_like(v)
+    memra.prompt_attn(q, q, v, torch.tensor([0, n], dtype=torch.int32, device="cuda"), out)
+    err = (out.double() - value).abs()
+    assert float(err.max()) <= max(U, 2.0 ** -25 / abs(value)) * abs(value) + 2.0 ** -13 * abs(value)
+
+
 def test_many_sequences(memra):
     rng = np.random.default_rng(2)
     check(memra, list(rng.integers(0, 40, 101)), 8, 2, 128, seed=9, pad=4)
