@@ -888,14 +888,16 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
       const float m1 = __uint_as_float(lds32(ml + (g ^ 1) * kTileRows * 8));
       const float l1 = __uint_as_float(lds32(ml + (g ^ 1) * kTileRows * 8 + 4));
       ok = __all_sync(0xffffffffu, ok && !(l1 < 0.f));
-      const float top = fmaxf(m, m1), mine = l > 0.f ? fast_exp2(m - top) : 0.f, other = l1 > 0.f ? fast_exp2(m1 - top) : 0.f;
+      // (a sum of NaN, from a query or a key that is not finite, is no empty one: the row becomes NaN)
+      const float top = fmaxf(m, m1);
+      const float mine = l != 0.f ? fast_exp2(m - top) : 0.f, other = l1 != 0.f ? fast_exp2(m1 - top) : 0.f;
       w[0] = g ? other : mine, w[C::kStep - 1] = g ? mine : other;
       l = l * mine + l1 * other;
       m = top;
     } else {
-      w[0] = l > 0.f ? 1.f : 0.f;
+      w[0] = l != 0.f ? 1.f : 0.f;
     }
-    const float inv = l > 0.f ? p.v_post / l : 0.f;
+    const float inv = l != 0.f ? p.v_post / l : 0.f;
 #pragma unroll
     for (int e = 0; e < C::kStep; ++e) w[e] *= inv;
     const uint32_t o_cols = C::kTurns ? tmem + tlane + C::kOCol : o_col;         // of the row's first group
@@ -946,7 +948,7 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
       }
     }
     if (live && ns > 1 && (!C::kTurns || g == 0))                // -inf, never weighed, without a visible key or after a wait that gave up
-      p.lse_part[static_cast<int64_t>(row_id(r)) * p.max_splits + item.split] = ok && l > 0.f ? m + __log2f(l) : -INFINITY;
+      p.lse_part[static_cast<int64_t>(row_id(r)) * p.max_splits + item.split] = ok && l != 0.f ? m + __log2f(l) : -INFINITY;
     // The rows to memory, each by a whole warp (a bulk copy per row took 100 clocks
     // to issue, 32 of them one after another).
     constexpr int WR = 32 / C::kStep;        // rows of a warp
@@ -1046,7 +1048,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
       }
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;          // (0: no visible key; a NaN stays one)
   uint32_t y[PER / 2];
 #pragma unroll
   for (int e = 0; e < PER / 2; ++e) y[e] = pack_half2(acc[2 * e] * inv, acc[2 * e + 1] * inv);

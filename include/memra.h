@@ -365,7 +365,9 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
  * accumulated in float32.  The keys are cut by the lengths of the whole call,
  * so that it fills the GPU: the same call gives the same bytes, another batch
  * groups a row's sums differently and may differ in the last bits.  A row that
- * sees no key yields zeros.  A sequence shorter than n_nodes
+ * sees no key yields zeros; a query, or a key that a row sees, that is not
+ * finite makes the row NaN.  A named node whose V is not finite may also reach
+ * the tree's rows that do not see it.  A sequence shorter than n_nodes
  * sets MEMRA_DEVERR_BAD_SEQ_LEN; its nodes at positions below 0 are seen by
  * no row and yield zeros.  Keys of a page id outside the pool are left out
  * (MEMRA_DEVERR_BAD_PAGE).  batch == 0 is a no-op. */

@@ -302,6 +302,47 @@ def test_peaked_scores_and_a_negative_scale(memra):
     assert (np.abs(dw.out.cpu().numpy().astype(np.float64) - want) <= tol).all()
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D,nodes,ctx", [(128, 9, 200), (128, 9, 2600), (128, 40, 200), (128, 40, 2600), (256, 9, 200),
+                                         (256, 9, 2600)])
+def test_a_query_that_is_not_finite_makes_its_row_nan(memra, D, nodes, ctx, value):
+    # one split, then several; no other row changes
+    w = W.random_case(70 + D, batch=2, q_len=nodes, n_heads=8, n_kv_heads=2, head_dim=D, ctx=(ctx - 30, ctx))
+    dw, args, _ = check(memra, w, words_for(w, 21))
+    want = dw.out.clone()
+    for b, i, h in ((0, 3, 2), (1, nodes - 1, 7)):
+        dw.q[b, i, h, 5] = value
+        want[b, i, h] = float("nan")
+    memra.tree_attn(*args)
+    assert memra.read_status(dw.cache) == 0
+    assert torch.equal(torch.isnan(dw.out), torch.isnan(want))
+    assert torch.equal(dw.out.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("D,nodes,ctx", [(128, 9, 200), (128, 9, 2600), (128, 40, 2600), (256, 9, 200), (256, 9, 2600)])
+def test_a_key_that_is_nan_reaches_the_rows_that_see_it(memra, D, nodes, ctx):
+    """fp8's NaN code in one key of one KV head: before the tree (every row sees it), then in the tree's row of a node."""
+    w = W.random_case(71 + D, batch=2, q_len=nodes, n_heads=8, n_kv_heads=2, head_dim=D, k_fmt="fp8", v_fmt="q5_1",
+                      ctx=(ctx - 30, ctx))
+    words = words_for(w, 22)
+    dw, args, _ = check(memra, w, words)
+    clean, h, group, node = dw.out.clone(), 1, 4, nodes // 2
+    pool = dw.cache.k_pool.view(w.num_pages, 2, -1)
+    T = int(w.seq_lens[1])
+    for pos, sees in ((37, np.ones(nodes, bool)), (T - nodes + node, (words[1] >> np.uint64(node)) & np.uint64(1) != 0)):
+        page, t = int(w.page_table[1, pos // 16]), pos % 16
+        byte = ((t // 8 * (D // 64)) * 32 + 4 * (t % 8)) * 16               # element 0 of token t
+        held = pool[page, h, byte].clone()
+        pool[page, h, byte] = 0x7F
+        memra.tree_attn(*args)
+        pool[page, h, byte] = held
+        want = clean.clone()
+        want[1, torch.from_numpy(sees).cuda(), h * group:(h + 1) * group] = float("nan")
+        assert memra.read_status(dw.cache) == 0
+        assert torch.equal(torch.isnan(dw.out), torch.isnan(want))
+        assert torch.equal(dw.out.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
 def test_bad_pages_are_left_out(memra):
     w = W.random_case(12, batch=1, q_len=4, n_heads=8, n_kv_heads=2, ctx=(300, 300))
     words = words_for(w, 8)
