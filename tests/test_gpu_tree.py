@@ -343,6 +343,27 @@ def test_a_key_that_is_nan_reaches_the_rows_that_see_it(memra, D, nodes, ctx):
         assert torch.equal(dw.out.nan_to_num(7.0), want.nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("D,nodes,ctx", [(128, 7, 200), (128, 40, 2600), (256, 7, 2600)])
+def test_a_scale_of_zero(memra, D, nodes, ctx):
+    # means over the keys that a row sees; zeros where it sees none
+    w = W.random_case(72 + D, batch=2, q_len=nodes, n_heads=8, n_kv_heads=2, head_dim=D, ctx=(ctx - 30, ctx))
+    w2 = W.random_case(73 + D, batch=1, q_len=nodes, n_heads=8, n_kv_heads=2, head_dim=D, ctx=(nodes, nodes))
+    for x, seed in ((w, 23), (w2, 24)):
+        words = words_for(x, seed)
+        if x is w2:
+            words[0, ::2] = 0                            # the tree alone: these rows see nothing
+        dw, args = run(memra, x, words)
+        dw.out.fill_(float("nan"))
+        memra.tree_attn(*args[:8], 0.0)
+        assert memra.read_status(dw.cache) == 0
+        flat = type("Flat", (W.Workload,), {"sm_scale": 0.0})(**x.__dict__)
+        want, tol = reference(flat, words)
+        got = dw.out.cpu().numpy().astype(np.float64)
+        assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all()
+        if x is w2:
+            assert (got[0, ::2] == 0).all() and (got[0, 1::2] != 0).any()
+
+
 def test_bad_pages_are_left_out(memra):
     w = W.random_case(12, batch=1, q_len=4, n_heads=8, n_kv_heads=2, ctx=(300, 300))
     words = words_for(w, 8)
