@@ -72,7 +72,12 @@ struct PromptCfg {
   static constexpr int kQStage = kStages - static_cast<int>(kQBytes / kKvBytes);
   static constexpr uint32_t kOffQ = kQSmem ? 0 : kOffKv + kQStage * kKvBytes;
   static constexpr uint32_t kOffBar = kOffKv + kStages * kKvBytes;
-  static constexpr uint32_t kSmem = kOffBar + 256 + 1024;    // 1024: aligning the base
+  // The barriers, 8 bytes each
+  enum Bar { kKvFull = 0, kKvEmpty = kStages, kQFull = 2 * kStages, kSFull = kQFull + 2, kPFull = kSFull + 4,
+             kPvDone = kPFull + 4, kVZeroed = kPvDone + 2, kSRead, kDrained, kSFree = kDrained + 2, kQLanded = kSFree + 2,
+             kBars };
+  static constexpr uint32_t kBarBytes = (8 * kBars + 15) / 16 * 16;
+  static constexpr uint32_t kSmem = kOffBar + kBarBytes + 1024;    // 1024: aligning the base
   static constexpr int kThreads = 128 * kTiles + 96;
   // tensor-memory columns: D 128 scores 0, P 128 + 64 i, O 256 + 128 i; D 256 scores 64 b, Q 128, O 256
   static constexpr uint32_t kQCol = 128, kOCol = 256;
@@ -164,17 +169,17 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   const uint32_t sb = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bars = sb + C::kOffBar;
-  auto kv_full = [&](int s) { return bars + 8 * s; };
-  auto kv_empty = [&](int s) { return bars + 8 * (ST + s); };
-  auto q_full = [&](int i) { return bars + 8 * (2 * ST + i); };
-  auto s_full = [&](int i, int b) { return bars + 8 * (2 * ST + 2 + 2 * i + b); };
-  auto p_full = [&](int i, int b) { return bars + 8 * (2 * ST + 6 + 2 * i + b); };
-  auto pv_done = [&](int i) { return bars + 8 * (2 * ST + 10 + i); };
-  const uint32_t v_zeroed = bars + 8 * (2 * ST + 12), s_read = v_zeroed + 8;
-  auto drained = [&](int which) { return s_read + 8 + 8 * which; };
-  auto s_free = [&](int b) { return s_read + 24 + 8 * b; };
+  auto kv_full = [&](int s) { return bars + 8 * (C::kKvFull + s); };
+  auto kv_empty = [&](int s) { return bars + 8 * (C::kKvEmpty + s); };
+  auto q_full = [&](int i) { return bars + 8 * (C::kQFull + i); };
+  auto s_full = [&](int i, int b) { return bars + 8 * (C::kSFull + 2 * i + b); };
+  auto p_full = [&](int i, int b) { return bars + 8 * (C::kPFull + 2 * i + b); };
+  auto pv_done = [&](int i) { return bars + 8 * (C::kPvDone + i); };
+  const uint32_t v_zeroed = bars + 8 * C::kVZeroed, s_read = bars + 8 * C::kSRead;
+  auto drained = [&](int which) { return bars + 8 * (C::kDrained + which); };
+  auto s_free = [&](int b) { return bars + 8 * (C::kSFree + b); };
   // Q in shared memory; where it goes on to tensor memory, q_full follows when it is there
-  auto q_landed = [&](int i) { return C::kQSmem ? q_full(i) : s_read + 40; };
+  auto q_landed = [&](int i) { return C::kQSmem ? q_full(i) : bars + 8 * C::kQLanded; };
   // columns of tile i's scores and P (score buffer b)
   auto s_col_of = [&](int b) { return static_cast<uint32_t>(NT == 2 ? 0 : b * KT); };
   auto p_col_of = [&](int i, int b) { return static_cast<uint32_t>(NT == 2 ? 128 + 64 * i : b * KT); };

@@ -105,6 +105,7 @@ struct TreeCfg {
   // tensor-memory columns: Q of each row tile, O of each group, two score buffers
   static constexpr uint32_t kQCol = 0, kOCol = MT * kQTmem / 2, kSCol = kOCol + kGroups * kOCols;
   static_assert(kOffPid + 4 * kTreeSplitPages <= kOffK && kRaw >= 2, "page ids; a chunk ahead");
+  static_assert(kOffBar + 8 * (2 * kRaw + 17) + 4 <= kOffPid, "barriers and the tensor-memory address");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kSCol + 2 * kTreeKeys <= kTCols, "tensor memory");
   static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
