@@ -876,6 +876,8 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
       for (int e = 0; e < 2; ++e)
         if (ok && (!C::kTurns || e < n_chunks)) ok = mbar_wait_suspended(pv_done(e), 0, p.status);
     }
+    // A length out of range (flagged) reads rows that nobody may have written: what they make of a row is left out.
+    if (item.bad && !(l > 0.f)) l = 0.f;
     // (every MMA is done: the operand tiles and raw pages are free for the output rows)
     ok = __all_sync(0xffffffffu, ok);
     tc::fence_after_sync();

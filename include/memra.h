@@ -366,7 +366,8 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
  * so that it fills the GPU: the same call gives the same bytes, another batch
  * groups a row's sums differently and may differ in the last bits.  A row that
  * sees no key yields zeros; a query, or a key that a row sees, that is not
- * finite makes the row NaN.  A named node whose V is not finite may also reach
+ * finite makes the row NaN (in a sequence whose length is out of range the
+ * split's keys are left out of the row instead).  A named node whose V is not finite may also reach
  * the tree's rows that do not see it.  A sequence shorter than n_nodes
  * sets MEMRA_DEVERR_BAD_SEQ_LEN; its nodes at positions below 0 are seen by
  * no row and yield zeros.  Keys of a page id outside the pool are left out
