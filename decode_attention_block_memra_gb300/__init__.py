@@ -113,6 +113,14 @@ _SIGS = {
                                              [ctypes.c_int32] * 6 + [ctypes.c_float, ctypes.c_void_p,
                                                                      ctypes.c_size_t, ctypes.c_void_p,
                                                                      ctypes.c_uint64, ctypes.c_void_p]),
+    "memra_testing_prompt_attn_short_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64] * 3 + [ctypes.c_void_p] +
+                                             [ctypes.c_int32] * 5 + [ctypes.c_float, ctypes.c_int32, ctypes.c_void_p,
+                                                                     ctypes.c_void_p, ctypes.c_void_p]),
+    "memra_testing_tree_attn_short_page": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p,
+                                                          ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                                          ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 5 +
+                                           [ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                            ctypes.c_void_p]),
     "memra_testing_scale_division_mismatches": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                                                 ctypes.c_void_p]),
     "memra_read_status": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.POINTER(ctypes.c_int32),
@@ -338,6 +346,11 @@ def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status
     int32 [B + 1]; out fp16 [tokens, Hq, D], dense.  status: a device int32
     the kernel ORs DEVERR_* bits into (KVCache.status will do).
     """
+    a = _prompt_args(q, k, v, cu_seqlens, out, sm_scale, window, status)
+    _check(lib().memra_prompt_attn(*a, _stream(stream)), "memra_prompt_attn")
+
+
+def _prompt_args(q, k, v, cu_seqlens, out, sm_scale, window, status):
     import torch
     T, Hq, D = q.shape
     Hkv = k.shape[1]
@@ -351,10 +364,9 @@ def prompt_attn(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status
                 x.dtype is not torch.float16 or x.get_device() != out.get_device()):
             raise MemraError(1, "memra_prompt_attn")
         strides.append(s[0] if T > 1 else x.shape[1] * D)
-    _check(lib().memra_prompt_attn(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(cu_seqlens),
-                                   int(cu_seqlens.shape[0]) - 1, T, Hq, Hkv, D,
-                                   float(sm_scale if sm_scale is not None else D ** -0.5), int(window), _ptr(out),
-                                   _ptr(status), _stream(stream)), "memra_prompt_attn")
+    return (_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(cu_seqlens),
+            int(cu_seqlens.shape[0]) - 1, T, Hq, Hkv, D, float(sm_scale if sm_scale is not None else D ** -0.5),
+            int(window), _ptr(out), _ptr(status))
 
 
 def tree_attn_workspace_bytes(batch: int, n_nodes: int, n_heads: int, head_dim: int, max_seq_len: int) -> int:
@@ -369,6 +381,11 @@ def tree_attn(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, tree_ma
     tree_mask int64 [B, N]: bit j of word [b, i] shows node j to node i; every
     node sees all keys before the tree.
     """
+    a = _tree_args(cache, q, page_table, seq_lens, max_seq_len, tree_mask, out, workspace, sm_scale)
+    _check(lib().memra_tree_attn(*a, _stream(stream)), "memra_tree_attn")
+
+
+def _tree_args(cache, q, page_table, seq_lens, max_seq_len, tree_mask, out, workspace, sm_scale):
     import torch
     B = q.shape[0]
     device = _need_dense("memra_tree_attn", (q, torch.float16, q.shape), (out, torch.float16, q.shape),
@@ -377,7 +394,8 @@ def tree_attn(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, tree_ma
     if cache.device_index != device or (workspace is not None and workspace.get_device() != device):
         raise MemraError(1, "memra_tree_attn")
     a = _decode_args(cache, q, page_table, seq_lens, max_seq_len, out, workspace, sm_scale)
-    _check(lib().memra_tree_attn(*a[:6], _ptr(tree_mask), *a[6:], _stream(stream)), "memra_tree_attn")
+    # (the decode calls' arguments, the mask behind max_seq_len)
+    return (*a[:6], _ptr(tree_mask), *a[6:])
 
 
 def kv_copy_pages(cache: KVCache, src_pages, dst_pages, n: int | None = None, stream=None) -> None:
@@ -420,6 +438,23 @@ def testing_decode_attn_short_page(cache: KVCache, q, page_table, seq_lens, max_
     a = _decode_args(cache, q, page_table, seq_lens, max_seq_len, out, workspace, sm_scale)
     _check(lib().memra_testing_decode_attn_short_page(*a, int(page_wait_ns), _stream(stream)),
            "memra_testing_decode_attn_short_page")
+
+
+def testing_prompt_attn_short_copy(q, k, v, cu_seqlens, out, sm_scale=None, window: int = 0, status=None,
+                                   stream=None) -> None:
+    """memra_testing_prompt_attn_short_copy (memra_testing.h): prompt attention whose CTA 0 waits for a copy that
+    cannot complete; the waits run out, the CTA's rows become NaN and DEVERR_TIMEOUT is flagged."""
+    a = _prompt_args(q, k, v, cu_seqlens, out, sm_scale, window, status)
+    _check(lib().memra_testing_prompt_attn_short_copy(*a, _stream(stream)),
+           "memra_testing_prompt_attn_short_copy")
+
+
+def testing_tree_attn_short_page(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, tree_mask, out, workspace,
+                                 sm_scale=None, stream=None) -> None:
+    """memra_testing_tree_attn_short_page (memra_testing.h): the same for tree attention's first chunk."""
+    a = _tree_args(cache, q, page_table, seq_lens, max_seq_len, tree_mask, out, workspace, sm_scale)
+    _check(lib().memra_testing_tree_attn_short_page(*a, _stream(stream)),
+           "memra_testing_tree_attn_short_page")
 
 
 def testing_scale_division_mismatches(scales, mismatches, stream=None) -> None:

@@ -1,13 +1,16 @@
-// Entry point of prompt attention in include/memra.h: argument validation and launch.
+// Entry point of prompt attention in include/memra.h: argument validation and launch; its test hook.
 #include "host_checks.cuh"
+#include "memra_testing.h"
 #include "prompt.cuh"
 
 using namespace memra;
 
-extern "C" int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
-                                 int64_t v_stride, const int32_t *cu_seqlens, int32_t batch, int32_t total_tokens,
-                                 int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale, int32_t window,
-                                 void *out, int32_t *status, void *stream) {
+namespace {
+
+int prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                const int32_t *cu_seqlens, int32_t batch, int32_t total_tokens, int32_t n_heads, int32_t n_kv_heads,
+                int32_t head_dim, float sm_scale, int32_t window, void *out, int32_t *status, void *stream,
+                int test_extra_tx = 0) {
   if (batch < 0 || total_tokens < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || window < 0)
     return MEMRA_ERR_INVALID_ARG;
   if (head_dim != 128 && head_dim != 256) return MEMRA_ERR_UNSUPPORTED;
@@ -41,5 +44,26 @@ extern "C" int memra_prompt_attn(const void *q, int64_t q_stride, const void *k,
   p.window = window;
   p.tpt = 128 / p.group;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.test_extra_tx = test_extra_tx;
   return cuda_status(launch_prompt(head_dim, p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const int32_t *cu_seqlens, int32_t batch, int32_t total_tokens,
+                                 int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale, int32_t window,
+                                 void *out, int32_t *status, void *stream) {
+  return prompt_attn(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, batch, total_tokens, n_heads, n_kv_heads,
+                     head_dim, sm_scale, window, out, status, stream);
+}
+
+// memra_testing.h: the same call with a first copy whose wait cannot complete.
+extern "C" int memra_testing_prompt_attn_short_copy(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                                    const void *v, int64_t v_stride, const int32_t *cu_seqlens,
+                                                    int32_t batch, int32_t total_tokens, int32_t n_heads,
+                                                    int32_t n_kv_heads, int32_t head_dim, float sm_scale,
+                                                    int32_t window, void *out, int32_t *status, void *stream) {
+  return prompt_attn(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, batch, total_tokens, n_heads, n_kv_heads,
+                     head_dim, sm_scale, window, out, status, stream, 16);
 }

@@ -1,7 +1,8 @@
-// Entry points of tree attention in include/memra.h: argument validation, the plan, the launches.
+// Entry points of tree attention in include/memra.h: argument validation, the plan, the launches; the test hook.
 #include <algorithm>
 
 #include "host_checks.cuh"
+#include "memra_testing.h"
 #include "tree.cuh"
 
 using namespace memra;
@@ -32,10 +33,14 @@ size_t memra_tree_attn_workspace_bytes(int32_t batch, int32_t n_nodes, int32_t n
   return tree_workspace(static_cast<int64_t>(batch) * n_nodes * n_heads, head_dim, max_seq_len, nullptr);
 }
 
-int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *page_table, int32_t max_pages_per_seq,
-                    const int32_t *seq_lens, int32_t max_seq_len, const uint64_t *tree_mask, int32_t batch,
-                    int32_t n_nodes, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale,
-                    void *workspace, size_t workspace_bytes, void *out, void *stream) {
+}  // extern "C"
+
+namespace {
+
+int tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *page_table, int32_t max_pages_per_seq,
+              const int32_t *seq_lens, int32_t max_seq_len, const uint64_t *tree_mask, int32_t batch, int32_t n_nodes,
+              int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale, void *workspace,
+              size_t workspace_bytes, void *out, void *stream, int test_extra_tx = 0) {
   int st = check_cache(cache);
   if (st) return st;
   if (batch < 0 || n_nodes < 1 || n_heads < 1 || max_seq_len < 0 || max_pages_per_seq < 1)
@@ -98,10 +103,31 @@ int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *p
   p.q_xor = sm_scale < 0.f ? 0x80008000u : 0u;
   if (p.scale_log2 == 0.f) p.scale_log2 = 1.f;
   p.v_post = scaled_format(cache->v_fmt) ? cache->v_scale : 2.f;
+  p.test_extra_tx = test_extra_tx;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = cuda_status(launch_tree(head_dim, cache->k_fmt, cache->v_fmt, p, s));
   if (st || one_split(max_seq_len)) return st;
   return cuda_status(launch_tree_merge(head_dim, p, s));
 }
 
-}  // extern "C"
+}  // namespace
+
+extern "C" int memra_tree_attn(const memra_kv_cache *cache, const void *q, const int32_t *page_table,
+                               int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t max_seq_len,
+                               const uint64_t *tree_mask, int32_t batch, int32_t n_nodes, int32_t n_heads,
+                               int32_t n_kv_heads, int32_t head_dim, float sm_scale, void *workspace,
+                               size_t workspace_bytes, void *out, void *stream) {
+  return tree_attn(cache, q, page_table, max_pages_per_seq, seq_lens, max_seq_len, tree_mask, batch, n_nodes, n_heads,
+                   n_kv_heads, head_dim, sm_scale, workspace, workspace_bytes, out, stream);
+}
+
+// memra_testing.h: the same call with a first chunk whose wait cannot complete.
+extern "C" int memra_testing_tree_attn_short_page(const memra_kv_cache *cache, const void *q, const int32_t *page_table,
+                                                  int32_t max_pages_per_seq, const int32_t *seq_lens,
+                                                  int32_t max_seq_len, const uint64_t *tree_mask, int32_t batch,
+                                                  int32_t n_nodes, int32_t n_heads, int32_t n_kv_heads,
+                                                  int32_t head_dim, float sm_scale, void *workspace,
+                                                  size_t workspace_bytes, void *out, void *stream) {
+  return tree_attn(cache, q, page_table, max_pages_per_seq, seq_lens, max_seq_len, tree_mask, batch, n_nodes, n_heads,
+                   n_kv_heads, head_dim, sm_scale, workspace, workspace_bytes, out, stream, 16);
+}

@@ -181,6 +181,18 @@ __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// The same barrier, and whether x holds in all of its threads.
+__device__ __forceinline__ bool named_barrier_and(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+      "bar.red.and.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+
 // ------------------------------------------------------------ tensor cores --
 
 // D = A * B + C, m16n8k16, fp16 inputs, fp32 accumulators (warp-wide).

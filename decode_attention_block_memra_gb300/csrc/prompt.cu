@@ -74,8 +74,8 @@ struct PromptCfg {
   static constexpr uint32_t kOffBar = kOffKv + kStages * kKvBytes;
   // The barriers, 8 bytes each
   enum Bar { kKvFull = 0, kKvEmpty = kStages, kQFull = 2 * kStages, kSFull = kQFull + 2, kPFull = kSFull + 4,
-             kPvDone = kPFull + 4, kVZeroed = kPvDone + 2, kSRead, kDrained, kSFree = kDrained + 2, kQLanded = kSFree + 2,
-             kBars };
+             kPvDone = kPFull + 4, kVZeroed = kPvDone + 2, kSRead, kDrained, kSFree = kDrained + 2,
+             kQLanded = kSFree + 2, kBars };
   static constexpr uint32_t kBarBytes = (8 * kBars + 15) / 16 * 16;
   static constexpr uint32_t kSmem = kOffBar + kBarBytes + 1024;    // 1024: aligning the base
   static constexpr int kThreads = 128 * kTiles + 96;
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         if (!C::kQSmem && n == C::kQStage) ok = mbar_wait_suspended(q_full(0), 0, p.status);   // Q has left the ring
         if (ok && n >= ST) ok = mbar_wait_suspended(kv_empty(s), (n / ST - 1) & 1, p.status);
         if (!ok) break;
-        mbar_arrive_expect_tx(kv_full(s), C::kKvBytes);
+        mbar_arrive_expect_tx(kv_full(s), C::kKvBytes + (n == 0 && blockIdx.x == 0 ? p.test_extra_tx : 0));
 #pragma unroll
         for (int c = 0; c < C::kBlocks; ++c)
           tma_load_3d(sb + C::kOffKv + s * C::kKvBytes + c * KT * 128, n & 1 ? &vmap : &kmap, 64 * c, kvh,
@@ -562,6 +562,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         const int64_t at = __shfl_sync(0xffffffffu, to, row);
         if (at >= 0) *reinterpret_cast<uint4 *>(p.out + at + 8 * u) = x;
       }
+    } else if (n_steps > 0 && live) {               // a wait gave up: NaN, and no part of a sum
+      uint4 *row = reinterpret_cast<uint4 *>(p.out + row_at());
+#pragma unroll 1
+      for (int u = 0; u < D / 8; ++u) row[u] = make_uint4(kNanPair, kNanPair, kNanPair, kNanPair);
     }
   }
   tc::fence_before_sync();

@@ -18,6 +18,7 @@ struct PromptParams {
   int batch, total, n_heads, n_kv_heads, group, window;
   int tpt;                        // tokens per 128-row tile: 128 / group
   float scale_log2;               // sm_scale * log2(e)
+  int test_extra_tx;              // the test hook's: bytes that CTA 0 expects beyond its first copy of K (0 elsewhere)
 };
 
 cudaError_t launch_prompt(int D, const PromptParams &p, cudaStream_t st);

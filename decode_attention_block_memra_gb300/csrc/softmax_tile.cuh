@@ -7,6 +7,9 @@
 
 namespace memra {
 
+// Two fp16 NaN; as one float32, NaN too: what rows hold whose kernel gave up a wait.
+constexpr uint32_t kNanPair = 0x7FFF7FFFu;
+
 // Largest of N scores (float bits).
 template <int N>
 __device__ __forceinline__ float row_max(const uint32_t (&s)[N]) {

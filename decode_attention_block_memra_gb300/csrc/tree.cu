@@ -549,7 +549,8 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
     const int s = ci % RAW, n = __popc(__ballot_sync(0xffffffffu, pid >= 0)) / 2;
     if (lane == 0) {
       if (n)
-        mbar_arrive_expect_tx(raw_full(s), n * (C::kKSeg + C::kVSeg));
+        mbar_arrive_expect_tx(raw_full(s),
+                              n * (C::kKSeg + C::kVSeg) + (ci == 0 && blockIdx.x == 0 ? p.test_extra_tx : 0));
       else
         mbar_arrive(raw_full(s));
     }
@@ -884,13 +885,12 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
     // O = sum of w[e] O_e over the row's groups
     float w[C::kStep];
     if constexpr (C::kTurns) {
-      // this group's (m, l) for the other, l < 0 after a wait that gave up
+      // this group's (m, l) for the other
       const uint32_t ml = sb + C::kOffMl + rl * 8;
-      sts64(ml + g * kTileRows * 8, __float_as_uint(m), __float_as_uint(ok ? l : -1.f));
+      sts64(ml + g * kTileRows * 8, __float_as_uint(m), __float_as_uint(l));
       named_barrier_sync(3, 32 * 8);
       const float m1 = __uint_as_float(lds32(ml + (g ^ 1) * kTileRows * 8));
       const float l1 = __uint_as_float(lds32(ml + (g ^ 1) * kTileRows * 8 + 4));
-      ok = __all_sync(0xffffffffu, ok && !(l1 < 0.f));
       // (a sum of NaN, from a query or a key that is not finite, is no empty one: the row becomes NaN)
       const float top = fmaxf(m, m1);
       const float mine = l != 0.f ? fast_exp2(m - top) : 0.f, other = l1 != 0.f ? fast_exp2(m1 - top) : 0.f;
@@ -950,20 +950,22 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
                                                __float_as_uint(x[e + 2]), __float_as_uint(x[e + 3])));
       }
     }
-    if (live && ns > 1 && (!C::kTurns || g == 0))                // -inf, never weighed, without a visible key or after a wait that gave up
-      p.lse_part[static_cast<int64_t>(row_id(r)) * p.max_splits + item.split] = ok && l != 0.f ? m + __log2f(l) : -INFINITY;
     // The rows to memory, each by a whole warp (a bulk copy per row took 100 clocks
     // to issue, 32 of them one after another).
     constexpr int WR = 32 / C::kStep;        // rows of a warp
     const int wr = r0 + WR * warp + lane;
     const int64_t id = lane < WR && wr < rows ? static_cast<int64_t>(row_id(wr)) : -1;
     if constexpr (C::kTurns)
-      named_barrier_sync(3, 32 * 8);         // both halves of the rows are there
+      ok = named_barrier_and(3, 32 * 8, ok);         // both halves of the rows are there
     else
       __syncwarp();
+    if (live && ns > 1 && (!C::kTurns || g == 0))                // -inf, never weighed, without a visible key
+      p.lse_part[static_cast<int64_t>(row_id(r)) * p.max_splits + item.split] =
+          !ok ? __uint_as_float(kNanPair) : l != 0.f ? m + __log2f(l) : -INFINITY;
     const uint32_t row0 = sb + C::kOffK + warp * WR * C::kRowBytes;
     constexpr int BATCH = 8;                 // rows in flight
-    auto write_rows = [&](auto units, auto to_row) {     // 16-byte units of a row; a row's address
+    // 16-byte units of a row, a row's address; NaN after a wait that gave up
+    auto write_rows = [&](auto units, auto to_row) {
       constexpr int U = decltype(units)::value;
 #pragma unroll 1
       for (int e0 = 0; e0 < WR; e0 += BATCH) {
@@ -972,7 +974,9 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
         for (int e = 0; e < BATCH; ++e)
 #pragma unroll
           for (int c = 0; c < U; c += 32)
-            if (U >= 32 || lane < U) x[e][c / 32] = lds128(row0 + (e0 + e) * C::kRowBytes + (c + lane) * 16);
+            if (U >= 32 || lane < U)
+              x[e][c / 32] = ok ? lds128(row0 + (e0 + e) * C::kRowBytes + (c + lane) * 16)
+                                : make_uint4(kNanPair, kNanPair, kNanPair, kNanPair);
 #pragma unroll
         for (int e = 0; e < BATCH; ++e) {
           const int64_t to = __shfl_sync(0xffffffffu, id, e0 + e);
@@ -982,9 +986,9 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
         }
       }
     };
-    if (ok && ns == 1)
+    if (ns == 1)
       write_rows(std::integral_constant<int, D / 8>{}, [&](int64_t to) { return reinterpret_cast<uint4 *>(p.out + to * D); });
-    if (ok && ns > 1)
+    else
       write_rows(std::integral_constant<int, D / 4>{}, [&](int64_t to) {
         return reinterpret_cast<uint4 *>(p.o_part + (to * p.max_splits + item.split) * D);
       });

@@ -75,6 +75,7 @@ struct TreeParams {
   float scale_log2;             // |sm_scale| * (post-scale of the staged K values) * log2(e); 1 for sm_scale 0
   uint32_t q_and, q_xor;        // applied to the query's fp16 pairs: the scale's sign, or zeros for sm_scale 0
   float v_post;                 // post-scale of the staged V values
+  int test_extra_tx;            // the test hook's: bytes that CTA 0 expects beyond its first chunk's (0 elsewhere)
 };
 
 cudaError_t launch_tree(int D, int kf, int vf, const TreeParams &p, cudaStream_t st);

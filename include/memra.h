@@ -105,7 +105,8 @@ typedef enum {
 #define MEMRA_DEVERR_BAD_SLOT    2   /* append slot >= num_pages*16, or an accepted node that
                                         is not one of the tree's: row skipped             */
 #define MEMRA_DEVERR_BAD_SEQ_LEN 4   /* seq_len < q_len, > max_seq_len or > table: clamped */
-#define MEMRA_DEVERR_TIMEOUT     8   /* a pipeline wait gave up after ~1 s: result invalid */
+#define MEMRA_DEVERR_TIMEOUT     8   /* a pipeline wait gave up after ~1 s: result invalid (prompt
+                                        and tree attention: the rows it concerns are NaN) */
 #define MEMRA_DEVERR_PREFIX     16   /* cascade: a page table differs from the first sequence's
                                         within the shared prefix: that row used the first's pages */
 

@@ -67,3 +67,55 @@ def test_the_hook_rejects_limits_outside_its_range(memra):
                                                  dw.out, dw.workspace, page_wait_ns=bad)
         assert e.value.status == 1
     assert memra.read_status(dw.cache) == 0
+
+
+@pytest.mark.parametrize("D,n", [(128, 100), (128, 1500), (256, 40), (256, 1500)])
+def test_prompt_rows_of_a_wait_that_runs_out_are_nan(memra, D, n):
+    """The last piece of the first prompt, first KV head (2 x 32 tokens of four heads at head_dim 128, 32 at 256): NaN;
+    every other row as always; the next call exact."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    rows = torch.randn(n + 90, 12, D, device="cuda", generator=g).half()
+    q, k, v = rows[:, :8], rows[:, 8:10], rows[:, 10:]
+    cu = torch.tensor([0, n, n + 90], dtype=torch.int32, device="cuda")
+    want, out = (torch.empty(n + 90, 8, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    memra.prompt_attn(q, k, v, cu, want, status=status)
+    assert int(status) == 0
+    t0 = time.monotonic()
+    memra.testing_prompt_attn_short_copy(q, k, v, cu, out, status=status)
+    assert int(status) == memra.DEVERR_TIMEOUT
+    assert time.monotonic() - t0 < 30.0
+    piece = 64 if D == 128 else 32
+    lost = torch.zeros(n + 90, 8, dtype=torch.bool, device="cuda")
+    lost[(n - 1) // piece * piece:n, :4] = True
+    assert bool(torch.isnan(out[lost]).all()) and torch.equal(out[~lost], want[~lost])
+    status.zero_()
+    memra.prompt_attn(q, k, v, cu, out, status=status)
+    assert int(status) == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D,nodes,ctx", [(128, 9, 200), (128, 9, 2600), (128, 40, 200), (128, 40, 2600), (256, 9, 200),
+                                         (256, 9, 2600), (256, 40, 2600)])
+def test_tree_rows_of_a_wait_that_runs_out_are_nan(memra, D, nodes, ctx):
+    """The first sequence's first split, first KV head (four heads; 32 nodes a row tile, two of them at head_dim 128):
+    its rows are NaN, also where other splits of theirs are whole; every other row as always; the next call exact."""
+    from decode_attention_block_memra_gb300.runner import upload
+    w = W.random_case(80 + D, batch=2, q_len=nodes, n_heads=8, n_kv_heads=2, head_dim=D, ctx=(ctx - 30, ctx))
+    dw = upload(w)
+    memra.kv_append(dw.cache, dw.step_k, dw.step_v, dw.step_slots)
+    words = torch.tril(torch.ones(nodes, nodes, dtype=torch.int64)) @ (1 << torch.arange(nodes))
+    mask = words.expand(2, nodes).contiguous().cuda()
+    ws = torch.empty(memra.tree_attn_workspace_bytes(2, nodes, 8, D, w.max_seq_len), dtype=torch.uint8, device="cuda")
+    args = (dw.cache, dw.q, dw.page_table, dw.seq_lens, w.max_seq_len, mask)
+    want, out = torch.empty_like(dw.q), torch.empty_like(dw.q)
+    memra.tree_attn(*args, want, ws)
+    assert memra.read_status(dw.cache) == 0 and bool(torch.isfinite(want).all())
+    t0 = time.monotonic()
+    memra.testing_tree_attn_short_page(*args, out, ws)
+    assert memra.read_status(dw.cache) == memra.DEVERR_TIMEOUT
+    assert time.monotonic() - t0 < 30.0
+    lost = torch.zeros(2, nodes, 8, dtype=torch.bool, device="cuda")
+    lost[0, :64 if D == 128 else 32, :4] = True
+    assert bool(torch.isnan(out[lost]).all()) and torch.equal(out[~lost], want[~lost])
+    memra.tree_attn(*args, out, ws)
+    assert memra.read_status(dw.cache) == 0 and torch.equal(out, want)

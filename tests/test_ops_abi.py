@@ -140,3 +140,12 @@ def test_tree_checks(memra):
     assert memra.tree_attn_workspace_bytes(2, 8, 8, 64, 5000) == 0
     # 262,144 tokens: 160 partials a row, whatever the device
     assert memra.tree_attn_workspace_bytes(1, 64, 32, 128, 262144) == 16 + 64 * 32 * 160 * 129 * 4
+
+
+def test_hooks_of_the_bounded_waits_check_as_the_plain_calls(memra):
+    L, c = memra.lib(), cache(memra)
+    for heads, batch, want in ((7, 2, INVALID), (8, -1, INVALID), (2 * 129, 2, UNSUPPORTED), (8, 0, 0)):
+        assert L.memra_testing_prompt_attn_short_copy(64, 128 * 258, 64, 256, 64, 256, 64, batch, 10, heads, 2, 128, 0.1,
+                                                      0, 64, 0, None) == want
+        assert L.memra_testing_tree_attn_short_page(ctypes.byref(c), 64, 64, 4, 64, 64, 64, batch, 8, heads, 2, 128, 0.1,
+                                                    64, 1 << 20, 64, None) == want
