@@ -355,7 +355,8 @@ def _prompt_args(q, k, v, cu_seqlens, out, sm_scale, window, status):
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     _need_dense("memra_prompt_attn", (out, torch.float16, q.shape), (cu_seqlens, torch.int32, cu_seqlens.shape))
-    if status is not None and status.get_device() != out.get_device():
+    if cu_seqlens.dim() != 1 or (status is not None and (status.dtype is not torch.int32 or status.numel() < 1 or
+                                                         status.get_device() != out.get_device())):
         raise MemraError(1, "memra_prompt_attn")
     strides = []
     for x in (q, k, v):

@@ -336,3 +336,15 @@ def test_binding_refuses_other_layouts(memra):
             memra.prompt_attn(*args)
     with pytest.raises(memra.MemraError):
         memra.prompt_attn(q, k, k, cu, q, status=torch.zeros(1, dtype=torch.int32))
+
+
+def test_binding_refuses_a_nested_list_and_other_status_words(memra):
+    """[[0, 4]] would be no sequence at all, and the kernel writes 32 bits of the status word."""
+    q = torch.zeros(4, 8, 128, device="cuda").half()
+    k = torch.zeros(4, 2, 128, device="cuda").half()
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    with pytest.raises(memra.MemraError):
+        memra.prompt_attn(q, k, k, cu[None], q)
+    for dtype, n in ((torch.uint8, 4), (torch.int64, 1), (torch.float32, 1), (torch.int32, 0)):
+        with pytest.raises(memra.MemraError):
+            memra.prompt_attn(q, k, k, cu, q, status=torch.zeros(n, dtype=dtype, device="cuda"))
