@@ -7,6 +7,32 @@
 
 namespace memra {
 
+// Two floats as an fp16 pair; what is past fp16's range is cut to its largest value (infinities too; NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_half2_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two float32 products in one instruction.
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// named_barrier_sync, and whether x holds in all of its threads.
+__device__ __forceinline__ bool named_barrier_and(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+      "bar.red.and.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+
 // Two fp16 NaN; as one float32, NaN too: what rows hold whose kernel gave up a wait.
 constexpr uint32_t kNanPair = 0x7FFF7FFFu;
 
