@@ -128,3 +128,56 @@ def test_prompt_fork_tree_compact_decode(memra, kf, vf, D):
         kh = dequantized(np.concatenate([held_k[b], sk[b]]), kf, ks)
         vh = dequantized(np.concatenate([held_v[b], sv[b]]), vf, vs)
         assert np.abs(got[b] - attention.attention_rows(sq[b], kh, vh, scale)).max() <= TOL
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_tensor_memory_kernels_side_by_side(memra, D):
+    """Prompt, tree and cascade calls on three streams at once, each with its own workspace: the same bytes as alone.
+
+    All three hold tensor memory; none of their CTAs may wait for another kernel's that waits for it."""
+    import workloads as W
+    from decode_attention_block_memra_gb300.runner import upload
+    g = torch.Generator(device="cuda").manual_seed(D)
+    rows = torch.randn(3000, 12, D, device="cuda", generator=g).half()
+    cu = torch.tensor([0, 1700, 1750, 3000], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = W.make_workload("tree", batch=6, q_len=7, n_heads=16, n_kv_heads=2, head_dim=D, k_fmt="q8_0", v_fmt="q5_1",
+                        seed=1, seq_lens=[900, 2000, 70, 3100, 1500, 400], permute_pages=True)
+    c = W.make_workload("cascade", batch=6, q_len=1, n_heads=16, n_kv_heads=2, head_dim=D, k_fmt="q8_0", v_fmt="q5_1",
+                        seed=2, seq_lens=[2100, 2300, 2031, 3100, 2025, 2400], shared_prefix=2016)
+    dw, dc = upload(w), upload(c)
+    for x in (dw, dc):
+        memra.kv_append(x.cache, x.step_k, x.step_v, x.step_slots)
+    mask = torch.full((6, 7), -1, dtype=torch.int64, device="cuda")
+
+    def calls():
+        outs = [torch.empty(3000, 8, D, dtype=torch.float16, device="cuda"), torch.empty_like(dw.q),
+                torch.empty_like(dc.q)]
+        sizes = (memra.tree_attn_workspace_bytes(6, 7, 16, D, w.max_seq_len),
+                 memra.decode_attn_cascade_workspace_bytes(6, 1, 16, D, c.max_seq_len, 2016))
+        tws, cws = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes)
+        return outs, (
+            lambda s: memra.prompt_attn(rows[:, :8], rows[:, 8:10], rows[:, 10:], cu, outs[0], status=status, stream=s),
+            lambda s: memra.tree_attn(dw.cache, dw.q, dw.page_table, dw.seq_lens, w.max_seq_len, mask, outs[1], tws,
+                                      stream=s),
+            lambda s: memra.decode_attn_cascade(dc.cache, dc.q, dc.page_table, dc.seq_lens, c.max_seq_len, 2016, outs[2],
+                                                cws, stream=s))
+
+    want, alone = calls()
+    for call in alone:
+        call(None)
+        torch.cuda.synchronize()
+    got, together = calls()
+    streams = [torch.cuda.Stream() for _ in together]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for call, s in zip(together, streams):
+            call(s)
+    torch.cuda.synchronize()
+    for _ in range(30):                                  # and behind one another on one stream, early launches overlapping
+        for call in together:
+            call(streams[0])
+    torch.cuda.synchronize()
+    assert int(status) == 0 and memra.read_status(dw.cache) == 0 and memra.read_status(dc.cache) == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
