@@ -1,7 +1,9 @@
-// Staging of quantized pages for the fifth-generation tensor cores: raw K and
-// V words of a page segment in shared memory to fp16 operand values (hi, and
-// for the block-scaled integer formats the low part of an exact pair), shared
-// by the kernels that dequantize pages into tensor-core tiles.
+// Shared-memory accesses and fp16 pieces of the kernels that feed the
+// fifth-generation tensor cores; and, for the prefix passes of cascade.cu, the
+// staging of quantized pages: raw K and V words of a page segment in shared
+// memory to fp16 operand values (hi, and for the block-scaled integer formats the
+// low part of an exact pair).  The tree kernel stages whole runs of codes and has
+// its own.
 #pragma once
 
 #include <cuda_fp16.h>

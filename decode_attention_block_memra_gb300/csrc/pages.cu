@@ -16,7 +16,8 @@ constexpr int kCopyUnroll = 4;                      // 16-byte units in flight p
 // contiguous run per pool.  CTA = one page's run of kCopyThreads * kCopyUnroll
 // 16-byte units (K's first, then V's), every load of a thread in flight before
 // its first store.  Bound by HBM: 16,384 pages of 14,848 bytes in 73.2 us (6,650
-// GB/s, 98% of the copy peak); a list of 16 pages takes 1.5 us, launch included.
+// GB/s, 98% of the copy peak); a list of 16 pages takes 1.5 us in a replayed graph and
+// 4.8 to 5.9 us as a call, which is the host's launch.
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPagesParams p) {
   grid_dependency_wait();
   allow_dependent_launch();

@@ -35,13 +35,13 @@
 // fp16 part moves to the row's place in `out`, over a power of two that keeps it
 // in range, and what is left of it, exact in float32, stays in O as the start of
 // the next sum: no bit is lost and no scratch is needed.  On 16,384 tokens this takes
-// 1% of the time (1,459 to 1,474 us; as a branch inside the step loop, where its
-// registers spill the loop's, 1,640).
+// 0.5 to 1% of the time (1,459 to 1,467 .. 1,474 us; as a branch inside the step loop,
+// where its registers spill the loop's, 1,640).
 // What bounds it: the tensor cores.  16,384 tokens, 32/4 heads, D 128: 1.47 ms a
 // call in a loop (1,500 TFLOP/s, the power cap on), 1.28 ms for a single one, the
-// tensor pipe active 77% of the time; 8 ragged prompts of up to 4,860 tokens 510 us
-// (1,283 TFLOP/s); 9,713 tokens, 16/2 heads, D 256, window 1,024: 148 us (940
-// TFLOP/s, 17 steps a CTA); 256 tokens, 8/2 heads: 8.5 us, all latency.
+// tensor pipe active 78% of the time; 8 ragged prompts of up to 4,860 tokens 490 to
+// 519 us (1,263 to 1,337 TFLOP/s, 67%); 9,713 tokens, 16/2 heads, D 256, window 1,024:
+// 149 us (935 TFLOP/s, 44%, 17 steps a CTA); 256 tokens, 8/2 heads: 9.1 us, all latency.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

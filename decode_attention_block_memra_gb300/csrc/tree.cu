@@ -22,13 +22,15 @@
 // an SM, which also leave twice the partial rows to the merge).  Four of the eight
 // staging warps take every other chunk (all eight on each: 44.8 for 39.8 us below).
 // head_dim 256: one group, two score buffers, the scores a chunk ahead.
-// What bounds it is the staging and the tensor cores' operand reads: both share a
-// shared memory of 128 bytes a clock, and a chunk of q8_0/q5_1 is 28 KB in, 64 KB
-// of tiles out, and 66 KB read by the MMAs of each row tile, for 1,060 clocks of
-// MMAs and 4,900 warp instructions.  8 sequences x 16 nodes over 6,316 keys (32/4
-// heads, D 128, q8_0/q5_1): 40.1 us a call, 5 of them the merge, for 47 MB of pages (4
-// splits a sequence on 128 of 152 SMs: 5 would not fit); 64 nodes over 262,144 keys:
-// 366 us; 31 nodes on 12 ragged sequences, D 256, fp8: 75.5 us.
+// What bounds it: no unit is saturated; the time is in chains of waits.  A chunk
+// of q8_0/q5_1 is 28 KB in, 64 KB of tiles out and 66 KB read by the MMAs of each
+// row tile through a shared memory of 128 bytes a clock, 1,060 clocks of MMAs and
+// 4,900 warp instructions, and takes 1,810 clocks with one row tile: the one issuing
+// thread finds its operands ready.  8 sequences x 16 nodes over 6,316 keys (32/4 heads,
+// D 128, q8_0/q5_1): 40.2 us a call, 5.5 of them the merge, for 47 MB of pages (4
+// splits a sequence on 128 of 152 SMs: 5 would not fit), tensor pipe 33%, shared memory
+// 50 to 60%; 64 nodes over 262,144 keys: 370 us, both 69%; 31 nodes on 12 ragged
+// sequences, D 256, fp8: 75.3 us, 38% and 68%.
 // A sequence of one split writes its rows directly; the others leave (o, lse)
 // partials that tree_merge_kernel joins.
 #include <cuda_fp16.h>
@@ -59,8 +61,10 @@ struct TreeCfg {
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
   static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
   // Staging warps in two groups that take the chunks by turns, each with K^ and V^ tiles of its own;
-  // at head_dim 256, where shared memory holds no two pairs, with NVFP4 and fp8 only (12 sequences x 31
-  // nodes over 3,000 keys: 45.1 for 48.0 us), but not with fp8 alone, whose staging is short (39.1 for 38.4).
+  // at head_dim 256, where shared memory holds two pairs of single values only, with NVFP4 for K, V or both
+  // beside fp8 (12 sequences x 31 nodes over 3,000 keys, one group / two: fp8/nvfp4 46.5 / 44.8, nvfp4/fp8
+  // 41.2 / 38.6, nvfp4/nvfp4 49.0 / 46.1 us; 1 x 32 over 65,536: 63.8 / 59.1, 53.9 / 48.3, 69.4 / 64.0), but
+  // not with fp8 alone, whose staging is short (38.3 / 39.6 and 48.7 / 50.9; 8 x 8 over 4,104: 23.2 / 22.6).
   static constexpr bool kNv = KF == MEMRA_KV_NVFP4 || VF == MEMRA_KV_NVFP4;
   static constexpr int kStageGroups = D == 128 || (kNv && !kKLo && !kVLo) ? 2 : 1, kStageWarps = 8 / kStageGroups;
   static constexpr int kStageWarp0 = 4 * kGroups, kMmaWarp = kStageWarp0 + 8, kCopyWarp = kMmaWarp + 1;

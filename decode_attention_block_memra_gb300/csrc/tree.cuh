@@ -15,7 +15,8 @@ constexpr int kTreeKeys = 64;
 
 // Row tiles (128 rows: nodes x the group's heads) of a CTA, one CTA to an SM: two
 // past 128 rows at head_dim 128, so that a page is dequantized once for both (64
-// nodes x 8 heads over 262,144 keys: 363 us, 438 with two CTAs of one tile).
+// nodes x 8 heads over 262,144 keys: 363 us when it was built, 438 with two CTAs of
+// one tile; 370 now).
 __host__ __device__ constexpr int tree_tiles(int D, int rows) { return D == 128 && rows > 128 ? 2 : 1; }
 
 // The split plan.  A call's keys, in chunks of kTreeKeys, are cut so that one
@@ -69,7 +70,7 @@ struct TreeParams {
   int32_t *status;
   int batch, n_nodes, n_heads, group, n_kv_heads, num_pages, max_pages, max_seq_len;
   int len_limit;                // min(max_seq_len, tokens of a page table's row): lengths are clamped to it
-  int slots;                    // CTAs of a wave per (KV head, rows of a CTA), 0: sequences are cut at kTreeMaxChunks only (or not at all)
+  int slots;                    // CTAs of a wave per (KV head, rows of a CTA); 0: sequences are cut at kTreeMaxChunks only
   int max_splits;               // partials per row in the workspace
   int row_ctas;                 // CTAs over the rows of one KV head
   float scale_log2;             // |sm_scale| * (post-scale of the staged K values) * log2(e); 1 for sm_scale 0
