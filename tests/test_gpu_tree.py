@@ -263,6 +263,34 @@ def test_long_sums_keep_their_precision(memra, kf, vf):
 
 
 @pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("kf,vf", [("q8_0", "q5_1"), ("fp8", "q4_0"), ("fp8", "fp8"), ("nvfp4", "nvfp4")])
+def test_long_means_keep_their_precision(memra, kf, vf, D):
+    """Equal scores over 15,000 keys, in splits of up to 7,680: every weight is 1 exactly, every row a mean.
+
+    Left are the output's rounding (half a step of fp16 at its value, which
+    V^'s rounding can bring above 2) and the float32 sums: 480 steps of 16 keys in
+    a split, two products each where V^ is a pair, every one off by at most
+    2^-21 of the sum so far, half of its end on average: 2^-12 relative.
+    """
+    w = W.make_workload("long_means", batch=1, q_len=64, n_heads=16 * 4, n_kv_heads=16, head_dim=D, k_fmt=kf,
+                        v_fmt=vf, seed=20, seq_lens=[15_000])
+    w.q[:] = 0
+    rng = np.random.default_rng(20)
+    w.v_rows[:] = (1.9 + 0.09 * rng.random(w.v_rows.shape)).astype(np.float16)
+    words = np.stack([chain(64)])
+    dw, _ = run(memra, w, words)
+    assert memra.read_status(dw.cache) == 0
+    got = dw.out.cpu().numpy().astype(np.float64)
+    rows = attention.sequence_rows(w, 0)
+    for h in (0, 15):
+        cache = quant.quantize_rows(w.v_rows[:, h], vf, w.v_scale)
+        v = quant.dequantize_rows(quant.select_rows(cache, rows)).astype(np.float64)
+        want = np.cumsum(v, 0)[-64:] / np.arange(len(v) - 63, len(v) + 1)[:, None]
+        tol = np.spacing(want.astype(np.float16)).astype(np.float64) / 2 + 2.0 ** -12 * want
+        assert (np.abs(got[0, :, 4 * h:4 * h + 4] - want[:, None]) <= tol[:, None]).all()
+
+
+@pytest.mark.parametrize("D", [128, 256])
 def test_alone_and_batched(memra, D):
     """A sequence alone (cut into other splits) within the tolerance; the same call twice, the same bytes."""
     w = W.random_case(9, batch=3, q_len=6, n_heads=16, n_kv_heads=2, head_dim=D, ctx=(300, 3000))
