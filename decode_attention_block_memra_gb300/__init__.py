@@ -55,6 +55,10 @@ class KVCacheStruct(ctypes.Structure):
 
 _LIB = None
 
+_CHUNK_ARGS = ([ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 6 +
+               [ctypes.c_float, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t] + [ctypes.c_void_p] * 3)
+
 _SIGS = {
     "memra_kv_segment_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
     "memra_kv_pool_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 6),
@@ -108,6 +112,17 @@ _SIGS = {
     "memra_kv_compact": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int32,
                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+    "memra_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64] * 3 + [ctypes.c_void_p] * 2 +
+                           [ctypes.c_float] + [ctypes.c_void_p] * 2 + [ctypes.c_int32] * 6 +
+                           [ctypes.c_void_p, ctypes.c_int64] * 2 + [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p,
+                                                                    ctypes.c_void_p]),
+    "memra_chunk_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "memra_chunk_attn": (ctypes.c_int, _CHUNK_ARGS),
+    "memra_testing_chunk_attn_short_page": (ctypes.c_int, _CHUNK_ARGS),
+    "memra_kv_evict": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                      ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p] +
+                       [ctypes.c_int32] * 3 + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                               ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
     "memra_testing_decode_attn_short_page": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p,
                                                             ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p] +
                                              [ctypes.c_int32] * 6 + [ctypes.c_float, ctypes.c_void_p,
@@ -432,6 +447,117 @@ def kv_compact(cache: KVCache, page_table, seq_lens, max_seq_len: int, accepted,
     _check(rc, "memra_kv_compact")
 
 
+def _row_stride(where: str, x, heads: int, dim: int, device: int) -> int:
+    """The token stride of rows x fp16 [tokens, heads, dim] on `device` whose heads lie side by side; refuses others."""
+    import torch
+    s = x.stride()
+    if (x.dim() != 3 or x.shape[1:] != (heads, dim) or x.dtype is not torch.float16 or x.get_device() != device or
+            s[2] != 1 or (heads > 1 and s[1] != dim)):
+        raise MemraError(1, where)
+    return s[0] if x.shape[0] > 1 else heads * dim
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, cache: KVCache | None = None, v=None, slot_mapping=None,
+                 stream=None) -> None:
+    """memra_qk_norm_rope: norm and rotation of query and key rows, and their append, in one pass.
+
+    q fp16 [tokens, Hq, D], k and v fp16 [tokens, Hkv, D], any token stride;
+    q_weight, k_weight float32 [D] or None (no norm); positions int32 [tokens]
+    and inv_freq float32 [rotary_dim / 2] (None: no rotation).  q_out and k_out
+    are rows like q and k (or q and k themselves).  cache, v and slot_mapping
+    int32 [tokens] together store the finished rows; k is None if it goes nowhere.
+    """
+    import torch
+    where = "memra_qk_norm_rope"
+    T, Hq, D = q.shape
+    Hkv = k.shape[1] if k is not None else 1
+    device = _device()
+    a = []
+    for x, heads in ((q, Hq), (k, Hkv), (v, Hkv), (q_out, Hq), (k_out, Hkv)):
+        if x is not None and x.shape[0] != T:
+            raise MemraError(1, where)
+        a.append((_ptr(x), _row_stride(where, x, heads, D, device) if x is not None else 0))
+    f32, i32 = torch.float32, torch.int32
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    _need_dense(where, *((t, dtype, shape) for t, dtype, shape in (
+        (q_weight, f32, (D,)), (k_weight, f32, (D,)), (positions, i32, (T,)), (inv_freq, f32, (half,)),
+        (slot_mapping, i32, (T,))) if t is not None))
+    if cache is not None and cache.device_index != device:
+        raise MemraError(1, where)
+    rc = lib().memra_qk_norm_rope(*a[0], *a[1], *a[2], _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions),
+                                  _ptr(inv_freq), 2 * half, int(bool(interleaved)), T, Hq, Hkv, D, *a[3], *a[4],
+                                  cache.ref if cache is not None else None, _ptr(slot_mapping), _stream(stream))
+    _check(rc, where)
+
+
+def chunk_attn_workspace_bytes(head_dim: int) -> int:
+    return int(lib().memra_chunk_attn_workspace_bytes(head_dim))
+
+
+def chunk_attn(cache: KVCache, q, cu_seqlens, page_table, seq_lens, max_seq_len: int, out, workspace, sm_scale=None,
+               window: int = 0, lse=None, stream=None) -> None:
+    """memra_chunk_attn: attention of the new tokens of every sequence over the cache that holds them and their context.
+
+    q fp16 [tokens, Hq, D] (any token stride), sequence b's rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1 (int32 [B + 1]); seq_lens int32 [B] include them; out
+    fp16 [tokens, Hq, D]; lse float32 [tokens, Hq] or None; workspace of
+    chunk_attn_workspace_bytes(D) bytes.  window > 0: page_table rows are rings.
+    """
+    a = _chunk_args(cache, q, cu_seqlens, page_table, seq_lens, max_seq_len, out, workspace, sm_scale, window, lse)
+    _check(lib().memra_chunk_attn(*a, _stream(stream)), "memra_chunk_attn")
+
+
+def _chunk_args(cache, q, cu_seqlens, page_table, seq_lens, max_seq_len, out, workspace, sm_scale, window, lse):
+    import torch
+    where = "memra_chunk_attn"
+    T, Hq, D = q.shape
+    B, pages = page_table.shape
+    i32 = torch.int32
+    wanted = [(out, torch.float16, (T, Hq, D)), (cu_seqlens, i32, (B + 1,)), (page_table, i32, (B, pages)),
+              (seq_lens, i32, (B,))]
+    if lse is not None:
+        wanted.append((lse, torch.float32, (T, Hq)))
+    device = _need_dense(where, *wanted)
+    if cache.device_index != device or workspace is None or workspace.get_device() != device:
+        raise MemraError(1, where)
+    return (cache.ref, _ptr(q), _row_stride(where, q, Hq, D, device), _ptr(cu_seqlens), _ptr(page_table), pages,
+            _ptr(seq_lens), int(max_seq_len), B, T, Hq, cache.n_kv_heads, D,
+            float(sm_scale if sm_scale is not None else D ** -0.5), int(window), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse))
+
+
+def kv_evict(cache: KVCache, page_table, seq_lens, max_seq_len: int, weights, budgets, dst_table, kept, sink: int = 0,
+             recent: int = 0, new_weights=None, new_lens=None, stream=None) -> None:
+    """memra_kv_evict: the budgets[b] rows of largest weight of each KV head move to the pages of dst_table.
+
+    weights float32 [B, Hkv, >= max_seq_len]; budgets int32 [B], at most
+    kept.shape[2]; dst_table int32 [B, pages] of pages that nothing else uses;
+    kept int32 [B, Hkv, max_budget] receives the kept indices, new_weights
+    float32 [B, Hkv, >= max_budget] their weights, new_lens int32 [B] how many.
+    """
+    import torch
+    where = "memra_kv_evict"
+    i32, f32 = torch.int32, torch.float32
+    B, Hkv, most = kept.shape
+    pages, to = page_table.shape[-1], dst_table.shape[-1]
+    wanted = [(kept, i32, (B, Hkv, most)), (page_table, i32, (B, pages)), (seq_lens, i32, (B,)),
+              (weights, f32, (B, Hkv, weights.shape[-1])), (budgets, i32, (B,)), (dst_table, i32, (B, to))]
+    if new_weights is not None:
+        wanted.append((new_weights, f32, (B, Hkv, new_weights.shape[-1])))
+    if new_lens is not None:
+        wanted.append((new_lens, i32, (B,)))
+    device = _need_dense(where, *wanted)
+    if cache.device_index != device or Hkv != cache.n_kv_heads:
+        raise MemraError(1, where)
+    rc = lib().memra_kv_evict(cache.ref, page_table.data_ptr(), pages, seq_lens.data_ptr(), int(max_seq_len),
+                              weights.data_ptr(), weights.shape[-1], budgets.data_ptr(), most, int(sink), int(recent),
+                              dst_table.data_ptr(), to, B, kept.data_ptr(), _ptr(new_weights),
+                              new_weights.shape[-1] if new_weights is not None else 0, _ptr(new_lens),
+                              _stream(stream))
+    _check(rc, where)
+
+
 def testing_decode_attn_short_page(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, out, workspace,
                                    page_wait_ns: int, sm_scale=None, stream=None) -> None:
     """memra_testing_decode_attn_short_page (memra_testing.h): decode attention whose first CTA's first
@@ -456,6 +582,13 @@ def testing_tree_attn_short_page(cache: KVCache, q, page_table, seq_lens, max_se
     a = _tree_args(cache, q, page_table, seq_lens, max_seq_len, tree_mask, out, workspace, sm_scale)
     _check(lib().memra_testing_tree_attn_short_page(*a, _stream(stream)),
            "memra_testing_tree_attn_short_page")
+
+
+def testing_chunk_attn_short_page(cache: KVCache, q, cu_seqlens, page_table, seq_lens, max_seq_len: int, out, workspace,
+                                  sm_scale=None, window: int = 0, lse=None, stream=None) -> None:
+    """memra_testing_chunk_attn_short_page (memra_testing.h): the same for chunk attention's first chunk of keys."""
+    a = _chunk_args(cache, q, cu_seqlens, page_table, seq_lens, max_seq_len, out, workspace, sm_scale, window, lse)
+    _check(lib().memra_testing_chunk_attn_short_page(*a, _stream(stream)), "memra_testing_chunk_attn_short_page")
 
 
 def testing_scale_division_mismatches(scales, mismatches, stream=None) -> None:

@@ -418,6 +418,112 @@ int memra_kv_compact(const memra_kv_cache *cache, const int32_t *page_table, int
                      const int32_t *seq_lens, int32_t max_seq_len, const int32_t *accepted, int32_t max_accepted,
                      const int32_t *n_accepted, int32_t batch, int32_t n_nodes, void *stream);
 
+/* Query and key rows made ready for attention, in one pass: what runs between
+ * the projections of a token and memra_kv_append.  Every head's row of q and k is
+ * normalized and its first dims are turned by the token's position:
+ *   y = x / sqrt(mean(x^2) + eps) * weight
+ *   (a, b) -> (a cos - b sin, b cos + a sin), angle = positions[t] * inv_freq[j],
+ *   (a, b) = dims (j, j + rotary_dim/2), or (2j, 2j+1) where interleaved is not 0
+ * computed in float32 and rounded once, to fp16.  Angles are exact to 2^-32 turns
+ * at any position up to 2^20 (2^-42 turns a position beyond that).
+ *   q, k, v       device fp16, token t's heads at q + t * q_stride, [n_heads][head_dim]
+ *                 (k, v: [n_kv_heads][head_dim]); strides in elements, multiples of
+ *                 8, at least the token's heads (views of one fused buffer will do)
+ *   q_weight, k_weight  device float32 [head_dim], or NULL: no norm
+ *   eps           finite, >= 0
+ *   positions     device int32 [n_tok]: the angle's, not the cache's: after an
+ *                 eviction they differ
+ *   inv_freq      device float32 [rotary_dim/2], finite
+ *   rotary_dim    0 (no rotation; positions and inv_freq may be NULL) .. head_dim, a multiple of 16
+ *   q_out, k_out  device fp16, strides as q's and k's; may be q and k themselves
+ *                 (same stride), else they overlap no input.  k_out may be NULL.
+ *   cache, slot_mapping, v  all three or none: the finished K rows and the V rows go
+ *                 to the slots of memra_kv_append (int32 [n_tok]; a negative slot
+ *                 skips the row, one past the pool skips it and sets
+ *                 MEMRA_DEVERR_BAD_SLOT; distinct within the call), the same bytes
+ *                 as that call makes of them
+ * k must be given exactly if there is a k_out or a cache.  head_dim 128 or 256; a
+ * cache must have the call's n_kv_heads and head_dim.  n_tok == 0 is a no-op. */
+int memra_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, const float *q_weight, const float *k_weight, float eps,
+                       const int32_t *positions, const float *inv_freq, int32_t rotary_dim, int32_t interleaved,
+                       int32_t n_tok, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, void *q_out,
+                       int64_t q_out_stride, void *k_out, int64_t k_out_stride, const memra_kv_cache *cache,
+                       const int32_t *slot_mapping, void *stream);
+
+/* Attention of a chunk of new tokens of every sequence over the paged cache: a long
+ * prompt that goes in piece by piece, several requests' pieces and other requests'
+ * single tokens in one call.
+ *   q             device fp16, token t's heads at q + t * q_stride, [n_heads][head_dim];
+ *                 q_stride in elements, a multiple of 8, at least the token's heads
+ *   cu_seqlens    device int32 [batch + 1]: sequence b's new tokens are the rows
+ *                 cu_seqlens[b] .. cu_seqlens[b+1] - 1 of q, as in memra_prompt_attn
+ *                 (any number of them, none too)
+ *   page_table    device int32 [batch][max_pages_per_seq]
+ *   seq_lens      device int32 [batch]; lengths INCLUDING the new tokens, whose rows
+ *                 are the sequence's last (append them first: memra_kv_append or
+ *                 memra_qk_norm_rope).  max_seq_len: host upper bound of them
+ *   total_tokens  rows of q and out (host); rows of no sequence keep what out holds
+ *   sm_scale      softmax scale, finite and > 0
+ *   window        0: the row at position p sees keys 0 .. p; > 0: keys max(0, p - window
+ *                 + 1) .. p, and page_table rows are rings: position p lies in column
+ *                 (p / 16) % max_pages_per_seq.  A ring that does not hold all keys
+ *                 that a chunk sees sets MEMRA_DEVERR_BAD_SEQ_LEN.  Pages wholly
+ *                 before the first key that a sequence sees need not be in the table.
+ *   workspace     device, >= memra_chunk_attn_workspace_bytes(head_dim) bytes, whatever the
+ *                 sizes; calls that may overlap on the GPU need one each
+ *   out           device fp16 [total_tokens][n_heads][head_dim]
+ *   lse           device float32 [total_tokens][n_heads], or NULL: the natural logarithm of
+ *                 the sum of a row's exponentials (-inf for a row that sees no key)
+ * All K and V formats, head_dim 128 or 256, n_heads / n_kv_heads <= MEMRA_MAX_GROUP,
+ * batch and n_kv_heads <= 65535.  K^ and V^ enter the products in fp16, each value
+ * rounded once (fp8 and NVFP4 exactly); with lse, q8_0 keys enter exactly.  The
+ * weights are fp16, scores, sums and output are accumulated in float32.  The work is
+ * cut by the lengths of the whole call, so that it fills the GPU: the same call gives
+ * the same bytes, another batch may differ in the last bits.  A query, or a key that
+ * a row sees, that is not finite makes the row NaN; a V that is not finite may also
+ * reach rows of its sequence that do not see it.  A length out of range is clamped and
+ * sets MEMRA_DEVERR_BAD_SEQ_LEN, as does a sequence shorter than its chunk, whose rows
+ * at positions below 0 yield zeros; that sequence's other rows are then unspecified.
+ * Keys of a page id outside the pool are left out (MEMRA_DEVERR_BAD_PAGE).  batch == 0
+ * or total_tokens == 0 is a no-op. */
+size_t memra_chunk_attn_workspace_bytes(int32_t head_dim);
+int memra_chunk_attn(const memra_kv_cache *cache, const void *q, int64_t q_stride, const int32_t *cu_seqlens,
+                     const int32_t *page_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+                     int32_t max_seq_len, int32_t batch, int32_t total_tokens, int32_t n_heads, int32_t n_kv_heads,
+                     int32_t head_dim, float sm_scale, int32_t window, void *workspace, size_t workspace_bytes,
+                     void *out, float *lse, void *stream);
+
+/* Eviction: the rows of a sequence that have collected the most attention weight
+ * move to other pages, for each KV head its own, and the rest is left behind.  Of
+ * a sequence of T = seq_lens[b] tokens n = min(T, budgets[b]) stay, in their order:
+ * the last r = min(recent, n), the first s = min(sink, n - r), and of the others
+ * the n - s - r of largest weight (of equal ones the lower index; NaN weighs least).
+ * Their K and V rows go, byte for byte, to positions 0 .. n - 1 of dst_table's pages.
+ *   page_table    device int32 [batch][max_pages_per_seq]
+ *   seq_lens      device int32 [batch];  max_seq_len: host upper bound of them
+ *   weights       device float32 [batch][n_kv_heads][weight_stride], weight_stride
+ *                 >= max_seq_len (memra_key_weights keeps them)
+ *   budgets       device int32 [batch], 0 .. max_budget (outside: clamped,
+ *                 MEMRA_DEVERR_BAD_SEQ_LEN)
+ *   dst_table     device int32 [batch][dst_pages_per_seq], dst_pages_per_seq * 16 >=
+ *                 max_budget: pages that no sequence of the call reads and no other
+ *                 sequence writes (shared pages may be read by several)
+ *   kept          device int32 [batch][n_kv_heads][max_budget]: written, the kept
+ *                 tokens' indices, -1 behind the last
+ *   new_weights   device float32 [batch][n_kv_heads][new_weight_stride], or NULL:
+ *                 their weights, what lies behind the last left as it was; overlaps
+ *                 nothing else of the call
+ *   new_lens      device int32 [batch], or NULL: n
+ * A length out of range is clamped (MEMRA_DEVERR_BAD_SEQ_LEN); a row whose page is
+ * outside the pool, on either side, does not move (MEMRA_DEVERR_BAD_PAGE).  batch *
+ * n_kv_heads <= 65535.  No workspace.  batch == 0 or max_budget == 0 is a no-op. */
+int memra_kv_evict(const memra_kv_cache *cache, const int32_t *page_table, int32_t max_pages_per_seq,
+                   const int32_t *seq_lens, int32_t max_seq_len, const float *weights, int64_t weight_stride,
+                   const int32_t *budgets, int32_t max_budget, int32_t sink, int32_t recent, const int32_t *dst_table,
+                   int32_t dst_pages_per_seq, int32_t batch, int32_t *kept, float *new_weights,
+                   int64_t new_weight_stride, int32_t *new_lens, void *stream);
+
 /* Fixed size of the device array that memra_decode_attn_noalloc uses for the
  * split-K partials (held on every device that calls it, until exit). */
 #define MEMRA_NOALLOC_SCRATCH_BYTES (16u << 20)

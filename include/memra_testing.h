@@ -60,6 +60,14 @@ int memra_testing_tree_attn_short_page(const memra_kv_cache *cache, const void *
                                        int32_t n_kv_heads, int32_t head_dim, float sm_scale, void *workspace,
                                        size_t workspace_bytes, void *out, void *stream);
 
+/* memra_chunk_attn, likewise: the copies of CTA 0's first chunk of keys. */
+int memra_testing_chunk_attn_short_page(const memra_kv_cache *cache, const void *q, int64_t q_stride,
+                                        const int32_t *cu_seqlens, const int32_t *page_table,
+                                        int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t max_seq_len,
+                                        int32_t batch, int32_t total_tokens, int32_t n_heads, int32_t n_kv_heads,
+                                        int32_t head_dim, float sm_scale, int32_t window, void *workspace,
+                                        size_t workspace_bytes, void *out, float *lse, void *stream);
+
 /* Adds to *mismatches (device, unsigned 64-bit; the caller zeroes it) the
  * number of (x, s) pairs, x every finite fp16 value and s each of the
  * n_scales float32 scales at `scales` (device, 1 .. 65535 of them, each

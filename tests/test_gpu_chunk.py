@@ -1,0 +1,310 @@
+"""Chunk attention on the GPU against float64 over the dequantized cache; tolerances from the roundings (chunk_cases.py)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from chunk_cases import PAIRS, Chunk, dev     # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def memra():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_attention_block_memra_gb300 import _build
+    _build.build()
+    import decode_attention_block_memra_gb300 as m
+    m.lib()
+    return m
+
+
+@pytest.mark.parametrize("new,past", [([1], [0]), ([1], [15]), ([1], [63]), ([17], [0]), ([64], [64]), ([5], [300])])
+@pytest.mark.parametrize("D", [128, 256])
+def test_small(memra, new, past, D):
+    c = Chunk(memra, "q8_0", "q5_1", D, 8, 2, new, past)
+    assert c.call() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("kf,vf", PAIRS)
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("lse", [False, True])
+def test_formats_and_ragged_chunks(memra, kf, vf, D, lse):
+    c = Chunk(memra, kf, vf, D, 8, 2, [33, 1, 200, 0, 5, 1], [100, 700, 3, 50, 0, 1500], pad=3, seed=D)
+    assert c.call(lse) == 0
+    c.check(lse)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (5, 1), (4, 4), (12, 4), (40, 8), (128, 1), (96, 2), (3, 3)])
+@pytest.mark.parametrize("D", [128, 256])
+def test_head_layouts(memra, Hq, Hkv, D):
+    c = Chunk(memra, "fp8", "q4_0", D, Hq, Hkv, [3, 40, 1], [90, 10, 333], seed=Hq)
+    assert c.call() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("new,past", [([1], [9000]), ([300], [5000]), ([1, 700], [20000, 100]), ([2000], [0]), ([129], [16383])])
+def test_long_contexts_are_cut_and_joined(memra, D, new, past):
+    c = Chunk(memra, "q8_0", "q5_1", D, 4, 1, new, past, seed=1)
+    assert c.call() == 0
+    c.check()
+
+
+def test_many_sequences(memra):
+    rng = np.random.default_rng(3)
+    new = [int(x) for x in rng.integers(0, 4, 150)]
+    past = [int(x) for x in rng.integers(0, 400, 150)]
+    c = Chunk(memra, "fp8", "fp8", 128, 8, 2, new, past, pad=1)
+    assert c.call() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("window", [1, 5, 16, 63, 64, 65, 300])
+def test_windows_over_rings(memra, D, window):
+    c = Chunk(memra, "q8_0", "q5_1", D, 8, 2, [40, 1, 130, 7], [1000, 2000, 0, 3], window=window)
+    assert c.call() == 0
+    c.check()
+    # a table of all pages is a ring that never wraps
+    c = Chunk(memra, "fp8", "fp8", D, 8, 2, [40, 1], [300, 200], window=window, extra_columns=30)
+    assert c.call() == 0
+    c.check()
+
+
+def test_pages_before_the_window_need_not_exist(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [20], [1000], window=50, extra_columns=80)
+    first = (1000 - 50 + 1) // 16
+    gone = [p % c.table.shape[1] for p in range(0, first)]
+    c.table[0, gone] = -1
+    assert c.call() == 0
+    c.check()
+
+
+def test_strided_queries_and_scale(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [30, 2], [40, 99], stride_heads=4)
+    assert c.call() == 0
+    c.check()
+    # keys a thousand times smaller under queries a thousand times larger; and the reverse
+    for gain in (1000.0, 0.001):
+        c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [30, 2], [40, 99], k_gain=1 / gain, q_gain=gain)
+        assert c.call() == 0
+        c.check()
+
+
+def test_peaked_rows(memra):
+    # scores of up to 100: one key has nearly all the weight, and which one changes along the keys
+    c = Chunk(memra, "fp8", "fp8", 128, 8, 2, [60, 3], [900, 4000], q_gain=10.0)
+    assert c.call() == 0
+    c.check()
+
+
+def test_large_values(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 4, 2, [20], [100],
+              v_of=lambda *s: np.random.default_rng(0).choice([-60000.0, 60000.0, 1.0], s))
+    assert c.call() == 0
+    c.check()
+
+
+def test_long_sums(memra):
+    """Each CTA takes over 7,680 keys of a block: its sums are joined in float32."""
+    for new in ([1], [130]):
+        c = Chunk(memra, "fp8", "q4_0", 128, 160, 160, new, [16384 - new[0]], fill=False,
+                  v_of=lambda *s: 1 + np.random.default_rng(1).random(s))
+        c.buf.mul_(0.1)
+        c.q = c.buf.cpu().numpy()[:, :160]
+        assert c.call() == 0
+        c.check(heads=[0, 1, 77, 159])
+
+
+def test_long_sums_at_head_dim_256(memra):
+    c = Chunk(memra, "fp8", "fp8", 256, 160, 160, [2], [16382], fill=False, v_of=lambda *s: 1 + np.random.default_rng(1).random(s))
+    assert c.call() == 0
+    c.check(heads=[0, 80, 159])
+
+
+def test_the_longest_context_means(memra):
+    """Queries of zeros: the mean of V over 262,144 keys, all of one sign."""
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 1, [3], [262141], q_gain=0.0, fill=False,
+              v_of=lambda *s: 1 + np.random.default_rng(1).random(s))
+    assert c.call() == 0
+    c.check()
+
+
+def test_same_call_same_bytes(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 32, 4, [200, 1, 1], [3000, 4000, 100])
+    c.call()
+    first, first_lse = c.out.clone(), c.lse.clone()
+    c.ws.fill_(0)
+    c.out.fill_(-7)
+    c.call()
+    assert torch.equal(c.out, first) and torch.equal(c.lse, first_lse)
+
+
+def test_agrees_with_decode(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [4, 4], [700, 3000])
+    c.call()
+    out = torch.empty(2, 4, 8, 128, dtype=torch.float16, device="cuda")
+    ws = torch.empty(memra.decode_attn_workspace_bytes(2, 4, 8, 128, 3004), dtype=torch.uint8, device="cuda")
+    memra.decode_attn(c.cache, c.buf.view(2, 4, 8, 128), dev(c.table), dev(np.array(c.lens, np.int32)), 3004, out, ws)
+    assert (out.view(8, 8, 128).float() - c.out.float()).abs().max() <= 2e-3
+
+
+def test_not_finite_queries_and_keys(memra):
+    c = Chunk(memra, "fp8", "fp8", 128, 4, 1, [40, 3], [100, 50])
+    c.buf[5, 2, 7] = float("nan")
+    c.buf[6, 1, 0] = float("inf")
+    # the key at position 120 of the first sequence: an fp8 NaN in its row
+    pages = c.cache.k_pool.view(-1, 1, 2048)
+    slot = c.table[0, 120 // 16]
+    from oracle import layout, quant
+    row = quant.quantize_rows(c.rows[0][1][120:121, 0], "fp8", c.scales[0])
+    seg = np.zeros((1, 1, 2048), np.uint8)
+    layout.write_rows(seg, "k", row, np.array([120 % 16]), 0, 128)
+    at = int(np.nonzero(seg[0, 0])[0][0])
+    pages[int(slot), 0, at] = 0x7F
+    assert c.call() == 0
+    nan = torch.isnan(c.out).any(-1).cpu().numpy()
+    want = np.zeros((43, 4), bool)
+    want[5, 2] = want[6, 1] = True
+    want[20:40] = True                       # tokens from position 120 on
+    assert np.array_equal(nan, want) and np.array_equal(torch.isnan(c.lse).cpu().numpy(), want)
+    whole = c.out.cpu().numpy().astype(np.float64)
+    out, tol, _, _ = c.expected(1, 0, True)
+    assert (np.abs(whole[40:] - out) <= tol).all()
+
+
+def test_bad_pages_are_left_out(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [30, 2], [200, 90])
+    table = c.table.copy()
+    table[0, 3], table[1, 0] = -1, c.cache.num_pages
+    assert c.call(page_table=dev(table)) == memra.DEVERR_BAD_PAGE
+    got = c.out.cpu().numpy().astype(np.float64)
+    from oracle import attention, chunked
+    for b, page in ((0, 3), (1, 0)):
+        sees = chunked.chunk_sees(c.new[b], c.lens[b])
+        sees[:, 16 * page:16 * page + 16] = False
+        for h in range(2):
+            _, k, v = c.keys(b, h)
+            rows = slice(c.starts[b], c.starts[b + 1])
+            want = attention.masked_rows(c.q[rows, 4 * h:4 * h + 4], k[:, None], v[:, None], sees, 128 ** -0.5)
+            assert np.abs(got[rows, 4 * h:4 * h + 4] - want).max() <= 2e-3
+
+
+def test_bad_lengths(memra):
+    M = memra
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [30, 20, 5], [200, 90, 60])
+    # shorter than its chunk: the rows at positions below 0 are zeros, the others see their keys
+    assert c.call(seq_lens=dev(np.array([230, 8, 65], np.int32))) == M.DEVERR_BAD_SEQ_LEN
+    assert not c.out[30:42].any() and torch.isinf(c.lse[30:42]).all() and c.out[42:50].any()
+    c.check(sequences=[0, 2])
+    for lens in ([230, -5, 65], [230, 2 ** 31 - 1, 65], [230, 0, 65]):
+        assert c.call(seq_lens=dev(np.array(lens, np.int32))) & M.DEVERR_BAD_SEQ_LEN
+        c.check(sequences=[0, 2])
+    for starts in ([0, 30, 50, 56], [-3, 30, 50, 55], [0, 30, 2 ** 31 - 1, 55], [0, 30, 10, 55]):
+        assert c.call(cu_seqlens=dev(np.array(starts, np.int32))) & M.DEVERR_BAD_SEQ_LEN
+    assert c.call() == 0
+    c.check()
+    # a ring too small for the window
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [30], [400], window=100)
+    assert c.call(page_table=dev(c.table[:, :5])) == M.DEVERR_BAD_SEQ_LEN
+
+
+def test_empty_calls(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [0, 0], [40, 0], pad=2)
+    assert c.call() == 0
+    c.check()
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [3], [40])
+    q = c.buf[:0]
+    c.memra.chunk_attn(c.cache, **{**c.args(), "q": q, "out": c.out[:0], "lse": c.lse[:0]})
+    assert memra.read_status(c.cache) == 0
+
+
+def test_captured_and_replayed_on_other_lengths(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 32, 4, [200, 1, 1], [3000, 4000, 100], pad=4)
+    a = c.args()
+    c.call(**a)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        memra.chunk_attn(c.cache, **a)
+    for new, past in (([200, 1, 1], [3000, 4000, 100]), ([3, 150, 40], [3100, 3851, 61]), ([0, 0, 1], [0, 0, 100])):
+        c.new, c.past, c.lens = new, past, [n + p for n, p in zip(new, past)]
+        c.starts = np.concatenate(([0], np.cumsum(new))).astype(np.int32)
+        a["cu_seqlens"].copy_(dev(c.starts))
+        a["seq_lens"].copy_(dev(np.array(c.lens, np.int32)))
+        rows = c.rows
+        c.rows = [(f, k[:T], v[:T]) for (f, k, v), T in zip(rows, c.lens)]
+        c.out.fill_(-7)
+        c.lse.fill_(-7)
+        graph.replay()
+        assert memra.read_status(c.cache) == 0
+        c.check()
+        c.rows = rows
+
+
+def test_calls_side_by_side(memra):
+    cases = [Chunk(memra, "q8_0", "q5_1", 128, 32, 4, [300, 1], [2000, 5000], seed=s) for s in range(3)]
+    alone = []
+    for c in cases:
+        c.call()
+        alone.append(c.out.clone())
+        c.out.fill_(-7)
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [c.args() for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, a, s in zip(cases, args, streams):
+            memra.chunk_attn(c.cache, **a, stream=s)
+    torch.cuda.synchronize()
+    for c, want in zip(cases, alone):
+        assert memra.read_status(c.cache) == 0
+        assert torch.equal(c.out, want)
+
+
+def test_thousands_of_calls_in_a_row(memra):
+    cases = [Chunk(memra, "q8_0", "q5_1", D, 8, 2, [70, 1, 9], [500, 1200, 0], seed=D) for D in (128, 256)]
+    want = []
+    for c in cases:
+        assert c.call() == 0
+        c.check()
+        want.append(c.out.clone())
+    args = [c.args() for c in cases]
+    for _ in range(1500):
+        for c, a in zip(cases, args):
+            memra.chunk_attn(c.cache, **a)
+    for c, w in zip(cases, want):
+        assert memra.read_status(c.cache) == 0 and torch.equal(c.out, w)
+
+
+def test_offsets_past_32_bits(memra):
+    """Pages whose bytes lie past 4 GiB of the pools."""
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [5], [100])
+    n = c.cache.num_pages
+    big = memra.KVCache("q8_0", "q5_1", 1_200_000, 2, 128)
+    shift = 1_200_000 - n
+    for src, dst, seg in ((c.cache.k_pool, big.k_pool, 2 * 2176), (c.cache.v_pool, big.v_pool, 2 * 1536)):
+        dst[shift * seg:] = src
+    assert shift * 2 * 2176 > 2 ** 32
+    out = c.out.clone()
+    a = c.args()
+    a.update(out=out, page_table=dev(c.table + shift))
+    memra.chunk_attn(big, **a)
+    assert memra.read_status(big) == 0
+    c.call()
+    assert torch.equal(out, c.out)
+
+
+def test_refusals_of_the_binding(memra):
+    c = Chunk(memra, "q8_0", "q5_1", 128, 8, 2, [30, 2], [40, 99])
+    good = c.args()
+    for bad in (dict(q=good["q"].float()), dict(q=good["q"][:, :7]), dict(out=c.out[:5]), dict(out=c.out.float()),
+                dict(cu_seqlens=good["cu_seqlens"].long()), dict(cu_seqlens=good["cu_seqlens"][:2]),
+                dict(page_table=good["page_table"].long()), dict(seq_lens=good["seq_lens"][:1]),
+                dict(lse=c.lse.half()), dict(lse=c.lse[:, :4]), dict(workspace=c.ws[:-1]), dict(workspace=None),
+                dict(workspace=c.ws.cpu()), dict(sm_scale=0.0), dict(sm_scale=-1.0), dict(window=-1),
+                dict(max_seq_len=-1), dict(q=good["q"].cpu())):
+        with pytest.raises(memra.MemraError):
+            c.call(**bad)
+    assert c.call() == 0
+    c.check()
