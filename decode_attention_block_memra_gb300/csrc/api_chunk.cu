@@ -20,7 +20,7 @@ struct Workspace {
     const size_t rows = static_cast<size_t>(kChunkCtasMax) * chunk_tiles(head_dim) * kChunkRows;
     lse = 2 * rows * head_dim * sizeof(float);
     far = lse + 2 * rows * sizeof(float);
-    bytes = far + rows * head_dim * sizeof(float);
+    bytes = far + rows * kChunkFarCols(head_dim) * sizeof(float);
   }
 };
 
@@ -79,7 +79,7 @@ int chunk_attn(const memra_kv_cache *cache, const void *q, int64_t q_stride, con
   p.v_post = scaled_format(cache->v_fmt) ? cache->v_scale : 2.f;
   p.test_extra_tx = test_extra_tx;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = cuda_status(launch_chunk(head_dim, cache->k_fmt, cache->v_fmt, lse != nullptr, p, s));
+  st = cuda_status(launch_chunk(head_dim, cache->k_fmt, cache->v_fmt, p, s));
   // Blocks of fewer steps than this are never cut: no merge.
   if (st || max_seq_len <= (2 * kChunkSnap - 1) * kChunkKeys) return st;
   return cuda_status(launch_chunk_merge(head_dim, p, s));

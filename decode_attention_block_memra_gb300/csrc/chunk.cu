@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(2 * D) chunk_merge_kernel(const ChunkParams p)
 
 }  // namespace
 
-cudaError_t launch_chunk(int D, int kf, int vf, bool pairs, const ChunkParams &p, cudaStream_t st) {
+cudaError_t launch_chunk(int D, int kf, int vf, const ChunkParams &p, cudaStream_t st) {
   switch (kf) {
-    case MEMRA_KV_Q8_0: return pairs ? launch_chunk_q8_pairs(D, vf, p, st) : launch_chunk_q8(D, vf, p, st);
+    case MEMRA_KV_Q8_0: return launch_chunk_q8(D, vf, p, st);
     case MEMRA_KV_FP8_E4M3: return launch_chunk_fp8(D, vf, p, st);
     case MEMRA_KV_NVFP4: return launch_chunk_nvfp4(D, vf, p, st);
     default: return cudaErrorInvalidValue;

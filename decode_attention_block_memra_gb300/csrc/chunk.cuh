@@ -15,6 +15,8 @@ constexpr int kChunkKeys = 64;
 constexpr int kChunkRows = 128;            // query rows of a tile: tokens x the group's heads
 // Row tiles of a block (what a CTA holds at a time): two at head_dim 128.
 __host__ __device__ constexpr int chunk_tiles(int D) { return D == 128 ? 2 : 1; }
+// Columns of a row in the workspace: the output's, and at head_dim 128 those of the q5_1 blocks' centres.
+__host__ __device__ constexpr int kChunkFarCols(int D) { return D + (D == 128 ? 16 : 0); }
 
 // How the work is cut.  A block is a run of a sequence's tokens (its rows fill the
 // row tiles) under one KV head, and costs a fixed part and its keys.  All blocks
@@ -41,7 +43,7 @@ struct ChunkParams {
   float *lse;                   // [total][n_heads], or null
   float *o_part;                // [2 * CTAs][D / 4][rows of a block][4]: the partial blocks at a CTA's start and end
   float *lse_part;              // [2 * CTAs][rows of a block], base 2
-  float *far;                   // [CTAs][row tiles][D / 4][128][4]: what earlier sums of a long block came to
+  float *far;                   // [CTAs][row tiles][columns / 4][128][4]: what earlier sums of a long block came to
   int32_t *status;
   int batch, total, n_heads, group, n_kv_heads, num_pages, max_pages, window;
   int len_limit;                // lengths are clamped to it
@@ -189,12 +191,11 @@ __device__ __forceinline__ ChunkCut chunk_cut(const ChunkParams &p, int64_t head
   return c;
 }
 
-cudaError_t launch_chunk(int D, int kf, int vf, bool pairs, const ChunkParams &p, cudaStream_t st);
+cudaError_t launch_chunk(int D, int kf, int vf, const ChunkParams &p, cudaStream_t st);
 cudaError_t launch_chunk_merge(int D, const ChunkParams &p, cudaStream_t st);
 
-// of one K format and precision each: a translation unit of its own
+// of one K format each: a translation unit of its own
 cudaError_t launch_chunk_q8(int D, int vf, const ChunkParams &p, cudaStream_t st);
-cudaError_t launch_chunk_q8_pairs(int D, int vf, const ChunkParams &p, cudaStream_t st);
 cudaError_t launch_chunk_fp8(int D, int vf, const ChunkParams &p, cudaStream_t st);
 cudaError_t launch_chunk_nvfp4(int D, int vf, const ChunkParams &p, cudaStream_t st);
 

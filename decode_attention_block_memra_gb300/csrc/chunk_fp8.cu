@@ -4,7 +4,7 @@
 namespace memra {
 
 cudaError_t launch_chunk_fp8(int D, int vf, const ChunkParams &p, cudaStream_t st) {
-  return launch_chunk_formats<MEMRA_KV_FP8_E4M3, false>(D, vf, p, st);
+  return launch_chunk_formats<MEMRA_KV_FP8_E4M3>(D, vf, p, st);
 }
 
 }  // namespace memra

@@ -19,12 +19,11 @@
 // tile at a chunk) alternately, and one's softmax fills the gaps of the other's MMAs.
 // head_dim 256: one group, two score buffers.
 //
-// Roundings.  K^ and V^ enter as fp16, rounded once (q8_0, q5_1, q4_0; exact for fp8 and
-// NVFP4): the queries are fp16 too, so a score loses no more to K^ than to them,
-// and V^ no more than the output.  Where the log-sum-exp is wanted, whose float32
-// tells of 2^-24, q8_0 enters as exact hi + lo pairs.  P is fp16, everything else
-// float32.  The tensor cores cut an accumulator's last bits at every step, so an O takes
-// kSumUnits chunks at most; then it is added to a float32 row in the workspace.
+// Roundings.  K^ and V^ enter exactly, or as fp16 hi + lo pairs (q8_0, q5_1, q4_0: a single fp16
+// value of either would cost as much as the output's own rounding, 4.2e-4 instead of 3.0e-4
+// with both).  P is fp16, everything else float32.  The tensor cores cut an accumulator's last bits
+// at every step, so an O takes kSumUnits chunks at most; then it is added to a
+// float32 row in the workspace.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -41,56 +40,25 @@ namespace {
 constexpr float kLazy = 8.f;               // log2 units: P stays <= 256 between rescales
 constexpr int kSumUnits = 120;             // chunks of one sum of the tensor cores: 7,680 keys
 
-template <int D, int KF, int VF, bool PAIR>
-struct ChunkCfg {
-  static constexpr int kTiles = chunk_tiles(D), kGroups = D == 128 ? 2 : 1;
-  static constexpr bool kKLo = KF == MEMRA_KV_Q8_0 && PAIR;
-  // (pairs of 256 dims leave room for one K^ tile)
-  static constexpr int kStageGroups = D == 256 && kKLo ? 1 : 2, kStageWarps = 8 / kStageGroups;
-  static constexpr int kStageWarp0 = 4 * kGroups, kMmaWarp = kStageWarp0 + 8, kCopyWarp = kMmaWarp + 1;
-  static constexpr int kThreads = 32 * (kCopyWarp + 1);
-  static constexpr int kPages = kChunkKeys / kPage;
-  static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
-  static constexpr bool kVRows = VF != MEMRA_KV_NVFP4;          // V staged as token rows (MN-major)
-  static constexpr uint32_t kTile = kChunkKeys * D * 2;
-  static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kTile;
-  static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
-  static constexpr int kKBufs = kStageGroups, kVBufs = 2;
-  // barriers, masks of the chunks' pages, (m, l) of two groups, then the tiles and the raw chunks
-  static constexpr uint32_t kOffBar = 0, kOffMask = 320, kOffCut = 384, kOffMl = 512, kOffK = 4096;
-  static constexpr uint32_t kOffV = kOffK + kKBufs * kKBuf, kOffRaw = kOffV + kVBufs * kVBuf;
-  static constexpr uint32_t kRoom = 227 * 1024;
-  static constexpr int kRaw = (kRoom - kOffRaw) / kRawBytes < 6 ? (kRoom - kOffRaw) / kRawBytes : 6;
-  // Tensor memory: a CTA that found its columns taken would wait in its allocation, so
-  // no more CTAs of the library's tensor-memory kernels may fit an SM than its 512 columns hold.
-  static constexpr uint32_t kTCols = 512, kNeed = kOffRaw + kRaw * kRawBytes, kFloor = 150 * 1024;
-  static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
-  // tensor-memory columns: Q of each row tile, O of each group, two score buffers
-  static constexpr uint32_t kQCol = 0, kOCol = kTiles * D / 2, kSCol = kOCol + kGroups * D;
-  static_assert(kRaw >= 2 && kRaw <= 8, "a chunk ahead; the masks' ring");
-  static_assert(kOffBar + 8 * (2 * kRaw + 17) + 4 <= kOffMask, "barriers and the tensor-memory address");
-  static_assert(kOffMl + 2 * kChunkRows * 8 <= kOffK, "maxima and sums");
-  static_assert(kSmem <= 232448, "shared memory");
-  static_assert(kSCol + 2 * kChunkKeys <= kTCols, "tensor memory");
-  static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
-};
-
 // Where a CTA's share of the line begins and ends.
 struct ChunkShare {
   int h0, b0, j0, k0, h1, b1, j1, k1;
 };
 
-// A block, or the part of one, that a CTA takes.
+// A block, or the part of one, that a CTA takes.  The copy warp finds them one
+// after another and leaves them in a ring in shared memory, some ahead of the other warps.
+constexpr int kChunkPieces = 4;
 struct ChunkPiece {
-  ChunkBlock block;
-  int first, pos0, T;           // row of token t0; its position; keys of the sequence
+  int first, tokens;            // row of the block's first token in the call, and its tokens
+  int pos0, T;                  // that token's position; keys of the sequence
   int h, b;
-  int step0, steps;             // steps over the keys
+  int step0, steps;             // steps over the keys; steps < 0: there is no more piece
   int tiles;
-  bool whole, head;             // all of the block's steps; its first ones
+  int whole, head;              // all of the block's steps; its first ones
+  int key0;                     // first key that a row of the block sees
 };
 
-// Walks a CTA's share, the same in every warp.
+// Walks a CTA's share.
 struct ChunkWalk {
   const ChunkParams &p;
   int h, b, j, k, h1, b1, j1, k1, tpb, seen;
@@ -109,22 +77,76 @@ struct ChunkWalk {
         if (++b == p.batch) b = 0, ++h;
         continue;
       }
-      x.block = chunk_block(p, s, j, tpb);
-      const int steps = max(0, x.block.hi - x.block.lo);
+      const ChunkBlock block = chunk_block(p, s, j, tpb);
+      const int steps = max(0, block.hi - block.lo);
       const bool last = h == h1 && b == b1 && j == j1;
       const int from = k, to = last ? k1 : steps;
-      x.h = h, x.b = b, x.T = s.T;
-      x.first = s.first + x.block.t0;
-      x.pos0 = s.T - s.n + x.block.t0;
-      x.step0 = x.block.lo + from;
+      x.first = s.first + block.t0;
+      x.tokens = block.t1 - block.t0;
+      x.pos0 = s.T - s.n + block.t0;
+      x.T = s.T;
+      x.h = h, x.b = b;
+      x.step0 = block.lo + from;
       x.steps = to - from;
-      x.tiles = x.block.t1 - x.block.t0 > p.tpt ? 2 : 1;
+      x.tiles = x.tokens > p.tpt ? 2 : 1;
       x.whole = from == 0 && to == steps;
       x.head = from == 0;
+      x.key0 = block.key0;
       if (last) k = k1; else ++j, k = 0;
       if (from < to || steps == 0) return true;
     }
   }
+};
+
+template <int D, int KF, int VF>
+struct ChunkCfg {
+  static constexpr int kTiles = chunk_tiles(D), kGroups = D == 128 ? 2 : 1;
+  static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
+  static constexpr bool kVLo = VF == MEMRA_KV_Q5_1 || VF == MEMRA_KV_Q4_0;
+  // (pairs of 256 dims leave room for one tile of theirs)
+  static constexpr int kStageGroups = D == 256 && (kKLo || kVLo) ? 1 : 2, kStageWarps = 8 / kStageGroups;
+  static constexpr int kStageWarp0 = 4 * kGroups, kMmaWarp = kStageWarp0 + 8, kCopyWarp = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kCopyWarp + 1);
+  static constexpr int kPages = kChunkKeys / kPage;
+  static constexpr int kKSeg = k_seg_bytes(KF, D), kVSeg = v_seg_bytes(VF, D);
+  // q5_1's d q + m as d (q - 16) and, in 16 more columns of V^, the blocks' centres m + 16 d (hi and lo parts),
+  // joined to O at the end: three operations a pair instead of ten, and no large sums that nearly cancel.  (The
+  // MMA is at most 256 wide, so at head_dim 256 it is the pair of d q + m.)
+  static constexpr bool kMCols = VF == MEMRA_KV_Q5_1 && D == 128;
+  static constexpr int kOCols = D + (kMCols ? 16 : 0);
+  static constexpr bool kVRows = VF != MEMRA_KV_NVFP4;          // V staged as token rows (MN-major)
+  static constexpr uint32_t kTile = kChunkKeys * D * 2;
+  static constexpr uint32_t kLoOff = kTile + (kMCols ? kChunkKeys * 128 : 0);     // V: hi, centres, lo
+  static constexpr uint32_t kKBuf = kTile * (kKLo ? 2 : 1), kVBuf = kVLo ? kLoOff + kTile : kTile;
+  static constexpr uint32_t kRawBytes = kPages * (kKSeg + kVSeg);
+  // Q in tensor memory; with the centres' columns, two row tiles fill it with 48 columns of Q, 144 of O and 64 of
+  // scores each: Q's last 32 dims lie in shared memory.
+  static constexpr int kQTmem = kMCols ? 96 : D, kQSmem = D - kQTmem;
+  static constexpr int kKBufs = kStageGroups, kVBufs = kStageGroups == 2 || !kVLo ? 2 : 1;
+  // barriers, masks of the chunks' pages, the share, the pieces, (m, l) of two groups; then Q's last dims, the tiles
+  // and the raw chunks
+  static constexpr uint32_t kOffBar = 0, kOffMask = 384, kOffCut = 400, kOffPiece = 448;
+  static constexpr uint32_t kOffMl = 1024, kOffQ = 4096;
+  static constexpr uint32_t kOffK = kOffQ + kTiles * kChunkRows * kQSmem * 2;
+  static constexpr uint32_t kOffV = kOffK + kKBufs * kKBuf, kOffRaw = kOffV + kVBufs * kVBuf;
+  static constexpr uint32_t kRoom = 227 * 1024;
+  static constexpr int kRaw = (kRoom - kOffRaw) / kRawBytes < 6 ? (kRoom - kOffRaw) / kRawBytes : 6;
+  // Tensor memory: a CTA that found its columns taken would wait in its allocation, so
+  // no more CTAs of the library's tensor-memory kernels may fit an SM than its 512 columns hold.
+  static constexpr uint32_t kTCols = 512, kNeed = kOffRaw + kRaw * kRawBytes, kFloor = 150 * 1024;
+  static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
+  // tensor-memory columns: Q of each row tile, O of each group, two score buffers
+  static constexpr uint32_t kQCol = 0, kOCol = kTiles * kQTmem / 2, kSCol = kOCol + kGroups * kOCols;
+  // barriers: the raw chunks', six pairs for the tiles, scores and weights, then
+  enum Bar { kPvDone = 2 * kRaw + 12, kQReady = kPvDone + 2, kDrained = kQReady + 2, kPieceFull, kPieceFree = kPieceFull + kChunkPieces,
+             kBars = kPieceFree + kChunkPieces };
+  static_assert(kRaw >= 2 && kRaw <= 8, "a chunk ahead; the masks' ring");
+  static_assert(kOffBar + 8 * kBars + 4 <= kOffMask, "barriers and the tensor-memory address");
+  static_assert(kOffPiece + kChunkPieces * sizeof(ChunkPiece) <= kOffMl, "pieces");
+  static_assert(kOffMl + 2 * kChunkRows * 8 <= kOffQ, "maxima and sums");
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kSCol + 2 * kChunkKeys <= kTCols, "tensor memory");
+  static_assert(kRawBytes % 16 == 0 && kOffRaw % 16 == 0 && kOffK % 1024 == 0 && kTile % 1024 == 0, "alignment");
 };
 
 // The keys of the chunk's pages whose bit is set.
@@ -145,9 +167,9 @@ __device__ __forceinline__ uint64_t chunk_seen(int last, int window) {
   return keys;
 }
 
-template <int D, int KF, int VF, bool PAIR>
-__global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_kernel(const ChunkParams p) {
-  using C = ChunkCfg<D, KF, VF, PAIR>;
+template <int D, int KF, int VF>
+__global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel(const ChunkParams p) {
+  using C = ChunkCfg<D, KF, VF>;
   constexpr int KT = kChunkKeys, NP = C::kPages, RAW = C::kRaw, SW = C::kStageWarps, G = C::kGroups;
   constexpr uint32_t kAllPages = (1u << NP) - 1u;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -158,10 +180,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
   auto raw_empty = [&](int s) { return bars + 8 * (RAW + s); };
   enum { kKFull = 0, kKEmpty, kVFull, kVEmpty, kSFull, kPFull };
   auto bar = [&](int kind, int b) { return bars + 8 * (2 * RAW + 2 * kind + b); };
-  auto pv_done = [&](int i) { return bars + 8 * (2 * RAW + 12 + i); };
-  auto q_ready = [&](int i) { return bars + 8 * (2 * RAW + 14 + i); };
-  const uint32_t drained = bars + 8 * (2 * RAW + 16);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * (2 * RAW + 17));
+  auto pv_done = [&](int i) { return bars + 8 * (C::kPvDone + i); };
+  auto q_ready = [&](int i) { return bars + 8 * (C::kQReady + i); };
+  auto piece_full = [&](int i) { return bars + 8 * (C::kPieceFull + i); };
+  auto piece_free = [&](int i) { return bars + 8 * (C::kPieceFree + i); };
+  const uint32_t drained = bars + 8 * C::kDrained;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
+  ChunkPiece *pieces = reinterpret_cast<ChunkPiece *>(smem + C::kOffPiece);
   // a byte for each chunk in flight: the pages that exist
   volatile uint8_t *page_mask = smem + C::kOffMask;
   ChunkShare *share = reinterpret_cast<ChunkShare *>(smem + C::kOffCut);
@@ -206,6 +231,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
         mbar_init(q_ready(k), 4);
       }
       mbar_init(drained, 1);
+      for (int k = 0; k < kChunkPieces; ++k) {
+        mbar_init(piece_full(k), 1);
+        mbar_init(piece_free(k), C::kCopyWarp);        // every other warp
+      }
       fence_barrier_init();
     }
   } else if (warp == C::kMmaWarp) {
@@ -216,10 +245,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  ChunkWalk walk(p, *share, tpb);
-  ChunkPiece x;
   bool ok = true;
-  int cc = 0;                                // chunks before the piece, in this CTA
+  int cc = 0, piece = 0;                     // chunks and pieces before the present one, in this CTA
+  // The next piece, for the warps that are told of it (one thread of the MMA warp); and that this warp is done with one.
+  auto next_piece = [&]() -> const volatile ChunkPiece * {
+    const int i = piece % kChunkPieces;
+    ok = ok && mbar_wait_suspended(piece_full(i), (piece / kChunkPieces) & 1, p.status);
+    return pieces + i;
+  };
+  auto free_piece = [&] {
+    mbar_arrive(piece_free(piece % kChunkPieces));
+    ++piece;
+  };
 
   if (warp == C::kCopyWarp) {
     // ----------------------------------------------------------------- copies --
@@ -228,12 +265,27 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
     const int cp_page = lane >> 1;
     const bool cp_v = lane & 1;
     const uint32_t cp_bytes = cp_v ? C::kVSeg : C::kKSeg;
-    while (ok && walk.next(x)) {
+    ChunkWalk walk(p, *share, tpb);
+    ChunkPiece x;
+    while (ok) {
+      const bool more = walk.next(x);
+      if (!more) x.steps = -1;
+      const int at = piece % kChunkPieces;
+      if (piece >= kChunkPieces) ok = mbar_wait_suspended(piece_free(at), (piece / kChunkPieces - 1) & 1, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        pieces[at] = x;
+        mbar_arrive(piece_full(at));
+      }
+      __syncwarp();
+      ++piece;
+      if (!more) break;
       const int32_t *table = p.page_table + static_cast<size_t>(x.b) * p.max_pages;
       // Page id of a logical page, -1: none (past the keys, before the first one seen, or outside the pool).
       auto page_id = [&](int step) {
         const int i = (x.step0 + step) * NP + (lane & (NP - 1));
-        if (step >= x.steps || i > (x.T - 1) / kPage || i < x.block.key0 / kPage) return -1;
+        if (step >= x.steps || i > (x.T - 1) / kPage || i < x.key0 / kPage) return -1;
         const int pid = table[p.window > 0 ? i % p.max_pages : i];
         if (pid >= 0 && pid < p.num_pages) return pid;
         flag_error(p.status, MEMRA_DEVERR_BAD_PAGE);
@@ -279,9 +331,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
     if (tc::elect_one()) {
       constexpr uint32_t idesc_s = tc::idesc_f16_f32(kChunkRows, KT);
       constexpr uint32_t idesc_o = C::kVRows ? tc::idesc_f16_f32_bmn(kChunkRows, D) : tc::idesc_f16_f32(kChunkRows, D);
-      int used[2] = {0, 0}, piece = 0;       // uses of the score buffers
-      while (ok && walk.next(x)) {
-        const int shift = x.tiles - 1, units = x.steps << shift;
+      constexpr uint32_t idesc_oc = C::kMCols ? tc::idesc_f16_f32_bmn(kChunkRows, C::kOCols) : idesc_o;
+      int used[2] = {0, 0};                  // uses of the score buffers
+      while (true) {
+        const volatile ChunkPiece *x = next_piece();
+        const int steps = ok ? x->steps : -1, shift = ok ? x->tiles - 1 : 0, units = steps << shift;
+        if (steps < 0) break;
         auto wait = [&](int kind, int k, int phase) {
           ok = ok && mbar_wait_suspended(bar(kind, k), phase & 1, p.status);
         };
@@ -295,14 +350,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
           if (!ok) return;
           tc::fence_after_sync();
           const uint32_t d = tmem + C::kSCol + sk * KT;
-          const uint32_t q = tmem + C::kQCol + (shift ? sk * (D / 2) : 0);
+          const int tile = shift ? sk : 0;
           const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffK + kb * C::kKBuf, 16, 1024);
+          const uint64_t qd = tc::smem_desc(sb + C::kOffQ + tile * kChunkRows * C::kQSmem * 2, 128, C::kQSmem / 8 * 128);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
-            for (int lo = 0; lo < (C::kKLo ? 2 : 1); ++lo)
-              tc::mma_f16_ta(d, q + 8 * ks, tc::desc_at(kd, (ks / 4) * KT * 128 + (ks % 4) * 32 + lo * C::kTile),
-                             idesc_s, ks + lo > 0);
+            for (int lo = 0; lo < (C::kKLo ? 2 : 1); ++lo) {
+              const uint64_t bd = tc::desc_at(kd, (ks / 4) * KT * 128 + (ks % 4) * 32 + lo * C::kTile);
+              if (16 * ks < C::kQTmem)
+                tc::mma_f16_ta(d, tmem + C::kQCol + tile * (C::kQTmem / 2) + 8 * ks, bd, idesc_s, ks + lo > 0);
+              else
+                tc::mma_f16(d, tc::desc_at(qd, 256 * (ks - C::kQTmem / 16)), bd, idesc_s, 1);
+            }
           }
           if (!shift || sk) tc::commit(bar(kKEmpty, kb));
           tc::commit(bar(kSFull, sk));
@@ -317,13 +377,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
           ++used[sk];
           tc::fence_after_sync();
           const uint32_t v = sb + C::kOffV + vb * C::kVBuf, a = tmem + C::kSCol + sk * KT;
-          const uint32_t d = tmem + C::kOCol + (G == 2 ? sk * D : 0);
+          const uint32_t d = tmem + C::kOCol + (G == 2 ? sk * C::kOCols : 0);
           const uint64_t vd = C::kVRows ? tc::smem_desc_sw128(v, KT * 128, 1024) : tc::smem_desc(v, 128, (KT / 8) * 128);
           constexpr uint32_t kStep = C::kVRows ? 2048 : 256;       // a K = 16 step further on
           const bool anew = (G == 2 ? u >> 1 : u) % kSumUnits == 0;
 #pragma unroll
-          for (int ks = 0; ks < KT / 16; ++ks)
-            tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks), idesc_o, !anew || ks > 0);
+          for (int ks = 0; ks < KT / 16; ++ks) {
+            tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks), idesc_oc, !anew || ks > 0);
+            if constexpr (C::kVLo) tc::mma_f16_ta(d, a + 8 * ks, tc::desc_at(vd, kStep * ks + C::kLoOff), idesc_o, 1);
+          }
           if (!shift || sk) tc::commit(bar(kVEmpty, vb));
           if (G == 1 || u + 2 >= units) tc::commit(pv_done(G == 2 ? sk : 0));
         };
@@ -335,8 +397,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
           mma_o(u);
           mma_s(u + 2);                      // behind the product that reads its buffer's P
         }
-        cc += x.steps;
-        ++piece;
+        cc += steps;
+        free_piece();
       }
       tc::commit(drained);                   // what was issued completes before the CTA can leave
       mbar_wait_suspended(drained, 0, p.status);
@@ -345,11 +407,24 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
   } else if (warp >= C::kStageWarp0) {
     // ---------------------------------------------------------------- staging --
     const int sg = (warp - C::kStageWarp0) / SW, sw = (warp - C::kStageWarp0) % SW, st = 32 * sw + lane;
-    while (ok && walk.next(x)) {
-      for (int i = 0; i < x.steps; ++i) {
+    if constexpr (C::kMCols) {               // the unused columns of the centres' block, once
+      for (int vb = sg; vb < C::kVBufs; vb += C::kStageGroups)
+        for (uint32_t i = st; i < KT * 8u; i += 32 * SW)
+          sts128(sb + C::kOffV + vb * C::kVBuf + C::kTile + 16 * i, make_uint4(0, 0, 0, 0));
+      named_barrier_sync(1 + sg, 32 * SW);
+    }
+    while (true) {
+      const volatile ChunkPiece *x = next_piece();
+      ok = __all_sync(0xffffffffu, ok);
+      const int steps = ok ? x->steps : -1;
+      if (steps < 0) break;
+      const int keys = x->T - x->step0 * KT; // from the first step on
+      __syncwarp();
+      if (lane == 0) free_piece(); else ++piece;
+      for (int i = 0; i < steps; ++i) {
         const int c = cc + i;
         if (C::kStageGroups == 2 && (c & 1) != sg) continue;
-        const int s = c % RAW, kb = c % C::kKBufs, vb = c % C::kVBufs, valid = x.T - (x.step0 + i) * KT;
+        const int s = c % RAW, kb = c % C::kKBufs, vb = c % C::kVBufs, valid = keys - i * KT;
         const uint32_t rawk = sb + C::kOffRaw + s * C::kRawBytes, rawv = rawk + NP * C::kKSeg;
         // (K^'s tile first: that its last scores are done says that the chunk RAW before this one has landed,
         // so that the raw chunk's parity names this use of its place and not the one two before)
@@ -357,7 +432,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
         if (ok) ok = mbar_wait_suspended(raw_full(s), (c / RAW) & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        stage_k<D, KF, KT, SW, C::kKLo>(rawk, sb + C::kOffK + kb * C::kKBuf, sw, lane);
+        stage_k<D, KF, KT, SW>(rawk, sb + C::kOffK + kb * C::kKBuf, sw, lane);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kKFull, kb));
@@ -370,9 +445,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
         if (pages != kAllPages) keep &= chunk_page_keys(pages);
         const uint32_t vbuf = sb + C::kOffV + vb * C::kVBuf;
         if constexpr (C::kVRows)
-          stage_v<D, VF, KT, SW, false, 0, false>(rawv, vbuf, keep, sw, lane);
+          stage_v<D, VF, KT, SW, C::kMCols, C::kLoOff>(rawv, vbuf, keep, sw, lane);
         else
           stage_v_nvfp4<D, KT, SW>(rawv, vbuf, keep, st);
+        if constexpr (C::kMCols) {           // 32 tokens by each of two warps, other ones each time
+          const int part = (sw - 2 * c) & (SW - 1);
+          if (part < KT / 32) stage_m<D, KT>(rawv, vbuf + C::kTile, keep, 32 * part + lane);
+        }
         fence_proxy_async();                 // V^ for the tensor cores, the raw chunk for the next copies
         __syncwarp();
         if (lane == 0) {
@@ -380,53 +459,68 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
           mbar_arrive(raw_empty(s));
         }
       }
-      cc += x.steps;
+      cc += steps;
     }
   } else {
     // ---------------------------------------------------------------- softmax --
     const int g = warp >> 2, rl = tid & 127;           // group, row of its tile
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t o_col = tmem + tlane + C::kOCol + g * D;
+    const uint32_t o_col = tmem + tlane + C::kOCol + g * C::kOCols;
     const int tl = rl / p.group, head = rl % p.group;
     float4 *const far = reinterpret_cast<float4 *>(p.far) +
-                        (static_cast<size_t>(blockIdx.x) * G + g) * (D / 4) * kChunkRows + rl;
-    int used[2] = {0, 0}, done = 0, piece = 0;         // uses of the score buffers; phases of pv_done
-    while (walk.next(x)) {
-      const bool turns = G == 2 && x.tiles == 1;
-      const int tile = turns ? 0 : g;
-      const int t = x.block.t0 + tile * p.tpt + tl;    // the row's token in the chunk
-      const bool live = tl < p.tpt && t < x.block.t1;
-      const int pos = x.pos0 + tile * p.tpt + tl;
-      const int pos_first = x.pos0 + tile * p.tpt, pos_last = x.pos0 + min(x.block.t1 - x.block.t0, (tile + 1) * p.tpt) - 1;
-      const int64_t row = static_cast<int64_t>(x.first + t - x.block.t0) * p.n_heads + x.h * p.group + head;
+                        (static_cast<size_t>(blockIdx.x) * G + g) * (kChunkFarCols(D) / 4) * kChunkRows + rl;
+    int used[2] = {0, 0}, done = 0;                    // uses of the score buffers; phases of pv_done
+    while (true) {
+      const volatile ChunkPiece *x = next_piece();
+      // All softmax warps go on together, or none; and both groups' rows are out: Q and the maxima may be this piece's.
+      tc::fence_before_sync();
+      ok = named_barrier_and(3, 32 * 4 * G, ok);
+      tc::fence_after_sync();
+      if (!ok || x->steps < 0) break;
+      const int shift = x->tiles - 1, units = x->steps << shift;
+      const bool turns = G == 2 && shift == 0;
+      const int tile = turns ? 0 : g, t = tile * p.tpt + tl;       // the row's token in the block
+      const bool live = tl < p.tpt && t < x->tokens;
+      // from the first step's first key: the row's own position (rows that do not exist see nothing), the tile's first
+      // and last
+      const int origin = x->step0 * KT;
+      const int pos = live ? x->pos0 + t - origin : -1;
+      const int pos_first = x->pos0 + tile * p.tpt - origin;
+      const int pos_last = x->pos0 + min(x->tokens, (tile + 1) * p.tpt) - 1 - origin;
       {
-        // the row of Q as fp16 pairs into tensor memory
+        // the row of Q: fp16 pairs into tensor memory, the last dims into core matrices
         const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q + (live ? (x.first + t - x.block.t0) * p.q_stride + static_cast<int64_t>(x.h * p.group + head) * D : 0));
+            p.q + (live ? (x->first + t) * p.q_stride + static_cast<int64_t>(x->h * p.group + head) * D : 0));
 #pragma unroll
-        for (int c = 0; c < D / 2; c += 16) {
-          if (turns && g != (c >= D / 4)) continue;    // half of the row by each group
+        for (int c = 0; c < C::kQTmem / 2; c += 16) {
+          if (turns && g != (c >= 32)) continue;       // a part of the row by each group
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint4 v = live ? src[c / 4 + e] : make_uint4(0, 0, 0, 0);
             y[4 * e] = v.x, y[4 * e + 1] = v.y, y[4 * e + 2] = v.z, y[4 * e + 3] = v.w;
           }
-          tc::st_32x32b_x16(tmem + tlane + C::kQCol + tile * (D / 2) + c, y);
+          tc::st_32x32b_x16(tmem + tlane + C::kQCol + tile * (C::kQTmem / 2) + c, y);
+        }
+#pragma unroll
+        for (int u = 0; u < C::kQSmem / 8; ++u) {
+          if (turns && g == 0) continue;
+          sts128(sb + C::kOffQ + tile * kChunkRows * C::kQSmem * 2 + ((rl >> 3) * (C::kQSmem / 8) + u) * 128 + (rl & 7) * 16,
+                 live ? src[C::kQTmem / 8 + u] : make_uint4(0, 0, 0, 0));
         }
       }
+      if constexpr (C::kQSmem > 0) fence_proxy_async();
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready(g));
       float m = -INFINITY, l = 0.f, m_far = -INFINITY;
-      const int shift = x.tiles - 1, units = x.steps << shift;
       // O plus what lies in `far`, to `far` (or back to O, at the end)
       auto join = [&](bool back) {
         const bool held = m_far != -INFINITY;
         const float scale = held ? fast_exp2(m_far - m) : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
+        for (int c = 0; c < C::kOCols; c += 16) {
           uint32_t o[16];
           tc::ld_32x32b_x16(o_col + c, o);
           float4 f[4];
@@ -457,7 +551,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
 #pragma unroll 1
       for (int u = g; u < units && ok; u += G) {
         const int i = u >> shift, nth = G == 2 ? u >> 1 : u, sk = u & 1;
-        const int tok0 = (x.step0 + i) * KT;
+        const int tok0 = i * KT;
         const uint32_t s_col = tmem + tlane + C::kSCol + sk * KT;
         ok = mbar_wait_suspended(bar(kSFull, sk), used[sk] & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
@@ -471,8 +565,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
         tc::wait_ld_all();
         tc::hold<KT>(s);
         if (pages != kAllPages || tok0 + KT - 1 > pos_first || (p.window > 0 && tok0 < pos_last - p.window + 1)) {
-          uint64_t sees = live ? chunk_seen(pos - tok0, p.window) : 0ull;
-          sees &= chunk_page_keys(pages);
+          const uint64_t sees = chunk_seen(pos - tok0, p.window) & chunk_page_keys(pages);
           const uint32_t half[2] = {static_cast<uint32_t>(sees), static_cast<uint32_t>(sees >> 32)};
 #pragma unroll
           for (int c = 0; c < KT; ++c)
@@ -506,7 +599,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
         }
         if (moved) {                         // O's rows of this warp times alpha
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
+          for (int c = 0; c < C::kOCols; c += 16) {
             uint32_t o[16];
             tc::ld_32x32b_x16(o_col + c, o);
             tc::wait_ld(o);
@@ -569,31 +662,43 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
       const float inv = l != 0.f ? p.v_post / l : 0.f;
       w[0] *= inv, w[1] *= inv;
       const uint32_t o_first = turns ? tmem + tlane + C::kOCol : o_col;      // of the row's first group
-      const int slot = 2 * blockIdx.x + (x.head ? 1 : 0);
-      const int part_row = tile * kChunkRows + rl;
+      const int parts = turns ? 2 : 1;
+      const bool whole = x->whole;
+      const int slot = 2 * blockIdx.x + (x->head ? 1 : 0), part_row = tile * kChunkRows + rl;
+      const int64_t row = static_cast<int64_t>(x->first + t) * p.n_heads + x->h * p.group + head;
       float4 *const part = reinterpret_cast<float4 *>(p.o_part) +
                            static_cast<size_t>(slot) * (D / 4) * (C::kTiles * kChunkRows) + part_row;
       uint4 *const to = reinterpret_cast<uint4 *>(p.out + row * D);
-#pragma unroll 1
-      for (int c0 = 0; c0 < (turns ? D / 2 : D); c0 += 16) {                 // (by turns: half of the columns each)
-        const int c = turns ? g * (D / 2) + c0 : c0;
+      // the centres' sums (hi and lo parts together) of this group's 32-dim blocks
+      float centre[D / 32];
+      if constexpr (C::kMCols) {
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) centre[e] = 0.f;
+        for (int k = 0; k < parts; ++k) {
+          uint32_t o[16];
+          tc::ld_32x32b_x16(o_first + k * C::kOCols + D, o);
+          tc::wait_ld(o);
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e)
+            centre[e] = w[k] != 0.f ? fmaf(__uint_as_float(o[e]) + __uint_as_float(o[D / 32 + e]), w[k], centre[e]) : centre[e];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        if (!ok || (turns && g != (c >= D / 2))) continue;                   // (by turns: half of the columns each)
         float y[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = 0.f;
-        for (int k = 0; k < (turns ? 2 : 1); ++k) {
+        for (int e = 0; e < 16; ++e) y[e] = C::kMCols ? centre[c / 32] : 0.f;
+        for (int k = 0; k < parts; ++k) {
           uint32_t o[16];
-          tc::ld_32x32b_x16(o_first + k * D + c, o);
+          tc::ld_32x32b_x16(o_first + k * C::kOCols + c, o);
           tc::wait_ld(o);
 #pragma unroll
           for (int e = 0; e < 16; ++e)       // (a group without a visible key: its O may hold anything)
             y[e] = w[k] != 0.f ? fmaf(__uint_as_float(o[e]), w[k], y[e]) : y[e];
         }
-        if (!ok) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = __uint_as_float(kNanPair);
-        }
         if (!live) continue;
-        if (x.whole) {
+        if (whole) {
 #pragma unroll
           for (int e = 0; e < 16; e += 8)
             to[(c + e) / 8] = make_uint4(pack_half2(y[e], y[e + 1]), pack_half2(y[e + 2], y[e + 3]),
@@ -604,20 +709,35 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
             part[static_cast<size_t>((c + e) / 4) * (C::kTiles * kChunkRows)] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
         }
       }
-      if (live && (!turns || g == 0)) {
+      if (ok && live && (!turns || g == 0)) {
         // base 2; -inf, never weighed, without a visible key
-        const float lse = !ok ? __uint_as_float(kNanPair) : l != 0.f ? m + log2f(l) : -INFINITY;
-        if (!x.whole)
+        const float lse = l != 0.f ? m + log2f(l) : -INFINITY;
+        if (!whole)
           p.lse_part[static_cast<size_t>(slot) * (C::kTiles * kChunkRows) + part_row] = lse;
         else if (p.lse)
           p.lse[row] = lse * 0.69314718055994531f;
       }
-      // (both groups' rows are out: Q and the maxima may be the next piece's)
-      tc::fence_before_sync();
-      named_barrier_sync(3, 32 * 4 * G);
-      tc::fence_after_sync();
-      cc += x.steps;
-      ++piece;
+      cc += x->steps;
+      __syncwarp();
+      if (lane == 0) free_piece(); else ++piece;
+    }
+    if (!ok) {
+      // A wait gave up: every row of the CTA's share becomes NaN.
+      ChunkWalk walk(p, *share, tpb);
+      ChunkPiece x;
+      while (walk.next(x)) {
+        const int tile = x.tiles == 2 ? g : 0, t = tile * p.tpt + tl;
+        if (tl >= p.tpt || t >= x.tokens || (G == 2 && x.tiles == 1 && g == 1)) continue;
+        const int64_t row = static_cast<int64_t>(x.first + t) * p.n_heads + x.h * p.group + head;
+        const float nan = __uint_as_float(kNanPair);
+        if (!x.whole) {
+          p.lse_part[static_cast<size_t>(2 * blockIdx.x + (x.head ? 1 : 0)) * (C::kTiles * kChunkRows) + tile * kChunkRows + rl] = nan;
+          continue;
+        }
+        if (p.lse) p.lse[row] = nan;
+        for (int u = 0; u < D / 8; ++u)
+          reinterpret_cast<uint4 *>(p.out + row * D)[u] = make_uint4(kNanPair, kNanPair, kNanPair, kNanPair);
+      }
     }
   }
   tc::fence_before_sync();
@@ -625,10 +745,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF, PAIR>::kThreads, 1) chunk_
   if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, C::kTCols);
 }
 
-template <int D, int KF, int VF, bool PAIR>
+template <int D, int KF, int VF>
 cudaError_t launch_chunk_one(const ChunkParams &p, cudaStream_t st) {
-  using C = ChunkCfg<D, KF, VF, PAIR>;
-  auto kernel = chunk_kernel<D, KF, VF, PAIR>;
+  using C = ChunkCfg<D, KF, VF>;
+  auto kernel = chunk_kernel<D, KF, VF>;
   static bool ready[64] = {};                // the shared-memory limit, set once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -644,11 +764,11 @@ cudaError_t launch_chunk_one(const ChunkParams &p, cudaStream_t st) {
   return launch_pdl(kernel, dim3(p.ctas), dim3(C::kThreads), C::kSmem, st, p);
 }
 
-template <int KF, bool PAIR>
+template <int KF>
 cudaError_t launch_chunk_formats(int D, int vf, const ChunkParams &p, cudaStream_t st) {
   auto by_dim = [&](auto v) -> cudaError_t {
     constexpr int V = decltype(v)::value;
-    return D == 128 ? launch_chunk_one<128, KF, V, PAIR>(p, st) : launch_chunk_one<256, KF, V, PAIR>(p, st);
+    return D == 128 ? launch_chunk_one<128, KF, V>(p, st) : launch_chunk_one<256, KF, V>(p, st);
   };
   switch (vf) {
     case MEMRA_KV_Q5_1: return by_dim(std::integral_constant<int, MEMRA_KV_Q5_1>{});

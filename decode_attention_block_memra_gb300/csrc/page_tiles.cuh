@@ -13,7 +13,7 @@ namespace memra {
 // that read it.  A warp task is one 512-byte run of codes.
 
 // Eight q8_0 or fp8 codes of K as fp16: q8_0 q d / 2 in hi + lo parts (d2 the
-// scale in both halves; hi alone is the value rounded once), fp8 the value in hi.
+// scale in both halves), fp8 the value in hi.
 template <int KF>
 __device__ __forceinline__ void convert_k16(uint2 w, uint32_t d2, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   if constexpr (KF == MEMRA_KV_Q8_0) {
@@ -37,8 +37,7 @@ __device__ __forceinline__ void convert_k16(uint2 w, uint32_t d2, uint32_t (&hi)
 // two 32-dim blocks; lanes of odd tokens store the second block first, so that
 // eight lanes' 16-byte stores always fall on different banks.
 // Tokens that do not exist stage whatever the pages hold: their scores are masked.
-// PAIR: q8_0 as exact hi + lo tiles, else as its hi part alone.
-template <int D, int KF, int KEYS, int WARPS, bool PAIR = true>
+template <int D, int KF, int KEYS, int WARPS>
 __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, int lane) {
   constexpr int NB = D / 32, SEG = k_seg_bytes(KF, D), B2 = D / 64;
   constexpr uint32_t LO = KEYS * D * 2;
@@ -99,10 +98,10 @@ __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, in
       uint32_t hi[4], lo[4];
       convert_k16<KF>(w0, __byte_perm(d[it % BATCH], 0, sel0), hi, lo);
       sts128(to0 + it * STEP * 1024, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      if constexpr (KF == MEMRA_KV_Q8_0 && PAIR) sts128(to0 + it * STEP * 1024 + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      if constexpr (KF == MEMRA_KV_Q8_0) sts128(to0 + it * STEP * 1024 + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       convert_k16<KF>(w1, __byte_perm(d[it % BATCH], 0, sel1), hi, lo);
       sts128(to1 + it * STEP * 1024, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      if constexpr (KF == MEMRA_KV_Q8_0 && PAIR) sts128(to1 + it * STEP * 1024 + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      if constexpr (KF == MEMRA_KV_Q8_0) sts128(to1 + it * STEP * 1024 + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
   }
 }
@@ -132,8 +131,7 @@ __device__ __forceinline__ uint32_t page_bits(uint64_t keep, int pg) {
 // warp's 8-byte stores fill all banks.  Tokens without a bit in `keep` become zeros:
 // 0 * (what their bytes stand for) need not be 0.  q5_1 stages d (q - 16) where
 // the blocks' centres have columns of their own (M_COLS), else d q + m by a TwoSum.
-// PAIR: hi + lo parts, else the value rounded once (d q + m by one fused operation).
-template <int D, int VF, int KEYS, int WARPS, bool M_COLS, uint32_t LO, bool PAIR = true>
+template <int D, int VF, int KEYS, int WARPS, bool M_COLS, uint32_t LO>
 __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint64_t keep, int warp, int lane) {
   constexpr int NB = D / 32, SEG = v_seg_bytes(VF, D), B2 = D / 64;
   const int vg = lane >> 2, c = lane & 3;
@@ -206,12 +204,6 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint64_t kee
             const int f = k >> 1, p = k & 1;
             const uint32_t sel = f ? 0x3232 : 0x1010;
             const uint32_t d2 = __byte_perm(bp ? (p ? d4.w : d4.z) : (p ? d4.y : d4.x), 0, sel);
-            if constexpr (VF == MEMRA_KV_Q5_1 && !PAIR) {
-              const __half2 m2 = __hmul2_rn(bits_h2(__byte_perm(bp ? (p ? m4.w : m4.z) : (p ? m4.y : m4.x), 0, sel)),
-                                            __float2half2_rn(0.5f));
-              hi[k][h] = hfma2_u32(q2, d2, h2_bits(m2));
-              continue;
-            }
             const uint32_t p_hi = h2_bits(__hmul2_rn(bits_h2(q2), bits_h2(d2)));
             const uint32_t p_lo = hfms2_u32(q2, d2, p_hi);
             if constexpr (VF == MEMRA_KV_Q5_1 && !M_COLS) {
@@ -231,16 +223,13 @@ __device__ __forceinline__ void stage_v(uint32_t raw, uint32_t buf, uint64_t kee
         if (bits != 0xFFFFu) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (!((bits >> (8 * (k & 1) + 2 * c + (k >> 1))) & 1u)) {
-              hi[k][0] = hi[k][1] = 0u;
-              if constexpr (PAIR) lo[k][0] = lo[k][1] = 0u;
-            }
+            if (!((bits >> (8 * (k & 1) + 2 * c + (k >> 1))) & 1u)) hi[k][0] = hi[k][1] = lo[k][0] = lo[k][1] = 0u;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t at = to[bp][k >> 1] + row + (k & 1) * 1024;
           sts64(at, hi[k][0], hi[k][1]);
-          if constexpr (PAIR) sts64(at + LO, lo[k][0], lo[k][1]);
+          sts64(at + LO, lo[k][0], lo[k][1]);
         }
       }
     }

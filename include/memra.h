@@ -476,10 +476,9 @@ int memra_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k
  *   lse           device float32 [total_tokens][n_heads], or NULL: the natural logarithm of
  *                 the sum of a row's exponentials (-inf for a row that sees no key)
  * All K and V formats, head_dim 128 or 256, n_heads / n_kv_heads <= MEMRA_MAX_GROUP,
- * batch and n_kv_heads <= 65535.  K^ and V^ enter the products in fp16, each value
- * rounded once (fp8 and NVFP4 exactly); with lse, q8_0 keys enter exactly.  The
- * weights are fp16, scores, sums and output are accumulated in float32.  The work is
- * cut by the lengths of the whole call, so that it fills the GPU: the same call gives
+ * batch and n_kv_heads <= 65535.  K^ and V^ enter the products exactly (or as fp16
+ * pairs), the softmax weights in fp16; everything is accumulated in float32, 7,680 keys
+ * to a sum of the tensor cores and the sums joined.  The work is cut by the lengths of the whole call, so that it fills the GPU: the same call gives
  * the same bytes, another batch may differ in the last bits.  A query, or a key that
  * a row sees, that is not finite makes the row NaN; a V that is not finite may also
  * reach rows of its sequence that do not see it.  A length out of range is clamped and

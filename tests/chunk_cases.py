@@ -74,16 +74,16 @@ class Chunk:
         first, k, v = self.rows[b]
         return first, dequantized(k[:, h], self.kf, self.scales[0]), dequantized(v[:, h], self.vf, self.scales[1])
 
-    def expected(self, b, h, exact_k):
+    def expected(self, b, h):
         """Rows of sequence b and KV head h: out [n, G, D], lse [n, G] and how far each may be off.
 
         To first order, with p the weights and d_u the errors of the scores:
-        |out - o| <= sum_u p_u (|d_u| |v_u - o| + (2 * 2^-11 + A) |v_u|) + 2^-11 |o|: a weight and a value of V rounded to
-        fp16, the output's rounding, and the accumulator, whose last bit is cut at each of up to 480 steps of a sum
-        (A = 480 * 2^-23, and 2^-19 for the sums of weights, the exponential and the joins).
-        d_u: K^ rounded (2^-11 of each product) unless exact, and D / 16 steps (twice for pairs) that cut the last bit.
-        Below fp16's normal range a rounding is off by half of 2^-24 instead, whatever the value: the integer formats are
-        staged at half size, K^'s low part too, so K^ is off by up to 2^-24 (2^-24 sum |q_j| in the score) and V^ likewise.
+        |out - o| <= sum_u p_u (|d_u| |v_u - o| + (2^-11 + A) |v_u|) + 2^-11 |o|: a weight rounded to fp16, the output's
+        rounding, and the accumulator, whose last bit is cut at each of up to 480 steps of a sum (960 with hi and lo parts:
+        A = 960 * 2^-23), and 2^-19 for the sums of weights, the exponential and the joins.
+        d_u: the accumulator of the score, cut at each of D / 16 steps (twice for pairs).
+        The integer formats enter as fp16 pairs of half their value.  Below fp16's normal range a rounding is off by half of
+        2^-24, whatever the value: K^ by up to 2^-24 (2^-24 sum |q_j| in the score), V^ likewise.
         """
         G, n = self.Hq // self.Hkv, self.new[b]
         first, k, v = self.keys(b, h)
@@ -91,7 +91,7 @@ class Chunk:
         sees = chunked.chunk_sees(n, T, self.window)[:, first:]
         q = self.q[self.starts[b]:self.starts[b + 1], h * G:(h + 1) * G].astype(np.float64)
         scale = self.D ** -0.5
-        per_key = 2.0 ** -23 * (self.D / 8) + (0 if exact_k or self.kf in ("fp8", "nvfp4") else 2.0 ** -11)
+        per_key = 2.0 ** -23 * (self.D / 8)
         out, tol = np.zeros((n, G, self.D)), np.zeros((n, G, self.D))
         lse, lse_tol = np.full((n, G), -np.inf), np.zeros((n, G))
         for g in range(G):
@@ -108,7 +108,7 @@ class Chunk:
             av = np.abs(v)
             # |v - o| <= |v| + |o|
             tol[:, g] = 1.05 * ((p * d) @ av + (p * d).sum(1, keepdims=True) * np.abs(out[:, g])) + \
-                (2.0 ** -10 + 480 * 2.0 ** -23 + 2.0 ** -19) * (p @ av) + 2.0 ** -11 * np.abs(out[:, g]) + 2.0 ** -23
+                (2.0 ** -11 + 960 * 2.0 ** -23 + 2.0 ** -19) * (p @ av) + 2.0 ** -11 * np.abs(out[:, g]) + 2.0 ** -23
             with np.errstate(divide="ignore"):
                 lse[:, g] = np.where(mass[:, 0] > 0, np.log(mass[:, 0]) + top[:, 0], -np.inf)
             lse_tol[:, g] = 1.05 * (p * d).sum(1) + 2.0 ** -19 + 2.0 ** -22 * np.where(np.isfinite(lse[:, g]), np.abs(lse[:, g]), 0)
@@ -121,7 +121,7 @@ class Chunk:
         for b in range(len(self.new)) if sequences is None else sequences:
             rows = slice(self.starts[b], self.starts[b + 1])
             for h in range(self.Hkv) if heads is None else heads:
-                out, tol, want_lse, lse_tol = self.expected(b, h, lse)
+                out, tol, want_lse, lse_tol = self.expected(b, h)
                 err = np.abs(got[rows, h * G:(h + 1) * G] - out)
                 assert (err <= tol).all(), f"sequence {b} head {h}: {np.nanmax(err / tol)} of the tolerance"
                 worst = max(worst, float((err / tol).max(initial=0.0)))
