@@ -119,6 +119,9 @@ _SIGS = {
     "memra_chunk_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
     "memra_chunk_attn": (ctypes.c_int, _CHUNK_ARGS),
     "memra_testing_chunk_attn_short_page": (ctypes.c_int, _CHUNK_ARGS),
+    "memra_key_weights": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int64] +
+                          [ctypes.c_void_p] * 3 + [ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 6 +
+                          [ctypes.c_float] * 2 + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     "memra_kv_evict": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p] +
                        [ctypes.c_int32] * 3 + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
@@ -525,6 +528,29 @@ def _chunk_args(cache, q, cu_seqlens, page_table, seq_lens, max_seq_len, out, wo
             _ptr(seq_lens), int(max_seq_len), B, T, Hq, cache.n_kv_heads, D,
             float(sm_scale if sm_scale is not None else D ** -0.5), int(window), _ptr(workspace),
             workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse))
+
+
+def key_weights(cache: KVCache, q, lse, cu_seqlens, page_table, seq_lens, max_seq_len: int, weights, keep: float = 1.0,
+                sm_scale=None, stream=None) -> None:
+    """memra_key_weights: adds to weights what each key collects from the rows of a chunk.
+
+    q, cu_seqlens, page_table, seq_lens as in chunk_attn, lse float32 [tokens,
+    Hq] as it writes them; weights float32 [B, Hkv, >= max_seq_len], times keep first.
+    """
+    import torch
+    where = "memra_key_weights"
+    T, Hq, D = q.shape
+    B, pages = page_table.shape
+    i32, f32 = torch.int32, torch.float32
+    device = _need_dense(where, (lse, f32, (T, Hq)), (cu_seqlens, i32, (B + 1,)), (page_table, i32, (B, pages)),
+                         (seq_lens, i32, (B,)), (weights, f32, (B, cache.n_kv_heads, weights.shape[-1])))
+    if cache.device_index != device:
+        raise MemraError(1, where)
+    rc = lib().memra_key_weights(cache.ref, _ptr(q), _row_stride(where, q, Hq, D, device), _ptr(lse), _ptr(cu_seqlens),
+                                 _ptr(page_table), pages, _ptr(seq_lens), int(max_seq_len), B, T, Hq, cache.n_kv_heads,
+                                 D, float(sm_scale if sm_scale is not None else D ** -0.5), float(keep), _ptr(weights),
+                                 weights.shape[-1], _stream(stream))
+    _check(rc, where)
 
 
 def kv_evict(cache: KVCache, page_table, seq_lens, max_seq_len: int, weights, budgets, dst_table, kept, sink: int = 0,

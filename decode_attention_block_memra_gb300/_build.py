@@ -26,11 +26,13 @@ STAMP = LIB + ".sha256"
 SOURCES = ["api.cu", "kv_append.cu", "combine.cu", "decode_d128.cu", "decode_d256.cu", "noalloc.cu", "cascade.cu",
            "api_pages.cu", "pages.cu", "api_prompt.cu", "prompt.cu",
            "api_tree.cu", "tree.cu", "api_norm_rope.cu", "norm_rope.cu", "api_evict.cu", "evict.cu",
-           "api_chunk.cu", "chunk.cu", "chunk_q8.cu", "chunk_fp8.cu", "chunk_nvfp4.cu"]
+           "api_chunk.cu", "chunk.cu", "chunk_q8.cu", "chunk_fp8.cu", "chunk_nvfp4.cu",
+           "api_key_weights.cu", "key_weights.cu"]
 HEADERS = ["memra_device.cuh", "decode_kernel.cuh", "kv_quant.cuh", "cascade.cuh", "tcgen05.cuh",
            "host_checks.cuh", "pages.cuh", "prompt.cuh", "kv_stage.cuh",
            "tree.cuh", "softmax_tile.cuh", "norm_rope.cuh", "page_rows.cuh", "evict.cuh",
-           "page_tiles.cuh", "chunk.cuh", "chunk_kernel.cuh"]
+           "page_tiles.cuh", "chunk.cuh", "chunk_kernel.cuh", "key_weights.cuh",
+           "tma.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]

@@ -1,0 +1,579 @@
+// Key weights: how much attention each cached key collects from a chunk of query
+// rows whose log-sum-exp is known, summed over the rows and the heads of a group.
+//
+//   w_u <- keep * w_u + sum over rows t, heads h that see key u of 2^(q_th . K^_u * scale * log2(e) - lse_th * log2(e))
+//
+// One pass over K, no V and no softmax state: the log-sum-exp makes every weight
+// final as its score is.  The keys are the M side of the tcgen05 MMAs, the query
+// rows the N side, so that a thread of the epilogue holds one key and adds up its
+// weights over all rows in a register: no sum crosses threads, and none is
+// atomic.  K^ is dequantized once (q8_0 as exact fp16 pairs: the weights are float32) and meets
+// every row tile while it lies in shared memory.
+//   * a copy warp brings raw pages, 32 keys at a time, into a ring of each staging group;
+//   * two groups of staging warps dequantize them into tiles of 128 keys;
+//   * a load warp brings row tiles of Q by TMA; where all rows of the chunk
+//     fit their ring, once for all keys of a CTA's run;
+//   * one MMA thread: S^T = K^ Q^T, two key tiles beside one another for each row tile;
+//   * two groups of four warps, one for each key tile: thread = key (at head_dim
+//     256 with q8_0 there is room for one tile of K^, and one group).
+// The (key tile, KV head, sequence) items of the call lie behind one another on a line
+// that the CTAs, one to an SM, share by their cost.
+#include <algorithm>
+#include <type_traits>
+
+#include "key_weights.cuh"
+#include "page_tiles.cuh"
+#include "softmax_tile.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace memra {
+namespace {
+
+constexpr int kStepKeys = 32;              // keys of a raw chunk
+constexpr int kTileSteps = kWeightKeys / kStepKeys;
+constexpr int kPieces = 4;
+
+// A run of key tiles of one KV head of a sequence.
+struct WeightPiece {
+  int first, n;                 // rows of the chunk
+  int T;
+  int h, b;
+  int tile0, tiles;             // tiles < 0: there is no more piece
+  int row_tiles;
+};
+
+struct WeightSeq {
+  int first, n, T;
+  bool bad;
+};
+
+__device__ __forceinline__ WeightSeq weight_seq(const WeightParams &p, int b) {
+  const int cs = p.cu_seqlens[b], ce = p.cu_seqlens[b + 1], T = p.seq_lens[b];
+  WeightSeq s;
+  s.first = min(max(cs, 0), p.total);
+  s.n = min(max(ce, s.first), p.total) - s.first;
+  s.T = max(0, min(T, p.len_limit));
+  s.bad = s.first != cs || s.first + s.n != ce || s.T != T || T < s.n;
+  return s;
+}
+
+// Tiles of a sequence's keys (none where the chunk has no row), and the cost of one: its row tiles and a fixed part.
+__device__ __forceinline__ int weight_tiles(const WeightSeq &s) { return s.n > 0 && s.T > 0 ? (s.T - 1) / kWeightKeys + 1 : 0; }
+__device__ __forceinline__ int weight_row_tiles(const WeightParams &p, int n) { return ((n - 1) / p.tpt + 1) * p.subs; }
+__device__ __forceinline__ int64_t weight_cost(const WeightParams &p, const WeightSeq &s) {
+  return s.n > 0 ? weight_row_tiles(p, s.n) + 1 : 1;
+}
+
+// Where a share begins: before a tile of a (head, sequence).
+struct WeightPlace {
+  int h, b, tile;
+};
+
+__device__ __forceinline__ int64_t weight_sum(int64_t x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+
+// Whole warp: the cost of one KV head's tiles.
+__device__ __forceinline__ int64_t weight_head_cost(const WeightParams &p, int lane) {
+  int64_t sum = 0;
+  for (int b = lane; b < p.batch; b += 32) {
+    const WeightSeq s = weight_seq(p, b);
+    sum += weight_tiles(s) * weight_cost(p, s);
+  }
+  return weight_sum(sum);
+}
+
+// Whole warp: the first tile that starts at `pos` of the line or behind it.
+__device__ __forceinline__ WeightPlace weight_place(const WeightParams &p, int64_t head_cost, int64_t pos, int lane) {
+  WeightPlace w{static_cast<int>(pos / head_cost), 0, 0};
+  const int64_t rest = pos % head_cost;
+  int64_t start = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int64_t mine = 0, per = 1;
+    if (b < p.batch) {
+      const WeightSeq s = weight_seq(p, b);
+      per = weight_cost(p, s);
+      mine = weight_tiles(s) * per;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
+    }
+    const int64_t at = rest - start - (incl - mine);
+    const unsigned who = __ballot_sync(0xffffffffu, at >= 0 && at < mine);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      w.b = b0 + src;
+      w.tile = static_cast<int>(__shfl_sync(0xffffffffu, (at + per - 1) / per, src));
+      break;
+    }
+    start += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return w;
+}
+
+// Walks a CTA's share.
+struct WeightWalk {
+  const WeightParams &p;
+  WeightPlace at, end;
+  __device__ __forceinline__ bool next(WeightPiece &x) {
+    while (true) {
+      if (at.h > end.h || (at.h == end.h && (at.b > end.b || (at.b == end.b && at.tile >= end.tile)))) return false;
+      const WeightSeq s = weight_seq(p, at.b);
+      const int tiles = weight_tiles(s);
+      const bool last = at.h == end.h && at.b == end.b;
+      x.first = s.first, x.n = s.n, x.T = s.T;
+      x.h = at.h, x.b = at.b;
+      x.tile0 = at.tile;
+      x.tiles = (last ? min(end.tile, tiles) : tiles) - at.tile;
+      x.row_tiles = s.n > 0 ? weight_row_tiles(p, s.n) : 0;
+      if (last)
+        at.tile = end.tile;
+      else {
+        at.tile = 0;
+        if (++at.b == p.batch) at.b = 0, ++at.h;
+      }
+      if (x.tiles > 0) return true;
+    }
+  }
+};
+
+template <int D, int KF>
+struct WeightCfg {
+  static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
+  static constexpr int kRows = weight_rows(D);
+  static constexpr int kTiles = D == 256 && kKLo ? 1 : 2;       // tiles of K^, and groups of the epilogue
+  static constexpr int kStageWarp0 = 4 * kTiles, kMmaWarp = kStageWarp0 + 8, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kCopyWarp = kLoadWarp + 1, kThreads = 32 * (kCopyWarp + 1);
+  static constexpr int kPages = kStepKeys / kPage;
+  static constexpr int kKSeg = k_seg_bytes(KF, D);
+  static constexpr int kBlocks = D / 64;                // 64-element column blocks of a row
+  static constexpr uint32_t kTile = kWeightKeys * D * 2, kKBuf = kTile * (kKLo ? 2 : 1);
+  static constexpr uint32_t kQBuf = kRows * D * 2, kRawBytes = kPages * kKSeg;
+  static constexpr uint32_t kRoom = 227 * 1024;
+  // barriers, page masks, the share, the pieces; each group's log-sum-exps of two row tiles; tiles of K^; Q; raw chunks
+  static constexpr uint32_t kOffBar = 0, kOffMask = 384, kOffShare = 448, kOffPiece = 480, kOffLse = 1024;
+  static constexpr uint32_t kOffK = kOffLse + 2048;
+  static constexpr uint32_t kOffQ = kOffK + kTiles * kKBuf;
+  // (two raw chunks at least beside the row tiles)
+  static constexpr int kQBufs = (kRoom - 1024 - kOffQ - 2 * kRawBytes) / kQBuf < 4 ? (kRoom - 1024 - kOffQ - 2 * kRawBytes) / kQBuf : 4;
+  static constexpr uint32_t kOffRaw = kOffQ + kQBufs * kQBuf;
+  // raw chunks of each staging group
+  static constexpr int kRaw = (kRoom - 1024 - kOffRaw) / (2 * kRawBytes) < 4 ? (kRoom - 1024 - kOffRaw) / (2 * kRawBytes) : 4;
+  static constexpr uint32_t kTCols = 512, kNeed = kOffRaw + 2 * kRaw * kRawBytes + 1024, kFloor = 150 * 1024;      // (1024: aligning the base)
+  static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
+  enum Bar { kRawFull = 0, kRawEmpty = kRawFull + 2 * kRaw, kKFull = kRawEmpty + 2 * kRaw, kKFree = kKFull + 2, kQFull = kKFree + 2,
+             kQFree = kQFull + kQBufs, kSFull = kQFree + kQBufs, kSFree = kSFull + 4, kDrained = kSFree + 4, kPieceFull,
+             kPieceFree = kPieceFull + kPieces, kBars = kPieceFree + kPieces };
+  static_assert(kQBufs >= 1 && kRaw >= 1, "rings");
+  static_assert(kOffBar + 8 * kBars + 4 <= kOffMask, "barriers and the tensor-memory address");
+  static_assert(kOffPiece + kPieces * sizeof(WeightPiece) <= kOffLse, "pieces");
+  static_assert(kTiles * 2 * kRows * 4 <= 2048, "log-sum-exps");
+  static_assert(kTiles * 2 * kRows <= 512, "tensor memory");
+  static_assert(kOffK % 1024 == 0 && kQBuf % 1024 == 0 && kOffRaw % 16 == 0 && kSmem <= 232448, "alignment, shared memory");
+};
+
+// Row tiles of a chunk that may see the keys from `key0` on: the first of them.
+__device__ __forceinline__ int weight_first_row_tile(const WeightParams &p, int n, int T, int key0) {
+  const int t = key0 - (T - n);                        // the first token that sees key0
+  return t > 0 ? t / p.tpt * p.subs : 0;
+}
+
+template <int D, int KF>
+__global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap qmap, const WeightParams p) {
+  using C = WeightCfg<D, KF>;
+  constexpr int N = C::kRows, G = C::kTiles, NP = C::kPages, RAW = C::kRaw, QB = C::kQBufs;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](int which, int i) { return sb + C::kOffBar + 8 * (which + i); };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffBar + 8 * C::kBars);
+  volatile uint8_t *page_mask = smem + C::kOffMask;
+  WeightPlace *share = reinterpret_cast<WeightPlace *>(smem + C::kOffShare);
+  WeightPiece *pieces = reinterpret_cast<WeightPiece *>(smem + C::kOffPiece);
+
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if (warp == 0) {
+    const int64_t head = weight_head_cost(p, lane), all = head * p.n_kv_heads;
+    const int c = blockIdx.x, n = p.ctas;
+    WeightPlace from{0, 0, 0}, to{-1, 0, 0};           // none
+    if (head > 0) {
+      if (c > 0) from = weight_place(p, head, all * c / n, lane);
+      to = WeightPlace{p.n_kv_heads, 0, 0};
+      if (c + 1 < n) to = weight_place(p, head, all * (c + 1) / n, lane);
+    }
+    if (lane == 0) share[0] = from, share[1] = to;
+    if (c == 0)                                        // one CTA checks every length
+      for (int b = lane; b < p.batch; b += 32)
+        if (weight_seq(p, b).bad) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
+  } else if (warp == C::kCopyWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < 2 * RAW; ++i) {
+        mbar_init(bar(C::kRawFull, i), 1);
+        mbar_init(bar(C::kRawEmpty, i), 4);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(C::kKFull, i), G == 2 ? 4 : 8);
+        mbar_init(bar(C::kKFree, i), 1);
+      }
+      for (int i = 0; i < QB; ++i) {
+        mbar_init(bar(C::kQFull, i), 1);
+        mbar_init(bar(C::kQFree, i), 1);
+      }
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(bar(C::kSFull, i), 1);
+        mbar_init(bar(C::kSFree, i), 4);
+      }
+      mbar_init(bar(C::kDrained, 0), 1);
+      for (int i = 0; i < kPieces; ++i) {
+        mbar_init(bar(C::kPieceFull, i), 1);
+        mbar_init(bar(C::kPieceFree, i), C::kCopyWarp);          // every other warp
+      }
+      fence_barrier_init();
+    }
+  } else if (warp == C::kMmaWarp) {
+    tc::tmem_alloc(smem_addr(tmem_slot), C::kTCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+  int piece = 0;
+  // The next piece, for the warps that are told of it (one thread of some); and that this warp is done with one.
+  auto next_piece = [&]() -> const volatile WeightPiece * {
+    const int i = piece % kPieces;
+    ok = ok && mbar_wait_suspended(bar(C::kPieceFull, i), (piece / kPieces) & 1, p.status);
+    return pieces + i;
+  };
+  auto free_piece = [&] {
+    mbar_arrive(bar(C::kPieceFree, piece % kPieces));
+    ++piece;
+  };
+  // Row tile rt: its first token in the chunk, the first of its heads, and its rows.
+  auto tokens_of = [&](int rt) { return rt / p.subs * p.tpt; };
+  auto heads_of = [&](int rt) { return rt % p.subs * p.hpt; };
+  auto rows_of = [&](int rt, int n) {
+    return min(p.tpt, n - tokens_of(rt)) * p.hpt - max(0, heads_of(rt) + p.hpt - p.group);
+  };
+
+  // The staging group that takes step i of a piece: tiles by turns, or the steps of the one tile.
+  auto owner_of = [](int i) { return G == 2 ? i / kTileSteps & 1 : i & 1; };
+
+  if (warp == C::kCopyWarp) {
+    // ----------------------------------------------------------------- copies --
+    WeightWalk walk{p, share[0], share[1]};
+    WeightPiece x;
+    int cc = 0, used[2] = {0, 0};            // raw chunks so far, and by staging group
+    while (ok) {
+      const bool more = walk.next(x);
+      if (!more) x.tiles = -1;
+      const int at = piece % kPieces;
+      if (piece >= kPieces) ok = mbar_wait_suspended(bar(C::kPieceFree, at), (piece / kPieces - 1) & 1, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        pieces[at] = x;
+        mbar_arrive(bar(C::kPieceFull, at));
+      }
+      __syncwarp();
+      ++piece;
+      if (!more) break;
+      const int32_t *table = p.page_table + static_cast<size_t>(x.b) * p.max_pages;
+      const int steps = kTileSteps * x.tiles;
+      // Page id of a logical page, -1: none (past the keys or outside the pool); 32 pages are read at a time, ahead.
+      auto page_id = [&](int step) {
+        const int i = (kTileSteps * x.tile0 + step) * NP + (lane & (NP - 1));
+        if (step >= steps || i > (x.T - 1) / kPage) return -1;
+        const int pid = table[i];
+        if (pid >= 0 && pid < p.num_pages) return pid;
+        flag_error(p.status, MEMRA_DEVERR_BAD_PAGE);
+        return -1;
+      };
+      constexpr int kAhead = 32 / NP;
+      int ids = page_id(lane / NP), ahead = page_id(kAhead + lane / NP);
+      for (int i = 0; i < steps; ++i, ++cc) {
+        if (i > 0 && i % kAhead == 0) {
+          ids = ahead;
+          ahead = page_id(i + kAhead + lane / NP);
+        }
+        int pid = __shfl_sync(0xffffffffu, ids, (i % kAhead) * NP + (lane & (NP - 1)));
+        if (lane >= NP) pid = -1;
+        const int o = owner_of(i), s = o * RAW + used[o] % RAW;
+        if (used[o] >= RAW) ok = mbar_wait_suspended(bar(C::kRawEmpty, s), (used[o] / RAW - 1) & 1, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++used[o];
+        const uint32_t there = __ballot_sync(0xffffffffu, pid >= 0);
+        if (lane == 0) {
+          page_mask[cc & 63] = static_cast<uint8_t>(there);
+          if (there)
+            mbar_arrive_expect_tx(bar(C::kRawFull, s), __popc(there) * C::kKSeg);
+          else
+            mbar_arrive(bar(C::kRawFull, s));
+        }
+        __syncwarp();
+        if (pid >= 0)
+          bulk_copy_g2s_nohint(sb + C::kOffRaw + s * C::kRawBytes + lane * C::kKSeg,
+                               p.k_pool + (static_cast<size_t>(pid) * p.n_kv_heads + x.h) * C::kKSeg, C::kKSeg,
+                               bar(C::kRawFull, s));
+      }
+    }
+    // every copy has landed before the CTA can leave
+    for (int o = 0; o < 2; ++o)
+      for (int c = max(0, used[o] - RAW); c < used[o]; ++c)
+        mbar_wait_suspended(bar(C::kRawFull, o * RAW + c % RAW), (c / RAW) & 1, p.status);
+    __syncwarp();
+  } else if (warp == C::kLoadWarp) {
+    // ---------------------------------------------------------------- Q tiles --
+    if (tc::elect_one()) {
+      int qn = 0;                            // loads so far
+      auto load = [&](const volatile WeightPiece *x, int rt) {
+        const int s = qn % QB;
+        if (ok && qn >= QB) ok = mbar_wait_suspended(bar(C::kQFree, s), (qn / QB - 1) & 1, p.status);
+        if (!ok) return;
+        mbar_arrive_expect_tx(bar(C::kQFull, s), static_cast<uint32_t>(p.hpt * p.tpt) * 128 * C::kBlocks);
+#pragma unroll
+        for (int c = 0; c < C::kBlocks; ++c)
+          tma_load_3d(sb + C::kOffQ + s * C::kQBuf + c * N * 128, &qmap, 64 * c, x->h * p.group + heads_of(rt),
+                      x->first + tokens_of(rt), bar(C::kQFull, s));
+        ++qn;
+      };
+      while (true) {
+        const volatile WeightPiece *x = next_piece();
+        if (!ok || x->tiles < 0) break;
+        const int tiles = x->tiles, rts = x->row_tiles, n = x->n, T = x->T, tile0 = x->tile0;
+        const int first = weight_first_row_tile(p, n, T, tile0 * kWeightKeys);
+        if (rts - first <= QB) {             // all that the run needs fit: once
+          for (int rt = first; rt < rts && ok; ++rt) load(x, rt);
+        } else {
+          for (int t = 0; t < tiles && ok; t += G)
+            for (int rt = weight_first_row_tile(p, n, T, (tile0 + t) * kWeightKeys); rt < rts && ok; ++rt) load(x, rt);
+        }
+        free_piece();
+      }
+      for (int c = max(0, qn - QB); c < qn; ++c) mbar_wait_suspended(bar(C::kQFull, c % QB), (c / QB) & 1, p.status);
+    }
+    __syncwarp();
+  } else if (warp == C::kMmaWarp) {
+    // -------------------------------------------------------------------- MMA --
+    if (tc::elect_one()) {
+      int qn = 0, kn[2] = {0, 0}, sn[2] = {0, 0};      // loads of Q used, tiles of K^ and score buffers used by group
+      auto wait = [&](int which, int i, int phase) { ok = ok && mbar_wait_suspended(bar(which, i), phase & 1, p.status); };
+      while (true) {
+        const volatile WeightPiece *x = next_piece();
+        if (!ok || x->tiles < 0) break;
+        const int tiles = x->tiles, rts = x->row_tiles, n = x->n, T = x->T, tile0 = x->tile0;
+        const int first = weight_first_row_tile(p, n, T, tile0 * kWeightKeys);
+        const bool held = rts - first <= QB;
+        for (int t = 0; t < tiles && ok; t += G) {
+          const int low = weight_first_row_tile(p, n, T, (tile0 + t) * kWeightKeys);
+          for (int rt = low; rt < rts && ok; ++rt) {
+            const int use = held ? qn + rt - first : qn, qs = use % QB;
+            wait(C::kQFull, qs, use / QB);
+            const uint32_t idesc = tc::idesc_f16_f32(kWeightKeys, (rows_of(rt, n) + 15) & ~15);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              if (t + g >= tiles) continue;
+              const int sbuf = 2 * g + (sn[g] & 1);
+              if (rt == low) wait(C::kKFull, g, kn[g]);
+              if (sn[g] >= 2) wait(C::kSFree, sbuf, (sn[g] >> 1) - 1);
+              if (!ok) continue;
+              tc::fence_after_sync();
+              const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffK + g * C::kKBuf, 16, 1024);
+              const uint64_t qd = tc::smem_desc_sw128(sb + C::kOffQ + qs * C::kQBuf, 16, 1024);
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint64_t bd = tc::desc_at(qd, (ks / 4) * N * 128 + (ks % 4) * 32);
+#pragma unroll
+                for (int lo = 0; lo < (C::kKLo ? 2 : 1); ++lo)
+                  tc::mma_f16(tmem + sbuf * N, tc::desc_at(kd, (ks / 4) * kWeightKeys * 128 + (ks % 4) * 32 + lo * C::kTile),
+                              bd, idesc, ks + lo > 0);
+              }
+              tc::commit(bar(C::kSFull, sbuf));
+              ++sn[g];
+              if (rt == rts - 1) {
+                tc::commit(bar(C::kKFree, g));
+                ++kn[g];
+              }
+            }
+            if (!ok) break;
+            if (!held) {
+              tc::commit(bar(C::kQFree, qs));
+              ++qn;
+            }
+          }
+        }
+        if (held && ok) {
+          for (int rt = first; rt < rts; ++rt) tc::commit(bar(C::kQFree, (qn + rt - first) % QB));
+          qn += rts - first;
+        }
+        free_piece();
+      }
+      tc::commit(bar(C::kDrained, 0));       // what was issued completes before the CTA can leave
+      mbar_wait_suspended(bar(C::kDrained, 0), 0, p.status);
+    }
+    __syncwarp();
+  } else if (warp >= C::kStageWarp0) {
+    // ---------------------------------------------------------------- staging --
+    const int sg = (warp - C::kStageWarp0) / 4, sw = (warp - C::kStageWarp0) % 4;
+    int used = 0, kn = 0;                    // raw chunks and tiles of K^ so far
+    while (true) {
+      const volatile WeightPiece *x = next_piece();
+      ok = __all_sync(0xffffffffu, ok);
+      const int tiles = ok ? x->tiles : -1;
+      if (tiles < 0) break;
+      __syncwarp();
+      if (lane == 0) free_piece(); else ++piece;
+      for (int t = G == 2 ? sg : 0; t < tiles && ok; t += G) {
+        const int g = G == 2 ? sg : 0;
+        if (kn > 0) ok = mbar_wait_suspended(bar(C::kKFree, g), (kn - 1) & 1, p.status);
+        ++kn;
+#pragma unroll 1
+        for (int i = G == 2 ? 0 : sg; i < kTileSteps; i += G == 2 ? 1 : 2, ++used) {
+          const int s = sg * RAW + used % RAW;
+          if (ok) ok = mbar_wait_suspended(bar(C::kRawFull, s), (used / RAW) & 1, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          stage_k<D, KF, kStepKeys, 4, kWeightKeys>(sb + C::kOffRaw + s * C::kRawBytes,
+                                                    sb + C::kOffK + g * C::kKBuf + i * kStepKeys * 128, sw, lane);
+          fence_proxy_async();               // K^ for the tensor cores, the raw chunk for the next copies
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kRawEmpty, s));
+        }
+        if (ok && lane == 0) mbar_arrive(bar(C::kKFull, g));
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- epilogue --
+    const int g = warp >> 2, kl = tid & 127;           // group, key of its tile
+    const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float *const lse_s = reinterpret_cast<float *>(smem + C::kOffLse) + g * 2 * N;
+    int sn = 0, cc = 0;
+    while (true) {
+      const volatile WeightPiece *x = next_piece();
+      ok = named_barrier_and(1 + g, 128, ok);          // a group's warps go on together, or none
+      if (!ok || x->tiles < 0) break;
+      const int tiles = x->tiles, rts = x->row_tiles, n = x->n, T = x->T, tile0 = x->tile0;
+      const int h = x->h, first = x->first;
+      float *const row = p.weights + (static_cast<int64_t>(x->b) * p.n_kv_heads + h) * p.weight_stride;
+      // log-sum-exp (base 2) of this thread's column of a row tile; none: +inf
+      auto lse_of = [&](int rt) {
+        if (rt >= rts || kl >= rows_of(rt, n)) return INFINITY;
+        const int t = first + tokens_of(rt) + kl / p.hpt;
+        return p.lse[static_cast<int64_t>(t) * p.n_heads + h * p.group + heads_of(rt) + kl % p.hpt] * 1.4426950408889634f;
+      };
+      for (int t = g; t < tiles && ok; t += G) {
+        const int key = (tile0 + t) * kWeightKeys + kl;
+        const int low = weight_first_row_tile(p, n, T, (tile0 + t / G * G) * kWeightKeys);
+        float old = 0.f, next = lse_of(low);
+        if (p.keep != 0.f && key < T) old = row[key];
+        bool here = key < T;
+        float sum = 0.f;
+        for (int rt = low; rt < rts; ++rt) {
+          float *const lse = lse_s + (sn & 1) * N;
+          const int live = rows_of(rt, n), sbuf = 2 * g + (sn & 1);
+          if (kl < N) lse[kl] = next;
+          next = lse_of(rt + 1);
+          ok = ok && mbar_wait_suspended(bar(C::kSFull, sbuf), (sn >> 1) & 1, p.status);
+          ok = named_barrier_and(1 + g, 128, ok);
+          if (!ok) break;
+          ++sn;
+          tc::fence_after_sync();
+          if (rt == low)
+            here = here && (page_mask[(cc + kTileSteps * t + kl / kStepKeys) & 63] >> (kl % kStepKeys / kPage) & 1);
+          // columns from `from` on belong to tokens that see the key
+          const int from = here ? min(max(0, key - (T - n) - tokens_of(rt)), N) * p.hpt : INT32_MAX;
+          const uint32_t s_col = tmem + tlane + sbuf * N;
+          uint64_t acc = 0;
+#pragma unroll 1
+          for (int c = 0; c < live; c += 32) {
+            uint32_t s[32];
+            tc::ld_32x32b_x32(s_col + c, s);
+            tc::wait_ld_all();
+            tc::hold<32>(s);
+            const uint64_t scale2 = pack_f2(p.scale_log2, p.scale_log2);
+            const bool all = __all_sync(0xffffffffu, from <= c) && c + 32 <= live;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 l = *reinterpret_cast<const float4 *>(lse + c + e);
+              float w[4];
+              unpack_f2(fma_f2(pack_f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, pack_f2(-l.x, -l.y)), w[0], w[1]);
+              unpack_f2(fma_f2(pack_f2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, pack_f2(-l.z, -l.w)), w[2], w[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = fast_exp2(w[k]);
+              if (!all) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = c + e + k >= from && c + e + k < live ? w[k] : 0.f;
+              }
+              acc = add_f2(acc, pack_f2(w[0], w[1]));
+              acc = add_f2(acc, pack_f2(w[2], w[3]));
+            }
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kSFree, sbuf));
+          float a0, a1;
+          unpack_f2(acc, a0, a1);
+          sum += a0 + a1;
+        }
+        if (ok && key < T) row[key] = p.keep != 0.f ? fmaf(p.keep, old, sum) : sum;
+      }
+      cc += kTileSteps * tiles;
+      __syncwarp();
+      if (lane == 0) free_piece(); else ++piece;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, C::kTCols);
+}
+
+template <int D, int KF>
+cudaError_t launch_one(const WeightParams &p, cudaStream_t st) {
+  using C = WeightCfg<D, KF>;
+  auto kernel = key_weights_kernel<D, KF>;
+  static bool ready[64] = {};                // the shared-memory limit, set once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  CUtensorMap qm;
+  if (!encode_rows(&qm, p.q, D, p.n_heads, p.total, p.q_stride, p.hpt, p.tpt)) return cudaErrorInvalidValue;
+  return launch_pdl(kernel, dim3(p.ctas), dim3(C::kThreads), C::kSmem, st, qm, p);
+}
+
+template <int D>
+cudaError_t launch_formats(int kf, const WeightParams &p, cudaStream_t st) {
+  switch (kf) {
+    case MEMRA_KV_Q8_0: return launch_one<D, MEMRA_KV_Q8_0>(p, st);
+    case MEMRA_KV_FP8_E4M3: return launch_one<D, MEMRA_KV_FP8_E4M3>(p, st);
+    case MEMRA_KV_NVFP4: return launch_one<D, MEMRA_KV_NVFP4>(p, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_key_weights(int D, int kf, const WeightParams &p, cudaStream_t st) {
+  return D == 128 ? launch_formats<128>(kf, p, st) : launch_formats<256>(kf, p, st);
+}
+
+}  // namespace memra

@@ -37,10 +37,11 @@ __device__ __forceinline__ void convert_k16(uint2 w, uint32_t d2, uint32_t (&hi)
 // two 32-dim blocks; lanes of odd tokens store the second block first, so that
 // eight lanes' 16-byte stores always fall on different banks.
 // Tokens that do not exist stage whatever the pages hold: their scores are masked.
-template <int D, int KF, int KEYS, int WARPS>
+// ROWS: of the tile that `buf` is a part of, KEYS of them from a multiple of 8 on.
+template <int D, int KF, int KEYS, int WARPS, int ROWS = KEYS>
 __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, int lane) {
   constexpr int NB = D / 32, SEG = k_seg_bytes(KF, D), B2 = D / 64;
-  constexpr uint32_t LO = KEYS * D * 2;
+  constexpr uint32_t LO = ROWS * D * 2;
   const int tg = lane >> 2, kc = lane & 3;
   if constexpr (KF == MEMRA_KV_NVFP4) {
     // run (page, 64-dim block): words (b % 2, e / 4), bytes tp + 2 (e % 4 / 2), nibbles e % 2
@@ -64,7 +65,7 @@ __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, in
           h.y = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2((w0 >> 16) & 0xFFu)), s2));
           h.z = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2(w1 & 0xFFu)), s2));
           h.w = h2_bits(__hmul2(bits_h2(e2m1x2_to_half2((w1 >> 16) & 0xFFu)), s2));
-          sts128(buf + b2 * KEYS * 128 + (kPage * pg + t) * 128 + ((u ^ tg) << 4), h);
+          sts128(buf + b2 * ROWS * 128 + (kPage * pg + t) * 128 + ((u ^ tg) << 4), h);
         }
     }
   } else {
@@ -74,7 +75,7 @@ __device__ __forceinline__ void stage_k(uint32_t raw, uint32_t buf, int warp, in
     const unsigned g0 = static_cast<unsigned>(warp) / B2, b2 = static_cast<unsigned>(warp) % B2;
     const bool odd = tg & 1;
     const uint32_t sel0 = odd ? 0x3232u : 0x1010u, sel1 = odd ? 0x1010u : 0x3232u;
-    const uint32_t row = buf + b2 * (KEYS * 128) + (8 * g0 + tg) * 128;
+    const uint32_t row = buf + b2 * (ROWS * 128) + (8 * g0 + tg) * 128;
     const uint32_t to0 = row + (((odd ? 4 : 0) + kc) ^ tg) * 16, to1 = row + (((odd ? 0 : 4) + kc) ^ tg) * 16;
     const uint32_t codes = raw + (g0 >> 1) * SEG + (((g0 & 1) * B2 + b2) * 32 + lane) * 16;
     const uint32_t scales = raw + (g0 >> 1) * SEG + 16 * D + ((8 * (g0 & 1) + tg) * NB + 2 * b2) * 2;

@@ -42,7 +42,6 @@
 // tensor pipe active 78% of the time; 8 ragged prompts of up to 4,860 tokens 490 to
 // 519 us (1,263 to 1,337 TFLOP/s, 67%); 9,713 tokens, 16/2 heads, D 256, window 1,024:
 // 149 us (935 TFLOP/s, 44%, 17 steps a CTA); 256 tokens, 8/2 heads: 9.1 us, all latency.
-#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -50,6 +49,7 @@
 #include "kv_stage.cuh"
 #include "softmax_tile.cuh"
 #include "tcgen05.cuh"
+#include "tma.cuh"
 
 namespace memra {
 namespace {
@@ -83,15 +83,6 @@ struct PromptCfg {
   static constexpr uint32_t kQCol = 128, kOCol = 256;
   static_assert(kSmem <= 232448, "shared memory");
 };
-
-// One TMA tensor copy: a box of a 3-D tensor map at (x, y, z) to shared memory.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
 
 // The sequence and the tile pair of this CTA, found from the packed lengths.
 struct Work {
@@ -571,38 +562,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   if (warp == kScoreWarp) tc::tmem_dealloc(tmem, 512);
-}
-
-// The driver's tensor-map encoder, looked up once (the library links the runtime only).
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
-
-// [tokens][heads][D] fp16 as a 3-D map with boxes of 64 elements x heads x tokens, 128-byte swizzle.
-bool encode_rows(CUtensorMap *map, const void *base, int D, int heads, int tokens, int64_t stride, int box_heads,
-                 int box_tokens) {
-  const EncodeFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
-                              static_cast<cuuint64_t>(tokens)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
-  const cuuint32_t one[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>

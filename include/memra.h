@@ -493,6 +493,30 @@ int memra_chunk_attn(const memra_kv_cache *cache, const void *q, int64_t q_strid
                      int32_t head_dim, float sm_scale, int32_t window, void *workspace, size_t workspace_bytes,
                      void *out, float *lse, void *stream);
 
+/* How much attention each cached key collects from a chunk, summed over the chunk's
+ * rows and the query heads of a KV head: what an eviction goes by.
+ *   w[b][g][u] = keep * w[b][g][u] + sum over rows t of sequence b that see key u and
+ *                heads h of KV head g of exp(q[t,h] . K^[u] * sm_scale - lse[t,h])
+ * for u < seq_lens[b]; what lies behind stays as it is.  keep 1 adds up over the calls,
+ * 0 starts anew (w need not have been written), between them older calls fade.
+ *   q, q_stride, cu_seqlens, page_table, seq_lens, max_seq_len, total_tokens, sm_scale
+ *                 as in memra_chunk_attn: rows see the keys up to their own position
+ *   lse           device float32 [total_tokens][n_heads], natural logarithms, as
+ *                 memra_chunk_attn writes them (of the same call or of other keys:
+ *                 the weights are then relative to those)
+ *   keep          finite
+ *   weights       device float32 [batch][n_kv_heads][weight_stride], weight_stride >= max_seq_len
+ * A sequence without rows in the call keeps its weights.  Keys of a page id outside the
+ * pool collect nothing (MEMRA_DEVERR_BAD_PAGE); a length out of range is clamped
+ * (MEMRA_DEVERR_BAD_SEQ_LEN).  K^ enters exactly (or as fp16 pairs); sums are
+ * float32, in a fixed order.  Limits as memra_chunk_attn; q_stride < 2^38.  No workspace.
+ * batch == 0 or total_tokens == 0 is a no-op. */
+int memra_key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stride, const float *lse,
+                      const int32_t *cu_seqlens, const int32_t *page_table, int32_t max_pages_per_seq,
+                      const int32_t *seq_lens, int32_t max_seq_len, int32_t batch, int32_t total_tokens, int32_t n_heads,
+                      int32_t n_kv_heads, int32_t head_dim, float sm_scale, float keep, float *weights,
+                      int64_t weight_stride, void *stream);
+
 /* Eviction: the rows of a sequence that have collected the most attention weight
  * move to other pages, for each KV head its own, and the rest is left behind.  Of
  * a sequence of T = seq_lens[b] tokens n = min(T, budgets[b]) stay, in their order:

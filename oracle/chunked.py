@@ -54,7 +54,7 @@ def logits(q, k, sees, sm_scale: float) -> np.ndarray:
 
 def logits_lse(s) -> np.ndarray:
     """[n, Hq] log of the sum of the exponentials; -inf for rows that see nothing."""
-    top = s.max(-1, keepdims=True)
+    top = s.max(-1, keepdims=True, initial=-np.inf)
     safe = np.where(np.isfinite(top), top, 0.0)
     with np.errstate(divide="ignore"):
         return (np.log(np.exp(s - safe).sum(-1)) + safe[..., 0]).T

@@ -131,3 +131,38 @@ def test_chunk_checks(memra):
         assert call(scale=scale) == INVALID
     hook = memra.lib().memra_testing_chunk_attn_short_page
     assert call(f=hook, Hq=7) == INVALID and call(f=hook, B=0) == 0
+
+
+def test_key_weights_checks(memra):
+    good = dict(q=64, qs=1024, lse=64, cu=64, pt=64, maxp=4, sl=64, maxlen=64, B=2, T=8, Hq=8, Hkv=2, D=128, scale=0.1,
+                keep=1.0, w=64, ws=64)
+
+    def call(c=None, **kw):
+        a = {**good, **kw}
+        return memra.lib().memra_key_weights(
+            ctypes.byref(c or cache(memra)), a["q"], a["qs"], a["lse"], a["cu"], a["pt"], a["maxp"], a["sl"], a["maxlen"],
+            a["B"], a["T"], a["Hq"], a["Hkv"], a["D"], a["scale"], a["keep"], a["w"], a["ws"], None)
+
+    assert call(B=0) == 0
+    assert call(T=0) == 0
+    for name in ("q", "lse", "cu", "pt", "sl", "w"):
+        assert call(**{name: 0}) == INVALID
+    assert call(q=72) == INVALID
+    for name in ("lse", "cu", "pt", "sl", "w"):
+        assert call(**{name: 66}) == INVALID
+    for name in ("B", "T", "maxlen"):
+        assert call(**{name: -1}) == INVALID
+    assert call(maxp=0) == INVALID
+    assert call(ws=63) == INVALID
+    assert call(qs=1016) == INVALID
+    assert call(qs=1028) == INVALID
+    assert call(qs=1 << 38) == UNSUPPORTED
+    assert call(Hq=7) == INVALID
+    assert call(Hkv=4) == INVALID                  # not the cache's
+    assert call(D=256) == INVALID
+    assert call(Hq=2 * 129, qs=2 * 129 * 128) == UNSUPPORTED
+    assert call(B=65536) == UNSUPPORTED
+    assert call(c=cache(memra, v_fmt=0)) == UNSUPPORTED
+    for x in (float("nan"), float("inf")):
+        assert call(keep=x) == INVALID and call(scale=x) == INVALID
+    assert call(scale=0.0) == INVALID
