@@ -30,7 +30,7 @@ SOURCES = ["api.cu", "kv_append.cu", "combine.cu", "decode_d128.cu", "decode_d25
            "api_key_weights.cu", "key_weights.cu"]
 HEADERS = ["memra_device.cuh", "decode_kernel.cuh", "kv_quant.cuh", "cascade.cuh", "tcgen05.cuh",
            "host_checks.cuh", "pages.cuh", "prompt.cuh", "kv_stage.cuh",
-           "tree.cuh", "softmax_tile.cuh", "norm_rope.cuh", "page_rows.cuh", "evict.cuh",
+           "tree.cuh", "softmax_tile.cuh", "norm_rope.cuh", "evict.cuh",
            "page_tiles.cuh", "chunk.cuh", "chunk_kernel.cuh", "key_weights.cuh",
            "tma.cuh"]
 

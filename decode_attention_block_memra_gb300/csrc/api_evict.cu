@@ -60,5 +60,5 @@ extern "C" int memra_kv_evict(const memra_kv_cache *cache, const int32_t *page_t
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = cuda_status(launch_evict_select(p, device_sms(), s));
   if (st) return st;
-  return cuda_status(launch_evict_move(cache->head_dim, p, s));
+  return cuda_status(launch_evict_move(cache->head_dim, p, device_sms(), s));
 }

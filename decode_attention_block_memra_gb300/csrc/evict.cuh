@@ -27,6 +27,6 @@ struct EvictParams {
 };
 
 cudaError_t launch_evict_select(const EvictParams &p, int sms, cudaStream_t st);
-cudaError_t launch_evict_move(int D, const EvictParams &p, cudaStream_t st);
+cudaError_t launch_evict_move(int D, const EvictParams &p, int sms, cudaStream_t st);
 
 }  // namespace memra
