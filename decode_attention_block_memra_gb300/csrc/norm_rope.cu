@@ -12,14 +12,18 @@
 // Angles.  position * inv_freq reaches 10^5 and more radians, where float32 has no
 // digits left behind the point.  So a frequency is kept in turns (inv_freq / 2 pi)
 // as a 64-bit binary fraction, rounded once, and the position multiplies it modulo
-// 2^64: whole turns fall away exactly, and the angle of position 2^20 is off by
-// less than 2^-27 turns.  Its sine and cosine are taken once a token, not once a head: the
-// CTA's threads put them into shared memory for all rows of their tokens.
+// 2^64: whole turns fall away exactly.  What is left within an eighth of a turn goes
+// through the Taylor series of sine and cosine, with what float32 drops of the angle and of the
+// leading terms carried along: a key next to a border of its 8-bit code falls to one
+// side or the other by its last bits, and should not do so by the sine's.
 //
 // A row is D / 8 lanes of 8 consecutive dims (one 16-byte load); a warp takes 32 / (D / 8)
 // heads of one token at a time, of one kind (K, V or Q), so that it never diverges
-// in the quantizer, and has the next rows' loads in flight meanwhile.
+// in the quantizer.  With many tokens a warp's unit is all rows of a token: every unit
+// costs the same, the angles are taken once, and no warp waits for another.  With few, a
+// unit is one row group.  The next rows' loads are in flight throughout.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_stage.cuh"
 #include "norm_rope.cuh"
@@ -28,150 +32,259 @@ namespace memra {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kTileMax = 8;                // tokens of a CTA at most
+
+// An unevaluated sum, |lo| <= half an ulp of hi.
+struct Two {
+  float hi, lo;
+};
+
+// a * b exactly (Dekker, with a fused product); a + b for |a| >= |b|.
+__device__ __forceinline__ Two two_prod(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Two fast_two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ void unpack(const uint4 &y, float (&x)[8]) {
+  const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(bits_h2(in[i]));
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+  return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+}
+
+// Sine and cosine of `rest` 2^-64 turns, an eighth of a turn at most, by their Taylor series.
+__device__ __forceinline__ void sin_cos(long long rest, float &sine, float &cosine) {
+  // 2 pi / 2^64
+  constexpr float kHi = 0x1.921fb6p-62f, kLo = -0x1.777a5cp-87f;
+  const float r = __ll2float_rn(rest), r_lo = __ll2float_rn(rest - __float2ll_rn(r));
+  const Two x0 = two_prod(r, kHi);
+  const Two x = fast_two_sum(x0.hi, fmaf(r, kLo, fmaf(r_lo, kHi, x0.lo)));
+  const Two z0 = two_prod(x.hi, x.hi);
+  const float z = z0.hi, z_lo = fmaf(2.f * x.hi, x.lo, z0.lo);
+  const float odd = fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
+  sine = x.hi + fmaf(x.hi * z, odd, x.lo * fmaf(-0.5f, z, 1.f));
+  const float even = z * fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
+  const Two one = fast_two_sum(1.f, -0.5f * z);
+  cosine = one.hi + (one.lo + fmaf(z, even, -0.5f * z_lo));
+}
+
+// e4m3 codes of the lane's eight values over the scale, the first in the lowest byte.
+__device__ __forceinline__ uint2 fp8_codes(const uint4 &y, float scale) {
+  const float r = __frcp_rn(scale);
+  const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+  uint32_t two[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(bits_h2(in[i]));
+    two[i] = __nv_cvt_float2_to_fp8x2(make_float2(div_by_scale(f.x, scale, r), div_by_scale(f.y, scale, r)),
+                                      __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
+}
+
+// The V rows of an even slot and the one behind it, whose bytes lie side by side: words
+// (a row alone takes a store for each byte: 16,384 tokens, 2 heads, D 256, fp8/fp8 137 us).
+template <int D>
+__device__ __forceinline__ void store_v_fp8_pair(const QuantTarget &dst, int page, int t, int head, int l, uint4 even,
+                                                 uint4 odd) {
+  uint8_t *to = dst.v_pool + (static_cast<size_t>(page) * dst.n_kv_heads + head) * v_seg_bytes(MEMRA_KV_FP8_E4M3, D) +
+                (l / 4 * 32 + 8 * (l % 4) + (t % 8) / 2) * 16 + 4 * (t / 8);
+  const uint2 a = fp8_codes(even, dst.v_scale), b = fp8_codes(odd, dst.v_scale);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {            // element 4 u + 2 h + s lies 64 u + 8 h + 2 s further on
+    *reinterpret_cast<uint32_t *>(to + 64 * u) = __byte_perm(u ? a.y : a.x, u ? b.y : b.x, 0x5140);
+    *reinterpret_cast<uint32_t *>(to + 64 * u + 8) = __byte_perm(u ? a.y : a.x, u ? b.y : b.x, 0x7362);
+  }
+}
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRopeParams p) {
   constexpr int L = D / 8, ROWS = 32 / L;  // lanes of a row, rows of a warp
   __shared__ unsigned long long s_turns[D / 2];
-  __shared__ __align__(16) float s_cos[kTileMax][D / 2], s_sin[kTileMax][D / 2];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L, sub = lane / L;
-  const int t0 = blockIdx.x * p.tile, tokens = min(p.tile, p.tokens - t0);
-  const int first = blockIdx.y * p.passes, count = min(p.passes, p.k_passes + p.v_passes + p.q_passes - first);
+  __shared__ __align__(16) float s_angles[kWarps][2][D / 2];    // sines and cosines of each warp's token
+  const int tid = threadIdx.x, lane = tid & 31, l = lane % L, sub = lane / L;
+  float(&table)[2][D / 2] = s_angles[tid >> 5];
   grid_dependency_wait();
   allow_dependent_launch();
-
-  // Row group `at` of this CTA: its token, kind and head.
-  enum { kK, kV, kQ };
-  struct Rows {
-    int token, kind, head;
-    bool live;
-    uint4 x;
-    int slot;
-  };
-  auto fetch = [&](int at) {
-    Rows r{t0, kK, 0, false, make_uint4(0, 0, 0, 0), -1};
-    if (at >= tokens * count) return r;
-    int pass = first + at % count;
-    r.token = t0 + at / count;
-    const __half *src = p.k;
-    int64_t stride = p.k_stride;
-    int heads = p.n_kv_heads;
-    if (pass >= p.k_passes + p.v_passes) {
-      pass -= p.k_passes + p.v_passes;
-      r.kind = kQ, src = p.q, stride = p.q_stride, heads = p.n_heads;
-    } else if (pass >= p.k_passes) {
-      pass -= p.k_passes;
-      r.kind = kV, src = p.v, stride = p.v_stride;
-    }
-    r.head = pass * ROWS + sub;
-    r.live = r.head < heads;
-    if (r.live) r.x = *reinterpret_cast<const uint4 *>(src + r.token * stride + static_cast<int64_t>(r.head) * D + 8 * l);
-    if (r.kind != kQ && p.slots) r.slot = p.slots[r.token];
-    return r;
-  };
-  Rows next = fetch(warp);
-
   if (p.half) {
     for (int j = tid; j < p.half; j += 32 * kWarps) {
       const double turns = static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577;      // 1 / (2 pi)
       s_turns[j] = __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
     }
     __syncthreads();
-    for (int i = tid; i < tokens * p.half; i += 32 * kWarps) {
-      const int t = i / p.half, j = i % p.half;
-      const unsigned long long turn =
-          s_turns[j] * static_cast<unsigned long long>(static_cast<long long>(p.positions[t0 + t]));
-      // The nearest quarter turn and what is left of the angle, an eighth of a turn at most: as a float that is
-      // off by less than 2^-28 turns.
-      const unsigned quarter = static_cast<unsigned>((turn + (1ull << 61)) >> 62);
-      const long long rest = static_cast<long long>(turn << 2) >> 2;     // (modulo a quarter)
-      float s, c;
-      sincospif(__ll2float_rn(rest) * 1.084202172485504434e-19f, &s, &c);        // 2^-63: in units of pi
-      s_sin[t][j] = quarter & 1 ? (quarter & 2 ? -c : c) : (quarter & 2 ? -s : s);
-      s_cos[t][j] = quarter & 1 ? (quarter & 2 ? s : -s) : (quarter & 2 ? -c : c);
-    }
-    __syncthreads();
   }
-
-  float qw[8], kw[8];                      // the norm's weights of this lane's dims
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    qw[i] = p.q_weight ? p.q_weight[8 * l + i] : 1.f;
-    kw[i] = p.k_weight && p.k ? p.k_weight[8 * l + i] : 1.f;
-  }
-  // Dims of this lane in the rotation: pair j + i (half-split), or the lane's own four pairs.
+  // Dims of this lane in the rotation: pairs j0 + i (half-split), or the lane's own four pairs.
   const bool turned = 8 * l < 2 * p.half, second = 8 * l >= p.half;
-  const int j0 = p.interleaved ? 4 * l : second ? 8 * l - p.half : 8 * l;
+  const int j0 = !turned ? 0 : p.interleaved ? 4 * l : second ? 8 * l - p.half : 8 * l;
   const int partner = turned && !p.interleaved ? (second ? l - p.half / 8 : l + p.half / 8) : l;
-
-#pragma unroll 1
-  for (int at = warp; at < tokens * count; at += kWarps) {
-    const Rows r = next;
-    next = fetch(at + kWarps);
-    uint4 y = r.x;
-    if (r.kind != kV) {
-      float x[8];
-      const uint32_t in[4] = {r.x.x, r.x.y, r.x.z, r.x.w};
+  const float sign = second ? 1.f : -1.f;  // of the sine, for the lane's dims (half-split)
+  float sn[8], cs[8];                      // this lane's
+  // Whole warp: the angles of a position.
+  auto angles = [&](int position) {
+    __syncwarp();                          // (the ones before have been read)
+    for (int j = lane; j < p.half; j += 32) {
+      const unsigned long long turn = s_turns[j] * static_cast<unsigned long long>(static_cast<long long>(position));
+      // the nearest quarter turn, and what is left (modulo a quarter)
+      const unsigned quarter = static_cast<unsigned>((turn + (1ull << 61)) >> 62);
+      float s, c;
+      sin_cos(static_cast<long long>(turn << 2) >> 2, s, c);
+      table[0][j] = quarter & 1 ? (quarter & 2 ? -c : c) : (quarter & 2 ? -s : s);
+      table[1][j] = quarter & 1 ? (quarter & 2 ? s : -s) : (quarter & 2 ? -c : c);
+    }
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(bits_h2(in[i]));
-        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    for (int i = 0; i < 8; i += 4) {
+      if (i > 0 && p.interleaved) continue;
+      const float4 s = *reinterpret_cast<const float4 *>(&table[0][j0 + i]);
+      const float4 c = *reinterpret_cast<const float4 *>(&table[1][j0 + i]);
+      sn[i] = s.x, sn[i + 1] = s.y, sn[i + 2] = s.z, sn[i + 3] = s.w;
+      cs[i] = c.x, cs[i + 1] = c.y, cs[i + 2] = c.z, cs[i + 3] = c.w;
+    }
+    if (!p.interleaved)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sn[i] *= sign;
+  };
+  // N rows of a kind, normalized and turned.
+  auto finish = [&](auto rows, bool norm, const float(&w)[8], float(&x)[decltype(rows)::value][8]) {
+    constexpr int N = decltype(rows)::value;
+    if (norm) {
+      float sum[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        sum[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[e] = fmaf(x[e][i], x[e][i], sum[e]);
       }
-      if (r.kind == kQ ? p.q_weight != nullptr : p.k_weight != nullptr) {
-        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+      for (int d = 1; d < L; d <<= 1)
 #pragma unroll
-        for (int d = 1; d < L; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float scale = 1.f / sqrtf(fmaf(sum, 1.f / D, p.eps));
+        for (int e = 0; e < N; ++e) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= scale * (r.kind == kQ ? qw[i] : kw[i]);
+      for (int e = 0; e < N; ++e) {
+        // 1 / sqrt(mean + eps): an approximation and one Newton step
+        const float m = fmaf(sum[e], 1.f / D, p.eps), y = rsqrtf(m);
+        const Two y2 = two_prod(y, y), one = two_prod(y2.hi, m);
+        const float scale = fmaf(0.5f * y, __fsub_rn(1.f, one.hi) - fmaf(y2.lo, m, one.lo), y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[e][i] *= scale * w[i];
       }
-      if (p.half) {
-        const float *cs = s_cos[r.token - t0] + j0, *sn = s_sin[r.token - t0] + j0;
-        if (p.interleaved) {
-          if (turned) {
-            const float4 c = *reinterpret_cast<const float4 *>(cs), s = *reinterpret_cast<const float4 *>(sn);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    }
+    if (!p.half) return;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = x[2 * i], b = x[2 * i + 1];
-              x[2 * i] = fmaf(a, cc[i], -b * ss[i]);
-              x[2 * i + 1] = fmaf(b, cc[i], a * ss[i]);
-            }
-          }
-        } else {
-          float other[8];
+    for (int e = 0; e < N; ++e) {
+      if (p.interleaved) {
+        if (turned) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(0xffffffffu, x[i], partner, L);
-          if (turned) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-              const float4 c = *reinterpret_cast<const float4 *>(cs + i), s = *reinterpret_cast<const float4 *>(sn + i);
-              const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                x[i + e] = fmaf(x[i + e], cc[e], second ? other[i + e] * ss[e] : -other[i + e] * ss[e]);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float a = x[e][2 * i], b = x[e][2 * i + 1];
+            x[e][2 * i] = fmaf(a, cs[i], -b * sn[i]);
+            x[e][2 * i + 1] = fmaf(b, cs[i], a * sn[i]);
           }
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float b = __shfl_sync(0xffffffffu, x[e][i], partner, L);
+          if (turned) x[e][i] = fmaf(x[e][i], cs[i], b * sn[i]);
+        }
       }
-      y = make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
-      if (r.live && r.kind == kQ)
-        *reinterpret_cast<uint4 *>(p.q_out + r.token * p.q_out_stride + static_cast<int64_t>(r.head) * D + 8 * l) = y;
-      if (r.live && r.kind == kK && p.k_out)
-        *reinterpret_cast<uint4 *>(p.k_out + r.token * p.k_out_stride + static_cast<int64_t>(r.head) * D + 8 * l) = y;
     }
-    if (r.kind != kQ && p.slots) {
-      int slot = r.slot;
-      if (slot >= 0 && slot / kPage >= p.num_pages) {
-        if (r.kind == kK && lane == 0) flag_error(p.status, MEMRA_DEVERR_BAD_SLOT);
-        slot = -1;
+  };
+
+  auto weights = [&](const float *weight, float(&w)[8]) {       // the norm's, of this lane's dims
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = weight ? weight[8 * l + i] : 1.f;
+  };
+  float qw[8];
+  weights(p.q_weight, qw);
+
+  // Consecutive units go to different CTAs, so that the last ones spread over the GPU.
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+#pragma unroll 1
+  for (int64_t unit = static_cast<int64_t>(tid >> 5) * gridDim.x + blockIdx.x; unit < p.units; unit += warps) {
+    const int token = static_cast<int>(unit / p.parts), part = static_cast<int>(unit % p.parts);
+    // Row groups of the unit by kind: all of the token's, or one share.
+    int v0 = 0, v1 = p.v_passes, k0 = 0, k1 = p.k_passes, q0 = 0, q1 = p.q_passes;
+    if (p.parts > 1) {
+      const int kv = p.v_passes + p.k_passes;
+      v0 = min(part, p.v_passes), v1 = min(part + 1, p.v_passes);
+      k0 = min(max(part - p.v_passes, 0), p.k_passes), k1 = min(max(part + 1 - p.v_passes, 0), p.k_passes);
+      q0 = max(part - kv, 0) * p.q_share, q1 = min(max(part + 1 - kv, 0) * p.q_share, p.q_passes);
+    }
+    auto load = [&](const __half *base, int64_t stride, int pass, int end, int heads) {
+      const int head = pass * ROWS + sub;
+      return pass < end && head < heads ? *reinterpret_cast<const uint4 *>(base + token * stride + (head * D + 8 * l))
+                                        : make_uint4(0, 0, 0, 0);
+    };
+    // the first rows of each kind
+    uint4 yv = load(p.v, p.v_stride, v0, v1, p.n_kv_heads), yk = load(p.k, p.k_stride, k0, k1, p.n_kv_heads);
+    uint4 yq[2] = {load(p.q, p.q_stride, q0, q1, p.n_heads), load(p.q, p.q_stride, q0 + 1, q1, p.n_heads)};
+    int slot = p.slots && (v0 < v1 || k0 < k1) ? p.slots[token] : -1;
+    const bool fp8 = v0 < v1 && p.cache.v_fmt == MEMRA_KV_FP8_E4M3;
+    const int slot_after = fp8 && token + 1 < p.tokens ? p.slots[token + 1] : -1;
+    const int slot_before = fp8 && token > 0 ? p.slots[token - 1] : -1;
+    const bool turning = p.half && (k0 < k1 || q0 < q1);
+    const int position = turning ? p.positions[token] : 0;
+    if (slot >= 0 && slot / kPage >= p.num_pages) {
+      if (k0 < k1 && lane == 0) flag_error(p.status, MEMRA_DEVERR_BAD_SLOT);
+      slot = -1;
+    }
+    const int page = slot >= 0 ? slot / kPage : 0, place = slot >= 0 ? slot % kPage : 0;
+    if (turning) angles(position);
+    // fp8 values of an even slot and of the next token's are stored together, by the first of the two.
+    const bool pair = fp8 && slot >= 0 && slot % 2 == 0 && slot_after == slot + 1;
+    if (fp8 && slot >= 0 && slot % 2 == 1 && slot_before == slot - 1) v0 = v1;
+#pragma unroll 1
+    for (int pass = v0; pass < v1; ++pass) {
+      const uint4 y = yv;
+      yv = load(p.v, p.v_stride, pass + 1, v1, p.n_kv_heads);
+      const int head = pass * ROWS + sub;
+      if (pair) {
+        const uint4 odd = load(p.v + p.v_stride, p.v_stride, pass, v1, p.n_kv_heads);
+        if (head < p.n_kv_heads) store_v_fp8_pair<D>(p.cache, page, place, head, l, y, odd);
+        continue;
       }
-      const bool act = r.live && slot >= 0;
-      quantize_store_row<D>(p.cache, act, act ? slot / kPage : 0, act ? slot % kPage : 0, act ? r.head : 0, l, y, y,
-                            r.kind == kK, r.kind == kV);
+      quantize_store_row<D>(p.cache, slot >= 0 && head < p.n_kv_heads, page, place, head, l, y, y, false, true);
+    }
+#pragma unroll 1
+    for (int pass = k0; pass < k1; ++pass) {
+      float x[1][8];
+      unpack(yk, x[0]);
+      yk = load(p.k, p.k_stride, pass + 1, k1, p.n_kv_heads);
+      float kw[8];
+      weights(p.k_weight, kw);
+      finish(std::integral_constant<int, 1>{}, p.k_weight != nullptr, kw, x);
+      const uint4 y = pack(x[0]);
+      const int head = pass * ROWS + sub;
+      if (p.k_out && head < p.n_kv_heads)
+        *reinterpret_cast<uint4 *>(p.k_out + token * p.k_out_stride + (head * D + 8 * l)) = y;
+      if (p.slots)
+        quantize_store_row<D>(p.cache, slot >= 0 && head < p.n_kv_heads, page, place, head, l, y, y, true, false);
+    }
+    // two query row groups at a time
+    __half *dst = p.q_out + token * p.q_out_stride + 8 * l;
+#pragma unroll 1
+    for (int pass = q0; pass < q1; pass += 2) {
+      float x[2][8];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        unpack(yq[e], x[e]);
+        yq[e] = load(p.q, p.q_stride, pass + 2 + e, q1, p.n_heads);
+      }
+      finish(std::integral_constant<int, 2>{}, p.q_weight != nullptr, qw, x);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int head = (pass + e) * ROWS + sub;
+        if (pass + e < q1 && head < p.n_heads) *reinterpret_cast<uint4 *>(dst + head * D) = pack(x[e]);
+      }
     }
   }
 }
@@ -179,18 +292,18 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopePa
 template <int D>
 cudaError_t launch(NormRopeParams p, int sms, cudaStream_t st) {
   constexpr int kRows = 32 / (D / 8);
-  auto groups = [](int heads) { return (heads + kRows - 1) / kRows; };
-  p.k_passes = p.k ? groups(p.n_kv_heads) : 0;
-  p.v_passes = p.slots ? groups(p.n_kv_heads) : 0;
-  p.q_passes = groups(p.n_heads);
-  const int all = p.k_passes + p.v_passes + p.q_passes;
-  // As many tokens to a CTA as still leave four CTAs to each SM; with few tokens, the row groups of one are
-  // spread over CTAs too, one to each warp.
-  p.tile = static_cast<int>(std::min<int64_t>(std::max<int64_t>(p.tokens / (4ll * sms), 1), kTileMax));
-  p.passes = p.tokens >= 4 * sms ? all : kWarps;
-  const dim3 grid((p.tokens + p.tile - 1) / p.tile, (all + p.passes - 1) / p.passes);
-  if (grid.y > 65535) return cudaErrorInvalidValue;
-  return launch_pdl(norm_rope_kernel<D>, grid, dim3(32 * kWarps), 0, st, p);
+  auto groups = [](int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); };
+  p.k_passes = p.k ? groups(p.n_kv_heads, kRows) : 0;
+  p.v_passes = p.slots ? groups(p.n_kv_heads, kRows) : 0;
+  p.q_passes = groups(p.n_heads, kRows);
+  // Whole tokens as units where they give every warp of the GPU two; else row groups, the queries' so many at a time.
+  const int64_t warps = 3ll * sms * kWarps, tokens = p.tokens;
+  p.q_share = static_cast<int>(std::min<int64_t>(std::max<int64_t>(tokens * p.q_passes / (2 * warps), 1), p.q_passes));
+  p.parts = tokens >= 2 * warps ? 1 : p.k_passes + p.v_passes + groups(p.q_passes, p.q_share);
+  p.units = tokens * p.parts;
+  // (an odd number of CTAs: even and odd tokens to every SM)
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((p.units + kWarps - 1) / kWarps, (3ll * sms - 1) | 1));
+  return launch_pdl(norm_rope_kernel<D>, dim3(grid), dim3(32 * kWarps), 0, st, p);
 }
 
 }  // namespace

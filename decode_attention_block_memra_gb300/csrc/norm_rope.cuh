@@ -24,8 +24,9 @@ struct NormRopeParams {
   int tokens, n_heads, n_kv_heads, num_pages;
   int half;                       // rotated pairs: rotary_dim / 2
   int interleaved;
-  int tile;                       // tokens of a CTA, set by the launcher
-  int k_passes, v_passes, q_passes, passes;       // row groups of a token by kind, and of a CTA's share, set by the launcher
+  // set by the launcher: row groups of a token by kind; units of a token, and row groups of one of its queries'; units in all
+  int k_passes, v_passes, q_passes, parts, q_share;
+  int64_t units;
 };
 
 cudaError_t launch_norm_rope(int D, NormRopeParams p, int sms, cudaStream_t st);
