@@ -450,14 +450,19 @@ def kv_compact(cache: KVCache, page_table, seq_lens, max_seq_len: int, accepted,
     _check(rc, "memra_kv_compact")
 
 
-def _row_stride(where: str, x, heads: int, dim: int, device: int) -> int:
-    """The token stride of rows x fp16 [tokens, heads, dim] on `device` whose heads lie side by side; refuses others."""
-    import torch
-    s = x.stride()
-    if (x.dim() != 3 or x.shape[1:] != (heads, dim) or x.dtype is not torch.float16 or x.get_device() != device or
-            s[2] != 1 or (heads > 1 and s[1] != dim)):
+def _dense(where: str, t, dtype, shape, device: int) -> int:
+    """The address of a dense tensor of the type, shape and device wanted; refuses others."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise MemraError(1, where)
-    return s[0] if x.shape[0] > 1 else heads * dim
+    return t.data_ptr()
+
+
+def _rows(where: str, x, dtype, shape, device: int):
+    """The address and token stride of rows x [tokens, heads, dim] whose heads lie side by side; refuses others."""
+    a, b, c = x.stride() if x.dim() == 3 else (0, 0, 0)
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or c != 1 or (b != shape[2] and shape[1] > 1):
+        raise MemraError(1, where)
+    return x.data_ptr(), a if shape[0] > 1 else shape[1] * shape[2]
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -472,26 +477,27 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out=None, q_weight=None, k_
     int32 [tokens] together store the finished rows; k is None if it goes nowhere.
     """
     import torch
-    where = "memra_qk_norm_rope"
-    T, Hq, D = q.shape
+    where, f16, f32, i32 = "memra_qk_norm_rope", torch.float16, torch.float32, torch.int32
+    T, Hq, D = shape = q.shape
     Hkv = k.shape[1] if k is not None else 1
-    device = _device()
-    a = []
-    for x, heads in ((q, Hq), (k, Hkv), (v, Hkv), (q_out, Hq), (k_out, Hkv)):
-        if x is not None and x.shape[0] != T:
-            raise MemraError(1, where)
-        a.append((_ptr(x), _row_stride(where, x, heads, D, device) if x is not None else 0))
-    f32, i32 = torch.float32, torch.int32
-    half = 0 if inv_freq is None else inv_freq.shape[0]
-    _need_dense(where, *((t, dtype, shape) for t, dtype, shape in (
-        (q_weight, f32, (D,)), (k_weight, f32, (D,)), (positions, i32, (T,)), (inv_freq, f32, (half,)),
-        (slot_mapping, i32, (T,))) if t is not None))
+    kv_shape, device = (T, Hkv, D), _device()
+    pq, sq = _rows(where, q, f16, shape, device)
+    po, so = _rows(where, q_out, f16, shape, device)
+    pk, sk = _rows(where, k, f16, kv_shape, device) if k is not None else (0, 0)
+    pv, sv = _rows(where, v, f16, kv_shape, device) if v is not None else (0, 0)
+    pko, sko = _rows(where, k_out, f16, kv_shape, device) if k_out is not None else (0, 0)
+    half = inv_freq.numel() if inv_freq is not None else 0
     if cache is not None and cache.device_index != device:
         raise MemraError(1, where)
-    rc = lib().memra_qk_norm_rope(*a[0], *a[1], *a[2], _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions),
-                                  _ptr(inv_freq), 2 * half, int(bool(interleaved)), T, Hq, Hkv, D, *a[3], *a[4],
-                                  cache.ref if cache is not None else None, _ptr(slot_mapping), _stream(stream))
-    _check(rc, where)
+    rc = lib().memra_qk_norm_rope(
+        pq, sq, pk, sk, pv, sv, _dense(where, q_weight, f32, (D,), device) if q_weight is not None else 0,
+        _dense(where, k_weight, f32, (D,), device) if k_weight is not None else 0, eps,
+        _dense(where, positions, i32, (T,), device) if positions is not None else 0,
+        _dense(where, inv_freq, f32, (half,), device) if half else 0, 2 * half, 1 if interleaved else 0, T, Hq, Hkv, D,
+        po, so, pko, sko, cache.ref if cache is not None else None,
+        _dense(where, slot_mapping, i32, (T,), device) if slot_mapping is not None else 0, _stream(stream))
+    if rc:
+        raise MemraError(rc, where)
 
 
 def chunk_attn_workspace_bytes(head_dim: int) -> int:
@@ -513,21 +519,18 @@ def chunk_attn(cache: KVCache, q, cu_seqlens, page_table, seq_lens, max_seq_len:
 
 def _chunk_args(cache, q, cu_seqlens, page_table, seq_lens, max_seq_len, out, workspace, sm_scale, window, lse):
     import torch
-    where = "memra_chunk_attn"
-    T, Hq, D = q.shape
-    B, pages = page_table.shape
-    i32 = torch.int32
-    wanted = [(out, torch.float16, (T, Hq, D)), (cu_seqlens, i32, (B + 1,)), (page_table, i32, (B, pages)),
-              (seq_lens, i32, (B,))]
-    if lse is not None:
-        wanted.append((lse, torch.float32, (T, Hq)))
-    device = _need_dense(where, *wanted)
+    where, f16, i32 = "memra_chunk_attn", torch.float16, torch.int32
+    T, Hq, D = shape = q.shape
+    B, pages = table = page_table.shape
+    device = _device()
     if cache.device_index != device or workspace is None or workspace.get_device() != device:
         raise MemraError(1, where)
-    return (cache.ref, _ptr(q), _row_stride(where, q, Hq, D, device), _ptr(cu_seqlens), _ptr(page_table), pages,
-            _ptr(seq_lens), int(max_seq_len), B, T, Hq, cache.n_kv_heads, D,
-            float(sm_scale if sm_scale is not None else D ** -0.5), int(window), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse))
+    pq, sq = _rows(where, q, f16, shape, device)
+    return (cache.ref, pq, sq, _dense(where, cu_seqlens, i32, (B + 1,), device),
+            _dense(where, page_table, i32, table, device), pages, _dense(where, seq_lens, i32, (B,), device),
+            int(max_seq_len), B, T, Hq, cache.n_kv_heads, D, D ** -0.5 if sm_scale is None else sm_scale, int(window),
+            workspace.data_ptr(), workspace.nbytes, _dense(where, out, f16, shape, device),
+            _dense(where, lse, torch.float32, (T, Hq), device) if lse is not None else 0)
 
 
 def key_weights(cache: KVCache, q, lse, cu_seqlens, page_table, seq_lens, max_seq_len: int, weights, keep: float = 1.0,
@@ -538,19 +541,20 @@ def key_weights(cache: KVCache, q, lse, cu_seqlens, page_table, seq_lens, max_se
     Hq] as it writes them; weights float32 [B, Hkv, >= max_seq_len], times keep first.
     """
     import torch
-    where = "memra_key_weights"
-    T, Hq, D = q.shape
-    B, pages = page_table.shape
-    i32, f32 = torch.int32, torch.float32
-    device = _need_dense(where, (lse, f32, (T, Hq)), (cu_seqlens, i32, (B + 1,)), (page_table, i32, (B, pages)),
-                         (seq_lens, i32, (B,)), (weights, f32, (B, cache.n_kv_heads, weights.shape[-1])))
+    where, f32, i32 = "memra_key_weights", torch.float32, torch.int32
+    T, Hq, D = shape = q.shape
+    B, pages = table = page_table.shape
+    device, Hkv, row = _device(), cache.n_kv_heads, weights.shape[-1]
     if cache.device_index != device:
         raise MemraError(1, where)
-    rc = lib().memra_key_weights(cache.ref, _ptr(q), _row_stride(where, q, Hq, D, device), _ptr(lse), _ptr(cu_seqlens),
-                                 _ptr(page_table), pages, _ptr(seq_lens), int(max_seq_len), B, T, Hq, cache.n_kv_heads,
-                                 D, float(sm_scale if sm_scale is not None else D ** -0.5), float(keep), _ptr(weights),
-                                 weights.shape[-1], _stream(stream))
-    _check(rc, where)
+    pq, sq = _rows(where, q, torch.float16, shape, device)
+    rc = lib().memra_key_weights(
+        cache.ref, pq, sq, _dense(where, lse, f32, (T, Hq), device), _dense(where, cu_seqlens, i32, (B + 1,), device),
+        _dense(where, page_table, i32, table, device), pages, _dense(where, seq_lens, i32, (B,), device),
+        int(max_seq_len), B, T, Hq, Hkv, D, D ** -0.5 if sm_scale is None else sm_scale, keep,
+        _dense(where, weights, f32, (B, Hkv, row), device), row, _stream(stream))
+    if rc:
+        raise MemraError(rc, where)
 
 
 def kv_evict(cache: KVCache, page_table, seq_lens, max_seq_len: int, weights, budgets, dst_table, kept, sink: int = 0,
@@ -563,25 +567,22 @@ def kv_evict(cache: KVCache, page_table, seq_lens, max_seq_len: int, weights, bu
     float32 [B, Hkv, >= max_budget] their weights, new_lens int32 [B] how many.
     """
     import torch
-    where = "memra_kv_evict"
-    i32, f32 = torch.int32, torch.float32
-    B, Hkv, most = kept.shape
-    pages, to = page_table.shape[-1], dst_table.shape[-1]
-    wanted = [(kept, i32, (B, Hkv, most)), (page_table, i32, (B, pages)), (seq_lens, i32, (B,)),
-              (weights, f32, (B, Hkv, weights.shape[-1])), (budgets, i32, (B,)), (dst_table, i32, (B, to))]
-    if new_weights is not None:
-        wanted.append((new_weights, f32, (B, Hkv, new_weights.shape[-1])))
-    if new_lens is not None:
-        wanted.append((new_lens, i32, (B,)))
-    device = _need_dense(where, *wanted)
+    where, f32, i32 = "memra_kv_evict", torch.float32, torch.int32
+    B, Hkv, most = shape = kept.shape
+    device, pages, to, row = _device(), page_table.shape[-1], dst_table.shape[-1], weights.shape[-1]
     if cache.device_index != device or Hkv != cache.n_kv_heads:
         raise MemraError(1, where)
-    rc = lib().memra_kv_evict(cache.ref, page_table.data_ptr(), pages, seq_lens.data_ptr(), int(max_seq_len),
-                              weights.data_ptr(), weights.shape[-1], budgets.data_ptr(), most, int(sink), int(recent),
-                              dst_table.data_ptr(), to, B, kept.data_ptr(), _ptr(new_weights),
-                              new_weights.shape[-1] if new_weights is not None else 0, _ptr(new_lens),
-                              _stream(stream))
-    _check(rc, where)
+    new_row = new_weights.shape[-1] if new_weights is not None else 0
+    rc = lib().memra_kv_evict(
+        cache.ref, _dense(where, page_table, i32, (B, pages), device), pages,
+        _dense(where, seq_lens, i32, (B,), device), int(max_seq_len),
+        _dense(where, weights, f32, (B, Hkv, row), device), row, _dense(where, budgets, i32, (B,), device), most,
+        int(sink), int(recent), _dense(where, dst_table, i32, (B, to), device), to, B,
+        _dense(where, kept, i32, shape, device),
+        _dense(where, new_weights, f32, (B, Hkv, new_row), device) if new_weights is not None else 0, new_row,
+        _dense(where, new_lens, i32, (B,), device) if new_lens is not None else 0, _stream(stream))
+    if rc:
+        raise MemraError(rc, where)
 
 
 def testing_decode_attn_short_page(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, out, workspace,

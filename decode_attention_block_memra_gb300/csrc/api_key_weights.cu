@@ -54,10 +54,11 @@ extern "C" int memra_key_weights(const memra_kv_cache *cache, const void *q, int
   // (positions up to a tile past the end stay below 2^31)
   p.len_limit = static_cast<int32_t>(std::min<int64_t>(std::min<int64_t>(max_seq_len, INT32_MAX - 4 * kWeightKeys),
                                                        static_cast<int64_t>(max_pages_per_seq) * kPage));
-  const int rows = weight_rows(head_dim);
+  const int64_t all_rows = static_cast<int64_t>(total_tokens) * p.group;
+  const int rows = all_rows <= static_cast<int64_t>(batch) * kWeightRowsFew ? kWeightRowsFew : weight_rows(head_dim);
   p.hpt = std::min(p.group, rows);
   p.subs = static_cast<int>(ceil_div(p.group, p.hpt));
   p.tpt = std::max(1, rows / p.group);
   p.ctas = device_sms();
-  return cuda_status(launch_key_weights(head_dim, cache->k_fmt, p, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_key_weights(head_dim, rows, cache->k_fmt, p, static_cast<cudaStream_t>(stream)));
 }

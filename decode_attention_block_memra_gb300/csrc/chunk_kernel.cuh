@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
     __syncwarp();
   } else if (warp >= C::kStageWarp0) {
     // ---------------------------------------------------------------- staging --
+    if constexpr (D == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int sg = (warp - C::kStageWarp0) / SW, sw = (warp - C::kStageWarp0) % SW, st = 32 * sw + lane;
     if constexpr (C::kMCols) {               // the unused columns of the centres' block, once
       for (int vb = sg; vb < C::kVBufs; vb += C::kStageGroups)
@@ -463,6 +464,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
     }
   } else {
     // ---------------------------------------------------------------- softmax --
+    if constexpr (D == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     const int g = warp >> 2, rl = tid & 127;           // group, row of its tile
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t o_col = tmem + tlane + C::kOCol + g * C::kOCols;

@@ -9,13 +9,16 @@
 // weights over all rows in a register: no sum crosses threads, and none is
 // atomic.  K^ is dequantized once (q8_0 as exact fp16 pairs: the weights are float32) and meets
 // every row tile while it lies in shared memory.
-//   * a copy warp brings raw pages, 32 keys at a time, into a ring of each staging group;
-//   * two groups of staging warps dequantize them into tiles of 128 keys;
+//   * a copy warp brings raw pages into a ring;
+//   * eight staging warps dequantize them into tiles of 128 keys, one tile after the
+//     other: while one is made, the tensor cores are at the other;
 //   * a load warp brings row tiles of Q by TMA; where all rows of the chunk
 //     fit their ring, once for all keys of a CTA's run;
 //   * one MMA thread: S^T = K^ Q^T, two key tiles beside one another for each row tile;
-//   * two groups of four warps, one for each key tile: thread = key (at head_dim
-//     256 with q8_0 there is room for one tile of K^, and one group).
+//   * four groups of four warps, two for each key tile, which take its row tiles by
+//     turns: thread = key (at head_dim 256 with q8_0 there is room for one tile of
+//     K^, and two groups).  A row tile takes a group about 3,000 clocks, the tensor cores
+//     1,024 (one group to a tile: 64 tokens over 262,144 keys 252 us).
 // The (key tile, KV head, sequence) items of the call lie behind one another on a line
 // that the CTAs, one to an SM, share by their cost.
 #include <algorithm>
@@ -30,9 +33,8 @@
 namespace memra {
 namespace {
 
-constexpr int kStepKeys = 32;              // keys of a raw chunk
-constexpr int kTileSteps = kWeightKeys / kStepKeys;
 constexpr int kPieces = 4;
+constexpr int kLseRows = 1024;             // rows of a chunk whose log-sum-exps stay in shared memory for a whole run of tiles
 
 // A run of key tiles of one KV head of a sequence.
 struct WeightPiece {
@@ -144,12 +146,14 @@ struct WeightWalk {
   }
 };
 
-template <int D, int KF>
+template <int D, int KF, int N>
 struct WeightCfg {
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
-  static constexpr int kRows = weight_rows(D);
-  static constexpr int kTiles = D == 256 && kKLo ? 1 : 2;       // tiles of K^, and groups of the epilogue
-  static constexpr int kStageWarp0 = 4 * kTiles, kMmaWarp = kStageWarp0 + 8, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kRows = N;          // query rows of a tile
+  // Keys of a raw chunk: at 32, a staging warp has two loads in flight and the waits around them; 64 where they fit.
+  static constexpr int kStepKeys = D == 128 ? 64 : 32, kTileSteps = kWeightKeys / kStepKeys;
+  static constexpr int kTiles = D == 256 && kKLo ? 1 : 2;       // tiles of K^, with two groups of the epilogue each
+  static constexpr int kStageWarp0 = 8 * kTiles, kMmaWarp = kStageWarp0 + 8, kLoadWarp = kMmaWarp + 1;
   static constexpr int kCopyWarp = kLoadWarp + 1, kThreads = 32 * (kCopyWarp + 1);
   static constexpr int kPages = kStepKeys / kPage;
   static constexpr int kKSeg = k_seg_bytes(KF, D);
@@ -157,24 +161,24 @@ struct WeightCfg {
   static constexpr uint32_t kTile = kWeightKeys * D * 2, kKBuf = kTile * (kKLo ? 2 : 1);
   static constexpr uint32_t kQBuf = kRows * D * 2, kRawBytes = kPages * kKSeg;
   static constexpr uint32_t kRoom = 227 * 1024;
-  // barriers, page masks, the share, the pieces; each group's log-sum-exps of two row tiles; tiles of K^; Q; raw chunks
+  // barriers, page masks, the share, the pieces; log-sum-exps (of the run's rows, or two row tiles of each group); half of
+  // the sums of two tiles for each tile of K^; tiles of K^; Q; raw chunks
   static constexpr uint32_t kOffBar = 0, kOffMask = 384, kOffShare = 448, kOffPiece = 480, kOffLse = 1024;
-  static constexpr uint32_t kOffK = kOffLse + 2048;
+  static constexpr uint32_t kOffSum = kOffLse + 4096, kOffK = kOffSum + 2048;
   static constexpr uint32_t kOffQ = kOffK + kTiles * kKBuf;
   // (two raw chunks at least beside the row tiles)
   static constexpr int kQBufs = (kRoom - 1024 - kOffQ - 2 * kRawBytes) / kQBuf < 4 ? (kRoom - 1024 - kOffQ - 2 * kRawBytes) / kQBuf : 4;
   static constexpr uint32_t kOffRaw = kOffQ + kQBufs * kQBuf;
-  // raw chunks of each staging group
-  static constexpr int kRaw = (kRoom - 1024 - kOffRaw) / (2 * kRawBytes) < 4 ? (kRoom - 1024 - kOffRaw) / (2 * kRawBytes) : 4;
-  static constexpr uint32_t kTCols = 512, kNeed = kOffRaw + 2 * kRaw * kRawBytes + 1024, kFloor = 150 * 1024;      // (1024: aligning the base)
+  static constexpr int kRaw = (kRoom - 1024 - kOffRaw) / kRawBytes < 8 ? (kRoom - 1024 - kOffRaw) / kRawBytes : 8;
+  static constexpr uint32_t kTCols = 512, kNeed = kOffRaw + kRaw * kRawBytes + 1024, kFloor = 150 * 1024;      // (1024: aligning the base)
   static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
-  enum Bar { kRawFull = 0, kRawEmpty = kRawFull + 2 * kRaw, kKFull = kRawEmpty + 2 * kRaw, kKFree = kKFull + 2, kQFull = kKFree + 2,
+  enum Bar { kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kKFree = kKFull + 2, kQFull = kKFree + 2,
              kQFree = kQFull + kQBufs, kSFull = kQFree + kQBufs, kSFree = kSFull + 4, kDrained = kSFree + 4, kPieceFull,
              kPieceFree = kPieceFull + kPieces, kBars = kPieceFree + kPieces };
   static_assert(kQBufs >= 1 && kRaw >= 1, "rings");
   static_assert(kOffBar + 8 * kBars + 4 <= kOffMask, "barriers and the tensor-memory address");
   static_assert(kOffPiece + kPieces * sizeof(WeightPiece) <= kOffLse, "pieces");
-  static_assert(kTiles * 2 * kRows * 4 <= 2048, "log-sum-exps");
+  static_assert(kTiles * 4 * kRows <= kLseRows && kLseRows * 4 <= 4096 && kTiles * 2 * kWeightKeys * 4 <= 2048, "log-sum-exps, sums");
   static_assert(kTiles * 2 * kRows <= 512, "tensor memory");
   static_assert(kOffK % 1024 == 0 && kQBuf % 1024 == 0 && kOffRaw % 16 == 0 && kSmem <= 232448, "alignment, shared memory");
 };
@@ -185,11 +189,12 @@ __device__ __forceinline__ int weight_first_row_tile(const WeightParams &p, int 
   return t > 0 ? t / p.tpt * p.subs : 0;
 }
 
-template <int D, int KF>
-__global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
+template <int D, int KF, int N>
+__global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap qmap, const WeightParams p) {
-  using C = WeightCfg<D, KF>;
-  constexpr int N = C::kRows, G = C::kTiles, NP = C::kPages, RAW = C::kRaw, QB = C::kQBufs;
+  using C = WeightCfg<D, KF, N>;
+  constexpr int G = C::kTiles, NP = C::kPages, RAW = C::kRaw, QB = C::kQBufs;
+  constexpr int kStepKeys = C::kStepKeys, kTileSteps = C::kTileSteps;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_addr(smem);
@@ -217,12 +222,12 @@ __global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
         if (weight_seq(p, b).bad) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
   } else if (warp == C::kCopyWarp) {
     if (lane == 0) {
-      for (int i = 0; i < 2 * RAW; ++i) {
+      for (int i = 0; i < RAW; ++i) {
         mbar_init(bar(C::kRawFull, i), 1);
-        mbar_init(bar(C::kRawEmpty, i), 4);
+        mbar_init(bar(C::kRawEmpty, i), 8);
       }
       for (int i = 0; i < 2; ++i) {
-        mbar_init(bar(C::kKFull, i), G == 2 ? 4 : 8);
+        mbar_init(bar(C::kKFull, i), 8);
         mbar_init(bar(C::kKFree, i), 1);
       }
       for (int i = 0; i < QB; ++i) {
@@ -261,20 +266,18 @@ __global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
     ++piece;
   };
   // Row tile rt: its first token in the chunk, the first of its heads, and its rows.
-  auto tokens_of = [&](int rt) { return rt / p.subs * p.tpt; };
-  auto heads_of = [&](int rt) { return rt % p.subs * p.hpt; };
+  // (a token's heads are one tile's but for groups wider than a tile: no division then)
+  auto tokens_of = [&](int rt) { return (p.subs == 1 ? rt : rt / p.subs) * p.tpt; };
+  auto heads_of = [&](int rt) { return p.subs == 1 ? 0 : rt % p.subs * p.hpt; };
   auto rows_of = [&](int rt, int n) {
     return min(p.tpt, n - tokens_of(rt)) * p.hpt - max(0, heads_of(rt) + p.hpt - p.group);
   };
-
-  // The staging group that takes step i of a piece: tiles by turns, or the steps of the one tile.
-  auto owner_of = [](int i) { return G == 2 ? i / kTileSteps & 1 : i & 1; };
 
   if (warp == C::kCopyWarp) {
     // ----------------------------------------------------------------- copies --
     WeightWalk walk{p, share[0], share[1]};
     WeightPiece x;
-    int cc = 0, used[2] = {0, 0};            // raw chunks so far, and by staging group
+    int cc = 0;                              // raw chunks so far
     while (ok) {
       const bool more = walk.next(x);
       if (!more) x.tiles = -1;
@@ -309,11 +312,10 @@ __global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
         }
         int pid = __shfl_sync(0xffffffffu, ids, (i % kAhead) * NP + (lane & (NP - 1)));
         if (lane >= NP) pid = -1;
-        const int o = owner_of(i), s = o * RAW + used[o] % RAW;
-        if (used[o] >= RAW) ok = mbar_wait_suspended(bar(C::kRawEmpty, s), (used[o] / RAW - 1) & 1, p.status);
+        const int s = cc % RAW;
+        if (cc >= RAW) ok = mbar_wait_suspended(bar(C::kRawEmpty, s), (cc / RAW - 1) & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        ++used[o];
         const uint32_t there = __ballot_sync(0xffffffffu, pid >= 0);
         if (lane == 0) {
           page_mask[cc & 63] = static_cast<uint8_t>(there);
@@ -330,9 +332,7 @@ __global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
       }
     }
     // every copy has landed before the CTA can leave
-    for (int o = 0; o < 2; ++o)
-      for (int c = max(0, used[o] - RAW); c < used[o]; ++c)
-        mbar_wait_suspended(bar(C::kRawFull, o * RAW + c % RAW), (c / RAW) & 1, p.status);
+    for (int c = max(0, cc - RAW); c < cc; ++c) mbar_wait_suspended(bar(C::kRawFull, c % RAW), (c / RAW) & 1, p.status);
     __syncwarp();
   } else if (warp == C::kLoadWarp) {
     // ---------------------------------------------------------------- Q tiles --
@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
     __syncwarp();
   } else if (warp >= C::kStageWarp0) {
     // ---------------------------------------------------------------- staging --
-    const int sg = (warp - C::kStageWarp0) / 4, sw = (warp - C::kStageWarp0) % 4;
-    int used = 0, kn = 0;                    // raw chunks and tiles of K^ so far
+    const int sw = warp - C::kStageWarp0;
+    int cc = 0, kn[2] = {0, 0};              // raw chunks, and uses of each tile of K^ so far
     while (true) {
       const volatile WeightPiece *x = next_piece();
       ok = __all_sync(0xffffffffu, ok);
@@ -435,17 +435,17 @@ __global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
       if (tiles < 0) break;
       __syncwarp();
       if (lane == 0) free_piece(); else ++piece;
-      for (int t = G == 2 ? sg : 0; t < tiles && ok; t += G) {
-        const int g = G == 2 ? sg : 0;
-        if (kn > 0) ok = mbar_wait_suspended(bar(C::kKFree, g), (kn - 1) & 1, p.status);
-        ++kn;
+      for (int t = 0; t < tiles && ok; ++t) {
+        const int g = t % G;
+        if (kn[g] > 0) ok = mbar_wait_suspended(bar(C::kKFree, g), (kn[g] - 1) & 1, p.status);
+        ++kn[g];
 #pragma unroll 1
-        for (int i = G == 2 ? 0 : sg; i < kTileSteps; i += G == 2 ? 1 : 2, ++used) {
-          const int s = sg * RAW + used % RAW;
-          if (ok) ok = mbar_wait_suspended(bar(C::kRawFull, s), (used / RAW) & 1, p.status);
+        for (int i = 0; i < kTileSteps; ++i, ++cc) {
+          const int s = cc % RAW;
+          if (ok) ok = mbar_wait_suspended(bar(C::kRawFull, s), (cc / RAW) & 1, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          stage_k<D, KF, kStepKeys, 4, kWeightKeys>(sb + C::kOffRaw + s * C::kRawBytes,
+          stage_k<D, KF, kStepKeys, 8, kWeightKeys>(sb + C::kOffRaw + s * C::kRawBytes,
                                                     sb + C::kOffK + g * C::kKBuf + i * kStepKeys * 128, sw, lane);
           fence_proxy_async();               // K^ for the tensor cores, the raw chunk for the next copies
           __syncwarp();
@@ -456,78 +456,112 @@ __global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- epilogue --
-    const int g = warp >> 2, kl = tid & 127;           // group, key of its tile
+    // Group, its tile of K^ and which of the tile's units it takes, key of the tile.
+    const int group = warp >> 2, g = group >> 1, turn = group & 1, kl = tid & 127;
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    float *const lse_s = reinterpret_cast<float *>(smem + C::kOffLse) + g * 2 * N;
-    int sn = 0, cc = 0;
+    float *const lse_all = reinterpret_cast<float *>(smem + C::kOffLse), *const lse_two = lse_all + group * 2 * N;
+    float *const half_s = reinterpret_cast<float *>(smem + C::kOffSum) + g * 2 * kWeightKeys + kl;
+    const uint64_t scale2 = pack_f2(p.scale_log2, p.scale_log2);
+    int sn = 0, cc = 0, tn = 0;              // units of this tile of K^ so far, raw chunks, tiles
     while (true) {
       const volatile WeightPiece *x = next_piece();
-      ok = named_barrier_and(1 + g, 128, ok);          // a group's warps go on together, or none
+      ok = named_barrier_and(7, 256 * G, ok);          // all groups go on together, or none
       if (!ok || x->tiles < 0) break;
       const int tiles = x->tiles, rts = x->row_tiles, n = x->n, T = x->T, tile0 = x->tile0;
-      const int h = x->h, first = x->first;
-      float *const row = p.weights + (static_cast<int64_t>(x->b) * p.n_kv_heads + h) * p.weight_stride;
-      // log-sum-exp (base 2) of this thread's column of a row tile; none: +inf
-      auto lse_of = [&](int rt) {
-        if (rt >= rts || kl >= rows_of(rt, n)) return INFINITY;
-        const int t = first + tokens_of(rt) + kl / p.hpt;
-        return p.lse[static_cast<int64_t>(t) * p.n_heads + h * p.group + heads_of(rt) + kl % p.hpt] * 1.4426950408889634f;
+      float *const row = p.weights + (static_cast<int64_t>(x->b) * p.n_kv_heads + x->h) * p.weight_stride;
+      const float *const lse_rows = p.lse + static_cast<int64_t>(x->first) * p.n_heads + x->h * p.group;
+      // log-sum-exp of a column of a row tile, base 2, negated; none: -inf
+      auto lse_of = [&](int rt, int col) {
+        if (rt >= rts || col >= rows_of(rt, n)) return -INFINITY;
+        return lse_rows[static_cast<int64_t>(tokens_of(rt) + col / p.hpt) * p.n_heads + heads_of(rt) + col % p.hpt] *
+               -1.4426950408889634f;
       };
-      for (int t = g; t < tiles && ok; t += G) {
+      // Where they fit, the run's are there once for all tiles.
+      const int run_low = weight_first_row_tile(p, n, T, tile0 * kWeightKeys);
+      const bool cached = (rts - run_low) * N <= kLseRows;
+      if (cached) {
+        for (int i = tid; i < (rts - run_low) * N; i += 256 * G) lse_all[i] = lse_of(run_low + i / N, i % N);
+        named_barrier_sync(7, 256 * G);
+      }
+      for (int t = g; t < tiles; t += G, ++tn) {
         const int key = (tile0 + t) * kWeightKeys + kl;
         const int low = weight_first_row_tile(p, n, T, (tile0 + t / G * G) * kWeightKeys);
-        float old = 0.f, next = lse_of(low);
+        int rt = low + ((sn ^ turn) & 1);              // this group's first
+        float old = 0.f, next = 0.f, sum = 0.f;
         if (p.keep != 0.f && key < T) old = row[key];
-        bool here = key < T;
-        float sum = 0.f;
-        for (int rt = low; rt < rts; ++rt) {
-          float *const lse = lse_s + (sn & 1) * N;
-          const int live = rows_of(rt, n), sbuf = 2 * g + (sn & 1);
-          if (kl < N) lse[kl] = next;
-          next = lse_of(rt + 1);
-          ok = ok && mbar_wait_suspended(bar(C::kSFull, sbuf), (sn >> 1) & 1, p.status);
-          ok = named_barrier_and(1 + g, 128, ok);
+        if (!cached && kl < N) next = lse_of(rt, kl);
+        for (; rt < rts && ok; rt += 2) {
+          const int nth = sn + rt - low, sbuf = 2 * g + turn;      // the unit's number
+          const int live = rows_of(rt, n);
+          const float *lse = lse_all + (rt - run_low) * N;
+          if (!cached) {
+            float *const mine = lse_two + (nth >> 1 & 1) * N;
+            if (kl < N) {
+              mine[kl] = next;
+              next = lse_of(rt + 2, kl);
+            }
+            lse = mine;
+          }
+          ok = mbar_wait_suspended(bar(C::kSFull, sbuf), (nth >> 1) & 1, p.status);
+          ok = cached ? __all_sync(0xffffffffu, ok) : named_barrier_and(1 + group, 128, ok);
           if (!ok) break;
-          ++sn;
           tc::fence_after_sync();
-          if (rt == low)
-            here = here && (page_mask[(cc + kTileSteps * t + kl / kStepKeys) & 63] >> (kl % kStepKeys / kPage) & 1);
+          const bool here = key < T && (page_mask[(cc + kTileSteps * t + kl / kStepKeys) & 63] >> (kl % kStepKeys / kPage) & 1);
           // columns from `from` on belong to tokens that see the key
           const int from = here ? min(max(0, key - (T - n) - tokens_of(rt)), N) * p.hpt : INT32_MAX;
+          const bool whole = __all_sync(0xffffffffu, from <= 0);
           const uint32_t s_col = tmem + tlane + sbuf * N;
-          uint64_t acc = 0;
-#pragma unroll 1
-          for (int c = 0; c < live; c += 32) {
-            uint32_t s[32];
-            tc::ld_32x32b_x32(s_col + c, s);
-            tc::wait_ld_all();
-            tc::hold<32>(s);
-            const uint64_t scale2 = pack_f2(p.scale_log2, p.scale_log2);
-            const bool all = __all_sync(0xffffffffu, from <= c) && c + 32 <= live;
+          uint64_t acc[2] = {0, 0};
+          // 16 columns; `masked`: those that a key does not see, or behind the last, add nothing
+          auto add = [&](const uint32_t(&s)[16], int c, auto masked) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < 16; e += 4) {
               const float4 l = *reinterpret_cast<const float4 *>(lse + c + e);
               float w[4];
-              unpack_f2(fma_f2(pack_f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, pack_f2(-l.x, -l.y)), w[0], w[1]);
-              unpack_f2(fma_f2(pack_f2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, pack_f2(-l.z, -l.w)), w[2], w[3]);
+              unpack_f2(fma_f2(pack_f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, pack_f2(l.x, l.y)), w[0], w[1]);
+              unpack_f2(fma_f2(pack_f2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, pack_f2(l.z, l.w)), w[2], w[3]);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) w[k] = fast_exp2(w[k]);
-              if (!all) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = c + e + k >= from && c + e + k < live ? w[k] : 0.f;
+              for (int k = 0; k < 4; ++k) {
+                w[k] = fast_exp2(w[k]);
+                if constexpr (decltype(masked)::value) w[k] = c + e + k >= from && c + e + k < live ? w[k] : 0.f;
               }
-              acc = add_f2(acc, pack_f2(w[0], w[1]));
-              acc = add_f2(acc, pack_f2(w[2], w[3]));
+              acc[0] = add_f2(acc[0], pack_f2(w[0], w[1]));
+              acc[1] = add_f2(acc[1], pack_f2(w[2], w[3]));
             }
-          }
+          };
+          // the next columns' load in flight beside these ones' sums
+          auto all = [&](auto masked) {
+            uint32_t s0[16], s1[16];
+            tc::ld_32x32b_x16(s_col, s0);
+#pragma unroll 1
+            for (int c = 0; c < live; c += 32) {
+              tc::wait_ld(s0);
+              tc::ld_32x32b_x16(s_col + c + 16, s1);
+              add(s0, c, masked);
+              tc::wait_ld(s1);
+              if (c + 32 < live) tc::ld_32x32b_x16(s_col + c + 32, s0);
+              add(s1, c + 16, masked);
+            }
+          };
+          if (whole && live % 32 == 0) all(std::false_type{}); else all(std::true_type{});
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::kSFree, sbuf));
           float a0, a1;
-          unpack_f2(acc, a0, a1);
+          unpack_f2(add_f2(acc[0], acc[1]), a0, a1);
           sum += a0 + a1;
         }
-        if (ok && key < T) row[key] = p.keep != 0.f ? fmaf(p.keep, old, sum) : sum;
+        // A tile of one unit is its group's; else the groups' sums are joined.
+        const int units = rts - low;
+        const bool mine = units > 1 ? turn == 0 : ((sn ^ turn) & 1) == 0;
+        if (units > 1) {
+          float *const half = half_s + (tn & 1) * kWeightKeys;
+          if (turn == 1) *half = sum;
+          ok = named_barrier_and(5 + g, 256, ok);
+          if (turn == 0) sum += *half;
+        }
+        sn += units;
+        if (ok && mine && key < T) row[key] = p.keep != 0.f ? fmaf(p.keep, old, sum) : sum;
       }
       cc += kTileSteps * tiles;
       __syncwarp();
@@ -539,10 +573,10 @@ __global__ void __launch_bounds__(WeightCfg<D, KF>::kThreads, 1)
   if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, C::kTCols);
 }
 
-template <int D, int KF>
+template <int D, int KF, int N>
 cudaError_t launch_one(const WeightParams &p, cudaStream_t st) {
-  using C = WeightCfg<D, KF>;
-  auto kernel = key_weights_kernel<D, KF>;
+  using C = WeightCfg<D, KF, N>;
+  auto kernel = key_weights_kernel<D, KF, N>;
   static bool ready[64] = {};                // the shared-memory limit, set once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -560,20 +594,22 @@ cudaError_t launch_one(const WeightParams &p, cudaStream_t st) {
   return launch_pdl(kernel, dim3(p.ctas), dim3(C::kThreads), C::kSmem, st, qm, p);
 }
 
-template <int D>
+template <int D, int N>
 cudaError_t launch_formats(int kf, const WeightParams &p, cudaStream_t st) {
   switch (kf) {
-    case MEMRA_KV_Q8_0: return launch_one<D, MEMRA_KV_Q8_0>(p, st);
-    case MEMRA_KV_FP8_E4M3: return launch_one<D, MEMRA_KV_FP8_E4M3>(p, st);
-    case MEMRA_KV_NVFP4: return launch_one<D, MEMRA_KV_NVFP4>(p, st);
+    case MEMRA_KV_Q8_0: return launch_one<D, MEMRA_KV_Q8_0, N>(p, st);
+    case MEMRA_KV_FP8_E4M3: return launch_one<D, MEMRA_KV_FP8_E4M3, N>(p, st);
+    case MEMRA_KV_NVFP4: return launch_one<D, MEMRA_KV_NVFP4, N>(p, st);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_key_weights(int D, int kf, const WeightParams &p, cudaStream_t st) {
-  return D == 128 ? launch_formats<128>(kf, p, st) : launch_formats<256>(kf, p, st);
+cudaError_t launch_key_weights(int D, int rows, int kf, const WeightParams &p, cudaStream_t st) {
+  if (rows == kWeightRowsFew)
+    return D == 128 ? launch_formats<128, kWeightRowsFew>(kf, p, st) : launch_formats<256, kWeightRowsFew>(kf, p, st);
+  return D == 128 ? launch_formats<128, weight_rows(128)>(kf, p, st) : launch_formats<256, weight_rows(256)>(kf, p, st);
 }
 
 }  // namespace memra

@@ -10,8 +10,10 @@
 namespace memra {
 
 constexpr int kWeightKeys = 128;           // keys of a tile (the M of the MMA)
-// Query rows of a tile (its N): what shared memory holds of them.
+// Query rows of a tile (its N): what shared memory holds of them; and where the sequences have few rows on
+// average, so that more raw pages can be in flight instead.
 __host__ __device__ constexpr int weight_rows(int D) { return D == 128 ? 128 : 64; }
+constexpr int kWeightRowsFew = 32;
 
 struct WeightParams {
   const uint8_t *k_pool;
@@ -31,6 +33,7 @@ struct WeightParams {
   int ctas;
 };
 
-cudaError_t launch_key_weights(int D, int kf, const WeightParams &p, cudaStream_t st);
+// `rows`: query rows of a tile, weight_rows(D) or kWeightRowsFew
+cudaError_t launch_key_weights(int D, int rows, int kf, const WeightParams &p, cudaStream_t st);
 
 }  // namespace memra
