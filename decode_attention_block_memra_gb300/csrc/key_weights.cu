@@ -14,7 +14,8 @@
 //     other: while one is made, the tensor cores are at the other;
 //   * a load warp brings row tiles of Q by TMA; where all rows of the chunk
 //     fit their ring, once for all keys of a CTA's run;
-//   * one MMA thread: S^T = K^ Q^T, two key tiles beside one another for each row tile;
+//   * an MMA thread for each key tile: S^T = K^ Q^T, two key tiles beside one another for
+//     each row tile (one thread for both took longer to issue than the MMAs run);
 //   * four groups of four warps, two for each key tile, which take its row tiles by
 //     turns: thread = key (at head_dim 256 with q8_0 there is room for one tile of
 //     K^, and two groups).  A row tile takes a group about 3,000 clocks, the tensor cores
@@ -153,7 +154,7 @@ struct WeightCfg {
   // Keys of a raw chunk: at 32, a staging warp has two loads in flight and the waits around them; 64 where they fit.
   static constexpr int kStepKeys = D == 128 ? 64 : 32, kTileSteps = kWeightKeys / kStepKeys;
   static constexpr int kTiles = D == 256 && kKLo ? 1 : 2;       // tiles of K^, with two groups of the epilogue each
-  static constexpr int kStageWarp0 = 8 * kTiles, kMmaWarp = kStageWarp0 + 8, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kStageWarp0 = 8 * kTiles, kMmaWarp = kStageWarp0 + 8, kLoadWarp = kMmaWarp + kTiles;
   static constexpr int kCopyWarp = kLoadWarp + 1, kThreads = 32 * (kCopyWarp + 1);
   static constexpr int kPages = kStepKeys / kPage;
   static constexpr int kKSeg = k_seg_bytes(KF, D);
@@ -173,7 +174,7 @@ struct WeightCfg {
   static constexpr uint32_t kTCols = 512, kNeed = kOffRaw + kRaw * kRawBytes + 1024, kFloor = 150 * 1024;      // (1024: aligning the base)
   static constexpr uint32_t kSmem = kNeed < kFloor ? kFloor : kNeed;
   enum Bar { kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kKFree = kKFull + 2, kQFull = kKFree + 2,
-             kQFree = kQFull + kQBufs, kSFull = kQFree + kQBufs, kSFree = kSFull + 4, kDrained = kSFree + 4, kPieceFull,
+             kQFree = kQFull + kQBufs, kSFull = kQFree + kQBufs, kSFree = kSFull + 4, kDrained = kSFree + 4, kPieceFull = kDrained + 2,
              kPieceFree = kPieceFull + kPieces, kBars = kPieceFree + kPieces };
   static_assert(kQBufs >= 1 && kRaw >= 1, "rings");
   static_assert(kOffBar + 8 * kBars + 4 <= kOffMask, "barriers and the tensor-memory address");
@@ -232,13 +233,13 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
       }
       for (int i = 0; i < QB; ++i) {
         mbar_init(bar(C::kQFull, i), 1);
-        mbar_init(bar(C::kQFree, i), 1);
+        mbar_init(bar(C::kQFree, i), G);
       }
       for (int i = 0; i < 4; ++i) {
         mbar_init(bar(C::kSFull, i), 1);
         mbar_init(bar(C::kSFree, i), 4);
       }
-      mbar_init(bar(C::kDrained, 0), 1);
+      for (int i = 0; i < G; ++i) mbar_init(bar(C::kDrained, i), 1);
       for (int i = 0; i < kPieces; ++i) {
         mbar_init(bar(C::kPieceFull, i), 1);
         mbar_init(bar(C::kPieceFree, i), C::kCopyWarp);          // every other warp
@@ -365,10 +366,13 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
       for (int c = max(0, qn - QB); c < qn; ++c) mbar_wait_suspended(bar(C::kQFull, c % QB), (c / QB) & 1, p.status);
     }
     __syncwarp();
-  } else if (warp == C::kMmaWarp) {
+  } else if (warp >= C::kMmaWarp) {
     // -------------------------------------------------------------------- MMA --
     if (tc::elect_one()) {
-      int qn = 0, kn[2] = {0, 0}, sn[2] = {0, 0};      // loads of Q used, tiles of K^ and score buffers used by group
+      const int g = warp - C::kMmaWarp;                // the tile of K^
+      const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffK + g * C::kKBuf, 16, 1024);
+      const uint64_t qd0 = tc::smem_desc_sw128(sb + C::kOffQ, 16, 1024);
+      int qn = 0, kn = 0, sn = 0;                      // loads of Q, tiles of K^ and score buffers used
       auto wait = [&](int which, int i, int phase) { ok = ok && mbar_wait_suspended(bar(which, i), phase & 1, p.status); };
       while (true) {
         const volatile WeightPiece *x = next_piece();
@@ -378,20 +382,19 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
         const bool held = rts - first <= QB;
         for (int t = 0; t < tiles && ok; t += G) {
           const int low = weight_first_row_tile(p, n, T, (tile0 + t) * kWeightKeys);
-          for (int rt = low; rt < rts && ok; ++rt) {
-            const int use = held ? qn + rt - first : qn, qs = use % QB;
+          const bool any = t + g < tiles;
+          for (int rt = low; rt < rts; ++rt) {
+            const int use = held ? qn + rt - first : qn, qs = use % QB, sbuf = 2 * g + (sn & 1);
+            // (Without a tile too: a slot is freed once by each for every load, and only after it.)
             wait(C::kQFull, qs, use / QB);
-            const uint32_t idesc = tc::idesc_f16_f32(kWeightKeys, (rows_of(rt, n) + 15) & ~15);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              if (t + g >= tiles) continue;
-              const int sbuf = 2 * g + (sn[g] & 1);
-              if (rt == low) wait(C::kKFull, g, kn[g]);
-              if (sn[g] >= 2) wait(C::kSFree, sbuf, (sn[g] >> 1) - 1);
-              if (!ok) continue;
+            if (!ok) break;
+            if (any) {
+              const uint32_t idesc = tc::idesc_f16_f32(kWeightKeys, (rows_of(rt, n) + 15) & ~15);
+              const uint64_t qd = tc::desc_at(qd0, qs * C::kQBuf);
+              if (rt == low) wait(C::kKFull, g, kn);
+              if (sn >= 2) wait(C::kSFree, sbuf, (sn >> 1) - 1);
+              if (!ok) break;
               tc::fence_after_sync();
-              const uint64_t kd = tc::smem_desc_sw128(sb + C::kOffK + g * C::kKBuf, 16, 1024);
-              const uint64_t qd = tc::smem_desc_sw128(sb + C::kOffQ + qs * C::kQBuf, 16, 1024);
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
                 const uint64_t bd = tc::desc_at(qd, (ks / 4) * N * 128 + (ks % 4) * 32);
@@ -401,13 +404,12 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
                               bd, idesc, ks + lo > 0);
               }
               tc::commit(bar(C::kSFull, sbuf));
-              ++sn[g];
+              ++sn;
               if (rt == rts - 1) {
                 tc::commit(bar(C::kKFree, g));
-                ++kn[g];
+                ++kn;
               }
             }
-            if (!ok) break;
             if (!held) {
               tc::commit(bar(C::kQFree, qs));
               ++qn;
@@ -420,8 +422,8 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
         }
         free_piece();
       }
-      tc::commit(bar(C::kDrained, 0));       // what was issued completes before the CTA can leave
-      mbar_wait_suspended(bar(C::kDrained, 0), 0, p.status);
+      tc::commit(bar(C::kDrained, g));       // what was issued completes before the CTA can leave
+      mbar_wait_suspended(bar(C::kDrained, g), 0, p.status);
     }
     __syncwarp();
   } else if (warp >= C::kStageWarp0) {
