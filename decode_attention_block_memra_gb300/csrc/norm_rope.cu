@@ -7,23 +7,31 @@
 //   (a, b) = (y_j, y_{j + R/2})  or, interleaved,  (y_{2j}, y_{2j+1})
 //
 // Everything is float32 until the one rounding to fp16; the stored bytes are those
-// that kv_append makes of the rounded row.
+// that kv_append makes of the rounded row.  A key next to a border of its 8-bit code
+// falls to one side or the other by its last bits: in float32 some five codes of 8
+// million differ from exact arithmetic's, so keys, a small part of the rows, are carried
+// as unevaluated sums of two floats from the sum of squares to the rounding, and none did
+// (16,384 tokens of 16 and 2 heads, D 256, fp8 cache: 84 us, 77 with keys in float32).
 //
 // Angles.  position * inv_freq reaches 10^5 and more radians, where float32 has no
 // digits left behind the point.  So a frequency is kept in turns (inv_freq / 2 pi)
 // as a 64-bit binary fraction, rounded once, and the position multiplies it modulo
 // 2^64: whole turns fall away exactly.  What is left within an eighth of a turn goes
-// through the Taylor series of sine and cosine, with what float32 drops of the angle and of the
-// leading terms carried along: a key next to a border of its 8-bit code falls to one
-// side or the other by its last bits, and should not do so by the sine's.
+// through the Taylor series of sine and cosine, their leading terms as two floats.
 //
 // A row is D / 8 lanes of 8 consecutive dims (one 16-byte load); a warp takes 32 / (D / 8)
 // heads of one token at a time, of one kind (K, V or Q), so that it never diverges
 // in the quantizer.  With many tokens a warp's unit is all rows of a token: every unit
 // costs the same, the angles are taken once, and no warp waits for another.  With few, a
-// unit is one row group.  The next rows' loads are in flight throughout.
+// token is cut into as many units as give every warp one.  The next rows' loads are in
+// flight throughout.
+//
+// Bound by bytes with many tokens, and by the arithmetic of the keys and of the quantizers
+// beside them: those 16,384 tokens move 319 MB in 84 us, 3.8 TB/s (queries alone: 268 MB in
+// 54 us, 5.0 TB/s); 2,048 tokens of 32 and 4 heads, D 128, no cache: 38 MB in
+// 15.6 us.  With few, by
+// the chain of one row: a launch of 8 tokens takes 5 us.
 #include <algorithm>
-#include <type_traits>
 
 #include "kv_stage.cuh"
 #include "norm_rope.cuh"
@@ -38,15 +46,36 @@ struct Two {
   float hi, lo;
 };
 
-// a * b exactly (Dekker, with a fused product); a + b for |a| >= |b|.
+// a * b exactly (Dekker, with a fused product); a + b exactly (Knuth), and for |a| >= |b|.
 __device__ __forceinline__ Two two_prod(float a, float b) {
   const float p = __fmul_rn(a, b);
   return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
 }
 __device__ __forceinline__ Two fast_two_sum(float a, float b) {
   const float s = __fadd_rn(a, b);
   return {s, __fsub_rn(b, __fsub_rn(s, a))};
 }
+// Sums and products but for 2^-45 of them (of the operands, for a sum that cancels).
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const Two s = two_sum(a.hi, b.hi);
+  return {s.hi, s.lo + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  const Two p = two_prod(a.hi, b.hi);
+  return {p.hi, fmaf(a.hi, b.lo, fmaf(a.lo, b.hi, p.lo))};
+}
+
+// 1 / sqrt(a): an approximation y and one Newton step, y + y (1 - a y^2) / 2, whose correction is the low part.
+__device__ __forceinline__ Two rsqrt_two(Two a) {
+  const float y = rsqrtf(a.hi);
+  const Two p = mul(a, two_prod(y, y));
+  return {y, 0.5f * y * (__fsub_rn(1.f, p.hi) - p.lo)};
+}
+
 __device__ __forceinline__ void unpack(const uint4 &y, float (&x)[8]) {
   const uint32_t in[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -60,20 +89,22 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
   return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
 }
 
-// Sine and cosine of `rest` 2^-64 turns, an eighth of a turn at most, by their Taylor series.
-__device__ __forceinline__ void sin_cos(long long rest, float &sine, float &cosine) {
-  // 2 pi / 2^64
+// Sine and cosine of `rest` 2^-64 turns, an eighth of a turn at most, by their Taylor series: off by less than 2^-29.
+__device__ __forceinline__ void sin_cos(long long rest, Two &sine, Two &cosine) {
+  // 2 pi / 2^64, 1 / 6
   constexpr float kHi = 0x1.921fb6p-62f, kLo = -0x1.777a5cp-87f;
+  constexpr float kSixth = 1.f / 6.f, kSixthLo = static_cast<float>(1.0 / 6.0 - static_cast<double>(kSixth));
   const float r = __ll2float_rn(rest), r_lo = __ll2float_rn(rest - __float2ll_rn(r));
-  const Two x0 = two_prod(r, kHi);
-  const Two x = fast_two_sum(x0.hi, fmaf(r, kLo, fmaf(r_lo, kHi, x0.lo)));
-  const Two z0 = two_prod(x.hi, x.hi);
-  const float z = z0.hi, z_lo = fmaf(2.f * x.hi, x.lo, z0.lo);
-  const float odd = fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
-  sine = x.hi + fmaf(x.hi * z, odd, x.lo * fmaf(-0.5f, z, 1.f));
-  const float even = z * fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
-  const Two one = fast_two_sum(1.f, -0.5f * z);
-  cosine = one.hi + (one.lo + fmaf(z, even, -0.5f * z_lo));
+  const Two x = mul({r, r_lo}, {kHi, kLo}), z = mul(x, x);
+  // x - x z / 6 + x z^2 (1/120 - ..)
+  const Two cube = mul(mul(x, z), {-kSixth, -kSixthLo});
+  const float odd = fmaf(z.hi, fmaf(z.hi, fmaf(z.hi, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f), 1.f / 120.f);
+  const Two s = two_sum(x.hi, cube.hi);
+  sine = fast_two_sum(s.hi, s.lo + (x.lo + cube.lo + x.hi * z.hi * z.hi * odd));
+  // 1 - z / 2 + z^2 (1/24 - ..)
+  const float even = fmaf(z.hi, fmaf(z.hi, fmaf(z.hi, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
+  const Two c = fast_two_sum(1.f, -0.5f * z.hi);
+  cosine = fast_two_sum(c.hi, c.lo + fmaf(z.hi * z.hi, even, -0.5f * z.lo));
 }
 
 // e4m3 codes of the lane's eight values over the scale, the first in the lowest byte.
@@ -109,9 +140,9 @@ template <int D>
 __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRopeParams p) {
   constexpr int L = D / 8, ROWS = 32 / L;  // lanes of a row, rows of a warp
   __shared__ unsigned long long s_turns[D / 2];
-  __shared__ __align__(16) float s_angles[kWarps][2][D / 2];    // sines and cosines of each warp's token
+  __shared__ __align__(16) float s_angles[kWarps][4][D / 2];    // sines, cosines and their low parts of each warp's token
   const int tid = threadIdx.x, lane = tid & 31, l = lane % L, sub = lane / L;
-  float(&table)[2][D / 2] = s_angles[tid >> 5];
+  float(&table)[4][D / 2] = s_angles[tid >> 5];
   grid_dependency_wait();
   allow_dependent_launch();
   if (p.half) {
@@ -134,10 +165,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
       const unsigned long long turn = s_turns[j] * static_cast<unsigned long long>(static_cast<long long>(position));
       // the nearest quarter turn, and what is left (modulo a quarter)
       const unsigned quarter = static_cast<unsigned>((turn + (1ull << 61)) >> 62);
-      float s, c;
+      Two s, c;
       sin_cos(static_cast<long long>(turn << 2) >> 2, s, c);
-      table[0][j] = quarter & 1 ? (quarter & 2 ? -c : c) : (quarter & 2 ? -s : s);
-      table[1][j] = quarter & 1 ? (quarter & 2 ? s : -s) : (quarter & 2 ? -c : c);
+      const float as = quarter & 2 ? -1.f : 1.f, bs = (quarter + 1) & 2 ? -1.f : 1.f;
+      table[0][j] = as * (quarter & 1 ? c.hi : s.hi), table[2][j] = as * (quarter & 1 ? c.lo : s.lo);
+      table[1][j] = bs * (quarter & 1 ? s.hi : c.hi), table[3][j] = bs * (quarter & 1 ? s.lo : c.lo);
     }
     __syncwarp();
 #pragma unroll
@@ -152,34 +184,28 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
 #pragma unroll
       for (int i = 0; i < 8; ++i) sn[i] *= sign;
   };
-  // N rows of a kind, normalized and turned.
-  auto finish = [&](auto rows, bool norm, const float(&w)[8], float(&x)[decltype(rows)::value][8]) {
-    constexpr int N = decltype(rows)::value;
-    if (norm) {
-      float sum[N];
+  // Two rows of queries, normalized and turned.
+  auto finish = [&](const float(&w)[8], float(&x)[2][8]) {
+    if (p.q_weight) {
+      float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        sum[e] = 0.f;
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[e] = fmaf(x[e][i], x[e][i], sum[e]);
-      }
 #pragma unroll
       for (int d = 1; d < L; d <<= 1)
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], d);
+        for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], d);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        // 1 / sqrt(mean + eps): an approximation and one Newton step
-        const float m = fmaf(sum[e], 1.f / D, p.eps), y = rsqrtf(m);
-        const Two y2 = two_prod(y, y), one = two_prod(y2.hi, m);
-        const float scale = fmaf(0.5f * y, __fsub_rn(1.f, one.hi) - fmaf(y2.lo, m, one.lo), y);
+      for (int e = 0; e < 2; ++e) {
+        const float scale = rsqrtf(fmaf(sum[e], 1.f / D, p.eps));
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[e][i] *= scale * w[i];
       }
     }
     if (!p.half) return;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
+    for (int e = 0; e < 2; ++e) {
       if (p.interleaved) {
         if (turned) {
 #pragma unroll
@@ -198,7 +224,45 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
       }
     }
   };
-
+  // A row of keys, the same in sums of two floats.
+  auto finish_key = [&](float(&x)[8]) {
+    Two v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = {x[i], 0.f};
+    if (p.k_weight) {
+      Two sum{x[0] * x[0], 0.f};           // (the square of an fp16 value is exact)
+#pragma unroll
+      for (int i = 1; i < 8; ++i) sum = add(sum, {x[i] * x[i], 0.f});
+#pragma unroll
+      for (int d = 1; d < L; d <<= 1)
+        sum = add(sum, {__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
+      const Two scale = rsqrt_two(add({sum.hi * (1.f / D), sum.lo * (1.f / D)}, {p.eps, 0.f}));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = mul(mul(scale, {p.k_weight[8 * l + i], 0.f}), v[i]);
+    }
+    // a cosine + b sine
+    auto turn = [&](Two a, Two b, int j, float s) {
+      const Two t = add(mul(a, {table[1][j], table[3][j]}), mul(b, {s * table[0][j], s * table[2][j]}));
+      return t.hi + t.lo;
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i].hi + v[i].lo;
+    if (p.half && p.interleaved) {
+      if (turned) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = turn(v[2 * i], v[2 * i + 1], j0 + i, -1.f);
+          x[2 * i + 1] = turn(v[2 * i + 1], v[2 * i], j0 + i, 1.f);
+        }
+      }
+    } else if (p.half) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const Two b{__shfl_sync(0xffffffffu, v[i].hi, partner, L), __shfl_sync(0xffffffffu, v[i].lo, partner, L)};
+        if (turned) x[i] = turn(v[i], b, j0 + i, sign);
+      }
+    }
+  };
   auto weights = [&](const float *weight, float(&w)[8]) {       // the norm's, of this lane's dims
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = weight ? weight[8 * l + i] : 1.f;
@@ -214,10 +278,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
     // Row groups of the unit by kind: all of the token's, or one share.
     int v0 = 0, v1 = p.v_passes, k0 = 0, k1 = p.k_passes, q0 = 0, q1 = p.q_passes;
     if (p.parts > 1) {
-      const int kv = p.v_passes + p.k_passes;
-      v0 = min(part, p.v_passes), v1 = min(part + 1, p.v_passes);
-      k0 = min(max(part - p.v_passes, 0), p.k_passes), k1 = min(max(part + 1 - p.v_passes, 0), p.k_passes);
-      q0 = max(part - kv, 0) * p.q_share, q1 = min(max(part + 1 - kv, 0) * p.q_share, p.q_passes);
+      const int vs = (p.v_passes + p.kv_share - 1) / p.kv_share, ks = (p.k_passes + p.kv_share - 1) / p.kv_share;
+      auto cut = [](int i, int share, int passes) { return min(max(i, 0) * share, passes); };
+      v0 = cut(part, p.kv_share, p.v_passes), v1 = cut(part + 1, p.kv_share, p.v_passes);
+      k0 = cut(part - vs, p.kv_share, p.k_passes), k1 = cut(part + 1 - vs, p.kv_share, p.k_passes);
+      q0 = cut(part - vs - ks, p.q_share, p.q_passes), q1 = cut(part + 1 - vs - ks, p.q_share, p.q_passes);
     }
     auto load = [&](const __half *base, int64_t stride, int pass, int end, int heads) {
       const int head = pass * ROWS + sub;
@@ -256,13 +321,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
     }
 #pragma unroll 1
     for (int pass = k0; pass < k1; ++pass) {
-      float x[1][8];
-      unpack(yk, x[0]);
+      float x[8];
+      unpack(yk, x);
       yk = load(p.k, p.k_stride, pass + 1, k1, p.n_kv_heads);
-      float kw[8];
-      weights(p.k_weight, kw);
-      finish(std::integral_constant<int, 1>{}, p.k_weight != nullptr, kw, x);
-      const uint4 y = pack(x[0]);
+      finish_key(x);
+      const uint4 y = pack(x);
       const int head = pass * ROWS + sub;
       if (p.k_out && head < p.n_kv_heads)
         *reinterpret_cast<uint4 *>(p.k_out + token * p.k_out_stride + (head * D + 8 * l)) = y;
@@ -279,7 +342,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
         unpack(yq[e], x[e]);
         yq[e] = load(p.q, p.q_stride, pass + 2 + e, q1, p.n_heads);
       }
-      finish(std::integral_constant<int, 2>{}, p.q_weight != nullptr, qw, x);
+      finish(qw, x);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int head = (pass + e) * ROWS + sub;
@@ -296,10 +359,18 @@ cudaError_t launch(NormRopeParams p, int sms, cudaStream_t st) {
   p.k_passes = p.k ? groups(p.n_kv_heads, kRows) : 0;
   p.v_passes = p.slots ? groups(p.n_kv_heads, kRows) : 0;
   p.q_passes = groups(p.n_heads, kRows);
-  // Whole tokens as units where they give every warp of the GPU two; else row groups, the queries' so many at a time.
-  const int64_t warps = 3ll * sms * kWarps, tokens = p.tokens;
-  p.q_share = static_cast<int>(std::min<int64_t>(std::max<int64_t>(tokens * p.q_passes / (2 * warps), 1), p.q_passes));
-  p.parts = tokens >= 2 * warps ? 1 : p.k_passes + p.v_passes + groups(p.q_passes, p.q_share);
+  // A unit to a warp: a token's row groups of K and of V in shares as small as leave the queries' a warp, these in as many
+  // as there are then (a row of K or V takes some three times a query's).  From so many tokens on that three units a
+  // token are too many, whole tokens (32 and 8 heads, D 128, fp8: 512 tokens 10 us so, 17 whole, 15 group by group; 4,096
+  // tokens 43 us whole, 67 group by group).
+  const int64_t warps = 3ll * sms * kWarps, tokens = p.tokens, room = tokens > 0 ? warps / tokens : 0;
+  p.parts = 1;
+  for (int share = 1; p.parts == 1 && share <= std::max({p.k_passes, p.v_passes, 1}); ++share) {
+    const int kv = groups(p.k_passes, share) + groups(p.v_passes, share);
+    if (room <= kv) continue;
+    p.kv_share = share, p.q_share = groups(p.q_passes, room - kv);
+    p.parts = kv + groups(p.q_passes, p.q_share);
+  }
   p.units = tokens * p.parts;
   // (an odd number of CTAs: even and odd tokens to every SM)
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((p.units + kWarps - 1) / kWarps, (3ll * sms - 1) | 1));

@@ -24,8 +24,8 @@ struct NormRopeParams {
   int tokens, n_heads, n_kv_heads, num_pages;
   int half;                       // rotated pairs: rotary_dim / 2
   int interleaved;
-  // set by the launcher: row groups of a token by kind; units of a token, and row groups of one of its queries'; units in all
-  int k_passes, v_passes, q_passes, parts, q_share;
+  // set by the launcher: row groups of a token by kind; units of a token, and row groups of one of its queries' and of one of its keys' or values'; units in all
+  int k_passes, v_passes, q_passes, parts, q_share, kv_share;
   int64_t units;
 };
 
