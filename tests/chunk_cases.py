@@ -74,6 +74,8 @@ class Chunk:
         first, k, v = self.rows[b]
         return first, dequantized(k[:, h], self.kf, self.scales[0]), dequantized(v[:, h], self.vf, self.scales[1])
 
+    operand = 0.0
+
     def expected(self, b, h):
         """Rows of sequence b and KV head h: out [n, G, D], lse [n, G] and how far each may be off.
 
@@ -84,6 +86,7 @@ class Chunk:
         d_u: the accumulator of the score, cut at each of D / 16 steps (twice for pairs).
         The integer formats enter as fp16 pairs of half their value.  Below fp16's normal range a rounding is off by half of
         2^-24, whatever the value: K^ by up to 2^-24 (2^-24 sum |q_j| in the score), V^ likewise.
+        `operand`: what K^ and V^ are off by, relative, where an operator rounds them (2^-11: to fp16).
         """
         G, n = self.Hq // self.Hkv, self.new[b]
         first, k, v = self.keys(b, h)
@@ -91,7 +94,7 @@ class Chunk:
         sees = chunked.chunk_sees(n, T, self.window)[:, first:]
         q = self.q[self.starts[b]:self.starts[b + 1], h * G:(h + 1) * G].astype(np.float64)
         scale = self.D ** -0.5
-        per_key = 2.0 ** -23 * (self.D / 8)
+        per_key = 2.0 ** -23 * (self.D / 8) + self.operand
         out, tol = np.zeros((n, G, self.D)), np.zeros((n, G, self.D))
         lse, lse_tol = np.full((n, G), -np.inf), np.zeros((n, G))
         for g in range(G):
@@ -108,7 +111,7 @@ class Chunk:
             av = np.abs(v)
             # |v - o| <= |v| + |o|
             tol[:, g] = 1.05 * ((p * d) @ av + (p * d).sum(1, keepdims=True) * np.abs(out[:, g])) + \
-                (2.0 ** -11 + 960 * 2.0 ** -23 + 2.0 ** -19) * (p @ av) + 2.0 ** -11 * np.abs(out[:, g]) + 2.0 ** -23
+                (2.0 ** -11 + 960 * 2.0 ** -23 + 2.0 ** -19 + self.operand) * (p @ av) + 2.0 ** -11 * np.abs(out[:, g]) + 2.0 ** -23
             with np.errstate(divide="ignore"):
                 lse[:, g] = np.where(mass[:, 0] > 0, np.log(mass[:, 0]) + top[:, 0], -np.inf)
             lse_tol[:, g] = 1.05 * (p * d).sum(1) + 2.0 ** -19 + 2.0 ** -22 * np.where(np.isfinite(lse[:, g]), np.abs(lse[:, g]), 0)
