@@ -4,6 +4,11 @@
 // n = min(T, budget) rows stay: the last `recent` of them, the first `sink`, and of
 // the others (the middle) the m with the largest weight, the lower index where
 // two weigh the same.
+//
+// Two kernels: who stays, which is a chain of latencies (a read of the weights, four rounds over a
+// cluster), and their rows' move, which is bytes.  q8_0/q5_1, D 128, with the graph's launches:
+// 262,144 keys of 4 heads to 16,384 35 us (16 to select, 19 to move 15 MB), 16 sequences of up to
+// 8,192 to 2,048 24 us (7 and 17 for 29 MB), one of 512 with 2 heads to 256 8 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -45,26 +50,26 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Inclusive sum over the CTA's threads; `total` the whole.
-__device__ __forceinline__ int block_scan(int x, int *warp_sums, int &total) {
+// Inclusive sum over the CTA's threads.
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T *warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, x, d);
+    const T up = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += up;
   }
   __syncthreads();                         // (the sums of the scan before have been read)
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int s = warp_sums[lane];
+  T s = warp_sums[lane];
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, s, d);
+    const T up = __shfl_up_sync(0xffffffffu, s, d);
     if (lane >= d) s += up;
   }
-  total = __shfl_sync(0xffffffffu, s, 31);
-  const int before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
-  return x + (warp > 0 ? before : 0);
+  const T before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+  return x + (warp > 0 ? before : T{0});
 }
 
 // Of up to 1,024 keys (one a thread): the m-th largest, bit by bit, by how many reach a candidate.
@@ -85,21 +90,22 @@ __device__ __forceinline__ uint32_t nth_key_by_bits(uint32_t key, bool in, int m
 // thread and finds it bit by bit.  Else by digits, the highest first: a histogram of the
 // digit over the keys that agree with the digits found, and the digit where the
 // count from above passes m.  A cluster holds one (sequence, KV head), each CTA a run of
-// the middle; the CTAs add up each other's histograms through shared memory.  A
-// CTA's keys are read once, E to a thread, all loads in flight, and stay in registers
-// (longer runs: read again from L2 for each digit).
+// the middle; every CTA adds up all histograms through shared memory, those of the runs before its
+// own also apart: they say where its rows go.  A CTA's keys are read once, E to a thread, all loads in
+// flight, and stay in registers (longer runs: read again from L2 for each digit).
+// Four digits of 8 bits: three of 11 take a round less, but a CTA then reads eight times the
+// counts of every other (4 x 262,144 weights in clusters of 16: 23 us for the digits, with these 11).
 template <int E>
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictParams p) {
   __shared__ int hist[E > 1 ? kDigits : 1][E > 1 ? kBins : 1];
+  __shared__ unsigned long long scan_sums[kWarps];
   __shared__ int warp_sums[kWarps], warp_over[kWarps];
-  __shared__ int found[2];                 // the digit, and how many of its keys are wanted
-  __shared__ int counts[2];                // of this CTA's run: keys above the last one taken, keys equal to it
+  __shared__ int found[4];                 // the digit, how many of its keys are wanted; in the runs before: keys above, and of it
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, ranks = E > 1 ? cluster.num_blocks() : 1, rank = E > 1 ? cluster.block_rank() : 0;
   const int row = blockIdx.x / ranks, b = row / p.n_kv_heads;
   if constexpr (E > 1)
     for (int i = tid; i < kDigits * kBins; i += kThreads) hist[i / kBins][i % kBins] = 0;
-  if (tid < 2) counts[tid] = 0;
   grid_dependency_wait();
   allow_dependent_launch();
   const Share s = share_of(p, b);
@@ -120,8 +126,16 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
   auto load = [&](int i0) {
     const int n = mine(i0);
     const float *at = w + index(i0, 0);
+    float x[E];
+    if (n >= E) {                          // (without conditions, so that all are in flight together)
 #pragma unroll
-    for (int e = 0; e < E; ++e) key[e] = e < n ? key_of(at[e * 32]) : 0u;
+      for (int e = 0; e < E; ++e) x[e] = at[e * 32];
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = e < n ? at[e * 32] : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) key[e] = key_of(x[e]);
   };
   // f(key) for this thread's keys
   auto each = [&](auto f) {
@@ -136,68 +150,50 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
   load(lo);
   __syncthreads();
 
-  // every key above `last` is taken, and the first `ties` equal to it
+  // every key above `last` is taken, and the first `ties` equal to it; and how many of either the runs before hold
   uint32_t last = 0;
-  int ties = middle;
-  if (m < middle) {                        // (the same for the whole cluster)
+  int ties = middle, over_before = lo - s.sink, equal_before = 0;
+  if (m == 0) {
+    last = 0xFFFFFFFFu, ties = 0;
+  } else if (m < middle) {                 // (the same for the whole cluster)
+    over_before = 0;
     if constexpr (E == 1) {
-      last = nth_key_by_bits(key[0], lo + tid < hi, max(m, 1), ties);
+      last = nth_key_by_bits(key[0], lo + tid < hi, m, ties);
     } else {
-      uint32_t prefix = 0;
-      int want = m;
+      ties = m;
 #pragma unroll
       for (int digit = 0; digit < kDigits; ++digit) {
         const int shift = 32 - kBits * (digit + 1);
         each([&](uint32_t k) {
-          if (digit == 0 || (k ^ prefix) >> shift < kBins) atomicAdd(&hist[digit][(k >> shift) & (kBins - 1)], 1);
+          if (digit == 0 || (k ^ last) >> shift < kBins) atomicAdd(&hist[digit][(k >> shift) & (kBins - 1)], 1);
         });
         cluster.sync();
-        // a bin of each of the first threads, from the highest down
-        int count = 0;
+        // a bin of each of the first threads, from the highest down: of all runs, and of those before (low half)
         const int bin = kBins - 1 - tid;
+        unsigned long long count = 0;
         if (bin >= 0) {
 #pragma unroll
-          for (int r = 0; r < kClusterMax; ++r)
-            if (r < ranks) count += cluster.map_shared_rank(&hist[digit][0], r)[bin];
+          for (int r = 0; r < kClusterMax; ++r) {
+            if (r >= ranks) break;
+            count += cluster.map_shared_rank(&hist[digit][0], r)[bin] * ((1ull << 32) + (r < rank));
+          }
         }
-        int all;
-        const int upto = block_scan(count, warp_sums, all);
-        if (want > upto - count && want <= upto) {
+        const unsigned long long above = block_scan(count, scan_sums) - count;
+        const int over = static_cast<int>(above >> 32);
+        if (ties > over && ties <= over + static_cast<int>(count >> 32)) {
           found[0] = bin;
-          found[1] = want - (upto - count);
+          found[1] = ties - over;
+          found[2] = static_cast<int>(above);
+          found[3] = static_cast<int>(count);
         }
         __syncthreads();
-        if (want > 0) {
-          prefix |= static_cast<uint32_t>(found[0]) << shift;
-          want = found[1];
-        }
+        last |= static_cast<uint32_t>(found[0]) << shift;
+        ties = found[1];
+        over_before += found[2];
+        equal_before = found[3];
       }
-      last = prefix;
-      ties = want;
+      if (ranks > 1) cluster.barrier_arrive();         // (waited for at the end: no CTA leaves while another reads its shared memory)
     }
-    if (m == 0) last = 0xFFFFFFFFu, ties = 0;
-  }
-  // How many the runs before this one hold, and so where its rows go.
-  int over_before = 0, equal_before = 0;
-  if (ranks > 1) {
-    int over = 0, equal = 0;
-    each([&](uint32_t k) {
-      over += k > last;
-      equal += k == last;
-    });
-    over = __reduce_add_sync(0xffffffffu, over);
-    equal = __reduce_add_sync(0xffffffffu, equal);
-    if ((tid & 31) == 0) {
-      atomicAdd(&counts[0], over);
-      atomicAdd(&counts[1], equal);
-    }
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-      const int *c = cluster.map_shared_rank(&counts[0], r);
-      over_before += c[0];
-      equal_before += c[1];
-    }
-    cluster.sync();                        // no CTA leaves while another reads its shared memory
   }
 
   int32_t *kept = p.kept + static_cast<int64_t>(row) * p.max_budget;
@@ -238,14 +234,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
       equals += __popc(ms);
     }
   }
+  if (E > 1 && ranks > 1 && m > 0 && m < middle) cluster.barrier_wait();
 }
 
 // The kept rows to their new pages, byte for byte, and their weights.  A thread makes one unit of the new
 // segment, at most 16 bytes: a K unit of one token is a copy, the others hold bytes of
 // two tokens (NVFP4 K) or of four (V), which it picks from the units that lie at the
 // same place of their old pages, all loads in flight.  (A thread that moved single
-// bytes of the page's 16 rows made seven times the loads: 81 us for 28,000 rows of 4 heads.)  What bounds
-// it: half of the bytes of a sector that a V unit is read from belong to other tokens.
+// bytes of the page's 16 rows made seven times the loads: 81 us for 28,000 rows of 4 heads.)  Bytes
+// bound it, those of other tokens too: a V unit is read from sectors that hold eight tokens' (65,536 rows
+// that lie apart: 15 MB of them, 135 MB of sectors, 87 MB from memory in 19 us).  Where a row
+// does not move, a unit is read from the new page and left unused: loads with conditions go one after the other.
 
 __device__ __forceinline__ uint32_t word_of(const uint4 &x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
 
@@ -291,8 +290,7 @@ struct KUnits {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         s[i] = spot(tg + 8 * i);
-        x[i] = s[i].seg ? *reinterpret_cast<const uint4 *>(s[i].seg + (w4 * 32 + 4 * (s[i].t & 7) + (lane & 3)) * 16)
-                        : make_uint4(0, 0, 0, 0);
+        x[i] = *reinterpret_cast<const uint4 *>((s[i].seg ? s[i].seg : to) + (w4 * 32 + 4 * (s[i].t & 7) + (lane & 3)) * 16);
       }
       uint4 *dst = reinterpret_cast<uint4 *>(to + u * 16);
       const uint32_t mask = (s[0].seg ? 0x00FF00FFu : 0u) | (s[1].seg ? 0xFF00FF00u : 0u);
@@ -342,12 +340,12 @@ struct VUnits {
       s[i] = spot(token(c, i));
       byte[i] = byte_of(s[i]);
       if (s[i].seg) mask |= 0xFFu << (8 * i);
-      const uint8_t *src = s[i].seg + at + step * s[i].c();
+      const uint8_t *src = (s[i].seg ? s[i].seg : to) + at + step * s[i].c();
       if constexpr (N == 4) {
-        const uint4 y = s[i].seg ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+        const uint4 y = *reinterpret_cast<const uint4 *>(src);
         x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
       } else {
-        const uint2 y = s[i].seg ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0, 0);
+        const uint2 y = *reinterpret_cast<const uint2 *>(src);
         x[i][0] = y.x, x[i][1] = y.y;
       }
     }
@@ -378,9 +376,8 @@ struct VUnits {
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const Spot s = spot(2 * c + f + 8 * p);
-            if (!s.seg) continue;
-            const uint4 x = *reinterpret_cast<const uint4 *>(s.seg + at + 16 * s.c());
-            mask[p] |= 0x00FF00FFu << (8 * f);
+            const uint4 x = *reinterpret_cast<const uint4 *>((s.seg ? s.seg : to) + at + 16 * s.c());
+            if (s.seg) mask[p] |= 0x00FF00FFu << (8 * f);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t w = s.p() ? word_of(x, 2 * h + 1) : word_of(x, 2 * h);
@@ -391,7 +388,8 @@ struct VUnits {
         uint4 *dst = reinterpret_cast<uint4 *>(to + at + 16 * c);
         if ((mask[0] & mask[1]) != 0xFFFFFFFFu) {
           const uint4 old = *dst;
-          y[0] |= old.x & ~mask[0], y[1] |= old.y & ~mask[1], y[2] |= old.z & ~mask[0], y[3] |= old.w & ~mask[1];
+          y[0] = merge_bytes(y[0], old.x, mask[0]), y[1] = merge_bytes(y[1], old.y, mask[1]);
+          y[2] = merge_bytes(y[2], old.z, mask[0]), y[3] = merge_bytes(y[3], old.w, mask[1]);
         }
         *dst = make_uint4(y[0], y[1], y[2], y[3]);
       } else {
@@ -404,13 +402,17 @@ struct VUnits {
       // scales, and D bytes on the minima of q5_1: block b of the tokens of one c, halves 2 p + f
       const int i = u - kCodes - kFifths, side = i / (4 * NB), c = i % (4 * NB) / NB, b = i % NB;
       const int at = (VF == MEMRA_KV_Q5_1 ? 10 : 8) * D + side * D + b * 8;
+      Spot s[4];
+      uint16_t x[4];
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const Spot s = spot(2 * c + (h & 1) + 8 * (h >> 1));
-        if (s.seg)
-          *reinterpret_cast<uint16_t *>(to + at + c * NB * 8 + 2 * h) =
-              *reinterpret_cast<const uint16_t *>(s.seg + at + s.c() * NB * 8 + 2 * (2 * s.p() + s.f()));
+        s[h] = spot(2 * c + (h & 1) + 8 * (h >> 1));
+        x[h] = *reinterpret_cast<const uint16_t *>((s[h].seg ? s[h].seg : to) + at + s[h].c() * NB * 8 +
+                                                   2 * (2 * s[h].p() + s[h].f()));
       }
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        if (s[h].seg) *reinterpret_cast<uint16_t *>(to + at + c * NB * 8 + 2 * h) = x[h];
     } else {
       const int i = u - kCodes - kFifths - kHalves, c = i / (D / 64), b4 = i % (D / 64);
       words<4>(to, c, 8 * D + b4 * 16, D / 4, spot);
@@ -418,7 +420,7 @@ struct VUnits {
   }
 };
 
-constexpr int kMovePages = 4;              // pages of a CTA at most
+constexpr int kMovePages = 8;              // pages of a CTA at most (16 x 8,192 tokens: 24 us, with 2 28, with 1 36)
 
 template <int D, int KF, int VF>
 struct MoveCfg {
@@ -429,7 +431,7 @@ struct MoveCfg {
 };
 
 template <int D, int KF, int VF>
-__global__ void __launch_bounds__(MoveCfg<D, KF, VF>::kThreads) evict_move_kernel(const EvictParams p, int pages) {
+__global__ void __launch_bounds__(MoveCfg<D, KF, VF>::kThreads, 1536 / MoveCfg<D, KF, VF>::kThreads) evict_move_kernel(const EvictParams p, int pages) {
   using C = MoveCfg<D, KF, VF>;
   __shared__ int s_page[kMovePages][kPage], s_token[kMovePages][kPage], s_to[kMovePages];
   grid_dependency_wait();
@@ -536,7 +538,8 @@ cudaError_t launch_select(const EvictParams &p, int64_t rows, int ranks, cudaStr
 cudaError_t launch_evict_select(const EvictParams &p, int sms, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.batch) * p.n_kv_heads;
   if (p.max_seq_len <= kThreads) return launch_select<1>(p, rows, 1, st);
-  // CTAs for the weights of one row: 4,096 of them each, as long as there are SMs
+  // CTAs for the weights of one row: 4,096 of them each, as long as there are SMs (16 x 8,192 weights of 4 heads 36 us so, 40
+  // with 16,384 to a CTA; one of 262,144 50 us in clusters of 16, 91 of 8; one of 512, by digits too, 12 us, by bits 8)
   int ranks = 1;
   while (ranks < kClusterMax && 4096ll * ranks < p.max_seq_len && 2 * ranks * rows <= 2 * sms) ranks *= 2;
   if (rows * ranks > INT32_MAX) return cudaErrorInvalidValue;
