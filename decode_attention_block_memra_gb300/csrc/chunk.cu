@@ -20,17 +20,17 @@ __global__ void __launch_bounds__(2 * D) chunk_merge_kernel(const ChunkParams p)
   if (warp == 0) {
     int pieces = 0;
     ChunkCut x{};
-    const int64_t head = chunk_head_cost(p, tpb, lane), all = head * p.n_kv_heads;
-    const int n = chunk_shares(p, head);
+    const int64_t head = chunk_head_cost<chunk_tiles(D)>(p, tpb, lane), all = head * p.n_kv_heads;
+    const int n = chunk_shares<chunk_tiles(D)>(p, head);
     if (head > 0 && c < n) {
-      x = chunk_cut(p, head, all * c / n, tpb, lane);
+      x = chunk_cut<chunk_tiles(D)>(p, head, all * c / n, tpb, lane);
       const int64_t before = all * (c - 1) / n - x.start;
-      if (x.k > 0 && x.k < x.steps && (before <= 0 || chunk_cut_step(before, x.steps) == 0)) {
+      if (x.k > 0 && x.k < x.steps && (before <= 0 || chunk_cut_step<chunk_tiles(D)>(before, x.steps, x.step) == 0)) {
         // the CTA before this cut has the block's head, the others a piece from their own cut on
         pieces = 2;
         for (int d = c + 1; d < n; ++d) {
           const int64_t off = all * d / n - x.start;
-          if (off >= x.cost || chunk_cut_step(off, x.steps) >= x.steps) break;
+          if (off >= x.cost || chunk_cut_step<chunk_tiles(D)>(off, x.steps, x.step) >= x.steps) break;
           ++pieces;
         }
       }

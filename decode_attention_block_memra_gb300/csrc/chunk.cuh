@@ -25,8 +25,14 @@ __host__ __device__ constexpr int kChunkFarCols(int D) { return D + (D == 128 ? 
 // its share, a part of one, whose rows it leaves as partial sums.  So the GPU is
 // evenly loaded whatever the lengths, one CTA to an SM, and no CTA leaves more
 // than two partial blocks.
-constexpr int kChunkFixed = 320;           // a block's fixed cost, in keys
-constexpr int kChunkShareMin = 512;        // least share of a CTA, in keys
+// A block's fixed cost, in keys (head_dim 128: 192 and 512 are within 4%; 256, chunks of 700, 1, 257 and 512 tokens that
+// see 1,024 keys: 48 us with 704, 52 with 320 or 1,024).
+__host__ __device__ constexpr int kChunkFixed(int tiles) { return tiles == 2 ? 320 : 704; }
+// Least share of a CTA, in keys: the fixed cost and three steps.
+__host__ __device__ constexpr int kChunkShareMin(int tiles) { return kChunkFixed(tiles) + 192; }
+// A step of a block that has one row tile where there is room for two costs half of another's (512 tokens beside 15 single
+// ones over 60,000 keys: 130 us; 138 with 3/4, 142 with 1, 152 with 3/8).
+constexpr int kChunkOneTileStep = kChunkKeys / 2;
 // A block is cut at least this many steps from either end.
 constexpr int kChunkSnap = 3;
 constexpr int kChunkCtasMax = 160;
@@ -94,20 +100,26 @@ __device__ __forceinline__ ChunkBlock chunk_block(const ChunkParams &p, const Ch
   return k;
 }
 
-// Cost of a sequence's blocks: kChunkFixed + 128 + min(A + (j + 1) tpb, M) for block
+// Cost of a sequence's blocks: the fixed cost + 128 + min(A + (j + 1) tpb, M) for block
 // j, which is more than its steps have keys, in a form that adds up without a loop.
+template <int TILES>
 struct ChunkCost {
-  int64_t A, M;
+  int64_t A, M, less;           // less: what the last block has not
   int tpb, blocks;
+  static constexpr int kFixed = kChunkFixed(TILES);
   __device__ __forceinline__ ChunkCost(const ChunkParams &p, const ChunkSeq &s, int tpb_) : tpb(tpb_) {
     blocks = s.n > 0 ? (s.n - 1) / tpb + 1 : 0;
     A = max(0, s.T - s.n);
     M = p.window > 0 ? static_cast<int64_t>(p.window) + tpb : INT64_MAX;
+    less = TILES == 2 && s.n - static_cast<int64_t>(blocks - 1) * tpb <= p.tpt ? min(A + static_cast<int64_t>(blocks) * tpb, M) / 2 : 0;
   }
+  // of a step of block j
+  __device__ __forceinline__ int step(int j) const { return less > 0 && j == blocks - 1 ? kChunkOneTileStep : kChunkKeys; }
   // of the first j blocks
   __device__ __forceinline__ int64_t upto(int j) const {
     const int64_t rising = M > A ? (M - A - 1) / tpb : 0, i = min(static_cast<int64_t>(j), rising);
-    return j * static_cast<int64_t>(kChunkFixed + 128) + i * A + tpb * (i * (i + 1) / 2) + (j - i ? (j - i) * M : 0);
+    return j * static_cast<int64_t>(kFixed + 128) + i * A + tpb * (i * (i + 1) / 2) + (j - i ? (j - i) * M : 0) -
+           (j == blocks ? less : 0);
   }
 };
 
@@ -115,23 +127,26 @@ struct ChunkCost {
 // from the block's first; k = 0: between blocks.
 struct ChunkCut {
   int h, b, j, k;
-  int steps;                    // of the block
+  int steps, step;              // of the block, and what one costs
   int64_t start, cost;          // of the block, on the line
 };
 
 // Steps of a block before a cut `off` behind its start: a block is cut only well inside.
-__device__ __forceinline__ int chunk_cut_step(int64_t off, int steps) {
-  const int64_t at = (off - kChunkFixed) / kChunkKeys;
-  const int k = off <= kChunkFixed ? 0 : static_cast<int>(min(at, static_cast<int64_t>(steps)));
+template <int TILES>
+__device__ __forceinline__ int chunk_cut_step(int64_t off, int steps, int step) {
+  constexpr int fixed = kChunkFixed(TILES);
+  const int64_t at = (off - fixed) / step;
+  const int k = off <= fixed ? 0 : static_cast<int>(min(at, static_cast<int64_t>(steps)));
   if (steps < 2 * kChunkSnap) return 2 * k > steps ? steps : 0;
   return k < kChunkSnap ? 0 : steps - k < kChunkSnap ? steps : k;
 }
 
 // Whole warp: the cost of one KV head's blocks.
+template <int TILES>
 __device__ __forceinline__ int64_t chunk_head_cost(const ChunkParams &p, int tpb, int lane) {
   int64_t sum = 0;
   for (int b = lane; b < p.batch; b += 32) {
-    const ChunkCost c(p, chunk_seq(p, b), tpb);
+    const ChunkCost<TILES> c(p, chunk_seq(p, b), tpb);
     sum += c.upto(c.blocks);
   }
 #pragma unroll
@@ -140,12 +155,14 @@ __device__ __forceinline__ int64_t chunk_head_cost(const ChunkParams &p, int tpb
 }
 
 // CTAs that share the line, and where the c-th share begins.
+template <int TILES>
 __device__ __forceinline__ int chunk_shares(const ChunkParams &p, int64_t head_cost) {
-  const int64_t want = head_cost * p.n_kv_heads / kChunkShareMin;
+  const int64_t want = head_cost * p.n_kv_heads / kChunkShareMin(TILES);
   return static_cast<int>(max(static_cast<int64_t>(1), min(want, static_cast<int64_t>(p.ctas))));
 }
 
 // Whole warp: the cut at `pos` of the line (0 <= pos < n_kv_heads * head_cost).
+template <int TILES>
 __device__ __forceinline__ ChunkCut chunk_cut(const ChunkParams &p, int64_t head_cost, int64_t pos, int tpb, int lane) {
   ChunkCut c{};
   c.h = static_cast<int>(pos / head_cost);
@@ -155,7 +172,7 @@ __device__ __forceinline__ ChunkCut chunk_cut(const ChunkParams &p, int64_t head
     const int b = b0 + lane;
     int64_t mine = 0;
     if (b < p.batch) {
-      const ChunkCost cost(p, chunk_seq(p, b), tpb);
+      const ChunkCost<TILES> cost(p, chunk_seq(p, b), tpb);
       mine = cost.upto(cost.blocks);
     }
     int64_t incl = mine;
@@ -176,7 +193,7 @@ __device__ __forceinline__ ChunkCut chunk_cut(const ChunkParams &p, int64_t head
     start += __shfl_sync(0xffffffffu, incl, 31);
   }
   const ChunkSeq s = chunk_seq(p, c.b);
-  const ChunkCost cost(p, s, tpb);
+  const ChunkCost<TILES> cost(p, s, tpb);
   int lo = 0, hi = cost.blocks;              // upto(lo) <= rest < upto(hi)
   while (hi - lo > 1) {
     const int mid = lo + (hi - lo) / 2;
@@ -187,7 +204,8 @@ __device__ __forceinline__ ChunkCut chunk_cut(const ChunkParams &p, int64_t head
   c.cost = cost.upto(lo + 1) - cost.upto(lo);
   const ChunkBlock k = chunk_block(p, s, lo, tpb);
   c.steps = max(0, k.hi - k.lo);
-  c.k = chunk_cut_step(rest - cost.upto(lo), c.steps);
+  c.step = cost.step(lo);
+  c.k = chunk_cut_step<TILES>(rest - cost.upto(lo), c.steps, c.step);
   return c;
 }
 

@@ -195,18 +195,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
   grid_dependency_wait();
   allow_dependent_launch();
   if (warp == 0) {
-    const int64_t head = chunk_head_cost(p, tpb, lane);
-    const int n = chunk_shares(p, head), c = blockIdx.x;
+    const int64_t head = chunk_head_cost<C::kTiles>(p, tpb, lane);
+    const int n = chunk_shares<C::kTiles>(p, head), c = blockIdx.x;
     ChunkShare mine{0, 0, 0, 0, -1, 0, 0, 0};          // none
     if (head > 0 && c < n) {
       const int64_t all = head * p.n_kv_heads;
       if (c > 0) {
-        const ChunkCut x = chunk_cut(p, head, all * c / n, tpb, lane);
+        const ChunkCut x = chunk_cut<C::kTiles>(p, head, all * c / n, tpb, lane);
         mine.h0 = x.h, mine.b0 = x.b, mine.j0 = x.j, mine.k0 = x.k;
       }
       mine.h1 = p.n_kv_heads;
       if (c + 1 < n) {
-        const ChunkCut x = chunk_cut(p, head, all * (c + 1) / n, tpb, lane);
+        const ChunkCut x = chunk_cut<C::kTiles>(p, head, all * (c + 1) / n, tpb, lane);
         mine.h1 = x.h, mine.b1 = x.b, mine.j1 = x.j, mine.k1 = x.k;
       }
     }
