@@ -31,7 +31,7 @@ __host__ __device__ constexpr int kChunkFixed(int tiles) { return tiles == 2 ? 3
 // Least share of a CTA, in keys: the fixed cost and three steps.
 __host__ __device__ constexpr int kChunkShareMin(int tiles) { return kChunkFixed(tiles) + 192; }
 // A step of a block that has one row tile where there is room for two costs half of another's (512 tokens beside 15 single
-// ones over 60,000 keys: 130 us; 138 with 3/4, 142 with 1, 152 with 3/8).
+// ones over 60,000 keys: 130 us; 138 with 3/4, 143 with 1, 151 with 3/8).
 constexpr int kChunkOneTileStep = kChunkKeys / 2;
 // A block is cut at least this many steps from either end.
 constexpr int kChunkSnap = 3;

@@ -40,9 +40,9 @@ namespace {
 constexpr float kLazy = 8.f;               // log2 units: P stays <= 256 between rescales
 constexpr int kSumUnits = 120;             // chunks of one sum of the tensor cores: 7,680 keys
 
-// Where a CTA's share of the line begins and ends.
-struct ChunkShare {
-  int h0, b0, j0, k0, h1, b1, j1, k1;
+// Where a CTA's share of the line begins, or ends.
+struct ChunkPlace {
+  int h, b, j, k;
 };
 
 // A block, or the part of one, that a CTA takes.  The copy warp finds them one
@@ -63,8 +63,8 @@ struct ChunkWalk {
   const ChunkParams &p;
   int h, b, j, k, h1, b1, j1, k1, tpb, seen;
   ChunkSeq s;
-  __device__ __forceinline__ ChunkWalk(const ChunkParams &p_, const ChunkShare &c, int tpb_)
-      : p(p_), h(c.h0), b(c.b0), j(c.j0), k(c.k0), h1(c.h1), b1(c.b1), j1(c.j1), k1(c.k1), tpb(tpb_), seen(-1) {}
+  __device__ __forceinline__ ChunkWalk(const ChunkParams &p_, const ChunkPlace &from, const ChunkPlace &to, int tpb_)
+      : p(p_), h(from.h), b(from.b), j(from.j), k(from.k), h1(to.h), b1(to.b), j1(to.j), k1(to.k), tpb(tpb_), seen(-1) {}
   __device__ __forceinline__ bool next(ChunkPiece &x) {
     while (true) {
       if (h > h1 || (h == h1 && (b > b1 || (b == b1 && (j > j1 || (j == j1 && k >= k1)))))) return false;
@@ -189,32 +189,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
   ChunkPiece *pieces = reinterpret_cast<ChunkPiece *>(smem + C::kOffPiece);
   // a byte for each chunk in flight: the pages that exist
   volatile uint8_t *page_mask = smem + C::kOffMask;
-  ChunkShare *share = reinterpret_cast<ChunkShare *>(smem + C::kOffCut);
+  ChunkPlace *share = reinterpret_cast<ChunkPlace *>(smem + C::kOffCut);
   const int tpb = C::kTiles * p.tpt;
 
-  grid_dependency_wait();
-  allow_dependent_launch();
-  if (warp == 0) {
-    const int64_t head = chunk_head_cost<C::kTiles>(p, tpb, lane);
-    const int n = chunk_shares<C::kTiles>(p, head), c = blockIdx.x;
-    ChunkShare mine{0, 0, 0, 0, -1, 0, 0, 0};          // none
-    if (head > 0 && c < n) {
-      const int64_t all = head * p.n_kv_heads;
-      if (c > 0) {
-        const ChunkCut x = chunk_cut<C::kTiles>(p, head, all * c / n, tpb, lane);
-        mine.h0 = x.h, mine.b0 = x.b, mine.j0 = x.j, mine.k0 = x.k;
-      }
-      mine.h1 = p.n_kv_heads;
-      if (c + 1 < n) {
-        const ChunkCut x = chunk_cut<C::kTiles>(p, head, all * (c + 1) / n, tpb, lane);
-        mine.h1 = x.h, mine.b1 = x.b, mine.j1 = x.j, mine.k1 = x.k;
-      }
-    }
-    if (lane == 0) *share = mine;
-    if (c == 0)                                        // one CTA checks every length
-      for (int b = lane; b < p.batch; b += 32)
-        if (chunk_seq(p, b).bad) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
-  } else if (warp == C::kCopyWarp) {
+  if (warp == C::kCopyWarp) {
     if (lane == 0) {
       for (int s = 0; s < RAW; ++s) {
         mbar_init(raw_full(s), 1);
@@ -241,6 +219,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
     tc::tmem_alloc(smem_addr(tmem_slot), C::kTCols);
     tc::tmem_relinquish();
   }
+  grid_dependency_wait();
+  allow_dependent_launch();
+  if (warp < 2) {                                      // the share's two ends, by a warp each
+    const int64_t head = chunk_head_cost<C::kTiles>(p, tpb, lane);
+    const int n = chunk_shares<C::kTiles>(p, head), c = blockIdx.x + warp;
+    const bool some = head > 0 && static_cast<int>(blockIdx.x) < n;
+    ChunkPlace at{warp == 0 ? 0 : some ? p.n_kv_heads : -1, 0, 0, 0};
+    if (some && c > 0 && c < n) {
+      const ChunkCut x = chunk_cut<C::kTiles>(p, head, head * p.n_kv_heads * c / n, tpb, lane);
+      at = ChunkPlace{x.h, x.b, x.j, x.k};
+    }
+    if (lane == 0) share[warp] = at;
+  } else if (warp == 2 && blockIdx.x == 0) {           // one CTA checks every length
+    for (int b = lane; b < p.batch; b += 32)
+      if (chunk_seq(p, b).bad) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -265,7 +259,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
     const int cp_page = lane >> 1;
     const bool cp_v = lane & 1;
     const uint32_t cp_bytes = cp_v ? C::kVSeg : C::kKSeg;
-    ChunkWalk walk(p, *share, tpb);
+    ChunkWalk walk(p, share[0], share[1], tpb);
     ChunkPiece x;
     while (ok) {
       const bool more = walk.next(x);
@@ -725,7 +719,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
     }
     if (!ok) {
       // A wait gave up: every row of the CTA's share becomes NaN.
-      ChunkWalk walk(p, *share, tpb);
+      ChunkWalk walk(p, share[0], share[1], tpb);
       ChunkPiece x;
       while (walk.next(x)) {
         const int tile = x.tiles == 2 ? g : 0, t = tile * p.tpt + tl;

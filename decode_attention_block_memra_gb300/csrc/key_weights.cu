@@ -15,11 +15,17 @@
 //   * a load warp brings row tiles of Q by TMA; where all rows of the chunk
 //     fit their ring, once for all keys of a CTA's run;
 //   * an MMA thread for each key tile: S^T = K^ Q^T, two key tiles beside one another for
-//     each row tile (one thread for both took longer to issue than the MMAs run);
+//     each row tile (one thread for both took longer to issue than the MMAs run: 205 us);
 //   * four groups of four warps, two for each key tile, which take its row tiles by
 //     turns: thread = key (at head_dim 256 with q8_0 there is room for one tile of
-//     K^, and two groups).  A row tile takes a group about 3,000 clocks, the tensor cores
-//     1,024 (one group to a tile: 64 tokens over 262,144 keys 252 us).
+//     K^, and two groups).
+// Row tiles have 128 rows (64 at head_dim 256).  With many rows the epilogue bounds it, an exponential for
+// every score: 64 tokens of 32 heads over 262,144 keys of 4, q8_0, take 183 us, 35% of the rate of
+// the tensor cores' fp16 products (one group to a key tile: 252).  With few, each key is staged
+// for a handful of rows: tiles of 32 rows then, 16 staging warps, one group to a key tile.  8 sequences
+// of one token over 6,316 keys each take 19 us, 23 in tiles of 128 (and those 64 tokens 379 us in tiles of 32).
+// Of the 19 some 5 pass before the first page is there; then a tile is staged in 1,300 clocks, and 28 MB
+// arrive in 10 us.
 // The (key tile, KV head, sequence) items of the call lie behind one another on a line
 // that the CTAs, one to an SM, share by their cost.
 #include <algorithm>
@@ -151,10 +157,14 @@ template <int D, int KF, int N>
 struct WeightCfg {
   static constexpr bool kKLo = KF == MEMRA_KV_Q8_0;
   static constexpr int kRows = N;          // query rows of a tile
-  // Keys of a raw chunk: at 32, a staging warp has two loads in flight and the waits around them; 64 where they fit.
-  static constexpr int kStepKeys = D == 128 ? 64 : 32, kTileSteps = kWeightKeys / kStepKeys;
-  static constexpr int kTiles = D == 256 && kKLo ? 1 : 2;       // tiles of K^, with two groups of the epilogue each
-  static constexpr int kStageWarp0 = 8 * kTiles, kMmaWarp = kStageWarp0 + 8, kLoadWarp = kMmaWarp + kTiles;
+  // Few rows: a key tile's time is its staging, so that twice as many warps stage, and one group takes its row tiles.
+  static constexpr bool kFew = N == kWeightRowsFew;
+  static constexpr int kStageWarps = kFew ? 16 : 8, kGroups = kFew ? 1 : 2;     // groups of the epilogue to a tile of K^
+  // Keys of a raw chunk: as many as fit, for the loads that a staging warp has in flight between two waits.
+  static constexpr int kStepKeys = (D == 128 ? 64 : 32) * (kFew ? 2 : 1), kTileSteps = kWeightKeys / kStepKeys;
+  static constexpr int kTiles = D == 256 && kKLo ? 1 : 2;       // tiles of K^
+  static constexpr int kEpilogue = 128 * kGroups * kTiles;      // threads
+  static constexpr int kStageWarp0 = kEpilogue / 32, kMmaWarp = kStageWarp0 + kStageWarps, kLoadWarp = kMmaWarp + kTiles;
   static constexpr int kCopyWarp = kLoadWarp + 1, kThreads = 32 * (kCopyWarp + 1);
   static constexpr int kPages = kStepKeys / kPage;
   static constexpr int kKSeg = k_seg_bytes(KF, D);
@@ -168,7 +178,8 @@ struct WeightCfg {
   static constexpr uint32_t kOffSum = kOffLse + 4096, kOffK = kOffSum + 2048;
   static constexpr uint32_t kOffQ = kOffK + kTiles * kKBuf;
   // (two raw chunks at least beside the row tiles)
-  static constexpr int kQBufs = (kRoom - 1024 - kOffQ - 2 * kRawBytes) / kQBuf < 4 ? (kRoom - 1024 - kOffQ - 2 * kRawBytes) / kQBuf : 4;
+  static constexpr int kQMost = kFew ? 2 : 4, kQFit = (kRoom - 1024 - kOffQ - 2 * kRawBytes) / kQBuf;
+  static constexpr int kQBufs = kQFit < kQMost ? kQFit : kQMost;
   static constexpr uint32_t kOffRaw = kOffQ + kQBufs * kQBuf;
   static constexpr int kRaw = (kRoom - 1024 - kOffRaw) / kRawBytes < 8 ? (kRoom - 1024 - kOffRaw) / kRawBytes : 8;
   static constexpr uint32_t kTCols = 512, kNeed = kOffRaw + kRaw * kRawBytes + 1024, kFloor = 150 * 1024;      // (1024: aligning the base)
@@ -194,7 +205,7 @@ template <int D, int KF, int N>
 __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap qmap, const WeightParams p) {
   using C = WeightCfg<D, KF, N>;
-  constexpr int G = C::kTiles, NP = C::kPages, RAW = C::kRaw, QB = C::kQBufs;
+  constexpr int G = C::kTiles, GP = C::kGroups, SW = C::kStageWarps, NP = C::kPages, RAW = C::kRaw, QB = C::kQBufs;
   constexpr int kStepKeys = C::kStepKeys, kTileSteps = C::kTileSteps;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -206,29 +217,14 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
   WeightPlace *share = reinterpret_cast<WeightPlace *>(smem + C::kOffShare);
   WeightPiece *pieces = reinterpret_cast<WeightPiece *>(smem + C::kOffPiece);
 
-  grid_dependency_wait();
-  allow_dependent_launch();
-  if (warp == 0) {
-    const int64_t head = weight_head_cost(p, lane), all = head * p.n_kv_heads;
-    const int c = blockIdx.x, n = p.ctas;
-    WeightPlace from{0, 0, 0}, to{-1, 0, 0};           // none
-    if (head > 0) {
-      if (c > 0) from = weight_place(p, head, all * c / n, lane);
-      to = WeightPlace{p.n_kv_heads, 0, 0};
-      if (c + 1 < n) to = weight_place(p, head, all * (c + 1) / n, lane);
-    }
-    if (lane == 0) share[0] = from, share[1] = to;
-    if (c == 0)                                        // one CTA checks every length
-      for (int b = lane; b < p.batch; b += 32)
-        if (weight_seq(p, b).bad) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
-  } else if (warp == C::kCopyWarp) {
+  if (warp == C::kCopyWarp) {
     if (lane == 0) {
       for (int i = 0; i < RAW; ++i) {
         mbar_init(bar(C::kRawFull, i), 1);
-        mbar_init(bar(C::kRawEmpty, i), 8);
+        mbar_init(bar(C::kRawEmpty, i), SW);
       }
       for (int i = 0; i < 2; ++i) {
-        mbar_init(bar(C::kKFull, i), 8);
+        mbar_init(bar(C::kKFull, i), SW);
         mbar_init(bar(C::kKFree, i), 1);
       }
       for (int i = 0; i < QB; ++i) {
@@ -249,6 +245,19 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
   } else if (warp == C::kMmaWarp) {
     tc::tmem_alloc(smem_addr(tmem_slot), C::kTCols);
     tc::tmem_relinquish();
+  }
+  grid_dependency_wait();
+  allow_dependent_launch();
+  // The share's two ends, by a warp each.
+  if (warp < 2) {
+    const int64_t head = weight_head_cost(p, lane), all = head * p.n_kv_heads;
+    const int c = blockIdx.x + warp, n = p.ctas;
+    WeightPlace at = warp == 0 ? WeightPlace{0, 0, 0} : WeightPlace{head > 0 ? p.n_kv_heads : -1, 0, 0};
+    if (head > 0 && c > 0 && c < n) at = weight_place(p, head, all * c / n, lane);
+    if (lane == 0) share[warp] = at;
+  } else if (warp == 2 && blockIdx.x == 0) {           // one CTA checks every length
+    for (int b = lane; b < p.batch; b += 32)
+      if (weight_seq(p, b).bad) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -447,7 +456,7 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
           if (ok) ok = mbar_wait_suspended(bar(C::kRawFull, s), (cc / RAW) & 1, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          stage_k<D, KF, kStepKeys, 8, kWeightKeys>(sb + C::kOffRaw + s * C::kRawBytes,
+          stage_k<D, KF, kStepKeys, SW, kWeightKeys>(sb + C::kOffRaw + s * C::kRawBytes,
                                                     sb + C::kOffK + g * C::kKBuf + i * kStepKeys * 128, sw, lane);
           fence_proxy_async();               // K^ for the tensor cores, the raw chunk for the next copies
           __syncwarp();
@@ -459,7 +468,7 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
   } else {
     // --------------------------------------------------------------- epilogue --
     // Group, its tile of K^ and which of the tile's units it takes, key of the tile.
-    const int group = warp >> 2, g = group >> 1, turn = group & 1, kl = tid & 127;
+    const int group = warp >> 2, g = group / GP, turn = group % GP, kl = tid & 127;
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     float *const lse_all = reinterpret_cast<float *>(smem + C::kOffLse), *const lse_two = lse_all + group * 2 * N;
     float *const half_s = reinterpret_cast<float *>(smem + C::kOffSum) + g * 2 * kWeightKeys + kl;
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
     int sn = 0, cc = 0, tn = 0;              // units of this tile of K^ so far, raw chunks, tiles
     while (true) {
       const volatile WeightPiece *x = next_piece();
-      ok = named_barrier_and(7, 256 * G, ok);          // all groups go on together, or none
+      ok = named_barrier_and(7, C::kEpilogue, ok);          // all groups go on together, or none
       if (!ok || x->tiles < 0) break;
       const int tiles = x->tiles, rts = x->row_tiles, n = x->n, T = x->T, tile0 = x->tile0;
       float *const row = p.weights + (static_cast<int64_t>(x->b) * p.n_kv_heads + x->h) * p.weight_stride;
@@ -482,25 +491,25 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
       const int run_low = weight_first_row_tile(p, n, T, tile0 * kWeightKeys);
       const bool cached = (rts - run_low) * N <= kLseRows;
       if (cached) {
-        for (int i = tid; i < (rts - run_low) * N; i += 256 * G) lse_all[i] = lse_of(run_low + i / N, i % N);
-        named_barrier_sync(7, 256 * G);
+        for (int i = tid; i < (rts - run_low) * N; i += C::kEpilogue) lse_all[i] = lse_of(run_low + i / N, i % N);
+        named_barrier_sync(7, C::kEpilogue);
       }
       for (int t = g; t < tiles; t += G, ++tn) {
         const int key = (tile0 + t) * kWeightKeys + kl;
         const int low = weight_first_row_tile(p, n, T, (tile0 + t / G * G) * kWeightKeys);
-        int rt = low + ((sn ^ turn) & 1);              // this group's first
+        int rt = low + (GP == 2 ? (sn ^ turn) & 1 : 0);          // this group's first
         float old = 0.f, next = 0.f, sum = 0.f;
         if (p.keep != 0.f && key < T) old = row[key];
         if (!cached && kl < N) next = lse_of(rt, kl);
-        for (; rt < rts && ok; rt += 2) {
-          const int nth = sn + rt - low, sbuf = 2 * g + turn;      // the unit's number
+        for (; rt < rts && ok; rt += GP) {
+          const int nth = sn + rt - low, sbuf = 2 * g + (nth & 1);     // the unit's number
           const int live = rows_of(rt, n);
           const float *lse = lse_all + (rt - run_low) * N;
           if (!cached) {
-            float *const mine = lse_two + (nth >> 1 & 1) * N;
+            float *const mine = lse_two + (nth / GP & 1) * N;
             if (kl < N) {
               mine[kl] = next;
-              next = lse_of(rt + 2, kl);
+              next = lse_of(rt + GP, kl);
             }
             lse = mine;
           }
@@ -555,8 +564,8 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
         }
         // A tile of one unit is its group's; else the groups' sums are joined.
         const int units = rts - low;
-        const bool mine = units > 1 ? turn == 0 : ((sn ^ turn) & 1) == 0;
-        if (units > 1) {
+        const bool mine = GP == 1 || (units > 1 ? turn == 0 : ((sn ^ turn) & 1) == 0);
+        if (GP == 2 && units > 1) {
           float *const half = half_s + (tn & 1) * kWeightKeys;
           if (turn == 1) *half = sum;
           ok = named_barrier_and(5 + g, 256, ok);
