@@ -13,14 +13,16 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 int chunk_ctas() { return std::min(device_sms(), kChunkCtasMax); }
 
-// Float32 rows: two partial blocks of each CTA and what earlier sums of its block came to; the partials' log-sum-exp.
+// Float32 rows: two partial blocks of each CTA and what earlier sums of its block came to; the partials' log-sum-exp;
+// what the merge joins.
 struct Workspace {
-  size_t lse, far, bytes;
+  size_t lse, far, merges, bytes;
   Workspace(int head_dim) {
     const size_t rows = static_cast<size_t>(kChunkCtasMax) * chunk_tiles(head_dim) * kChunkRows;
     lse = 2 * rows * head_dim * sizeof(float);
     far = lse + 2 * rows * sizeof(float);
-    bytes = far + rows * kChunkFarCols(head_dim) * sizeof(float);
+    merges = far + rows * kChunkFarCols(head_dim) * sizeof(float);
+    bytes = merges + kChunkCtasMax * sizeof(int4);
   }
 };
 
@@ -59,6 +61,9 @@ int chunk_attn(const memra_kv_cache *cache, const void *q, int64_t q_stride, con
   p.o_part = reinterpret_cast<float *>(w);
   p.lse_part = reinterpret_cast<float *>(w + ws.lse);
   p.far = reinterpret_cast<float *>(w + ws.far);
+  // Blocks of fewer steps than this are never cut: no merge.
+  const bool merged = max_seq_len > (2 * kChunkSnap - 1) * kChunkKeys;
+  p.merges = merged ? reinterpret_cast<int4 *>(w + ws.merges) : nullptr;
   p.status = cache->status;
   p.batch = batch;
   p.total = total_tokens;
@@ -80,8 +85,7 @@ int chunk_attn(const memra_kv_cache *cache, const void *q, int64_t q_stride, con
   p.test_extra_tx = test_extra_tx;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = cuda_status(launch_chunk(head_dim, cache->k_fmt, cache->v_fmt, p, s));
-  // Blocks of fewer steps than this are never cut: no merge.
-  if (st || max_seq_len <= (2 * kChunkSnap - 1) * kChunkKeys) return st;
+  if (st || !merged) return st;
   return cuda_status(launch_chunk_merge(head_dim, p, s));
 }
 

@@ -6,50 +6,20 @@
 namespace memra {
 namespace {
 
-// CTA = 32 rows of a cut block, warp = 16 columns, thread = row.  The block is
-// found from the cut between two CTAs' shares; the CTA of its first cut merges it,
-// the pieces in their order along the keys.
+// CTA = 32 rows of a cut block, warp = 16 columns, thread = row.  The CTA of the
+// block's first cut merges it, the pieces in their order along the keys.
 template <int D>
 __global__ void __launch_bounds__(2 * D) chunk_merge_kernel(const ChunkParams p) {
-  constexpr int kRows = chunk_tiles(D) * kChunkRows, kSides = kRows / 32, BATCH = 4;
-  __shared__ ChunkCut s_cut;
-  __shared__ int s_pieces;
+  constexpr int kRows = chunk_tiles(D) * kChunkRows, kSides = kRows / 32, BATCH = 2;
   const int c = 1 + blockIdx.x / kSides, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part_row = blockIdx.x % kSides * 32 + lane, tpb = chunk_tiles(D) * p.tpt;
-  allow_dependent_launch();
-  if (warp == 0) {
-    int pieces = 0;
-    ChunkCut x{};
-    const int64_t head = chunk_head_cost<chunk_tiles(D)>(p, tpb, lane), all = head * p.n_kv_heads;
-    const int n = chunk_shares<chunk_tiles(D)>(p, head);
-    if (head > 0 && c < n) {
-      x = chunk_cut<chunk_tiles(D)>(p, head, all * c / n, tpb, lane);
-      const int64_t before = all * (c - 1) / n - x.start;
-      if (x.k > 0 && x.k < x.steps && (before <= 0 || chunk_cut_step<chunk_tiles(D)>(before, x.steps, x.step) == 0)) {
-        // the CTA before this cut has the block's head, the others a piece from their own cut on
-        pieces = 2;
-        for (int d = c + 1; d < n; ++d) {
-          const int64_t off = all * d / n - x.start;
-          if (off >= x.cost || chunk_cut_step<chunk_tiles(D)>(off, x.steps, x.step) >= x.steps) break;
-          ++pieces;
-        }
-      }
-    }
-    if (lane == 0) {
-      s_cut = x;
-      s_pieces = pieces;
-    }
-  }
-  __syncthreads();
-  const int pieces = s_pieces;
-  if (pieces == 0) return;
-  const ChunkSeq s = chunk_seq(p, s_cut.b);
-  const ChunkBlock block = chunk_block(p, s, s_cut.j, tpb);
+  const int part_row = blockIdx.x % kSides * 32 + lane;
   const int rl = part_row % kChunkRows, tl = rl / p.group;
-  const int t = block.t0 + part_row / kChunkRows * p.tpt + tl;
-  const bool live = tl < p.tpt && t < block.t1;
-  if (!__any_sync(0xffffffffu, live)) return;
   grid_dependency_wait();                    // the partial blocks are complete
+  allow_dependent_launch();
+  const int4 merge = p.merges[c];
+  const int pieces = merge.x, t = part_row / kChunkRows * p.tpt + tl;       // the row's token in the block
+  const bool live = tl < p.tpt && t < merge.w;
+  if (pieces == 0 || !__any_sync(0xffffffffu, live)) return;
   float mw = -INFINITY, L = 0.f, acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
@@ -89,7 +59,7 @@ __global__ void __launch_bounds__(2 * D) chunk_merge_kernel(const ChunkParams p)
   }
   if (!live) return;
   const float inv = L != 0.f ? 1.f / L : 0.f;          // (0: no visible key; a NaN stays one)
-  const int64_t row = static_cast<int64_t>(s.first + t) * p.n_heads + s_cut.h * p.group + rl % p.group;
+  const int64_t row = static_cast<int64_t>(merge.z + t) * p.n_heads + merge.y * p.group + rl % p.group;
   uint4 *to = reinterpret_cast<uint4 *>(p.out + row * D + 16 * warp);
 #pragma unroll
   for (int e = 0; e < 16; e += 8)

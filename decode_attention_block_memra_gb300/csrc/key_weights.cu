@@ -20,8 +20,8 @@
 //     turns: thread = key (at head_dim 256 with q8_0 there is room for one tile of
 //     K^, and two groups).
 // Row tiles have 128 rows (64 at head_dim 256).  With many rows the epilogue bounds it, an exponential for
-// every score: 64 tokens of 32 heads over 262,144 keys of 4, q8_0, take 183 us, 35% of the rate of
-// the tensor cores' fp16 products (one group to a key tile: 252).  With few, each key is staged
+// every score: 64 tokens of 32 heads over 262,144 keys of 4, q8_0, take 183 us, 78% of the rate of
+// the tensor cores' fp16 products, pairs counted (one group to a key tile: 252).  With few, each key is staged
 // for a handful of rows: tiles of 32 rows then, 16 staging warps, one group to a key tile.  8 sequences
 // of one token over 6,316 keys each take 19 us, 23 in tiles of 128 (and those 64 tokens 379 us in tiles of 32).
 // Of the 19 some 5 pass before the first page is there; then a tile is staged in 1,300 clocks, and 28 MB
