@@ -25,7 +25,7 @@
 // at every step, so an O takes kSumUnits chunks at most; then it is added to a
 // float32 row in the workspace.
 //
-// What it measured (q8_0/q5_1, D 128, 32/4 heads).  2,048 tokens behind 30,000: 1.39 ms, 79% of the tensor
+// What it measured (q8_0/q5_1, D 128, 32/4 heads).  2,048 tokens behind 30,000: 1.39 ms, 78% of the tensor
 // cores' rate counting the pairs' products; a step of two row tiles takes 3,500 clocks, 2,112 of them
 // MMAs, the rest the chain from a score to its P and the next score over it, which two groups
 // do not quite hide.  512 tokens beside 15 single ones over 60,000 keys: 115 us.  One token over 255

@@ -2,7 +2,7 @@
  * memra_testing.h - test hooks of the decode library (libmemra.so), not part
  * of the decode ABI in memra.h.  The memra pages have no counterpart: they
  * exist so that a test can drive, on a real GPU, the path that every
- * pipeline wait of the decode split kernel, of prompt attention and of tree
+ * pipeline wait of the decode split kernel, of prompt, tree and chunk
  * attention takes when it runs out, and check the quantizer's division-free
  * quotient against the IEEE one.
  *
