@@ -11,7 +11,7 @@
 // falls to one side or the other by its last bits: in float32 some five codes of 8
 // million differ from exact arithmetic's, so keys, a small part of the rows, are carried
 // as unevaluated sums of two floats from the sum of squares to the rounding, and none did
-// (16,384 tokens of 16 and 2 heads, D 256, fp8 cache: 84 us, 77 with keys in float32).
+// (16,384 tokens of 16 and 2 heads, D 256, fp8 cache: 86 us, 77 with keys in float32).
 //
 // Angles.  position * inv_freq reaches 10^5 and more radians, where float32 has no
 // digits left behind the point.  So a frequency is kept in turns (inv_freq / 2 pi)
@@ -27,7 +27,7 @@
 // flight throughout.
 //
 // Bound by bytes with many tokens, and by the arithmetic of the keys and of the quantizers
-// beside them: those 16,384 tokens move 319 MB in 84 us, 3.8 TB/s (queries alone: 268 MB in
+// beside them: those 16,384 tokens move 319 MB in 86 us, 3.7 TB/s (queries alone: 268 MB in
 // 54 us, 5.0 TB/s); 2,048 tokens of 32 and 4 heads, D 128, no cache: 38 MB in
 // 15.6 us.  With few, by
 // the chain of one row: a launch of 8 tokens takes 5 us.
@@ -67,6 +67,12 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 __device__ __forceinline__ Two mul(Two a, Two b) {
   const Two p = two_prod(a.hi, b.hi);
   return {p.hi, fmaf(a.hi, b.lo, fmaf(a.lo, b.hi, p.lo))};
+}
+
+// The sum rounded; where a part is infinite or NaN, what float32 alone gives.
+__device__ __forceinline__ float rounded(Two a) {
+  const float y = a.hi + a.lo;
+  return y == y ? y : a.hi;
 }
 
 // 1 / sqrt(a): an approximation y and one Newton step, y + y (1 - a y^2) / 2, whose correction is the low part.
@@ -243,10 +249,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
     // a cosine + b sine
     auto turn = [&](Two a, Two b, int j, float s) {
       const Two t = add(mul(a, {table[1][j], table[3][j]}), mul(b, {s * table[0][j], s * table[2][j]}));
-      return t.hi + t.lo;
+      return rounded(t);
     };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = v[i].hi + v[i].lo;
+    for (int i = 0; i < 8; ++i) x[i] = rounded(v[i]);
     if (p.half && p.interleaved) {
       if (turned) {
 #pragma unroll

@@ -197,6 +197,14 @@ def test_captured_and_replayed(memra):
     c.check(1.0)
 
 
+@pytest.mark.parametrize("kf,D", [("q8_0", 128), ("fp8", 128), ("q8_0", 256), ("nvfp4", 256)])
+def test_a_chunk_among_many_single_tokens(memra, kf, D):
+    """On average few rows a sequence, so that row tiles are small; one sequence has more than the ring and the kept log-sum-exps hold."""
+    c = Weights(memra, kf, "q5_1", D, 8, 1, [1] * 31 + [140] + [1] * 32, [100] * 31 + [300] + [20] * 32, seed=D)
+    assert c.call(0.5) == 0
+    c.check(0.5)
+
+
 def test_thousands_of_calls_in_a_row(memra):
     cases = [Weights(memra, kf, "q5_1", D, 8, 2, [70, 1, 9], [500, 1200, 0], seed=D)
              for D in (128, 256) for kf in ("q8_0", "fp8")]

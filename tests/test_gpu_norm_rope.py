@@ -122,6 +122,21 @@ def test_large_and_small_rows(memra):
     assert not q_out[4].any()
 
 
+@pytest.mark.parametrize("norm,rotary,interleaved", [(False, 128, False), (False, 32, True), (False, 0, False), (True, 128, False),
+                                                     (True, 0, True)])
+def test_infinite_and_nan_elements_of_keys_as_of_queries(memra, norm, rotary, interleaved):
+    rows, pos, freq, qw, _ = case(8, 1, 1, 128, rotary, positions=np.arange(8) * 1000)
+    for t, x in enumerate((np.inf, -np.inf, np.nan, 65504.0)):
+        rows[t, :, 5] = x
+        rows[t + 4, :, [5, 69, 120]] = x
+    x, w = dev(rows), dev(qw) if norm else None
+    q_out, k_out = (torch.empty(8, 1, 128, dtype=torch.float16, device="cuda") for _ in range(2))
+    memra.qk_norm_rope(x[:, :1], x[:, :1], dev(pos), None if freq is None else dev(freq), q_out, k_out, w, w, EPS, interleaved)
+    assert torch.equal(q_out.isnan(), k_out.isnan())
+    assert torch.equal(q_out.isinf(), k_out.isinf()) and torch.equal(q_out[q_out.isinf()], k_out[q_out.isinf()])
+    assert q_out.isnan()[2].any() and not q_out.isnan()[3].any() and (norm or q_out.isinf()[0].any())
+
+
 PAIRS = [("q8_0", "q5_1"), ("q8_0", "q4_0"), ("fp8", "fp8"), ("nvfp4", "nvfp4"), ("fp8", "q5_1"), ("nvfp4", "q4_0")]
 
 
