@@ -61,9 +61,7 @@ int chunk_attn(const memra_kv_cache *cache, const void *q, int64_t q_stride, con
   p.o_part = reinterpret_cast<float *>(w);
   p.lse_part = reinterpret_cast<float *>(w + ws.lse);
   p.far = reinterpret_cast<float *>(w + ws.far);
-  // Blocks of fewer steps than this are never cut: no merge.
-  const bool merged = max_seq_len > (2 * kChunkSnap - 1) * kChunkKeys;
-  p.merges = merged ? reinterpret_cast<int4 *>(w + ws.merges) : nullptr;
+  p.merges = reinterpret_cast<int4 *>(w + ws.merges);
   p.status = cache->status;
   p.batch = batch;
   p.total = total_tokens;
@@ -85,7 +83,8 @@ int chunk_attn(const memra_kv_cache *cache, const void *q, int64_t q_stride, con
   p.test_extra_tx = test_extra_tx;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = cuda_status(launch_chunk(head_dim, cache->k_fmt, cache->v_fmt, p, s));
-  if (st || !merged) return st;
+  // Blocks of fewer steps than this are never cut: no merge.
+  if (st || max_seq_len <= (2 * kChunkSnap - 1) * kChunkKeys) return st;
   return cuda_status(launch_chunk_merge(head_dim, p, s));
 }
 

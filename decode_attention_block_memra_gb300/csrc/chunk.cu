@@ -6,6 +6,43 @@
 namespace memra {
 namespace {
 
+// Whole warp: what the merge joins at the cut where CTA c's share begins (c > 0): pieces (0: nothing was cut
+// there, or the cut is a later one of its block), KV head, first row and tokens.
+template <int TILES>
+__device__ __forceinline__ int4 chunk_merge_of(const ChunkParams &p, int c, int tpb, int lane) {
+  const int64_t head = chunk_head_cost<TILES>(p, tpb, lane), all = head * p.n_kv_heads;
+  const int n = chunk_shares<TILES>(p, head);
+  if (head <= 0 || c >= n) return make_int4(0, 0, 0, 0);
+  const ChunkCut x = chunk_cut<TILES>(p, head, all * c / n, tpb, lane);
+  const int64_t before = all * (c - 1) / n - x.start;
+  if (x.k <= 0 || x.k >= x.steps || (before > 0 && chunk_cut_step<TILES>(before, x.steps, x.step) != 0))
+    return make_int4(0, 0, 0, 0);
+  // the CTA before this cut has the block's head, the others a piece from their own cut on
+  int pieces = 2;
+  for (int d = c + 1; d < n; ++d) {
+    const int64_t off = all * d / n - x.start;
+    if (off >= x.cost || chunk_cut_step<TILES>(off, x.steps, x.step) >= x.steps) break;
+    ++pieces;
+  }
+  const ChunkSeq s = chunk_seq(p, x.b);
+  const ChunkBlock block = chunk_block(p, s, x.j, tpb);
+  return make_int4(pieces, x.h, s.first + block.t0, block.t1 - block.t0);
+}
+
+// A warp for each cut.  A kernel of its own: the merge's CTAs, several one after another on an SM, would each find their
+// cut in front of their loads (512 tokens beside 15 single ones over 60,000 keys: 123 us for 111), and in the pass it takes
+// registers from the loops over the keys (2,048 tokens behind 30,000: 1,410 us for 1,350).
+constexpr int kCutWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kCutWarps) chunk_cuts_kernel(const ChunkParams p) {
+  allow_dependent_launch();
+  const int c = 1 + blockIdx.x * kCutWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  // (the pass has begun, so that what it reads is there, and what a call before has left is used up)
+  const int4 merge = chunk_merge_of<chunk_tiles(D)>(p, c, chunk_tiles(D) * p.tpt, lane);
+  if (lane == 0 && c < p.ctas) p.merges[c] = merge;
+  grid_dependency_wait();                    // with this kernel the pass has ended
+}
+
 // CTA = 32 rows of a cut block, warp = 16 columns, thread = row.  The CTA of the
 // block's first cut merges it, the pieces in their order along the keys.
 template <int D>
@@ -81,9 +118,12 @@ cudaError_t launch_chunk(int D, int kf, int vf, const ChunkParams &p, cudaStream
 
 cudaError_t launch_chunk_merge(int D, const ChunkParams &p, cudaStream_t st) {
   if (p.ctas < 2) return cudaSuccess;
-  const dim3 grid((p.ctas - 1) * (chunk_tiles(D) * kChunkRows / 32));
-  if (D == 128) return launch_pdl(chunk_merge_kernel<128>, grid, dim3(256), 0, st, p);
-  return launch_pdl(chunk_merge_kernel<256>, grid, dim3(512), 0, st, p);
+  const dim3 cuts((p.ctas - 1 + kCutWarps - 1) / kCutWarps), grid((p.ctas - 1) * (chunk_tiles(D) * kChunkRows / 32));
+  auto run = [&](auto find, auto merge) {
+    const cudaError_t e = launch_pdl(find, cuts, dim3(32 * kCutWarps), 0, st, p);
+    return e != cudaSuccess ? e : launch_pdl(merge, grid, dim3(2 * D), 0, st, p);
+  };
+  return D == 128 ? run(chunk_cuts_kernel<128>, chunk_merge_kernel<128>) : run(chunk_cuts_kernel<256>, chunk_merge_kernel<256>);
 }
 
 }  // namespace memra

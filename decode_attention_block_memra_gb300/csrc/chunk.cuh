@@ -50,7 +50,7 @@ struct ChunkParams {
   float *lse;                   // [total][n_heads], or null
   float *o_part;                // [2 * CTAs][D / 4][rows of a block][4]: the partial blocks at a CTA's start and end
   float *lse_part;              // [2 * CTAs][rows of a block], base 2
-  int4 *merges;                 // [CTAs]: the block that was cut where a CTA's share begins (chunk_merge_of); null: no merge
+  int4 *merges;                 // [CTAs]: the block that was cut where a CTA's share begins (chunk_merge_of)
   float *far;                   // [CTAs][row tiles][columns / 4][128][4]: what earlier sums of a long block came to
   int32_t *status;
   int batch, total, n_heads, group, n_kv_heads, num_pages, max_pages, window;
@@ -209,29 +209,6 @@ __device__ __forceinline__ ChunkCut chunk_cut(const ChunkParams &p, int64_t head
   c.step = cost.step(lo);
   c.k = chunk_cut_step<TILES>(rest - cost.upto(lo), c.steps, c.step);
   return c;
-}
-
-// Whole warp: what the merge joins at the cut where CTA c's share begins (c > 0): pieces (0: nothing was cut
-// there, or the cut is a later one of its block), KV head, first row and tokens.
-template <int TILES>
-__device__ __forceinline__ int4 chunk_merge_of(const ChunkParams &p, int c, int tpb, int lane) {
-  const int64_t head = chunk_head_cost<TILES>(p, tpb, lane), all = head * p.n_kv_heads;
-  const int n = chunk_shares<TILES>(p, head);
-  if (head <= 0 || c >= n) return make_int4(0, 0, 0, 0);
-  const ChunkCut x = chunk_cut<TILES>(p, head, all * c / n, tpb, lane);
-  const int64_t before = all * (c - 1) / n - x.start;
-  if (x.k <= 0 || x.k >= x.steps || (before > 0 && chunk_cut_step<TILES>(before, x.steps, x.step) != 0))
-    return make_int4(0, 0, 0, 0);
-  // the CTA before this cut has the block's head, the others a piece from their own cut on
-  int pieces = 2;
-  for (int d = c + 1; d < n; ++d) {
-    const int64_t off = all * d / n - x.start;
-    if (off >= x.cost || chunk_cut_step<TILES>(off, x.steps, x.step) >= x.steps) break;
-    ++pieces;
-  }
-  const ChunkSeq s = chunk_seq(p, x.b);
-  const ChunkBlock block = chunk_block(p, s, x.j, tpb);
-  return make_int4(pieces, x.h, s.first + block.t0, block.t1 - block.t0);
 }
 
 cudaError_t launch_chunk(int D, int kf, int vf, const ChunkParams &p, cudaStream_t st);

@@ -25,11 +25,11 @@
 // at every step, so an O takes kSumUnits chunks at most; then it is added to a
 // float32 row in the workspace.
 //
-// What it measured (q8_0/q5_1, D 128, 32/4 heads).  2,048 tokens behind 30,000: 1.39 ms, 78% of the tensor
+// What it measured (q8_0/q5_1, D 128, 32/4 heads).  2,048 tokens behind 30,000: 1.35 ms, 80% of the tensor
 // cores' rate counting the pairs' products; a step of two row tiles takes 3,500 clocks, 2,112 of them
 // MMAs, the rest the chain from a score to its P and the next score over it, which two groups
-// do not quite hide.  512 tokens beside 15 single ones over 60,000 keys: 115 us.  One token over 255
-// keys: 12 us, a chain of latencies.  Not faster: an MMA thread for each group (1,818 us), P in columns
+// do not quite hide.  512 tokens beside 15 single ones over 60,000 keys: 111 us.  One token over 255
+// keys: 11 us, a chain of latencies.  Not faster: an MMA thread for each group (1,818 us), P in columns
 // of its own with most of Q in shared memory (1,507 us).
 #pragma once
 
@@ -323,12 +323,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
                                (cp_v ? p.v_pool : p.k_pool) + (static_cast<size_t>(pid) * p.n_kv_heads + x.h) * cp_bytes,
                                cp_bytes, raw_full(s));
       }
-    }
-    // (the merge's CTAs, several one after another on an SM, would each find it out in front of their loads: 123 us for 115)
-    if (blockIdx.x > 0 && p.merges) {
-      int4 merge = make_int4(0, 0, 0, 0);
-      if (share[0].k > 0) merge = chunk_merge_of<C::kTiles>(p, blockIdx.x, tpb, lane);
-      if (lane == 0) p.merges[blockIdx.x] = merge;
     }
     // every copy has landed before the CTA can leave
     for (int c = max(0, cc - RAW); c < cc; ++c) mbar_wait_suspended(raw_full(c % RAW), (c / RAW) & 1, p.status);
