@@ -11,7 +11,7 @@
 // falls to one side or the other by its last bits: in float32 some five codes of 8
 // million differ from exact arithmetic's, so keys, a small part of the rows, are carried
 // as unevaluated sums of two floats from the sum of squares to the rounding, and none did
-// (16,384 tokens of 16 and 2 heads, D 256, fp8 cache: 86 us, 77 with keys in float32).
+// (16,384 tokens of 16 and 2 heads, D 256, fp8 cache: 85 us, 77 with keys in float32).
 //
 // Angles.  position * inv_freq reaches 10^5 and more radians, where float32 has no
 // digits left behind the point.  So a frequency is kept in turns (inv_freq / 2 pi)
@@ -27,7 +27,7 @@
 // flight throughout.
 //
 // Bound by bytes with many tokens, and by the arithmetic of the keys and of the quantizers
-// beside them: those 16,384 tokens move 319 MB in 86 us, 3.7 TB/s (queries alone: 268 MB in
+// beside them: those 16,384 tokens move 319 MB in 85 us, 3.8 TB/s (queries alone: 268 MB in
 // 54 us, 5.0 TB/s); 2,048 tokens of 32 and 4 heads, D 128, no cache: 38 MB in
 // 15.6 us.  With few, by
 // the chain of one row: a launch of 8 tokens takes 5 us.
@@ -73,6 +73,18 @@ __device__ __forceinline__ Two mul(Two a, Two b) {
 __device__ __forceinline__ float rounded(Two a) {
   const float y = a.hi + a.lo;
   return y == y ? y : a.hi;
+}
+
+// Times a float.
+__device__ __forceinline__ Two times(Two a, float b) {
+  const Two p = two_prod(a.hi, b);
+  return {p.hi, fmaf(a.lo, b, p.lo)};
+}
+// a b + c d.
+__device__ __forceinline__ Two dot(Two a, Two b, Two c, Two d) {
+  const Two p = two_prod(a.hi, b.hi), q = two_prod(c.hi, d.hi), s = two_sum(p.hi, q.hi);
+  const float lo = fmaf(a.hi, b.lo, fmaf(a.lo, b.hi, p.lo)), lo1 = fmaf(c.hi, d.lo, fmaf(c.lo, d.hi, q.lo));
+  return {s.hi, s.lo + (lo + lo1)};
 }
 
 // 1 / sqrt(a): an approximation y and one Newton step, y + y (1 - a y^2) / 2, whose correction is the low part.
@@ -238,18 +250,20 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
     if (p.k_weight) {
       Two sum{x[0] * x[0], 0.f};           // (the square of an fp16 value is exact)
 #pragma unroll
-      for (int i = 1; i < 8; ++i) sum = add(sum, {x[i] * x[i], 0.f});
+      for (int i = 1; i < 8; ++i) {
+        const Two s = two_sum(sum.hi, x[i] * x[i]);
+        sum = {s.hi, sum.lo + s.lo};
+      }
 #pragma unroll
       for (int d = 1; d < L; d <<= 1)
         sum = add(sum, {__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
       const Two scale = rsqrt_two(add({sum.hi * (1.f / D), sum.lo * (1.f / D)}, {p.eps, 0.f}));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = mul(mul(scale, {p.k_weight[8 * l + i], 0.f}), v[i]);
+      for (int i = 0; i < 8; ++i) v[i] = times(times(scale, p.k_weight[8 * l + i]), x[i]);
     }
     // a cosine + b sine
     auto turn = [&](Two a, Two b, int j, float s) {
-      const Two t = add(mul(a, {table[1][j], table[3][j]}), mul(b, {s * table[0][j], s * table[2][j]}));
-      return rounded(t);
+      return rounded(dot(a, {table[1][j], table[3][j]}, b, {s * table[0][j], s * table[2][j]}));
     };
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = rounded(v[i]);
