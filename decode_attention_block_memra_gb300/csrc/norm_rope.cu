@@ -29,8 +29,8 @@
 // Bound by bytes with many tokens, and by the arithmetic of the keys and of the quantizers
 // beside them: those 16,384 tokens move 319 MB in 85 us, 3.8 TB/s (queries alone: 268 MB in
 // 54 us, 5.0 TB/s); 2,048 tokens of 32 and 4 heads, D 128, no cache: 38 MB in
-// 15.6 us.  With few, by
-// the chain of one row: a launch of 8 tokens takes 5 us.
+// 11.5 us.  With few, by
+// the chain of one row: a launch of 8 tokens takes 4.5 us.
 #include <algorithm>
 
 #include "kv_stage.cuh"
@@ -154,8 +154,10 @@ __device__ __forceinline__ void store_v_fp8_pair(const QuantTarget &dst, int pag
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRopeParams p) {
+// CTAS: to an SM.  Two, with all their registers, as long as their warps have a token each at most, so that the chain of one
+// is what counts; else three (32 and 4 heads, D 128, fp8 cache: 2,048 tokens 15 us with two, 21 with three, 16,384 99 and 92).
+template <int D, int CTAS>
+__global__ void __launch_bounds__(32 * kWarps, CTAS) norm_rope_kernel(const NormRopeParams p) {
   constexpr int L = D / 8, ROWS = 32 / L;  // lanes of a row, rows of a warp
   __shared__ unsigned long long s_turns[D / 2];
   __shared__ __align__(16) float s_angles[kWarps][4][D / 2];    // sines, cosines and their low parts of each warp's token
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) norm_rope_kernel(const NormRop
   }
 }
 
-template <int D>
+template <int D, int CTAS>
 cudaError_t launch(NormRopeParams p, int sms, cudaStream_t st) {
   constexpr int kRows = 32 / (D / 8);
   auto groups = [](int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); };
@@ -381,9 +383,9 @@ cudaError_t launch(NormRopeParams p, int sms, cudaStream_t st) {
   p.q_passes = groups(p.n_heads, kRows);
   // A unit to a warp: a token's row groups of K and of V in shares as small as leave the queries' a warp, these in as many
   // as there are then (a row of K or V takes some three times a query's).  From so many tokens on that three units a
-  // token are too many, whole tokens (32 and 8 heads, D 128, fp8: 512 tokens 10 us so, 17 whole, 15 group by group; 4,096
+  // token are too many, whole tokens (32 and 8 heads, D 128, fp8: 512 tokens 11 us so, 17 whole, 15 group by group; 4,096
   // tokens 43 us whole, 67 group by group).
-  const int64_t warps = 3ll * sms * kWarps, tokens = p.tokens, room = tokens > 0 ? warps / tokens : 0;
+  const int64_t warps = static_cast<int64_t>(CTAS) * sms * kWarps, tokens = p.tokens, room = tokens > 0 ? warps / tokens : 0;
   p.parts = 1;
   for (int share = 1; p.parts == 1 && share <= std::max({p.k_passes, p.v_passes, 1}); ++share) {
     const int kv = groups(p.k_passes, share) + groups(p.v_passes, share);
@@ -393,14 +395,15 @@ cudaError_t launch(NormRopeParams p, int sms, cudaStream_t st) {
   }
   p.units = tokens * p.parts;
   // (an odd number of CTAs: even and odd tokens to every SM)
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((p.units + kWarps - 1) / kWarps, (3ll * sms - 1) | 1));
-  return launch_pdl(norm_rope_kernel<D>, dim3(grid), dim3(32 * kWarps), 0, st, p);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((p.units + kWarps - 1) / kWarps, (static_cast<int64_t>(CTAS) * sms - 1) | 1));
+  return launch_pdl(norm_rope_kernel<D, CTAS>, dim3(grid), dim3(32 * kWarps), 0, st, p);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(int D, NormRopeParams p, int sms, cudaStream_t st) {
-  return D == 128 ? launch<128>(p, sms, st) : launch<256>(p, sms, st);
+  if (p.tokens <= 2 * sms * kWarps) return D == 128 ? launch<128, 2>(p, sms, st) : launch<256, 2>(p, sms, st);
+  return D == 128 ? launch<128, 3>(p, sms, st) : launch<256, 3>(p, sms, st);
 }
 
 }  // namespace memra
