@@ -109,10 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   grid_dependency_wait();
   allow_dependent_launch();
   const Share s = share_of(p, b);
-  if (row % p.n_kv_heads == 0 && rank == 0 && tid == 0) {
-    if (s.bad) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
-    if (p.new_lens) p.new_lens[b] = s.n;
-  }
+  if (s.bad && row % p.n_kv_heads == 0 && rank == 0 && tid == 0) flag_error(p.status, MEMRA_DEVERR_BAD_SEQ_LEN);
   const float *w = p.weights + static_cast<int64_t>(row) * p.weight_stride;
   const int middle = s.T - s.sink - s.recent, m = s.n - s.sink - s.recent;
   const int run = (middle + ranks - 1) / ranks, lo = s.sink + min(rank * run, middle),
@@ -451,6 +448,11 @@ __global__ void __launch_bounds__(MoveCfg<D, KF, VF>::kThreads, 1536 / MoveCfg<D
         from = -1;
         flag_error(p.status, MEMRA_DEVERR_BAD_PAGE);
       }
+    }
+    // How many stay: stored here, because new_lens may be seq_lens or budgets, and every CTA of the selection reads those.
+    if (p.new_lens && h == 0) {
+      const int after = j + 1 < p.max_budget ? p.kept[row * p.max_budget + j + 1] : -1;
+      if (i >= 0 ? after < 0 : j == 0) p.new_lens[b] = i >= 0 ? j + 1 : 0;
     }
     s_page[tid / kPage][tid % kPage] = from;
     s_token[tid / kPage][tid % kPage] = i & (kPage - 1);

@@ -539,7 +539,7 @@ int memra_key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stri
  *   new_weights   device float32 [batch][n_kv_heads][new_weight_stride], or NULL:
  *                 their weights, what lies behind the last left as it was; overlaps
  *                 nothing else of the call
- *   new_lens      device int32 [batch], or NULL: n
+ *   new_lens      device int32 [batch], or NULL: n; may be seq_lens or budgets themselves
  * A length out of range is clamped (MEMRA_DEVERR_BAD_SEQ_LEN); a row whose page is
  * outside the pool, on either side, does not move (MEMRA_DEVERR_BAD_PAGE).  batch *
  * n_kv_heads <= 65535.  No workspace.  batch == 0 or max_budget == 0 is a no-op. */

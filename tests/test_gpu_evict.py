@@ -206,3 +206,47 @@ def test_refusals_of_the_binding(memra):
             c.call(**bad)
     assert c.call() == 0
     c.check()
+
+
+@pytest.mark.parametrize("lens,budgets,heads", [
+    ([700 - 9 * b for b in range(64)], [40 + b % 3 for b in range(64)], 8),          # more rows than run at once
+    ([9000, 5000, 1, 4097], [300, 1000, 1, 64], 2),                                   # clusters
+    ([70000], [500], 4), ([5, 0, 30, 16], [3, 3, 0, 16], 3),
+])
+@pytest.mark.parametrize("which", ["seq_lens", "budgets"])
+def test_lengths_updated_in_place(memra, lens, budgets, heads, which):
+    c = Case(memra, "fp8", "fp8", 128, heads, lens, budgets, 1, 4)
+    c.new_lens = dev(lens if which == "seq_lens" else budgets)
+    assert c.call(**{which: c.new_lens}) == 0
+    c.check()
+
+
+def test_lengths_updated_in_place_by_a_replayed_graph(memra):
+    """Two evictions of a cache to half, then to a quarter, by one pair of captured calls: the second reads what the first left."""
+    c = Case(memra, "q8_0", "q5_1", 128, 2, [3000, 1200], [1500, 600], 2, 8)
+    lens, weights, first, second = dev(c.lens), dev(c.weights, np.float32), dev(c.budgets), dev([750, 300])
+    kept, w2 = torch.empty(2, 2, 750, dtype=torch.int32, device="cuda"), torch.zeros(2, 2, 1500, device="cuda")
+    to = dev(np.arange(2 * 47).reshape(2, 47) + c.pages)
+    cache = memra.KVCache("q8_0", "q5_1", c.pages + 94, 2, 128)
+    cache.k_pool[:c.cache.k_pool.numel()], cache.v_pool[:c.cache.v_pool.numel()] = c.cache.k_pool, c.cache.v_pool
+    table, half = dev(c.table), dev(c.to)
+
+    def calls():
+        memra.kv_evict(cache, table, lens, 3000, weights, first, half, c.kept, 2, 8, new_weights=w2, new_lens=lens)
+        memra.kv_evict(cache, half, lens, 1500, w2, second, to, kept, 2, 8, new_lens=lens)
+
+    calls()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(3):
+        lens.copy_(dev(c.lens))
+        kept.fill_(77)
+        graph.replay()
+        assert memra.read_status(cache) == 0 and lens.tolist() == [750, 300]
+        for b in range(2):
+            for h in range(2):
+                rows = chunked.kept_tokens(c.weights[b, h, :c.lens[b]], c.budgets[b], 2, 8)
+                again = chunked.kept_tokens(c.weights[b, h, rows], lens[b].item(), 2, 8)
+                assert np.array_equal(kept[b, h].cpu().numpy()[:len(again)], again)
+                assert (kept[b, h, len(again):] == -1).all()
