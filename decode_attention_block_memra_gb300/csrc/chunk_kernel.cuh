@@ -494,13 +494,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
         // the row of Q: fp16 pairs into tensor memory, the last dims into core matrices
         const uint4 *src = reinterpret_cast<const uint4 *>(
             p.q + (live ? (x->first + t) * p.q_stride + static_cast<int64_t>(x->h * p.group + head) * D : 0));
+        auto load = [&](int u) {
+          const uint4 v = live ? src[u] : make_uint4(0, 0, 0, 0);
+          return make_uint4(nan_for_inf(v.x), nan_for_inf(v.y), nan_for_inf(v.z), nan_for_inf(v.w));
+        };
 #pragma unroll
         for (int c = 0; c < C::kQTmem / 2; c += 16) {
           if (turns && g != (c >= 32)) continue;       // a part of the row by each group
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint4 v = live ? src[c / 4 + e] : make_uint4(0, 0, 0, 0);
+            const uint4 v = load(c / 4 + e);
             y[4 * e] = v.x, y[4 * e + 1] = v.y, y[4 * e + 2] = v.z, y[4 * e + 3] = v.w;
           }
           tc::st_32x32b_x16(tmem + tlane + C::kQCol + tile * (C::kQTmem / 2) + c, y);
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
         for (int u = 0; u < C::kQSmem / 8; ++u) {
           if (turns && g == 0) continue;
           sts128(sb + C::kOffQ + tile * kChunkRows * C::kQSmem * 2 + ((rl >> 3) * (C::kQSmem / 8) + u) * 128 + (rl & 7) * 16,
-                 live ? src[C::kQTmem / 8 + u] : make_uint4(0, 0, 0, 0));
+                 load(C::kQTmem / 8 + u));
         }
       }
       if constexpr (C::kQSmem > 0) fence_proxy_async();

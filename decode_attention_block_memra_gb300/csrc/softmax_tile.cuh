@@ -14,6 +14,10 @@ __device__ __forceinline__ uint32_t pack_half2_sat(float lo, float hi) {
   return r;
 }
 
+// An fp16 pair as it is, but infinities as NaN (inf * 0).  For queries: the scores of an infinite element with keys
+// of one sign can all be -inf, which the softmax could not tell from hidden ones.
+__device__ __forceinline__ uint32_t nan_for_inf(uint32_t x) { return hfma2_u32(x, 0u, x); }
+
 // Two float32 products in one instruction.
 __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
   uint64_t r;

@@ -329,3 +329,29 @@ def test_a_wait_that_runs_out(memra, D):
     assert torch.equal(c.cache.k_pool, pools[0]) and torch.equal(c.cache.v_pool, pools[1])
     assert c.call() == 0
     assert torch.equal(c.out, good) and torch.equal(c.lse, good_lse)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("kf,vf", [("fp8", "fp8"), ("q8_0", "q5_1"), ("nvfp4", "nvfp4")])
+@pytest.mark.parametrize("new,past", [([3, 1, 140], [0, 0, 200]), ([1], [9000]), ([2, 1], [20000, 500])])
+@pytest.mark.parametrize("value", [-np.inf, np.inf])
+def test_infinite_queries_whose_scores_have_one_sign(memra, kf, vf, D, new, past, value):
+    """Every key is positive in the channel where a query is infinite: its scores are all -inf, or all inf."""
+    c = Chunk(memra, kf, vf, D, 4, 1, new, past)
+    for b, T in enumerate(c.lens):
+        k = np.abs(c.rows[b][1])
+        k[..., [7, D - 1]] += 1
+        pos = np.arange(T)
+        memra.kv_append(c.cache, dev(k), dev(c.rows[b][2]),
+                        dev((c.table[b, pos // 16] * 16 + pos % 16).astype(np.int32)))
+        c.rows[b] = (0, k, c.rows[b][2])
+    assert c.call() == 0
+    c.check()
+    good, good_lse = c.out.clone(), c.lse.clone()
+    want = torch.zeros(c.lse.shape, dtype=torch.bool, device="cuda")
+    for t in range(sum(new)):                # (a channel of each part of a row: the last dims may lie elsewhere)
+        c.buf[t, t % 4, 7 if t % 2 else D - 1] = float(value)
+        want[t, t % 4] = True
+    assert c.call() == 0
+    assert torch.equal(c.out.isnan().all(-1), want) and torch.equal(c.lse.isnan(), want)
+    assert torch.equal(c.out[~want], good[~want]) and torch.equal(c.lse[~want], good_lse[~want])
