@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(TreeCfg<D, KF, VF, MT>::kThreads, 1)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (live ? row_id(r) : 0) * D);
       auto load = [&](int u) {
         const uint4 y = live ? src[u] : make_uint4(0, 0, 0, 0);
-        return make_uint4((y.x & p.q_and) ^ p.q_xor, (y.y & p.q_and) ^ p.q_xor, (y.z & p.q_and) ^ p.q_xor,
-                          (y.w & p.q_and) ^ p.q_xor);
+        return make_uint4(nan_for_inf((y.x & p.q_and) ^ p.q_xor), nan_for_inf((y.y & p.q_and) ^ p.q_xor),
+                          nan_for_inf((y.z & p.q_and) ^ p.q_xor), nan_for_inf((y.w & p.q_and) ^ p.q_xor));
       };
 #pragma unroll
       for (int c = 0; c < C::kQTmem / 2; c += 16) {

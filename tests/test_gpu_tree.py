@@ -521,3 +521,22 @@ def test_two_streams_with_their_own_workspaces(memra):
     torch.cuda.synchronize()
     for out, _ in outs:
         assert torch.equal(out, dw.out)
+
+
+@pytest.mark.parametrize("kf,vf", [("fp8", "fp8"), ("q8_0", "q5_1"), ("nvfp4", "nvfp4")])
+@pytest.mark.parametrize("D,nodes,ctx", [(128, 9, 200), (128, 9, 2600), (128, 40, 2600), (256, 9, 200), (256, 9, 2600)])
+@pytest.mark.parametrize("value", [-np.inf, np.inf])
+def test_an_infinite_query_whose_scores_have_one_sign(memra, kf, vf, D, nodes, ctx, value):
+    """Every key is positive in the channel where a query is infinite: its scores are all -inf, or all inf."""
+    w = W.random_case(72 + D, batch=2, q_len=nodes, n_heads=8, n_kv_heads=2, head_dim=D, k_fmt=kf, v_fmt=vf, ctx=(ctx - 30, ctx))
+    w.k_rows = np.abs(w.k_rows)
+    w.k_rows[..., [5, D - 1]] += 1
+    dw, args, _ = check(memra, w, words_for(w, 23))
+    want = dw.out.clone()
+    for b, i, h, j in ((0, 3, 2, 5), (1, nodes - 1, 7, D - 1)):
+        dw.q[b, i, h, j] = float(value)
+        want[b, i, h] = float("nan")
+    memra.tree_attn(*args)
+    assert memra.read_status(dw.cache) == 0
+    assert torch.equal(torch.isnan(dw.out), torch.isnan(want))
+    assert torch.equal(dw.out.nan_to_num(7.0), want.nan_to_num(7.0))
