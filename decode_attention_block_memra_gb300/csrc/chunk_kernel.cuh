@@ -21,7 +21,9 @@
 //
 // Roundings.  K^ and V^ enter exactly, or as fp16 hi + lo pairs (q8_0, q5_1, q4_0: a single fp16
 // value of either would cost as much as the output's own rounding, 4.2e-4 instead of 3.0e-4
-// with both).  P is fp16, everything else float32.  The tensor cores cut an accumulator's last bits
+// with both).  P is fp16, everything else float32.  P is lifted by 2^7: weights below 2^-21 of a row's largest are off by up to
+// 2^-32 of it, those below 2^-32 are lost (2^-25 with P at 1: 262,143 keys that weigh 2^-25.1 of one other are 0.7% of the
+// row, and all of it was lost).  The tensor cores cut an accumulator's last bits
 // at every step, so an O takes kSumUnits chunks at most; then it is added to a
 // float32 row in the workspace.
 //
@@ -44,7 +46,9 @@
 namespace memra {
 namespace {
 
-constexpr float kLazy = 8.f;               // log2 units: P stays <= 256 between rescales
+// log2 units: a row's maximum passes its reference m by no more between rescales; and P is 2^(s - m + kLift), so
+// that it uses fp16's range: 2^15 at most, and 2^7 at least for the row's largest.
+constexpr float kLazy = 8.f, kLift = 7.f;
 constexpr int kSumUnits = 120;             // chunks of one sum of the tensor cores: 7,680 keys
 
 // Where a CTA's share of the line begins, or ends.
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
           }
           l *= alpha;
         }
-        const float mu = m == -INFINITY ? 0.f : m;
+        const float mu = m == -INFINITY ? 0.f : m - kLift;
         uint64_t sum = 0;
 #pragma unroll
         for (int c = 0; c < KT; c += 32) {
@@ -718,7 +722,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
       }
       if (ok && live && (!turns || g == 0)) {
         // base 2; -inf, never weighed, without a visible key
-        const float lse = l != 0.f ? m + log2f(l) : -INFINITY;
+        const float lse = l != 0.f ? m - kLift + log2f(l) : -INFINITY;
         if (!whole)
           p.lse_part[static_cast<size_t>(slot) * (C::kTiles * kChunkRows) + part_row] = lse;
         else if (p.lse)

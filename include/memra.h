@@ -479,7 +479,9 @@ int memra_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k
  *                 the sum of a row's exponentials (-inf for a row that sees no key)
  * All K and V formats, head_dim 128 or 256, n_heads / n_kv_heads <= MEMRA_MAX_GROUP,
  * batch and n_kv_heads <= 65535.  K^ and V^ enter the products exactly (or as fp16
- * pairs), the softmax weights in fp16; everything is accumulated in float32, 7,680 keys
+ * pairs), the softmax weights in fp16: each off by up to 2^-11 of itself, or 2^-32 of
+ * the row's largest, whichever is more, so that N keys far below the largest may
+ * move the row by N * 2^-32 |V|.  Everything is accumulated in float32, 7,680 keys
  * to a sum of the tensor cores and the sums joined.  The work is cut by the lengths of the whole call, so that it fills the GPU: the same call gives
  * the same bytes, another batch may differ in the last bits.  A query, or a key that
  * a row sees, that is not finite makes the row NaN; a V that is not finite may also

@@ -5,7 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from chunk_cases import PAIRS, Chunk, dev     # noqa: E402
+from chunk_cases import PAIRS, Chunk, dequantized, dev     # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -355,3 +355,37 @@ def test_infinite_queries_whose_scores_have_one_sign(memra, kf, vf, D, new, past
     assert c.call() == 0
     assert torch.equal(c.out.isnan().all(-1), want) and torch.equal(c.lse.isnan(), want)
     assert torch.equal(c.out[~want], good[~want]) and torch.equal(c.lse[~want], good_lse[~want])
+
+
+@pytest.mark.parametrize("tail", [22.5, 24.6, 25.1, 27.0, 31.0])
+@pytest.mark.parametrize("kf,vf,D,T,n", [("q8_0", "q5_1", 128, 262144, 4864), ("fp8", "fp8", 128, 131072, 4864),
+                                         ("fp8", "q4_0", 256, 131072, 2432)])
+def test_a_dominant_key_over_a_long_even_tail(memra, kf, vf, D, T, n, tail):
+    """The first key's score is `tail` log2 units above the others', whose values have one sign; blocks enough that most CTAs take all
+    keys of theirs.  A row at position p is r sum(v_1 .. v_p) / (1 + p r), r = e^-s.
+
+    Tolerance: r is off by the score's accumulator (D / 16 steps, twice for pairs) and 2^-19 for the exponential, once in the sum
+    above and once below; weights by 2^-11 of themselves or 2^-32 of the first's; the accumulator's cut bits and the output's
+    rounding as in Chunk.expected; the sum of weights by a rounding of 2^-24 for each 64 keys.
+    """
+    c = Chunk(memra, kf, vf, D, 8, 1, [n], [T - n], fill=False,
+              v_of=lambda *s: (1 + np.random.default_rng(1).random(s)) * (np.arange(s[0]) > 0)[:, None, None])
+    k = np.zeros((T, 1, D), np.float16)
+    k[0, 0, 0] = 5.0
+    for lo in range(0, T, 65536):
+        pos = np.arange(lo, lo + 65536)
+        memra.kv_append(c.cache, dev(k[pos]), dev(c.rows[0][2][pos]), dev((c.table[0, pos // 16] * 16 + pos % 16).astype(np.int32)))
+    k0 = dequantized(k[:1, 0], kf, c.scales[0])[0, 0]
+    c.buf.zero_()
+    c.buf[..., 0] = float(tail * np.log(2) * D ** 0.5 / k0)
+    s = float(c.buf[0, 0, 0]) * k0 * D ** -0.5
+    assert c.call() == 0
+    p, r = np.arange(T - n, T)[:, None], np.exp(-s)
+    v = np.cumsum(dequantized(c.rows[0][2][:, 0], vf, c.scales[1]), 0)[T - n:]
+    want, want_lse = r * v / (1 + p * r), s + np.log1p(p * r)
+    r_off, l_off = 1.05 * s * 2.0 ** -23 * (D / 8) + 2.0 ** -19, T / 64 * 2.0 ** -24
+    tol = want * (2 * r_off + l_off + 2 * 2.0 ** -11 + 960 * 2.0 ** -23) + T * 2.0 ** -32 * 2 + 2.0 ** -25
+    err = np.abs(c.out.cpu().numpy().astype(np.float64) - want[:, None]) / tol[:, None]
+    assert err.max() <= 1, f"{err.max()} of the tolerance"
+    lse = c.lse.cpu().numpy().astype(np.float64)
+    assert (np.abs(lse - want_lse) <= r_off + l_off + 2.0 ** -22 * want_lse).all()
