@@ -197,3 +197,24 @@ def test_refusals_of_the_binding(memra):
             memra.qk_norm_rope(**{**good, **bad})
     none = torch.empty(0, 2, 128, dtype=torch.float16, device="cuda")
     memra.qk_norm_rope(none, none, pos[:0], freq, none, none)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("stored", [False, True])
+def test_keys_are_rounded_once(memra, D, stored):
+    """Normalized keys are the fp16 values next to the exact ones: 2 to 4 million of them, of which some 120 to 250 lie so close
+    to the middle of two that float32 is the middle.  (numpy rounds float64 to fp16 once; the sums of two floats are off by 2^-45,
+    so that one of these keys would differ by chance once in 8,000 runs of other inputs.)"""
+    T, rng = 4096, np.random.default_rng(D)
+    x = rng.standard_normal((T, 4, D)).astype(np.float16)
+    w = (1 + 0.2 * rng.standard_normal(D)).astype(np.float32)
+    k_out = torch.empty(T, 4, D, dtype=torch.float16, device="cuda")
+    cache = memra.KVCache("fp8", "fp8", T // 16, 4, D, 0.02, 0.02) if stored else None
+    memra.qk_norm_rope(dev(x), dev(x), None, None, torch.empty_like(k_out), k_out, None, dev(w), EPS, cache=cache,
+                       v=dev(x) if stored else None, slot_mapping=dev(np.arange(T, dtype=np.int32)) if stored else None)
+    want = chunked.norm_rope_rows(x, w, EPS, None, None, False).astype(np.float16)
+    assert np.array_equal(k_out.cpu().numpy().view(np.uint16), want.view(np.uint16))
+    if stored:
+        plain = memra.KVCache("fp8", "fp8", T // 16, 4, D, 0.02, 0.02)
+        memra.kv_append(plain, dev(want), dev(x), dev(np.arange(T, dtype=np.int32)))
+        assert torch.equal(cache.k_pool, plain.k_pool) and torch.equal(cache.v_pool, plain.v_pool)
