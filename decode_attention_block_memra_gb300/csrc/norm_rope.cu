@@ -10,8 +10,10 @@
 // that kv_append makes of the rounded row.  A key next to a border of its 8-bit code
 // falls to one side or the other by its last bits: in float32 some five codes of 8
 // million differ from exact arithmetic's, so keys, a small part of the rows, are carried
-// as unevaluated sums of two floats from the sum of squares to the rounding, and none did
-// (16,384 tokens of 16 and 2 heads, D 256, fp8 cache: 85 us, 77 with keys in float32).
+// as unevaluated sums of two floats from the sum of squares to the rounding.  What is left
+// is the angles' 2^-33: of 2 to 4 million turned keys a few at most are not the fp16 value next to
+// the exact one, and those lie within 2^-32 of the middle of two (16,384 tokens of 16 and 2 heads, D 256,
+// fp8 cache: 88 us, 77 with keys in float32).
 //
 // Angles.  position * inv_freq reaches 10^5 and more radians, where float32 has no
 // digits left behind the point.  So a frequency is kept in turns (inv_freq / 2 pi)
@@ -127,22 +129,27 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
   return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
 }
 
-// Sine and cosine of `rest` 2^-64 turns, an eighth of a turn at most, by their Taylor series: off by less than 2^-29.
+// Sine and cosine of `rest` 2^-64 turns, an eighth of a turn at most, by their Taylor series, the first three terms as sums of two floats: off
+// by less than 2^-33 (with the third in float32, and the square of the angle as the product leaves it, the cosine was off by 2^-26.8).
 __device__ __forceinline__ void sin_cos(long long rest, Two &sine, Two &cosine) {
-  // 2 pi / 2^64, 1 / 6
+  // 2 pi / 2^64, 1 / 6, 1 / 24, 1 / 120
   constexpr float kHi = 0x1.921fb6p-62f, kLo = -0x1.777a5cp-87f;
-  constexpr float kSixth = 1.f / 6.f, kSixthLo = static_cast<float>(1.0 / 6.0 - static_cast<double>(kSixth));
+  constexpr float k6 = 1.f / 6.f, k6Lo = static_cast<float>(1.0 / 6.0 - static_cast<double>(k6));
+  constexpr float k24 = 1.f / 24.f, k24Lo = static_cast<float>(1.0 / 24.0 - static_cast<double>(k24));
+  constexpr float k120 = 1.f / 120.f, k120Lo = static_cast<float>(1.0 / 120.0 - static_cast<double>(k120));
   const float r = __ll2float_rn(rest), r_lo = __ll2float_rn(rest - __float2ll_rn(r));
-  const Two x = mul({r, r_lo}, {kHi, kLo}), z = mul(x, x);
-  // x - x z / 6 + x z^2 (1/120 - ..)
-  const Two cube = mul(mul(x, z), {-kSixth, -kSixthLo});
-  const float odd = fmaf(z.hi, fmaf(z.hi, fmaf(z.hi, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f), 1.f / 120.f);
-  const Two s = two_sum(x.hi, cube.hi);
-  sine = fast_two_sum(s.hi, s.lo + (x.lo + cube.lo + x.hi * z.hi * z.hi * odd));
-  // 1 - z / 2 + z^2 (1/24 - ..)
-  const float even = fmaf(z.hi, fmaf(z.hi, fmaf(z.hi, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
-  const Two c = fast_two_sum(1.f, -0.5f * z.hi);
-  cosine = fast_two_sum(c.hi, c.lo + fmaf(z.hi * z.hi, even, -0.5f * z.lo));
+  const Two x = mul({r, r_lo}, {kHi, kLo}), square = mul(x, x), z = fast_two_sum(square.hi, square.lo);
+  const float z3 = z.hi * z.hi * z.hi;
+  // x - x z / 6 + x z^2 / 120 - x z^3 (1/5040 - ..)
+  const Two xz = mul(x, z), cube = mul(xz, {-k6, -k6Lo}), fifth = mul(mul(xz, z), {k120, k120Lo});
+  const float odd = fmaf(z.hi, fmaf(z.hi, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f);
+  const Two s0 = two_sum(x.hi, cube.hi), s = two_sum(s0.hi, fifth.hi);
+  sine = fast_two_sum(s.hi, fmaf(x.hi * z3, odd, (s0.lo + s.lo) + (x.lo + cube.lo) + fifth.lo));
+  // 1 - z / 2 + z^2 / 24 - z^3 (1/720 - ..)
+  const Two fourth = mul(mul(z, z), {k24, k24Lo});
+  const float even = fmaf(z.hi, fmaf(z.hi, fmaf(z.hi, 1.f / 479001600.f, -1.f / 3628800.f), 1.f / 40320.f), -1.f / 720.f);
+  const Two c0 = fast_two_sum(1.f, -0.5f * z.hi), c = two_sum(c0.hi, fourth.hi);
+  cosine = fast_two_sum(c.hi, fmaf(z3, even, (c0.lo + c.lo) + fmaf(-0.5f, z.lo, fourth.lo)));
 }
 
 // e4m3 codes of the lane's eight values over the scale, the first in the lowest byte.

@@ -425,8 +425,9 @@ int memra_kv_compact(const memra_kv_cache *cache, const int32_t *page_table, int
  *   y = x / sqrt(mean(x^2) + eps) * weight
  *   (a, b) -> (a cos - b sin, b cos + a sin), angle = positions[t] * inv_freq[j],
  *   (a, b) = dims (j, j + rotary_dim/2), or (2j, 2j+1) where interleaved is not 0
- * computed in float32 (keys in sums of two floats, so that the codes in the cache are
- * the exact rows') and rounded once, to fp16.  An angle is off by at most 2^-52 turns
+ * computed in float32 and rounded once, to fp16; keys in sums of two floats, so that a key
+ * is the fp16 value next to the exact one but where that lies within 2^-32 (|a| + |b|)
+ * of the middle of two, and its code in the cache with it.  An angle is off by at most 2^-52 turns
  * times |positions[t]| max(1, |inv_freq[j]|): 2^-32 turns at position 2^20.
  *   q, k, v       device fp16, token t's heads at q + t * q_stride, [n_heads][head_dim]
  *                 (k, v: [n_kv_heads][head_dim]); strides in elements, multiples of

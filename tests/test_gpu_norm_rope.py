@@ -218,3 +218,26 @@ def test_keys_are_rounded_once(memra, D, stored):
         plain = memra.KVCache("fp8", "fp8", T // 16, 4, D, 0.02, 0.02)
         memra.kv_append(plain, dev(want), dev(x), dev(np.arange(T, dtype=np.int32)))
         assert torch.equal(cache.k_pool, plain.k_pool) and torch.equal(cache.v_pool, plain.v_pool)
+
+
+@pytest.mark.parametrize("D,rotary", [(128, 128), (256, 256), (256, 64)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_turned_keys_fall_to_the_right_side(memra, D, rotary, interleaved):
+    """A turned key is the fp16 value next to the exact one, but where the exact one lies within 2^-32 (|a| + |b|) of the middle of two:
+    sine and cosine are off by 2^-33, angles below 1,000 turns by 2^-43 turns, the sums of two floats by 2^-45."""
+    T, rng = 4096, np.random.default_rng(D + rotary)
+    x = rng.standard_normal((T, 4, D)).astype(np.float16)
+    w = (1 + 0.2 * rng.standard_normal(D)).astype(np.float32)
+    pos = rng.integers(0, 1000, T).astype(np.int32)
+    freq = (1e4 ** (-np.arange(rotary // 2) / (rotary // 2))).astype(np.float32)
+    k_out = torch.empty(T, 4, D, dtype=torch.float16, device="cuda")
+    memra.qk_norm_rope(dev(x), dev(x), dev(pos), dev(freq), torch.empty_like(k_out), k_out, None, dev(w), EPS, interleaved)
+    exact = chunked.norm_rope_rows(x, w, EPS, pos, freq, interleaved)
+    a = np.abs(chunked.norm_rope_rows(x, w, EPS, None, None, interleaved))
+    first, second = chunked.rope_pairs(rotary // 2, interleaved)
+    a[..., first] = a[..., second] = a[..., first] + a[..., second]
+    want, got = exact.astype(np.float16), k_out.cpu().numpy()
+    other = got != want
+    assert other.sum() <= 10                 # (by chance one in 2^21)
+    near = np.abs(exact[other] - (got[other].astype(np.float64) + want[other].astype(np.float64)) / 2)
+    assert (near <= 2.0 ** -32 * a[other]).all()
