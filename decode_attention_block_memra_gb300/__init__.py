@@ -59,6 +59,10 @@ _CHUNK_ARGS = ([ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int64, 
                 ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 6 +
                [ctypes.c_float, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t] + [ctypes.c_void_p] * 3)
 
+_WEIGHT_ARGS = ([ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 3 +
+                [ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 6 + [ctypes.c_float] * 2 +
+                [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p])
+
 _SIGS = {
     "memra_kv_segment_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 3),
     "memra_kv_pool_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 6),
@@ -119,9 +123,8 @@ _SIGS = {
     "memra_chunk_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
     "memra_chunk_attn": (ctypes.c_int, _CHUNK_ARGS),
     "memra_testing_chunk_attn_short_page": (ctypes.c_int, _CHUNK_ARGS),
-    "memra_key_weights": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int64] +
-                          [ctypes.c_void_p] * 3 + [ctypes.c_int32, ctypes.c_void_p] + [ctypes.c_int32] * 6 +
-                          [ctypes.c_float] * 2 + [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "memra_key_weights": (ctypes.c_int, _WEIGHT_ARGS),
+    "memra_testing_key_weights_short_page": (ctypes.c_int, _WEIGHT_ARGS),
     "memra_kv_evict": (ctypes.c_int, [ctypes.POINTER(KVCacheStruct), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                       ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p] +
                        [ctypes.c_int32] * 3 + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
@@ -540,6 +543,11 @@ def key_weights(cache: KVCache, q, lse, cu_seqlens, page_table, seq_lens, max_se
     q, cu_seqlens, page_table, seq_lens as in chunk_attn, lse float32 [tokens,
     Hq] as it writes them; weights float32 [B, Hkv, >= max_seq_len], times keep first.
     """
+    a = _weight_args(cache, q, lse, cu_seqlens, page_table, seq_lens, max_seq_len, weights, keep, sm_scale)
+    _check(lib().memra_key_weights(*a, _stream(stream)), "memra_key_weights")
+
+
+def _weight_args(cache, q, lse, cu_seqlens, page_table, seq_lens, max_seq_len, weights, keep, sm_scale):
     import torch
     where, f32, i32 = "memra_key_weights", torch.float32, torch.int32
     T, Hq, D = shape = q.shape
@@ -548,13 +556,10 @@ def key_weights(cache: KVCache, q, lse, cu_seqlens, page_table, seq_lens, max_se
     if cache.device_index != device:
         raise MemraError(1, where)
     pq, sq = _rows(where, q, torch.float16, shape, device)
-    rc = lib().memra_key_weights(
-        cache.ref, pq, sq, _dense(where, lse, f32, (T, Hq), device), _dense(where, cu_seqlens, i32, (B + 1,), device),
-        _dense(where, page_table, i32, table, device), pages, _dense(where, seq_lens, i32, (B,), device),
-        int(max_seq_len), B, T, Hq, Hkv, D, D ** -0.5 if sm_scale is None else sm_scale, keep,
-        _dense(where, weights, f32, (B, Hkv, row), device), row, _stream(stream))
-    if rc:
-        raise MemraError(rc, where)
+    return (cache.ref, pq, sq, _dense(where, lse, f32, (T, Hq), device), _dense(where, cu_seqlens, i32, (B + 1,), device),
+            _dense(where, page_table, i32, table, device), pages, _dense(where, seq_lens, i32, (B,), device),
+            int(max_seq_len), B, T, Hq, Hkv, D, D ** -0.5 if sm_scale is None else sm_scale, keep,
+            _dense(where, weights, f32, (B, Hkv, row), device), row)
 
 
 def kv_evict(cache: KVCache, page_table, seq_lens, max_seq_len: int, weights, budgets, dst_table, kept, sink: int = 0,
@@ -616,6 +621,13 @@ def testing_chunk_attn_short_page(cache: KVCache, q, cu_seqlens, page_table, seq
     """memra_testing_chunk_attn_short_page (memra_testing.h): the same for chunk attention's first chunk of keys."""
     a = _chunk_args(cache, q, cu_seqlens, page_table, seq_lens, max_seq_len, out, workspace, sm_scale, window, lse)
     _check(lib().memra_testing_chunk_attn_short_page(*a, _stream(stream)), "memra_testing_chunk_attn_short_page")
+
+
+def testing_key_weights_short_page(cache: KVCache, q, lse, cu_seqlens, page_table, seq_lens, max_seq_len: int, weights,
+                                   keep: float = 1.0, sm_scale=None, stream=None) -> None:
+    """memra_testing_key_weights_short_page (memra_testing.h): the same for the key weights' first chunk of keys."""
+    a = _weight_args(cache, q, lse, cu_seqlens, page_table, seq_lens, max_seq_len, weights, keep, sm_scale)
+    _check(lib().memra_testing_key_weights_short_page(*a, _stream(stream)), "memra_testing_key_weights_short_page")
 
 
 def testing_scale_division_mismatches(scales, mismatches, stream=None) -> None:

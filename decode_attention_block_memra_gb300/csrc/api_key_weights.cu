@@ -1,20 +1,21 @@
-// Entry point of the key weights in include/memra.h: argument validation and the launch.
+// Entry point of the key weights in include/memra.h: argument validation and the launch; the test hook.
 #include <algorithm>
 
 #include "host_checks.cuh"
 #include "key_weights.cuh"
+#include "memra_testing.h"
 
 using namespace memra;
 
 namespace {
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-}  // namespace
 
-extern "C" int memra_key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stride, const float *lse,
-                                 const int32_t *cu_seqlens, const int32_t *page_table, int32_t max_pages_per_seq,
-                                 const int32_t *seq_lens, int32_t max_seq_len, int32_t batch, int32_t total_tokens,
-                                 int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale, float keep,
-                                 float *weights, int64_t weight_stride, void *stream) {
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stride, const float *lse,
+                const int32_t *cu_seqlens, const int32_t *page_table, int32_t max_pages_per_seq,
+                const int32_t *seq_lens, int32_t max_seq_len, int32_t batch, int32_t total_tokens, int32_t n_heads,
+                int32_t n_kv_heads, int32_t head_dim, float sm_scale, float keep, float *weights,
+                int64_t weight_stride, void *stream, int test_extra_tx = 0) {
   const int st = check_cache(cache);
   if (st) return st;
   if (batch < 0 || total_tokens < 0 || n_heads < 1 || max_seq_len < 0 || max_pages_per_seq < 1 ||
@@ -60,5 +61,32 @@ extern "C" int memra_key_weights(const memra_kv_cache *cache, const void *q, int
   p.subs = static_cast<int>(ceil_div(p.group, p.hpt));
   p.tpt = std::max(1, rows / p.group);
   p.ctas = device_sms();
+  p.test_extra_tx = test_extra_tx;
   return cuda_status(launch_key_weights(head_dim, rows, cache->k_fmt, p, static_cast<cudaStream_t>(stream)));
 }
+
+}  // namespace
+
+extern "C" {
+
+int memra_key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stride, const float *lse,
+                      const int32_t *cu_seqlens, const int32_t *page_table, int32_t max_pages_per_seq,
+                      const int32_t *seq_lens, int32_t max_seq_len, int32_t batch, int32_t total_tokens,
+                      int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float sm_scale, float keep,
+                      float *weights, int64_t weight_stride, void *stream) {
+  return key_weights(cache, q, q_stride, lse, cu_seqlens, page_table, max_pages_per_seq, seq_lens, max_seq_len, batch,
+                     total_tokens, n_heads, n_kv_heads, head_dim, sm_scale, keep, weights, weight_stride, stream);
+}
+
+// memra_testing.h: the same call with a first raw chunk whose wait cannot complete.
+int memra_testing_key_weights_short_page(const memra_kv_cache *cache, const void *q, int64_t q_stride,
+                                         const float *lse, const int32_t *cu_seqlens, const int32_t *page_table,
+                                         int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t max_seq_len,
+                                         int32_t batch, int32_t total_tokens, int32_t n_heads, int32_t n_kv_heads,
+                                         int32_t head_dim, float sm_scale, float keep, float *weights,
+                                         int64_t weight_stride, void *stream) {
+  return key_weights(cache, q, q_stride, lse, cu_seqlens, page_table, max_pages_per_seq, seq_lens, max_seq_len, batch,
+                     total_tokens, n_heads, n_kv_heads, head_dim, sm_scale, keep, weights, weight_stride, stream, 16);
+}
+
+}  // extern "C"

@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
         if (lane == 0) {
           page_mask[cc & 63] = static_cast<uint8_t>(there);
           if (there)
-            mbar_arrive_expect_tx(bar(C::kRawFull, s), __popc(there) * C::kKSeg);
+            mbar_arrive_expect_tx(bar(C::kRawFull, s),
+                                  __popc(there) * C::kKSeg + (cc == 0 && blockIdx.x == 0 ? p.test_extra_tx : 0));
           else
             mbar_arrive(bar(C::kRawFull, s));
         }
@@ -577,6 +578,16 @@ __global__ void __launch_bounds__(WeightCfg<D, KF, N>::kThreads, 1)
       cc += kTileSteps * tiles;
       __syncwarp();
       if (lane == 0) free_piece(); else ++piece;
+    }
+    if (!ok) {
+      // A wait gave up: every key of the CTA's share becomes NaN (some hold their new weights, others the old ones).
+      WeightWalk walk{p, share[0], share[1]};
+      WeightPiece x;
+      while (walk.next(x)) {
+        float *const row = p.weights + (static_cast<int64_t>(x.b) * p.n_kv_heads + x.h) * p.weight_stride;
+        const int end = min(x.T, (x.tile0 + x.tiles) * kWeightKeys);
+        for (int key = x.tile0 * kWeightKeys + tid; key < end; key += C::kEpilogue) row[key] = __uint_as_float(kNanPair);
+      }
     }
   }
   tc::fence_before_sync();

@@ -31,6 +31,7 @@ struct WeightParams {
   int len_limit;                // lengths are clamped to it
   int hpt, subs, tpt;           // heads of a row tile, row tiles that a token's heads take, tokens of a row tile
   int ctas;
+  int test_extra_tx;            // the test hook's: bytes that CTA 0 expects beyond its first raw chunk's (0 elsewhere)
 };
 
 // `rows`: query rows of a tile, weight_rows(D) or kWeightRowsFew

@@ -107,7 +107,8 @@ typedef enum {
 #define MEMRA_DEVERR_BAD_SEQ_LEN 4   /* seq_len < q_len, > max_seq_len or > table: clamped */
 #define MEMRA_DEVERR_TIMEOUT     8   /* a pipeline wait gave up after ~1 s: result invalid (prompt,
                                         tree and chunk attention: the rows it concerns are NaN, of chunks
-                                        all that the CTA worked on; key weights: keys are missing) */
+                                        all that the CTA worked on; key weights: all keys that the CTA
+                                        worked on are NaN) */
 #define MEMRA_DEVERR_PREFIX     16   /* cascade: a page table differs from the first sequence's
                                         within the shared prefix: that row used the first's pages */
 

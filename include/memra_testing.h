@@ -3,8 +3,8 @@
  * of the decode ABI in memra.h.  The memra pages have no counterpart: they
  * exist so that a test can drive, on a real GPU, the path that every
  * pipeline wait of the decode split kernel, of prompt, tree and chunk
- * attention takes when it runs out, and check the quantizer's division-free
- * quotient against the IEEE one.
+ * attention and of the key weights takes when it runs out, and check the
+ * quantizer's division-free quotient against the IEEE one.
  *
  * Every wait of the library's kernels is bounded (about 1 s): past the bound
  * the kernel ORs MEMRA_DEVERR_TIMEOUT into *cache->status, stays until the
@@ -67,6 +67,14 @@ int memra_testing_chunk_attn_short_page(const memra_kv_cache *cache, const void 
                                         int32_t batch, int32_t total_tokens, int32_t n_heads, int32_t n_kv_heads,
                                         int32_t head_dim, float sm_scale, int32_t window, void *workspace,
                                         size_t workspace_bytes, void *out, float *lse, void *stream);
+
+/* memra_key_weights, likewise. */
+int memra_testing_key_weights_short_page(const memra_kv_cache *cache, const void *q, int64_t q_stride,
+                                         const float *lse, const int32_t *cu_seqlens, const int32_t *page_table,
+                                         int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t max_seq_len,
+                                         int32_t batch, int32_t total_tokens, int32_t n_heads, int32_t n_kv_heads,
+                                         int32_t head_dim, float sm_scale, float keep, float *weights,
+                                         int64_t weight_stride, void *stream);
 
 /* Adds to *mismatches (device, unsigned 64-bit; the caller zeroes it) the
  * number of (x, s) pairs, x every finite fp16 value and s each of the

@@ -166,3 +166,11 @@ def test_key_weights_checks(memra):
     for x in (float("nan"), float("inf")):
         assert call(keep=x) == INVALID and call(scale=x) == INVALID
     assert call(scale=0.0) == INVALID
+
+
+def test_key_weights_hook_checks(memra):
+    c, none = cache(memra), [0.1, 1.0, 64, 64, None]
+    hook = memra.lib().memra_testing_key_weights_short_page
+    good = [64, 1024, 64, 64, 64, 4, 64, 64, 2, 8, 8, 2, 128]
+    for at, value, want in ((8, 0, 0), (9, 0, 0), (0, 0, INVALID), (10, 7, INVALID), (1, 1016, INVALID)):
+        assert hook(ctypes.byref(c), *[value if i == at else x for i, x in enumerate(good)], *none) == want

@@ -232,3 +232,39 @@ def test_refusals_of_the_binding(memra):
             c.call(**bad)
     assert c.call() == 0
     c.check(1.0)
+
+
+@pytest.mark.parametrize("kf,D", [("q8_0", 128), ("fp8", 128), ("q8_0", 256), ("nvfp4", 256)])
+@pytest.mark.parametrize("new,past", [
+    ([40, 1, 300], [3000, 4000, 100]),       # large row tiles; log-sum-exps kept for a run, and not
+    ([1] * 6, [3000, 5000, 700, 4000, 1, 900]),                                       # small ones
+    ([1] * 15 + [140], [300] * 15 + [2000]),
+])
+@pytest.mark.parametrize("first", [True, False])
+def test_a_wait_that_runs_out(memra, kf, D, new, past, first):
+    """The copies of CTA 0's first chunk are declared 16 bytes too long: the keys of its share become NaN, the others keep their bytes."""
+    import time
+    if not first:                            # CTA 0 begins in the longest chunk
+        new, past = new[::-1], past[::-1]
+    c = Weights(memra, kf, "q5_1", D, 8, 2, new, past, stride=max(n + p for n, p in zip(new, past)) + 7)
+    assert c.call(0.5) == 0
+    c.check(0.5)
+    good, pool = c.weights.clone(), c.cache.k_pool.clone()
+    c.weights.copy_(dev(c.old))
+    begin = time.monotonic()
+    memra.testing_key_weights_short_page(
+        c.cache, c.buf, dev(c.lse_in), dev(c.starts), dev(c.table), dev(np.array(c.lens, np.int32)), max(c.lens), c.weights, 0.5)
+    assert memra.read_status(c.cache) == memra.DEVERR_TIMEOUT
+    assert time.monotonic() - begin < 20
+    nan = torch.isnan(c.weights)
+    assert nan[0, 0, 0] and not nan.all(-1).all()
+    # whole tiles of keys, and nothing behind a sequence's last
+    for b, T in enumerate(c.lens):
+        assert not nan[b, :, T:].any()
+        for h in range(2):
+            x = nan[b, h, :T].cpu().numpy()
+            assert all(x[lo:lo + 128].all() or not x[lo:lo + 128].any() for lo in range(0, T, 128))
+    assert torch.equal(c.weights[~nan], good[~nan]) and torch.equal(c.cache.k_pool, pool)
+    c.weights.copy_(dev(c.old))
+    assert c.call(0.5) == 0
+    assert torch.equal(c.weights, good)
