@@ -569,7 +569,8 @@ def kv_evict(cache: KVCache, page_table, seq_lens, max_seq_len: int, weights, bu
     weights float32 [B, Hkv, >= max_seq_len]; budgets int32 [B], at most
     kept.shape[2]; dst_table int32 [B, pages] of pages that nothing else uses;
     kept int32 [B, Hkv, max_budget] receives the kept indices, new_weights
-    float32 [B, Hkv, >= max_budget] their weights, new_lens int32 [B] how many.
+    float32 [B, Hkv, >= max_budget] their weights, new_lens int32 [B] how many
+    (seq_lens or budgets themselves will do).
     """
     import torch
     where, f32, i32 = "memra_kv_evict", torch.float32, torch.int32
@@ -588,6 +589,11 @@ def kv_evict(cache: KVCache, page_table, seq_lens, max_seq_len: int, weights, bu
         _dense(where, new_lens, i32, (B,), device) if new_lens is not None else 0, _stream(stream))
     if rc:
         raise MemraError(rc, where)
+    if most == 0 and new_lens is not None:             # (the entry point has done nothing)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            new_lens.zero_()
 
 
 def testing_decode_attn_short_page(cache: KVCache, q, page_table, seq_lens, max_seq_len: int, out, workspace,

@@ -250,3 +250,19 @@ def test_lengths_updated_in_place_by_a_replayed_graph(memra):
                 again = chunked.kept_tokens(c.weights[b, h, rows], lens[b].item(), 2, 8)
                 assert np.array_equal(kept[b, h].cpu().numpy()[:len(again)], again)
                 assert (kept[b, h, len(again):] == -1).all()
+
+
+@pytest.mark.parametrize("on", ["current", "stream", "handle"])
+def test_budgets_of_nothing(memra, on):
+    """kept has no column: no sequence keeps a token, and new_lens says so."""
+    c = Case(memra, "fp8", "fp8", 128, 2, [50, 0, 7], [0, 0, 0], 1, 2)
+    c.kept, c.to, c.new_w = c.kept[..., :0], c.to[:, :0], c.new_w[..., :0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert c.call(stream={"current": None, "stream": side, "handle": side.cuda_stream}[on]) == 0
+    torch.cuda.synchronize()
+    c.check()
+    lens = dev(c.lens)
+    assert c.call(seq_lens=lens, new_lens=lens, new_weights=None) == 0 and lens.tolist() == [0, 0, 0]
+    with pytest.raises(memra.MemraError):
+        c.call(new_lens=torch.zeros(2, dtype=torch.int32, device="cuda"))
