@@ -23,6 +23,7 @@ extern "C" int memra_kv_evict(const memra_kv_cache *cache, const int32_t *page_t
       static_cast<int64_t>(dst_pages_per_seq) * kPage < max_budget || (new_weights && new_weight_stride < max_budget))
     return MEMRA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(batch) * cache->n_kv_heads > 65535) return MEMRA_ERR_UNSUPPORTED;
+  if (max_budget > INT32_MAX - 65536) return MEMRA_ERR_UNSUPPORTED;        // rows up to some pages behind the last stay below 2^31
   if (batch == 0 || max_budget == 0) return MEMRA_OK;
   if (!page_table || !seq_lens || !weights || !budgets || !dst_table || !kept || !aligned4(page_table) ||
       !aligned4(seq_lens) || !aligned4(weights) || !aligned4(budgets) || !aligned4(dst_table) || !aligned4(kept) ||

@@ -546,7 +546,7 @@ int memra_key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stri
  *   new_lens      device int32 [batch], or NULL: n; may be seq_lens or budgets themselves
  * A length out of range is clamped (MEMRA_DEVERR_BAD_SEQ_LEN); a row whose page is
  * outside the pool, on either side, does not move (MEMRA_DEVERR_BAD_PAGE).  batch *
- * n_kv_heads <= 65535.  No workspace.  batch == 0 or max_budget == 0 is a no-op: new_lens
+ * n_kv_heads <= 65535, max_budget < 2^31 - 65536.  No workspace.  batch == 0 or max_budget == 0 is a no-op: new_lens
  * too stays as it is (every n is 0; the Python binding stores that). */
 int memra_kv_evict(const memra_kv_cache *cache, const int32_t *page_table, int32_t max_pages_per_seq,
                    const int32_t *seq_lens, int32_t max_seq_len, const float *weights, int64_t weight_stride,

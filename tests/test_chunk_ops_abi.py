@@ -174,3 +174,13 @@ def test_key_weights_hook_checks(memra):
     good = [64, 1024, 64, 64, 64, 4, 64, 64, 2, 8, 8, 2, 128]
     for at, value, want in ((8, 0, 0), (9, 0, 0), (0, 0, INVALID), (10, 7, INVALID), (1, 1016, INVALID)):
         assert hook(ctypes.byref(c), *[value if i == at else x for i, x in enumerate(good)], *none) == want
+
+
+def test_evict_refuses_budgets_at_the_end_of_int32(memra):
+    """Row numbers up to a CTA's pages behind the last would pass 2^31."""
+    def call(most):
+        return memra.lib().memra_kv_evict(ctypes.byref(cache(memra)), 64, 4, 64, 64, 64, 64, 64, most, 1, 1, 64, 1 << 27, 2, 64,
+                                          128, 1 << 31, 64, None)
+
+    assert call(2 ** 31 - 1) == UNSUPPORTED
+    assert call(2 ** 31 - 65536) == UNSUPPORTED
