@@ -25,9 +25,10 @@ extern "C" int memra_kv_evict(const memra_kv_cache *cache, const int32_t *page_t
   if (static_cast<int64_t>(batch) * cache->n_kv_heads > 65535) return MEMRA_ERR_UNSUPPORTED;
   if (max_budget > INT32_MAX - 65536) return MEMRA_ERR_UNSUPPORTED;        // rows up to some pages behind the last stay below 2^31
   if (batch == 0 || max_budget == 0) return MEMRA_OK;
-  if (!page_table || !seq_lens || !weights || !budgets || !dst_table || !kept || !aligned4(page_table) ||
+  // (without a token there is no weight: null will do)
+  if (!page_table || !seq_lens || (!weights && max_seq_len > 0) || !budgets || !dst_table || !kept || !aligned4(page_table) ||
       !aligned4(seq_lens) || !aligned4(weights) || !aligned4(budgets) || !aligned4(dst_table) || !aligned4(kept) ||
-      !aligned4(new_weights) || !aligned4(new_lens) || weights == new_weights)
+      !aligned4(new_weights) || !aligned4(new_lens) || (weights && weights == new_weights))
     return MEMRA_ERR_INVALID_ARG;
   EvictParams p;
   p.k_pool = static_cast<uint8_t *>(cache->k_pool);

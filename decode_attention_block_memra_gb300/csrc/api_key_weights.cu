@@ -28,7 +28,8 @@ int key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stride, co
   if (q_stride < static_cast<int64_t>(n_heads) * head_dim || q_stride % 8) return MEMRA_ERR_INVALID_ARG;
   if (q_stride >= (1ll << 38)) return MEMRA_ERR_UNSUPPORTED;       // what the tensor copies take
   if (batch == 0 || total_tokens == 0) return MEMRA_OK;
-  if (!q || !lse || !cu_seqlens || !page_table || !seq_lens || !weights || !aligned16(q) || !aligned4(lse) ||
+  // (without a key there is no weight: null will do)
+  if (!q || !lse || !cu_seqlens || !page_table || !seq_lens || (!weights && max_seq_len > 0) || !aligned16(q) || !aligned4(lse) ||
       !aligned4(cu_seqlens) || !aligned4(page_table) || !aligned4(seq_lens) || !aligned4(weights))
     return MEMRA_ERR_INVALID_ARG;
   WeightParams p;

@@ -266,3 +266,14 @@ def test_budgets_of_nothing(memra, on):
     assert c.call(seq_lens=lens, new_lens=lens, new_weights=None) == 0 and lens.tolist() == [0, 0, 0]
     with pytest.raises(memra.MemraError):
         c.call(new_lens=torch.zeros(2, dtype=torch.int32, device="cuda"))
+
+
+def test_sequences_without_a_token_and_no_weights(memra):
+    c = Case(memra, "fp8", "fp8", 128, 2, [0, 0], [3, 3], 1, 2)
+    empty = torch.empty(2, 2, 0, device="cuda")
+    for new_weights in (c.new_w, None):
+        assert c.call(weights=empty, max_seq_len=0, new_weights=new_weights) == 0
+        c.check()
+    # a length past the bound of 0 is clamped
+    assert c.call(weights=empty, max_seq_len=0, seq_lens=dev([5, 0])) == memra.DEVERR_BAD_SEQ_LEN
+    c.check()

@@ -268,3 +268,15 @@ def test_a_wait_that_runs_out(memra, kf, D, new, past, first):
     c.weights.copy_(dev(c.old))
     assert c.call(0.5) == 0
     assert torch.equal(c.weights, good)
+
+
+def test_no_keys_and_no_weights(memra):
+    c = Weights(memra, "fp8", "fp8", 128, 8, 2, [2, 0], [5, 0])
+    empty = torch.empty(2, 2, 0, device="cuda")
+    lens, starts = dev(np.zeros(2, np.int32)), dev(np.zeros(3, np.int32))
+    assert c.call(weights=empty, max_seq_len=0, seq_lens=lens, cu_seqlens=starts) == 0
+    # rows of a sequence without a key, and a length past the bound of 0: flagged, nothing is read or written
+    assert c.call(weights=empty, max_seq_len=0, seq_lens=lens) == memra.DEVERR_BAD_SEQ_LEN
+    assert c.call(weights=empty, max_seq_len=0) == memra.DEVERR_BAD_SEQ_LEN
+    assert c.call() == 0
+    c.check(1.0)
