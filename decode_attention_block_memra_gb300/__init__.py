@@ -541,7 +541,8 @@ def key_weights(cache: KVCache, q, lse, cu_seqlens, page_table, seq_lens, max_se
     """memra_key_weights: adds to weights what each key collects from the rows of a chunk.
 
     q, cu_seqlens, page_table, seq_lens as in chunk_attn, lse float32 [tokens,
-    Hq] as it writes them; weights float32 [B, Hkv, >= max_seq_len], times keep first.
+    Hq] as it writes them; weights float32 [B, Hkv, >= max_seq_len], times keep first
+    (so that those of new tokens must be set, to 0 as a rule, unless keep is 0).
     """
     a = _weight_args(cache, q, lse, cu_seqlens, page_table, seq_lens, max_seq_len, weights, keep, sm_scale)
     _check(lib().memra_key_weights(*a, _stream(stream)), "memra_key_weights")

@@ -504,7 +504,9 @@ int memra_chunk_attn(const memra_kv_cache *cache, const void *q, int64_t q_strid
  *   w[b][g][u] = keep * w[b][g][u] + sum over rows t of sequence b that see key u and
  *                heads h of KV head g of exp(q[t,h] . K^[u] * sm_scale - lse[t,h])
  * for u < seq_lens[b]; what lies behind stays as it is.  keep 1 adds up over the calls,
- * 0 starts anew (w need not have been written), between them older calls fade.
+ * 0 starts anew (w need not have been written), between them older calls fade.  With keep
+ * other than 0 the weights of tokens that are new since the last call must have been
+ * set, to 0 as a rule: the call adds to what lies there.
  *   q, q_stride, cu_seqlens, page_table, seq_lens, max_seq_len, total_tokens, sm_scale
  *                 as in memra_chunk_attn: rows see the keys up to their own position
  *   lse           device float32 [total_tokens][n_heads], natural logarithms, as
@@ -541,8 +543,9 @@ int memra_key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stri
  *   kept          device int32 [batch][n_kv_heads][max_budget]: written, the kept
  *                 tokens' indices, -1 behind the last
  *   new_weights   device float32 [batch][n_kv_heads][new_weight_stride], or NULL:
- *                 their weights, what lies behind the last left as it was; overlaps
- *                 nothing else of the call
+ *                 their weights, what lies behind the last left as it was (zeros must be
+ *                 put there before memra_key_weights adds to the tokens appended next);
+ *                 overlaps nothing else of the call
  *   new_lens      device int32 [batch], or NULL: n; may be seq_lens or budgets themselves
  * A length out of range is clamped (MEMRA_DEVERR_BAD_SEQ_LEN); a row whose page is
  * outside the pool, on either side, does not move (MEMRA_DEVERR_BAD_PAGE).  batch *

@@ -178,3 +178,25 @@ def test_a_captured_round_on_another_stream(memra):     # noqa: F811
         for got, ref in zip(results, want):
             assert torch.equal(got, ref)
     assert memra.read_status(f.cache) == 0
+
+
+def test_weights_that_must_be_set_are_those_of_new_tokens(memra):     # noqa: F811
+    """Zeros where the round's tokens come in, NaN everywhere else: the same tokens stay, with the same weights, as with zeros."""
+    flows = [Flow(memra, "q8_0", "q5_1", 128, 8, 2, 3, [100, 64, 9], sink=4, recent=8, seed=5) for _ in range(2)]
+    flows[1].weights.fill_(float("nan"))
+    for new in ([70, 33, 5], [130, 1, 64], [1, 100, 0], [1, 1, 1]):
+        got = []
+        for i, f in enumerate(flows):
+            before = list(f.lens)
+            f.step(new)
+            now, other = f.weights[f.half], f.weights[1 - f.half]
+            for b, (T, n) in enumerate(zip(before, new)):
+                now[b, :, T:T + n] = 0
+            other.fill_(float("nan") if i else 0.0)
+            f.all()
+            assert memra.read_status(f.cache) == 0
+            lens = f.new_lens.tolist()
+            assert lens == [min(T, n) for T, n in zip(f.lens, f.budgets)]
+            got.append([f.kept.clone(), f.out.clone()] + [other[b, :, :n].clone() for b, n in enumerate(lens)])
+            f.lens, f.half = lens, 1 - f.half
+        assert all(torch.equal(a, b) for a, b in zip(*got))
