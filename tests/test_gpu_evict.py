@@ -277,3 +277,71 @@ def test_sequences_without_a_token_and_no_weights(memra):
     # a length past the bound of 0 is clamped
     assert c.call(weights=empty, max_seq_len=0, seq_lens=dev([5, 0])) == memra.DEVERR_BAD_SEQ_LEN
     c.check()
+
+
+def best(w, T, n, sink, recent):
+    """kept_tokens of float32 weights without NaN, by numpy's sort."""
+    recent = min(recent, n)
+    sink = min(sink, n - recent)
+    middle = np.arange(sink, T - recent)
+    first = middle[np.lexsort((middle, -w[middle]))][:n - sink - recent]
+    return np.concatenate((np.arange(sink), np.sort(first), np.arange(T - recent, T))).astype(np.int64)
+
+
+@pytest.mark.parametrize("kind", ["random", "few", "rising"])
+@pytest.mark.parametrize("batch,heads,T,budget", [(40, 8, 40000, 3000),      # one CTA to a row, three rounds of its registers
+                                                  (24, 4, 50000, 700),       # two to a row
+                                                  (1, 2, 700000, 30000)])    # sixteen
+def test_rows_that_pass_a_cta_s_registers(memra, batch, heads, T, budget, kind):
+    rng = np.random.default_rng(T)
+    shape = (batch, heads, T)
+    w = {"random": lambda: rng.random(shape), "few": lambda: rng.choice([0.0, 0.25, 0.5], shape),
+         "rising": lambda: np.broadcast_to(np.arange(T) % 60000, shape)}[kind]().astype(np.float32)
+    lens = [T - 1000 * b for b in range(batch)] if batch < 30 else [T - 300 * b for b in range(batch)]
+    pages = T // 16 + 1                      # every sequence reads the same pages
+    cache = memra.KVCache("fp8", "fp8", pages + batch * (-(-budget // 16)), heads, 128)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for pool in (cache.k_pool, cache.v_pool):
+        pool.copy_(torch.randint(0, 256, pool.shape, dtype=torch.uint8, device="cuda", generator=g))
+    before = cache.k_pool.view(-1, heads, 2048)[:pages].cpu().numpy()
+    table = np.tile(rng.permutation(pages).astype(np.int32), (batch, 1))
+    to = (pages + rng.permutation(batch * (-(-budget // 16)))).astype(np.int32).reshape(batch, -1)
+    kept, new = torch.empty(batch, heads, budget, dtype=torch.int32, device="cuda"), torch.zeros(batch, heads, budget, device="cuda")
+    new_lens = dev(lens)
+    memra.kv_evict(cache, dev(table), new_lens, T, dev(w, np.float32), dev([budget] * batch), dev(to), kept, 5, 100,
+                   new_weights=new, new_lens=new_lens)
+    assert memra.read_status(cache) == 0 and new_lens.tolist() == [budget] * batch
+    after = cache.k_pool.view(-1, heads, 2048).cpu().numpy()
+    where = np.stack([np.nonzero(m)[0] for m in token_bytes("k", "fp8", 128)])
+    kept, new, j = kept.cpu().numpy(), new.cpu().numpy(), np.arange(budget)
+    for b in range(batch):
+        for h in range(heads):
+            rows = best(w[b, h], lens[b], budget, 5, 100)
+            assert np.array_equal(kept[b, h], rows) and np.array_equal(new[b, h], w[b, h, rows])
+            got = after[to[b, j // 16][:, None], h, where[j % 16]]
+            assert np.array_equal(got, before[table[b, rows // 16][:, None], h, where[rows % 16]])
+
+
+def test_many_calls_in_a_row_and_side_by_side(memra):
+    cases = [Case(memra, "q8_0", "q5_1", 128, 2, [700, 40], [301, 40], 2, 3, seed=1),
+             Case(memra, "fp8", "fp8", 256, 3, [5000, 4097], [1000, 2049], 5, 64, seed=2),
+             Case(memra, "nvfp4", "q4_0", 128, 1, [70000], [900], 0, 16, seed=3)]
+    calls, want = [], []
+    for c in cases:
+        assert c.call() == 0
+        c.check()
+        want.append([t.clone() for t in (c.kept, c.new_w, c.new_lens, c.cache.k_pool, c.cache.v_pool)])
+        a = dict(page_table=dev(c.table), seq_lens=dev(c.lens), max_seq_len=max(c.lens), weights=dev(c.weights, np.float32),
+                 budgets=dev(c.budgets), dst_table=dev(c.to), kept=c.kept, sink=c.sink, recent=c.recent, new_weights=c.new_w,
+                 new_lens=c.new_lens)
+        calls.append((c.cache, a))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for turn in range(600):
+        for (cache, a), stream in zip(calls, streams):
+            memra.kv_evict(cache, **a, stream=stream if turn < 300 else None)
+        if turn == 299:
+            torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert memra.read_status(c.cache) == 0
+        assert all(torch.equal(t, u) for t, u in zip((c.kept, c.new_w, c.new_lens, c.cache.k_pool, c.cache.v_pool), w))

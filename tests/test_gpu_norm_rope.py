@@ -241,3 +241,28 @@ def test_turned_keys_fall_to_the_right_side(memra, D, rotary, interleaved):
     assert other.sum() <= 10                 # (by chance one in 2^21)
     near = np.abs(exact[other] - (got[other].astype(np.float64) + want[other].astype(np.float64)) / 2)
     assert (near <= 2.0 ** -32 * a[other]).all()
+
+
+def test_many_calls_in_a_row_and_side_by_side(memra):
+    calls, outs, want = [], [], []
+    for i, (T, Hq, Hkv, D) in enumerate(((7, 8, 2, 128), (300, 4, 2, 256), (2600, 3, 1, 128))):
+        rows, pos, freq, qw, kw = case(T, Hq, Hkv, D, D // 2, seed=i)
+        fused = dev(rows)
+        cache = memra.KVCache("fp8", "fp8", T // 16 + 1, Hkv, D, 0.02, 0.02)
+        q_out, k_out = (torch.empty(T, h, D, dtype=torch.float16, device="cuda") for h in (Hq, Hkv))
+        calls.append(lambda stream, a=(fused[:, :Hq], fused[:, Hq:Hq + Hkv], dev(pos), dev(freq), q_out, k_out, dev(qw), dev(kw)),
+                     kw_=dict(cache=cache, v=fused[:, Hq + Hkv:], slot_mapping=dev(np.arange(T, dtype=np.int32))):
+                     memra.qk_norm_rope(*a, EPS, False, **kw_, stream=stream))
+        calls[-1](None)
+        check(q_out, rows[:, :Hq], qw, pos, freq, False)
+        assert memra.read_status(cache) == 0
+        outs.append((q_out, k_out, cache.k_pool, cache.v_pool))
+        want.append([t.clone() for t in outs[-1]])
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for turn in range(600):
+        for call, stream in zip(calls, streams):
+            call(stream if turn < 300 else None)
+        if turn == 299:
+            torch.cuda.synchronize()
+    assert all(torch.equal(t, u) for a, b in zip(outs, want) for t, u in zip(a, b))
