@@ -57,6 +57,7 @@ int key_weights(const memra_kv_cache *cache, const void *q, int64_t q_stride, co
   p.len_limit = static_cast<int32_t>(std::min<int64_t>(std::min<int64_t>(max_seq_len, INT32_MAX - 4 * kWeightKeys),
                                                        static_cast<int64_t>(max_pages_per_seq) * kPage));
   const int64_t all_rows = static_cast<int64_t>(total_tokens) * p.group;
+  // (small row tiles by the rows of a sequence on average: what that costs and gains stands in key_weights.cu)
   const int rows = all_rows <= static_cast<int64_t>(batch) * kWeightRowsFew ? kWeightRowsFew : weight_rows(head_dim);
   p.hpt = std::min(p.group, rows);
   p.subs = static_cast<int>(ceil_div(p.group, p.hpt));

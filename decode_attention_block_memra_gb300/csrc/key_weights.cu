@@ -23,7 +23,9 @@
 // every score: 64 tokens of 32 heads over 262,144 keys of 4, q8_0, take 183 us, 78% of the rate of
 // the tensor cores' fp16 products, pairs counted (one group to a key tile: 252).  With few, each key is staged
 // for a handful of rows: tiles of 32 rows then, 16 staging warps, one group to a key tile.  8 sequences
-// of one token over 6,316 keys each take 19 us, 23 in tiles of 128 (and those 64 tokens 379 us in tiles of 32).
+// of one token over 6,316 keys each take 19 us, 23 in tiles of 128 (and those 64 tokens 379 us in tiles of 32).  The choice goes by
+// the rows of a sequence on average, which the host knows: 64 single tokens over 4,000 keys 65 us, 86 in tiles of 128;
+// but with 190 tokens behind 30,000 among them, still 32 rows on average, 288 us, where tiles of 128 take 168.
 // Of the 19 some 5 pass before the first page is there; then a tile is staged in 1,300 clocks, and 28 MB
 // arrive in 10 us.
 // The (key tile, KV head, sequence) items of the call lie behind one another on a line

@@ -19,7 +19,7 @@
 // digits left behind the point.  So a frequency is kept in turns (inv_freq / 2 pi)
 // as a 64-bit binary fraction, rounded once, and the position multiplies it modulo
 // 2^64: whole turns fall away exactly.  What is left within an eighth of a turn goes
-// through the Taylor series of sine and cosine, their leading terms as two floats.
+// through the Taylor series of sine and cosine, their first three terms as two floats.
 //
 // A row is D / 8 lanes of 8 consecutive dims (one 16-byte load); a warp takes 32 / (D / 8)
 // heads of one token at a time, of one kind (K, V or Q), so that it never diverges
@@ -29,10 +29,10 @@
 // flight throughout.
 //
 // Bound by bytes with many tokens, and by the arithmetic of the keys and of the quantizers
-// beside them: those 16,384 tokens move 319 MB in 85 us, 3.8 TB/s (queries alone: 268 MB in
-// 54 us, 5.0 TB/s); 2,048 tokens of 32 and 4 heads, D 128, no cache: 38 MB in
-// 11.5 us.  With few, by
-// the chain of one row: a launch of 8 tokens takes 4.5 us.
+// beside them: those 16,384 tokens move 319 MB in 88 us, 3.6 TB/s (queries alone: 268 MB in
+// 54 us, 5.0 TB/s; 130 us into q8_0/q5_1, all dims turned, where fp8 takes 106).  2,048 tokens of 32 and 4 heads,
+// D 128, no cache: 38 MB in 14.6 us, 12.2 where they are in L2; a warp walks a token's 20 row groups.  With few, by
+// the chain of one row: a launch of 8 tokens takes 4.9 us.
 #include <algorithm>
 
 #include "kv_stage.cuh"

@@ -329,9 +329,10 @@ int memra_decode_step_cascade(const memra_kv_cache *cache, const void *k_new, co
  * 128 or 256, batch and n_kv_heads <= 65535.  Scores, softmax and output are
  * accumulated in float32, 8,192 keys to a sum of the tensor cores (which cut a
  * sum's last bits at every step) and the sums joined; the weights enter the
- * product with V in fp16.  While the call runs, rows of out may hold parts of
- * those sums.  A sequence's result bytes are the same alone or packed with
- * others, and no two sequences see each other's rows.  A v that is not finite
+ * product with V in fp16, each off by up to 2^-11 of itself or 2^-25 of the row's
+ * largest, so that N keys far below the largest may move the row by N * 2^-25 |v|.
+ * While the call runs, rows of out may hold parts of those sums.  A sequence's
+ * result bytes are the same alone or packed with others, and no two sequences see each other's rows.  A v that is not finite
  * may also reach rows of its sequence within 256 tokens of those that see it.
  * No workspace.  batch == 0 or total_tokens == 0 is a no-op. */
 int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -364,7 +365,8 @@ int memra_prompt_attn(const void *q, int64_t q_stride, const void *k, int64_t k_
  * All K and V formats, head_dim 128 or 256, n_heads / n_kv_heads <=
  * MEMRA_MAX_GROUP, batch <= 65535, n_kv_heads * ceil(n_nodes * n_heads /
  * n_kv_heads / 128) <= 65535; sm_scale finite.  K^ and V^ enter the products
- * exactly (or as fp16 pairs), the softmax weights in fp16; everything is
+ * exactly (or as fp16 pairs), the softmax weights in fp16 (of the 7,680 keys at most of a
+ * split, each off by up to 2^-11 of itself or 2^-25 of the split's largest); everything is
  * accumulated in float32.  The keys are cut by the lengths of the whole call,
  * so that it fills the GPU: the same call gives the same bytes, another batch
  * groups a row's sums differently and may differ in the last bits.  A row that
@@ -484,9 +486,9 @@ int memra_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k
  * pairs), the softmax weights in fp16: each off by up to 2^-11 of itself, or 2^-32 of
  * the row's largest, whichever is more, so that N keys far below the largest may
  * move the row by N * 2^-32 |V|.  Everything is accumulated in float32, 7,680 keys
- * to a sum of the tensor cores and the sums joined.  The work is cut by the lengths of the whole call, so that it fills the GPU: the same call gives
- * the same bytes, another batch may differ in the last bits.  A query, or a key that
- * a row sees, that is not finite makes the row NaN; a V that is not finite may also
+ * to a sum of the tensor cores and the sums joined.  The work is cut by the lengths of
+ * the whole call, so that it fills the GPU: the same call gives the same bytes, another
+ * batch may differ in the last bits.  A query, or a key that a row sees, that is not finite makes the row NaN; a V that is not finite may also
  * reach rows of its sequence that do not see it.  A length out of range is clamped and
  * sets MEMRA_DEVERR_BAD_SEQ_LEN, as does a sequence shorter than its chunk, whose rows
  * at positions below 0 yield zeros; that sequence's other rows are then unspecified.
