@@ -49,6 +49,7 @@ namespace {
 // log2 units: a row's maximum passes its reference m by no more between rescales; and P is 2^(s - m + kLift), so
 // that it uses fp16's range: 2^15 at most, and 2^7 at least for the row's largest.
 constexpr float kLazy = 8.f, kLift = 7.f;
+constexpr float kLarge = 1048576.f;        // log2 units: float32 holds smaller scores to 2^-4
 constexpr int kSumUnits = 120;             // chunks of one sum of the tensor cores: 7,680 keys
 
 // Where a CTA's share of the line begins, or ends.
@@ -526,6 +527,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready(g));
       float m = -INFINITY, l = 0.f, m_far = -INFINITY;
+      bool large = false;                    // of the warp: some row's reference is
       // O plus what lies in `far`, to `far` (or back to O, at the end)
       auto join = [&](bool back) {
         const bool held = m_far != -INFINITY;
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
           for (int c = 0; c < KT; ++c)
             if (!(half[c / 32] & (1u << (c % 32)))) s[c] = 0xff800000u;      // -inf
         }
-        const float top = row_max(s) * p.scale_log2;
+        const float most = row_max(s), top = __fmul_rn(most, p.scale_log2);      // (rounded: not a part of a fused sum below)
         if (G == 1 && nth > 0 && nth % kSumUnits == 0) {
           ok = mbar_wait_suspended(pv_done(0), (done + nth - 1) & 1, p.status);
           ok = __all_sync(0xffffffffu, ok);
@@ -594,11 +596,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
           m_far = m;
         }
         float alpha = 1.f;
-        if (top > m + kLazy) {               // also the first chunk with a key (m = -inf)
-          if (m != -INFINITY) alpha = fast_exp2(m - top);
-          m = top;
+        const bool passed = __any_sync(0xffffffffu, top - m > kLazy), moved = nth > 0 && passed;
+        if (passed) {
+          if (top - m > kLazy) {             // also the first chunk with a key (m = -inf)
+            if (m != -INFINITY) alpha = fast_exp2(m - top);
+            m = top;
+          }
+          large = __any_sync(0xffffffffu, fabsf(m) > kLarge && m != -INFINITY);
         }
-        const bool moved = nth > 0 && __any_sync(0xffffffffu, alpha != 1.f);
         if (G == 1 && nth > 0 && (moved || nth == units - 1)) {
           // The product before has completed, O is still (a group of two: these scores were issued behind it).
           // At the last chunk in any case: the wait behind the loop names the last product by its
@@ -620,7 +625,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, KF, VF>::kThreads, 1) chunk_kernel
           }
           l *= alpha;
         }
-        const float mu = m == -INFINITY ? 0.f : m - kLift;
+        float mu = m == -INFINITY ? 0.f : m - kLift;
+        if (large) {
+          // s * scale - m may be off by more than P has room for: the difference from the chunk's largest first, which is exact
+          // for what lies near it
+          const float from = most == -INFINITY ? 0.f : most;
+#pragma unroll
+          for (int c = 0; c < KT; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) - from);
+          if (most != -INFINITY) mu = (m - top) - kLift;
+        }
         uint64_t sum = 0;
 #pragma unroll
         for (int c = 0; c < KT; c += 32) {

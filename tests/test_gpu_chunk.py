@@ -389,3 +389,60 @@ def test_a_dominant_key_over_a_long_even_tail(memra, kf, vf, D, T, n, tail):
     assert err.max() <= 1, f"{err.max()} of the tolerance"
     lse = c.lse.cpu().numpy().astype(np.float64)
     assert (np.abs(lse - want_lse) <= r_off + l_off + 2.0 ** -22 * want_lse).all()
+
+
+@pytest.mark.parametrize("vf", ["q5_1", "fp8"])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("new,past", [([3], [700]), ([1, 200], [9000, 40])])
+@pytest.mark.parametrize("k0", [200.0, 2200.0, 60000.0])
+def test_scores_so_large_that_float32_has_no_digits_left(memra, vf, D, new, past, k0):
+    """Scores of 2^20 to 2^29 log2 units that differ by up to 16: float32 holds them to 2^-3 .. 64 units, so that a row may weigh its keys
+    anyhow, but it is a mean of them: V between 1 and 2 (to a step of its format and of fp16) gives rows between 1 and 2."""
+    def some(c, b):
+        T = c.lens[b]
+        k = np.zeros((T, 1, D), np.float16)
+        k[:, 0, 0] = k0
+        k[:, 0, 32] = np.random.default_rng(b).random(T) * 16 * D ** 0.5 / 1.4427
+        return k
+
+    c = Chunk(memra, "q8_0", vf, D, 4, 1, new, past, v_of=lambda *s: 1 + np.random.default_rng(1).random(s))
+    for b, T in enumerate(c.lens):
+        pos = np.arange(T)
+        memra.kv_append(c.cache, dev(some(c, b)), dev(c.rows[b][2]),
+                        dev((c.table[b, pos // 16] * 16 + pos % 16).astype(np.int32)))
+        c.rows[b] = (0, some(c, b), c.rows[b][2])
+    c.buf.zero_()
+    c.buf[..., 0], c.buf[..., 32] = 60000.0, 1.0
+    assert c.call() == 0
+    score = 60000.0 * dequantized(c.rows[0][1][:1, 0], "q8_0", 1.0)[0, 0] * D ** -0.5
+    # (a row's reference is off by half a step of float32, 2^-24 of itself, the score by D / 8 of 2^-23)
+    assert (c.lse - score).abs().max() <= 16 + 11 + score * (2.0 ** -22 + D / 8 * 2.0 ** -23)
+    for b in range(len(new)):
+        v = dequantized(c.rows[b][2][:, 0], vf, c.scales[1])
+        out = c.out[c.starts[b]:c.starts[b + 1]].float().cpu().numpy()
+        # (weights rounded to fp16: 2^-11; sums cut by the tensor cores: 960 * 2^-23; the output's own 2^-11)
+        assert (out >= v.min(0) * (1 - 2.0 ** -9)).all() and (out <= v.max(0) * (1 + 2.0 ** -9)).all()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("q_gain,k_gain", [(1e3, 1e3), (1e4, 2e3), (1.2e4, 1.2e4)])
+def test_large_queries_and_keys_pick_one_key(memra, D, q_gain, k_gain):
+    """Random scores of 10^6 to 10^8: a row is the value of its largest score."""
+    c = Chunk(memra, "q8_0", "q4_0", D, 4, 2, [30, 2], [2000, 300], q_gain=q_gain, k_gain=k_gain)
+    assert c.call() == 0 and torch.isfinite(c.out).all() and torch.isfinite(c.lse).all()
+    picked = 0
+    for b in range(2):
+        T, n = c.lens[b], c.new[b]
+        for h in range(2):
+            _, k, v = c.keys(b, h)
+            q = c.q[c.starts[b]:c.starts[b + 1], 2 * h:2 * h + 2].astype(np.float64)
+            s = np.einsum("ngd,td->ngt", q, k) * D ** -0.5
+            s[np.broadcast_to(~(np.arange(T) <= np.arange(T - n, T)[:, None])[:, None], s.shape)] = -np.inf
+            off = np.einsum("ngd,td->ngt", np.abs(q), np.abs(k)).max(-1) * D ** -0.5 * (D / 8 + 2) * 2.0 ** -23
+            two = np.sort(s, -1)[..., -2:]
+            sure = two[..., 1] - two[..., 0] > 2 * off + 40        # the second weighs below 2^-57
+            out = c.out[c.starts[b]:c.starts[b + 1], 2 * h:2 * h + 2].float().cpu().numpy()
+            want = v[s.argmax(-1)]
+            assert (np.abs(out - want)[sure] <= 2.0 ** -9 * np.abs(want[sure]) + 2.0 ** -24).all()
+            picked += sure.sum()
+    assert picked > 100
