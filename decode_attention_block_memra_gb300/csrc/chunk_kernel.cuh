@@ -28,9 +28,9 @@
 // float32 row in the workspace.
 //
 // What it measured (q8_0/q5_1, D 128, 32/4 heads).  2,048 tokens behind 30,000: 1.36 ms, with the pairs' products 81% of
-// the rate of a large library product, the tensor pipe 69% active; fp8/fp8, which has no pairs and half of the products, 0.97 ms
-// with the pipe 46% active.  So the chain bounds it, from a score to its P and to the next score over it, which two groups
-// do not quite hide.  512 tokens beside 15 single ones over 60,000 keys: 108 us.  One token over 255
+// the rate of a large library product, the tensor pipe 69% active; fp8/fp8, which has no pairs and half of the products, 0.95 ms
+// with the pipe 47% active.  So the chain bounds it, from a score to its P and to the next score over it, which two groups
+// do not quite hide.  512 tokens beside 15 single ones over 60,000 keys: 109 us.  One token over 255
 // keys: 11 us, a chain of latencies.  Not faster: an MMA thread for each group (1,818 us), P in columns
 // of its own with most of Q in shared memory (1,507 us).
 #pragma once
